@@ -87,7 +87,10 @@ typedef enum {
   NF4_OP_DEQUANTIZE = 1,
   NF4_OP_LINEAR_FWD = 2,
   NF4_OP_LINEAR_BWD = 3,
-  NF4_OP_MERGE = 4
+  NF4_OP_MERGE = 4,
+  NF4_OP_GROUPED_FWD = 5,
+  NF4_OP_GROUPED_BWD = 6,
+  NF4_OP_INT8_LINEAR = 7
 } nf4_op;
 
 /*
@@ -162,7 +165,9 @@ NF4_API nf4_status nf4_profile_get(int kernel_id, int64_t* launches, double* tot
 /*
  * Bytes of workspace an operation needs (0 = none).  M, N, K, r are the
  * linear-layer sizes (N = W rows, K = W cols); for NF4_OP_QUANTIZE and
- * NF4_OP_DEQUANTIZE pass N = rows, K = cols and M = r = 0.  Needs no GPU.
+ * NF4_OP_DEQUANTIZE pass N = rows, K = cols and M = r = 0; for the grouped
+ * operations N is the rows of one expert; for NF4_OP_INT8_LINEAR r,
+ * block_size and double_quant are not used.  Needs no GPU.
  */
 NF4_API size_t nf4_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int block_size,
                            int double_quant);
@@ -386,6 +391,106 @@ NF4_API nf4_status qlora_linear_bwd(const nf4_weight* w, const void* x, int64_t 
 NF4_API nf4_status nf4_merge(const nf4_weight* w, const void* A, const void* B, int r, float alpha,
                              int out_dtype, void* out, void* workspace, size_t ws_bytes,
                              void* stream);
+
+/*
+ * QLoRA linear of a stack of experts, forward (the layer of qlora_linear_fwd,
+ * one weight and one adapter per expert, as in a mixture-of-experts block):
+ *   for every row m of expert e, offsets[e] <= m < offsets[e + 1],
+ *   y[m] = x[m] W'_e^T + s (x[m] A_e^T) B_e^T (+ bias_e),  s = alpha / r.
+ * The rows are sorted by expert; an expert may have any number of rows, none
+ * included.
+ *   w              the experts' weights stacked row-wise and quantized as one
+ *                  tensor: w->rows = num_experts * N, expert e holds rows
+ *                  [e N, (e + 1) N); w->cols = K.  N % 8 == 0, K % 64 == 0,
+ *                  block sizes as in qlora_linear_fwd.
+ *   num_experts    1 .. 512; divides w->rows.
+ *   x              [M, K] compute_dtype; M >= 0 (0: nothing is enqueued; x,
+ *                  y and t_out may then be NULL).
+ *   offsets        int32 [num_experts + 1], DEVICE memory, 4-byte aligned,
+ *                  non-decreasing, 0 <= offsets[e] <= M.  Read on the GPU, so
+ *                  a router's result is used without a copy to the host.
+ *                  Rows before offsets[0] and behind offsets[num_experts]
+ *                  belong to no expert: y and t_out are not written there.
+ *                  Offsets outside that range are clamped into it (each to at
+ *                  least the ones before it, at most M), no row is read or
+ *                  written out of bounds, and NF4_ERR_INVALID_ARG is recorded
+ *                  in the status word.
+ *   A, B           [num_experts, r, K] and [num_experts, N, r] compute_dtype;
+ *                  8 <= r <= 256, r % 8 == 0.
+ *   compute_dtype  as qlora_linear_fwd (NF4_F32: the fp32 reference mode).
+ *   bias           [num_experts, N] compute_dtype, or NULL.
+ *   y              [M, N] compute_dtype.
+ *   t_out          [M, r] compute_dtype, or NULL: T = s (x A_e^T), which
+ *                  qlora_grouped_bwd accepts as `t`.
+ *   workspace      >= nf4_workspace_bytes(NF4_OP_GROUPED_FWD, M, N, K, r, 64, dq).
+ * A row's result depends on the rows it shares a tile with only through the
+ * order of its sums, and a non-finite row leaves the others as they are.
+ */
+NF4_API nf4_status qlora_grouped_fwd(const nf4_weight* w, int num_experts, const void* x, int64_t M,
+                                     const int32_t* offsets, const void* A, const void* B, int r,
+                                     float alpha, int compute_dtype, const void* bias, void* y,
+                                     void* t_out, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Adapter backward of qlora_grouped_fwd for L = sum(dy * y), the base frozen.
+ * For every expert e, over its rows:
+ *   U  = s (dy B_e)
+ *   dB_e = dy^T T   fp32 [num_experts, N, r]      dA_e = U^T x   fp32 [num_experts, r, K]
+ *   dx = dy W'_e + U A_e                          [M, K] compute_dtype, or NULL
+ * dA and dB are overwritten for every expert, with zeros for one without rows
+ * (M == 0 included).  dx is written only in rows that belong to an expert.
+ * `t` is the T of the forward's t_out, or NULL to recompute it.  With BF16 or
+ * F16, dA is summed from U as two 16-bit terms (the rounded value and what the
+ * rounding left), so it keeps U to 16 bits (BF16) or 22 (F16); dx uses the
+ * rounded U.  Other arguments as qlora_grouped_fwd and qlora_linear_bwd.
+ *   workspace      >= nf4_workspace_bytes(NF4_OP_GROUPED_BWD, M, N, K, r, 64, dq).
+ */
+NF4_API nf4_status qlora_grouped_bwd(const nf4_weight* w, int num_experts, const void* x, int64_t M,
+                                     const int32_t* offsets, const void* A, const void* B, int r,
+                                     float alpha, int compute_dtype, const void* dy, const void* t,
+                                     float* dA, float* dB, void* dx, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
+/*
+ * Row-wise quantization to 8-bit integers, for the operands of
+ * int8_linear_fwd: a scale per token for activations, per output channel for
+ * a weight (for instance one that nf4_merge made dense).
+ *   x       [rows, cols] of in_dtype (NF4_F32, NF4_BF16, NF4_F16), 16-byte
+ *           aligned; any rows, cols >= 0.
+ *   scales  fp32 [rows], 4-byte aligned: fp32(max |x| of the row / 127).
+ *   codes   int8 [rows, cols], 16-byte aligned: the integer nearest to
+ *           x / scale (the quotient of the stored scale taken exactly; a half
+ *           goes to the even integer), within -127 .. 127.
+ * A row of zeros, or one so small that its scale is 0, has codes 0.  A row
+ * that holds NaN or Inf has scale NaN and codes 0, so what is computed from
+ * it is NaN.
+ */
+NF4_API nf4_status int8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols,
+                                 int8_t* codes, float* scales, void* stream);
+
+/*
+ * Linear layer on 8-bit integers:
+ *   y[m, n] = (sum_k x_codes[m, k] w_codes[n, k]) x_scale[m] w_scale[n] (+ bias[n])
+ * with the sum exact in 32-bit integers, the scales and the bias applied in
+ * fp32 and one rounding to compute_dtype.
+ *   w_codes        int8 [N, K], w_scale fp32 [N] (4-byte aligned): a weight
+ *                  from int8_quantize.  N % 8 == 0, K % 16 == 0,
+ *                  16 <= K <= 131072.
+ *   x, x_scale     x_scale NULL: x is [M, K] of compute_dtype and is quantized
+ *                  in the call exactly as int8_quantize does, into the
+ *                  workspace.  Otherwise x is int8 [M, K] with one fp32 scale
+ *                  per row (4-byte aligned).  M >= 1.
+ *   compute_dtype  NF4_BF16, NF4_F16 or NF4_F32: type of y, bias and, without
+ *                  x_scale, of x.
+ *   bias           [N] or NULL.
+ *   y              [M, N], written.
+ *   workspace      >= nf4_workspace_bytes(NF4_OP_INT8_LINEAR, M, N, K, 0, 0, 0).
+ * It is a serving operator: it has no backward pass.
+ */
+NF4_API nf4_status int8_linear_fwd(const int8_t* w_codes, const float* w_scale, int64_t N, int64_t K,
+                                   const void* x, const float* x_scale, int64_t M, int compute_dtype,
+                                   const void* bias, void* y, void* workspace, size_t ws_bytes,
+                                   void* stream);
 
 #ifdef __cplusplus
 }

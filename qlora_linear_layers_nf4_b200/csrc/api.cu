@@ -42,7 +42,13 @@ size_t quantize_ws(int64_t numel, int bs, int dq) {
   return bytes;
 }
 
-// Checks shared by the two linear entry points.
+// int8 linear workspace: the header, then the codes and scales of x.
+size_t int8_linear_ws(int64_t M, int64_t K) {
+  if (M < 0 || K < 0) return nf4::kWsHeader;
+  return nf4::kWsHeader + round_up(size_t(M) * size_t(K), 256) + round_up(size_t(M) * sizeof(float), 256);
+}
+
+// Checks shared by the linear entry points.
 nf4_status check_linear(const nf4_weight* w, const void* x, int64_t M, const void* A,
                         const void* B, int r, float alpha, int compute_dtype) {
   if (w == nullptr || x == nullptr || A == nullptr || B == nullptr || w->codes == nullptr)
@@ -87,7 +93,8 @@ double g_prof_ms[nf4::kNumKernelIds];
 const char* const kKernelNames[nf4::kNumKernelIds] = {
     "nf4_quantize", "nf4_double_quant", "nf4_dequantize", "adapter_gemm_T",
     "fused_nf4_gemm_fwd", "fused_nf4_gemm_dx", "nf4_gemv", "nf4_merge", "gemm_f32", "nf4_absmax_max",
-    "adapter_gemm_U", "adapter_gemm_dB", "adapter_gemm_dA"};
+    "adapter_gemm_U", "adapter_gemm_dB", "adapter_gemm_dA", "grouped_T", "grouped_fwd", "grouped_U",
+    "grouped_dB", "grouped_dA", "grouped_dx", "int8_quantize", "int8_linear"};
 
 cudaEvent_t prof_event() {
   if (!g_prof_free.empty()) {
@@ -190,7 +197,7 @@ const char* nf4_status_string(int status) {
   }
 }
 
-int nf4_version(void) { return 100; }
+int nf4_version(void) { return 101; }
 
 void nf4_codebook(float* levels, float* thresholds) {
   if (levels != nullptr)
@@ -209,6 +216,9 @@ size_t nf4_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int b
     case NF4_OP_LINEAR_FWD: return nf4::kWsHeader + nf4::linear_workspace_bytes(false, M, N, K, r);
     case NF4_OP_LINEAR_BWD: return nf4::kWsHeader + nf4::linear_workspace_bytes(true, M, N, K, r);
     case NF4_OP_MERGE: return nf4::kWsHeader;
+    case NF4_OP_GROUPED_FWD: return nf4::kWsHeader + nf4::grouped_workspace_bytes(false, M, N, K, r);
+    case NF4_OP_GROUPED_BWD: return nf4::kWsHeader + nf4::grouped_workspace_bytes(true, M, N, K, r);
+    case NF4_OP_INT8_LINEAR: return int8_linear_ws(M, K);
     default: return 0;
   }
 }
@@ -467,6 +477,165 @@ nf4_status nf4_merge(const nf4_weight* w, const void* A, const void* B, int r, f
   const int kind = out_dtype == NF4_F32 ? nf4::kMergeF32 : (out_dtype == NF4_F16 ? nf4::kMergeF16 : nf4::kMergeBf16);
   const cudaError_t e = nf4::launch_merge(*w, A, B, r, alpha, kind, out,
                                           status, static_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks and common arguments of the two grouped entry points.  With M == 0
+// there are no activations: x may be null.
+nf4_status grouped_args(const nf4_weight* w, int num_experts, const void* x, int64_t M,
+                        const int32_t* offsets, const void* A, const void* B, int r, float alpha,
+                        int compute_dtype, void* workspace, size_t ws_bytes, bool backward,
+                        nf4::GroupedArgs* out) {
+  if (M < 0) return NF4_ERR_SHAPE;
+  // the linear checks; with no rows A stands in for x
+  const nf4_status s = check_linear(w, M > 0 ? x : A, M > 0 ? M : 1, A, B, r, alpha, compute_dtype);
+  if (s != NF4_OK) return s;
+  if (offsets == nullptr || num_experts < 1 || num_experts > nf4::kMaxExperts) return NF4_ERR_INVALID_ARG;
+  if (w->rows % num_experts != 0 || (w->rows / num_experts) % 8 != 0) return NF4_ERR_SHAPE;
+  const int64_t N = w->rows / num_experts;
+  // offsets are 32-bit, and the tile arithmetic stays below them
+  if (M > (int64_t(1) << 30) || N > (int64_t(1) << 30) || w->cols > (int64_t(1) << 30)) return NF4_ERR_SHAPE;
+  if (!aligned4(offsets)) return NF4_ERR_ALIGNMENT;
+  if (workspace == nullptr || !aligned16(workspace)) return NF4_ERR_WORKSPACE;
+  if (ws_bytes < nf4_workspace_bytes(backward ? NF4_OP_GROUPED_BWD : NF4_OP_GROUPED_FWD, M, N, w->cols, r, 64,
+                                     w->double_quant))
+    return NF4_ERR_WORKSPACE;
+  *out = nf4::GroupedArgs{};
+  out->E = num_experts;
+  out->offsets = offsets;
+  nf4::LinearArgs& a = out->lin;
+  a.w = w;
+  a.M = M;
+  a.N = N;
+  a.K = w->cols;
+  a.r = r;
+  a.s = alpha / float(r);
+  a.f16 = compute_dtype == NF4_F16 ? 1 : 0;
+  a.f32 = compute_dtype == NF4_F32 ? 1 : 0;
+  a.x = x;
+  a.A = A;
+  a.B = B;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.ws_bytes = ws_bytes;
+  a.status = reinterpret_cast<uint32_t*>(a.ws + nf4::kWsStatus);
+  return NF4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nf4_status qlora_grouped_fwd(const nf4_weight* w, int num_experts, const void* x, int64_t M,
+                             const int32_t* offsets, const void* A, const void* B, int r, float alpha,
+                             int compute_dtype, const void* bias, void* y, void* t_out, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  NF4_API_RANGE("qlora_grouped_fwd");
+  nf4::GroupedArgs g;
+  const nf4_status s = grouped_args(w, num_experts, x, M, offsets, A, B, r, alpha, compute_dtype, workspace,
+                                    ws_bytes, false, &g);
+  if (s != NF4_OK) return s;
+  if (M > 0 && y == nullptr) return NF4_ERR_INVALID_ARG;
+  if ((y && !aligned16(y)) || (bias && !aligned16(bias)) || (t_out && !aligned16(t_out)))
+    return NF4_ERR_ALIGNMENT;
+  if (M == 0) return NF4_OK;
+  g.lin.bias = bias;
+  g.lin.y = y;
+  g.lin.t_out = t_out;
+  int launches = 0;
+  const cudaError_t e = nf4::launch_grouped_fwd(g, sm_count(), static_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches);
+}
+
+nf4_status qlora_grouped_bwd(const nf4_weight* w, int num_experts, const void* x, int64_t M,
+                             const int32_t* offsets, const void* A, const void* B, int r, float alpha,
+                             int compute_dtype, const void* dy, const void* t, float* dA, float* dB,
+                             void* dx, void* workspace, size_t ws_bytes, void* stream) {
+  NF4_API_RANGE("qlora_grouped_bwd");
+  nf4::GroupedArgs g;
+  const nf4_status s = grouped_args(w, num_experts, x, M, offsets, A, B, r, alpha, compute_dtype, workspace,
+                                    ws_bytes, true, &g);
+  if (s != NF4_OK) return s;
+  if ((M > 0 && dy == nullptr) || dA == nullptr || dB == nullptr) return NF4_ERR_INVALID_ARG;
+  if ((dy && !aligned16(dy)) || !aligned16(dA) || !aligned16(dB) || (dx && !aligned16(dx)) ||
+      (t && !aligned16(t)))
+    return NF4_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) {   // no rows: every gradient is zero
+    const size_t per = size_t(num_experts) * size_t(r) * sizeof(float);
+    if (cudaMemsetAsync(dA, 0, per * size_t(g.lin.K), st) != cudaSuccess ||
+        cudaMemsetAsync(dB, 0, per * size_t(g.lin.N), st) != cudaSuccess)
+      return NF4_ERR_CUDA;
+    return NF4_OK;
+  }
+  g.lin.dy = dy;
+  g.lin.t_in = t;
+  g.lin.dA = dA;
+  g.lin.dB = dB;
+  g.lin.dx = dx;
+  int launches = 0;
+  const cudaError_t e = nf4::launch_grouped_bwd(g, sm_count(), st, &launches);
+  return finish(e, launches);
+}
+
+nf4_status int8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols, int8_t* codes,
+                         float* scales, void* stream) {
+  NF4_API_RANGE("int8_quantize");
+  if (in_dtype != NF4_F32 && in_dtype != NF4_BF16 && in_dtype != NF4_F16) return NF4_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX) return NF4_ERR_SHAPE;
+  if (rows == 0) return NF4_OK;
+  if (scales == nullptr || (cols > 0 && (x == nullptr || codes == nullptr))) return NF4_ERR_INVALID_ARG;
+  if (!aligned4(scales) || (x && !aligned16(x)) || (codes && !aligned16(codes))) return NF4_ERR_ALIGNMENT;
+  int launches = 0;
+  const cudaError_t e = nf4::launch_int8_quantize(x, in_dtype, rows, cols, codes, scales, sm_count(),
+                                                  static_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches);
+}
+
+nf4_status int8_linear_fwd(const int8_t* w_codes, const float* w_scale, int64_t N, int64_t K, const void* x,
+                           const float* x_scale, int64_t M, int compute_dtype, const void* bias, void* y,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  NF4_API_RANGE("int8_linear_fwd");
+  if (w_codes == nullptr || w_scale == nullptr || x == nullptr || y == nullptr) return NF4_ERR_INVALID_ARG;
+  if (compute_dtype != NF4_BF16 && compute_dtype != NF4_F16 && compute_dtype != NF4_F32)
+    return NF4_ERR_INVALID_ARG;
+  // K <= 131072 keeps 127 * 127 * K below 2^31
+  if (M < 1 || N < 1 || K < 16 || N % 8 != 0 || K % 16 != 0 || K > 131072 || M > (int64_t(1) << 30) ||
+      N > (int64_t(1) << 30))
+    return NF4_ERR_SHAPE;
+  if (!aligned16(w_codes) || !aligned4(w_scale) || !aligned16(x) || (x_scale && !aligned4(x_scale)) ||
+      !aligned16(y) || (bias && !aligned16(bias)))
+    return NF4_ERR_ALIGNMENT;
+  if (workspace == nullptr || !aligned16(workspace)) return NF4_ERR_WORKSPACE;
+  if (ws_bytes < int8_linear_ws(M, K)) return NF4_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  nf4::Int8LinearArgs a{};
+  a.w = w_codes;
+  a.w_scale = w_scale;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.dtype = compute_dtype;
+  a.bias = bias;
+  a.y = y;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.status = reinterpret_cast<uint32_t*>(a.ws + nf4::kWsStatus);
+  int launches = 0;
+  cudaError_t e = cudaSuccess;
+  if (x_scale == nullptr) {
+    int8_t* codes = reinterpret_cast<int8_t*>(a.ws + nf4::kWsHeader);
+    float* scales = reinterpret_cast<float*>(codes + round_up(size_t(M) * size_t(K), 256));
+    e = nf4::launch_int8_quantize(x, compute_dtype, M, K, codes, scales, sm_count(), st, &launches);
+    a.x = codes;
+    a.x_scale = scales;
+  } else {
+    a.x = static_cast<const int8_t*>(x);
+    a.x_scale = x_scale;
+  }
+  if (e == cudaSuccess) e = nf4::launch_int8_linear(a, sm_count(), st, &launches);
   return finish(e, launches);
 }
 

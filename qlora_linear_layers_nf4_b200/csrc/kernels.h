@@ -118,6 +118,41 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, int sms, cudaStream_t stream,
 cudaError_t launch_linear_fwd_f32(const LinearArgs& a, cudaStream_t stream, int* launches);
 cudaError_t launch_linear_bwd_f32(const LinearArgs& a, cudaStream_t stream, int* launches);
 
+// ---- experts (grouped.cu, grouped_f32.cu) ----
+
+constexpr int kMaxExperts = 512;
+
+// lin: the layer of one expert (N = rows of an expert; w, A, B, bias, dA, dB
+// hold all E experts one after another); rows of x, y, ... sorted by expert.
+struct GroupedArgs {
+  LinearArgs lin;
+  int E;
+  const int32_t* offsets;   // device, [E + 1]
+};
+
+size_t grouped_workspace_bytes(bool backward, int64_t M, int64_t N, int64_t K, int r);
+cudaError_t launch_grouped_fwd(const GroupedArgs& a, int sms, cudaStream_t stream, int* launches);
+cudaError_t launch_grouped_bwd(const GroupedArgs& a, int sms, cudaStream_t stream, int* launches);
+
+// ---- 8-bit integers (int8.cu) ----
+
+struct Int8LinearArgs {
+  const int8_t* w;
+  const float* w_scale;
+  int64_t M, N, K;
+  const int8_t* x;         // [M, K] codes
+  const float* x_scale;    // [M]
+  int dtype;               // of y and bias
+  const void* bias;
+  void* y;
+  uint8_t* ws;
+  uint32_t* status;
+};
+
+cudaError_t launch_int8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols, int8_t* codes,
+                                 float* scales, int sms, cudaStream_t stream, int* launches);
+cudaError_t launch_int8_linear(const Int8LinearArgs& a, int sms, cudaStream_t stream, int* launches);
+
 // Bounded-wait self-check (selfcheck.cu): waits that nothing completes give
 // up after limit_ns, record NF4_ERR_TIMEOUT in *status and raise the abort
 // flag, which the second role counts into *seen_abort (one per CTA).
@@ -151,6 +186,14 @@ enum KernelId {
   kKAdapterU,        // adapter_gemm computing U = s dy B
   kKAdapterDB,       // adapter_gemm computing dB = dy^T T
   kKAdapterDA,       // adapter_gemm computing dA^T = x^T U
+  kKGroupedT,        // experts: T = s x A_e^T
+  kKGroupedFwd,      // experts: y
+  kKGroupedU,        // experts: U = s dy B_e
+  kKGroupedDB,       // experts: dB_e = dy^T T
+  kKGroupedDA,       // experts: dA_e = U^T x
+  kKGroupedDx,       // experts: dx
+  kKInt8Quantize,
+  kKInt8Linear,
   kNumKernelIds
 };
 

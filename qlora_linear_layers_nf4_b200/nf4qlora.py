@@ -22,6 +22,7 @@ STATUS_NAMES = {
 }
 NF4_F32, NF4_BF16, NF4_F16 = 0, 1, 2
 OP_QUANTIZE, OP_DEQUANTIZE, OP_LINEAR_FWD, OP_LINEAR_BWD, OP_MERGE = 0, 1, 2, 3, 4
+OP_GROUPED_FWD, OP_GROUPED_BWD, OP_INT8_LINEAR = 5, 6, 7
 
 EXPORTED = (
     "nf4_status_string", "nf4_version", "nf4_codebook", "nf4_launch_count",
@@ -29,7 +30,7 @@ EXPORTED = (
     "nf4_profile_get", "nf4_workspace_bytes", "nf4_read_status", "nf4_quantize",
     "nf4_dequantize", "qlora_linear_fwd", "qlora_linear_bwd", "nf4_quantize_noalloc",
     "nf4_merge", "nf4_quantize_typed", "nf4_check_wait_timeout", "nf4_absmax_max",
-    "nf4_double_quant",
+    "nf4_double_quant", "qlora_grouped_fwd", "qlora_grouped_bwd", "int8_quantize", "int8_linear_fwd",
 )
 
 
@@ -107,6 +108,16 @@ def lib() -> ctypes.CDLL:
     L.nf4_absmax_max.restype = i32
     L.nf4_double_quant.argtypes = [vp, i64, vp, vp, vp, vp]
     L.nf4_double_quant.restype = i32
+    L.qlora_grouped_fwd.argtypes = [ctypes.POINTER(CWeight), i32, vp, i64, vp, vp, vp, i32, f32, i32, vp,
+                                    vp, vp, vp, sz, vp]
+    L.qlora_grouped_fwd.restype = i32
+    L.qlora_grouped_bwd.argtypes = [ctypes.POINTER(CWeight), i32, vp, i64, vp, vp, vp, i32, f32, i32, vp,
+                                    vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_grouped_bwd.restype = i32
+    L.int8_quantize.argtypes = [vp, i32, i64, i64, vp, vp, vp]
+    L.int8_quantize.restype = i32
+    L.int8_linear_fwd.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, sz, vp]
+    L.int8_linear_fwd.restype = i32
     _lib = L
     return L
 
@@ -398,3 +409,182 @@ def linear_bwd(q: QuantizedWeight, x, A, B, alpha: float, dy, t=None, want_dx: b
                                 _ptr(buf), buf.numel(), _stream(stream))
     _check(st, "qlora_linear_bwd")
     return dA, dB, dx
+
+
+_stream_ws = {}
+
+
+def _on_stream(stream):
+    """Context in which a call on `stream` allocates: the stream's own device and
+    memory pool, so that nothing the call uses is handed out again before that
+    stream has finished with it (None: the current stream, nothing to do)."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _scratch(workspace: Workspace | None, device, nbytes: int):
+    """Device scratch of a call on the current stream.
+
+    A given workspace is used as it is (calls that share one must be ordered).
+    Otherwise every stream has a buffer of its own, and while a CUDA graph is
+    being captured the call takes fresh memory of that graph's pool, so two
+    graphs, or a graph and eager calls, never share scratch."""
+    import torch
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current CUDA device")
+    if workspace is not None:
+        return workspace.get(nbytes)
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        buf[:256].zero_()   # the status word
+        return buf
+    key = (device.index, torch.cuda.current_stream().cuda_stream)
+    ws = _stream_ws.get(key)
+    if ws is None:
+        ws = _stream_ws[key] = Workspace(device)
+    return ws.get(nbytes)
+
+
+def _grouped_shapes(q: QuantizedWeight, x, offsets, A):
+    """(M, E, N, K, r) of a grouped call; the experts' weights are stacked row-wise in q."""
+    import torch
+    if x.dim() != 2 or A.dim() != 3:
+        raise ValueError("x must be 2-D ([M, K]) and A 3-D ([num_experts, r, K])")
+    E, r = int(A.shape[0]), int(A.shape[1])
+    if E < 1 or q.rows % E:
+        raise ValueError(f"the weight's {q.rows} rows do not divide into {E} experts")
+    _expect("offsets", offsets, (E + 1,), torch.int32, q.device)
+    return int(x.shape[0]), E, q.rows // E, q.cols, r
+
+
+def grouped_fwd(q: QuantizedWeight, x, offsets, A, B, alpha: float, bias=None, want_t: bool = True,
+                out=None, t_out=None, workspace: Workspace | None = None, stream=None):
+    """QLoRA linear of a stack of experts; returns (y, T or None).
+
+    q stacks the experts' weights row-wise (rows = num_experts * N); A is
+    [num_experts, r, K], B [num_experts, N, r], bias [num_experts, N].  Row m of
+    x [M, K] belongs to the expert e with offsets[e] <= m < offsets[e + 1]
+    (offsets int32 [num_experts + 1] on the GPU).  Rows that belong to no expert
+    are left as they are in `out` and `t_out` (unset in tensors made here)."""
+    import torch
+    dt = _compute_dtype(x)
+    M, E, N, K, r = _grouped_shapes(q, x, offsets, A)
+    dev = q.device
+    _expect("x", x, (M, K), x.dtype, dev)
+    _expect("A", A, (E, r, K), x.dtype, dev)
+    _expect("B", B, (E, N, r), x.dtype, dev)
+    _expect("bias", bias, (E, N), x.dtype, dev)
+    _expect("out", out, (M, N), x.dtype, dev)
+    _expect("t_out", t_out, (M, r), x.dtype, dev)
+    with _on_stream(stream):
+        buf = _scratch(workspace, dev, workspace_bytes(OP_GROUPED_FWD, M, N, K, r, q.block_size, q.double_quant))
+        y = out if out is not None else torch.empty((M, N), dtype=x.dtype, device=dev)
+        if want_t and t_out is None:
+            t_out = torch.empty((M, r), dtype=x.dtype, device=dev)
+        cw = q.c_struct()
+        _check(lib().qlora_grouped_fwd(ctypes.byref(cw), E, _ptr(x), M, _ptr(offsets), _ptr(A), _ptr(B), r,
+                                       float(alpha), dt, _ptr(bias), _ptr(y), _ptr(t_out), _ptr(buf),
+                                       buf.numel(), _stream(stream)), "qlora_grouped_fwd")
+    return y, t_out
+
+
+def grouped_bwd(q: QuantizedWeight, x, offsets, A, B, alpha: float, dy, t=None, want_dx: bool = True,
+                dA=None, dB=None, dx=None, workspace: Workspace | None = None, stream=None):
+    """Adapter backward of grouped_fwd; returns (dA fp32 [E, r, K], dB fp32 [E, N, r],
+    dx [M, K] in x's dtype or None).  Experts without rows get zero gradients."""
+    import torch
+    dt = _compute_dtype(x)
+    M, E, N, K, r = _grouped_shapes(q, x, offsets, A)
+    dev = q.device
+    _expect("x", x, (M, K), x.dtype, dev)
+    _expect("A", A, (E, r, K), x.dtype, dev)
+    _expect("B", B, (E, N, r), x.dtype, dev)
+    _expect("dy", dy, (M, N), x.dtype, dev)
+    _expect("t", t, (M, r), x.dtype, dev)
+    _expect("dA", dA, (E, r, K), torch.float32, dev)
+    _expect("dB", dB, (E, N, r), torch.float32, dev)
+    _expect("dx", dx, (M, K), x.dtype, dev)
+    with _on_stream(stream):
+        buf = _scratch(workspace, dev, workspace_bytes(OP_GROUPED_BWD, M, N, K, r, q.block_size, q.double_quant))
+        dA = dA if dA is not None else torch.empty((E, r, K), dtype=torch.float32, device=dev)
+        dB = dB if dB is not None else torch.empty((E, N, r), dtype=torch.float32, device=dev)
+        if want_dx and dx is None:
+            dx = torch.empty((M, K), dtype=x.dtype, device=dev)
+        cw = q.c_struct()
+        _check(lib().qlora_grouped_bwd(ctypes.byref(cw), E, _ptr(x), M, _ptr(offsets), _ptr(A), _ptr(B), r,
+                                       float(alpha), dt, _ptr(dy), _ptr(t), _ptr(dA), _ptr(dB), _ptr(dx),
+                                       _ptr(buf), buf.numel(), _stream(stream)), "qlora_grouped_bwd")
+    return dA, dB, dx
+
+
+@dataclass
+class Int8Matrix:
+    """Device tensors of a matrix in 8-bit integers with one scale per row."""
+    codes: object                    # int8 [rows, cols]
+    scale: object                    # fp32 [rows]
+
+    def dequantize(self):
+        """The fp32 matrix that the codes and scales stand for."""
+        return self.codes * self.scale[:, None]
+
+
+def int8_quantize(x, codes=None, scale=None, stream=None) -> Int8Matrix:
+    """Quantize the rows of a 2-D float32, bfloat16 or float16 CUDA tensor to 8-bit
+    integers, one scale per row (per token, or per output channel of a weight)."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D ([rows, cols])")
+    dt = _compute_dtype(x)
+    rows, cols = int(x.shape[0]), int(x.shape[1])
+    _expect("x", x, (rows, cols), x.dtype, x.device)
+    _expect("codes", codes, (rows, cols), torch.int8, x.device)
+    _expect("scale", scale, (rows,), torch.float32, x.device)
+    with _on_stream(stream):
+        if x.device.type != "cuda" or x.device.index != torch.cuda.current_device():
+            raise ValueError(f"x is on {x.device}, which is not the current CUDA device")
+        codes = codes if codes is not None else torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+        scale = scale if scale is not None else torch.empty(rows, dtype=torch.float32, device=x.device)
+        _check(lib().int8_quantize(_ptr(x), dt, rows, cols, _ptr(codes), _ptr(scale), _stream(stream)),
+               "int8_quantize")
+    return Int8Matrix(codes, scale)
+
+
+def int8_linear_fwd(w: Int8Matrix, x, bias=None, out_dtype=None, out=None,
+                    workspace: Workspace | None = None, stream=None):
+    """y = (codes_x codes_w^T) scale_x scale_w (+ bias), [M, N].
+
+    x is a bfloat16, float16 or float32 tensor [M, K], quantized per row in the
+    call (y comes back in its dtype), or an Int8Matrix (y in `out_dtype`,
+    bfloat16 unless given)."""
+    import torch
+    if w.codes.dim() != 2:
+        raise ValueError("w.codes must be 2-D ([N, K])")
+    N, K = int(w.codes.shape[0]), int(w.codes.shape[1])
+    dev = w.codes.device
+    _expect("w.codes", w.codes, (N, K), torch.int8, dev)
+    _expect("w.scale", w.scale, (N,), torch.float32, dev)
+    if isinstance(x, Int8Matrix):
+        xv, xs, want = x.codes, x.scale, torch.int8
+        y_dtype = out_dtype if out_dtype is not None else torch.bfloat16
+    else:
+        xv, xs, want = x, None, x.dtype
+        y_dtype = x.dtype
+        if out_dtype is not None and out_dtype != y_dtype:
+            raise TypeError(f"out_dtype: {out_dtype}, but a {y_dtype} x gives a {y_dtype} y")
+    dt = {torch.bfloat16: NF4_BF16, torch.float16: NF4_F16, torch.float32: NF4_F32}.get(y_dtype)
+    if dt is None:
+        raise TypeError(f"compute dtype must be bfloat16, float16 or float32, got {y_dtype}")
+    if xv.dim() != 2:
+        raise ValueError("x must be 2-D ([M, K])")
+    M = int(xv.shape[0])
+    _expect("x", xv, (M, K), want, dev)
+    _expect("x.scale", xs, (M,), torch.float32, dev)
+    _expect("bias", bias, (N,), y_dtype, dev)
+    _expect("out", out, (M, N), y_dtype, dev)
+    with _on_stream(stream):
+        buf = _scratch(workspace, dev, workspace_bytes(OP_INT8_LINEAR, M, N, K, 0, 0, False))
+        y = out if out is not None else torch.empty((M, N), dtype=y_dtype, device=dev)
+        _check(lib().int8_linear_fwd(_ptr(w.codes), _ptr(w.scale), N, K, _ptr(xv), _ptr(xs), M, dt, _ptr(bias),
+                                     _ptr(y), _ptr(buf), buf.numel(), _stream(stream)), "int8_linear_fwd")
+    return y
