@@ -1,0 +1,62 @@
+// QLoRA linear of a stack of experts: the launches of a call.  Every launch is
+// prepared (its tensor maps encoded) before the first is enqueued, so a call
+// that fails on the host enqueues nothing.
+#include "expert_gemm.h"
+#include "expert_rank.h"
+#include "kernels.h"
+#include "nf4_common.cuh"
+
+namespace nf4 {
+namespace {
+
+// One [M, r] scratch matrix, sized for fp32 so that the same workspace serves
+// every compute dtype; U's two 16-bit terms share one.
+size_t mr_bytes(int64_t M, int r) { return (size_t(M) * size_t(r) * 4 + 255) / 256 * 256; }
+
+}  // namespace
+
+// fwd: [T]; bwd: [T] [U]
+size_t grouped_workspace_bytes(bool backward, int64_t M, int64_t N, int64_t K, int r) {
+  (void)N;
+  (void)K;
+  if (M < 0 || r < 0) return 0;
+  return (backward ? 2 : 1) * mr_bytes(M, r);
+}
+
+cudaError_t launch_grouped_fwd(const GroupedArgs& g, int sms, cudaStream_t st, int* launches) {
+  const LinearArgs& a = g.lin;
+  if (a.f32) return launch_grouped_fwd_f32(g, st, launches);
+  void* T = a.t_out ? a.t_out : a.ws + kWsHeader;
+  ExpertRank t;
+  ExpertGemm y;
+  if (!t.prepare(g, kRankT, nullptr, nullptr, T, nullptr) || !y.prepare(g, false, T, sms)) return cudaErrorInvalidValue;
+  cudaError_t e = t.run(st, launches, false);
+  if (e == cudaSuccess) e = y.run(st, launches);
+  return e;
+}
+
+cudaError_t launch_grouped_bwd(const GroupedArgs& g, int sms, cudaStream_t st, int* launches) {
+  const LinearArgs& a = g.lin;
+  if (a.f32) return launch_grouped_bwd_f32(g, st, launches);
+  uint8_t* ws = a.ws + kWsHeader;
+  const void* T = a.t_in ? a.t_in : ws;
+  uint8_t* U = ws + mr_bytes(a.M, a.r);
+  uint8_t* U_lo = U + size_t(a.M) * size_t(a.r) * 2;   // r % 8 == 0: 16-byte aligned
+  ExpertRank t, u, db, da;
+  ExpertGemm dx;
+  bool ok = a.t_in != nullptr || t.prepare(g, kRankT, nullptr, nullptr, ws, nullptr);
+  ok = ok && u.prepare(g, kRankU, nullptr, nullptr, U, U_lo);
+  ok = ok && db.prepare(g, kRankDB, T, nullptr, a.dB, nullptr);
+  ok = ok && da.prepare(g, kRankDA, U, U_lo, a.dA, nullptr);
+  ok = ok && (a.dx == nullptr || dx.prepare(g, true, U, sms));
+  if (!ok) return cudaErrorInvalidValue;
+  cudaError_t e = cudaSuccess;
+  if (a.t_in == nullptr) e = t.run(st, launches, false);
+  if (e == cudaSuccess) e = u.run(st, launches, false);
+  if (e == cudaSuccess && a.dx != nullptr) e = dx.run(st, launches);
+  if (e == cudaSuccess) e = db.run(st, launches, false);
+  if (e == cudaSuccess) e = da.run(st, launches, false);
+  return e;
+}
+
+}  // namespace nf4

@@ -290,14 +290,7 @@ size_t mr_bytes(int64_t M, int r) { return (size_t(M) * size_t(r) * sizeof(float
 
 }  // namespace
 
-size_t grouped_workspace_bytes(bool backward, int64_t M, int64_t N, int64_t K, int r) {
-  (void)N;
-  (void)K;
-  return (backward ? 2 : 1) * mr_bytes(M, r);
-}
-
-cudaError_t launch_grouped_fwd(const GroupedArgs& g, int sms, cudaStream_t st, int* launches) {
-  (void)sms;
+cudaError_t launch_grouped_fwd_f32(const GroupedArgs& g, cudaStream_t st, int* launches) {
   const LinearArgs& a = g.lin;
   void* T = a.t_out ? a.t_out : a.ws + kWsHeader;
   Launch l[2];
@@ -322,8 +315,7 @@ cudaError_t launch_grouped_fwd(const GroupedArgs& g, int sms, cudaStream_t st, i
   return e;
 }
 
-cudaError_t launch_grouped_bwd(const GroupedArgs& g, int sms, cudaStream_t st, int* launches) {
-  (void)sms;
+cudaError_t launch_grouped_bwd_f32(const GroupedArgs& g, cudaStream_t st, int* launches) {
   const LinearArgs& a = g.lin;
   uint8_t* ws = a.ws + kWsHeader;
   const void* T = a.t_in ? a.t_in : ws;

@@ -9,6 +9,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "expert_gemm.h"
 #include "kernels.h"
 #include "nf4_common.cuh"
 #include "tc_common.cuh"
@@ -179,63 +180,6 @@ cudaError_t quantize_t(const void* x, int64_t rows, int64_t cols, int8_t* codes,
              : cudaLaunchKernelEx(&cfg, int8_quantize_kernel<T, false>, xt, int(cols), codes, scales);
 }
 
-// ------------------------------------------------------------------ linear
-
-// 64 x 64 outputs a CTA, 256 threads with 4 x 4 int32 sums each over packed
-// groups of four codes.
-constexpr int kITile = 64;
-constexpr int kIThreads = 256;
-
-__device__ __forceinline__ void store_out(void* y, int dtype, int64_t at, float v) {
-  if (dtype == NF4_F32) static_cast<float*>(y)[at] = v;
-  else if (dtype == NF4_F16) static_cast<__half*>(y)[at] = __float2half_rn(v);
-  else static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
-}
-__device__ __forceinline__ float load_bias(const void* b, int dtype, int64_t at) {
-  if (dtype == NF4_F32) return static_cast<const float*>(b)[at];
-  if (dtype == NF4_F16) return __half2float(static_cast<const __half*>(b)[at]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(b)[at]);
-}
-
-__global__ void __launch_bounds__(kIThreads) int8_linear_kernel(const Int8LinearArgs a, int col_tiles) {
-  __shared__ int sx[16][kITile + 1];
-  __shared__ int sw[16][kITile + 1];
-  const int t = threadIdx.x;
-  const int64_t m0 = int64_t(blockIdx.x / col_tiles) * kITile, n0 = int64_t(blockIdx.x % col_tiles) * kITile;
-  const int ty = t >> 4, tx = t & 15;
-  int acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < a.K; k0 += 64) {
-    const int row = t >> 2, c = t & 3;
-    int4 vx = make_int4(0, 0, 0, 0), vw = vx;
-    const bool in = k0 + 16 * c < a.K;   // K is a multiple of 16
-    if (in && m0 + row < a.M) vx = *reinterpret_cast<const int4*>(a.x + (m0 + row) * a.K + k0 + 16 * c);
-    if (in && n0 + row < a.N) vw = *reinterpret_cast<const int4*>(a.w + (n0 + row) * a.K + k0 + 16 * c);
-    sx[4 * c][row] = vx.x; sx[4 * c + 1][row] = vx.y; sx[4 * c + 2][row] = vx.z; sx[4 * c + 3][row] = vx.w;
-    sw[4 * c][row] = vw.x; sw[4 * c + 1][row] = vw.y; sw[4 * c + 2][row] = vw.z; sw[4 * c + 3][row] = vw.w;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(sx[k][4 * ty + i], sw[k][tx + 16 * j], acc[i][j]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + 4 * ty + i;
-    if (m >= a.M) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + tx + 16 * j;
-      if (n >= a.N) continue;
-      float v = __fmul_rn(__fmul_rn(float(acc[i][j]), a.x_scale[m]), a.w_scale[n]);
-      if (a.bias != nullptr) v = __fadd_rn(v, load_bias(a.bias, a.dtype, n));
-      store_out(a.y, a.dtype, m * a.N + n, v);
-    }
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_int8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols, int8_t* codes,
@@ -252,15 +196,7 @@ cudaError_t launch_int8_quantize(const void* x, int in_dtype, int64_t rows, int6
 }
 
 cudaError_t launch_int8_linear(const Int8LinearArgs& a, int sms, cudaStream_t st, int* launches) {
-  (void)sms;
-  const int64_t ct = (a.N + kITile - 1) / kITile, rt = (a.M + kITile - 1) / kITile;
-  if (ct * rt > int64_t(0x7fffffff)) return cudaErrorInvalidValue;
-  NF4_PROF_BEGIN(st, kKInt8Linear);
-  int8_linear_kernel<<<unsigned(ct * rt), kIThreads, 0, st>>>(a, int(ct));
-  NF4_PROF_END(st, kKInt8Linear);
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) ++*launches;
-  return e;
+  return launch_int8_gemm(a, sms, st, launches);
 }
 
 }  // namespace nf4

@@ -133,6 +133,9 @@ struct GroupedArgs {
 size_t grouped_workspace_bytes(bool backward, int64_t M, int64_t N, int64_t K, int r);
 cudaError_t launch_grouped_fwd(const GroupedArgs& a, int sms, cudaStream_t stream, int* launches);
 cudaError_t launch_grouped_bwd(const GroupedArgs& a, int sms, cudaStream_t stream, int* launches);
+// The F32 compute dtype, on the CUDA cores (grouped_simt.cu).
+cudaError_t launch_grouped_fwd_f32(const GroupedArgs& a, cudaStream_t stream, int* launches);
+cudaError_t launch_grouped_bwd_f32(const GroupedArgs& a, cudaStream_t stream, int* launches);
 
 // ---- 8-bit integers (int8.cu) ----
 
