@@ -4,20 +4,24 @@
 //   kDx    dx[m, k] = sum_n W'_e[n, k] dy[m, n] + sum_j A_e[j, k] U[m, j]
 //   kI8    y[m, n]  = (sum_k wq[n, k] xq[m, k]) sx[m] sw[n] (+ bias[n])
 //
-// The weight is the A operand of the MMA (128 outputs of an expert = the 128
-// TMEM lanes) and the tokens are the B operand, whose count is any multiple of
-// 16 up to 256: an expert's ragged rows are cut into even tiles that waste at
-// most 15 columns, where tokens on the lanes would waste up to 127.  It also
-// puts the outputs' contiguous dimension on the lanes, so a row's results are
-// stored under its own row predicate, rows of other experts untouched.
+// The weight is the A operand of the MMA (an expert's outputs on the TMEM
+// lanes) and the tokens are the B operand, whose count is any multiple of 16 up
+// to 256: an expert's ragged rows are cut into even tiles that waste at most 15
+// columns, where tokens on the lanes would waste up to 127.  It also puts the
+// outputs' contiguous dimension on the lanes, so a row's results are stored
+// under its own row predicate and rows of other experts stay untouched.
 //
-// One persistent CTA per SM walks over (expert, 128 outputs, token tile); the
-// tile list comes from the offsets in device memory, scanned once per CTA.
-// Roles: two token-tile TMA producers, one producer of the weight side (NF4
-// code boxes or the int8 tile), one MMA issuer, four epilogue warps, eight
-// dequant warps (NF4).  Rings: four stages of [weight tile 16 KB | token tile
-// 32 KB], three code boxes of two K steps; two accumulators of 256 TMEM
-// columns, so a tile's epilogue runs under the next tile's MMAs.
+// Two CTAs on two SMs form a pair (cta_group::2, M = 256): each holds 128 of a
+// tile's 256 weight rows and half of its tokens, so the tokens' shared-memory
+// traffic, which bounds a single CTA (104 KB a step of 512 MMA cycles at 128
+// bytes a cycle), is shared.  Persistent pairs walk over (expert, 256 outputs,
+// token tile); the tile list comes from the offsets in device memory, scanned
+// once per CTA.
+// Roles in each CTA: warp 0 token TMA, warp 1 weight-side TMA (NF4 codes or the
+// int8 tile), warp 2 MMA (issued by the pair's leader), warps 4-7 epilogue,
+// warps 8-19 dequant (NF4).  Rings: six stages of [weight tile 16 KB | tokens
+// 16 KB] with a code slot each; two accumulators of 256 TMEM columns, so a
+// tile's epilogue runs under the next tile's MMAs.
 #include <algorithm>
 
 #include <cuda.h>
@@ -29,6 +33,7 @@
 #include "kernels.h"
 #include "nf4_common.cuh"
 #include "nf4_dequant.cuh"
+#include "ring_wait.cuh"
 #include "tc_common.cuh"
 #include "tensor_maps.h"
 
@@ -42,25 +47,24 @@ constexpr int kFwd = 0;
 constexpr int kDx = 1;
 constexpr int kI8 = 2;
 
-constexpr int kTileW = 128;                 // outputs per tile
-constexpr int kTileT = 256;                 // tokens per tile at most
-constexpr int kStages = 4;
-constexpr uint32_t kWBytes = 128 * 128;     // weight tile: 128 x 128 bytes
-constexpr uint32_t kTBytes = 256 * 128;     // token tile
+constexpr int kTileW = 256;                 // outputs per tile, 128 in each CTA
+constexpr int kTileT = 256;                 // tokens per tile at most, half in each CTA
+constexpr int kStages = 6;
+constexpr uint32_t kWBytes = 128 * 128;     // weight tile of a CTA: 128 x 128 bytes
+constexpr uint32_t kTBytes = 128 * 128;     // its tokens
 constexpr uint32_t kStageBytes = kWBytes + kTBytes;
-constexpr int kCodeSteps = 2;               // K steps per code box
-constexpr int kCodeSlots = 3;
-constexpr uint32_t kCodeBytes = 128 * 64;
-constexpr int kDeqWarps = 8;
+constexpr uint32_t kCodeBytes = 128 * 32;   // kDx: NF4 codes of one step, a slot per stage
 constexpr int kEpiWarp = 4;                 // warps 4..7
-constexpr int kDeqWarp = 8;                 // warps 8..15
+constexpr int kDeqWarp = 8;
+constexpr int kDeqGroups = 3;               // of four warps; kStages is a multiple
+constexpr int kThreads = 32 * (kDeqWarp + 4 * kDeqGroups);
+constexpr int kThreadsI8 = 32 * kDeqWarp;
 
 struct GemmShared {
-  uint64_t full[kStages];       // TMA bytes of a stage landed
-  uint64_t wready[kStages];     // dequantized weight tile written (8 warp arrivals)
+  uint64_t full[kStages];       // leader: both CTAs' bytes landed and weight tiles written
   uint64_t empty[kStages];      // the MMAs that read a stage finished
-  uint64_t cfull[kCodeSlots];
-  uint64_t cempty[kCodeSlots];
+  uint64_t cfull[kStages];      // kDx: a step's codes landed
+  uint64_t cempty[kStages];     // kDx: and were read
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t drain;               // after an abort
@@ -69,19 +73,19 @@ struct GemmShared {
   GroupTable groups;
 };
 
-constexpr size_t gemm_smem(bool i8) {
-  return size_t(kStages) * kStageBytes + (i8 ? 0 : size_t(kCodeSlots) * kCodeBytes) + sizeof(GemmShared) + 1024;
+constexpr size_t gemm_smem(int mode) {
+  return size_t(kStages) * (kStageBytes + (mode == kDx ? kCodeBytes : 0)) + sizeof(GemmShared) + 1024;
 }
-static_assert(gemm_smem(false) <= 232448, "shared memory of one CTA");
+static_assert(gemm_smem(kDx) <= 232448, "shared memory of one CTA");
 
 // int8 x int8 -> int32 MMA and its instruction descriptor (kind::i8: D s32,
 // A and B signed 8-bit, both K-major).
-__device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                         uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -89,8 +93,35 @@ __device__ __forceinline__ constexpr uint32_t idesc_i8(int M, int N) {
   return (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void tma_load_stack(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
-  tma_load_3d(dst, map, bar, x, y, z);
+// 3-D tiled load into this CTA whose bytes complete on the leader's barrier.
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster_addr,
+                                                 int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Arrive on a barrier of the pair's leader.  What it announces is not plain data
+// of this thread's generic proxy: operand tiles that fence.proxy.async has handed
+// to the async proxy of this SM (whose tensor core reads them), or accumulators
+// whose reads tcgen05.wait has completed.  So CTA scope is enough; at cluster
+// scope the arrival waited for every store in flight, the epilogue's output
+// included: 1,400 to 1,900 cycles a step against 500.
+__device__ __forceinline__ void arrive_leader(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 struct Tile {
@@ -101,7 +132,7 @@ struct Tile {
 };
 
 // Tile `id` of the list ordered by expert, then output tile, then token tile
-// (the CTAs that run together share an expert's weight tiles and tokens).
+// (the pairs that run together share an expert's weight tiles and tokens).
 // The tokens of an expert are cut into ceil(c / 256) tiles of one size.
 __device__ __forceinline__ Tile tile_at(const GroupTable* g, int E, int col_tiles, int id) {
   Tile t;
@@ -118,44 +149,43 @@ __device__ __forceinline__ Tile tile_at(const GroupTable* g, int E, int col_tile
   return t;
 }
 
-// Byte offset in a code box (128 rows of 64 bytes, 64-byte swizzle) of the 16
-// code bytes that (row, half) of the weight tile needs at step j of the box.
-// kFwd: box row = W row; kDx: box row = reduction index j * 64 + (row & 63),
-// and the tile's k range takes two 32-byte column groups.
-template <int MODE>
-__device__ __forceinline__ uint32_t box_offset(uint32_t row, uint32_t half, uint32_t j) {
-  const uint32_t R = MODE == kFwd ? row : j * 64u + (row & 63u);
-  const uint32_t c = (MODE == kFwd ? 2u * j : 2u * (row >> 6)) + half;
+// Byte offset in a step's code slot (kDx: 64 reduction rows of 64 bytes, the
+// tile's k range, 64-byte swizzle) of the first of the two 16-byte chunks that
+// weight-tile row `row` needs: k group row >> 6 of reduction row row & 63.  The
+// second is at that offset ^ 16.  Eight consecutive rows read from eight
+// different bank groups.
+__device__ __forceinline__ uint32_t code_offset(uint32_t row) {
+  const uint32_t R = row & 63u, c = 2u * (row >> 6);
   return R * 64u + ((c ^ ((R >> 1) & 3u)) << 4);
 }
 
 template <int MODE, bool F16>
-__global__ void __launch_bounds__(MODE == kI8 ? 256 : 512, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThreadsI8 : kThreads, 1)
     expert_gemm_kernel(const __grid_constant__ ExpertMaps maps, const ExpertParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* code_base = smem + kStages * kStageBytes;
-  GemmShared* sh = reinterpret_cast<GemmShared*>(code_base + (MODE == kI8 ? 0 : kCodeSlots * kCodeBytes));
+  GemmShared* sh = reinterpret_cast<GemmShared*>(code_base + (MODE == kDx ? kStages * kCodeBytes : 0));
   auto stage_w = [&](int s) { return smem + s * kStageBytes; };
   auto stage_t = [&](int s) { return smem + s * kStageBytes + kWBytes; };
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
   volatile uint32_t* abort_flag = &sh->abort_flag;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sh->full[s], MODE == kI8 ? 3 : 2);
-      mbar_init(&sh->wready[s], kDeqWarps);
+      // leader: its token producer (which expects every byte) and the dequant
+      // warps of both CTAs
+      mbar_init(&sh->full[s], MODE == kI8 ? 1 : 1 + 8);
       mbar_init(&sh->empty[s], 1);
-    }
-    for (int c = 0; c < kCodeSlots; ++c) {
-      mbar_init(&sh->cfull[c], 1);
-      mbar_init(&sh->cempty[c], kDeqWarps);
+      mbar_init(&sh->cfull[s], 1);
+      mbar_init(&sh->cempty[s], 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->acc_full[b], 1);
-      mbar_init(&sh->acc_empty[b], 4);
+      mbar_init(&sh->acc_empty[b], 8);   // leader: the epilogue warps of both CTAs
     }
     mbar_init(&sh->drain, 1);
     sh->abort_flag = 0;
@@ -163,9 +193,9 @@ __global__ void __launch_bounds__(MODE == kI8 ? 256 : 512, 1)
     fence_proxy_async_smem();
     tma_prefetch(&maps.tok_l);
     tma_prefetch(&maps.tok_s);
-    tma_prefetch(&maps.w);
+    if (MODE != kFwd) tma_prefetch(&maps.w);
   }
-  if (warp == 2) {
+  if (warp == 1) {
     if (p.offsets != nullptr) {
       build_groups(&sh->groups, p.offsets, p.E, p.M, kTileT, blockIdx.x == 0 ? p.status : nullptr);
     } else if (lane == 0) {
@@ -174,151 +204,170 @@ __global__ void __launch_bounds__(MODE == kI8 ? 256 : 512, 1)
       sh->groups.tiles[1] = (p.M + kTileT - 1) / kTileT;
     }
   }
-  if (warp == 3) {
-    tmem_alloc(&sh->tmem_base, 512);
-    tmem_relinquish();
+  if (warp == 2) {
+    tmem_alloc_pair(&sh->tmem_base, 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   const int tiles = sh->groups.tiles[p.E] * p.col_tiles;
   const int steps = p.main_steps + p.adapter_steps;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  auto leader_bar = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
 
-  if (warp < 2) {
-    // ---------------- token producers: warp p loads rows 128 p .. of a tile in
-    // 128-row boxes (32 p .. in 32-row boxes for up to 64 tokens)
-    if (lane == 0) {
-      if (MODE == kI8) grid_dep_wait();
-      bool waited = false;
-      int it = 0;
-      bool ok = true;
-      for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x) {
-        const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
-        const bool large = t.nt > 64;
-        const int rows = large ? 128 : 32;
-        const bool loads = warp * rows < t.nt;
-        const uint32_t bytes = loads ? uint32_t(rows) * 128u : 0u;
-        const uint32_t at = uint32_t(warp * rows) * 128u;
-        const CUtensorMap* tok = large ? &maps.tok_l : &maps.tok_s;
-        const CUtensorMap* ad = large ? &maps.ad_l : &maps.ad_s;
-        for (int k = 0; k < steps; ++k, ++it) {
-          const int s = it % kStages;
-          ok = mbar_wait(&sh->empty[s], ((it / kStages) & 1) ^ 1, abort_flag, p.status);
-          if (!ok) break;
-          if (k < p.main_steps) {
-            mbar_arrive_expect_tx(&sh->full[s], bytes);
-            if (loads) tma_load_2d(stage_t(s) + at, tok, &sh->full[s], k * (MODE == kI8 ? 128 : 64), t.t0 + warp * rows);
+  // The single-issuer roles run as whole warps with one elected lane, so that
+  // their counters and addresses stay in uniform registers (issued from a
+  // divergent lane, the four MMAs of a step took 770 cycles).
+  if (warp == 0) {
+    // ---------------- tokens: this CTA's half of the tile, in a 128-row box (or
+    // a 32-row one)
+    const bool issue = elect_one();
+    if (MODE == kI8) grid_dep_wait();
+    bool waited = false, ok = true;
+    int s = 0, issued = 0;
+    uint32_t ph = 1;
+    for (int id = pair; id < tiles && ok; id += pairs) {
+      const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
+      const int half = t.nt >> 1;
+      const bool large = half > 32;
+      const uint32_t bytes = large ? 128u * 128u : 32u * 128u;   // of one CTA
+      const int y = t.t0 + int(rank) * half;
+      const CUtensorMap* tok = large ? &maps.tok_l : &maps.tok_s;
+      const CUtensorMap* ad = large ? &maps.ad_l : &maps.ad_s;
+      for (int k = 0; k < steps; ++k) {
+        ok = ring_wait(&sh->empty[s], ph, abort_flag, p.status);
+        if (!ok) break;
+        const bool main = k < p.main_steps;
+        if (!main && !waited) grid_dep_wait();     // T or U: the kernel before
+        waited |= !main;
+        if (issue) {
+          const uint32_t bar = leader_bar(&sh->full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], 2 * (bytes + (MODE == kI8 || !main ? kWBytes : 0u)));
+          if (main) {
+            tma_load_2d_pair(stage_t(s), tok, bar, k * (MODE == kI8 ? 128 : 64), y);
           } else {
-            if (!waited) grid_dep_wait();     // T or U: the kernel before
-            waited = true;
-            const int r0 = (k - p.main_steps) * 64;
-            mbar_arrive_expect_tx(&sh->full[s], bytes + (warp == 0 ? kWBytes : 0u));
-            if (loads) tma_load_2d(stage_t(s) + at, ad, &sh->full[s], r0, t.t0 + warp * rows);
-            if (warp == 0) {
-              if (MODE == kFwd) {
-                tma_load_stack(stage_w(s), &maps.wad, &sh->full[s], r0, t.n0, t.e);
-              } else {
-                tma_load_stack(stage_w(s), &maps.wad, &sh->full[s], t.n0, r0, t.e);
-                tma_load_stack(stage_w(s) + 8192, &maps.wad, &sh->full[s], t.n0 + 64, r0, t.e);
-              }
+            const int r0 = (k - p.main_steps) * 64, n0 = t.n0 + 128 * int(rank);
+            tma_load_2d_pair(stage_t(s), ad, bar, r0, y);
+            if (MODE == kFwd) {
+              tma_load_3d_pair(stage_w(s), &maps.wad, bar, r0, n0, t.e);
+            } else {
+              tma_load_3d_pair(stage_w(s), &maps.wad, bar, n0, r0, t.e);
+              tma_load_3d_pair(stage_w(s) + 8192, &maps.wad, bar, n0 + 64, r0, t.e);
             }
           }
         }
+        __syncwarp();
+        ++issued;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      if (*abort_flag)   // unwind: wait (bounded) for the copies in flight
-        for (int j = std::max(0, it - kStages); j < it; ++j) {
+    }
+    if (*abort_flag)   // unwind: wait (bounded) for the stages in flight
+      for (int j = max(0, issued - kStages); j < issued; ++j) {
+        uint32_t none = 0;
+        ring_wait(&sh->empty[j % kStages], (j / kStages) & 1, &none, nullptr);
+      }
+  } else if (warp == 1) {
+    // ---------------- weight side: the int8 tile of every step (kI8), or the
+    // codes of every main step into the stage's own code slot (kDx)
+    if (MODE != kFwd) {
+      const bool issue = elect_one();
+      if (MODE == kI8) grid_dep_wait();
+      int s = 0;
+      uint32_t ph = (1u << kStages) - 1;   // bit s: parity of the wait for slot s, toggled at each use
+      bool ok = true;
+      for (int id = pair; id < tiles && ok; id += pairs) {
+        const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
+        const int n0 = t.n0 + 128 * int(rank);
+        for (int k = 0; k < steps; ++k) {
+          if (k < p.main_steps) {
+            ok = ring_wait(MODE == kI8 ? &sh->empty[s] : &sh->cempty[s], (ph >> s) & 1u, abort_flag, p.status);
+            if (!ok) break;
+            ph ^= 1u << s;
+            if (issue) {
+              if (MODE == kI8) {
+                tma_load_3d_pair(stage_w(s), &maps.w, leader_bar(&sh->full[s]), k * 128, n0, t.e);
+              } else {
+                mbar_arrive_expect_tx(&sh->cfull[s], kCodeBytes);
+                tma_load_3d(code_base + s * kCodeBytes, &maps.w, &sh->cfull[s], n0 / 2, k * 64, t.e);
+              }
+            }
+            __syncwarp();
+          }
+          if (++s == kStages) s = 0;
+        }
+      }
+      if (MODE == kDx && *abort_flag)   // unwind: wait (bounded) for the codes in flight
+        for (int j = 0; j < kStages; ++j) {
           uint32_t none = 0;
-          mbar_wait(&sh->full[j % kStages], (j / kStages) & 1, &none, nullptr);
+          ring_wait(&sh->cfull[j], (ph >> j) & 1u, &none, nullptr);
         }
     }
   } else if (warp == 2) {
-    // ---------------- weight-side producer
-    if (lane == 0) {
-      if (MODE == kI8) grid_dep_wait();
-      int it = 0;
+    // ---------------- MMA: the leader's warp walks the steps, one lane issues
+    if (rank == 0) {
+      const bool issue = elect_one();
+      // descriptors of stage 0; a stage is kStageBytes further, a K substep 32
+      // bytes (K-major) or 16 rows of 128 bytes (MN-major)
+      const uint64_t w_desc = MODE == kDx ? smem_desc_sw128(smem_u32(stage_w(0)), 8192, 1024)
+                                          : smem_desc_sw128(smem_u32(stage_w(0)), 16, 1024);
+      const uint64_t t_desc = smem_desc_sw128(smem_u32(stage_t(0)), 16, 1024);
+      constexpr uint32_t kWSub = (MODE == kDx ? 2048 : 32) >> 4, kTSub = 32 >> 4;
+      int s = 0, n = 0;
+      uint32_t ph = 0;
       bool ok = true;
-      const int groups = MODE == kI8 ? p.main_steps : (p.main_steps + kCodeSteps - 1) / kCodeSteps;
-      for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x) {
+      for (int id = pair; id < tiles && ok; id += pairs, ++n) {
         const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
-        for (int g = 0; g < groups; ++g, ++it) {
-          if (MODE == kI8) {
-            const int s = it % kStages;
-            ok = mbar_wait(&sh->empty[s], ((it / kStages) & 1) ^ 1, abort_flag, p.status);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&sh->full[s], kWBytes);
-            tma_load_stack(stage_w(s), &maps.w, &sh->full[s], g * 128, t.n0, t.e);
-          } else {
-            const int c = it % kCodeSlots;
-            ok = mbar_wait(&sh->cempty[c], ((it / kCodeSlots) & 1) ^ 1, abort_flag, p.status);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&sh->cfull[c], kCodeBytes);
-            uint8_t* dst = code_base + c * kCodeBytes;
-            if (MODE == kFwd) tma_load_stack(dst, &maps.w, &sh->cfull[c], g * 64, t.n0, t.e);
-            else tma_load_stack(dst, &maps.w, &sh->cfull[c], t.n0 / 2, g * 128, t.e);
-          }
-        }
-      }
-      if (*abort_flag) {
-        const int ring = MODE == kI8 ? kStages : kCodeSlots;
-        for (int j = std::max(0, it - ring); j < it; ++j) {
-          uint32_t none = 0;
-          mbar_wait(MODE == kI8 ? &sh->full[j % ring] : &sh->cfull[j % ring], (j / ring) & 1, &none, nullptr);
-        }
-      }
-    }
-  } else if (warp == 3) {
-    // ---------------- MMA issuer
-    if (lane == 0) {
-      int it = 0, n = 0;
-      bool ok = true;
-      for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x, ++n) {
-        const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
-        const uint32_t idesc = MODE == kI8 ? idesc_i8(128, t.nt) : idesc_f32acc(128, t.nt, MODE == kDx, false, F16);
+        const uint32_t idesc = MODE == kI8 ? idesc_i8(256, t.nt) : idesc_f32acc(256, t.nt, MODE == kDx, false, F16);
         const uint32_t d = tmem + uint32_t(n & 1) * 256u;
-        ok = mbar_wait(&sh->acc_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        for (int k = 0; k < steps; ++k, ++it) {
-          const int s = it % kStages;
-          const uint32_t ph = (it / kStages) & 1;
-          ok = mbar_wait(&sh->full[s], ph, abort_flag, p.status);
-          if (ok && MODE != kI8) ok = mbar_wait(&sh->wready[s], ph, abort_flag, p.status);
+        ok = mbar_wait_cluster(&sh->acc_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, p.status);
+        for (int k = 0; k < steps && ok; ++k) {
+          ok = mbar_wait_cluster(&sh->full[s], ph, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t w_base = smem_u32(stage_w(s));
-          const uint32_t t_base = smem_u32(stage_t(s));
-          int ksub = 4;
-          if (MODE != kI8 && k >= p.main_steps) {
-            const int left = p.r - (k - p.main_steps) * 64;
-            ksub = left >= 64 ? 4 : (left + 15) / 16;
+          const uint64_t wd = w_desc + uint32_t(s) * (kStageBytes >> 4);
+          const uint64_t td = t_desc + uint32_t(s) * (kStageBytes >> 4);
+          if (issue) {
+            if (MODE == kI8) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_i8_pair(d, wd + kk * kWSub, td + kk * kTSub, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+            } else {
+              const int left = k < p.main_steps ? 64 : p.r - (k - p.main_steps) * 64;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                if (kk * 16 < left) umma_f16_pair(d, wd + kk * kWSub, td + kk * kTSub, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+            }
+            // The last step's commit goes to the accumulator's barrier; the
+            // epilogue then releases that step's stage.  MMAs finish in order,
+            // so the commit covers the whole accumulation.
+            umma_commit_pair_mc(k + 1 < steps ? &sh->empty[s] : &sh->acc_full[n & 1], 0x3);
           }
-          for (int kk = 0; kk < ksub; ++kk) {
-            const uint64_t adesc = MODE == kDx ? smem_desc_sw128(w_base + kk * 2048, 8192, 1024)
-                                               : smem_desc_sw128(w_base + kk * 32, 16, 1024);
-            const uint64_t bdesc = smem_desc_sw128(t_base + kk * 32, 16, 1024);
-            const uint32_t acc = (k > 0 || kk > 0) ? 1u : 0u;
-            if (MODE == kI8) umma_i8(d, adesc, bdesc, idesc, acc);
-            else umma_f16(d, adesc, bdesc, idesc, acc);
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
           }
-          umma_commit(&sh->empty[s]);
         }
-        if (ok) umma_commit(&sh->acc_full[n & 1]);
       }
-      if (!ok) {   // unwind: wait (bounded) for the MMAs in flight
-        umma_commit(&sh->drain);
+      if (!ok && issue) {   // unwind: wait (bounded) for the MMAs in flight
+        umma_commit_pair_mc(&sh->drain, 0x1);
         uint32_t none = 0;
-        mbar_wait(&sh->drain, 0, &none, nullptr);
+        ring_wait(&sh->drain, 0, &none, nullptr);
       }
     }
-  } else if (warp < kDeqWarp) {
+  } else if (warp >= kEpiWarp && warp < kDeqWarp) {
     // ---------------- epilogue: lane = output n, register = token
     if (MODE == kI8) grid_dep_wait();
     const int quad = warp - kEpiWarp;
-    int n = 0;
-    for (int id = blockIdx.x; id < tiles; id += gridDim.x, ++n) {
+    int n = 0, last = 0;   // last: stage of the tile's last step
+    for (int id = pair; id < tiles; id += pairs, ++n) {
       const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
-      const int col = t.n0 + quad * 32 + lane;
+      const int col = t.n0 + 128 * int(rank) + quad * 32 + lane;
       const bool col_ok = col < p.out_cols;
       float bias = 0.0f, sw = 0.0f;
       if (col_ok) {
@@ -330,8 +379,10 @@ __global__ void __launch_bounds__(MODE == kI8 ? 256 : 512, 1)
           else bias = __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[at]);
         }
       }
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(&sh->acc_full[n & 1], (n >> 1) & 1, abort_flag, p.status));
+      const bool ok = warp_wait<300>(&sh->acc_full[n & 1], (n >> 1) & 1, abort_flag, p.status);
       if (!ok) break;
+      last = (last + steps) % kStages;
+      if (quad == 0 && lane == 0) mbar_arrive(&sh->empty[(last + kStages - 1) % kStages]);
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c * 32 < t.cnt; ++c) {
@@ -371,66 +422,100 @@ __global__ void __launch_bounds__(MODE == kI8 ? 256 : 512, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->acc_empty[n & 1]);
+      if (lane == 0) arrive_leader(leader_bar(&sh->acc_empty[n & 1]));
     }
-  } else {
-    // ---------------- dequant warps: two threads per weight-tile row (16 rows a
-    // warp), half an NF4 chunk of 64 each
-    const int row = (warp - kDeqWarp) * 16 + (lane & 15);
-    const uint32_t half = uint32_t(lane >> 4);
+  } else if (warp >= kDeqWarp) {
+    // ---------------- dequant warps: one thread per weight-tile row and step, so
+    // the table of a block's sixteen values is built once.  A group of four warps
+    // takes every kDeqGroups-th step: decoding (codes to registers) needs no free
+    // stage, so it runs ahead of the MMAs, and only the stores wait for the stage.
+    const int group = (warp - kDeqWarp) >> 2;
+    const int row = threadIdx.x & 127;
     const bool dq = p.dq != 0;
     const float s_g = dq ? __ldg(p.absmax_scale) : 0.0f;
-    int it = 0, box = 0;
+    int base = 0;         // steps of the tiles before
+    uint32_t ph = (1u << kStages) - 1, cph = 0;   // bit s: parity of the next wait for stage s, and its codes
+    int s = group;        // stage of this group's next step
     bool ok = true;
-    for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x) {
+    for (int id = pair; id < tiles && ok; id += pairs) {
       const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
-      const int64_t first = int64_t(t.e) * p.w_rows;
-      auto scale_at = [&](int k) -> float {
-        if (k >= p.main_steps) return 0.0f;
-        const int wr = MODE == kFwd ? t.n0 + row : k * 64 + (row & 63);
-        const int ch = MODE == kFwd ? k : (t.n0 >> 6) + (row >> 6);
-        if (wr >= p.w_rows || ch * 64 >= p.w_cols) return 0.0f;   // zero rows: the codes there are 0 too
-        return load_scale(p.absmax_q, p.absmax, s_g, dq, chunk_block(first + wr, p.w_cols, ch, p.bs_shift));
+      // this row's element index at step k: e0 + k * e_step; its scale is the
+      // block's that holds it (a 64-element chunk never straddles two blocks)
+      const int n0 = t.n0 + 128 * int(rank);
+      const int wr0 = MODE == kFwd ? n0 + row : row & 63;
+      const int ch0 = MODE == kFwd ? 0 : (n0 >> 6) + (row >> 6);
+      const int64_t e0 = (int64_t(t.e) * p.w_rows + wr0) * p.w_cols + int64_t(ch0) * 64;
+      const int64_t e_step = MODE == kFwd ? 64 : int64_t(64) * p.w_cols;
+      const int64_t e0_safe = int64_t(t.e) * p.w_rows * p.w_cols;   // read where there is no such row
+      // rows past the expert's weight decode to zeros: their scale counts as 0
+      const int k_end = MODE == kFwd ? (wr0 < p.w_rows ? p.main_steps : 0)
+                                     : (ch0 * 64 < p.w_cols ? (p.w_rows - wr0 + 63) >> 6 : 0);
+      // Scales are loaded two of this thread's steps ahead and converted only
+      // where they are used, so that no step waits for a load.
+      auto raw_scale = [&](int k) -> uint32_t {
+        const int64_t b = (k < k_end ? e0 + k * e_step : e0_safe) >> p.bs_shift;
+        return dq ? uint32_t(__ldg(p.absmax_q + b)) : __float_as_uint(__ldg(p.absmax + b));
       };
-      float sc[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sc[j] = scale_at(j);
-      for (int k = 0; k < steps; ++k, ++it) {
-        const int s = it % kStages;
-        const float scale = sc[0];
-        sc[0] = sc[1];
-        sc[1] = sc[2];
-        sc[2] = sc[3];
-        sc[3] = scale_at(k + 4);
-        bool good = mbar_wait(&sh->empty[s], ((it / kStages) & 1) ^ 1, abort_flag, p.status);
+      auto load_codes = [&](int k) -> Codes {
+        return load_codes64(p.codes + ((k < k_end ? e0 + k * e_step : e0_safe) >> 1), p.codes32 != 0);
+      };
+      const int first = (group + kDeqGroups - base % kDeqGroups) % kDeqGroups;
+      uint32_t raw0 = raw_scale(first), raw1 = raw_scale(first + kDeqGroups);
+      // Forward: a row's codes run along it, so four steps share a line and each
+      // thread loads its own a step ahead.  dx walks down the rows: there the same
+      // loads took 430 us against 405 through TMA (4096 x 11008, 4096 rows), and
+      // the forward 665 us against 703 (11008 x 4096, 8192 rows).
+      Codes next;
+      if (MODE == kFwd) next = load_codes(first);
+      for (int k = first; k < steps; k += kDeqGroups) {
+        const uint32_t raw = raw0;
+        raw0 = raw1;
+        raw1 = raw_scale(k + 2 * kDeqGroups);
         const bool main = k < p.main_steps;
-        const int j = k % kCodeSteps;
-        if (good && main && j == 0)
-          good = mbar_wait(&sh->cfull[box % kCodeSlots], (box / kCodeSlots) & 1, abort_flag, p.status);
-        ok = __all_sync(0xffffffffu, good);
-        if (!ok) break;
+        uint4 v[8];
+        Codes codes;
+        if (MODE == kFwd) {
+          codes = next;
+          next = load_codes(k + kDeqGroups);
+        } else if (main) {
+          ok = warp_wait(&sh->cfull[s], (cph >> s) & 1u, abort_flag, p.status);
+          if (!ok) break;
+          cph ^= 1u << s;
+          const uint8_t* slot = code_base + s * kCodeBytes;
+          const uint32_t at = code_offset(uint32_t(row));
+          const uint4 c0 = *reinterpret_cast<const uint4*>(slot + at), c1 = *reinterpret_cast<const uint4*>(slot + (at ^ 16u));
+          codes = Codes{{c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w}};
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->cempty[s]);
+        }
         if (main) {
-          dequant_half_row(code_base + (box % kCodeSlots) * kCodeBytes + box_offset<MODE>(uint32_t(row), half, uint32_t(j)),
-                           scale, stage_w(s), uint32_t(row), half, F16);
+          const float scale = k < k_end ? (dq ? __fmul_rn(float(raw), s_g) : __uint_as_float(raw)) : 0.0f;
+          decode_row(codes, make_table(scale, F16), v);
+        }
+        ok = warp_wait(&sh->empty[s], (ph >> s) & 1u, abort_flag, p.status);
+        if (!ok) break;
+        ph ^= 1u << s;
+        if (main) {
+          uint8_t* tile = stage_w(s);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tile + sw128_offset(uint32_t(row), uint32_t(c))) = v[c];
           fence_proxy_async_smem();
         }
         __syncwarp();
-        // one arrival per step, adapter steps too, so the phases of wready follow the ring
-        if (lane == 0) mbar_arrive(&sh->wready[s]);
-        if (main && (j == kCodeSteps - 1 || k == p.main_steps - 1)) {
-          if (lane == 0) mbar_arrive(&sh->cempty[box % kCodeSlots]);
-          ++box;
-        }
+        if (lane == 0) arrive_leader(leader_bar(&sh->full[s]));   // adapter steps too: the same arrivals every phase
+        s += kDeqGroups;
+        if (s >= kStages) s -= kStages;
       }
+      base += steps;
     }
   }
 
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
-  if (warp == 3) {
+  cluster_sync();
+  if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -441,14 +526,12 @@ PerDeviceOnce g_attr_done;
 cudaError_t set_attrs() {
   const int dev = PerDeviceOnce::current();
   if (g_attr_done.done(dev)) return cudaSuccess;
-  const void* nf4[4] = {(const void*)expert_gemm_kernel<kFwd, false>, (const void*)expert_gemm_kernel<kFwd, true>,
-                        (const void*)expert_gemm_kernel<kDx, false>, (const void*)expert_gemm_kernel<kDx, true>};
+  const void* kernels[5] = {(const void*)expert_gemm_kernel<kFwd, false>, (const void*)expert_gemm_kernel<kFwd, true>,
+                            (const void*)expert_gemm_kernel<kDx, false>, (const void*)expert_gemm_kernel<kDx, true>,
+                            (const void*)expert_gemm_kernel<kI8, false>};
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-    e = cudaFuncSetAttribute(nf4[i], cudaFuncAttributeMaxDynamicSharedMemorySize, int(gemm_smem(false)));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute((const void*)expert_gemm_kernel<kI8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(gemm_smem(true)));
+  for (int i = 0; i < 5 && e == cudaSuccess; ++i)
+    e = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, int(gemm_smem(kDx)));
   if (e == cudaSuccess) g_attr_done.mark(dev);
   return e;
 }
@@ -458,7 +541,7 @@ bool set_grid(ExpertGemm* L, int sms) {
   p.col_tiles = int((int64_t(p.out_cols) + kTileW - 1) / kTileW);
   const int64_t tiles = max_row_tiles(p.M, p.E, kTileT) * p.col_tiles;
   if (tiles > int64_t(0x7fffffff)) return false;
-  L->grid = unsigned(std::min<int64_t>(tiles, sms));
+  L->grid = 2u * unsigned(std::min<int64_t>(tiles, std::max(sms / 2, 1)));
   return true;
 }
 
@@ -477,8 +560,8 @@ cudaError_t launch(const ExpertGemm& L, int prof_id, cudaStream_t st, int* launc
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(L.grid, 1, 1);
-  cfg.blockDim = dim3(MODE == kI8 ? 256 : 512, 1, 1);
-  cfg.dynamicSmemBytes = gemm_smem(MODE == kI8);
+  cfg.blockDim = dim3(MODE == kI8 ? kThreadsI8 : kThreads, 1, 1);
+  cfg.dynamicSmemBytes = gemm_smem(MODE);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -501,11 +584,12 @@ bool ExpertGemm::prepare(const GroupedArgs& g, bool backward, const void* ad, in
   f16 = a.f16 != 0;
   ExpertGemm* L = this;
   const uint64_t N = uint64_t(a.N), K = uint64_t(a.K), E = uint64_t(g.E);
-  const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B, s64 = CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B;
   bool ok = token_maps(L, backward ? a.dy : a.x, backward ? N : K, ad, a.r, uint64_t(a.M));
-  // code boxes: 128 W rows x 64 bytes (kFwd: two K steps of a row tile; kDx: two
-  // reduction steps of 128 columns)
-  ok = ok && encode_map_stack(&L->maps.w, a.w->codes, MapElem::kU8, K / 2, N, E, 64, 128, s64);
+  // a step's codes in dx: 128 columns of 64 W rows
+  L->maps.w = L->maps.tok_l;
+  if (backward)
+    ok = ok && encode_map_stack(&L->maps.w, a.w->codes, MapElem::kU8, K / 2, N, E, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B);
   ok = ok && (backward ? encode_map_stack(&L->maps.wad, a.A, MapElem::k16, K, uint64_t(a.r), E, 64, 64, s128)
                        : encode_map_stack(&L->maps.wad, a.B, MapElem::k16, uint64_t(a.r), N, E, 64, 128, s128));
   p = ExpertParams{};
@@ -520,6 +604,8 @@ bool ExpertGemm::prepare(const GroupedArgs& g, bool backward, const void* ad, in
   p.bs_shift = log2_block(a.w->block_size);
   p.dq = a.w->double_quant;
   p.offsets = g.offsets;
+  p.codes = a.w->codes;
+  p.codes32 = (reinterpret_cast<uintptr_t>(a.w->codes) & 31u) == 0;
   p.absmax_q = a.w->absmax_q;
   p.absmax = a.w->absmax;
   p.absmax_scale = a.w->absmax_scale;

@@ -11,7 +11,7 @@ struct ExpertMaps {
   CUtensorMap tok_l, tok_s;   // tokens: 128-row and 32-row boxes
   CUtensorMap ad_l, ad_s;     // T or U: the same
   CUtensorMap wad;            // adapter operand on the weight side
-  CUtensorMap w;              // NF4 codes, or the int8 weight
+  CUtensorMap w;              // kI8: the weight
 };
 
 struct ExpertParams {
@@ -24,6 +24,8 @@ struct ExpertParams {
   int bs_shift, dq;
   int out_dtype;              // kI8: nf4_dtype of out and bias
   const int32_t* offsets;     // null: all M rows are the one expert's
+  const uint8_t* codes;
+  int codes32;                // codes start on a 32-byte boundary
   const uint8_t* absmax_q;
   const float* absmax;
   const float* absmax_scale;

@@ -27,6 +27,7 @@
 #include "kernels.h"
 #include "nf4_common.cuh"
 #include "nf4_dequant.cuh"
+#include "ring_wait.cuh"
 #include "tc_common.cuh"
 #include "tensor_maps.h"
 
@@ -35,6 +36,7 @@ namespace {
 
 using namespace tc;
 using expert::pack2;
+using expert::ring_wait;
 using expert::unpack2;
 
 constexpr int kRkThreads = 192;    // A producer, MMA, B producer / epilogue, 3 more epilogue warps
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kRkThreads, 1)
     int issued = 0;
     for (int i = 0; i < nsteps; ++i) {
       const int s = i % p.stages;
-      if (!mbar_wait(&sh->empty[s], ((i / p.stages) & 1) ^ 1, abort_flag, p.status)) break;
+      if (!ring_wait(&sh->empty[s], ((i / p.stages) & 1) ^ 1, abort_flag, p.status)) break;
       uint8_t* a = smem + s * stage_bytes;
       uint8_t* b = a + kRkABytes;
       const int red0 = (step0 + i) * 64;
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(kRkThreads, 1)
     if (*abort_flag) {   // unwind: wait (bounded) for this issuer's copies in flight
       for (int i = issued - 1; i >= 0 && i >= issued - p.stages; --i) {
         uint32_t none = 0;
-        mbar_wait(&sh->full[i % p.stages], (i / p.stages) & 1, &none, nullptr);
+        ring_wait(&sh->full[i % p.stages], (i / p.stages) & 1, &none, nullptr);
       }
     }
   }
@@ -190,10 +192,10 @@ __global__ void __launch_bounds__(kRkThreads, 1)
       int issued = 0;
       for (int i = 0; i < nsteps; ++i) {
         const int s = i % p.stages;
-        ok = mbar_wait(&sh->full[s], (i / p.stages) & 1, abort_flag, p.status);
+        ok = ring_wait(&sh->full[s], (i / p.stages) & 1, abort_flag, p.status);
         if (ok && tail < 64 && i == nsteps - 1) {
           mbar_arrive(&sh->tail);
-          ok = mbar_wait(&sh->fixed, 0, abort_flag, p.status);
+          ok = ring_wait(&sh->fixed, 0, abort_flag, p.status);
         }
         if (!ok) break;
         tc_fence_after();
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kRkThreads, 1)
     // The last step's rows of another expert: cleared once they have landed (the
     // MMA thread, which follows the ring, says so).
     if (warp >= 3 && tail < 64) {
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(&sh->tail, 0, abort_flag, p.status));
+      const bool ok = __all_sync(0xffffffffu, ring_wait(&sh->tail, 0, abort_flag, p.status));
       if (ok) {
         uint8_t* a = smem + ((nsteps - 1) % p.stages) * stage_bytes;
         const int blocks = 2 + (p.NP / 64) * (two ? 2 : 1);   // [64 rows][128 bytes] each, A then B
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kRkThreads, 1)
       if (ok && lane == 0) mbar_arrive(&sh->fixed);
     }
     // epilogue warps 2..5 -> TMEM lane quadrants 2, 3, 0, 1
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(&sh->accum, 0, abort_flag, p.status));
+    const bool ok = __all_sync(0xffffffffu, ring_wait(&sh->accum, 0, abort_flag, p.status));
     tc_fence_after();
     const int quad = warp & 3;
     const int prow = quad * 32 + lane;

@@ -1,5 +1,4 @@
-// NF4 codes to 16-bit values in registers and in the 128-byte-swizzled tiles
-// that the tensor core reads (the expert GEMM).
+// NF4 codes to 16-bit values in registers (the expert GEMM).
 #pragma once
 
 #include <cstdint>
@@ -7,7 +6,6 @@
 #include <cuda_fp16.h>
 
 #include "nf4_common.cuh"
-#include "tc_common.cuh"
 
 namespace nf4 {
 
@@ -61,35 +59,46 @@ __device__ __forceinline__ BlockTable make_table(float scale, bool f16) {
   return t;
 }
 
-// Four codes (the low 16 bits of `w`: two packed bytes, even element in the
-// high nibble) -> four bf16 values as two bf16x2 words in element order.
-__device__ __forceinline__ uint2 decode4(uint32_t w, const BlockTable& t) {
-  const uint32_t sel = w & 0x7777u;                          // code & 7 per nibble
-  const uint32_t pick = ((w >> 1) & 0x4444u) | 0x3210u;      // code >= 8 -> upper plane
+// Four codes given by their selectors (low 16 bits: the code's low three bits per
+// nibble, and 4 * its top bit + the nibble's place) -> four 16-bit values as two
+// words in element order.  Byte permutes and logic share one half-rate pipe,
+// which is what bounds the GEMM, so both selectors are made for eight codes at
+// a time.
+__device__ __forceinline__ uint2 decode4(uint32_t sel, uint32_t pick, const BlockTable& t) {
   const uint32_t lo = prmt(prmt(t.lo[0], t.lo[1], sel), prmt(t.lo[2], t.lo[3], sel), pick);
   const uint32_t hi = prmt(prmt(t.hi[0], t.hi[1], sel), prmt(t.hi[2], t.hi[3], sel), pick);
   // lo/hi bytes are in nibble order (odd element first within a byte).
   return make_uint2(prmt(lo, hi, 0x4051u), prmt(lo, hi, 0x6273u));
 }
 
-// Half a block (32 elements, 16 code bytes at `codes`, smem) into 16-byte
-// chunks 4*half .. 4*half+3 of row `row` of a 128-byte-swizzled bf16 tile.
-__device__ __forceinline__ void dequant_half_row(const uint8_t* codes, float scale, uint8_t* tile,
-                                                 uint32_t row, uint32_t half, bool f16) {
-  const uint4 c = *reinterpret_cast<const uint4*>(codes);
-  const BlockTable t = make_table(scale, f16);
-  const uint32_t words[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint2 a = decode4(words[k], t);
-    const uint2 b = decode4(words[k] >> 16, t);
-    *reinterpret_cast<uint4*>(tile + tc::sw128_offset(row, 4 * half + k)) = make_uint4(a.x, a.y, b.x, b.y);
+// The codes of one 64-element chunk, 32 bytes of global memory that nothing
+// writes meanwhile: one 32-byte load where they are so aligned.
+struct Codes {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Codes load_codes64(const uint8_t* p, bool aligned32) {
+  Codes c;
+  if (aligned32) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(c.w[0]), "=r"(c.w[1]), "=r"(c.w[2]), "=r"(c.w[3]), "=r"(c.w[4]), "=r"(c.w[5]), "=r"(c.w[6]), "=r"(c.w[7])
+        : "l"(p));
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    c = Codes{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
   }
+  return c;
 }
 
-__device__ __forceinline__ float load_scale(const uint8_t* absmax_q, const float* absmax,
-                                            float s_g, bool dq, int64_t idx) {
-  return dq ? __fmul_rn(float(__ldg(absmax_q + idx)), s_g) : __ldg(absmax + idx);
+// Their 64 values, as eight 16-byte chunks of 16-bit values.
+__device__ __forceinline__ void decode_row(const Codes& c, const BlockTable& t, uint4 (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t sel = c.w[k] & 0x77777777u;
+    const uint32_t pick = ((c.w[k] >> 1) & 0x44444444u) | 0x32103210u;
+    const uint2 a = decode4(sel, pick, t);
+    const uint2 b = decode4(sel >> 16, pick >> 16, t);
+    v[k] = make_uint4(a.x, a.y, b.x, b.y);
+  }
 }
 
 }  // namespace expert
