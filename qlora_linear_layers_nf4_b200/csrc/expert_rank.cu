@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(kRkThreads, 1)
   // A kernel launched as this one's programmatic dependent may start on the SMs
   // this grid leaves free; it waits for this grid before it reads the result.
   grid_dep_launch();
+  if (p.zero != nullptr && blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < p.zero_n; i += kRkThreads) p.zero[i] = 0;
   if (warp == 0) build_groups(&sh->groups, p.offsets, p.E, p.M, 128, blockIdx.x == 0 && blockIdx.y == 0 ? p.status : nullptr);
   __syncthreads();
   int e, row0, row_end;          // output rows of this tile (absolute tokens, or of the expert)

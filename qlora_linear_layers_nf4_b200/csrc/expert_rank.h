@@ -24,6 +24,8 @@ struct RankParams {
   void* out;         // T, U (16-bit) or dB, dA (fp32)
   void* out_lo;      // U: the second term
   uint32_t* status;
+  int* zero;         // ints cleared on the way (for the kernel after), or null
+  int zero_n;
 };
 
 // One product, prepared on the host before the first launch of a call.

@@ -1,6 +1,7 @@
 // QLoRA linear of a stack of experts: the launches of a call.  Every launch is
 // prepared (its tensor maps encoded) before the first is enqueued, so a call
 // that fails on the host enqueues nothing.
+#include "expert_decode.h"
 #include "expert_gemm.h"
 #include "expert_rank.h"
 #include "kernels.h"
@@ -13,24 +14,48 @@ namespace {
 // every compute dtype; U's two 16-bit terms share one.
 size_t mr_bytes(int64_t M, int r) { return (size_t(M) * size_t(r) * 4 + 255) / 256 * 256; }
 
+// Few rows per expert: stream the weights (16 rows a pass) instead of feeding
+// the GEMM, which spends the same time on one row of an expert as on 256.
+bool use_decode(int64_t M, int64_t E) { return M <= 16 * E; }
+
+// Rows x r up to which T takes one small CTA per element instead of the GEMM.
+constexpr int64_t kSmallT = 4096;
+
 }  // namespace
 
-// fwd: [T]; bwd: [T] [U]
+// fwd: [T] [the decode kernel's partials and counters]; bwd: [T] [U]
 size_t grouped_workspace_bytes(bool backward, int64_t M, int64_t N, int64_t K, int r) {
   (void)N;
   (void)K;
   if (M < 0 || r < 0) return 0;
-  return (backward ? 2 : 1) * mr_bytes(M, r);
+  return backward ? 2 * mr_bytes(M, r) : mr_bytes(M, r) + decode_scratch_bytes();
 }
 
 cudaError_t launch_grouped_fwd(const GroupedArgs& g, int sms, cudaStream_t st, int* launches) {
   const LinearArgs& a = g.lin;
   if (a.f32) return launch_grouped_fwd_f32(g, st, launches);
   void* T = a.t_out ? a.t_out : a.ws + kWsHeader;
+  cudaError_t e;
+  if (use_decode(a.M, g.E)) {
+    ExpertDecode d;
+    ExpertRank t;
+    const bool small = a.M * a.r <= kSmallT;
+    bool ok = d.prepare(g, T, a.ws + kWsHeader + mr_bytes(a.M, a.r), sms);
+    ok = ok && (small || t.prepare(g, kRankT, nullptr, nullptr, T, nullptr));
+    if (!ok) return cudaErrorInvalidValue;
+    if (small) {
+      e = launch_expert_t_small(g, T, d.p.counters, st, launches);
+    } else {
+      t.p.zero = d.p.counters;
+      t.p.zero_n = kDecodeMaxCtas;
+      e = t.run(st, launches, false);
+    }
+    return e == cudaSuccess ? d.run(st, launches) : e;
+  }
   ExpertRank t;
   ExpertGemm y;
   if (!t.prepare(g, kRankT, nullptr, nullptr, T, nullptr) || !y.prepare(g, false, T, sms)) return cudaErrorInvalidValue;
-  cudaError_t e = t.run(st, launches, false);
+  e = t.run(st, launches, false);
   if (e == cudaSuccess) e = y.run(st, launches);
   return e;
 }
