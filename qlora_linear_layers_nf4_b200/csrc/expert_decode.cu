@@ -12,15 +12,19 @@
 // (so the result does not depend on who came last) and finishes the tile.
 // Nothing waits for another CTA.
 //
-// Inside a CTA a producer warp keeps a ring of code and x boxes in flight; 16
-// warps take one 64-wide K block of a unit and 32 rows each: a code byte becomes
-// two 16-bit levels with one lookup in a 256-entry table replicated per lane
-// (conflict-free), the levels are A fragments of mma.sync m16n8k16 with x as B,
-// and the block scale multiplies the block's fp32 sums.  So the base enters as
-// level (rounded to the compute type) times scale, the product not rounded
-// again, where the GEMM rounds level * scale: either is within half a step of
-// the exact product.  Measured limit of the inner loop: the table lookups, one
-// shared-memory wavefront per 64 codes.
+// Inside a CTA groups of eight warps take turns at the units (so that their waits,
+// loads and MMAs overlap), a warp two of a unit's 64-wide K blocks and 32 rows: a
+// code byte becomes two 16-bit levels with one lookup in a 256-entry table
+// replicated per lane (conflict-free; entries 256 bytes apart, so that one byte
+// permute makes the address), the levels are A fragments of mma.sync m16n8k16 with
+// x as B, and the block scale multiplies the block's fp32 sums.  So the base enters
+// as level (rounded to the compute type) times scale, the product not rounded
+// again, where the GEMM rounds level * scale: either is within half a step of the
+// exact product.  A producer warp keeps code and x boxes in flight and a warp per
+// group the scales of its units; three more warps finish a tile (sums, bias, split
+// tiles) while the next one streams.  What bounds it is instruction issue (the byte
+// permutes and lookups are 3 of 4 issue cycles a code pair), so everything else
+// stays out of the consumers' loop.
 //
 // T = s x A_e^T comes from a small kernel launched just before, which this one
 // overlaps (programmatic dependent launch) until it finishes its first tile.
@@ -45,24 +49,31 @@ using namespace tc;
 using expert::ring_wait;
 using expert::warp_wait;
 
-constexpr int kDcWarps = 16;                         // consumer warps
-constexpr int kDcThreads = 32 * (kDcWarps + 1);
+constexpr int kDcGroupWarps = 8;                     // 2 K halves x 4 sets of 32 rows
+constexpr int kDcEpiWarps = 3;                       // finish tiles
 constexpr int kDcRows = 128;
-constexpr int kDcBlocks = 4;                         // 64-wide K blocks per unit = phases
-constexpr int kDcSets = 4;                           // 32-row sets
+constexpr int kDcBlocks = 4;                         // 64-wide K blocks per unit
 constexpr uint32_t kDcCodeBytes = kDcRows * 128;
-constexpr uint32_t kLutBytes = 256 * 32 * 4;
+constexpr uint32_t kLutBytes = 256 * 256;            // entry e, lane l at 256 e + 4 l
 
-constexpr int dc_stages(int np) { return np == 8 ? 8 : 6; }
+// Groups of consumer warps, each with a scale warp; 16 tokens leave registers for two.
+constexpr int dc_groups(int np) { return np == 8 ? 3 : 2; }
+constexpr int dc_consumers(int np) { return dc_groups(np) * kDcGroupWarps; }
+constexpr int dc_threads(int np) { return 32 * (dc_consumers(np) + kDcEpiWarps + dc_groups(np) + 1); }
+// A multiple of the groups: a stage always belongs to the same one.
+constexpr int dc_stages(int np) { return np == 8 ? 6 : 4; }
 constexpr uint32_t dc_stage_bytes(int np) { return kDcCodeBytes + uint32_t(np) * 512u; }
 
 template <int NP>
 struct DcShared {
-  uint64_t full[dc_stages(NP)];
+  uint64_t full[dc_stages(NP)];                      // boxes landed, scales written
   uint64_t empty[dc_stages(NP)];
+  uint64_t red_full;                                 // the consumers have stored their sums of a tile
+  uint64_t red_free;                                 // the finishing warps have read them
   uint32_t abort_flag;
   int last;                                          // this CTA finishes the tile
-  float red[kDcBlocks][kDcRows * NP];                // the phases' sums of a tile
+  float scales[dc_stages(NP)][kDcBlocks][kDcRows];
+  float red[2 * dc_groups(NP)][kDcRows * NP];        // the consumers' sums of a tile, [token][row]
   GroupTable groups;
 };
 template <int NP>
@@ -111,35 +122,47 @@ __device__ __forceinline__ float one_float(uint16_t v) {
   return two_floats<F16>(uint32_t(v)).x;
 }
 
-// Eight products of two 16-byte chunks of 16-bit values, added to acc in order.
-template <bool F16>
-__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
-  const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 u = two_floats<F16>(aw[i]), v = two_floats<F16>(bw[i]);
-    acc = fmaf(u.x, v.x, acc);
-    acc = fmaf(u.y, v.y, acc);
-  }
-  return acc;
+// Byte offset of lane's copy of the table entry for byte J of `word`.
+template <int J>
+__device__ __forceinline__ uint32_t lut_at(uint32_t word, uint32_t lane4) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(word), "r"(lane4), "n"(0x5504 | (J << 4)));   // {lane4.b0, word.bJ, 0, 0}
+  return d;
 }
 
-// Byte offset of lane's copy of the table entry for byte j of `word`.
-__device__ __forceinline__ uint32_t lut_at(uint32_t word, int j, uint32_t lane4) {
-  const uint32_t shifted = j == 0 ? (word << 7) : (word >> (8 * j - 7));
-  return (shifted & 0x7f80u) | lane4;
-}
-
-struct Unit {
-  int rt, nt, kc;   // row group, 128-row tile, K chunk
-  int e;
+// A tile of the work list: row group, its expert and first row, 128 W rows.  The
+// roles walk the tiles of a share one after another.
+struct DcTile {
+  int rt, nt;
+  int e, row0;
 };
+__device__ __forceinline__ void dc_expert(const GroupTable* g, int E, int np, DcTile& t) {
+  t.e = expert_of_tile(g, E, t.rt);
+  t.row0 = g->start[t.e] + (t.rt - g->tiles[t.e]) * np;
+}
+__device__ __forceinline__ DcTile dc_tile(const GroupTable* g, int E, int np, int n_tiles, uint32_t tile) {
+  DcTile t;
+  t.rt = int(tile / uint32_t(n_tiles));
+  t.nt = int(tile) - t.rt * n_tiles;
+  dc_expert(g, E, np, t);
+  return t;
+}
+__device__ __forceinline__ void dc_next(const GroupTable* g, int E, int np, int n_tiles, DcTile& t) {
+  if (++t.nt < n_tiles) return;
+  t.nt = 0;
+  if (++t.rt < g->tiles[E]) dc_expert(g, E, np, t);
+}
 
 template <int NP, bool F16>
-__global__ void __launch_bounds__(kDcThreads, 1)
+__global__ void __launch_bounds__(dc_threads(NP), 1)
     expert_decode_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_x,
                          const DecodeParams p) {
   constexpr int kStages = dc_stages(NP);
+  constexpr int kGroups = dc_groups(NP);
+  constexpr int kConsumers = dc_consumers(NP);
+  constexpr int kScaler = kConsumers + kDcEpiWarps;  // first scale warp
+  constexpr int kProducer = kScaler + kGroups;
+  constexpr int kParts = 2 * kGroups;
   constexpr int NT8 = NP / 8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -151,74 +174,72 @@ __global__ void __launch_bounds__(kDcThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], kDcWarps);
+      mbar_init(&sh->full[s], 2);   // the producer and the scale warp
+      mbar_init(&sh->empty[s], kDcGroupWarps);
     }
+    mbar_init(&sh->red_full, kConsumers);
+    mbar_init(&sh->red_free, kDcEpiWarps);
     sh->abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
     tma_prefetch(&tm_codes);
     tma_prefetch(&tm_x);
   }
-  if (warp == kDcWarps) {
+  if (warp == kProducer) {
     build_groups(&sh->groups, p.offsets, p.E, p.M, NP, blockIdx.x == 0 ? p.status : nullptr);
-  } else {
+  } else if (warp < kConsumers) {
     // Lookup table: byte (even element in the high nibble) -> two levels in the
     // compute type, one copy per lane.
     uint32_t my = 0;
 #pragma unroll
     for (int c = 0; c < 16; ++c) my = (lane & 15) == c ? level_bits(c) : my;
     const float lv = __uint_as_float(my);
-    for (int e = warp; e < 256; e += kDcWarps) {
+    for (int e = warp; e < 256; e += kConsumers) {
       const float hi = __shfl_sync(0xffffffffu, lv, e >> 4);
       const float lo = __shfl_sync(0xffffffffu, lv, e & 15);
-      reinterpret_cast<uint32_t*>(lut)[e * 32 + lane] = two_rounded<F16>(hi, lo);
+      reinterpret_cast<uint32_t*>(lut)[e * 64 + lane] = two_rounded<F16>(hi, lo);
     }
   }
   __syncthreads();
 
-  const int64_t units = int64_t(sh->groups.tiles[p.E]) * p.n_tiles * p.k_chunks;
-  const int64_t G = min(int64_t(gridDim.x), units);   // CTAs with work: at least one unit each
-  const bool works = int64_t(blockIdx.x) < G;
-  const int64_t u0 = works ? units * blockIdx.x / G : 0, u1 = works ? units * (blockIdx.x + 1) / G : 0;
-  auto unit_at = [&](int64_t u) {
-    Unit r;
-    const int64_t tile = u / p.k_chunks;
-    r.kc = int(u - tile * p.k_chunks);
-    r.rt = int(tile / p.n_tiles);
-    r.nt = int(tile - int64_t(r.rt) * p.n_tiles);
-    r.e = expert_of_tile(&sh->groups, p.E, r.rt);
-    return r;
-  };
-  auto advance = [&](Unit& r) {
-    if (++r.kc < p.k_chunks) return;
-    r.kc = 0;
-    if (++r.nt < p.n_tiles) return;
-    r.nt = 0;
-    if (++r.rt < sh->groups.tiles[p.E]) r.e = expert_of_tile(&sh->groups, p.E, r.rt);
-  };
-  auto first_row = [&](const Unit& r) { return sh->groups.start[r.e] + (r.rt - sh->groups.tiles[r.e]) * NP; };
+  // Shares: CTA c of G takes units [units c / G, units (c + 1) / G).  G counts the
+  // CTAs with work, at least one unit each.
+  const GroupTable* groups = &sh->groups;
+  const uint32_t kch = uint32_t(p.k_chunks);
+  const uint32_t units = uint32_t(groups->tiles[p.E]) * uint32_t(p.n_tiles) * kch;   // < 2^31
+  const uint32_t G = min(gridDim.x, units);
+  const bool works = blockIdx.x < G;
+  const uint32_t u0 = works ? uint32_t(uint64_t(units) * blockIdx.x / G) : 0u;
+  const uint32_t u1 = works ? uint32_t(uint64_t(units) * (blockIdx.x + 1) / G) : 0u;
+  const uint32_t tile0 = u0 / kch;
+  const int kc0 = int(u0 - tile0 * kch);             // the share's first chunk of its first tile
 
-  if (warp == kDcWarps) {
+  if (warp == kProducer) {
     // ---------------- producer
-    if (lane == 0 && u0 < u1) {
-      Unit r = unit_at(u0);
-      int s = 0, issued = 0;
+    if (u0 < u1) {
+      DcTile t = dc_tile(groups, p.E, NP, p.n_tiles, tile0);
+      int kc = kc0, s = 0, issued = 0;
       uint32_t ph = 1;
-      for (int64_t u = u0; u < u1; ++u) {
-        if (!ring_wait(&sh->empty[s], ph, abort_flag, p.status)) break;
-        uint8_t* dst = smem + s * dc_stage_bytes(NP);
-        mbar_arrive_expect_tx(&sh->full[s], dc_stage_bytes(NP));
-        tma_load_3d(dst, &tm_codes, &sh->full[s], r.kc * 128, r.nt * kDcRows, r.e);
-        tma_load_3d(dst + kDcCodeBytes, &tm_x, &sh->full[s], 0, first_row(r), r.kc * kDcBlocks);
-        advance(r);
+      for (uint32_t u = u0; u < u1; ++u) {
+        if (!warp_wait(&sh->empty[s], ph, abort_flag, p.status)) break;
+        if (lane == 0) {
+          uint8_t* dst = smem + s * dc_stage_bytes(NP);
+          mbar_arrive_expect_tx(&sh->full[s], dc_stage_bytes(NP));
+          tma_load_3d(dst, &tm_codes, &sh->full[s], kc * 128, t.nt * kDcRows, t.e);
+          tma_load_3d(dst + kDcCodeBytes, &tm_x, &sh->full[s], 0, t.row0, kc * kDcBlocks);
+        }
+        __syncwarp();
+        if (++kc == p.k_chunks) {
+          kc = 0;
+          dc_next(groups, p.E, NP, p.n_tiles, t);
+        }
         ++issued;
         if (++s == kStages) {
           s = 0;
           ph ^= 1;
         }
       }
-      if (*abort_flag)   // unwind: wait (bounded) for the copies in flight
+      if (*abort_flag)   // unwind: wait (bounded) for the boxes in flight
         for (int j = max(0, issued - kStages); j < issued; ++j) {
           uint32_t none = 0;
           ring_wait(&sh->full[j % kStages], (j / kStages) & 1, &none, nullptr);
@@ -227,171 +248,299 @@ __global__ void __launch_bounds__(kDcThreads, 1)
     return;
   }
 
-  // ---------------- consumers: warp = (set of 32 rows, K block of the unit)
-  const int set = warp & (kDcSets - 1);
-  const int phase = warp >> 2;
+  if (warp >= kScaler) {
+    // ---------------- scales of a group's units: loaded a unit ahead, stored when
+    // the stage is free
+    const int group = warp - kScaler;
+    const bool dq = p.dq != 0;
+    const float s_g = dq ? __ldg(p.absmax_scale) : 0.0f;
+    const int kb_per_row = p.K >> 6;
+    // Block 64 and whole chunks: a row's four scales of a unit are one aligned word or vector.
+    const bool vec = p.vec_scales != 0;
+    uint4 raw[4];
+    auto load_scales = [&](const DcTile& t, int kc) {   // rows lane, lane + 32, ...
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = min(t.nt * kDcRows + 32 * i + lane, p.N - 1);
+        const int64_t at = (int64_t(t.e) * p.N + n) * p.K + int64_t(kc) * (64 * kDcBlocks);
+        if (vec) {
+          if (dq) raw[i].x = __ldg(reinterpret_cast<const uint32_t*>(p.absmax_q + (at >> 6)));
+          else raw[i] = __ldg(reinterpret_cast<const uint4*>(p.absmax + (at >> 6)));
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t b = (at + min(j, kb_per_row - 1 - kc * kDcBlocks) * 64) >> p.bs_shift;
+            w[j] = dq ? uint32_t(__ldg(p.absmax_q + b)) : __float_as_uint(__ldg(p.absmax + b));
+          }
+          raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    };
+    DcTile t{};
+    int kc = kc0 + group;
+    auto settle = [&]() {   // (t, kc) to the tile that holds the chunk
+      while (kc >= p.k_chunks) {
+        kc -= p.k_chunks;
+        dc_next(groups, p.E, NP, p.n_tiles, t);
+      }
+    };
+    if (u0 + uint32_t(group) < u1) {
+      t = dc_tile(groups, p.E, NP, p.n_tiles, tile0);
+      settle();
+      load_scales(t, kc);
+    }
+    int s = group;
+    uint32_t ph = 1;
+    for (uint32_t u = u0 + group; u < u1; u += kGroups) {
+      uint4 now[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) now[i] = raw[i];
+      if (u + kGroups < u1) {
+        kc += kGroups;
+        settle();
+        load_scales(t, kc);
+      }
+      if (!warp_wait(&sh->empty[s], ph, abort_flag, p.status)) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+        if (vec && dq) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = (now[i].x >> (8 * j)) & 0xffu;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sh->scales[s][j][32 * i + lane] = dq ? __fmul_rn(float(w[j]), s_g) : __uint_as_float(w[j]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->full[s]);
+      s += kGroups;
+      if (s >= kStages) {
+        s -= kStages;
+        ph ^= 1;
+      }
+    }
+    return;
+  }
+
+  if (warp >= kConsumers) {
+    // ---------------- finishing warps: a thread per row of the tile
+    constexpr int kEpi = 32 * kDcEpiWarps;
+    const int first = threadIdx.x - 32 * kConsumers;
+    bool ok = true, waited = false;
+    uint32_t ph = 0;
+    DcTile t{};
+    if (u0 < u1) t = dc_tile(groups, p.E, NP, p.n_tiles, tile0);
+    uint32_t tile_u = tile0 * kch;            // first unit of the tile, in whatever CTA
+    for (uint32_t u = u0; u < u1; tile_u += kch, dc_next(groups, p.E, NP, p.n_tiles, t)) {
+      const bool starts = u == tile_u;        // this CTA has the tile's first chunk
+      const uint32_t end = min(u1, tile_u + kch);
+      const bool split = end - u < kch;
+      u = end;
+      const int rows = min(NP, groups->start[t.e + 1] - t.row0);
+      const int64_t n0 = int64_t(t.e) * p.N;
+      if (starts)
+        for (int row = first; row < kDcRows; row += kEpi) {
+          const uint16_t* b = p.B + (n0 + min(t.nt * kDcRows + row, p.N - 1)) * p.r;
+          for (int j = 0; j < p.r; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + j));
+        }
+      if (!waited) grid_dep_wait();   // the counters' zeros, of the kernel before
+      waited = true;
+      if (ok) ok = warp_wait<100>(&sh->red_full, ph, abort_flag, p.status);
+      ph ^= 1;
+      auto part_sum = [&](int m, int row) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) v += sh->red[i][m * kDcRows + row];
+        return v;
+      };
+      uint32_t c0 = 0, c1 = 0;
+      bool finish = true;
+      if (split) {
+        // contributors are consecutive CTAs, the first from chunk 0
+        c0 = uint32_t((uint64_t(tile_u + 1) * G - 1) / units);
+        c1 = uint32_t((uint64_t(tile_u + kch) * G - 1) / units);
+        float* mine = p.partials + (size_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * (kDcRows * NP);
+        for (int row = first; row < kDcRows; row += kEpi)
+          for (int m = 0; m < rows; ++m) __stcg(mine + m * kDcRows + row, part_sum(m, row));
+        __threadfence();
+        named_barrier(1, kEpi);
+        if (first == 0) sh->last = atomicAdd(p.counters + c0, 1) == int(c1 - c0);
+        named_barrier(1, kEpi);
+        finish = sh->last != 0;
+        if (finish) __threadfence();
+      }
+      if (finish && ok) {
+        for (int row = first; row < kDcRows; row += kEpi) {
+          const int n = t.nt * kDcRows + row;
+          if (n >= p.N) continue;
+          const float bias = p.bias != nullptr ? one_float<F16>(__ldg(p.bias + n0 + n)) : 0.0f;
+          uint16_t* y = p.y + int64_t(t.row0) * p.N + n;
+          for (int m = 0; m < rows; ++m, y += p.N) {
+            float v = 0.0f;
+            if (!split) v = part_sum(m, row);
+            else
+              for (uint32_t c = c0; c <= c1; ++c)
+                v += __ldcg(p.partials + (size_t(c) * 2 + (c == c0 ? 1 : 0)) * (kDcRows * NP) + m * kDcRows + row);
+            *y = one_rounded<F16>(v + bias);
+          }
+        }
+      }
+      named_barrier(1, kEpi);   // red and last may be written again
+      if (lane == 0) mbar_arrive(&sh->red_free);
+    }
+    if (!waited) grid_dep_wait();
+    return;
+  }
+
+  // ---------------- consumers
+  const int group = warp / kDcGroupWarps;
+  const int pair = (warp >> 2) & 1;         // K blocks 2 pair, 2 pair + 1 of the unit
+  const int set = warp & 3;                 // rows 32 set ..
   const int g = lane >> 2, q = lane & 3;
   const uint32_t lane4 = uint32_t(lane) << 2;
-  const bool dq = p.dq != 0;
-  const float s_g = dq ? __ldg(p.absmax_scale) : 0.0f;
   const int kb_per_row = p.K >> 6;
-  // The four rows of this thread: two 16-row groups, W rows 2 g and 2 g + 1 of
-  // each (MMA rows g and g + 8): a half-warp's code loads then hit different
-  // bank groups.
-  auto raw_scales = [&](const Unit& r, uint32_t (&raw)[4]) {
-    const int ch = min(r.kc * kDcBlocks + phase, kb_per_row - 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = min(r.nt * kDcRows + set * 32 + (i >> 1) * 16 + 2 * g + (i & 1), p.N - 1);
-      const int64_t b = chunk_block(int64_t(r.e) * p.N + n, p.K, ch, p.bs_shift);
-      raw[i] = dq ? uint32_t(__ldg(p.absmax_q + b)) : __float_as_uint(__ldg(p.absmax + b));
-    }
-  };
-
-  int s = 0;
-  uint32_t ph = 0;
   bool ok = true, waited = false;
-  uint32_t raw[4] = {0, 0, 0, 0};
-  Unit r{};
-  if (u0 < u1) {
-    r = unit_at(u0);
-    raw_scales(r, raw);
+  int s = group;
+  uint32_t ph = 0, red_ph = 1;
+  // Addresses inside a stage, of the first of the two blocks.  This thread's four
+  // rows: two 16-row groups (2048 bytes apart), W rows 2 g and 2 g + 1 of each (MMA
+  // rows g and g + 8): a half-warp's code loads then hit different bank groups.
+  uint32_t code_at[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t row = uint32_t(set * 32 + 2 * g + i);
+    code_at[i] = row * 128u + (((4u * uint32_t(pair) + uint32_t(q >> 1)) ^ (row & 7u)) << 4) + (uint32_t(q & 1) << 3);
   }
-  int64_t u = u0;
-  while (u < u1) {
-    const Unit tile = r;                 // first unit of this CTA's part of the tile
-    const int k0 = r.kc;
-    const int k1 = int(min(int64_t(p.k_chunks), int64_t(k0) + (u1 - u)));
+  const uint32_t x_at = kDcCodeBytes + uint32_t(pair) * (2 * NP * 128) + sw128_offset(uint32_t(g), uint32_t(2 * q));
+  DcTile t{};
+  if (u0 < u1) t = dc_tile(groups, p.E, NP, p.n_tiles, tile0);
+  int kc = kc0 + group;                     // chunk of this warp's next unit, counted from tile t
+  uint32_t tile_u = tile0 * kch;
+  for (uint32_t seg = u0; seg < u1; tile_u += kch, dc_next(groups, p.E, NP, p.n_tiles, t)) {
+    const bool first_part = seg == tile_u;
+    seg = min(u1, tile_u + kch);
+    const int kend = int(seg - tile_u);     // this CTA's chunks of the tile end here
     float acc[2][NT8][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int t = 0; t < NT8; ++t) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.0f;
-    for (int kc = k0; kc < k1; ++kc, ++u) {
-      float sc[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i] = dq ? __fmul_rn(float(raw[i]), s_g) : __uint_as_float(raw[i]);
-      advance(r);
-      if (u + 1 < u1) raw_scales(r, raw);
+      for (int c = 0; c < NT8; ++c) acc[i][c][0] = acc[i][c][1] = acc[i][c][2] = acc[i][c][3] = 0.0f;
+    for (; kc < kend; kc += kGroups) {
       if (ok) ok = warp_wait(&sh->full[s], ph, abort_flag, p.status);
-      if (ok && kc * kDcBlocks + phase < kb_per_row) {
-        const uint8_t* cb = smem + s * dc_stage_bytes(NP);
-        const uint8_t* xt = cb + kDcCodeBytes + phase * (NP * 128);
-        uint4 xl[NT8], xh[NT8];
+      if (ok) {
+        const uint8_t* st = smem + s * dc_stage_bytes(NP);
+        const float* sc = &sh->scales[s][2 * pair][set * 32 + 2 * g];
 #pragma unroll
-        for (int t = 0; t < NT8; ++t) {
-          xl[t] = *reinterpret_cast<const uint4*>(xt + sw128_offset(uint32_t(8 * t + g), uint32_t(2 * q)));
-          xh[t] = *reinterpret_cast<const uint4*>(xt + sw128_offset(uint32_t(8 * t + g), uint32_t(2 * q + 1)));
-        }
+        for (int j = 0; j < 2; ++j) {
+          if (kc * kDcBlocks + 2 * pair + j >= kb_per_row) break;   // past the row's end
+          uint4 xl[NT8], xh[NT8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t row = uint32_t(set * 32 + i * 16 + 2 * g);
-          const uint32_t chunk = 2u * uint32_t(phase) + uint32_t(q >> 1);
-          const uint2 w0 = *reinterpret_cast<const uint2*>(cb + row * 128u + ((chunk ^ (row & 7u)) << 4) + ((q & 1) << 3));
-          const uint2 w1 = *reinterpret_cast<const uint2*>(cb + (row + 1) * 128u + ((chunk ^ ((row + 1) & 7u)) << 4) + ((q & 1) << 3));
-          uint32_t a[4][4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t wa = k < 2 ? w0.x : w0.y, wb = k < 2 ? w1.x : w1.y;
-            const int j = (2 * k) & 3;
-            a[k][0] = *reinterpret_cast<const uint32_t*>(lut + lut_at(wa, j, lane4));
-            a[k][1] = *reinterpret_cast<const uint32_t*>(lut + lut_at(wb, j, lane4));
-            a[k][2] = *reinterpret_cast<const uint32_t*>(lut + lut_at(wa, j + 1, lane4));
-            a[k][3] = *reinterpret_cast<const uint32_t*>(lut + lut_at(wb, j + 1, lane4));
+          for (int c = 0; c < NT8; ++c) {
+            xl[c] = *reinterpret_cast<const uint4*>(st + x_at + j * (NP * 128) + c * 1024);
+            xh[c] = *reinterpret_cast<const uint4*>(st + (x_at ^ 16u) + j * (NP * 128) + c * 1024);
           }
 #pragma unroll
-          for (int t = 0; t < NT8; ++t) {
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma_16816<F16>(d, a[0], xl[t].x, xl[t].y);
-            mma_16816<F16>(d, a[1], xl[t].z, xl[t].w);
-            mma_16816<F16>(d, a[2], xh[t].x, xh[t].y);
-            mma_16816<F16>(d, a[3], xh[t].z, xh[t].w);
-            acc[i][t][0] = fmaf(sc[2 * i], d[0], acc[i][t][0]);
-            acc[i][t][1] = fmaf(sc[2 * i], d[1], acc[i][t][1]);
-            acc[i][t][2] = fmaf(sc[2 * i + 1], d[2], acc[i][t][2]);
-            acc[i][t][3] = fmaf(sc[2 * i + 1], d[3], acc[i][t][3]);
+          for (int i = 0; i < 2; ++i) {
+            const uint2 w0 = *reinterpret_cast<const uint2*>(st + (code_at[0] ^ (j * 32u)) + i * 2048);
+            const uint2 w1 = *reinterpret_cast<const uint2*>(st + (code_at[1] ^ (j * 32u)) + i * 2048);
+            const float2 scale = *reinterpret_cast<const float2*>(sc + j * kDcRows + i * 16);
+            uint32_t a[4][4];
+            auto look = [&](uint32_t at) { return *reinterpret_cast<const uint32_t*>(lut + at); };
+            a[0][0] = look(lut_at<0>(w0.x, lane4)); a[0][1] = look(lut_at<0>(w1.x, lane4));
+            a[0][2] = look(lut_at<1>(w0.x, lane4)); a[0][3] = look(lut_at<1>(w1.x, lane4));
+            a[1][0] = look(lut_at<2>(w0.x, lane4)); a[1][1] = look(lut_at<2>(w1.x, lane4));
+            a[1][2] = look(lut_at<3>(w0.x, lane4)); a[1][3] = look(lut_at<3>(w1.x, lane4));
+            a[2][0] = look(lut_at<0>(w0.y, lane4)); a[2][1] = look(lut_at<0>(w1.y, lane4));
+            a[2][2] = look(lut_at<1>(w0.y, lane4)); a[2][3] = look(lut_at<1>(w1.y, lane4));
+            a[3][0] = look(lut_at<2>(w0.y, lane4)); a[3][1] = look(lut_at<2>(w1.y, lane4));
+            a[3][2] = look(lut_at<3>(w0.y, lane4)); a[3][3] = look(lut_at<3>(w1.y, lane4));
+#pragma unroll
+            for (int c = 0; c < NT8; ++c) {
+              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma_16816<F16>(d, a[0], xl[c].x, xl[c].y);
+              mma_16816<F16>(d, a[1], xl[c].z, xl[c].w);
+              mma_16816<F16>(d, a[2], xh[c].x, xh[c].y);
+              mma_16816<F16>(d, a[3], xh[c].z, xh[c].w);
+              acc[i][c][0] = fmaf(scale.x, d[0], acc[i][c][0]);
+              acc[i][c][1] = fmaf(scale.x, d[1], acc[i][c][1]);
+              acc[i][c][2] = fmaf(scale.y, d[2], acc[i][c][2]);
+              acc[i][c][3] = fmaf(scale.y, d[3], acc[i][c][3]);
+            }
           }
         }
       }
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&sh->empty[s]);
-      if (++s == kStages) {
-        s = 0;
+      s += kGroups;
+      if (s >= kStages) {
+        s -= kStages;
         ph ^= 1;
       }
     }
+    kc -= p.k_chunks;
 
-    // ---------------- this CTA's part of the tile: the four phases meet in
-    // shared memory, [token][row] so that neighbouring threads take neighbouring rows
+    // The adapter's product enters the tile's first part, as MMAs with the rows
+    // of B_e as A and T as B; the pairs of K halves take 16 columns in turn.
+    if (first_part) {
+      if (!waited) grid_dep_wait();   // T of the kernel before
+      waited = true;
+      for (int j0 = 16 * (2 * group + pair); j0 < p.r; j0 += 16 * kParts) {
+        const int ja = j0 + 2 * q, jb = ja + 8;   // r is a multiple of 8: the second half may be missing
+        uint32_t tb[NT8][2];
+#pragma unroll
+        for (int c = 0; c < NT8; ++c) {
+          const int m = t.row0 + 8 * c + g;
+          const uint16_t* trow = p.T + int64_t(min(m, p.M - 1)) * p.r;
+          tb[c][0] = m < p.M ? __ldcg(reinterpret_cast<const uint32_t*>(trow + ja)) : 0u;
+          tb[c][1] = m < p.M && jb < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(trow + jb)) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t a[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int n = min(t.nt * kDcRows + set * 32 + i * 16 + 2 * g + h, p.N - 1);
+            const uint16_t* brow = p.B + (int64_t(t.e) * p.N + n) * p.r;
+            a[h] = __ldg(reinterpret_cast<const uint32_t*>(brow + ja));
+            a[2 + h] = jb < p.r ? __ldg(reinterpret_cast<const uint32_t*>(brow + jb)) : 0u;
+          }
+#pragma unroll
+          for (int c = 0; c < NT8; ++c) mma_16816<F16>(acc[i][c], a, tb[c][0], tb[c][1]);
+        }
+      }
+    }
+
+    // the tile's sums, for the finishing warps
+    if (ok) ok = warp_wait(&sh->red_free, red_ph, abort_flag, p.status);
+    red_ph ^= 1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = set * 32 + i * 16 + 2 * g;
 #pragma unroll
-      for (int t = 0; t < NT8; ++t) {
-        float* o = sh->red[phase] + (8 * t + 2 * q) * kDcRows + row;
-        *reinterpret_cast<float2*>(o) = make_float2(acc[i][t][0], acc[i][t][2]);
-        *reinterpret_cast<float2*>(o + kDcRows) = make_float2(acc[i][t][1], acc[i][t][3]);
+      for (int c = 0; c < NT8; ++c) {
+        float* o = sh->red[2 * group + pair] + (8 * c + 2 * q) * kDcRows + row;
+        *reinterpret_cast<float2*>(o) = make_float2(acc[i][c][0], acc[i][c][2]);
+        *reinterpret_cast<float2*>(o + kDcRows) = make_float2(acc[i][c][1], acc[i][c][3]);
       }
     }
-    if (!waited) grid_dep_wait();   // T, and the counters' zeros, of the kernel before
-    waited = true;
-    named_barrier(1, 32 * kDcWarps);
-    const int row0 = first_row(tile);
-    const int rows = min(NP, sh->groups.start[tile.e + 1] - row0);
-    const int trow = threadIdx.x & (kDcRows - 1);
-    const int n = tile.nt * kDcRows + trow;
-    const int tok0 = threadIdx.x >> 7;
-    float v[NP / 4];
-#pragma unroll
-    for (int i = 0; i < NP / 4; ++i) {
-      const int at = (tok0 + 4 * i) * kDcRows + trow;
-      v[i] = (sh->red[0][at] + sh->red[1][at]) + (sh->red[2][at] + sh->red[3][at]);
-    }
-    bool finish = true;
-    if (k1 - k0 < p.k_chunks) {
-      // split tile: contributors are consecutive CTAs, the first from chunk 0
-      const int64_t t0 = (int64_t(tile.rt) * p.n_tiles + tile.nt) * p.k_chunks, t1 = t0 + p.k_chunks;
-      const int c0 = int(((t0 + 1) * G - 1) / units), c1 = int((t1 * G - 1) / units);
-      float* mine = p.partials + (size_t(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0)) * (kDcRows * NP);
-#pragma unroll
-      for (int i = 0; i < NP / 4; ++i) __stcg(mine + (tok0 + 4 * i) * kDcRows + trow, v[i]);
-      __threadfence();
-      named_barrier(1, 32 * kDcWarps);
-      if (threadIdx.x == 0) sh->last = atomicAdd(p.counters + c0, 1) == c1 - c0;
-      named_barrier(1, 32 * kDcWarps);
-      finish = sh->last != 0;
-      if (finish) {
-        __threadfence();
-#pragma unroll
-        for (int i = 0; i < NP / 4; ++i) v[i] = 0.0f;
-        for (int c = c0; c <= c1; ++c) {
-          const float* from = p.partials + (size_t(c) * 2 + (c == c0 ? 1 : 0)) * (kDcRows * NP);
-#pragma unroll
-          for (int i = 0; i < NP / 4; ++i) v[i] += __ldcg(from + (tok0 + 4 * i) * kDcRows + trow);
-        }
-      }
-    }
-    if (finish && ok && n < p.N) {
-      const uint16_t* b = p.B + (int64_t(tile.e) * p.N + n) * p.r;
-      float ad[NP / 4];
-#pragma unroll
-      for (int i = 0; i < NP / 4; ++i) ad[i] = 0.0f;
-      for (int j = 0; j < p.r; j += 8) {
-        const uint4 bv = __ldg(reinterpret_cast<const uint4*>(b + j));
-#pragma unroll
-        for (int i = 0; i < NP / 4; ++i)
-          if (tok0 + 4 * i < rows)
-            ad[i] = dot8<F16>(bv, __ldcg(reinterpret_cast<const uint4*>(p.T + int64_t(row0 + tok0 + 4 * i) * p.r + j)), ad[i]);
-      }
-      const float bias = p.bias != nullptr ? one_float<F16>(p.bias[int64_t(tile.e) * p.N + n]) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < NP / 4; ++i)
-        if (tok0 + 4 * i < rows)
-          p.y[int64_t(row0 + tok0 + 4 * i) * p.N + n] = one_rounded<F16>(v[i] + ad[i] + bias);
-    }
-    named_barrier(1, 32 * kDcWarps);   // red and last may be written again
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->red_full);
   }
-  if (!waited) grid_dep_wait();
+}
+
+// Eight products of two 16-byte chunks of 16-bit values, added to acc in order.
+template <bool F16>
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
+  const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = two_floats<F16>(aw[i]), v = two_floats<F16>(bw[i]);
+    acc = fmaf(u.x, v.x, acc);
+    acc = fmaf(u.y, v.y, acc);
+  }
+  return acc;
 }
 
 // T = s x A_e^T for a few rows: one CTA per adapter row and token, fp32 sums in
@@ -445,7 +594,7 @@ template <int NP, bool F16>
 cudaError_t launch(const ExpertDecode& L, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(L.grid, 1, 1);
-  cfg.blockDim = dim3(kDcThreads, 1, 1);
+  cfg.blockDim = dim3(dc_threads(NP), 1, 1);
   cfg.dynamicSmemBytes = dc_smem<NP>();
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -462,7 +611,7 @@ size_t decode_scratch_bytes() { return size_t(kDecodeMaxCtas) * (2 * kDcRows * 1
 
 bool ExpertDecode::prepare(const GroupedArgs& g, const void* T, uint8_t* scratch, int sms) {
   const LinearArgs& a = g.lin;
-  np = a.M <= 8 ? 8 : 16;
+  np = a.M <= 8 || a.M <= 4 * int64_t(g.E) ? 8 : 16;   // rows of an expert per pass over its weight
   f16 = a.f16 != 0;
   const uint64_t K = uint64_t(a.K), N = uint64_t(a.N), M = uint64_t(a.M), kb = K / 64;
   bool ok = encode_map_stack(&codes, a.w->codes, MapElem::kU8, K / 2, N, uint64_t(g.E), 128, kDcRows,
@@ -493,7 +642,9 @@ bool ExpertDecode::prepare(const GroupedArgs& g, const void* T, uint8_t* scratch
   p.partials = reinterpret_cast<float*>(scratch);
   p.counters = reinterpret_cast<int*>(scratch + size_t(kDecodeMaxCtas) * 2 * kDcRows * 16 * sizeof(float));
   p.status = a.status;
+  p.vec_scales = a.w->block_size == 64 && a.K % 256 == 0;   // scale pointers are 16-byte aligned
   const int64_t most = max_row_tiles(a.M, g.E, np) * p.n_tiles * p.k_chunks;
+  if (most > int64_t(0x7fffffff)) return false;
   grid = unsigned(std::min<int64_t>(std::min(sms, kDecodeMaxCtas), most));
   return ok;
 }

@@ -13,6 +13,7 @@ struct DecodeParams {
   int M, E, N, K, r;
   int n_tiles, k_chunks;    // 128-row tiles of an expert, 256-wide chunks of a row
   int bs_shift, dq;
+  int vec_scales;           // a row's four scales of a chunk are one aligned vector
   const int32_t* offsets;
   const uint8_t* absmax_q;
   const float* absmax;

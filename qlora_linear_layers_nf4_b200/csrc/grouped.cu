@@ -36,13 +36,11 @@ cudaError_t launch_grouped_fwd(const GroupedArgs& g, int sms, cudaStream_t st, i
   if (a.f32) return launch_grouped_fwd_f32(g, st, launches);
   void* T = a.t_out ? a.t_out : a.ws + kWsHeader;
   cudaError_t e;
-  if (use_decode(a.M, g.E)) {
-    ExpertDecode d;
+  ExpertDecode d;
+  if (use_decode(a.M, g.E) && d.prepare(g, T, a.ws + kWsHeader + mr_bytes(a.M, a.r), sms)) {
     ExpertRank t;
     const bool small = a.M * a.r <= kSmallT;
-    bool ok = d.prepare(g, T, a.ws + kWsHeader + mr_bytes(a.M, a.r), sms);
-    ok = ok && (small || t.prepare(g, kRankT, nullptr, nullptr, T, nullptr));
-    if (!ok) return cudaErrorInvalidValue;
+    if (!small && !t.prepare(g, kRankT, nullptr, nullptr, T, nullptr)) return cudaErrorInvalidValue;
     if (small) {
       e = launch_expert_t_small(g, T, d.p.counters, st, launches);
     } else {
