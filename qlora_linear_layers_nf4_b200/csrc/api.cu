@@ -623,19 +623,10 @@ nf4_status int8_linear_fwd(const int8_t* w_codes, const float* w_scale, int64_t 
   a.y = y;
   a.ws = static_cast<uint8_t*>(workspace);
   a.status = reinterpret_cast<uint32_t*>(a.ws + nf4::kWsStatus);
+  int8_t* codes = reinterpret_cast<int8_t*>(a.ws + nf4::kWsHeader);
+  float* scales = reinterpret_cast<float*>(codes + round_up(size_t(M) * size_t(K), 256));
   int launches = 0;
-  cudaError_t e = cudaSuccess;
-  if (x_scale == nullptr) {
-    int8_t* codes = reinterpret_cast<int8_t*>(a.ws + nf4::kWsHeader);
-    float* scales = reinterpret_cast<float*>(codes + round_up(size_t(M) * size_t(K), 256));
-    e = nf4::launch_int8_quantize(x, compute_dtype, M, K, codes, scales, sm_count(), st, &launches);
-    a.x = codes;
-    a.x_scale = scales;
-  } else {
-    a.x = static_cast<const int8_t*>(x);
-    a.x_scale = x_scale;
-  }
-  if (e == cudaSuccess) e = nf4::launch_int8_linear(a, sm_count(), st, &launches);
+  const cudaError_t e = nf4::launch_int8_linear(a, x, x_scale, codes, scales, sm_count(), st, &launches);
   return finish(e, launches);
 }
 

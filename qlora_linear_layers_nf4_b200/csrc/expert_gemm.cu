@@ -620,8 +620,8 @@ cudaError_t ExpertGemm::run(cudaStream_t st, int* launches) const {
   return f16 ? launch<kFwd, true>(*this, kKGroupedFwd, st, launches) : launch<kFwd, false>(*this, kKGroupedFwd, st, launches);
 }
 
-cudaError_t launch_int8_gemm(const Int8LinearArgs& a, int sms, cudaStream_t st, int* launches) {
-  ExpertGemm L;
+bool Int8Gemm::prepare(const Int8LinearArgs& a, int sms) {
+  ExpertGemm& L = g;
   const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t M = uint64_t(a.M), N = uint64_t(a.N), K = uint64_t(a.K);
   bool ok = encode_map_2d(&L.maps.tok_l, a.x, MapElem::kU8, K, M, 128, 128, s128) &&
@@ -641,8 +641,11 @@ cudaError_t launch_int8_gemm(const Int8LinearArgs& a, int sms, cudaStream_t st, 
   p.w_scale = a.w_scale;
   p.x_scale = a.x_scale;
   p.status = a.status;
-  if (!ok || !set_grid(&L, sms)) return cudaErrorInvalidValue;
-  return launch<kI8, false>(L, kKInt8Linear, st, launches);
+  return ok && set_grid(&L, sms);
+}
+
+cudaError_t Int8Gemm::run(cudaStream_t st, int* launches) const {
+  return launch<kI8, false>(g, kKInt8Linear, st, launches);
 }
 
 }  // namespace nf4

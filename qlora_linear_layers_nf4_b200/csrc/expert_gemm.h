@@ -49,6 +49,10 @@ struct ExpertGemm {
 };
 
 // The 8-bit linear on the tensor cores.
-cudaError_t launch_int8_gemm(const Int8LinearArgs& a, int sms, cudaStream_t st, int* launches);
+struct Int8Gemm {
+  ExpertGemm g;
+  bool prepare(const Int8LinearArgs& a, int sms);
+  cudaError_t run(cudaStream_t st, int* launches) const;
+};
 
 }  // namespace nf4

@@ -180,6 +180,165 @@ cudaError_t quantize_t(const void* x, int64_t rows, int64_t cols, int8_t* codes,
              : cudaLaunchKernelEx(&cfg, int8_quantize_kernel<T, false>, xt, int(cols), codes, scales);
 }
 
+// ------------------------------------------------------------------ linear, few tokens
+
+// y for up to eight tokens: the weight bytes are the whole cost, and one launch
+// the largest other one, so the tokens are quantized here too.  A CTA holds the
+// codes of all tokens in shared memory (every CTA makes them again: 2 M K bytes
+// from L2 against a kernel of its own) and 32 weight rows, two to a warp, whose
+// first 4 KB are already on their way while the tokens are quantized.  Sums by
+// dp4a, exact; the warp's lanes meet in one integer reduction a sum.
+constexpr int kSmThreads = 512;
+constexpr int kSmRows = 2;                             // weight rows per warp
+constexpr int kSmTileRows = kSmRows * kSmThreads / 32;
+constexpr int kSmAhead = 4;                            // 16-byte loads a lane has in flight per row
+constexpr int64_t kSmMaxCodes = 160 * 1024;            // M * K
+
+template <typename T, int MT>
+__global__ void __launch_bounds__(kSmThreads) int8_small_kernel(const Int8LinearArgs a, const T* __restrict__ x,
+                                                               const float* __restrict__ given_scale) {
+  extern __shared__ __align__(16) int8_t codes[];      // [M][K]
+  __shared__ float scale[MT];
+  __shared__ uint32_t part[kSmThreads / 32];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int K = int(a.K), M = int(a.M);
+  const int vecs = K / 16;
+  grid_dep_wait();
+  const int64_t n0 = int64_t(blockIdx.x) * kSmTileRows + warp * kSmRows;
+  const uint4* w[kSmRows];
+#pragma unroll
+  for (int i = 0; i < kSmRows; ++i) w[i] = reinterpret_cast<const uint4*>(a.w + (n0 + i < a.N ? n0 + i : a.N - 1) * a.K);
+  uint4 wv[kSmRows][kSmAhead];
+  auto load_w = [&](int v0) {
+#pragma unroll
+    for (int j = 0; j < kSmAhead; ++j)
+#pragma unroll
+      for (int i = 0; i < kSmRows; ++i) {
+        const int v = v0 + 32 * j + lane;
+        wv[i][j] = v < vecs ? __ldg(w[i] + v) : make_uint4(0u, 0u, 0u, 0u);
+      }
+  };
+  load_w(0);
+
+  if constexpr (sizeof(T) == 1) {
+    for (int i = t; i < M * vecs; i += kSmThreads)
+      reinterpret_cast<uint4*>(codes)[i] = __ldg(reinterpret_cast<const uint4*>(x) + i);
+    if (t < M) scale[t] = given_scale[t];
+  } else {
+    constexpr int V = Elem<T>::kVec;
+    for (int m = 0; m < M; ++m) {
+      const uint4* xv = reinterpret_cast<const uint4*>(x + int64_t(m) * K);
+      uint32_t top = 0;
+      for (int i = t; i < K / V; i += kSmThreads) {
+        float f[V];
+        Elem<T>::unpack(__ldg(xv + i), f);
+#pragma unroll
+        for (int u = 0; u < V; ++u) top = max(top, __float_as_uint(f[u]) & 0x7fffffffu);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) part[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kSmThreads / 32; ++i) top = max(top, part[i]);
+      const RowScale r = row_scale(top);
+      if (t == 0) scale[m] = r.s;
+      for (int i = t; i < K / V; i += kSmThreads) {
+        float f[V];
+        Elem<T>::unpack(__ldg(xv + i), f);
+        uint32_t c[V / 4];
+#pragma unroll
+        for (int g = 0; g < V / 4; ++g) {
+          c[g] = 0;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) c[g] |= (uint32_t(int8_code(f[4 * g + u], r)) & 0xffu) << (8 * u);
+          reinterpret_cast<uint32_t*>(codes)[(m * K + i * V) / 4 + g] = c[g];
+        }
+      }
+      __syncthreads();   // part may be written again
+    }
+  }
+  __syncthreads();
+
+  int acc[kSmRows][MT];
+#pragma unroll
+  for (int i = 0; i < kSmRows; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[i][m] = 0;
+  for (int v0 = 0; v0 < vecs; v0 += 32 * kSmAhead) {
+#pragma unroll
+    for (int j = 0; j < kSmAhead; ++j) {
+      const int v = v0 + 32 * j + lane;
+      if (v < vecs) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (m >= M) break;
+          const uint4 c = *reinterpret_cast<const uint4*>(codes + m * K + v * 16);
+#pragma unroll
+          for (int i = 0; i < kSmRows; ++i) {
+            int s = acc[i][m];
+            s = __dp4a(int(wv[i][j].x), int(c.x), s);
+            s = __dp4a(int(wv[i][j].y), int(c.y), s);
+            s = __dp4a(int(wv[i][j].z), int(c.z), s);
+            acc[i][m] = __dp4a(int(wv[i][j].w), int(c.w), s);
+          }
+        }
+      }
+    }
+    if (v0 + 32 * kSmAhead < vecs) load_w(v0 + 32 * kSmAhead);
+  }
+#pragma unroll
+  for (int i = 0; i < kSmRows; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (m >= M) break;
+      const int sum = __reduce_add_sync(0xffffffffu, acc[i][m]);
+      const int64_t n = n0 + i;
+      if (lane == m && n < a.N) {
+        float v = __fmul_rn(__fmul_rn(float(sum), scale[m]), a.w_scale[n]);
+        const int64_t at = int64_t(m) * a.N + n;
+        if (a.dtype == NF4_F32) {
+          if (a.bias != nullptr) v = __fadd_rn(v, static_cast<const float*>(a.bias)[n]);
+          static_cast<float*>(a.y)[at] = v;
+        } else if (a.dtype == NF4_F16) {
+          if (a.bias != nullptr) v = __fadd_rn(v, __half2float(static_cast<const __half*>(a.bias)[n]));
+          static_cast<__half*>(a.y)[at] = __float2half_rn(v);
+        } else {
+          if (a.bias != nullptr) v = __fadd_rn(v, __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[n]));
+          static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+        }
+      }
+    }
+}
+
+template <typename T, int MT>
+cudaError_t small_tm(const Int8LinearArgs& a, const void* x, const float* scale, cudaStream_t st) {
+  static PerDeviceOnce attr_done;
+  const int dev = PerDeviceOnce::current();
+  if (!attr_done.done(dev)) {
+    const cudaError_t e = cudaFuncSetAttribute(int8_small_kernel<T, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmMaxCodes));
+    if (e != cudaSuccess) return e;
+    attr_done.mark(dev);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((a.N + kSmTileRows - 1) / kSmTileRows), 1, 1);
+  cfg.blockDim = dim3(kSmThreads, 1, 1);
+  cfg.dynamicSmemBytes = size_t(a.M * a.K);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = prof_on() ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, int8_small_kernel<T, MT>, a, static_cast<const T*>(x), scale);
+}
+template <typename T>
+cudaError_t small_t(const Int8LinearArgs& a, const void* x, const float* scale, cudaStream_t st) {
+  return a.M == 1 ? small_tm<T, 1>(a, x, scale, st) : a.M == 2 ? small_tm<T, 2>(a, x, scale, st)
+       : a.M <= 4 ? small_tm<T, 4>(a, x, scale, st) : small_tm<T, 8>(a, x, scale, st);
+}
+
+bool use_small(const Int8LinearArgs& a) { return a.M <= 8 && a.M * a.K <= kSmMaxCodes; }
+
 }  // namespace
 
 cudaError_t launch_int8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols, int8_t* codes,
@@ -195,8 +354,29 @@ cudaError_t launch_int8_quantize(const void* x, int in_dtype, int64_t rows, int6
   return e;
 }
 
-cudaError_t launch_int8_linear(const Int8LinearArgs& a, int sms, cudaStream_t st, int* launches) {
-  return launch_int8_gemm(a, sms, st, launches);
+cudaError_t launch_int8_linear(const Int8LinearArgs& given, const void* x, const float* x_scale, int8_t* codes,
+                               float* scales, int sms, cudaStream_t st, int* launches) {
+  Int8LinearArgs a = given;
+  if (use_small(a)) {
+    NF4_PROF_BEGIN(st, kKInt8Linear);
+    cudaError_t e = x_scale != nullptr      ? small_t<int8_t>(a, x, x_scale, st)
+                    : a.dtype == NF4_F32    ? small_t<float>(a, x, nullptr, st)
+                    : a.dtype == NF4_F16    ? small_t<__half>(a, x, nullptr, st)
+                                            : small_t<__nv_bfloat16>(a, x, nullptr, st);
+    NF4_PROF_END(st, kKInt8Linear);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess) ++*launches;
+    return e;
+  }
+  Int8Gemm g;
+  a.x = x_scale != nullptr ? static_cast<const int8_t*>(x) : codes;
+  a.x_scale = x_scale != nullptr ? x_scale : scales;
+  if (!g.prepare(a, sms)) return cudaErrorInvalidValue;
+  if (x_scale == nullptr) {
+    const cudaError_t e = launch_int8_quantize(x, a.dtype, a.M, a.K, codes, scales, sms, st, launches);
+    if (e != cudaSuccess) return e;
+  }
+  return g.run(st, launches);
 }
 
 }  // namespace nf4

@@ -154,7 +154,10 @@ struct Int8LinearArgs {
 
 cudaError_t launch_int8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols, int8_t* codes,
                                  float* scales, int sms, cudaStream_t stream, int* launches);
-cudaError_t launch_int8_linear(const Int8LinearArgs& a, int sms, cudaStream_t stream, int* launches);
+// x: [M, K] of a.dtype, quantized into codes and scales on the way, or (x_scale
+// given) int8; a.x and a.x_scale are set here.
+cudaError_t launch_int8_linear(const Int8LinearArgs& a, const void* x, const float* x_scale, int8_t* codes,
+                               float* scales, int sms, cudaStream_t stream, int* launches);
 
 // Bounded-wait self-check (selfcheck.cu): waits that nothing completes give
 // up after limit_ns, record NF4_ERR_TIMEOUT in *status and raise the abort
