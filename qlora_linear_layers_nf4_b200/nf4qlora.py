@@ -412,18 +412,39 @@ def linear_bwd(q: QuantizedWeight, x, A, B, alpha: float, dy, t=None, want_dx: b
 
 
 _stream_ws = {}
+_sizes = {}
 
 
-def _on_stream(stream):
-    """Context in which a call on `stream` allocates: the stream's own device and
-    memory pool, so that nothing the call uses is handed out again before that
-    stream has finished with it (None: the current stream, nothing to do)."""
-    import contextlib
+def _fits(name: str, t, shape, dtype, device):
+    """_expect, without its messages where everything fits (these calls are made per token)."""
+    if t is not None and not (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        _expect(name, t, shape, dtype, device)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace_size(op: int, M: int, N: int, K: int, r: int) -> int:
+    """Cached workspace_bytes of the operations whose size the block does not change."""
+    key = (op, M, N, K, r)
+    n = _sizes.get(key)
+    if n is None:
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        n = _sizes[key] = workspace_bytes(op, M, N, K, r, 64, False)
+    return n
+
+
+def _here(device) -> int:
+    """The current stream's handle; the tensors have to be on the current CUDA device."""
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {device}, which is not the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _scratch(workspace: Workspace | None, device, nbytes: int):
+def _scratch(workspace: Workspace | None, device, stream: int, nbytes: int):
     """Device scratch of a call on the current stream.
 
     A given workspace is used as it is (calls that share one must be ordered).
@@ -431,19 +452,30 @@ def _scratch(workspace: Workspace | None, device, nbytes: int):
     being captured the call takes fresh memory of that graph's pool, so two
     graphs, or a graph and eager calls, never share scratch."""
     import torch
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, which is not the current CUDA device")
     if workspace is not None:
         return workspace.get(nbytes)
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         buf[:256].zero_()   # the status word
         return buf
-    key = (device.index, torch.cuda.current_stream().cuda_stream)
-    ws = _stream_ws.get(key)
+    ws = _stream_ws.get((device.index, stream))
     if ws is None:
-        ws = _stream_ws[key] = Workspace(device)
+        ws = _stream_ws[device.index, stream] = Workspace(device)
     return ws.get(nbytes)
+
+
+def _on_stream(call):
+    """The call's `stream` argument: it then runs with that stream current, so that what it allocates belongs to it."""
+    import functools
+
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return run
 
 
 def _grouped_shapes(q: QuantizedWeight, x, offsets, A):
@@ -454,12 +486,13 @@ def _grouped_shapes(q: QuantizedWeight, x, offsets, A):
     E, r = int(A.shape[0]), int(A.shape[1])
     if E < 1 or q.rows % E:
         raise ValueError(f"the weight's {q.rows} rows do not divide into {E} experts")
-    _expect("offsets", offsets, (E + 1,), torch.int32, q.device)
+    _fits("offsets", offsets, (E + 1,), torch.int32, q.device)
     return int(x.shape[0]), E, q.rows // E, q.cols, r
 
 
+@_on_stream
 def grouped_fwd(q: QuantizedWeight, x, offsets, A, B, alpha: float, bias=None, want_t: bool = True,
-                out=None, t_out=None, workspace: Workspace | None = None, stream=None):
+                out=None, t_out=None, workspace: Workspace | None = None):
     """QLoRA linear of a stack of experts; returns (y, T or None).
 
     q stacks the experts' weights row-wise (rows = num_experts * N); A is
@@ -471,50 +504,54 @@ def grouped_fwd(q: QuantizedWeight, x, offsets, A, B, alpha: float, bias=None, w
     dt = _compute_dtype(x)
     M, E, N, K, r = _grouped_shapes(q, x, offsets, A)
     dev = q.device
-    _expect("x", x, (M, K), x.dtype, dev)
-    _expect("A", A, (E, r, K), x.dtype, dev)
-    _expect("B", B, (E, N, r), x.dtype, dev)
-    _expect("bias", bias, (E, N), x.dtype, dev)
-    _expect("out", out, (M, N), x.dtype, dev)
-    _expect("t_out", t_out, (M, r), x.dtype, dev)
-    with _on_stream(stream):
-        buf = _scratch(workspace, dev, workspace_bytes(OP_GROUPED_FWD, M, N, K, r, q.block_size, q.double_quant))
-        y = out if out is not None else torch.empty((M, N), dtype=x.dtype, device=dev)
-        if want_t and t_out is None:
-            t_out = torch.empty((M, r), dtype=x.dtype, device=dev)
-        cw = q.c_struct()
-        _check(lib().qlora_grouped_fwd(ctypes.byref(cw), E, _ptr(x), M, _ptr(offsets), _ptr(A), _ptr(B), r,
-                                       float(alpha), dt, _ptr(bias), _ptr(y), _ptr(t_out), _ptr(buf),
-                                       buf.numel(), _stream(stream)), "qlora_grouped_fwd")
+    _fits("x", x, (M, K), x.dtype, dev)
+    _fits("A", A, (E, r, K), x.dtype, dev)
+    _fits("B", B, (E, N, r), x.dtype, dev)
+    _fits("bias", bias, (E, N), x.dtype, dev)
+    _fits("out", out, (M, N), x.dtype, dev)
+    _fits("t_out", t_out, (M, r), x.dtype, dev)
+    here = _here(dev)
+    need = _workspace_size(OP_GROUPED_FWD, M, N, K, r)
+    buf = _scratch(workspace, dev, here, need)
+    y = out if out is not None else torch.empty((M, N), dtype=x.dtype, device=dev)
+    if want_t and t_out is None:
+        t_out = torch.empty((M, r), dtype=x.dtype, device=dev)
+    st = lib().qlora_grouped_fwd(q.c_struct(), E, x.data_ptr(), M, offsets.data_ptr(), A.data_ptr(), B.data_ptr(), r,
+                                 alpha, dt, _at(bias), y.data_ptr(), _at(t_out), buf.data_ptr(), need, here)
+    if st:
+        raise NF4Error(st, "qlora_grouped_fwd")
     return y, t_out
 
 
+@_on_stream
 def grouped_bwd(q: QuantizedWeight, x, offsets, A, B, alpha: float, dy, t=None, want_dx: bool = True,
-                dA=None, dB=None, dx=None, workspace: Workspace | None = None, stream=None):
+                dA=None, dB=None, dx=None, workspace: Workspace | None = None):
     """Adapter backward of grouped_fwd; returns (dA fp32 [E, r, K], dB fp32 [E, N, r],
     dx [M, K] in x's dtype or None).  Experts without rows get zero gradients."""
     import torch
     dt = _compute_dtype(x)
     M, E, N, K, r = _grouped_shapes(q, x, offsets, A)
     dev = q.device
-    _expect("x", x, (M, K), x.dtype, dev)
-    _expect("A", A, (E, r, K), x.dtype, dev)
-    _expect("B", B, (E, N, r), x.dtype, dev)
-    _expect("dy", dy, (M, N), x.dtype, dev)
-    _expect("t", t, (M, r), x.dtype, dev)
-    _expect("dA", dA, (E, r, K), torch.float32, dev)
-    _expect("dB", dB, (E, N, r), torch.float32, dev)
-    _expect("dx", dx, (M, K), x.dtype, dev)
-    with _on_stream(stream):
-        buf = _scratch(workspace, dev, workspace_bytes(OP_GROUPED_BWD, M, N, K, r, q.block_size, q.double_quant))
-        dA = dA if dA is not None else torch.empty((E, r, K), dtype=torch.float32, device=dev)
-        dB = dB if dB is not None else torch.empty((E, N, r), dtype=torch.float32, device=dev)
-        if want_dx and dx is None:
-            dx = torch.empty((M, K), dtype=x.dtype, device=dev)
-        cw = q.c_struct()
-        _check(lib().qlora_grouped_bwd(ctypes.byref(cw), E, _ptr(x), M, _ptr(offsets), _ptr(A), _ptr(B), r,
-                                       float(alpha), dt, _ptr(dy), _ptr(t), _ptr(dA), _ptr(dB), _ptr(dx),
-                                       _ptr(buf), buf.numel(), _stream(stream)), "qlora_grouped_bwd")
+    _fits("x", x, (M, K), x.dtype, dev)
+    _fits("A", A, (E, r, K), x.dtype, dev)
+    _fits("B", B, (E, N, r), x.dtype, dev)
+    _fits("dy", dy, (M, N), x.dtype, dev)
+    _fits("t", t, (M, r), x.dtype, dev)
+    _fits("dA", dA, (E, r, K), torch.float32, dev)
+    _fits("dB", dB, (E, N, r), torch.float32, dev)
+    _fits("dx", dx, (M, K), x.dtype, dev)
+    here = _here(dev)
+    need = _workspace_size(OP_GROUPED_BWD, M, N, K, r)
+    buf = _scratch(workspace, dev, here, need)
+    dA = dA if dA is not None else torch.empty((E, r, K), dtype=torch.float32, device=dev)
+    dB = dB if dB is not None else torch.empty((E, N, r), dtype=torch.float32, device=dev)
+    if want_dx and dx is None:
+        dx = torch.empty((M, K), dtype=x.dtype, device=dev)
+    st = lib().qlora_grouped_bwd(q.c_struct(), E, x.data_ptr(), M, offsets.data_ptr(), A.data_ptr(), B.data_ptr(), r,
+                                 alpha, dt, dy.data_ptr(), _at(t), dA.data_ptr(), dB.data_ptr(), _at(dx),
+                                 buf.data_ptr(), need, here)
+    if st:
+        raise NF4Error(st, "qlora_grouped_bwd")
     return dA, dB, dx
 
 
@@ -529,7 +566,8 @@ class Int8Matrix:
         return self.codes * self.scale[:, None]
 
 
-def int8_quantize(x, codes=None, scale=None, stream=None) -> Int8Matrix:
+@_on_stream
+def int8_quantize(x, codes=None, scale=None) -> Int8Matrix:
     """Quantize the rows of a 2-D float32, bfloat16 or float16 CUDA tensor to 8-bit
     integers, one scale per row (per token, or per output channel of a weight)."""
     import torch
@@ -537,21 +575,21 @@ def int8_quantize(x, codes=None, scale=None, stream=None) -> Int8Matrix:
         raise ValueError("x must be 2-D ([rows, cols])")
     dt = _compute_dtype(x)
     rows, cols = int(x.shape[0]), int(x.shape[1])
-    _expect("x", x, (rows, cols), x.dtype, x.device)
-    _expect("codes", codes, (rows, cols), torch.int8, x.device)
-    _expect("scale", scale, (rows,), torch.float32, x.device)
-    with _on_stream(stream):
-        if x.device.type != "cuda" or x.device.index != torch.cuda.current_device():
-            raise ValueError(f"x is on {x.device}, which is not the current CUDA device")
-        codes = codes if codes is not None else torch.empty((rows, cols), dtype=torch.int8, device=x.device)
-        scale = scale if scale is not None else torch.empty(rows, dtype=torch.float32, device=x.device)
-        _check(lib().int8_quantize(_ptr(x), dt, rows, cols, _ptr(codes), _ptr(scale), _stream(stream)),
-               "int8_quantize")
+    _fits("x", x, (rows, cols), x.dtype, x.device)
+    _fits("codes", codes, (rows, cols), torch.int8, x.device)
+    _fits("scale", scale, (rows,), torch.float32, x.device)
+    here = _here(x.device)
+    codes = codes if codes is not None else torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    scale = scale if scale is not None else torch.empty(rows, dtype=torch.float32, device=x.device)
+    st = lib().int8_quantize(x.data_ptr(), dt, rows, cols, codes.data_ptr(), scale.data_ptr(), here)
+    if st:
+        raise NF4Error(st, "int8_quantize")
     return Int8Matrix(codes, scale)
 
 
+@_on_stream
 def int8_linear_fwd(w: Int8Matrix, x, bias=None, out_dtype=None, out=None,
-                    workspace: Workspace | None = None, stream=None):
+                    workspace: Workspace | None = None):
     """y = (codes_x codes_w^T) scale_x scale_w (+ bias), [M, N].
 
     x is a bfloat16, float16 or float32 tensor [M, K], quantized per row in the
@@ -562,8 +600,8 @@ def int8_linear_fwd(w: Int8Matrix, x, bias=None, out_dtype=None, out=None,
         raise ValueError("w.codes must be 2-D ([N, K])")
     N, K = int(w.codes.shape[0]), int(w.codes.shape[1])
     dev = w.codes.device
-    _expect("w.codes", w.codes, (N, K), torch.int8, dev)
-    _expect("w.scale", w.scale, (N,), torch.float32, dev)
+    _fits("w.codes", w.codes, (N, K), torch.int8, dev)
+    _fits("w.scale", w.scale, (N,), torch.float32, dev)
     if isinstance(x, Int8Matrix):
         xv, xs, want = x.codes, x.scale, torch.int8
         y_dtype = out_dtype if out_dtype is not None else torch.bfloat16
@@ -578,13 +616,16 @@ def int8_linear_fwd(w: Int8Matrix, x, bias=None, out_dtype=None, out=None,
     if xv.dim() != 2:
         raise ValueError("x must be 2-D ([M, K])")
     M = int(xv.shape[0])
-    _expect("x", xv, (M, K), want, dev)
-    _expect("x.scale", xs, (M,), torch.float32, dev)
-    _expect("bias", bias, (N,), y_dtype, dev)
-    _expect("out", out, (M, N), y_dtype, dev)
-    with _on_stream(stream):
-        buf = _scratch(workspace, dev, workspace_bytes(OP_INT8_LINEAR, M, N, K, 0, 0, False))
-        y = out if out is not None else torch.empty((M, N), dtype=y_dtype, device=dev)
-        _check(lib().int8_linear_fwd(_ptr(w.codes), _ptr(w.scale), N, K, _ptr(xv), _ptr(xs), M, dt, _ptr(bias),
-                                     _ptr(y), _ptr(buf), buf.numel(), _stream(stream)), "int8_linear_fwd")
+    _fits("x", xv, (M, K), want, dev)
+    _fits("x.scale", xs, (M,), torch.float32, dev)
+    _fits("bias", bias, (N,), y_dtype, dev)
+    _fits("out", out, (M, N), y_dtype, dev)
+    here = _here(dev)
+    need = _workspace_size(OP_INT8_LINEAR, M, N, K, 0)
+    buf = _scratch(workspace, dev, here, need)
+    y = out if out is not None else torch.empty((M, N), dtype=y_dtype, device=dev)
+    st = lib().int8_linear_fwd(w.codes.data_ptr(), w.scale.data_ptr(), N, K, xv.data_ptr(), _at(xs), M, dt, _at(bias),
+                               y.data_ptr(), buf.data_ptr(), need, here)
+    if st:
+        raise NF4Error(st, "int8_linear_fwd")
     return y
