@@ -94,7 +94,7 @@ const char* const kKernelNames[nf4::kNumKernelIds] = {
     "nf4_quantize", "nf4_double_quant", "nf4_dequantize", "adapter_gemm_T",
     "fused_nf4_gemm_fwd", "fused_nf4_gemm_dx", "nf4_gemv", "nf4_merge", "gemm_f32", "nf4_absmax_max",
     "adapter_gemm_U", "adapter_gemm_dB", "adapter_gemm_dA", "grouped_T", "grouped_fwd", "grouped_U",
-    "grouped_dB", "grouped_dA", "grouped_dx", "int8_quantize", "int8_linear"};
+    "grouped_dB", "grouped_dA", "grouped_grad", "grouped_dx", "int8_quantize", "int8_linear"};
 
 cudaEvent_t prof_event() {
   if (!g_prof_free.empty()) {

@@ -197,6 +197,7 @@ enum KernelId {
   kKGroupedU,        // experts: U = s dy B_e
   kKGroupedDB,       // experts: dB_e = dy^T T
   kKGroupedDA,       // experts: dA_e = U^T x
+  kKGroupedGrad,     // experts: dA_e and dB_e in one launch
   kKGroupedDx,       // experts: dx
   kKInt8Quantize,
   kKInt8Linear,

@@ -7,8 +7,8 @@ Bounds per element, with e = half a step of the compute type (bf16 2^-8, f16
   T   e |T| + s (K + 2) f |x||A|
   y   (few rows per expert: 2 e |x||W'|, see Stack.streams) + e |y| + e |T||B| + (K + r + 3) f (|x||W'| + |T||B| + |bias|) + the T sum's own error times |B|
   dB  (c + 2) f |dy||T|                         (c rows; t is an input)
-  dA  (u + (N + 2) f) s |dy||B||x| + (c + 2) f |U||x|,  u what two terms of the compute type lose of U:
-      2^-16 (bf16), 2^-21 (f16), 2^-23 (fp32)
+  dA  (u + (N + 2) f) s |dy||B||x| + (c + 2) f |U||x|,  u what the terms of the compute type lose of U:
+      2^-23 (three terms of bf16), 2^-21 (two of f16), 2^-23 (fp32)
   dx  e |dx| + e |U||A| + (N + r + 3) f (|dy||W'| + |U||A|) + the U sum's own error times |A|
 """
 import numpy as np
@@ -19,7 +19,7 @@ from oracle import nf4_oracle as O
 pytestmark = pytest.mark.gpu
 
 HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
-SPLIT = {"bf16": 2.0 ** -16, "f16": 2.0 ** -21, "f32": 2.0 ** -23}
+SPLIT = {"bf16": 2.0 ** -23, "f16": 2.0 ** -21, "f32": 2.0 ** -23}
 F = 2.0 ** -23
 
 
