@@ -439,26 +439,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
     bool ok = true;
     for (int id = pair; id < tiles && ok; id += pairs) {
       const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
-      // this row's element index at step k: e0 + k * e_step; its scale is the
-      // block's that holds it (a 64-element chunk never straddles two blocks)
+      // this row's 64-element chunk at step k: c0 + k * c_step, counted over the
+      // whole stack; its scale is that of the block that holds it
       const int n0 = t.n0 + 128 * int(rank);
       const int wr0 = MODE == kFwd ? n0 + row : row & 63;
       const int ch0 = MODE == kFwd ? 0 : (n0 >> 6) + (row >> 6);
-      const int64_t e0 = (int64_t(t.e) * p.w_rows + wr0) * p.w_cols + int64_t(ch0) * 64;
-      const int64_t e_step = MODE == kFwd ? 64 : int64_t(64) * p.w_cols;
-      const int64_t e0_safe = int64_t(t.e) * p.w_rows * p.w_cols;   // read where there is no such row
-      // rows past the expert's weight decode to zeros: their scale counts as 0
+      const uint32_t per_row = uint32_t(p.w_cols) >> 6;
+      const uint32_t c0 = (uint32_t(t.e) * uint32_t(p.w_rows) + uint32_t(wr0)) * per_row + uint32_t(ch0);
+      const uint32_t c_step = MODE == kFwd ? 1u : 64u * per_row;
+      // rows past the expert's weight decode to zeros: their scale counts as 0 (and
+      // their loads read the last row that is there, or the expert's first)
       const int k_end = MODE == kFwd ? (wr0 < p.w_rows ? p.main_steps : 0)
-                                     : (ch0 * 64 < p.w_cols ? (p.w_rows - wr0 + 63) >> 6 : 0);
+                                     : (uint32_t(ch0) < per_row ? (p.w_rows - wr0 + 63) >> 6 : 0);
+      const uint32_t c_base = k_end > 0 ? c0 : uint32_t(t.e) * uint32_t(p.w_rows) * per_row;
+      auto chunk_at = [&](int k) { return c_base + uint32_t(max(min(k, k_end - 1), 0)) * c_step; };
       // Scales are loaded two of this thread's steps ahead and converted only
       // where they are used, so that no step waits for a load.
       auto raw_scale = [&](int k) -> uint32_t {
-        const int64_t b = (k < k_end ? e0 + k * e_step : e0_safe) >> p.bs_shift;
+        const uint32_t b = chunk_at(k) >> p.block_chunks_shift;
         return dq ? uint32_t(__ldg(p.absmax_q + b)) : __float_as_uint(__ldg(p.absmax + b));
       };
-      auto load_codes = [&](int k) -> Codes {
-        return load_codes64(p.codes + ((k < k_end ? e0 + k * e_step : e0_safe) >> 1), p.codes32 != 0);
-      };
+      auto load_codes = [&](int k) -> Codes { return load_codes64(p.codes + uint64_t(chunk_at(k)) * 32u, p.codes32 != 0); };
       const int first = (group + kDeqGroups - base % kDeqGroups) % kDeqGroups;
       uint32_t raw0 = raw_scale(first), raw1 = raw_scale(first + kDeqGroups);
       // Forward: a row's codes run along it, so four steps share a line and each
@@ -490,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
         }
         if (main) {
           const float scale = k < k_end ? (dq ? __fmul_rn(float(raw), s_g) : __uint_as_float(raw)) : 0.0f;
-          decode_row(codes, make_table(scale, F16), v);
+          decode_row(codes, make_table(scale, F16), p.mul_shr1, p.mul_shr16, v);
         }
         ok = warp_wait(&sh->empty[s], (ph >> s) & 1u, abort_flag, p.status);
         if (!ok) break;
@@ -601,7 +602,9 @@ bool ExpertGemm::prepare(const GroupedArgs& g, bool backward, const void* ad, in
   p.r = a.r;
   p.main_steps = int(backward ? (a.N + 63) / 64 : a.K / 64);
   p.adapter_steps = (a.r + 63) / 64;
-  p.bs_shift = log2_block(a.w->block_size);
+  p.block_chunks_shift = log2_block(a.w->block_size) - 6;
+  p.mul_shr1 = 1u << 31;
+  p.mul_shr16 = 1u << 16;
   p.dq = a.w->double_quant;
   p.offsets = g.offsets;
   p.codes = a.w->codes;
@@ -612,7 +615,8 @@ bool ExpertGemm::prepare(const GroupedArgs& g, bool backward, const void* ad, in
   p.bias = backward ? nullptr : a.bias;
   p.out = backward ? a.dx : a.y;
   p.status = a.status;
-  return ok && set_grid(L, sms);
+  // chunks are counted in 32 bits: stacks of up to 2.7e11 elements
+  return ok && N * E * (K / 64) <= 0xffffffffull && set_grid(L, sms);
 }
 
 cudaError_t ExpertGemm::run(cudaStream_t st, int* launches) const {

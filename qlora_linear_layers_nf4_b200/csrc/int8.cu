@@ -4,7 +4,9 @@
 // x / scale, ties to even.  The quotient is taken exactly without a division
 // per element: q = rint(x * (1 / scale)) is at most one off, and the remainder
 // x - q scale, which one FMA gives exactly (it has at most 24 bits), says
-// whether a neighbour is nearer.
+// whether a neighbour is nearer.  Rounding to an integer is the addition of 1.5
+// 2^23, whose low byte then is the code: the conversion instructions run at an
+// eighth of that rate and bounded the kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -86,6 +88,28 @@ __device__ __forceinline__ int int8_code(float x, const RowScale& r) {
   return min(max(c, -127), 127);
 }
 
+// Four codes, packed.  The common case is four operations an element; a group in
+// which one remainder reaches half a step (or whose scale is 0, NaN or subnormal)
+// takes int8_code for all four.
+__device__ __forceinline__ uint32_t int8_codes4(const float* x, const RowScale& r) {
+  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
+  const float half = 0.5f * r.s;
+  bool rare = r.zero || r.tiny;
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float m = fmaf(x[i], r.inv, kMagic);
+    b[i] = __float_as_uint(m);
+    const float rem = fmaf(kMagic - m, r.s, x[i]);
+    rare |= !(fabsf(rem) < half);
+  }
+  if (rare) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = uint32_t(int8_code(x[i], r));
+  }
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+
 constexpr int kQThreads = 256;
 constexpr int kQKeep = 4;        // 16-byte vectors of a row that a thread keeps in registers
 
@@ -144,11 +168,7 @@ __global__ void __launch_bounds__(kQThreads) int8_quantize_kernel(const T* __res
       Elem<T>::unpack(v, f);
       uint32_t w[V / 4];
 #pragma unroll
-      for (int g = 0; g < V / 4; ++g) {
-        w[g] = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) w[g] |= (uint32_t(int8_code(f[4 * g + u], r)) & 0xffu) << (8 * u);
-      }
+      for (int g = 0; g < V / 4; ++g) w[g] = int8_codes4(f + 4 * g, r);
       if (V == 4) *reinterpret_cast<uint32_t*>(cr + int64_t(at) * V) = w[0];
       else *reinterpret_cast<uint2*>(cr + int64_t(at) * V) = make_uint2(w[0], w[V / 4 - 1]);
     };
@@ -245,14 +265,9 @@ __global__ void __launch_bounds__(kSmThreads) int8_small_kernel(const Int8Linear
       for (int i = t; i < K / V; i += kSmThreads) {
         float f[V];
         Elem<T>::unpack(__ldg(xv + i), f);
-        uint32_t c[V / 4];
 #pragma unroll
-        for (int g = 0; g < V / 4; ++g) {
-          c[g] = 0;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) c[g] |= (uint32_t(int8_code(f[4 * g + u], r)) & 0xffu) << (8 * u);
-          reinterpret_cast<uint32_t*>(codes)[(m * K + i * V) / 4 + g] = c[g];
-        }
+        for (int g = 0; g < V / 4; ++g)
+          reinterpret_cast<uint32_t*>(codes)[(m * K + i * V) / 4 + g] = int8_codes4(f + 4 * g, r);
       }
       __syncthreads();   // part may be written again
     }
