@@ -14,17 +14,16 @@
 //
 // Inside a CTA groups of eight warps take turns at the units (so that their waits,
 // loads and MMAs overlap), a warp two of a unit's 64-wide K blocks and 32 rows: a
-// code byte becomes two 16-bit levels with one lookup in a 256-entry table
-// replicated per lane (conflict-free; entries 256 bytes apart, so that one byte
-// permute makes the address), the levels are A fragments of mma.sync m16n8k16 with
-// x as B, and the block scale multiplies the block's fp32 sums.  So the base enters
-// as level (rounded to the compute type) times scale, the product not rounded
-// again, where the GEMM rounds level * scale: either is within half a step of the
-// exact product.  A producer warp keeps code and x boxes in flight and a warp per
+// code byte becomes two fp32 levels with one lookup in a 256-entry table replicated
+// per lane (conflict-free; entries 256 bytes apart, so that one byte permute makes
+// the address), each is multiplied by its row's scale, and the pair is rounded to
+// the compute type: the same W' as the GEMM's, as A fragments of mma.sync m16n8k16
+// with x as B.  (Rounded levels in the table and the scale on the block's sums
+// would halve the lookups' traffic, but the levels' rounding made y's error 1.6
+// times as large.)  A producer warp keeps code and x boxes in flight and a warp per
 // group the scales of its units; three more warps finish a tile (sums, bias, split
-// tiles) while the next one streams.  What bounds it is instruction issue (the byte
-// permutes and lookups are 3 of 4 issue cycles a code pair), so everything else
-// stays out of the consumers' loop.
+// tiles) while the next one streams.  The lookups are 1,024 of a unit's 1,280
+// shared-memory wavefronts, its MMAs about 600 cycles.
 //
 // T = s x A_e^T comes from a small kernel launched just before, which this one
 // overlaps (programmatic dependent launch) until it finishes its first tile.
@@ -54,7 +53,7 @@ constexpr int kDcEpiWarps = 3;                       // finish tiles
 constexpr int kDcRows = 128;
 constexpr int kDcBlocks = 4;                         // 64-wide K blocks per unit
 constexpr uint32_t kDcCodeBytes = kDcRows * 128;
-constexpr uint32_t kLutBytes = 256 * 256;            // entry e, lane l at 256 e + 4 l
+constexpr uint32_t kLutBytes = 256 * 256;            // entry e, lane l at 256 e + 8 l
 
 // Groups of consumer warps, each with a scale warp; 16 tokens leave registers for two.
 constexpr int dc_groups(int np) { return np == 8 ? 3 : 2; }
@@ -122,12 +121,14 @@ __device__ __forceinline__ float one_float(uint16_t v) {
   return two_floats<F16>(uint32_t(v)).x;
 }
 
-// Byte offset of lane's copy of the table entry for byte J of `word`.
-template <int J>
-__device__ __forceinline__ uint32_t lut_at(uint32_t word, uint32_t lane4) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(word), "r"(lane4), "n"(0x5504 | (J << 4)));   // {lane4.b0, word.bJ, 0, 0}
-  return d;
+// Two weights: byte J of `word` looked up in the lane's copy of the table, times
+// the scale, rounded to the compute type.
+template <int J, bool F16>
+__device__ __forceinline__ uint32_t two_weights(const uint8_t* lut, uint32_t word, uint32_t lane8, float scale) {
+  uint32_t at;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(at) : "r"(word), "r"(lane8), "n"(0x5504 | (J << 4)));   // {lane8.b0, word.bJ, 0, 0}
+  const float2 l = *reinterpret_cast<const float2*>(lut + at);
+  return two_rounded<F16>(__fmul_rn(l.x, scale), __fmul_rn(l.y, scale));
 }
 
 // A tile of the work list: row group, its expert and first row, 128 W rows.  The
@@ -188,8 +189,7 @@ __global__ void __launch_bounds__(dc_threads(NP), 1)
   if (warp == kProducer) {
     build_groups(&sh->groups, p.offsets, p.E, p.M, NP, blockIdx.x == 0 ? p.status : nullptr);
   } else if (warp < kConsumers) {
-    // Lookup table: byte (even element in the high nibble) -> two levels in the
-    // compute type, one copy per lane.
+    // Lookup table: byte (even element in the high nibble) -> two levels, one copy per lane.
     uint32_t my = 0;
 #pragma unroll
     for (int c = 0; c < 16; ++c) my = (lane & 15) == c ? level_bits(c) : my;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(dc_threads(NP), 1)
     for (int e = warp; e < 256; e += kConsumers) {
       const float hi = __shfl_sync(0xffffffffu, lv, e >> 4);
       const float lo = __shfl_sync(0xffffffffu, lv, e & 15);
-      reinterpret_cast<uint32_t*>(lut)[e * 64 + lane] = two_rounded<F16>(hi, lo);
+      reinterpret_cast<float2*>(lut)[e * 32 + lane] = make_float2(hi, lo);
     }
   }
   __syncthreads();
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(dc_threads(NP), 1)
   const int pair = (warp >> 2) & 1;         // K blocks 2 pair, 2 pair + 1 of the unit
   const int set = warp & 3;                 // rows 32 set ..
   const int g = lane >> 2, q = lane & 3;
-  const uint32_t lane4 = uint32_t(lane) << 2;
+  const uint32_t lane8 = uint32_t(lane) << 3;   // below 256: one byte
   const int kb_per_row = p.K >> 6;
   bool ok = true, waited = false;
   int s = group;
@@ -446,27 +446,19 @@ __global__ void __launch_bounds__(dc_threads(NP), 1)
             const uint2 w0 = *reinterpret_cast<const uint2*>(st + (code_at[0] ^ (j * 32u)) + i * 2048);
             const uint2 w1 = *reinterpret_cast<const uint2*>(st + (code_at[1] ^ (j * 32u)) + i * 2048);
             const float2 scale = *reinterpret_cast<const float2*>(sc + j * kDcRows + i * 16);
-            uint32_t a[4][4];
-            auto look = [&](uint32_t at) { return *reinterpret_cast<const uint32_t*>(lut + at); };
-            a[0][0] = look(lut_at<0>(w0.x, lane4)); a[0][1] = look(lut_at<0>(w1.x, lane4));
-            a[0][2] = look(lut_at<1>(w0.x, lane4)); a[0][3] = look(lut_at<1>(w1.x, lane4));
-            a[1][0] = look(lut_at<2>(w0.x, lane4)); a[1][1] = look(lut_at<2>(w1.x, lane4));
-            a[1][2] = look(lut_at<3>(w0.x, lane4)); a[1][3] = look(lut_at<3>(w1.x, lane4));
-            a[2][0] = look(lut_at<0>(w0.y, lane4)); a[2][1] = look(lut_at<0>(w1.y, lane4));
-            a[2][2] = look(lut_at<1>(w0.y, lane4)); a[2][3] = look(lut_at<1>(w1.y, lane4));
-            a[3][0] = look(lut_at<2>(w0.y, lane4)); a[3][1] = look(lut_at<2>(w1.y, lane4));
-            a[3][2] = look(lut_at<3>(w0.y, lane4)); a[3][3] = look(lut_at<3>(w1.y, lane4));
 #pragma unroll
-            for (int c = 0; c < NT8; ++c) {
-              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma_16816<F16>(d, a[0], xl[c].x, xl[c].y);
-              mma_16816<F16>(d, a[1], xl[c].z, xl[c].w);
-              mma_16816<F16>(d, a[2], xh[c].x, xh[c].y);
-              mma_16816<F16>(d, a[3], xh[c].z, xh[c].w);
-              acc[i][c][0] = fmaf(scale.x, d[0], acc[i][c][0]);
-              acc[i][c][1] = fmaf(scale.x, d[1], acc[i][c][1]);
-              acc[i][c][2] = fmaf(scale.y, d[2], acc[i][c][2]);
-              acc[i][c][3] = fmaf(scale.y, d[3], acc[i][c][3]);
+            for (int h = 0; h < 2; ++h) {          // elements 0..7 and 8..15 of the lane's sixteen
+              const uint32_t c0 = h ? w0.y : w0.x, c1 = h ? w1.y : w1.x;
+              const uint32_t a0[4] = {two_weights<0, F16>(lut, c0, lane8, scale.x), two_weights<0, F16>(lut, c1, lane8, scale.y),
+                                      two_weights<1, F16>(lut, c0, lane8, scale.x), two_weights<1, F16>(lut, c1, lane8, scale.y)};
+              const uint32_t a1[4] = {two_weights<2, F16>(lut, c0, lane8, scale.x), two_weights<2, F16>(lut, c1, lane8, scale.y),
+                                      two_weights<3, F16>(lut, c0, lane8, scale.x), two_weights<3, F16>(lut, c1, lane8, scale.y)};
+#pragma unroll
+              for (int c = 0; c < NT8; ++c) {
+                const uint4& v = h ? xh[c] : xl[c];
+                mma_16816<F16>(acc[i][c], a0, v.x, v.y);
+                mma_16816<F16>(acc[i][c], a1, v.z, v.w);
+              }
             }
           }
         }

@@ -2,7 +2,7 @@
 //   dB_e = dy^T T  [N, r]      dA_e = U^T x  [r, K]      sums over the expert's rows
 //
 // A tile is an expert's 128 outputs (rows of dy^T or x^T, MN-major boxes straight
-// from the row-major batch) by up to 128 adapter columns; the reduction walks the
+// from the row-major batch) by 64 adapter columns; the reduction walks the
 // expert's ragged rows in steps of 64.  Persistent CTAs take the tiles of both
 // gradients round robin in one launch; rings and two accumulators run on across
 // tiles, so that an expert with a handful of rows costs its loads and not a
@@ -14,10 +14,12 @@
 //
 // dA sums products of U, whose rounding to 16 bits would be its largest error by
 // far (2^-9 against 2^-24 for a sum's step).  U comes as three bf16 terms that
-// together hold its 24 bits and are summed in one accumulator, or as two f16 terms,
-// the second scaled by 2^11 (its values would be subnormal otherwise) in an
-// accumulator of its own.  They cost adapter columns in a product that is bound by
-// reading x.
+// together hold its 24 bits, or as two f16 terms, the second scaled by 2^11 (its
+// values would be subnormal otherwise).  They cost adapter columns in a product that
+// is bound by reading x.  The tensor core truncates when it adds to an accumulator,
+// so what counts is how often it adds to a large one: the first terms of even and
+// odd steps have an accumulator each and the small terms a third, summed in fp32 at
+// the end (dA's error on 512 rows an expert: 2.0e-6 with one, 0.5e-6 with three).
 #include <algorithm>
 
 #include <cuda.h>
@@ -39,7 +41,7 @@ using expert::ring_wait;
 using expert::warp_wait;
 
 constexpr int kGrThreads = 256;    // A loads, B loads, MMA, tail rows; four epilogue warps
-constexpr int kGrCols = 128;       // adapter columns per tile at most
+constexpr int kGrCols = 64;        // adapter columns per tile
 constexpr int kGrMaxStages = 6;
 constexpr uint32_t kGrABytes = 128 * 128;
 
@@ -125,8 +127,8 @@ __global__ void __launch_bounds__(kGrThreads, 1)
   const uint32_t tmem = sh->tmem_base;
 
   if (warp < 2) {
-    // ---------------- loads: warp 0 the A boxes, warp 1 the adapter terms.  B in a
-    // stage: per 64 columns, the terms' [64 rows][128 bytes] one after another.
+    // ---------------- loads: warp 0 the A boxes, warp 1 the adapter terms, [64
+    // rows][128 bytes] one after another
     const bool issue = elect_one();
     int s = 0, issued = 0;
     uint32_t ph = 1;
@@ -134,7 +136,6 @@ __global__ void __launch_bounds__(kGrThreads, 1)
     for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x) {
       const GradTile t = grad_tile(&sh->groups, p, id);
       const GradJob& job = p.job[t.job];
-      const int boxes = min(p.np, (p.r - t.col0 + 63) & ~63) / 64;   // 64-column boxes that hold columns
       for (int k = 0; k < t.cnt; k += 64) {
         ok = ring_wait(&sh->empty[s], ph, abort_flag, p.status);
         if (!ok) break;
@@ -149,9 +150,8 @@ __global__ void __launch_bounds__(kGrThreads, 1)
               tma_load_2d(a + 8192, &maps.a[t.job], &sh->full[s], t.row0 + 64, t.tok0 + k);
             }
           } else {
-            mbar_arrive_expect_tx(&sh->full[s], uint32_t(boxes * job.terms) * 8192u);
-            for (int g = 0; g < boxes; ++g)
-              tma_load_3d(a + kGrABytes + g * job.terms * 8192, &maps.b[t.job], &sh->full[s], t.col0 + 64 * g, t.tok0 + k, 0);
+            mbar_arrive_expect_tx(&sh->full[s], uint32_t(job.terms) * 8192u);
+            tma_load_3d(a + kGrABytes, &maps.b[t.job], &sh->full[s], t.col0, t.tok0 + k, 0);
           }
         }
         __syncwarp();
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
       const GradTile t = grad_tile(&sh->groups, p, id);
       if (t.cnt == 0) continue;   // the epilogue writes zeros
       const int terms = p.job[t.job].terms;
-      const int cols = min(p.np, (p.r - t.col0 + 15) & ~15);
+      const int cols = min(kGrCols, (p.r - t.col0 + 15) & ~15);
       const uint32_t idesc = idesc_f32acc(128, cols, true, true, p.f16 != 0);
       const uint32_t d = tmem + uint32_t(n & 1) * 256u;
       ok = ring_wait(&sh->acc_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, p.status);
@@ -194,16 +194,16 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         tc_fence_after();
         const uint32_t a_base = smem_u32(smem + s * stage_bytes);
         const uint64_t adesc = smem_desc_sw128(a_base, 8192, 1024);
-        const uint64_t bdesc = smem_desc_sw128(a_base + kGrABytes, uint32_t(terms) * 8192u, 1024);
+        const uint64_t bdesc = smem_desc_sw128(a_base + kGrABytes, 8192, 1024);
         if (issue) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk * 16 >= left) break;
-            const uint32_t more = (k > 0 || kk > 0) ? 1u : 0u;
-            umma_f16(d, adesc + kk * 128, bdesc + kk * 128, idesc, more);
-            // the scaled second term of f16 in columns of its own, bf16's in the same
-            if (terms > 1) umma_f16(d + (p.f16 ? 128u : 0u), adesc + kk * 128, bdesc + 512 + kk * 128, idesc, p.f16 ? more : 1u);
-            if (terms > 2) umma_f16(d, adesc + kk * 128, bdesc + 1024 + kk * 128, idesc, 1u);
+            // first terms: columns 0 (even steps) and 64 (odd); the others: 128
+            const uint32_t first = (k >> 6) & 1;
+            umma_f16(d + 64u * first, adesc + kk * 128, bdesc + kk * 128, idesc, (k >= 128 || kk > 0) ? 1u : 0u);
+            if (terms > 1) umma_f16(d + 128u, adesc + kk * 128, bdesc + 512 + kk * 128, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+            if (terms > 2) umma_f16(d + 128u, adesc + kk * 128, bdesc + 1024 + kk * 128, idesc, 1u);
           }
           umma_commit(&sh->empty[s]);
           if (k + 64 >= t.cnt) umma_commit(&sh->acc_full[n & 1]);
@@ -236,8 +236,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         if (!ok) break;
         ph ^= 1;
         uint8_t* a = smem + s * stage_bytes;
-        const int boxes = min(p.np, (p.r - t.col0 + 63) & ~63) / 64;
-        const int blocks = 2 + p.job[t.job].terms * boxes;   // [64 rows][128 bytes] each, A then the terms
+        const int blocks = 2 + p.job[t.job].terms;   // [64 rows][128 bytes] each, A then the terms
         const int chunks = (16 - (left & 15)) * 8;
         for (int i = lane; i < blocks * chunks; i += 32)
           *reinterpret_cast<uint4*>(a + (i / chunks) * 8192 + left * 128 + (i % chunks) * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -271,7 +270,13 @@ __global__ void __launch_bounds__(kGrThreads, 1)
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-          if (job.terms > 1 && p.f16) {
+          if (t.cnt > 64) {
+            tmem_ld_32x32b_x32(at + 64u, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] += __uint_as_float(v[i]);
+          }
+          if (job.terms > 1) {
             tmem_ld_32x32b_x32(at + 128u, v);
             tmem_ld_wait();
 #pragma unroll
@@ -324,10 +329,9 @@ bool ExpertGrad::prepare(const GroupedArgs& g, const void* T, const void* U, int
   p.M = int(a.M);
   p.r = a.r;
   p.f16 = a.f16;
-  p.lo_scale = 1.0f / kULoMul;
+  p.lo_scale = a.f16 ? 1.0f / kULoMul : 1.0f;
   p.offsets = g.offsets;
   p.status = a.status;
-  p.np = std::min(kGrCols, (a.r + 63) / 64 * 64);
   p.col_tiles = (a.r + kGrCols - 1) / kGrCols;
   const void* in[2] = {a.x, a.dy};
   const void* terms[2] = {U, T};
@@ -357,7 +361,7 @@ bool ExpertGrad::prepare(const GroupedArgs& g, const void* T, const void* U, int
     const uint32_t box[3] = {64, 64, uint32_t(j.terms)};
     ok = ok && encode_map(&maps.b[i], terms[i], MapElem::k16, 3, dims, strides, box, sw);
   }
-  p.stage_bytes = kGrABytes + uint32_t(p.np) * 128u * uint32_t(u_terms);
+  p.stage_bytes = kGrABytes + 8192u * uint32_t(u_terms);
   p.stages = int(std::min<uint32_t>(kGrMaxStages, 208u * 1024u / p.stage_bytes));
   smem = size_t(p.stages) * p.stage_bytes + sizeof(GradShared) + 1024;
   grid = unsigned(std::min<int64_t>(tiles, sms));

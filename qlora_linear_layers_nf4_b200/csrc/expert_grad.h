@@ -24,7 +24,7 @@ struct GradJob {
 
 struct GradParams {
   GradJob job[2];        // dA, dB
-  int E, M, r, np;       // np: adapter columns of a tile's boxes
+  int E, M, r;
   int col_tiles;
   int f16;
   int stages;

@@ -3,7 +3,9 @@
 // One tile is 128 rows of an expert by r columns; the reduction runs in steps of
 // 64 through a TMA ring and may be split over the CTAs of a cluster, which sum
 // their fp32 partials through distributed shared memory in a fixed order.
-// U is written as the terms that dA sums (see expert_grad.cu).
+// U is written as the terms that dA sums (see expert_grad.cu).  Even and odd steps
+// have an accumulator each: the tensor core truncates when it adds, and half as many
+// additions to smaller sums lose less.
 #include <algorithm>
 
 #include <cuda.h>
@@ -153,8 +155,7 @@ __global__ void __launch_bounds__(kRkThreads, 1)
           const uint64_t adesc = smem_desc_sw128(a_base + kk * 32, 16, 1024);
           const uint64_t bdesc = b_mn ? smem_desc_sw128(b_base + kk * 2048, 8192, 1024)
                                       : smem_desc_sw128(b_base + kk * 32, 16, 1024);
-          const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
-          umma_f16(tmem, adesc, bdesc, idesc, acc);
+          umma_f16(tmem + uint32_t(i & 1) * uint32_t(p.NP), adesc, bdesc, idesc, (i > 1 || kk > 0) ? 1u : 0u);
         }
         // the last step's commit goes to accum (nobody waits on its stage)
         umma_commit(i + 1 < nsteps ? &sh->empty[s] : &sh->accum);
@@ -176,6 +177,13 @@ __global__ void __launch_bounds__(kRkThreads, 1)
       uint32_t v[32];
       tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + c * 32, v);
       tmem_ld_wait();
+      if (nsteps > 1) {
+        uint32_t w[32];
+        tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + p.NP + c * 32, w);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+      }
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -268,7 +276,7 @@ bool ExpertRank::prepare(const GroupedArgs& g, RankKind kind, void* out0, void* 
   while (p.slices * 2 <= cap) p.slices *= 2;
   p.stages = kRkMaxStages;
   p.tmem_cols = 64;
-  while (p.tmem_cols < p.NP) p.tmem_cols *= 2;
+  while (p.tmem_cols < 2 * p.NP) p.tmem_cols *= 2;
   smem = size_t(p.stages) * (kRkABytes + size_t(p.NP) * 128) + sizeof(RankShared) + 1024;
   grid = dim3(unsigned(tiles), unsigned(p.slices), 1);
   return true;

@@ -5,7 +5,7 @@ Bounds per element, with e = half a step of the compute type (bf16 2^-8, f16
 2^-11, fp32 2^-24), f = 2^-23 per fp32 add (the tensor core may truncate) and
 |.| products taken with absolute values:
   T   e |T| + s (K + 2) f |x||A|
-  y   (few rows per expert: 2 e |x||W'|, see Stack.streams) + e |y| + e |T||B| + (K + r + 3) f (|x||W'| + |T||B| + |bias|) + the T sum's own error times |B|
+  y   e |y| + e |T||B| + (K + r + 3) f (|x||W'| + |T||B| + |bias|) + the T sum's own error times |B|
   dB  (c + 2) f |dy||T|                         (c rows; t is an input)
   dA  (u + (N + 2) f) s |dy||B||x| + (c + 2) f |U||x|,  u what the terms of the compute type lose of U:
       2^-23 (three terms of bf16), 2^-21 (two of f16), 2^-23 (fp32)
@@ -73,11 +73,6 @@ class Stack:
     def bwd(self, **kw):
         return _Q().grouped_bwd(self.q, self.x, self.offsets, self.A, self.B, self.alpha, self.dy, **kw)
 
-    def streams(self):
-        """Few rows per expert: the base enters as rounded level times scale, not as the rounded product.  Both are
-        within half a step of the exact product, so 2 e |x||W'| apart at most."""
-        return self.dtype != "f32" and self.m <= 16 * self.e
-
     def check_fwd(self, y, t, experts=None):
         h = HALF[self.dtype]
         y, t = y.double().cpu().numpy(), t.double().cpu().numpy()
@@ -91,15 +86,7 @@ class Stack:
             b = 0.0 if self.biasn is None else self.biasn[e]
             yw = x @ W.T + tw @ B.T + b
             ta = abs(tw) @ abs(B).T
-            if self.streams():
-                base = 2 * h * (1 + h) * (abs(x) @ abs(W).T)
-                off = np.linalg.norm(y[self.rows(e)] - yw)
-                # the roundings of a row's weights are independent and even: their sum is no larger than that of K
-                # errors of half a step each way, at random (1 / sqrt(3) of a step's half, rms, twice), and y's own
-                assert off <= 2 * h * np.linalg.norm(yw) + 2 * h * np.linalg.norm(abs(x) @ abs(W).T) / np.sqrt(self.k), off
-            else:
-                base = 0.0
-            bound = (base + h * abs(yw) + h * ta + (1 + h) ** 2 * (t_sum @ abs(B).T) +
+            bound = (h * abs(yw) + h * ta + (1 + h) ** 2 * (t_sum @ abs(B).T) +
                      (1 + h) * (self.k + self.r + 3) * F * (abs(x) @ abs(W).T + (1 + h) * ta + abs(b)))
             _within("y", y[self.rows(e)], yw, bound)
 
