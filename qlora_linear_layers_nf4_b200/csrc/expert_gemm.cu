@@ -486,8 +486,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
           const uint32_t at = code_offset(uint32_t(row));
           const uint4 c0 = *reinterpret_cast<const uint4*>(slot + at), c1 = *reinterpret_cast<const uint4*>(slot + (at ^ 16u));
           codes = Codes{{c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w}};
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->cempty[s]);
         }
         if (main) {
           const float scale = k < k_end ? (dq ? __fmul_rn(float(raw), s_g) : __uint_as_float(raw)) : 0.0f;
@@ -503,7 +501,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) arrive_leader(leader_bar(&sh->full[s]));   // adapter steps too: the same arrivals every phase
+        if (lane == 0) {
+          arrive_leader(leader_bar(&sh->full[s]));   // adapter steps too: the same arrivals every phase
+          // The code slot is given back only now: the stores above needed its codes
+          // in registers.  Given back right after the loads were issued, the next
+          // box could land before a load waiting behind other warps' stores.
+          if (MODE == kDx && main) mbar_arrive(&sh->cempty[s]);
+        }
         s += kDeqGroups;
         if (s >= kStages) s -= kStages;
       }

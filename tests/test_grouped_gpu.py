@@ -292,6 +292,21 @@ def test_same_bits_every_time(cuda_device, dtype):
         assert all(torch.equal(a, b) for a, b in zip(first, got))
 
 
+@pytest.mark.parametrize("counts,n,k,r", [([2, 1, 2, 2], 1768, 6528, 64), ([40, 90], 6528, 1792, 24), ([3, 0, 5], 4096, 1024, 8)])
+def test_weight_bound_calls_repeated(cuda_device, counts, n, k, r):
+    """Few tokens an expert: the tensor core waits for every weight tile, so a tile that is read before it is whole, or
+    made from codes already overwritten, shows.  Such a race needs its timing; many calls must give the same bits."""
+    import torch
+    g = Stack(cuda_device, counts, n, k, r, dq=False, block=128, seed=6)
+    y, t = g.fwd()
+    g.check_fwd(y, t)
+    dA, dB, dx = g.bwd(t=t)
+    g.check_bwd(dA, dB, dx, t)
+    for _ in range(150):
+        again = g.fwd()[:1] + g.bwd(t=t)
+        assert all(torch.equal(a, b) for a, b in zip(again, (y, dA, dB, dx)))
+
+
 @pytest.mark.parametrize("counts", [[1, 0, 2], [80, 200, 3]])
 def test_one_expert_equals_the_dense_layer(cuda_device, counts):
     """Each expert's rows give what the dense layer gives on that expert's weight, to rounding."""
