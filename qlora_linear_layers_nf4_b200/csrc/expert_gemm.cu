@@ -113,17 +113,6 @@ __device__ __forceinline__ void arrive_leader(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// True in one lane of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 struct Tile {
   int e;        // expert
   int t0, cnt;  // first token row, tokens

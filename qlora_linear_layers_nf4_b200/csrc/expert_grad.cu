@@ -37,6 +37,7 @@ namespace nf4 {
 namespace {
 
 using namespace tc;
+using expert::elect_one;
 using expert::ring_wait;
 using expert::warp_wait;
 
@@ -75,16 +76,6 @@ __device__ __forceinline__ GradTile grad_tile(const GroupTable* g, const GradPar
   t.tok0 = g->start[t.e];
   t.cnt = g->start[t.e + 1] - t.tok0;
   return t;
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(p));
-  return p != 0;
 }
 
 __global__ void __launch_bounds__(kGrThreads, 1)

@@ -27,16 +27,18 @@ namespace {
 
 using namespace tc;
 using expert::pack2;
+using expert::elect_one;
 using expert::ring_wait;
+using expert::warp_wait;
 using expert::unpack2;
 
-constexpr int kRkThreads = 192;    // A producer, MMA, B producer / epilogue, 3 more epilogue warps
-constexpr int kRkMaxStages = 4;
+constexpr int kRkThreads = 256;    // A loads, B loads, MMA, TMEM; four epilogue warps
+constexpr int kRkStages = 4;
 constexpr uint32_t kRkABytes = 128 * 128;
 
 struct RankShared {
-  uint64_t full[kRkMaxStages];
-  uint64_t empty[kRkMaxStages];
+  uint64_t full[kRkStages];
+  uint64_t empty[kRkStages];
   uint64_t accum;
   uint32_t tmem_base;
   uint32_t abort_flag;
@@ -68,7 +70,7 @@ __global__ void __launch_bounds__(kRkThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t b_bytes = uint32_t(p.NP) * 128u;
   const uint32_t stage_bytes = kRkABytes + b_bytes;
-  RankShared* sh = reinterpret_cast<RankShared*>(smem + p.stages * stage_bytes);
+  RankShared* sh = reinterpret_cast<RankShared*>(smem + kRkStages * stage_bytes);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   volatile uint32_t* abort_flag = &sh->abort_flag;
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kRkThreads, 1)
   const int nsteps = min(step0 + per, p.red_steps) - step0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (int s = 0; s < kRkStages; ++s) {
       mbar_init(&sh->full[s], 2);
       mbar_init(&sh->empty[s], 1);
     }
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kRkThreads, 1)
     fence_barrier_init();
     fence_proxy_async_smem();
   }
-  if (warp == 1) {
+  if (warp == 3) {
     tmem_alloc(&sh->tmem_base, uint32_t(p.tmem_cols));
     tmem_relinquish();
   }
@@ -108,67 +110,77 @@ __global__ void __launch_bounds__(kRkThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
 
-  const bool a_issuer = warp == 0 && lane == 0;
-  const bool b_issuer = warp == 2 && lane == 0;
-  if (a_issuer || b_issuer) {
-    int issued = 0;
+  // Loads (warp 0 the A box, warp 1 the B boxes) and MMAs (warp 2) run as whole
+  // warps with one elected lane; warps 4..7 are the epilogue.
+  if (warp < 2) {
+    const bool issue = elect_one();
+    int issued = 0, s = 0;
+    uint32_t ph = 1;
     for (int i = 0; i < nsteps; ++i) {
-      const int s = i % p.stages;
-      if (!ring_wait(&sh->empty[s], ((i / p.stages) & 1) ^ 1, abort_flag, p.status)) break;
-      uint8_t* a = smem + s * stage_bytes;
-      uint8_t* b = a + kRkABytes;
-      const int red0 = (step0 + i) * 64;
-      if (a_issuer) {
-        mbar_arrive_expect_tx(&sh->full[s], kRkABytes);
-        tma_load_2d(a, &tm_a, &sh->full[s], red0, row0);
-      } else {
-        mbar_arrive_expect_tx(&sh->full[s], b_bytes);
-        if (p.kind == kRankT) {
-          tma_load_3d(b, &tm_b, &sh->full[s], red0, 0, e);
+      if (!ring_wait(&sh->empty[s], ph, abort_flag, p.status)) break;
+      if (issue) {
+        uint8_t* a = smem + s * stage_bytes;
+        uint8_t* b = a + kRkABytes;
+        const int red0 = (step0 + i) * 64;
+        if (warp == 0) {
+          mbar_arrive_expect_tx(&sh->full[s], kRkABytes);
+          tma_load_2d(a, &tm_a, &sh->full[s], red0, row0);
         } else {
-          for (int g = 0; g < p.NP / 64; ++g) tma_load_3d(b + g * 8192, &tm_b, &sh->full[s], 64 * g, red0, e);
+          mbar_arrive_expect_tx(&sh->full[s], b_bytes);
+          if (p.kind == kRankT) {
+            tma_load_3d(b, &tm_b, &sh->full[s], red0, 0, e);
+          } else {
+            for (int g = 0; g < p.NP / 64; ++g) tma_load_3d(b + g * 8192, &tm_b, &sh->full[s], 64 * g, red0, e);
+          }
         }
       }
+      __syncwarp();
       ++issued;
-    }
-    if (*abort_flag) {   // unwind: wait (bounded) for this issuer's copies in flight
-      for (int i = issued - 1; i >= 0 && i >= issued - p.stages; --i) {
-        uint32_t none = 0;
-        ring_wait(&sh->full[i % p.stages], (i / p.stages) & 1, &none, nullptr);
+      if (++s == kRkStages) {
+        s = 0;
+        ph ^= 1;
       }
     }
-  }
-  if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f32acc(128, p.NP, false, b_mn, p.f16 != 0);
-      bool ok = true;
-      int issued = 0;
-      for (int i = 0; i < nsteps; ++i) {
-        const int s = i % p.stages;
-        ok = ring_wait(&sh->full[s], (i / p.stages) & 1, abort_flag, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t a_base = smem_u32(smem + s * stage_bytes);
-        const uint32_t b_base = a_base + kRkABytes;
+    if (*abort_flag) {   // unwind: wait (bounded) for the copies in flight
+      for (int i = max(0, issued - kRkStages); i < issued; ++i) {
+        uint32_t none = 0;
+        ring_wait(&sh->full[i % kRkStages], (i / kRkStages) & 1, &none, nullptr);
+      }
+    }
+  } else if (warp == 2) {
+    const bool issue = elect_one();
+    const uint32_t idesc = idesc_f32acc(128, p.NP, false, b_mn, p.f16 != 0);
+    const uint32_t b_sub = b_mn ? 2048u >> 4 : 32u >> 4;
+    bool ok = true;
+    int s = 0, issued = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < nsteps; ++i) {
+      ok = ring_wait(&sh->full[s], ph, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t a_base = smem_u32(smem + s * stage_bytes);
+      const uint64_t adesc = smem_desc_sw128(a_base, 16, 1024);
+      const uint64_t bdesc = smem_desc_sw128(a_base + kRkABytes, b_mn ? 8192 : 16, 1024);
+      if (issue) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t adesc = smem_desc_sw128(a_base + kk * 32, 16, 1024);
-          const uint64_t bdesc = b_mn ? smem_desc_sw128(b_base + kk * 2048, 8192, 1024)
-                                      : smem_desc_sw128(b_base + kk * 32, 16, 1024);
-          umma_f16(tmem + uint32_t(i & 1) * uint32_t(p.NP), adesc, bdesc, idesc, (i > 1 || kk > 0) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16(tmem + uint32_t(i & 1) * uint32_t(p.NP), adesc + kk * 2, bdesc + kk * b_sub, idesc, (i > 1 || kk > 0) ? 1u : 0u);
         // the last step's commit goes to accum (nobody waits on its stage)
         umma_commit(i + 1 < nsteps ? &sh->empty[s] : &sh->accum);
-        ++issued;
       }
-      if (!ok) drain_issued(sh->empty, issued, p.stages);
-      else if (nsteps == 0) mbar_arrive(&sh->accum);
+      __syncwarp();
+      ++issued;
+      if (++s == kRkStages) {
+        s = 0;
+        ph ^= 1;
+      }
     }
-  } else if (warp >= 2) {
-    // epilogue warps 2..5 -> TMEM lane quadrants 2, 3, 0, 1
-    const bool ok = __all_sync(0xffffffffu, ring_wait(&sh->accum, 0, abort_flag, p.status));
+    if (issue && !ok) drain_issued(sh->empty, issued, kRkStages);
+    else if (issue && nsteps == 0) mbar_arrive(&sh->accum);
+  } else if (warp >= 4) {
+    const bool ok = warp_wait(&sh->accum, 0, abort_flag, p.status);
     tc_fence_after();
-    const int quad = warp & 3;
+    const int quad = warp - 4;
     const int prow = quad * 32 + lane;
     const int row = row0 + prow;
     float* dst = reinterpret_cast<float*>(smem) + prow * p.NP;   // parked partial, chunks swizzled by row
@@ -227,7 +239,7 @@ __global__ void __launch_bounds__(kRkThreads, 1)
     }
     cluster_sync();
   }
-  if (warp == 1) {
+  if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tmem, uint32_t(p.tmem_cols));
   }
@@ -274,10 +286,9 @@ bool ExpertRank::prepare(const GroupedArgs& g, RankKind kind, void* out0, void* 
   const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(296 / tiles, 8), p.red_steps / 4));
   p.slices = 1;
   while (p.slices * 2 <= cap) p.slices *= 2;
-  p.stages = kRkMaxStages;
   p.tmem_cols = 64;
   while (p.tmem_cols < 2 * p.NP) p.tmem_cols *= 2;
-  smem = size_t(p.stages) * (kRkABytes + size_t(p.NP) * 128) + sizeof(RankShared) + 1024;
+  smem = size_t(kRkStages) * (kRkABytes + size_t(p.NP) * 128) + sizeof(RankShared) + 1024;
   grid = dim3(unsigned(tiles), unsigned(p.slices), 1);
   return true;
 }

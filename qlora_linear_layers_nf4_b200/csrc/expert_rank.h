@@ -13,7 +13,7 @@ struct RankParams {
   RankKind kind;
   int red_steps;     // 64-deep steps of the reduction
   int NP, r;         // columns, rounded up to 64 and kept
-  int slices, stages, tmem_cols;
+  int slices, tmem_cols;
   int E, M;
   int f16;
   float scale;       // s

@@ -1,10 +1,21 @@
-// mbarrier waits of the expert kernels (bounded, as tc::mbar_wait).
+// mbarrier waits (bounded, as tc::mbar_wait) and the elected lane of the expert kernels.
 #pragma once
 
 #include "tc_common.cuh"
 
 namespace nf4 {
 namespace expert {
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 
 // A try_wait that may suspend the thread for up to `hint_ns` before it answers:
 // waiting warps then take few issue slots from the working ones.

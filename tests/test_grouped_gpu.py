@@ -405,6 +405,50 @@ def test_streams_and_graphs(cuda_device, counts):
             assert all(torch.equal(a, b) for a, b in zip(out, w))
 
 
+def test_codes_on_a_16_byte_boundary(cuda_device):
+    """Codes that start on a 16-byte boundary and no larger one (a slice of a bigger buffer)."""
+    import torch
+    for counts in ([3, 0, 2], [90, 0, 200]):
+        g = Stack(cuda_device, counts, 264, 320, 16, dq=False, seed=13)
+        y, t = g.fwd()
+        want = (y, t) + g.bwd(t=t)
+        buf = torch.empty(g.q.codes.numel() + 16, dtype=torch.uint8, device=cuda_device)
+        assert buf.data_ptr() % 32 == 0
+        buf[16:] = g.q.codes
+        g.q.codes = buf[16:]
+        y, t = g.fwd()
+        assert all(torch.equal(a, b) for a, b in zip(want, (y, t) + g.bwd(t=t)))
+
+
+def test_two_threads(cuda_device):
+    """Two host threads, each with a stream, on layers of their own."""
+    import threading
+    import torch
+    stacks = [Stack(cuda_device, c, 264, 320, 16, seed=17) for c in ([2, 0, 1], [70, 5, 140])]
+    want = []
+    for g in stacks:
+        y, t = g.fwd()
+        want.append((y, t) + g.bwd(t=t))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(g, w):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(40):
+                y, t = g.fwd()
+                got = (y, t) + g.bwd(t=t)
+                s.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, w)):
+                    wrong.append(1)
+    threads = [threading.Thread(target=work, args=a) for a in zip(stacks, want)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong
+
+
 def test_large_offsets_in_the_stack(cuda_device):
     """A stack of more than 2^32 weight elements: the last expert's codes lie past 32-bit element indexes."""
     import torch
