@@ -48,23 +48,26 @@ constexpr int kDx = 1;
 constexpr int kI8 = 2;
 
 constexpr int kTileW = 256;                 // outputs per tile, 128 in each CTA
-constexpr int kTileT = 256;                 // tokens per tile at most, half in each CTA
-constexpr int kStages = 6;
+constexpr int kPartT = 256;                 // tokens of one MMA at most, half in each CTA
 constexpr uint32_t kWBytes = 128 * 128;     // weight tile of a CTA: 128 x 128 bytes
-constexpr uint32_t kTBytes = 128 * 128;     // its tokens
-constexpr uint32_t kStageBytes = kWBytes + kTBytes;
-constexpr uint32_t kCodeBytes = 128 * 32;   // kDx: NF4 codes of one step, a slot per stage
+constexpr uint32_t kTBytes = 128 * 128;     // its tokens of one part
+constexpr uint32_t kCodeBytes = 128 * 32;   // kDx: NF4 codes of one step
+constexpr int kCodeSlots = 6;
 constexpr int kEpiWarp = 4;                 // warps 4..7
 constexpr int kDeqWarp = 8;
-constexpr int kDeqGroups = 3;               // of four warps; kStages is a multiple
+constexpr int kDeqGroups = 3;               // of four warps; kCodeSlots is a multiple
 constexpr int kThreads = 32 * (kDeqWarp + 4 * kDeqGroups);
 constexpr int kThreadsI8 = 32 * kDeqWarp;
 
+// Ring stages: [weight tile | tokens of each part].
+constexpr int stages_of(int parts) { return parts == 2 ? 4 : 6; }
+constexpr uint32_t stage_bytes_of(int parts) { return kWBytes + uint32_t(parts) * kTBytes; }
+
 struct GemmShared {
-  uint64_t full[kStages];       // leader: both CTAs' bytes landed and weight tiles written
-  uint64_t empty[kStages];      // the MMAs that read a stage finished
-  uint64_t cfull[kStages];      // kDx: a step's codes landed
-  uint64_t cempty[kStages];     // kDx: and were read
+  uint64_t full[stages_of(1)];  // leader: both CTAs' bytes landed and weight tiles written
+  uint64_t empty[stages_of(1)]; // the MMAs that read a stage finished
+  uint64_t cfull[kCodeSlots];   // kDx: a step's codes landed
+  uint64_t cempty[kCodeSlots];  // kDx: and were read
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t drain;               // after an abort
@@ -73,10 +76,11 @@ struct GemmShared {
   GroupTable groups;
 };
 
-constexpr size_t gemm_smem(int mode) {
-  return size_t(kStages) * (kStageBytes + (mode == kDx ? kCodeBytes : 0)) + sizeof(GemmShared) + 1024;
+constexpr size_t gemm_smem(int mode, int parts) {
+  return size_t(stages_of(parts)) * stage_bytes_of(parts) + (mode == kDx ? kCodeSlots * kCodeBytes : 0) +
+         sizeof(GemmShared) + 1024;
 }
-static_assert(gemm_smem(kDx) <= 232448, "shared memory of one CTA");
+static_assert(gemm_smem(kDx, 1) <= 232448 && gemm_smem(kDx, 2) <= 232448, "shared memory of one CTA");
 
 // int8 x int8 -> int32 MMA and its instruction descriptor (kind::i8: D s32,
 // A and B signed 8-bit, both K-major).
@@ -116,13 +120,14 @@ __device__ __forceinline__ void arrive_leader(uint32_t cluster_addr) {
 struct Tile {
   int e;        // expert
   int t0, cnt;  // first token row, tokens
-  int nt;       // tokens rounded up to 16
+  int nt[2];    // MMA columns of the parts (multiples of 16; 0: no second part)
   int n0;       // first output
 };
 
 // Tile `id` of the list ordered by expert, then output tile, then token tile
 // (the pairs that run together share an expert's weight tiles and tokens).
-// The tokens of an expert are cut into ceil(c / 256) tiles of one size.
+// The tokens of an expert are cut into ceil(c / (256 PARTS)) tiles of one size.
+template <int PARTS>
 __device__ __forceinline__ Tile tile_at(const GroupTable* g, int E, int col_tiles, int id) {
   Tile t;
   t.e = expert_of_tile(g, E, id / col_tiles);
@@ -133,7 +138,9 @@ __device__ __forceinline__ Tile tile_at(const GroupTable* g, int E, int col_tile
   const int size = ((end - first + parts - 1) / parts + 15) & ~15;
   t.t0 = first + rt * size;
   t.cnt = min(size, end - t.t0);
-  t.nt = (t.cnt + 15) & ~15;
+  const int nt = (t.cnt + 15) & ~15;
+  t.nt[0] = PARTS == 2 && nt > kPartT ? ((nt >> 1) + 15) & ~15 : nt;
+  t.nt[1] = nt - t.nt[0];
   t.n0 = ct * kTileW;
   return t;
 }
@@ -148,13 +155,15 @@ __device__ __forceinline__ uint32_t code_offset(uint32_t row) {
   return R * 64u + ((c ^ ((R >> 1) & 3u)) << 4);
 }
 
-template <int MODE, bool F16>
+template <int MODE, bool F16, int PARTS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThreadsI8 : kThreads, 1)
     expert_gemm_kernel(const __grid_constant__ ExpertMaps maps, const ExpertParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kStages = stages_of(PARTS);
+  constexpr uint32_t kStageBytes = stage_bytes_of(PARTS);
   uint8_t* code_base = smem + kStages * kStageBytes;
-  GemmShared* sh = reinterpret_cast<GemmShared*>(code_base + (MODE == kDx ? kStages * kCodeBytes : 0));
+  GemmShared* sh = reinterpret_cast<GemmShared*>(code_base + (MODE == kDx ? kCodeSlots * kCodeBytes : 0));
   auto stage_w = [&](int s) { return smem + s * kStageBytes; };
   auto stage_t = [&](int s) { return smem + s * kStageBytes + kWBytes; };
 
@@ -169,6 +178,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
       // warps of both CTAs
       mbar_init(&sh->full[s], MODE == kI8 ? 1 : 1 + 8);
       mbar_init(&sh->empty[s], 1);
+    }
+    for (int s = 0; s < kCodeSlots; ++s) {
       mbar_init(&sh->cfull[s], 1);
       mbar_init(&sh->cempty[s], 4);
     }
@@ -186,11 +197,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
   }
   if (warp == 1) {
     if (p.offsets != nullptr) {
-      build_groups(&sh->groups, p.offsets, p.E, p.M, kTileT, blockIdx.x == 0 ? p.status : nullptr);
+      build_groups(&sh->groups, p.offsets, p.E, p.M, PARTS * kPartT, blockIdx.x == 0 ? p.status : nullptr);
     } else if (lane == 0) {
       sh->groups.start[0] = sh->groups.tiles[0] = 0;
       sh->groups.start[1] = p.M;
-      sh->groups.tiles[1] = (p.M + kTileT - 1) / kTileT;
+      sh->groups.tiles[1] = (p.M + kPartT - 1) / kPartT;
     }
   }
   if (warp == 2) {
@@ -218,11 +229,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
     int s = 0, issued = 0;
     uint32_t ph = 1;
     for (int id = pair; id < tiles && ok; id += pairs) {
-      const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
-      const int half = t.nt >> 1;
+      const Tile t = tile_at<PARTS>(&sh->groups, p.E, p.col_tiles, id);
+      const int half = t.nt[0] >> 1;
       const bool large = half > 32;
-      const uint32_t bytes = large ? 128u * 128u : 32u * 128u;   // of one CTA
+      const bool two = PARTS == 2 && t.nt[1] > 0;
+      const uint32_t bytes = two ? 2 * kTBytes : large ? kTBytes : 32u * 128u;   // of one CTA
       const int y = t.t0 + int(rank) * half;
+      const int y2 = t.t0 + t.nt[0] + int(rank) * (t.nt[1] >> 1);
       const CUtensorMap* tok = large ? &maps.tok_l : &maps.tok_s;
       const CUtensorMap* ad = large ? &maps.ad_l : &maps.ad_s;
       for (int k = 0; k < steps; ++k) {
@@ -236,9 +249,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
           if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], 2 * (bytes + (MODE == kI8 || !main ? kWBytes : 0u)));
           if (main) {
             tma_load_2d_pair(stage_t(s), tok, bar, k * (MODE == kI8 ? 128 : 64), y);
+            if (two) tma_load_2d_pair(stage_t(s) + kTBytes, tok, bar, k * 64, y2);
           } else {
             const int r0 = (k - p.main_steps) * 64, n0 = t.n0 + 128 * int(rank);
             tma_load_2d_pair(stage_t(s), ad, bar, r0, y);
+            if (two) tma_load_2d_pair(stage_t(s) + kTBytes, ad, bar, r0, y2);
             if (MODE == kFwd) {
               tma_load_3d_pair(stage_w(s), &maps.wad, bar, r0, n0, t.e);
             } else {
@@ -262,15 +277,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
       }
   } else if (warp == 1) {
     // ---------------- weight side: the int8 tile of every step (kI8), or the
-    // codes of every main step into the stage's own code slot (kDx)
+    // codes of every main step (kDx)
     if (MODE != kFwd) {
       const bool issue = elect_one();
       if (MODE == kI8) grid_dep_wait();
+      constexpr int kSlots = MODE == kI8 ? kStages : kCodeSlots;
       int s = 0;
-      uint32_t ph = (1u << kStages) - 1;   // bit s: parity of the wait for slot s, toggled at each use
+      uint32_t ph = (1u << kSlots) - 1;   // bit s: parity of the wait for slot s, toggled at each use
       bool ok = true;
       for (int id = pair; id < tiles && ok; id += pairs) {
-        const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
+        const Tile t = tile_at<PARTS>(&sh->groups, p.E, p.col_tiles, id);
         const int n0 = t.n0 + 128 * int(rank);
         for (int k = 0; k < steps; ++k) {
           if (k < p.main_steps) {
@@ -287,11 +303,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
             }
             __syncwarp();
           }
-          if (++s == kStages) s = 0;
+          if (++s == kSlots) s = 0;
         }
       }
       if (MODE == kDx && *abort_flag)   // unwind: wait (bounded) for the codes in flight
-        for (int j = 0; j < kStages; ++j) {
+        for (int j = 0; j < kCodeSlots; ++j) {
           uint32_t none = 0;
           ring_wait(&sh->cfull[j], (ph >> j) & 1u, &none, nullptr);
         }
@@ -309,32 +325,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
       int s = 0, n = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int id = pair; id < tiles && ok; id += pairs, ++n) {
-        const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
-        const uint32_t idesc = MODE == kI8 ? idesc_i8(256, t.nt) : idesc_f32acc(256, t.nt, MODE == kDx, false, F16);
-        const uint32_t d = tmem + uint32_t(n & 1) * 256u;
-        ok = mbar_wait_cluster(&sh->acc_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, p.status);
+      for (int id = pair; id < tiles && ok; id += pairs) {
+        const Tile t = tile_at<PARTS>(&sh->groups, p.E, p.col_tiles, id);
+        const int parts = PARTS == 2 && t.nt[1] > 0 ? 2 : 1;
         for (int k = 0; k < steps && ok; ++k) {
           ok = mbar_wait_cluster(&sh->full[s], ph, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
           const uint64_t wd = w_desc + uint32_t(s) * (kStageBytes >> 4);
-          const uint64_t td = t_desc + uint32_t(s) * (kStageBytes >> 4);
-          if (issue) {
-            if (MODE == kI8) {
+          const int left = MODE == kI8 || k < p.main_steps ? 64 : p.r - (k - p.main_steps) * 64;
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_i8_pair(d, wd + kk * kWSub, td + kk * kTSub, idesc, (k > 0 || kk > 0) ? 1u : 0u);
-            } else {
-              const int left = k < p.main_steps ? 64 : p.r - (k - p.main_steps) * 64;
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                if (kk * 16 < left) umma_f16_pair(d, wd + kk * kWSub, td + kk * kTSub, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+          for (int h = 0; h < PARTS; ++h) {
+            if (h >= parts) break;
+            const int b = (n + h) & 1;
+            if (k == 0) {
+              ok = mbar_wait_cluster(&sh->acc_empty[b], (((n + h) >> 1) & 1) ^ 1, abort_flag, p.status);
+              if (!ok) break;
+              tc_fence_after();
             }
-            // The last step's commit goes to the accumulator's barrier; the
-            // epilogue then releases that step's stage.  MMAs finish in order,
-            // so the commit covers the whole accumulation.
-            umma_commit_pair_mc(k + 1 < steps ? &sh->empty[s] : &sh->acc_full[n & 1], 0x3);
+            const uint32_t d = tmem + uint32_t(b) * 256u;
+            const uint32_t idesc = MODE == kI8 ? idesc_i8(256, t.nt[h]) : idesc_f32acc(256, t.nt[h], MODE == kDx, false, F16);
+            const uint64_t td = t_desc + uint32_t(s) * (kStageBytes >> 4) + uint32_t(h) * (kTBytes >> 4);
+            if (issue) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t acc = (k > 0 || kk > 0) ? 1u : 0u;
+                if (MODE == kI8) umma_i8_pair(d, wd + kk * kWSub, td + kk * kTSub, idesc, acc);
+                else if (kk * 16 < left) umma_f16_pair(d, wd + kk * kWSub, td + kk * kTSub, idesc, acc);
+              }
+              // The last step's commits go to the accumulators' barriers; the
+              // epilogue then releases that step's stage.  MMAs finish in order,
+              // so a commit covers the whole accumulation.
+              if (k + 1 == steps) umma_commit_pair_mc(&sh->acc_full[b], 0x3);
+              else if (h + 1 == parts) umma_commit_pair_mc(&sh->empty[s], 0x3);
+            }
           }
           __syncwarp();
           if (++s == kStages) {
@@ -342,6 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
             ph ^= 1;
           }
         }
+        n += parts;
       }
       if (!ok && issue) {   // unwind: wait (bounded) for the MMAs in flight
         umma_commit_pair_mc(&sh->drain, 0x1);
@@ -354,8 +379,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
     if (MODE == kI8) grid_dep_wait();
     const int quad = warp - kEpiWarp;
     int n = 0, last = 0;   // last: stage of the tile's last step
-    for (int id = pair; id < tiles; id += pairs, ++n) {
-      const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
+    bool ok = true;
+    for (int id = pair; id < tiles && ok; id += pairs) {
+      const Tile t = tile_at<PARTS>(&sh->groups, p.E, p.col_tiles, id);
       const int col = t.n0 + 128 * int(rank) + quad * 32 + lane;
       const bool col_ok = col < p.out_cols;
       float bias = 0.0f, sw = 0.0f;
@@ -368,50 +394,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
           else bias = __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[at]);
         }
       }
-      const bool ok = warp_wait<300>(&sh->acc_full[n & 1], (n >> 1) & 1, abort_flag, p.status);
-      if (!ok) break;
       last = (last + steps) % kStages;
-      if (quad == 0 && lane == 0) mbar_arrive(&sh->empty[(last + kStages - 1) % kStages]);
-      tc_fence_after();
+      const int parts = PARTS == 2 && t.nt[1] > 0 ? 2 : 1;
 #pragma unroll 1
-      for (int c = 0; c * 32 < t.cnt; ++c) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + uint32_t(n & 1) * 256u + c * 32, v);
-        float sx = 0.0f;
-        if (MODE == kI8 && c * 32 + lane < t.cnt) sx = __ldg(p.x_scale + t.t0 + c * 32 + lane);
-        tmem_ld_wait();
-        float f[32];
+      for (int h = 0; h < parts; ++h, ++n) {
+        const int t0 = h == 0 ? t.t0 : t.t0 + t.nt[0];
+        const int cnt = h + 1 == parts ? t.t0 + t.cnt - t0 : t.nt[0];
+        ok = warp_wait<300>(&sh->acc_full[n & 1], (n >> 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        if (h + 1 == parts && quad == 0 && lane == 0) mbar_arrive(&sh->empty[(last + kStages - 1) % kStages]);
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c * 32 < cnt; ++c) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + uint32_t(n & 1) * 256u + c * 32, v);
+          float sx = 0.0f;
+          if (MODE == kI8 && c * 32 + lane < cnt) sx = __ldg(p.x_scale + t0 + c * 32 + lane);
+          tmem_ld_wait();
+          float f[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (MODE == kI8)
-            f[i] = __fmul_rn(__fmul_rn(float(int(v[i])), __shfl_sync(0xffffffffu, sx, i)), sw);
-          else
-            f[i] = __uint_as_float(v[i]);
-          if (p.bias != nullptr) f[i] = __fadd_rn(f[i], bias);
-        }
-        const int left = t.cnt - c * 32;
-        const int64_t row0 = int64_t(t.t0) + c * 32;
-        if (MODE == kI8 && p.out_dtype == NF4_F32) {
-          float* o = static_cast<float*>(p.out) + row0 * p.out_cols + col;
+          for (int i = 0; i < 32; ++i) {
+            if (MODE == kI8)
+              f[i] = __fmul_rn(__fmul_rn(float(int(v[i])), __shfl_sync(0xffffffffu, sx, i)), sw);
+            else
+              f[i] = __uint_as_float(v[i]);
+            if (p.bias != nullptr) f[i] = __fadd_rn(f[i], bias);
+          }
+          const int left = cnt - c * 32;
+          const int64_t row0 = int64_t(t0) + c * 32;
+          if (MODE == kI8 && p.out_dtype == NF4_F32) {
+            float* o = static_cast<float*>(p.out) + row0 * p.out_cols + col;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (col_ok && i < left) o[int64_t(i) * p.out_cols] = f[i];
-        } else {
-          // two lanes trade so that each stores two neighbouring outputs of one token
-          const bool odd = lane & 1;
-          const bool f16 = MODE == kI8 ? p.out_dtype == NF4_F16 : F16;
-          uint16_t* o = static_cast<uint16_t*>(p.out) + (row0 + odd) * p.out_cols + (col & ~1);
+            for (int i = 0; i < 32; ++i)
+              if (col_ok && i < left) o[int64_t(i) * p.out_cols] = f[i];
+          } else {
+            // two lanes trade so that each stores two neighbouring outputs of one token
+            const bool odd = lane & 1;
+            const bool f16 = MODE == kI8 ? p.out_dtype == NF4_F16 : F16;
+            uint16_t* o = static_cast<uint16_t*>(p.out) + (row0 + odd) * p.out_cols + (col & ~1);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? f[i] : f[i + 1], 1);
-            const uint32_t two = pack2(f16, odd ? got : f[i], odd ? f[i + 1] : got);
-            if (col_ok && i + int(odd) < left) *reinterpret_cast<uint32_t*>(o + int64_t(i) * p.out_cols) = two;
+            for (int i = 0; i < 32; i += 2) {
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? f[i] : f[i + 1], 1);
+              const uint32_t two = pack2(f16, odd ? got : f[i], odd ? f[i + 1] : got);
+              if (col_ok && i + int(odd) < left) *reinterpret_cast<uint32_t*>(o + int64_t(i) * p.out_cols) = two;
+            }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(leader_bar(&sh->acc_empty[n & 1]));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_leader(leader_bar(&sh->acc_empty[n & 1]));
     }
   } else if (warp >= kDeqWarp) {
     // ---------------- dequant warps: one thread per weight-tile row and step, so
@@ -423,11 +455,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
     const bool dq = p.dq != 0;
     const float s_g = dq ? __ldg(p.absmax_scale) : 0.0f;
     int base = 0;         // steps of the tiles before
-    uint32_t ph = (1u << kStages) - 1, cph = 0;   // bit s: parity of the next wait for stage s, and its codes
-    int s = group;        // stage of this group's next step
+    int s = group;               // stage of this group's next step
+    uint32_t ph = 1;             // parity of the wait for that stage
+    int slot = group;            // and its code slot
+    uint32_t cph = 0;
     bool ok = true;
     for (int id = pair; id < tiles && ok; id += pairs) {
-      const Tile t = tile_at(&sh->groups, p.E, p.col_tiles, id);
+      const Tile t = tile_at<PARTS>(&sh->groups, p.E, p.col_tiles, id);
       // this row's 64-element chunk at step k: c0 + k * c_step, counted over the
       // whole stack; its scale is that of the block that holds it
       const int n0 = t.n0 + 128 * int(rank);
@@ -468,21 +502,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
           codes = next;
           next = load_codes(k + kDeqGroups);
         } else if (main) {
-          ok = warp_wait(&sh->cfull[s], (cph >> s) & 1u, abort_flag, p.status);
+          ok = warp_wait(&sh->cfull[slot], (cph >> slot) & 1u, abort_flag, p.status);
           if (!ok) break;
-          cph ^= 1u << s;
-          const uint8_t* slot = code_base + s * kCodeBytes;
-          const uint32_t at = code_offset(uint32_t(row));
-          const uint4 c0 = *reinterpret_cast<const uint4*>(slot + at), c1 = *reinterpret_cast<const uint4*>(slot + (at ^ 16u));
+          cph ^= 1u << slot;
+          const uint8_t* src = code_base + slot * kCodeBytes;
+          const uint32_t off = code_offset(uint32_t(row));
+          const uint4 c0 = *reinterpret_cast<const uint4*>(src + off), c1 = *reinterpret_cast<const uint4*>(src + (off ^ 16u));
           codes = Codes{{c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w}};
         }
         if (main) {
           const float scale = k < k_end ? (dq ? __fmul_rn(float(raw), s_g) : __uint_as_float(raw)) : 0.0f;
           decode_row(codes, make_table(scale, F16), p.mul_shr1, p.mul_shr16, v);
         }
-        ok = warp_wait(&sh->empty[s], (ph >> s) & 1u, abort_flag, p.status);
+        ok = warp_wait(&sh->empty[s], ph, abort_flag, p.status);
         if (!ok) break;
-        ph ^= 1u << s;
         if (main) {
           uint8_t* tile = stage_w(s);
 #pragma unroll
@@ -495,10 +528,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
           // The code slot is given back only now: the stores above needed its codes
           // in registers.  Given back right after the loads were issued, the next
           // box could land before a load waiting behind other warps' stores.
-          if (MODE == kDx && main) mbar_arrive(&sh->cempty[s]);
+          if (MODE == kDx && main) mbar_arrive(&sh->cempty[slot]);
         }
         s += kDeqGroups;
-        if (s >= kStages) s -= kStages;
+        if (s >= kStages) {
+          s -= kStages;
+          ph ^= 1;
+        }
+        slot += kDeqGroups;
+        if (slot >= kCodeSlots) slot -= kCodeSlots;
       }
       base += steps;
     }
@@ -520,12 +558,17 @@ PerDeviceOnce g_attr_done;
 cudaError_t set_attrs() {
   const int dev = PerDeviceOnce::current();
   if (g_attr_done.done(dev)) return cudaSuccess;
-  const void* kernels[5] = {(const void*)expert_gemm_kernel<kFwd, false>, (const void*)expert_gemm_kernel<kFwd, true>,
-                            (const void*)expert_gemm_kernel<kDx, false>, (const void*)expert_gemm_kernel<kDx, true>,
-                            (const void*)expert_gemm_kernel<kI8, false>};
+  const void* kernels[] = {
+      (const void*)expert_gemm_kernel<kFwd, false, 1>, (const void*)expert_gemm_kernel<kFwd, true, 1>,
+      (const void*)expert_gemm_kernel<kFwd, false, 2>, (const void*)expert_gemm_kernel<kFwd, true, 2>,
+      (const void*)expert_gemm_kernel<kDx, false, 1>,  (const void*)expert_gemm_kernel<kDx, true, 1>,
+      (const void*)expert_gemm_kernel<kDx, false, 2>,  (const void*)expert_gemm_kernel<kDx, true, 2>,
+      (const void*)expert_gemm_kernel<kI8, false, 1>};
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 5 && e == cudaSuccess; ++i)
-    e = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, int(gemm_smem(kDx)));
+  for (const void* k : kernels)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               int(std::max(gemm_smem(kDx, 1), gemm_smem(kDx, 2))));
   if (e == cudaSuccess) g_attr_done.mark(dev);
   return e;
 }
@@ -533,7 +576,7 @@ cudaError_t set_attrs() {
 bool set_grid(ExpertGemm* L, int sms) {
   ExpertParams& p = L->p;
   p.col_tiles = int((int64_t(p.out_cols) + kTileW - 1) / kTileW);
-  const int64_t tiles = max_row_tiles(p.M, p.E, kTileT) * p.col_tiles;
+  const int64_t tiles = max_row_tiles(p.M, p.E, L->parts * kPartT) * p.col_tiles;
   if (tiles > int64_t(0x7fffffff)) return false;
   L->grid = 2u * unsigned(std::min<int64_t>(tiles, std::max(sms / 2, 1)));
   return true;
@@ -548,14 +591,14 @@ bool token_maps(ExpertGemm* L, const void* tok, uint64_t cols, const void* ad, i
          encode_map_2d(&L->maps.ad_s, ad, MapElem::k16, r, M, 64, 32, sw);
 }
 
-template <int MODE, bool F16>
+template <int MODE, bool F16, int PARTS>
 cudaError_t launch(const ExpertGemm& L, int prof_id, cudaStream_t st, int* launches) {
   cudaError_t e = set_attrs();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(L.grid, 1, 1);
   cfg.blockDim = dim3(MODE == kI8 ? kThreadsI8 : kThreads, 1, 1);
-  cfg.dynamicSmemBytes = gemm_smem(MODE);
+  cfg.dynamicSmemBytes = gemm_smem(MODE, PARTS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -563,7 +606,7 @@ cudaError_t launch(const ExpertGemm& L, int prof_id, cudaStream_t st, int* launc
   cfg.attrs = attr;
   cfg.numAttrs = prof_on() ? 0 : 1;
   NF4_PROF_BEGIN(st, prof_id);
-  e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<MODE, F16>, L.maps, L.p);
+  e = cudaLaunchKernelEx(&cfg, expert_gemm_kernel<MODE, F16, PARTS>, L.maps, L.p);
   NF4_PROF_END(st, prof_id);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess) ++*launches;
@@ -576,6 +619,7 @@ bool ExpertGemm::prepare(const GroupedArgs& g, bool backward, const void* ad, in
   const LinearArgs& a = g.lin;
   dx = backward;
   f16 = a.f16 != 0;
+  parts = a.M > int64_t(kPartT) * g.E ? 2 : 1;
   ExpertGemm* L = this;
   const uint64_t N = uint64_t(a.N), K = uint64_t(a.K), E = uint64_t(g.E);
   const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -613,8 +657,13 @@ bool ExpertGemm::prepare(const GroupedArgs& g, bool backward, const void* ad, in
 }
 
 cudaError_t ExpertGemm::run(cudaStream_t st, int* launches) const {
-  if (dx) return f16 ? launch<kDx, true>(*this, kKGroupedDx, st, launches) : launch<kDx, false>(*this, kKGroupedDx, st, launches);
-  return f16 ? launch<kFwd, true>(*this, kKGroupedFwd, st, launches) : launch<kFwd, false>(*this, kKGroupedFwd, st, launches);
+  const int id = dx ? kKGroupedDx : kKGroupedFwd;
+  if (parts == 2) {
+    if (dx) return f16 ? launch<kDx, true, 2>(*this, id, st, launches) : launch<kDx, false, 2>(*this, id, st, launches);
+    return f16 ? launch<kFwd, true, 2>(*this, id, st, launches) : launch<kFwd, false, 2>(*this, id, st, launches);
+  }
+  if (dx) return f16 ? launch<kDx, true, 1>(*this, id, st, launches) : launch<kDx, false, 1>(*this, id, st, launches);
+  return f16 ? launch<kFwd, true, 1>(*this, id, st, launches) : launch<kFwd, false, 1>(*this, id, st, launches);
 }
 
 bool Int8Gemm::prepare(const Int8LinearArgs& a, int sms) {
@@ -642,7 +691,7 @@ bool Int8Gemm::prepare(const Int8LinearArgs& a, int sms) {
 }
 
 cudaError_t Int8Gemm::run(cudaStream_t st, int* launches) const {
-  return launch<kI8, false>(g, kKInt8Linear, st, launches);
+  return launch<kI8, false, 1>(g, kKInt8Linear, st, launches);
 }
 
 }  // namespace nf4

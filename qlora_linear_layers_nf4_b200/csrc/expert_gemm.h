@@ -44,6 +44,7 @@ struct ExpertGemm {
   ExpertMaps maps;
   ExpertParams p;
   unsigned grid = 0;
+  int parts = 1;              // MMAs of 256 tokens a tile
   bool dx = false, f16 = false;
   bool prepare(const GroupedArgs& g, bool backward, const void* ad, int sms);
   cudaError_t run(cudaStream_t st, int* launches) const;
