@@ -7,7 +7,9 @@
 // The weight is the A operand of the MMA (an expert's outputs on the TMEM
 // lanes) and the tokens are the B operand, whose count is any multiple of 16 up
 // to 256: an expert's ragged rows are cut into even tiles that waste at most 15
-// columns, where tokens on the lanes would waste up to 127.  It also puts the
+// columns, where tokens on the lanes would waste up to 127.  A tile has one or
+// two such MMAs (parts): the second takes the same decoded weight tile, so that
+// a weight is decoded once for 512 tokens.  The layout also puts the
 // outputs' contiguous dimension on the lanes, so a row's results are stored
 // under its own row predicate and rows of other experts stay untouched.
 //
@@ -20,8 +22,9 @@
 // Roles in each CTA: warp 0 token TMA, warp 1 weight-side TMA (NF4 codes or the
 // int8 tile), warp 2 MMA (issued by the pair's leader), warps 4-7 epilogue,
 // warps 8-19 dequant (NF4).  Rings: six stages of [weight tile 16 KB | tokens
-// 16 KB] with a code slot each; two accumulators of 256 TMEM columns, so a
-// tile's epilogue runs under the next tile's MMAs.
+// 16 KB], or four with 32 KB of tokens; six code slots; two accumulators of 256
+// TMEM columns, so that a one-part tile's epilogue runs under the next tile's
+// MMAs, and a two-part tile's first half under the next tile's first steps.
 #include <algorithm>
 
 #include <cuda.h>
@@ -55,12 +58,13 @@ constexpr uint32_t kCodeBytes = 128 * 32;   // kDx: NF4 codes of one step
 constexpr int kCodeSlots = 6;
 constexpr int kEpiWarp = 4;                 // warps 4..7
 constexpr int kDeqWarp = 8;
-constexpr int kDeqGroups = 3;               // of four warps; kCodeSlots is a multiple
-constexpr int kThreads = 32 * (kDeqWarp + 4 * kDeqGroups);
-constexpr int kThreadsI8 = 32 * kDeqWarp;
 
 // Ring stages: [weight tile | tokens of each part].
 constexpr int stages_of(int parts) { return parts == 2 ? 4 : 6; }
+// Dequant groups of four warps each take every deq_groups-th step; the stages and
+// the code slots are multiples of their number, so that each belongs to one group.
+constexpr int deq_groups(int parts) { return parts == 2 ? 2 : 3; }
+constexpr int threads_of(int mode, int parts) { return 32 * (kDeqWarp + (mode == kI8 ? 0 : 4 * deq_groups(parts))); }
 constexpr uint32_t stage_bytes_of(int parts) { return kWBytes + uint32_t(parts) * kTBytes; }
 
 struct GemmShared {
@@ -156,11 +160,13 @@ __device__ __forceinline__ uint32_t code_offset(uint32_t row) {
 }
 
 template <int MODE, bool F16, int PARTS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThreadsI8 : kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PARTS), 1)
     expert_gemm_kernel(const __grid_constant__ ExpertMaps maps, const ExpertParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kStages = stages_of(PARTS);
+  constexpr int kDeqGroups = deq_groups(PARTS);
+  static_assert(kStages % kDeqGroups == 0 && kCodeSlots % kDeqGroups == 0, "a stage and a slot belong to one group");
   constexpr uint32_t kStageBytes = stage_bytes_of(PARTS);
   uint8_t* code_base = smem + kStages * kStageBytes;
   GemmShared* sh = reinterpret_cast<GemmShared*>(code_base + (MODE == kDx ? kCodeSlots * kCodeBytes : 0));
@@ -397,7 +403,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
       last = (last + steps) % kStages;
       const int parts = PARTS == 2 && t.nt[1] > 0 ? 2 : 1;
 #pragma unroll 1
-      for (int h = 0; h < parts; ++h, ++n) {
+      for (int h = 0; h < PARTS; ++h, ++n) {
+        if (h >= parts) break;
         const int t0 = h == 0 ? t.t0 : t.t0 + t.nt[0];
         const int cnt = h + 1 == parts ? t.t0 + t.cnt - t0 : t.nt[0];
         ok = warp_wait<300>(&sh->acc_full[n & 1], (n >> 1) & 1, abort_flag, p.status);
@@ -457,8 +464,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
     int base = 0;         // steps of the tiles before
     int s = group;               // stage of this group's next step
     uint32_t ph = 1;             // parity of the wait for that stage
-    int slot = group;            // and its code slot
-    uint32_t cph = 0;
+    int own_slot = group;        // and its code slot (with as many stages as slots: the stage's)
+    uint32_t cph = 0;            // bit i: parity of the wait for the codes in slot i
     bool ok = true;
     for (int id = pair; id < tiles && ok; id += pairs) {
       const Tile t = tile_at<PARTS>(&sh->groups, p.E, p.col_tiles, id);
@@ -502,6 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
           codes = next;
           next = load_codes(k + kDeqGroups);
         } else if (main) {
+          const int slot = kStages == kCodeSlots ? s : own_slot;
           ok = warp_wait(&sh->cfull[slot], (cph >> slot) & 1u, abort_flag, p.status);
           if (!ok) break;
           cph ^= 1u << slot;
@@ -528,15 +536,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kI8 ? kThrea
           // The code slot is given back only now: the stores above needed its codes
           // in registers.  Given back right after the loads were issued, the next
           // box could land before a load waiting behind other warps' stores.
-          if (MODE == kDx && main) mbar_arrive(&sh->cempty[slot]);
+          if (MODE == kDx && main) mbar_arrive(&sh->cempty[kStages == kCodeSlots ? s : own_slot]);
         }
         s += kDeqGroups;
         if (s >= kStages) {
           s -= kStages;
           ph ^= 1;
         }
-        slot += kDeqGroups;
-        if (slot >= kCodeSlots) slot -= kCodeSlots;
+        own_slot += kDeqGroups;
+        if (own_slot >= kCodeSlots) own_slot -= kCodeSlots;
       }
       base += steps;
     }
@@ -597,7 +605,7 @@ cudaError_t launch(const ExpertGemm& L, int prof_id, cudaStream_t st, int* launc
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(L.grid, 1, 1);
-  cfg.blockDim = dim3(MODE == kI8 ? kThreadsI8 : kThreads, 1, 1);
+  cfg.blockDim = dim3(threads_of(MODE, PARTS), 1, 1);
   cfg.dynamicSmemBytes = gemm_smem(MODE, PARTS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -619,7 +627,14 @@ bool ExpertGemm::prepare(const GroupedArgs& g, bool backward, const void* ad, in
   const LinearArgs& a = g.lin;
   dx = backward;
   f16 = a.f16 != 0;
-  parts = a.M > int64_t(kPartT) * g.E ? 2 : 1;
+  // Two MMAs a decoded weight tile where experts have more rows than one MMA
+  // takes and one-MMA tiles would need a second wave of CTA pairs: a wide tile
+  // costs 1.3 times a narrow one.  Measured, narrow against wide, 4096 x 4096:
+  // 8 experts of 272 rows 132 us against 102, of 512 rows 138 against 117, of 240
+  // rows 80 against 80; 2 experts of 1024 rows 78 against 64, but of 512 rows, 64
+  // narrow tiles on 74 pairs, 48 against 61.
+  const int64_t out_tiles = ((backward ? a.K : a.N) + kTileW - 1) / kTileW;
+  parts = a.M > int64_t(kPartT) * g.E && a.M / kPartT * out_tiles > sms / 2 ? 2 : 1;
   ExpertGemm* L = this;
   const uint64_t N = uint64_t(a.N), K = uint64_t(a.K), E = uint64_t(g.E);
   const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B;

@@ -307,6 +307,22 @@ def test_weight_bound_calls_repeated(cuda_device, counts, n, k, r):
         assert all(torch.equal(a, b) for a, b in zip(again, (y, dA, dB, dx)))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("counts,r", [([1500, 1000, 100], 72), ([2331, 17, 257], 8), ([0, 2800], 64)])
+def test_many_rows_an_expert(cuda_device, counts, r, dtype):
+    """Tiles of up to 512 tokens, two products of a decoded weight tile: tiles with both and with one of them, odd
+    halves; and the same bits every time."""
+    import torch
+    g = Stack(cuda_device, counts, 2040, 1984, r, dtype, dq=r == 8, bias=r == 72, seed=12)
+    y, t = g.fwd()
+    g.check_fwd(y, t)
+    dA, dB, dx = g.bwd(t=t)
+    g.check_bwd(dA, dB, dx, t)
+    for _ in range(60):
+        again = g.fwd()[:1] + g.bwd(t=t)
+        assert all(torch.equal(a, b) for a, b in zip(again, (y, dA, dB, dx)))
+
+
 @pytest.mark.parametrize("counts", [[1, 0, 2], [80, 200, 3]])
 def test_one_expert_equals_the_dense_layer(cuda_device, counts):
     """Each expert's rows give what the dense layer gives on that expert's weight, to rounding."""
