@@ -10,7 +10,8 @@
 //
 // TMA boxes start at any row, so only a tile's last step holds rows of the next
 // expert.  Its MMAs stop at the next multiple of 16 rows, and a warp clears the up
-// to 15 rows between in both operands (a cleared row times NaN would still be NaN).
+// to 15 rows between in both operands (a cleared row times NaN would still be NaN)
+// as soon as they land, ahead of the MMAs.
 //
 // dA sums products of U, whose rounding to 16 bits would be its largest error by
 // far (2^-9 against 2^-24 for a sum's step).  U comes as three bf16 terms that
@@ -51,8 +52,7 @@ struct GradShared {
   uint64_t empty[kGrMaxStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
-  uint64_t tail;      // a tile's last step has landed and holds rows past the expert
-  uint64_t fixed;     // they are cleared
+  uint64_t fixed[kGrMaxStages];   // the rows past the expert in a tile's last step are cleared
   uint64_t drain;
   uint32_t tmem_base;
   uint32_t abort_flag;
@@ -92,14 +92,13 @@ __global__ void __launch_bounds__(kGrThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&sh->full[s], 2);
-      mbar_init(&sh->empty[s], 1);
+      mbar_init(&sh->empty[s], 2);   // the MMAs and the tail warp
+      mbar_init(&sh->fixed[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->acc_full[b], 1);
       mbar_init(&sh->acc_empty[b], 4);
     }
-    mbar_init(&sh->tail, 1);
-    mbar_init(&sh->fixed, 1);
     mbar_init(&sh->drain, 1);
     sh->abort_flag = 0;
     fence_barrier_init();
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(kGrThreads, 1)
     // ---------------- MMA: the whole warp walks the steps, one lane issues
     const bool issue = elect_one();
     int s = 0, n = 0;
-    uint32_t ph = 0, fixed_ph = 0;
+    uint32_t ph = 0, fixed_ph = 0;   // fixed_ph: bit s for stage s
     bool ok = true;
     for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x) {
       const GradTile t = grad_tile(&sh->groups, p, id);
@@ -177,9 +176,8 @@ __global__ void __launch_bounds__(kGrThreads, 1)
         ok = ring_wait(&sh->full[s], ph, abort_flag, p.status);
         const int left = t.cnt - k;
         if (ok && left < 64 && (left & 15)) {
-          if (issue) mbar_arrive(&sh->tail);
-          ok = ring_wait(&sh->fixed, fixed_ph, abort_flag, p.status);
-          fixed_ph ^= 1;
+          ok = ring_wait(&sh->fixed[s], (fixed_ph >> s) & 1u, abort_flag, p.status);
+          fixed_ph ^= 1u << s;
         }
         if (!ok) break;
         tc_fence_after();
@@ -213,29 +211,38 @@ __global__ void __launch_bounds__(kGrThreads, 1)
       ring_wait(&sh->drain, 0, &none, nullptr);
     }
   } else if (warp == 3) {
-    // ---------------- rows past an expert's last, up to the next multiple of 16, in its last step
+    // ---------------- tail: clears the rows past an expert's last, up to the next
+    // multiple of 16, as soon as a tile's last step has landed.  It walks every
+    // step and gives each stage back too, so that it stays within the ring.
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (int id = blockIdx.x; id < tiles && ok; id += gridDim.x) {
       const GradTile t = grad_tile(&sh->groups, p, id);
-      if (t.cnt == 0) continue;
-      s = (s + (t.cnt - 1) / 64) % p.stages;   // stage of the last step
-      const int left = t.cnt - (t.cnt - 1) / 64 * 64;
-      if (left < 64 && (left & 15)) {
-        ok = warp_wait(&sh->tail, ph, abort_flag, p.status);
+      for (int k = 0; k < t.cnt; k += 64) {
+        ok = warp_wait(&sh->full[s], ph, abort_flag, p.status);
         if (!ok) break;
-        ph ^= 1;
-        uint8_t* a = smem + s * stage_bytes;
-        const int blocks = 2 + p.job[t.job].terms;   // [64 rows][128 bytes] each, A then the terms
-        const int chunks = (16 - (left & 15)) * 8;
-        for (int i = lane; i < blocks * chunks; i += 32)
-          *reinterpret_cast<uint4*>(a + (i / chunks) * 8192 + left * 128 + (i % chunks) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
+        const int left = t.cnt - k;
+        const bool clear = left < 64 && (left & 15);
+        if (clear) {
+          uint8_t* a = smem + s * stage_bytes;
+          const int blocks = 2 + p.job[t.job].terms;   // [64 rows][128 bytes] each, A then the terms
+          const int chunks = (16 - (left & 15)) * 8;
+          for (int b = 0; b < blocks; ++b)
+            for (int i = lane; i < chunks; i += 32)
+              *reinterpret_cast<uint4*>(a + b * 8192 + left * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->fixed);
+        if (lane == 0) {
+          if (clear) mbar_arrive(&sh->fixed[s]);
+          mbar_arrive(&sh->empty[s]);
+        }
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      if (++s == p.stages) s = 0;
     }
   } else {
     // ---------------- epilogue: lane = output row, register = adapter column
