@@ -12,18 +12,22 @@
 // (so the result does not depend on who came last) and finishes the tile.
 // Nothing waits for another CTA.
 //
-// Inside a CTA groups of eight warps take turns at the units (so that their waits,
-// loads and MMAs overlap), a warp two of a unit's 64-wide K blocks and 32 rows: a
-// code byte becomes two fp32 levels with one lookup in a 256-entry table replicated
-// per lane (conflict-free; entries 256 bytes apart, so that one byte permute makes
-// the address), each is multiplied by its row's scale, and the pair is rounded to
-// the compute type: the same W' as the GEMM's, as A fragments of mma.sync m16n8k16
-// with x as B.  (Rounded levels in the table and the scale on the block's sums
-// would halve the lookups' traffic, but the levels' rounding made y's error 1.6
-// times as large.)  A producer warp keeps code and x boxes in flight and a warp per
-// group the scales of its units; three more warps finish a tile (sums, bias, split
-// tiles) while the next one streams.  The lookups are 1,024 of a unit's 1,280
-// shared-memory wavefronts, its MMAs about 600 cycles.
+// Inside a CTA two groups of eight warps take turns at the units (so that their
+// waits, loads and MMAs overlap), a warp 16 rows.  W' is made in registers, as A
+// fragments of mma.sync m16n8k16 with x as B, bit for bit the GEMM's: the fp32
+// product of level and scale rounded to the compute type.  Two ways share the work,
+// because each fills another pipe.  Half of the rows go through byte permutes on a
+// table of their block's sixteen products, in registers; the other half looks a
+// code byte up in a 256-entry table of fp32 level pairs, replicated per lane
+// (conflict-free; entries 256 bytes apart, so that one byte permute makes the
+// offset), and multiplies and rounds.  A 16-token step took 86 us so, 95 with the
+// lookups alone (1,024 of a unit's 1,400 shared-memory wavefronts) and more with
+// the permutes alone.  (Levels rounded to 16 bits in the table and the scale on the
+// block's sums would be cheaper still, but made y's error 1.6 times as large.)
+// A producer warp keeps code and x boxes in flight and a warp per group the scales
+// of its units; four more warps finish a tile (sums, bias, split tiles) while the
+// next one streams.  A unit takes about 1,600 cycles: latency between these steps,
+// no pipe is above two thirds.
 //
 // T = s x A_e^T comes from a small kernel launched just before, which this one
 // overlaps (programmatic dependent launch) until it finishes its first tile.
@@ -37,6 +41,7 @@
 #include "grouped.cuh"
 #include "kernels.h"
 #include "nf4_common.cuh"
+#include "nf4_dequant.cuh"
 #include "ring_wait.cuh"
 #include "tc_common.cuh"
 #include "tensor_maps.h"
@@ -48,9 +53,9 @@ using namespace tc;
 using expert::ring_wait;
 using expert::warp_wait;
 
-constexpr int kDcGroupWarps = 8;                     // 2 K halves x 4 sets of 32 rows
-constexpr int kDcEpiWarps = 3;                       // finish tiles
-constexpr int kDcRows = 128;
+constexpr int kDcGroupWarps = 8;                     // 16 rows each
+constexpr int kDcEpiWarps = 4;                       // finish tiles, a thread per row
+constexpr int kDcRows = 32 * kDcEpiWarps;
 constexpr int kDcBlocks = 4;                         // 64-wide K blocks per unit
 constexpr uint32_t kDcCodeBytes = kDcRows * 128;
 constexpr uint32_t kLutBytes = 256 * 256;            // entry e, lane l at 256 e + 8 l
@@ -72,8 +77,8 @@ struct DcShared {
   uint64_t red_free;                                 // the finishing warps have read them
   uint32_t abort_flag;
   int last;                                          // this CTA finishes the tile
-  float scales[dc_stages(NP)][kDcBlocks][kDcRows];
-  float red[2 * kDcGroups][kDcRows * NP];        // the consumers' sums of a tile, [token][row]
+  float scales[dc_stages(NP)][kDcBlocks][kDcRows + 8];   // + 8: a warp's reads of four blocks hit different banks
+  float red[kDcGroups][kDcRows * NP];        // the consumers' sums of a tile, [token][row]
   GroupTable groups;
 };
 template <int NP>
@@ -163,10 +168,9 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   constexpr int kGroups = kDcGroups, kConsumers = kDcConsumers;
   constexpr int kScaler = kConsumers + kDcEpiWarps;  // first scale warp
   constexpr int kProducer = kScaler + kGroups;
-  constexpr int kParts = 2 * kGroups;
   constexpr int NT8 = NP / 8;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = expert::align_1024(smem_raw);
   uint8_t* lut = smem + kStages * dc_stage_bytes(NP);
   DcShared<NP>* sh = reinterpret_cast<DcShared<NP>*>(lut + kLutBytes);
   const int warp = threadIdx.x >> 5;
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   if (warp >= kConsumers) {
     // ---------------- finishing warps: a thread per row of the tile
     constexpr int kEpi = 32 * kDcEpiWarps;
-    const int first = threadIdx.x - 32 * kConsumers;
+    const int row = threadIdx.x - 32 * kConsumers;
     bool ok = true, waited = false;
     uint32_t ph = 0;
     DcTile t{};
@@ -340,52 +344,56 @@ __global__ void __launch_bounds__(kDcThreads, 1)
       u = end;
       const int rows = min(NP, groups->start[t.e + 1] - t.row0);
       const int64_t n0 = int64_t(t.e) * p.N;
-      if (starts)
-        for (int row = first; row < kDcRows; row += kEpi) {
-          const uint16_t* b = p.B + (n0 + min(t.nt * kDcRows + row, p.N - 1)) * p.r;
-          for (int j = 0; j < p.r; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + j));
-        }
+      const int n = t.nt * kDcRows + row;
+      if (starts) {
+        const uint16_t* b = p.B + (n0 + min(n, p.N - 1)) * p.r;
+        for (int j = 0; j < p.r; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + j));
+      }
       if (!waited) grid_dep_wait();   // the counters' zeros, of the kernel before
       waited = true;
       if (ok) ok = warp_wait<100>(&sh->red_full, ph, abort_flag, p.status);
       ph ^= 1;
-      auto part_sum = [&](int m, int row) {
-        float v = 0.0f;
+      float v[NP];
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) v += sh->red[i][m * kDcRows + row];
-        return v;
-      };
-      uint32_t c0 = 0, c1 = 0;
+      for (int m = 0; m < NP; ++m) {
+        v[m] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) v[m] += sh->red[i][m * kDcRows + row];
+      }
       bool finish = true;
       if (split) {
         // contributors are consecutive CTAs, the first from chunk 0
-        c0 = uint32_t((uint64_t(tile_u + 1) * G - 1) / units);
-        c1 = uint32_t((uint64_t(tile_u + kch) * G - 1) / units);
-        float* mine = p.partials + (size_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * (kDcRows * NP);
-        for (int row = first; row < kDcRows; row += kEpi)
-          for (int m = 0; m < rows; ++m) __stcg(mine + m * kDcRows + row, part_sum(m, row));
+        const uint32_t c0 = uint32_t((uint64_t(tile_u + 1) * G - 1) / units);
+        const uint32_t c1 = uint32_t((uint64_t(tile_u + kch) * G - 1) / units);
+        float* mine = p.partials + (size_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * (kDcRows * NP) + row;
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+          if (m < rows) __stcg(mine + m * kDcRows, v[m]);
         __threadfence();
         named_barrier(1, kEpi);
-        if (first == 0) sh->last = atomicAdd(p.counters + c0, 1) == int(c1 - c0);
+        if (row == 0) sh->last = atomicAdd(p.counters + c0, 1) == int(c1 - c0);
         named_barrier(1, kEpi);
         finish = sh->last != 0;
-        if (finish) __threadfence();
-      }
-      if (finish && ok) {
-        for (int row = first; row < kDcRows; row += kEpi) {
-          const int n = t.nt * kDcRows + row;
-          if (n >= p.N) continue;
-          const float bias = p.bias != nullptr ? one_float<F16>(__ldg(p.bias + n0 + n)) : 0.0f;
-          uint16_t* y = p.y + int64_t(t.row0) * p.N + n;
-          for (int m = 0; m < rows; ++m, y += p.N) {
-            float v = 0.0f;
-            if (!split) v = part_sum(m, row);
-            else
-              for (uint32_t c = c0; c <= c1; ++c)
-                v += __ldcg(p.partials + (size_t(c) * 2 + (c == c0 ? 1 : 0)) * (kDcRows * NP) + m * kDcRows + row);
-            *y = one_rounded<F16>(v + bias);
+        if (finish) {
+          // a contributor's rows are loaded together: one after another they were a
+          // tail of 13 us behind the last tile (a tenth of a 16-token step)
+          __threadfence();
+#pragma unroll
+          for (int m = 0; m < NP; ++m) v[m] = 0.0f;
+          for (uint32_t c = c0; c <= c1; ++c) {
+            const float* part = p.partials + (size_t(c) * 2 + (c == c0 ? 1 : 0)) * (kDcRows * NP) + row;
+#pragma unroll
+            for (int m = 0; m < NP; ++m)
+              if (m < rows) v[m] += __ldcg(part + m * kDcRows);
           }
         }
+      }
+      if (finish && ok && n < p.N) {
+        const float bias = p.bias != nullptr ? one_float<F16>(__ldg(p.bias + n0 + n)) : 0.0f;
+        uint16_t* y = p.y + int64_t(t.row0) * p.N + n;
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+          if (m < rows) y[int64_t(m) * p.N] = one_rounded<F16>(v[m] + bias);
       }
       named_barrier(1, kEpi);   // red and last may be written again
       if (lane == 0) mbar_arrive(&sh->red_free);
@@ -395,25 +403,29 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   }
 
   // ---------------- consumers
+  // A warp takes 16 W rows of a unit.  The four lanes of a row pair (2 g and 2 g + 1,
+  // the MMA rows g and g + 8) take a 64-wide block each, whole: the k index of an MMA
+  // is free as long as W' and x agree, so lane q's four k positions are columns of
+  // block q.  Row 2 g is decoded with byte permutes from a table of its block's
+  // sixteen products (as in the GEMM), row 2 g + 1 with the shared-memory lookups.
   const int group = warp / kDcGroupWarps;
-  const int pair = (warp >> 2) & 1;         // K blocks 2 pair, 2 pair + 1 of the unit
-  const int set = warp & 3;                 // rows 32 set ..
+  const int set = warp % kDcGroupWarps;     // rows 16 set ..
   const int g = lane >> 2, q = lane & 3;
   const uint32_t lane8 = uint32_t(lane) << 3;   // below 256: one byte
   const int kb_per_row = p.K >> 6;
   bool ok = true, waited = false;
   int s = group;
   uint32_t ph = 0, red_ph = 1;
-  // Addresses inside a stage, of the first of the two blocks.  This thread's four
-  // rows: two 16-row groups (2048 bytes apart), W rows 2 g and 2 g + 1 of each (MMA
-  // rows g and g + 8): a half-warp's code loads then hit different bank groups.
+  // Addresses inside a stage.  Lane q walks its block's 16-byte-of-x steps in the
+  // order i ^ 2 q and its code granules in the order m ^ q, so that the lanes' loads
+  // hit different banks.
   uint32_t code_at[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t row = uint32_t(set * 32 + 2 * g + i);
-    code_at[i] = row * 128u + (((4u * uint32_t(pair) + uint32_t(q >> 1)) ^ (row & 7u)) << 4) + (uint32_t(q & 1) << 3);
+    const uint32_t row = uint32_t(set * 16 + 2 * g + i);
+    code_at[i] = row * 128u + ((uint32_t(2 * q + (q >> 1)) ^ (row & 7u)) << 4) + (uint32_t(q & 1) << 3);
   }
-  const uint32_t x_at = kDcCodeBytes + uint32_t(pair) * (2 * NP * 128) + sw128_offset(uint32_t(g), uint32_t(2 * q));
+  const uint32_t x_at = kDcCodeBytes + uint32_t(q) * (NP * 128) + uint32_t(g) * 128u + (uint32_t((2 * q) ^ g) << 4);
   DcTile t{};
   if (u0 < u1) t = dc_tile(groups, p.E, NP, p.n_tiles, tile0);
   int kc = kc0 + group;                     // chunk of this warp's next unit, counted from tile t
@@ -422,7 +434,7 @@ __global__ void __launch_bounds__(kDcThreads, 1)
     const bool first_part = seg == tile_u;
     seg = min(u1, tile_u + kch);
     const int kend = int(seg - tile_u);     // this CTA's chunks of the tile end here
-    float acc[2][NT8][4];
+    float acc[2][NT8][4];                   // of even and odd MMAs
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -431,34 +443,24 @@ __global__ void __launch_bounds__(kDcThreads, 1)
       if (ok) ok = warp_wait(&sh->full[s], ph, abort_flag, p.status);
       if (ok) {
         const uint8_t* st = smem + s * dc_stage_bytes(NP);
-        const float* sc = &sh->scales[s][2 * pair][set * 32 + 2 * g];
+        float2 scale = *reinterpret_cast<const float2*>(&sh->scales[s][q][set * 16 + 2 * g]);
+        if (kc * kDcBlocks + q >= kb_per_row) scale = make_float2(0.0f, 0.0f);   // past the row's end: x is zero there
+        const expert::BlockTable table = expert::make_table(scale.x, F16);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (kc * kDcBlocks + 2 * pair + j >= kb_per_row) break;   // past the row's end
-          uint4 xl[NT8], xh[NT8];
+        for (int m = 0; m < 4; ++m) {
+          const uint2 w0 = *reinterpret_cast<const uint2*>(st + (code_at[0] ^ (m * 8u)));
+          const uint2 w1 = *reinterpret_cast<const uint2*>(st + (code_at[1] ^ (m * 8u)));
 #pragma unroll
-          for (int c = 0; c < NT8; ++c) {
-            xl[c] = *reinterpret_cast<const uint4*>(st + x_at + j * (NP * 128) + c * 1024);
-            xh[c] = *reinterpret_cast<const uint4*>(st + (x_at ^ 16u) + j * (NP * 128) + c * 1024);
-          }
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t c0 = h ? w0.y : w0.x, c1 = h ? w1.y : w1.x;
+            const uint4 v = expert::decode8(c0, table);
+            const uint32_t a0[4] = {v.x, two_weights<0, F16>(lut, c1, lane8, scale.y), v.y, two_weights<1, F16>(lut, c1, lane8, scale.y)};
+            const uint32_t a1[4] = {v.z, two_weights<2, F16>(lut, c1, lane8, scale.y), v.w, two_weights<3, F16>(lut, c1, lane8, scale.y)};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint2 w0 = *reinterpret_cast<const uint2*>(st + (code_at[0] ^ (j * 32u)) + i * 2048);
-            const uint2 w1 = *reinterpret_cast<const uint2*>(st + (code_at[1] ^ (j * 32u)) + i * 2048);
-            const float2 scale = *reinterpret_cast<const float2*>(sc + j * kDcRows + i * 16);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {          // elements 0..7 and 8..15 of the lane's sixteen
-              const uint32_t c0 = h ? w0.y : w0.x, c1 = h ? w1.y : w1.x;
-              const uint32_t a0[4] = {two_weights<0, F16>(lut, c0, lane8, scale.x), two_weights<0, F16>(lut, c1, lane8, scale.y),
-                                      two_weights<1, F16>(lut, c0, lane8, scale.x), two_weights<1, F16>(lut, c1, lane8, scale.y)};
-              const uint32_t a1[4] = {two_weights<2, F16>(lut, c0, lane8, scale.x), two_weights<2, F16>(lut, c1, lane8, scale.y),
-                                      two_weights<3, F16>(lut, c0, lane8, scale.x), two_weights<3, F16>(lut, c1, lane8, scale.y)};
-#pragma unroll
-              for (int c = 0; c < NT8; ++c) {
-                const uint4& v = h ? xh[c] : xl[c];
-                mma_16816<F16>(acc[i][c], a0, v.x, v.y);
-                mma_16816<F16>(acc[i][c], a1, v.z, v.w);
-              }
+            for (int c = 0; c < NT8; ++c) {
+              const uint4 xv = *reinterpret_cast<const uint4*>(st + (x_at ^ ((2 * m + h) * 16u)) + c * 1024);
+              mma_16816<F16>(acc[0][c], a0, xv.x, xv.y);
+              mma_16816<F16>(acc[1][c], a1, xv.z, xv.w);
             }
           }
         }
@@ -472,34 +474,33 @@ __global__ void __launch_bounds__(kDcThreads, 1)
       }
     }
     kc -= p.k_chunks;
+#pragma unroll
+    for (int c = 0; c < NT8; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[0][c][i] += acc[1][c][i];
 
     // The adapter's product enters the tile's first part, as MMAs with the rows
-    // of B_e as A and T as B; the pairs of K halves take 16 columns in turn.
+    // of B_e as A and T as B; the groups take 16 columns in turn.
     if (first_part) {
       if (!waited) grid_dep_wait();   // T of the kernel before
       waited = true;
-      for (int j0 = 16 * (2 * group + pair); j0 < p.r; j0 += 16 * kParts) {
+      for (int j0 = 16 * group; j0 < p.r; j0 += 16 * kGroups) {
         const int ja = j0 + 2 * q, jb = ja + 8;   // r is a multiple of 8: the second half may be missing
-        uint32_t tb[NT8][2];
+        uint32_t a[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = min(t.nt * kDcRows + set * 16 + 2 * g + h, p.N - 1);
+          const uint16_t* brow = p.B + (int64_t(t.e) * p.N + n) * p.r;
+          a[h] = __ldg(reinterpret_cast<const uint32_t*>(brow + ja));
+          a[2 + h] = jb < p.r ? __ldg(reinterpret_cast<const uint32_t*>(brow + jb)) : 0u;
+        }
 #pragma unroll
         for (int c = 0; c < NT8; ++c) {
           const int m = t.row0 + 8 * c + g;
           const uint16_t* trow = p.T + int64_t(min(m, p.M - 1)) * p.r;
-          tb[c][0] = m < p.M ? __ldcg(reinterpret_cast<const uint32_t*>(trow + ja)) : 0u;
-          tb[c][1] = m < p.M && jb < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(trow + jb)) : 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t a[4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int n = min(t.nt * kDcRows + set * 32 + i * 16 + 2 * g + h, p.N - 1);
-            const uint16_t* brow = p.B + (int64_t(t.e) * p.N + n) * p.r;
-            a[h] = __ldg(reinterpret_cast<const uint32_t*>(brow + ja));
-            a[2 + h] = jb < p.r ? __ldg(reinterpret_cast<const uint32_t*>(brow + jb)) : 0u;
-          }
-#pragma unroll
-          for (int c = 0; c < NT8; ++c) mma_16816<F16>(acc[i][c], a, tb[c][0], tb[c][1]);
+          const uint32_t b0 = m < p.M ? __ldcg(reinterpret_cast<const uint32_t*>(trow + ja)) : 0u;
+          const uint32_t b1 = m < p.M && jb < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(trow + jb)) : 0u;
+          mma_16816<F16>(acc[0][c], a, b0, b1);
         }
       }
     }
@@ -507,15 +508,12 @@ __global__ void __launch_bounds__(kDcThreads, 1)
     // the tile's sums, for the finishing warps
     if (ok) ok = warp_wait(&sh->red_free, red_ph, abort_flag, p.status);
     red_ph ^= 1;
+    const int row = set * 16 + 2 * g;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = set * 32 + i * 16 + 2 * g;
-#pragma unroll
-      for (int c = 0; c < NT8; ++c) {
-        float* o = sh->red[2 * group + pair] + (8 * c + 2 * q) * kDcRows + row;
-        *reinterpret_cast<float2*>(o) = make_float2(acc[i][c][0], acc[i][c][2]);
-        *reinterpret_cast<float2*>(o + kDcRows) = make_float2(acc[i][c][1], acc[i][c][3]);
-      }
+    for (int c = 0; c < NT8; ++c) {
+      float* o = sh->red[group] + (8 * c + 2 * q) * kDcRows + row;
+      *reinterpret_cast<float2*>(o) = make_float2(acc[0][c][0], acc[0][c][2]);
+      *reinterpret_cast<float2*>(o + kDcRows) = make_float2(acc[0][c][1], acc[0][c][3]);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->red_full);

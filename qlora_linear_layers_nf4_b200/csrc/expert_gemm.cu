@@ -163,7 +163,7 @@ template <int MODE, bool F16, int PARTS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PARTS), 1)
     expert_gemm_kernel(const __grid_constant__ ExpertMaps maps, const ExpertParams p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = expert::align_1024(smem_raw);
   constexpr int kStages = stages_of(PARTS);
   constexpr int kDeqGroups = deq_groups(PARTS);
   static_assert(kStages % kDeqGroups == 0 && kCodeSlots % kDeqGroups == 0, "a stage and a slot belong to one group");
@@ -520,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
         }
         if (main) {
           const float scale = k < k_end ? (dq ? __fmul_rn(float(raw), s_g) : __uint_as_float(raw)) : 0.0f;
-          decode_row(codes, make_table(scale, F16), p.mul_shr1, p.mul_shr16, v);
+          decode_row(codes, make_table(scale, F16), v);
         }
         ok = warp_wait(&sh->empty[s], ph, abort_flag, p.status);
         if (!ok) break;
@@ -655,8 +655,6 @@ bool ExpertGemm::prepare(const GroupedArgs& g, bool backward, const void* ad, in
   p.main_steps = int(backward ? (a.N + 63) / 64 : a.K / 64);
   p.adapter_steps = (a.r + 63) / 64;
   p.block_chunks_shift = log2_block(a.w->block_size) - 6;
-  p.mul_shr1 = 1u << 31;
-  p.mul_shr16 = 1u << 16;
   p.dq = a.w->double_quant;
   p.offsets = g.offsets;
   p.codes = a.w->codes;

@@ -22,7 +22,6 @@ struct ExpertParams {
   int main_steps, adapter_steps;
   int col_tiles;
   int block_chunks_shift, dq;   // log2 of the 64-element chunks per block
-  uint32_t mul_shr1, mul_shr16; // 2^31, 2^16: right shifts as high products
   int out_dtype;              // kI8: nf4_dtype of out and bias
   const int32_t* offsets;     // null: all M rows are the one expert's
   const uint8_t* codes;

@@ -81,7 +81,7 @@ __device__ __forceinline__ GradTile grad_tile(const GroupTable* g, const GradPar
 __global__ void __launch_bounds__(kGrThreads, 1)
     expert_grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = expert::align_1024(smem_raw);
   const uint32_t stage_bytes = p.stage_bytes;
   GradShared* sh = reinterpret_cast<GradShared*>(smem + p.stages * stage_bytes);
   const int warp = threadIdx.x >> 5;

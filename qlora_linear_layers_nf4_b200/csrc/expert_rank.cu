@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRkThreads, 1)
     expert_rank_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                        const RankParams p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = expert::align_1024(smem_raw);
   const uint32_t b_bytes = uint32_t(p.NP) * 128u;
   const uint32_t stage_bytes = kRkABytes + b_bytes;
   RankShared* sh = reinterpret_cast<RankShared*>(smem + kRkStages * stage_bytes);

@@ -1,4 +1,4 @@
-// QLoRA linear of a stack of experts on the CUDA cores.
+// QLoRA linear of a stack of experts on the CUDA cores: the fp32 mode.
 //
 // For the rows m of expert e (rows sorted by expert):
 //     y  = x W'_e^T + T B_e^T (+ bias_e),   T = s x A_e^T
@@ -13,8 +13,6 @@
 // with the next slice's loads in flight.
 #include <algorithm>
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "grouped.cuh"
@@ -29,24 +27,8 @@ constexpr int kSK = 16;
 constexpr int kSThreads = 256;
 constexpr int kSRow = kSTile + 4;
 
-__device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float load1(const __half* p) { return __half2float(*p); }
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void store1(__half* p, float v) { *p = __float2half_rn(v); }
-template <typename T>
-__device__ __forceinline__ float round_to(float v) {
-  T t;
-  store1(&t, v);
-  return load1(&t);
-}
-template <>
-__device__ __forceinline__ float round_to<float>(float v) { return v; }
-
 struct SimtOperand {
-  const void* p;         // T elements, or fp32 (f32 == 1); null for the NF4 weight
-  int f32;
+  const float* p;        // null: the NF4 weight
   int64_t ld;            // elements between consecutive stored rows
   int kmajor;            // 1: (i, kk) at p[i * ld + kk]; 0: at p[kk * ld + i]
   int token;             // 1: i is a row of the batch, 2: kk is; 0: the operand is the expert's
@@ -65,10 +47,9 @@ struct SimtParams {
   int by_rows;           // 1: i is a row of the batch; 0: C is per expert, kk is
   int64_t rows;          // by_rows == 0: rows of an expert's C
   int64_t cols;
-  void* c;               // fp32 (c_f32) or T, row-major [*, cols]
-  int c_f32;
+  float* c;              // row-major [*, cols]
   float alpha;
-  const void* bias;      // T, [E, cols] or null
+  const float* bias;     // [E, cols] or null
   int col_tiles, row_tiles;
   int E, M;
   const int32_t* offsets;
@@ -82,7 +63,6 @@ struct SimtParams {
   uint32_t* status;
 };
 
-template <typename T>
 __global__ void __launch_bounds__(kSThreads) grouped_simt_kernel(const SimtParams p) {
   __shared__ float sa[2][kSK * kSRow];
   __shared__ float sb[2][kSK * kSRow];
@@ -125,9 +105,9 @@ __global__ void __launch_bounds__(kSThreads) grouped_simt_kernel(const SimtParam
           const uint32_t byte = p.codes[at >> 1];
           const int64_t blk = at >> p.bs_shift;
           const float scale = p.dq ? __fmul_rn(float(p.absmax_q[blk]), *p.absmax_scale) : p.absmax[blk];
-          f = round_to<T>(__fmul_rn(lut[(at & 1) ? (byte & 15u) : (byte >> 4)], scale));
+          f = __fmul_rn(lut[(at & 1) ? (byte & 15u) : (byte >> 4)], scale);
         } else {
-          f = o.f32 ? load1(static_cast<const float*>(o.p) + at) : load1(static_cast<const T*>(o.p) + at);
+          f = __ldg(o.p + at);
         }
       }
       v[u] = f;
@@ -190,18 +170,15 @@ __global__ void __launch_bounds__(kSThreads) grouped_simt_kernel(const SimtParam
       const int64_t j = j0 + 4 * tx + b;
       if (j >= p.cols) continue;
       float v = __fmul_rn(p.alpha, acc[a][b]);
-      if (p.bias != nullptr) v = __fadd_rn(v, load1(static_cast<const T*>(p.bias) + int64_t(e) * p.cols + j));
-      const int64_t at = ((p.by_rows ? 0 : int64_t(e) * p.rows) + i) * p.cols + j;
-      if (p.c_f32) static_cast<float*>(p.c)[at] = v;
-      else store1(static_cast<T*>(p.c) + at, v);
+      if (p.bias != nullptr) v = __fadd_rn(v, __ldg(p.bias + int64_t(e) * p.cols + j));
+      p.c[((p.by_rows ? 0 : int64_t(e) * p.rows) + i) * p.cols + j] = v;
     }
   }
 }
 
-SimtOperand token_rows(const void* p, int64_t ld, bool kmajor, int token, int64_t extent, bool f32 = false) {
+SimtOperand token_rows(const void* p, int64_t ld, bool kmajor, int token, int64_t extent) {
   SimtOperand o{};
-  o.p = p;
-  o.f32 = f32;
+  o.p = static_cast<const float*>(p);
   o.ld = ld;
   o.kmajor = kmajor;
   o.token = token;
@@ -210,7 +187,7 @@ SimtOperand token_rows(const void* p, int64_t ld, bool kmajor, int token, int64_
 }
 SimtOperand of_expert(const void* p, int64_t ld, bool kmajor, int64_t stride, int64_t extent) {
   SimtOperand o{};
-  o.p = p;
+  o.p = static_cast<const float*>(p);
   o.ld = ld;
   o.kmajor = kmajor;
   o.stride = stride;
@@ -247,11 +224,9 @@ bool set_grid(SimtParams& p, int64_t* ctas) {
   return true;
 }
 
-cudaError_t run(const GroupedArgs& g, const SimtParams& p, int64_t ctas, int id, cudaStream_t st, int* launches) {
+cudaError_t run(const SimtParams& p, int64_t ctas, int id, cudaStream_t st, int* launches) {
   NF4_PROF_BEGIN(st, id);
-  if (g.lin.f32) grouped_simt_kernel<float><<<unsigned(ctas), kSThreads, 0, st>>>(p);
-  else if (g.lin.f16) grouped_simt_kernel<__half><<<unsigned(ctas), kSThreads, 0, st>>>(p);
-  else grouped_simt_kernel<__nv_bfloat16><<<unsigned(ctas), kSThreads, 0, st>>>(p);
+  grouped_simt_kernel<<<unsigned(ctas), kSThreads, 0, st>>>(p);
   NF4_PROF_END(st, id);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) ++*launches;
@@ -281,7 +256,7 @@ SimtParams product_T(const GroupedArgs& g, void* T) {
   p.seg[0].b = of_expert(a.A, a.K, true, int64_t(a.r) * a.K, a.r);
   p.seg[0].kdim = a.K;
   p.cols = a.r;
-  p.c = T;
+  p.c = static_cast<float*>(T);
   p.alpha = a.s;
   return p;
 }
@@ -306,12 +281,12 @@ cudaError_t launch_grouped_fwd_f32(const GroupedArgs& g, cudaStream_t st, int* l
   p.seg[1].b = of_expert(a.B, a.r, true, a.N * a.r, a.N);
   p.seg[1].kdim = a.r;
   p.cols = a.N;
-  p.c = a.y;
-  p.bias = a.bias;
+  p.c = static_cast<float*>(a.y);
+  p.bias = static_cast<const float*>(a.bias);
   ok = ok && add(l, &n, p, kKGroupedFwd);
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < n && e == cudaSuccess; ++i) e = run(g, l[i].p, l[i].ctas, l[i].id, st, launches);
+  for (int i = 0; i < n && e == cudaSuccess; ++i) e = run(l[i].p, l[i].ctas, l[i].id, st, launches);
   return e;
 }
 
@@ -319,7 +294,7 @@ cudaError_t launch_grouped_bwd_f32(const GroupedArgs& g, cudaStream_t st, int* l
   const LinearArgs& a = g.lin;
   uint8_t* ws = a.ws + kWsHeader;
   const void* T = a.t_in ? a.t_in : ws;
-  float* U = reinterpret_cast<float*>(ws + mr_bytes(a.M, a.r));   // fp32 whatever the compute type
+  float* U = reinterpret_cast<float*>(ws + mr_bytes(a.M, a.r));
   Launch l[5];
   int n = 0;
   bool ok = a.t_in != nullptr || add(l, &n, product_T(g, ws), kKGroupedT);
@@ -331,7 +306,6 @@ cudaError_t launch_grouped_bwd_f32(const GroupedArgs& g, cudaStream_t st, int* l
     p.seg[0].kdim = a.N;
     p.cols = a.r;
     p.c = U;
-    p.c_f32 = 1;
     p.alpha = a.s;
     ok = ok && add(l, &n, p, kKGroupedU);
   }
@@ -342,17 +316,15 @@ cudaError_t launch_grouped_bwd_f32(const GroupedArgs& g, cudaStream_t st, int* l
     p.seg[0].b = token_rows(T, a.r, false, 2, a.r);
     p.cols = a.r;
     p.c = a.dB;
-    p.c_f32 = 1;
     ok = ok && add(l, &n, p, kKGroupedDB);
   }
   {  // dA_e = U^T x
     SimtParams p = common(g);
     p.rows = a.r;
-    p.seg[0].a = token_rows(U, a.r, false, 2, a.r, true);
+    p.seg[0].a = token_rows(U, a.r, false, 2, a.r);
     p.seg[0].b = token_rows(a.x, a.K, false, 2, a.K);
     p.cols = a.K;
     p.c = a.dA;
-    p.c_f32 = 1;
     ok = ok && add(l, &n, p, kKGroupedDA);
   }
   if (a.dx != nullptr) {  // dx = dy W'_e + U A_e
@@ -362,16 +334,16 @@ cudaError_t launch_grouped_bwd_f32(const GroupedArgs& g, cudaStream_t st, int* l
     p.seg[0].a = token_rows(a.dy, a.N, true, 1, 0);
     p.seg[0].b = of_expert(nullptr, a.K, false, a.N * a.K, a.K);
     p.seg[0].kdim = a.N;
-    p.seg[1].a = token_rows(U, a.r, true, 1, 0, true);
+    p.seg[1].a = token_rows(U, a.r, true, 1, 0);
     p.seg[1].b = of_expert(a.A, a.K, false, int64_t(a.r) * a.K, a.K);
     p.seg[1].kdim = a.r;
     p.cols = a.K;
-    p.c = a.dx;
+    p.c = static_cast<float*>(a.dx);
     ok = ok && add(l, &n, p, kKGroupedDx);
   }
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < n && e == cudaSuccess; ++i) e = run(g, l[i].p, l[i].ctas, l[i].id, st, launches);
+  for (int i = 0; i < n && e == cudaSuccess; ++i) e = run(l[i].p, l[i].ctas, l[i].id, st, launches);
   return e;
 }
 

@@ -17,6 +17,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// The first 1024-byte boundary of dynamic shared memory.  An offset added to the array
+// keeps its accesses shared-memory instructions; rounding the pointer as an integer
+// would make them generic ones, with 64-bit addresses.
+__device__ __forceinline__ uint8_t* align_1024(uint8_t* smem_raw) {
+  return smem_raw + ((0u - tc::smem_u32(smem_raw)) & 1023u);
+}
+
 // A try_wait that may suspend the thread for up to `hint_ns` before it answers:
 // waiting warps then take few issue slots from the working ones.
 __device__ __forceinline__ bool try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
