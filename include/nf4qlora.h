@@ -25,7 +25,8 @@
  *              default stream).  All work is enqueued on it; buffers must stay
  *              alive until it completes.  Nothing synchronizes except
  *              nf4_read_status.  Several kernels (quantize, double quant,
- *              dequantize, decode, the forward GEMM) are launched with
+ *              dequantize, decode, the forward GEMM, the expert and the 8-bit
+ *              GEMM, the expert decode) are launched with
  *              programmatic stream serialisation: each reads nothing that
  *              earlier work on the stream may still be writing (and writes
  *              nothing it may still be reading) before that work has
@@ -440,9 +441,10 @@ NF4_API nf4_status qlora_grouped_fwd(const nf4_weight* w, int num_experts, const
  * dA and dB are overwritten for every expert, with zeros for one without rows
  * (M == 0 included).  dx is written only in rows that belong to an expert.
  * `t` is the T of the forward's t_out, or NULL to recompute it.  With BF16 or
- * F16, dA is summed from U as two 16-bit terms (the rounded value and what the
- * rounding left), so it keeps U to 16 bits (BF16) or 22 (F16); dx uses the
- * rounded U.  Other arguments as qlora_grouped_fwd and qlora_linear_bwd.
+ * F16, dA is summed from U as three or two 16-bit terms (the rounded value, then
+ * what the roundings before left), which keep 24 of its bits (BF16) or 22 (F16);
+ * dx uses the rounded U.  Other arguments as qlora_grouped_fwd and
+ * qlora_linear_bwd.
  *   workspace      >= nf4_workspace_bytes(NF4_OP_GROUPED_BWD, M, N, K, r, 64, dq).
  */
 NF4_API nf4_status qlora_grouped_bwd(const nf4_weight* w, int num_experts, const void* x, int64_t M,
