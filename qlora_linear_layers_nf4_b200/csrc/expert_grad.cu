@@ -21,6 +21,10 @@
 // so what counts is how often it adds to a large one: the first terms of even and
 // odd steps have an accumulator each and the small terms a third, summed in fp32 at
 // the end (dA's error on 512 rows an expert: 2.0e-6 with one, 0.5e-6 with three).
+//
+// 4096 rows of 4 experts of 4096 x 4096, r 64: 33 us for 73 MB (DRAM 27 %, tensor
+// pipe 21 %); 64 experts of 1024 x 2048 with 4,001 uneven rows: 29 us.  Bound by the
+// steps' latency and by the CTAs that drew the longest tiles.
 #include <algorithm>
 
 #include <cuda.h>

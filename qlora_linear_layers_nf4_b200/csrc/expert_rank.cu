@@ -6,6 +6,9 @@
 // U is written as the terms that dA sums (see expert_grad.cu).  Even and odd steps
 // have an accumulator each: the tensor core truncates when it adds, and half as many
 // additions to smaller sums lose less.
+//
+// Bound by latency: T of 4096 rows, K 4096, r 64 reads 36 MB in 23.6 us (DRAM 18 %,
+// tensor pipe 8 %): setup, a few ring passes a slice, cluster reduction.
 #include <algorithm>
 
 #include <cuda.h>

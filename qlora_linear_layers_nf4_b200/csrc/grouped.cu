@@ -17,10 +17,15 @@ size_t mr_bytes(int64_t M, int r) { return (size_t(M) * size_t(r) * 4 + 255) / 2
 
 // Few rows per expert: stream the weights (16 rows a pass) instead of feeding
 // the GEMM, which spends the same time on one row of an expert as on 256.
+// Measured, this against the GEMM, us: 8 experts of 4096 x 4096 with 4, 16 and 24
+// rows on average 44, 63 and 84 against 68 to 69; 64 experts of 1024 x 2048 with
+// 16 and 24 rows 69 and 86 against 75.
 bool use_decode(int64_t M, int64_t E) { return M <= 16 * E; }
 
-// Rows x r up to which T takes one small CTA per element instead of the GEMM.
-constexpr int64_t kSmallT = 4096;
+// Rows x r up to which T takes one small CTA per element instead of the GEMM: whole
+// calls on 8 experts of 4096 x 4096, r = 64, with 16, 32 and 64 rows 40.5, 44.3 and
+// 54.5 us against 42.0, 44.6 and 51.2.
+constexpr int64_t kSmallT = 2048;
 
 }  // namespace
 

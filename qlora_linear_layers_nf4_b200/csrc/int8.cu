@@ -202,7 +202,7 @@ cudaError_t quantize_t(const void* x, int64_t rows, int64_t cols, int8_t* codes,
 
 // ------------------------------------------------------------------ linear, few tokens
 
-// y for up to eight tokens: the weight bytes are the whole cost, and one launch
+// y for up to four tokens: the weight bytes are the whole cost, and one launch
 // the largest other one, so the tokens are quantized here too.  A CTA holds the
 // codes of all tokens in shared memory (every CTA makes them again: 2 M K bytes
 // from L2 against a kernel of its own) and 32 weight rows, two to a warp, whose
@@ -349,10 +349,16 @@ cudaError_t small_tm(const Int8LinearArgs& a, const void* x, const float* scale,
 template <typename T>
 cudaError_t small_t(const Int8LinearArgs& a, const void* x, const float* scale, cudaStream_t st) {
   return a.M == 1 ? small_tm<T, 1>(a, x, scale, st) : a.M == 2 ? small_tm<T, 2>(a, x, scale, st)
-       : a.M <= 4 ? small_tm<T, 4>(a, x, scale, st) : small_tm<T, 8>(a, x, scale, st);
+                  : small_tm<T, 4>(a, x, scale, st);
 }
 
-bool use_small(const Int8LinearArgs& a) { return a.M <= 8 && a.M * a.K <= kSmMaxCodes; }
+// Its products cost dp4a's on every SM; the GEMM's cost nothing beside its fixed 8 to
+// 12 us.  Measured, this kernel against the GEMM, us: 4096 x 4096 with 1, 2, 4 and 8
+// tokens 4.9, 6.9, 9.5 and 16 against 12; 8192 x 4096 with 2 and 4 tokens 8.6 and 13.5
+// against 12.5; 11008 x 16384 with 1 and 2 tokens 37 and 42 against 39.
+bool use_small(const Int8LinearArgs& a) {
+  return a.M * a.K <= kSmMaxCodes && (a.M == 1 || (a.M <= 4 && a.M * a.N * a.K <= int64_t(100) << 20));
+}
 
 }  // namespace
 
