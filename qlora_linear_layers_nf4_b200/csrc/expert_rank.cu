@@ -37,6 +37,7 @@ using expert::unpack2;
 
 constexpr int kRkThreads = 256;    // A loads, B loads, MMA, TMEM; four epilogue warps
 constexpr int kRkStages = 4;
+constexpr int kRkMaxSlices = 8;    // CTAs of a cluster
 constexpr uint32_t kRkABytes = 128 * 128;
 
 struct RankShared {
@@ -85,16 +86,9 @@ __global__ void __launch_bounds__(kRkThreads, 1)
   if (p.zero != nullptr && blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < p.zero_n; i += kRkThreads) p.zero[i] = 0;
   if (warp == 0) build_groups(&sh->groups, p.offsets, p.E, p.M, 128, blockIdx.x == 0 && blockIdx.y == 0 ? p.status : nullptr);
-  __syncthreads();
-  if (int(blockIdx.x) >= sh->groups.tiles[p.E]) return;   // the whole cluster
-  const int e = expert_of_tile(&sh->groups, p.E, blockIdx.x);
-  const int row0 = sh->groups.start[e] + (blockIdx.x - sh->groups.tiles[e]) * 128;
-  const int row_end = sh->groups.start[e + 1];
-  const int per = (p.red_steps + p.slices - 1) / p.slices;
-  const int step0 = min(int(blockIdx.y) * per, p.red_steps);
-  const int nsteps = min(step0 + per, p.red_steps) - step0;
-
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32) {
+    tma_prefetch(&tm_a);
+    tma_prefetch(&tm_b);
     for (int s = 0; s < kRkStages; ++s) {
       mbar_init(&sh->full[s], 2);
       mbar_init(&sh->empty[s], 1);
@@ -112,6 +106,16 @@ __global__ void __launch_bounds__(kRkThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
+  if (int(blockIdx.x) >= sh->groups.tiles[p.E]) {   // the whole cluster
+    if (warp == 3) tmem_dealloc(tmem, uint32_t(p.tmem_cols));
+    return;
+  }
+  const int e = expert_of_tile(&sh->groups, p.E, blockIdx.x);
+  const int row0 = sh->groups.start[e] + (blockIdx.x - sh->groups.tiles[e]) * 128;
+  const int row_end = sh->groups.start[e + 1];
+  const int per = (p.red_steps + p.slices - 1) / p.slices;
+  const int step0 = min(int(blockIdx.y) * per, p.red_steps);
+  const int nsteps = min(step0 + per, p.red_steps) - step0;
 
   // Loads (warp 0 the A box, warp 1 the B boxes) and MMAs (warp 2) run as whole
   // warps with one elected lane; warps 4..7 are the epilogue.
@@ -230,13 +234,17 @@ __global__ void __launch_bounds__(kRkThreads, 1)
       const int cv = i % vec, rr = i / vec;
       const int trow = int(q) * rows_per + rr;
       const uint32_t off = uint32_t((trow * p.NP + 4 * (cv ^ (trow & 7))) * 4);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int sl = 0; sl < p.slices; ++sl) {
-        const float4 v = ld_shared_cluster_f4(mapa_shared(base + off, uint32_t(sl)));
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
+      float4 part[kRkMaxSlices], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int sl = 0; sl < kRkMaxSlices; ++sl)   // all on their way before the first is needed
+        if (sl < p.slices) part[sl] = ld_shared_cluster_f4(mapa_shared(base + off, uint32_t(sl)));
+#pragma unroll
+      for (int sl = 0; sl < kRkMaxSlices; ++sl) {
+        if (sl >= p.slices) break;
+        acc.x += part[sl].x;
+        acc.y += part[sl].y;
+        acc.z += part[sl].z;
+        acc.w += part[sl].w;
       }
       if (row0 + trow < row_end) rank_store4(p, row0 + trow, 4 * cv, acc);
     }
@@ -286,7 +294,7 @@ bool ExpertRank::prepare(const GroupedArgs& g, RankKind kind, void* out0, void* 
   const int64_t tiles = max_row_tiles(a.M, g.E, 128);
   if (tiles > int64_t(0x7fffffff)) return false;
   // one wave of about two CTAs per SM of a 148-SM part, four steps a slice at least
-  const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(296 / tiles, 8), p.red_steps / 4));
+  const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(296 / tiles, kRkMaxSlices), p.red_steps / 4));
   p.slices = 1;
   while (p.slices * 2 <= cap) p.slices *= 2;
   p.tmem_cols = 64;

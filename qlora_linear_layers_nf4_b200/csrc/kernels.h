@@ -118,7 +118,7 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, int sms, cudaStream_t stream,
 cudaError_t launch_linear_fwd_f32(const LinearArgs& a, cudaStream_t stream, int* launches);
 cudaError_t launch_linear_bwd_f32(const LinearArgs& a, cudaStream_t stream, int* launches);
 
-// ---- experts (grouped.cu, grouped_f32.cu) ----
+// ---- experts (grouped.cu and the files it launches) ----
 
 constexpr int kMaxExperts = 512;
 
