@@ -156,6 +156,11 @@ __global__ void __launch_bounds__(kSThreads) grouped_simt_kernel(const SimtParam
         load(sg.a, i0, a_end, kbeg + (s + 1) * kSK, kend, va);
         load(sg.b, j0, sg.b.extent, kbeg + (s + 1) * kSK, kend, vb);
       }
+      float sum[4][4];   // of the slice: short sums added to the long one lose less
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) sum[a][b] = 0.0f;
 #pragma unroll
       for (int kk = 0; kk < kSK; ++kk) {
         const float4 a4 = *reinterpret_cast<const float4*>(&sa[cur][kk * kSRow + 4 * ty]);
@@ -164,8 +169,12 @@ __global__ void __launch_bounds__(kSThreads) grouped_simt_kernel(const SimtParam
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
-          for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(ar[a], br[b], acc[a][b]);
+          for (int b = 0; b < 4; ++b) sum[a][b] = fmaf(ar[a], br[b], sum[a][b]);
       }
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[a][b] += sum[a][b];
     }
     __syncthreads();
   }
