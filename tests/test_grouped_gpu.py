@@ -323,6 +323,20 @@ def test_many_rows_an_expert(cuda_device, counts, r, dtype):
         assert all(torch.equal(a, b) for a, b in zip(again, (y, dA, dB, dx)))
 
 
+@pytest.mark.parametrize("n,k,r", [(2040, 64, 8), (64, 1984, 8), (8, 1984, 256), (2040, 64, 256)])
+def test_many_rows_of_short_sums(cuda_device, n, k, r):
+    """The same tiles where a tile has fewer steps than the ring has stages, or more adapter steps than others."""
+    import torch
+    g = Stack(cuda_device, [2600, 0, 3, 290], n, k, r, seed=14)
+    y, t = g.fwd()
+    g.check_fwd(y, t)
+    dA, dB, dx = g.bwd(t=t)
+    g.check_bwd(dA, dB, dx, t)
+    for _ in range(100):
+        again = g.fwd()[:1] + g.bwd(t=t)
+        assert all(torch.equal(a, b) for a, b in zip(again, (y, dA, dB, dx)))
+
+
 @pytest.mark.parametrize("counts", [[1, 0, 2], [80, 200, 3]])
 def test_one_expert_equals_the_dense_layer(cuda_device, counts):
     """Each expert's rows give what the dense layer gives on that expert's weight, to rounding."""
