@@ -51,7 +51,9 @@
  *   Workspace  Caller-allocated device scratch of at least
  *              nf4_workspace_bytes(...) bytes, zero-filled once before first
  *              use (the status word must start at 0).  Calls that share a
- *              workspace must be ordered on one stream.
+ *              workspace must be ordered on one stream, each call whole (it
+ *              enqueues several kernels): host threads that share one take
+ *              turns.
  */
 #ifndef NF4QLORA_H_
 #define NF4QLORA_H_

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -172,11 +173,23 @@ def workspace_bytes(op: int, M: int, N: int, K: int, r: int, block_size: int, do
 
 
 class Workspace:
-    """A zero-filled device byte buffer reused across calls (grown on demand)."""
+    """A zero-filled device byte buffer reused across calls (grown on demand).
+
+    The kernels of a call hand results to each other through it, so the calls
+    that share one have to be ordered on one stream.  `lock` is held while a call
+    enqueues: calls of several host threads then follow one another whole."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
+        self.lock = threading.Lock()
+
+    def __getstate__(self):
+        return {"device": self.device, "buf": self.buf}   # a copy has a lock of its own
+
+    def __setstate__(self, state):
+        self.__init__(state["device"])
+        self.buf = state["buf"]
 
     def get(self, nbytes: int):
         import torch
@@ -444,24 +457,32 @@ def _here(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _scratch(workspace: Workspace | None, device, stream: int, nbytes: int):
-    """Device scratch of a call on the current stream.
+def _scratch(workspace: Workspace | None, device, stream: int) -> Workspace:
+    """Workspace of a call on the current stream; its lock is held while the call enqueues.
 
     A given workspace is used as it is (calls that share one must be ordered).
-    Otherwise every stream has a buffer of its own, and while a CUDA graph is
-    being captured the call takes fresh memory of that graph's pool, so two
-    graphs, or a graph and eager calls, never share scratch."""
+    Otherwise every stream has one of its own, and while a CUDA graph is being
+    captured the call takes fresh memory of that graph's pool, so two graphs, or
+    a graph and eager calls, never share scratch."""
     import torch
     if workspace is not None:
-        return workspace.get(nbytes)
+        return workspace
     if torch._C._cuda_isCurrentStreamCapturing():
-        buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        buf[:256].zero_()   # the status word
-        return buf
+        return _CapturedScratch(device)
     ws = _stream_ws.get((device.index, stream))
     if ws is None:
-        ws = _stream_ws[device.index, stream] = Workspace(device)
-    return ws.get(nbytes)
+        ws = _stream_ws.setdefault((device.index, stream), Workspace(device))
+    return ws
+
+
+class _CapturedScratch(Workspace):
+    """Scratch of one captured call."""
+
+    def get(self, nbytes: int):
+        import torch
+        self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        self.buf[:256].zero_()   # the status word
+        return self.buf
 
 
 def _on_stream(call):
@@ -512,12 +533,13 @@ def grouped_fwd(q: QuantizedWeight, x, offsets, A, B, alpha: float, bias=None, w
     _fits("t_out", t_out, (M, r), x.dtype, dev)
     here = _here(dev)
     need = _workspace_size(OP_GROUPED_FWD, M, N, K, r)
-    buf = _scratch(workspace, dev, here, need)
+    ws = _scratch(workspace, dev, here)
     y = out if out is not None else torch.empty((M, N), dtype=x.dtype, device=dev)
     if want_t and t_out is None:
         t_out = torch.empty((M, r), dtype=x.dtype, device=dev)
-    st = lib().qlora_grouped_fwd(q.c_struct(), E, x.data_ptr(), M, offsets.data_ptr(), A.data_ptr(), B.data_ptr(), r,
-                                 alpha, dt, _at(bias), y.data_ptr(), _at(t_out), buf.data_ptr(), need, here)
+    with ws.lock:
+        st = lib().qlora_grouped_fwd(q.c_struct(), E, x.data_ptr(), M, offsets.data_ptr(), A.data_ptr(), B.data_ptr(), r,
+                                     alpha, dt, _at(bias), y.data_ptr(), _at(t_out), ws.get(need).data_ptr(), need, here)
     if st:
         raise NF4Error(st, "qlora_grouped_fwd")
     return y, t_out
@@ -542,14 +564,15 @@ def grouped_bwd(q: QuantizedWeight, x, offsets, A, B, alpha: float, dy, t=None, 
     _fits("dx", dx, (M, K), x.dtype, dev)
     here = _here(dev)
     need = _workspace_size(OP_GROUPED_BWD, M, N, K, r)
-    buf = _scratch(workspace, dev, here, need)
+    ws = _scratch(workspace, dev, here)
     dA = dA if dA is not None else torch.empty((E, r, K), dtype=torch.float32, device=dev)
     dB = dB if dB is not None else torch.empty((E, N, r), dtype=torch.float32, device=dev)
     if want_dx and dx is None:
         dx = torch.empty((M, K), dtype=x.dtype, device=dev)
-    st = lib().qlora_grouped_bwd(q.c_struct(), E, x.data_ptr(), M, offsets.data_ptr(), A.data_ptr(), B.data_ptr(), r,
-                                 alpha, dt, dy.data_ptr(), _at(t), dA.data_ptr(), dB.data_ptr(), _at(dx),
-                                 buf.data_ptr(), need, here)
+    with ws.lock:
+        st = lib().qlora_grouped_bwd(q.c_struct(), E, x.data_ptr(), M, offsets.data_ptr(), A.data_ptr(), B.data_ptr(), r,
+                                     alpha, dt, dy.data_ptr(), _at(t), dA.data_ptr(), dB.data_ptr(), _at(dx),
+                                     ws.get(need).data_ptr(), need, here)
     if st:
         raise NF4Error(st, "qlora_grouped_bwd")
     return dA, dB, dx
@@ -622,10 +645,11 @@ def int8_linear_fwd(w: Int8Matrix, x, bias=None, out_dtype=None, out=None,
     _fits("out", out, (M, N), y_dtype, dev)
     here = _here(dev)
     need = _workspace_size(OP_INT8_LINEAR, M, N, K, 0)
-    buf = _scratch(workspace, dev, here, need)
+    ws = _scratch(workspace, dev, here)
     y = out if out is not None else torch.empty((M, N), dtype=y_dtype, device=dev)
-    st = lib().int8_linear_fwd(w.codes.data_ptr(), w.scale.data_ptr(), N, K, xv.data_ptr(), _at(xs), M, dt, _at(bias),
-                               y.data_ptr(), buf.data_ptr(), need, here)
+    with ws.lock:
+        st = lib().int8_linear_fwd(w.codes.data_ptr(), w.scale.data_ptr(), N, K, xv.data_ptr(), _at(xs), M, dt, _at(bias),
+                                   y.data_ptr(), ws.get(need).data_ptr(), need, here)
     if st:
         raise NF4Error(st, "int8_linear_fwd")
     return y

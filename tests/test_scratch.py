@@ -1,0 +1,101 @@
+"""CPU checks of the binding's scratch: what calls from several host threads are handed.
+
+The library is replaced by one that records each call's workspace while the call runs; no GPU is touched.  A call
+enqueues several kernels that hand results to each other through its scratch, so two calls that enqueue at the same
+time must not hold the same memory, on one stream or on several."""
+import threading
+import time
+
+import pytest
+import torch
+
+from qlora_linear_layers_nf4_b200 import nf4qlora as Q
+
+E, N, K, R, M = 2, 64, 64, 8, 5
+
+
+class RecordingLibrary:
+    """Entry points that take a while; `shared` counts calls that ran while another held the same workspace."""
+
+    def __init__(self):
+        self.guard = threading.Lock()
+        self.active = []
+        self.shared = 0
+        self.calls = 0
+
+    def nf4_workspace_bytes(self, op, m, n, k, r, block_size, double_quant):
+        return 256 + 64 * m
+
+    def __getattr__(self, name):
+        at = {"qlora_grouped_fwd": -3, "qlora_grouped_bwd": -3, "int8_linear_fwd": -3}[name]
+
+        def call(*args):
+            ws = args[at]
+            with self.guard:
+                self.shared += ws in self.active
+                self.active.append(ws)
+                self.calls += 1
+            time.sleep(0.002)
+            with self.guard:
+                self.active.remove(ws)
+            return 0
+        return call
+
+
+@pytest.fixture
+def recorder(monkeypatch):
+    fake = RecordingLibrary()
+    stream = threading.local()
+    monkeypatch.setattr(Q, "lib", lambda: fake)
+    monkeypatch.setattr(Q, "_here", lambda device: getattr(stream, "handle", 0))
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False, raising=False)
+    monkeypatch.setattr(Q, "_sizes", {})
+    if hasattr(Q, "_stream_ws"):
+        monkeypatch.setattr(Q, "_stream_ws", {})
+    fake.stream = stream
+    return fake
+
+
+def _operands(m):
+    bf = torch.bfloat16
+    q = Q.QuantizedWeight(codes=torch.zeros(E * N * K // 2, dtype=torch.uint8), absmax=torch.zeros(E * N * K // 64),
+                          absmax_q=None, absmax_scale=None, rows=E * N, cols=K, block_size=64, double_quant=False)
+    off = torch.tensor([0, m // 2, m], dtype=torch.int32)
+    return (q, torch.zeros(m, K, dtype=bf), off, torch.zeros(E, R, K, dtype=bf), torch.zeros(E, N, R, dtype=bf), 16.0)
+
+
+def _calls(m, workspace=None):
+    args = _operands(m)
+    dy = torch.zeros(m, N, dtype=torch.bfloat16)
+    w8 = Q.Int8Matrix(torch.zeros(N, K, dtype=torch.int8), torch.ones(N))
+    return (lambda: Q.grouped_fwd(*args, workspace=workspace), lambda: Q.grouped_bwd(*args, dy, workspace=workspace),
+            lambda: Q.int8_linear_fwd(w8, args[1], workspace=workspace))
+
+
+def _run(fake, threads, handles, workspace=None):
+    def work(i):
+        fake.stream.handle = handles[i]
+        for _ in range(5):
+            for call in _calls(M * (i + 1), workspace):    # sizes differ, so scratch grows on the way
+                call()
+    pool = [threading.Thread(target=work, args=(i,)) for i in range(threads)]
+    for t in pool:
+        t.start()
+    for t in pool:
+        t.join()
+    assert fake.calls == threads * 15
+
+
+def test_threads_on_one_stream(recorder):
+    _run(recorder, 4, [0] * 4)
+    assert recorder.shared == 0
+
+
+def test_threads_with_one_workspace(recorder):
+    _run(recorder, 4, [0] * 4, Q.Workspace(torch.device("cpu")))
+    assert recorder.shared == 0
+
+
+def test_threads_on_their_own_streams(recorder):
+    _run(recorder, 4, [1, 2, 3, 4])
+    assert recorder.shared == 0
