@@ -1,4 +1,5 @@
-// Host side: TMA tensor maps of any rank up to 3 (expert and 8-bit GEMMs).
+// Host side: the driver's tensor map encoder, and TMA tensor maps of any rank up to 3
+// (expert and 8-bit GEMMs).
 #pragma once
 
 #include <cstdint>
@@ -7,6 +8,30 @@
 
 namespace nf4 {
 
+// cuTensorMapEncodeTiled.  It wants a current context, and a host thread that has
+// launched nothing yet has none: there the device's context is made current, as the
+// runtime does at a thread's first launch.
+inline CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, void* base,
+                             const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                             const cuuint32_t* elem_strides, CUtensorMapInterleave interleave,
+                             CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion, CUtensorMapFloatOOBfill fill) {
+  static const auto fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(p) : nullptr;
+  }();
+  if (fn == nullptr) return CUDA_ERROR_NOT_FOUND;
+  CUresult r = fn(map, type, rank, base, dims, strides, box, elem_strides, interleave, swizzle, promotion, fill);
+  if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+      r = fn(map, type, rank, base, dims, strides, box, elem_strides, interleave, swizzle, promotion, fill);
+  }
+  return r;
+}
+
 enum class MapElem { kU8, k16 };   // 1-byte or 2-byte elements
 
 // Row-major tensor of `rank` dims, innermost first; strides of dims 1 .. in
@@ -14,17 +39,6 @@ enum class MapElem { kU8, k16 };   // 1-byte or 2-byte elements
 // is zero.  False if it cannot be encoded.
 inline bool encode_map(CUtensorMap* map, const void* base, MapElem elem, int rank, const uint64_t* dims,
                        const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
-  using Fn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                          const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                          CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static const Fn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<Fn>(p) : nullptr;
-  }();
-  if (fn == nullptr) return false;
   cuuint64_t d[3], s[2];
   cuuint32_t b[3], one[3] = {1, 1, 1};
   for (int i = 0; i < rank; ++i) {
@@ -32,9 +46,9 @@ inline bool encode_map(CUtensorMap* map, const void* base, MapElem elem, int ran
     b[i] = box[i];
     if (i + 1 < rank) s[i] = strides[i];
   }
-  return fn(map, elem == MapElem::kU8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
-            cuuint32_t(rank), const_cast<void*>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(map, elem == MapElem::kU8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                      cuuint32_t(rank), const_cast<void*>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline bool encode_map_2d(CUtensorMap* map, const void* base, MapElem elem, uint64_t inner, uint64_t outer,
