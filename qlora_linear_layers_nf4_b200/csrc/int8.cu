@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kQThreads) int8_quantize_kernel(const T* __res
       for (int u = 0; u < V; ++u) top = max(top, __float_as_uint(f[u]) & 0x7fffffffu);
     }
   } else {
-    for (int at = t; at < cols; at += kQThreads)
+    // unsigned: the column after the last may lie past 2^31
+    for (uint32_t at = t; at < uint32_t(cols); at += kQThreads)
       top = max(top, __float_as_uint(Elem<T>::one(xr + at)) & 0x7fffffffu);
   }
   top = __reduce_max_sync(0xffffffffu, top);
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kQThreads) int8_quantize_kernel(const T* __res
     }
     for (int at = t + kQKeep * kQThreads; at < nvec; at += kQThreads) put(at, __ldg(xv + at));
   } else {
-    for (int at = t; at < cols; at += kQThreads) cr[at] = int8_t(int8_code(Elem<T>::one(xr + at), r));
+    for (uint32_t at = t; at < uint32_t(cols); at += kQThreads) cr[at] = int8_t(int8_code(Elem<T>::one(xr + at), r));
   }
 }
 
