@@ -284,6 +284,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
         }
       }
     }
+    // Without a tile too: what runs after this grid may count on the kernel before it
+    // being done (it may read the offsets still when no row belongs to an expert).
+    if (MODE != kI8 && !waited) grid_dep_wait();
     if (*abort_flag)   // unwind: wait (bounded) for the stages in flight
       for (int j = max(0, issued - kStages); j < issued; ++j) {
         uint32_t none = 0;
