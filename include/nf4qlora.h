@@ -444,8 +444,10 @@ NF4_API nf4_status qlora_grouped_fwd(const nf4_weight* w, int num_experts, const
  * (M == 0 included).  dx is written only in rows that belong to an expert.
  * `t` is the T of the forward's t_out, or NULL to recompute it.  With BF16 or
  * F16, dA is summed from U as three or two 16-bit terms (the rounded value, then
- * what the roundings before left), which keep 24 of its bits (BF16) or 22 (F16);
- * dx uses the rounded U.  Other arguments as qlora_grouped_fwd and
+ * what the roundings before left), which keep 24 of its bits (BF16) or 22 (F16,
+ * for |U| from 2^-14 to 65504; below, U is off by up to 2^-36, so gradients that
+ * small are scaled before the call).  dx uses the rounded U.  A U beyond the
+ * compute type's range counts as infinite in both.  Other arguments as qlora_grouped_fwd and
  * qlora_linear_bwd.
  *   workspace      >= nf4_workspace_bytes(NF4_OP_GROUPED_BWD, M, N, K, r, 64, dq).
  */

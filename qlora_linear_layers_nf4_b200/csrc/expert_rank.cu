@@ -50,7 +50,8 @@ struct RankShared {
 };
 
 // Four consecutive output columns of one row: T, or the terms of U (each what the
-// roundings before it left, f16's second one scaled).
+// roundings before it left, f16's second one scaled; nothing is left of an infinity,
+// whose difference to itself would be NaN).
 __device__ __forceinline__ void rank_store4(const RankParams& p, int row, int col, float4 v) {
   const bool f16 = p.f16 != 0;
   const int64_t at = int64_t(row) * p.r + col;
@@ -63,7 +64,7 @@ __device__ __forceinline__ void rank_store4(const RankParams& p, int row, int co
     const float2 a = unpack2(f16, w.x), b = unpack2(f16, w.y);
     const float rounded[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = (u[j] - rounded[j]) * p.lo_mul;
+    for (int j = 0; j < 4; ++j) u[j] = isfinite(rounded[j]) ? (u[j] - rounded[j]) * p.lo_mul : 0.0f;
   }
 }
 
