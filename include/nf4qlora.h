@@ -24,7 +24,7 @@
  *   Streams    `stream` is a cudaStream_t passed as void* (NULL = the legacy
  *              default stream).  All work is enqueued on it; buffers must stay
  *              alive until it completes.  Nothing synchronizes except
- *              nf4_read_status.  Several kernels (quantize, double quant,
+ *              nf4_read_status and nf4_read_device_status.  Several kernels (quantize, double quant,
  *              dequantize, decode, the forward GEMM, the expert and the 8-bit
  *              GEMM, the expert decode) are launched with
  *              programmatic stream serialisation: each reads nothing that
@@ -47,7 +47,8 @@
  *              Conditions only the GPU can see (non-finite input to quantize,
  *              an internal wait that exceeded its limit) are recorded in the
  *              status word at the head of `workspace` and returned by
- *              nf4_read_status.
+ *              nf4_read_status (or in one of the device's own, see
+ *              nf4_status_on_device).
  *   Workspace  Caller-allocated device scratch of at least
  *              nf4_workspace_bytes(...) bytes, zero-filled once before first
  *              use (the status word must start at 0).  Calls that share a
@@ -181,6 +182,18 @@ NF4_API size_t nf4_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int 
  * CUDA call gives NF4_ERR_CUDA.
  */
 NF4_API nf4_status nf4_read_status(void* workspace, void* stream);
+
+/*
+ * For callers whose workspace does not outlive the call, or whose status word
+ * nobody would read there (scratch that belongs to a captured graph):
+ * nf4_status_on_device(1) makes the calls that the calling host thread makes
+ * from then on record in a word that the library keeps on every device instead
+ * of in their workspace, nf4_status_on_device(0) ends that.  Calls captured
+ * meanwhile record there at every replay.  nf4_read_device_status does for that
+ * word of the current device what nf4_read_status does for a workspace's.
+ */
+NF4_API nf4_status nf4_status_on_device(int on);
+NF4_API nf4_status nf4_read_device_status(void* stream);
 
 /*
  * Blockwise NF4 quantization (qlora-rs quantize_nf4; capability matrix

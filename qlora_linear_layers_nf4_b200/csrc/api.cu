@@ -31,6 +31,35 @@ nf4_status finish(cudaError_t e, int launches) {
   return e == cudaSuccess ? NF4_OK : NF4_ERR_CUDA;
 }
 
+// The word that calls of a thread which asked for it record device-detected
+// conditions in, one on every device (zero when the library is loaded there).
+__device__ uint32_t g_device_status;
+thread_local bool t_status_on_device = false;
+
+cudaError_t device_status_word(uint32_t** out) {
+  void* p = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&p, g_device_status);
+  *out = static_cast<uint32_t*>(p);
+  return e;
+}
+
+// Where a call with this workspace records them.  False: a CUDA error.
+bool status_word(void* workspace, uint32_t** out) {
+  if (t_status_on_device) return device_status_word(out) == cudaSuccess;
+  *out = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + nf4::kWsStatus);
+  return true;
+}
+
+// Waits for the stream; returns the word and clears it.
+nf4_status read_word(uint32_t* dev, cudaStream_t st) {
+  uint32_t host = 0;
+  if (cudaMemcpyAsync(&host, dev, sizeof(host), cudaMemcpyDeviceToHost, st) != cudaSuccess)
+    return NF4_ERR_CUDA;
+  if (cudaMemsetAsync(dev, 0, sizeof(uint32_t), st) != cudaSuccess) return NF4_ERR_CUDA;
+  if (cudaStreamSynchronize(st) != cudaSuccess) return NF4_ERR_CUDA;
+  return static_cast<nf4_status>(host);
+}
+
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Quantize workspace: the header; with double quant also the per-CTA maxima of
@@ -197,7 +226,7 @@ const char* nf4_status_string(int status) {
   }
 }
 
-int nf4_version(void) { return 101; }
+int nf4_version(void) { return 102; }
 
 void nf4_codebook(float* levels, float* thresholds) {
   if (levels != nullptr)
@@ -225,14 +254,20 @@ size_t nf4_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int b
 
 nf4_status nf4_read_status(void* workspace, void* stream) {
   if (workspace == nullptr) return NF4_ERR_INVALID_ARG;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  uint32_t host = 0;
-  uint32_t* dev = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + nf4::kWsStatus);
-  if (cudaMemcpyAsync(&host, dev, sizeof(host), cudaMemcpyDeviceToHost, st) != cudaSuccess)
-    return NF4_ERR_CUDA;
-  if (cudaMemsetAsync(dev, 0, sizeof(uint32_t), st) != cudaSuccess) return NF4_ERR_CUDA;
-  if (cudaStreamSynchronize(st) != cudaSuccess) return NF4_ERR_CUDA;
-  return static_cast<nf4_status>(host);
+  return read_word(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + nf4::kWsStatus),
+                   static_cast<cudaStream_t>(stream));
+}
+
+nf4_status nf4_status_on_device(int on) {
+  if (on != 0 && on != 1) return NF4_ERR_INVALID_ARG;
+  t_status_on_device = on != 0;
+  return NF4_OK;
+}
+
+nf4_status nf4_read_device_status(void* stream) {
+  uint32_t* word = nullptr;
+  if (device_status_word(&word) != cudaSuccess) return NF4_ERR_CUDA;
+  return read_word(word, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
@@ -265,7 +300,8 @@ nf4_status quantize_impl(const void* w, int in_dtype, int64_t rows, int64_t cols
   if (ws_bytes < quantize_ws(numel, block_size, double_quant)) return NF4_ERR_WORKSPACE;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  uint32_t* status = reinterpret_cast<uint32_t*>(ws + nf4::kWsStatus);
+  uint32_t* status = nullptr;
+  if (!status_word(ws, &status)) return NF4_ERR_CUDA;
   float* max_slots = reinterpret_cast<float*>(ws + nf4::kWsHeader);
   const int sms = sm_count();
   int launches = 0;
@@ -384,7 +420,7 @@ nf4_status qlora_linear_fwd(const nf4_weight* w, const void* x, int64_t M, const
   a.t_out = t_out;
   a.ws = static_cast<uint8_t*>(workspace);
   a.ws_bytes = ws_bytes;
-  a.status = reinterpret_cast<uint32_t*>(a.ws + nf4::kWsStatus);
+  if (!status_word(a.ws, &a.status)) return NF4_ERR_CUDA;
   int launches = 0;
   cudaError_t e = a.f32 ? nf4::launch_linear_fwd_f32(a, static_cast<cudaStream_t>(stream), &launches)
                         : nf4::launch_linear_fwd(a, sm_count(), static_cast<cudaStream_t>(stream),
@@ -427,7 +463,7 @@ nf4_status qlora_linear_bwd(const nf4_weight* w, const void* x, int64_t M, const
   a.dx = dx;
   a.ws = static_cast<uint8_t*>(workspace);
   a.ws_bytes = ws_bytes;
-  a.status = reinterpret_cast<uint32_t*>(a.ws + nf4::kWsStatus);
+  if (!status_word(a.ws, &a.status)) return NF4_ERR_CUDA;
   int launches = 0;
   cudaError_t e = a.f32 ? nf4::launch_linear_bwd_f32(a, static_cast<cudaStream_t>(stream), &launches)
                         : nf4::launch_linear_bwd(a, sm_count(), static_cast<cudaStream_t>(stream),
@@ -472,7 +508,8 @@ nf4_status nf4_merge(const nf4_weight* w, const void* A, const void* B, int r, f
   if (workspace == nullptr || !aligned16(workspace)) return NF4_ERR_WORKSPACE;
   if (ws_bytes < nf4_workspace_bytes(NF4_OP_MERGE, 0, w->rows, w->cols, r, 64, w->double_quant))
     return NF4_ERR_WORKSPACE;
-  uint32_t* status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + nf4::kWsStatus);
+  uint32_t* status = nullptr;
+  if (!status_word(workspace, &status)) return NF4_ERR_CUDA;
   int launches = 0;
   const int kind = out_dtype == NF4_F32 ? nf4::kMergeF32 : (out_dtype == NF4_F16 ? nf4::kMergeF16 : nf4::kMergeBf16);
   const cudaError_t e = nf4::launch_merge(*w, A, B, r, alpha, kind, out,
@@ -521,7 +558,7 @@ nf4_status grouped_args(const nf4_weight* w, int num_experts, const void* x, int
   a.B = B;
   a.ws = static_cast<uint8_t*>(workspace);
   a.ws_bytes = ws_bytes;
-  a.status = reinterpret_cast<uint32_t*>(a.ws + nf4::kWsStatus);
+  if (!status_word(a.ws, &a.status)) return NF4_ERR_CUDA;
   return NF4_OK;
 }
 
@@ -622,7 +659,7 @@ nf4_status int8_linear_fwd(const int8_t* w_codes, const float* w_scale, int64_t 
   a.bias = bias;
   a.y = y;
   a.ws = static_cast<uint8_t*>(workspace);
-  a.status = reinterpret_cast<uint32_t*>(a.ws + nf4::kWsStatus);
+  if (!status_word(a.ws, &a.status)) return NF4_ERR_CUDA;
   int8_t* codes = reinterpret_cast<int8_t*>(a.ws + nf4::kWsHeader);
   float* scales = reinterpret_cast<float*>(codes + round_up(size_t(M) * size_t(K), 256));
   int launches = 0;

@@ -32,6 +32,7 @@ EXPORTED = (
     "nf4_dequantize", "qlora_linear_fwd", "qlora_linear_bwd", "nf4_quantize_noalloc",
     "nf4_merge", "nf4_quantize_typed", "nf4_check_wait_timeout", "nf4_absmax_max",
     "nf4_double_quant", "qlora_grouped_fwd", "qlora_grouped_bwd", "int8_quantize", "int8_linear_fwd",
+    "nf4_status_on_device", "nf4_read_device_status",
 )
 
 
@@ -119,6 +120,10 @@ def lib() -> ctypes.CDLL:
     L.int8_quantize.restype = i32
     L.int8_linear_fwd.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, sz, vp]
     L.int8_linear_fwd.restype = i32
+    L.nf4_status_on_device.argtypes = [i32]
+    L.nf4_status_on_device.restype = i32
+    L.nf4_read_device_status.argtypes = [vp]
+    L.nf4_read_device_status.restype = i32
     _lib = L
     return L
 
@@ -177,7 +182,9 @@ class Workspace:
 
     The kernels of a call hand results to each other through it, so the calls
     that share one have to be ordered on one stream.  `lock` is held while a call
-    enqueues: calls of several host threads then follow one another whole."""
+    enqueues: calls of several host threads then follow one another whole.
+    Growing replaces the buffer, so one that captured calls use has to have its
+    largest size (`get`) before the capture and as long as the graph lives."""
 
     def __init__(self, device=None):
         self.device = device
@@ -196,7 +203,9 @@ class Workspace:
         nbytes = max(int(nbytes), 256)
         if self.buf is None or self.buf.numel() < nbytes:
             dev = self.device if self.device is not None else torch.device("cuda", torch.cuda.current_device())
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+            old, self.buf = self.buf, torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+            if old is not None and not (old.is_cuda and torch.cuda.is_current_stream_capturing()):
+                self.buf[:256].copy_(old[:256])   # the status that earlier calls recorded (a graph would copy it at every replay)
         return self.buf
 
     def read_status(self, stream=None) -> int:
@@ -457,13 +466,14 @@ def _here(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _scratch(workspace: Workspace | None, device, stream: int) -> Workspace:
+def _scratch(workspace: Workspace | None, device, stream: int):
     """Workspace of a call on the current stream; its lock is held while the call enqueues.
 
     A given workspace is used as it is (calls that share one must be ordered).
     Otherwise every stream has one of its own, and while a CUDA graph is being
     captured the call takes fresh memory of that graph's pool, so two graphs, or
-    a graph and eager calls, never share scratch."""
+    a graph and eager calls, never share scratch.  read_status reads what calls
+    without a workspace recorded."""
     import torch
     if workspace is not None:
         return workspace
@@ -475,14 +485,41 @@ def _scratch(workspace: Workspace | None, device, stream: int) -> Workspace:
     return ws
 
 
-class _CapturedScratch(Workspace):
-    """Scratch of one captured call."""
+class _StatusOnDevice:
+    """While entered, this thread's calls record in the device's status word."""
+
+    def __enter__(self):
+        lib().nf4_status_on_device(1)
+
+    def __exit__(self, *exc):
+        lib().nf4_status_on_device(0)
+
+
+class _CapturedScratch:
+    """Scratch of one captured call (nobody else's, so its lock locks nothing)."""
+
+    def __init__(self, device):
+        self.device = device
+        self.lock = _StatusOnDevice()
 
     def get(self, nbytes: int):
         import torch
-        self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
-        self.buf[:256].zero_()   # the status word
+        self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         return self.buf
+
+
+def read_status(stream=None) -> int:
+    """What the GPU found in the expert and 8-bit calls made without a workspace,
+    since the last reading: the eager calls of `stream` (a torch stream; the
+    current one unless given) and the replays of all captured calls on its
+    device.  NF4_OK, or the first code recorded (NF4_ERR_INVALID_ARG for offsets
+    out of order or range).  Waits for the stream."""
+    import torch
+    s = torch.cuda.current_stream() if stream is None else stream
+    with torch.cuda.stream(s):
+        captured = int(lib().nf4_read_device_status(s.cuda_stream))
+        ws = _stream_ws.get((s.device.index, s.cuda_stream))
+        return (NF4_OK if ws is None else ws.read_status(s)) or captured
 
 
 def _on_stream(call):

@@ -99,3 +99,23 @@ def test_threads_with_one_workspace(recorder):
 def test_threads_on_their_own_streams(recorder):
     _run(recorder, 4, [1, 2, 3, 4])
     assert recorder.shared == 0
+
+
+def test_growing_keeps_the_status():
+    ws = Q.Workspace(torch.device("cpu"))
+    ws.get(256)[0] = 8
+    grown = ws.get(5000)
+    assert grown.numel() == 5000 and grown[0] == 8 and not grown[1:].any()
+
+
+def test_workspace_copies_have_their_own_lock():
+    import copy
+    ws = Q.Workspace(torch.device("cpu"))
+    ws.get(300)[5] = 1
+    other = copy.deepcopy(ws)
+    assert other.lock is not ws.lock and torch.equal(other.buf, ws.buf) and other.buf is not ws.buf
+
+
+def test_status_on_device_refuses():
+    assert Q.lib().nf4_status_on_device(2) == 1 and Q.lib().nf4_status_on_device(-1) == 1
+    assert Q.lib().nf4_status_on_device(0) == 0
