@@ -218,10 +218,11 @@ _default_ws = {}
 
 
 def default_workspace(device) -> Workspace:
+    """The device's workspace of dense calls without one.  Calls on several streams
+    at once need workspaces of their own."""
     key = str(device)
-    if key not in _default_ws:
-        _default_ws[key] = Workspace(device)
-    return _default_ws[key]
+    ws = _default_ws.get(key)
+    return ws if ws is not None else _default_ws.setdefault(key, Workspace(device))
 
 
 @dataclass
@@ -272,15 +273,16 @@ def quantize(w, block_size: int = 64, double_quant: bool = False, keep_absmax: b
     absmax_q = torch.empty(max(nblocks, 1), dtype=torch.uint8, device=dev) if double_quant else None
     absmax_scale = torch.empty(1, dtype=torch.float32, device=dev) if double_quant else None
     ws = workspace or default_workspace(dev)
-    buf = ws.get(workspace_bytes(OP_QUANTIZE, 0, rows, cols, 0, block_size, double_quant))
-    if in_dtype == NF4_F32:
-        st = lib().nf4_quantize(_ptr(w), rows, cols, block_size, int(double_quant), _ptr(codes),
-                                _ptr(absmax), _ptr(absmax_q), _ptr(absmax_scale), _ptr(buf),
-                                buf.numel(), _stream(stream))
-    else:
-        st = lib().nf4_quantize_typed(_ptr(w), in_dtype, rows, cols, block_size, int(double_quant),
-                                      _ptr(codes), _ptr(absmax), _ptr(absmax_q), _ptr(absmax_scale),
-                                      _ptr(buf), buf.numel(), _stream(stream))
+    with ws.lock:
+        buf = ws.get(workspace_bytes(OP_QUANTIZE, 0, rows, cols, 0, block_size, double_quant))
+        if in_dtype == NF4_F32:
+            st = lib().nf4_quantize(_ptr(w), rows, cols, block_size, int(double_quant), _ptr(codes),
+                                    _ptr(absmax), _ptr(absmax_q), _ptr(absmax_scale), _ptr(buf),
+                                    buf.numel(), _stream(stream))
+        else:
+            st = lib().nf4_quantize_typed(_ptr(w), in_dtype, rows, cols, block_size, int(double_quant),
+                                          _ptr(codes), _ptr(absmax), _ptr(absmax_q), _ptr(absmax_scale),
+                                          _ptr(buf), buf.numel(), _stream(stream))
     _check(st, "nf4_quantize")
     if check_status:
         _check(ws.read_status(stream), "nf4_quantize (device)")
@@ -334,10 +336,11 @@ def merge(q: QuantizedWeight, A, B, alpha: float, out_dtype: str = "bf16", out=N
         out = torch.empty((q.rows, q.cols), dtype=dt[1], device=q.device)
     ws = workspace if workspace is not None else Workspace(q.device)
     need = lib().nf4_workspace_bytes(OP_MERGE, 0, q.rows, q.cols, r, q.block_size, int(q.double_quant))
-    buf = ws.get(need)
     cw = q.c_struct()
-    _check(lib().nf4_merge(ctypes.byref(cw), _ptr(A), _ptr(B), r, float(alpha), dt[0], _ptr(out),
-                           _ptr(buf), buf.numel(), _stream(stream)), "nf4_merge")
+    with ws.lock:
+        buf = ws.get(need)
+        _check(lib().nf4_merge(ctypes.byref(cw), _ptr(A), _ptr(B), r, float(alpha), dt[0], _ptr(out),
+                               _ptr(buf), buf.numel(), _stream(stream)), "nf4_merge")
     return out
 
 
@@ -395,11 +398,12 @@ def linear_fwd(q: QuantizedWeight, x, A, B, alpha: float, bias=None, want_t: boo
     if want_t and t_out is None:
         t_out = torch.empty((M, r), dtype=x.dtype, device=x.device)
     ws = workspace or default_workspace(x.device)
-    buf = ws.get(workspace_bytes(OP_LINEAR_FWD, M, q.rows, q.cols, r, q.block_size, q.double_quant))
     cw = q.c_struct()
-    st = lib().qlora_linear_fwd(ctypes.byref(cw), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha),
-                                dt, _ptr(bias), _ptr(y), _ptr(t_out), _ptr(buf), buf.numel(),
-                                _stream(stream))
+    with ws.lock:
+        buf = ws.get(workspace_bytes(OP_LINEAR_FWD, M, q.rows, q.cols, r, q.block_size, q.double_quant))
+        st = lib().qlora_linear_fwd(ctypes.byref(cw), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha),
+                                    dt, _ptr(bias), _ptr(y), _ptr(t_out), _ptr(buf), buf.numel(),
+                                    _stream(stream))
     _check(st, "qlora_linear_fwd")
     return y, t_out
 
@@ -424,11 +428,12 @@ def linear_bwd(q: QuantizedWeight, x, A, B, alpha: float, dy, t=None, want_dx: b
     if want_dx and dx is None:
         dx = torch.empty((M, q.cols), dtype=x.dtype, device=x.device)
     ws = workspace or default_workspace(x.device)
-    buf = ws.get(workspace_bytes(OP_LINEAR_BWD, M, q.rows, q.cols, r, q.block_size, q.double_quant))
     cw = q.c_struct()
-    st = lib().qlora_linear_bwd(ctypes.byref(cw), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha),
-                                dt, _ptr(dy), _ptr(t), _ptr(dA), _ptr(dB), _ptr(dx),
-                                _ptr(buf), buf.numel(), _stream(stream))
+    with ws.lock:
+        buf = ws.get(workspace_bytes(OP_LINEAR_BWD, M, q.rows, q.cols, r, q.block_size, q.double_quant))
+        st = lib().qlora_linear_bwd(ctypes.byref(cw), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha),
+                                    dt, _ptr(dy), _ptr(t), _ptr(dA), _ptr(dB), _ptr(dx),
+                                    _ptr(buf), buf.numel(), _stream(stream))
     _check(st, "qlora_linear_bwd")
     return dA, dB, dx
 

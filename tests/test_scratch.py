@@ -27,10 +27,12 @@ class RecordingLibrary:
         return 256 + 64 * m
 
     def __getattr__(self, name):
-        at = {"qlora_grouped_fwd": -3, "qlora_grouped_bwd": -3, "int8_linear_fwd": -3}[name]
+        if name not in ("qlora_grouped_fwd", "qlora_grouped_bwd", "int8_linear_fwd", "qlora_linear_fwd", "qlora_linear_bwd",
+                        "nf4_quantize"):
+            raise AttributeError(name)
 
         def call(*args):
-            ws = args[at]
+            ws = getattr(args[-3], "value", args[-3])
             with self.guard:
                 self.shared += ws in self.active
                 self.active.append(ws)
@@ -119,3 +121,29 @@ def test_workspace_copies_have_their_own_lock():
 def test_status_on_device_refuses():
     assert Q.lib().nf4_status_on_device(2) == 1 and Q.lib().nf4_status_on_device(-1) == 1
     assert Q.lib().nf4_status_on_device(0) == 0
+
+
+@pytest.mark.parametrize("own_workspace", [False, True])
+def test_threads_in_the_dense_calls(recorder, monkeypatch, own_workspace):
+    """quantize, linear_fwd and linear_bwd on one stream, as above."""
+    monkeypatch.setattr(Q, "_stream", lambda stream=None: 0)
+    monkeypatch.setattr(Q, "_default_ws", {})
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)   # quantize takes CUDA tensors only
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    ws = Q.Workspace(torch.device("cpu")) if own_workspace else None
+
+    def work(i):
+        bf, m = torch.bfloat16, M * (i + 1)
+        q = Q.QuantizedWeight(codes=torch.zeros(N * K // 2, dtype=torch.uint8), absmax=torch.zeros(N * K // 64),
+                              absmax_q=None, absmax_scale=None, rows=N, cols=K, block_size=64, double_quant=False)
+        x, A, B, dy = (torch.zeros(s, dtype=bf) for s in ((m, K), (R, K), (N, R), (m, N)))
+        for _ in range(5):
+            Q.linear_fwd(q, x, A, B, 16.0, workspace=ws)
+            Q.linear_bwd(q, x, A, B, 16.0, dy, workspace=ws)
+            Q.quantize(torch.zeros(m, 64), 64, True, workspace=ws)
+    pool = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in pool:
+        t.start()
+    for t in pool:
+        t.join()
+    assert recorder.calls == 60 and recorder.shared == 0

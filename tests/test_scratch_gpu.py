@@ -50,3 +50,17 @@ def test_threads_on_one_stream(cuda_device, own_workspace):
     jobs += [lambda g=g: g.bwd(workspace=ws) for g in (few, many)]
     jobs += [lambda x=x: (Q.int8_linear_fwd(w8, x, workspace=ws),) for x in x8]
     _together(jobs, 25)
+
+
+def test_dense_calls_of_threads_on_one_stream(cuda_device):
+    """The dense layer's calls, which share the device's default workspace."""
+    import torch
+    Q = _Q()
+    g = Stack(cuda_device, [150, 70], 264, 320, 16, dq=False, seed=2)
+    q = Q.QuantizedWeight(g.q.codes[:264 * 160], g.q.absmax[:264 * 5], None, None, 264, 320, 64, False)
+    x, dy, A, B = g.x, g.dy, g.A[0], g.B[0]
+    w = torch.randn(264, 320, device=cuda_device)
+    jobs = [lambda m=m: Q.linear_fwd(q, x[:m], A, B, 32.0, want_t=False)[:1] for m in (4, 100, 220)]
+    jobs += [lambda m=m: Q.linear_bwd(q, x[:m], A, B, 32.0, dy[:m]) for m in (40, 220)]
+    jobs += [lambda m=m: (lambda r: (r.codes, r.absmax_q, r.absmax_scale))(Q.quantize(w[:m], 64, True)) for m in (30, 264)]
+    _together(jobs, 25)
