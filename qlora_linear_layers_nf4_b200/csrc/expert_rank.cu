@@ -263,7 +263,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-bool ExpertRank::prepare(const GroupedArgs& g, RankKind kind, void* out0, void* out1, void* out2) {
+bool ExpertRank::prepare(const GroupedArgs& g, RankKind kind, void* out0, void* out1, void* out2, int sms) {
   const LinearArgs& a = g.lin;
   const uint64_t M = uint64_t(a.M), N = uint64_t(a.N), K = uint64_t(a.K), E = uint64_t(g.E), r = uint64_t(a.r);
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -294,8 +294,8 @@ bool ExpertRank::prepare(const GroupedArgs& g, RankKind kind, void* out0, void* 
   if (!ok) return false;
   const int64_t tiles = max_row_tiles(a.M, g.E, 128);
   if (tiles > int64_t(0x7fffffff)) return false;
-  // one wave of about two CTAs per SM of a 148-SM part, four steps a slice at least
-  const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(296 / tiles, kRkMaxSlices), p.red_steps / 4));
+  // one wave of about two CTAs per SM, four steps a slice at least
+  const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(2 * sms / tiles, kRkMaxSlices), p.red_steps / 4));
   p.slices = 1;
   while (p.slices * 2 <= cap) p.slices *= 2;
   p.tmem_cols = 64;

@@ -31,7 +31,7 @@ struct ExpertRank {
   RankParams p;
   dim3 grid;
   size_t smem = 0;
-  bool prepare(const GroupedArgs& g, RankKind kind, void* out0, void* out1, void* out2);
+  bool prepare(const GroupedArgs& g, RankKind kind, void* out0, void* out1, void* out2, int sms);
   cudaError_t run(cudaStream_t st, int* launches) const;
 };
 

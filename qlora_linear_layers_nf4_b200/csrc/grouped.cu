@@ -46,7 +46,7 @@ cudaError_t launch_grouped_fwd(const GroupedArgs& g, int sms, cudaStream_t st, i
   if (use_decode(a.M, g.E) && d.prepare(g, T, a.ws + kWsHeader + mr_bytes(a.M, a.r), sms)) {
     ExpertRank t;
     const bool small = a.M * a.r <= kSmallT;
-    if (!small && !t.prepare(g, kRankT, T, nullptr, nullptr)) return cudaErrorInvalidValue;
+    if (!small && !t.prepare(g, kRankT, T, nullptr, nullptr, sms)) return cudaErrorInvalidValue;
     if (small) {
       e = launch_expert_t_small(g, T, d.p.counters, st, launches);
     } else {
@@ -58,7 +58,7 @@ cudaError_t launch_grouped_fwd(const GroupedArgs& g, int sms, cudaStream_t st, i
   }
   ExpertRank t;
   ExpertGemm y;
-  if (!t.prepare(g, kRankT, T, nullptr, nullptr) || !y.prepare(g, false, T, sms)) return cudaErrorInvalidValue;
+  if (!t.prepare(g, kRankT, T, nullptr, nullptr, sms) || !y.prepare(g, false, T, sms)) return cudaErrorInvalidValue;
   e = t.run(st, launches);
   if (e == cudaSuccess) e = y.run(st, launches);
   return e;
@@ -74,8 +74,8 @@ cudaError_t launch_grouped_bwd(const GroupedArgs& g, int sms, cudaStream_t st, i
   ExpertRank t, u;
   ExpertGrad grad;
   ExpertGemm dx;
-  bool ok = a.t_in != nullptr || t.prepare(g, kRankT, ws, nullptr, nullptr);
-  ok = ok && u.prepare(g, kRankU, U[0], U[1], U[2]);
+  bool ok = a.t_in != nullptr || t.prepare(g, kRankT, ws, nullptr, nullptr, sms);
+  ok = ok && u.prepare(g, kRankU, U[0], U[1], U[2], sms);
   ok = ok && grad.prepare(g, T, U[0], a.f16 ? 2 : 3, sms);
   ok = ok && (a.dx == nullptr || dx.prepare(g, true, U[0], sms));
   if (!ok) return cudaErrorInvalidValue;
