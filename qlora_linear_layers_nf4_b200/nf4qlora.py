@@ -198,7 +198,8 @@ class Workspace:
         self.__init__(state["device"])
         self.buf = state["buf"]
 
-    def get(self, nbytes: int):
+    def get(self, nbytes: int, device=None):
+        """The buffer, of at least nbytes; with `device`, refused if it is elsewhere."""
         import torch
         nbytes = max(int(nbytes), 256)
         if self.buf is None or self.buf.numel() < nbytes:
@@ -206,6 +207,8 @@ class Workspace:
             old, self.buf = self.buf, torch.zeros(nbytes, dtype=torch.uint8, device=dev)
             if old is not None and not (old.is_cuda and torch.cuda.is_current_stream_capturing()):
                 self.buf[:256].copy_(old[:256])   # the status that earlier calls recorded (a graph would copy it at every replay)
+        if device is not None and self.buf.device != device:
+            raise ValueError(f"workspace is on {self.buf.device}, the weight on {device}")
         return self.buf
 
     def read_status(self, stream=None) -> int:
@@ -274,7 +277,7 @@ def quantize(w, block_size: int = 64, double_quant: bool = False, keep_absmax: b
     absmax_scale = torch.empty(1, dtype=torch.float32, device=dev) if double_quant else None
     ws = workspace or default_workspace(dev)
     with ws.lock:
-        buf = ws.get(workspace_bytes(OP_QUANTIZE, 0, rows, cols, 0, block_size, double_quant))
+        buf = ws.get(workspace_bytes(OP_QUANTIZE, 0, rows, cols, 0, block_size, double_quant), dev)
         if in_dtype == NF4_F32:
             st = lib().nf4_quantize(_ptr(w), rows, cols, block_size, int(double_quant), _ptr(codes),
                                     _ptr(absmax), _ptr(absmax_q), _ptr(absmax_scale), _ptr(buf),
@@ -338,7 +341,7 @@ def merge(q: QuantizedWeight, A, B, alpha: float, out_dtype: str = "bf16", out=N
     need = lib().nf4_workspace_bytes(OP_MERGE, 0, q.rows, q.cols, r, q.block_size, int(q.double_quant))
     cw = q.c_struct()
     with ws.lock:
-        buf = ws.get(need)
+        buf = ws.get(need, dev)
         _check(lib().nf4_merge(ctypes.byref(cw), _ptr(A), _ptr(B), r, float(alpha), dt[0], _ptr(out),
                                _ptr(buf), buf.numel(), _stream(stream)), "nf4_merge")
     return out
@@ -400,7 +403,7 @@ def linear_fwd(q: QuantizedWeight, x, A, B, alpha: float, bias=None, want_t: boo
     ws = workspace or default_workspace(x.device)
     cw = q.c_struct()
     with ws.lock:
-        buf = ws.get(workspace_bytes(OP_LINEAR_FWD, M, q.rows, q.cols, r, q.block_size, q.double_quant))
+        buf = ws.get(workspace_bytes(OP_LINEAR_FWD, M, q.rows, q.cols, r, q.block_size, q.double_quant), dev)
         st = lib().qlora_linear_fwd(ctypes.byref(cw), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha),
                                     dt, _ptr(bias), _ptr(y), _ptr(t_out), _ptr(buf), buf.numel(),
                                     _stream(stream))
@@ -430,7 +433,7 @@ def linear_bwd(q: QuantizedWeight, x, A, B, alpha: float, dy, t=None, want_dx: b
     ws = workspace or default_workspace(x.device)
     cw = q.c_struct()
     with ws.lock:
-        buf = ws.get(workspace_bytes(OP_LINEAR_BWD, M, q.rows, q.cols, r, q.block_size, q.double_quant))
+        buf = ws.get(workspace_bytes(OP_LINEAR_BWD, M, q.rows, q.cols, r, q.block_size, q.double_quant), dev)
         st = lib().qlora_linear_bwd(ctypes.byref(cw), _ptr(x), M, _ptr(A), _ptr(B), r, float(alpha),
                                     dt, _ptr(dy), _ptr(t), _ptr(dA), _ptr(dB), _ptr(dx),
                                     _ptr(buf), buf.numel(), _stream(stream))
@@ -507,7 +510,7 @@ class _CapturedScratch:
         self.device = device
         self.lock = _StatusOnDevice()
 
-    def get(self, nbytes: int):
+    def get(self, nbytes: int, device=None):
         import torch
         self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         return self.buf
@@ -581,7 +584,7 @@ def grouped_fwd(q: QuantizedWeight, x, offsets, A, B, alpha: float, bias=None, w
         t_out = torch.empty((M, r), dtype=x.dtype, device=dev)
     with ws.lock:
         st = lib().qlora_grouped_fwd(q.c_struct(), E, x.data_ptr(), M, offsets.data_ptr(), A.data_ptr(), B.data_ptr(), r,
-                                     alpha, dt, _at(bias), y.data_ptr(), _at(t_out), ws.get(need).data_ptr(), need, here)
+                                     alpha, dt, _at(bias), y.data_ptr(), _at(t_out), ws.get(need, dev).data_ptr(), need, here)
     if st:
         raise NF4Error(st, "qlora_grouped_fwd")
     return y, t_out
@@ -614,7 +617,7 @@ def grouped_bwd(q: QuantizedWeight, x, offsets, A, B, alpha: float, dy, t=None, 
     with ws.lock:
         st = lib().qlora_grouped_bwd(q.c_struct(), E, x.data_ptr(), M, offsets.data_ptr(), A.data_ptr(), B.data_ptr(), r,
                                      alpha, dt, dy.data_ptr(), _at(t), dA.data_ptr(), dB.data_ptr(), _at(dx),
-                                     ws.get(need).data_ptr(), need, here)
+                                     ws.get(need, dev).data_ptr(), need, here)
     if st:
         raise NF4Error(st, "qlora_grouped_bwd")
     return dA, dB, dx
@@ -691,7 +694,7 @@ def int8_linear_fwd(w: Int8Matrix, x, bias=None, out_dtype=None, out=None,
     y = out if out is not None else torch.empty((M, N), dtype=y_dtype, device=dev)
     with ws.lock:
         st = lib().int8_linear_fwd(w.codes.data_ptr(), w.scale.data_ptr(), N, K, xv.data_ptr(), _at(xs), M, dt, _at(bias),
-                                   y.data_ptr(), ws.get(need).data_ptr(), need, here)
+                                   y.data_ptr(), ws.get(need, dev).data_ptr(), need, here)
     if st:
         raise NF4Error(st, "int8_linear_fwd")
     return y

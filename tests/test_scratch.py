@@ -147,3 +147,12 @@ def test_threads_in_the_dense_calls(recorder, monkeypatch, own_workspace):
     for t in pool:
         t.join()
     assert recorder.calls == 60 and recorder.shared == 0
+
+
+def test_workspace_of_another_device_is_refused(recorder):
+    """A pointer of another device, or of the host, would reach the kernels unseen."""
+    elsewhere = Q.Workspace(torch.device("meta"))
+    for call in _calls(M, elsewhere):
+        with pytest.raises(ValueError, match="workspace"):
+            call()
+    assert recorder.calls == 0
