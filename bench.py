@@ -42,8 +42,8 @@ FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustain
 # the hash of the kernel source it was taken on; reported as null once the
 # source changes.
 NCU_TRAFFIC = {
-    # forward 127.4 MB, dx 181.0 MB per launch
-    "0afa7f14ba671346": {"fwd": 72_147_712 + 55_230_976, "dx": 162_442_240 + 18_569_984},
+    # forward 124.4 MB, dx 178.1 MB per launch
+    "75df1629cf21e231": {"fwd": 70_136_576 + 54_258_432, "dx": 159_048_448 + 19_063_808},
 }
 
 
