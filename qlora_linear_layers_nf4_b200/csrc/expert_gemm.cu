@@ -119,18 +119,18 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// Arrive on a barrier of the pair's leader.  What it announces is not plain data
-// of this thread's generic proxy: operand tiles that fence.proxy.async has handed
-// to the async proxy of this SM (whose tensor core reads them), or accumulators
-// whose reads tcgen05.wait has completed.  The release has CTA scope, though the
-// waiter may be in the other CTA: that the writes to this SM's own shared memory
-// are done when the arrival is seen there is a property of the hardware that is
-// relied on here; the memory model promises it at cluster scope only.  There the
-// arrival waits for every store in flight, the epilogue's output included: y of
-// 8192 rows on 8 experts of 11008 x 4096 takes 894 us instead of 719 (871 with the
-// operand tiles' arrivals alone, 743 with the accumulators').
+// Arrive on a barrier of the pair's leader, releasing at cluster scope: the waiter
+// may be in the other CTA.  What the arrival announces are operand tiles in this
+// CTA's shared memory, which fence.proxy.async has handed to the async proxy, or
+// accumulators whose reads tcgen05.wait has completed.  So the release is restricted
+// to this CTA's shared memory; a full one waits for every store in flight, the
+// epilogue's output included (y of 8192 rows on 8 experts of 11008 x 4096: 894 us
+// against 715).
 __device__ __forceinline__ void arrive_leader(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+      : "memory");
 }
 
 struct Tile {

@@ -520,8 +520,9 @@ def read_status(stream=None) -> int:
     """What the GPU found in the expert and 8-bit calls made without a workspace,
     since the last reading: the eager calls of `stream` (a torch stream; the
     current one unless given) and the replays of all captured calls on its
-    device.  NF4_OK, or the first code recorded (NF4_ERR_INVALID_ARG for offsets
-    out of order or range).  Waits for the stream."""
+    device, as far as they have run.  NF4_OK, or the first code recorded
+    (NF4_ERR_INVALID_ARG for offsets out of order or range).  Waits for the
+    stream."""
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
     with torch.cuda.stream(s):
