@@ -94,8 +94,15 @@ typedef enum {
   NF4_OP_MERGE = 4,
   NF4_OP_GROUPED_FWD = 5,
   NF4_OP_GROUPED_BWD = 6,
-  NF4_OP_INT8_LINEAR = 7
+  NF4_OP_INT8_LINEAR = 7,
+  NF4_OP_GATED_FWD = 8,      /* compute types BF16 and F16 */
+  NF4_OP_GATED_BWD = 9,
+  NF4_OP_GATED_FWD_F32 = 10, /* compute type F32 */
+  NF4_OP_GATED_BWD_F32 = 11
 } nf4_op;
+
+/* The gate's activation: x / (1 + exp(-x)), and 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))). */
+typedef enum { NF4_ACT_SILU = 0, NF4_ACT_GELU_TANH = 1 } nf4_activation;
 
 /*
  * A quantized weight, mirroring the QuantizedTensor of the qlora-rs
@@ -469,6 +476,65 @@ NF4_API nf4_status qlora_grouped_bwd(const nf4_weight* w, int num_experts, const
                                      float alpha, int compute_dtype, const void* dy, const void* t,
                                      float* dA, float* dB, void* dx, void* workspace,
                                      size_t ws_bytes, void* stream);
+
+/*
+ * Gated feed-forward layer on two QLoRA linears that share their input, forward
+ * (the gate and up projections of a decoder block with the product between them and
+ * the down projection):
+ *   T_p = s x A_p^T                                        p = 0 gate, 1 up;  s = alpha / r
+ *   g = x W'_gate^T + T_0 B_0^T (+ bias_0),  u = x W'_up^T + T_1 B_1^T (+ bias_1)
+ *   h = act(g) * u
+ * in one product kernel: g and u are summed in fp32 and never rounded before h is.
+ *   w_gate, w_up   of the same rows (N), cols (K), block size and scale form
+ *                  (double_quant); N % 8 == 0, K % 64 == 0, block sizes as in
+ *                  qlora_linear_fwd.  N, K and M up to 2^30.
+ *   x              [M, K] compute_dtype; M >= 0 (0: nothing is enqueued; x, h, pre_out
+ *                  and t_out may then be NULL).
+ *   A, B           [2, r, K] and [2, N, r] compute_dtype, the gate's first;
+ *                  8 <= r <= 256, r % 8 == 0.
+ *   activation     an nf4_activation.
+ *   compute_dtype  as qlora_linear_fwd (NF4_F32: the fp32 reference mode).
+ *   bias           [2, N] compute_dtype, or NULL.
+ *   h              [M, N] compute_dtype.
+ *   pre_out        [2, M, N] compute_dtype, or NULL: g, then u, each rounded once; what
+ *                  qlora_gated_bwd takes as `pre`.
+ *   t_out          [2, M, r] compute_dtype, or NULL: T, rounded; its `t`.
+ *   workspace      >= nf4_workspace_bytes(NF4_OP_GATED_FWD, M, N, K, r, 64, dq), with
+ *                  NF4_F32 of NF4_OP_GATED_FWD_F32 (which holds g and u).
+ * A token's result depends on the tokens beside it only through the order of its sums.  In
+ * BF16 and F16 a T beyond the compute type's range makes g and u of its token non-finite in
+ * both projections.
+ */
+NF4_API nf4_status qlora_gated_fwd(const nf4_weight* w_gate, const nf4_weight* w_up, const void* x,
+                                   int64_t M, const void* A, const void* B, int r, float alpha,
+                                   int activation, int compute_dtype, const void* bias, void* h,
+                                   void* pre_out, void* t_out, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
+/*
+ * Adapter backward of qlora_gated_fwd for L = sum(dh * h), both bases frozen, from the g, u
+ * and T that the forward saved:
+ *   dg = dh * u * act'(g),  du = dh * act(g)
+ *   U_p = s d_p B_p                                  (d_0 = dg, d_1 = du)
+ *   dB_p = d_p^T T_p   fp32 [2, N, r], overwritten   dA_p = U_p^T x   fp32 [2, r, K], overwritten
+ *   dx = dg W'_gate + du W'_up + U_0 A_0 + U_1 A_1   [M, K] compute_dtype, or NULL
+ * M == 0 gives zero dA and dB.
+ *   dh             [M, N] compute_dtype.
+ *   pre            [2, M, N] compute_dtype: g, u (the biases are in them already).
+ *   t              [2, M, r] compute_dtype, or NULL to recompute it.
+ * With BF16 and F16 dg, du and U enter dx rounded to the compute type; dA and dB are summed
+ * from three or two 16-bit terms of them, which keep 24 bits (BF16) or 22 (F16: for values
+ * from 2^-14 to 65504; below, they are off by up to 2^-36, so gradients that small are scaled
+ * before the call).  A value beyond the compute type's range counts as infinite.  The other
+ * arguments as in qlora_gated_fwd.
+ *   workspace      >= nf4_workspace_bytes(NF4_OP_GATED_BWD, M, N, K, r, 64, dq), with
+ *                  NF4_F32 of NF4_OP_GATED_BWD_F32 (they hold dg and du).
+ */
+NF4_API nf4_status qlora_gated_bwd(const nf4_weight* w_gate, const nf4_weight* w_up, const void* x,
+                                   int64_t M, const void* A, const void* B, int r, float alpha,
+                                   int activation, int compute_dtype, const void* dh, const void* pre,
+                                   const void* t, float* dA, float* dB, void* dx, void* workspace,
+                                   size_t ws_bytes, void* stream);
 
 /*
  * Row-wise quantization to 8-bit integers, for the operands of

@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "nf4_common.cuh"
+#include "gated.h"
 #include "kernels.h"
 #include "nvtx_range.h"
 
@@ -123,7 +124,8 @@ const char* const kKernelNames[nf4::kNumKernelIds] = {
     "nf4_quantize", "nf4_double_quant", "nf4_dequantize", "adapter_gemm_T",
     "fused_nf4_gemm_fwd", "fused_nf4_gemm_dx", "nf4_gemv", "nf4_merge", "gemm_f32", "nf4_absmax_max",
     "adapter_gemm_U", "adapter_gemm_dB", "adapter_gemm_dA", "grouped_T", "grouped_fwd", "grouped_U",
-    "grouped_dB", "grouped_dA", "grouped_grad", "grouped_dx", "int8_quantize", "int8_linear"};
+    "grouped_dB", "grouped_dA", "grouped_grad", "grouped_dx", "int8_quantize", "int8_linear",
+    "gated_T", "gated_fwd", "gated_U", "gated_dB", "gated_dA", "gated_dx", "gated_act_f32"};
 
 cudaEvent_t prof_event() {
   if (!g_prof_free.empty()) {
@@ -248,6 +250,10 @@ size_t nf4_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int b
     case NF4_OP_GROUPED_FWD: return nf4::kWsHeader + nf4::grouped_workspace_bytes(false, M, N, K, r);
     case NF4_OP_GROUPED_BWD: return nf4::kWsHeader + nf4::grouped_workspace_bytes(true, M, N, K, r);
     case NF4_OP_INT8_LINEAR: return int8_linear_ws(M, K);
+    case NF4_OP_GATED_FWD: return nf4::kWsHeader + nf4::gated_workspace_bytes(false, false, M, N, K, r);
+    case NF4_OP_GATED_BWD: return nf4::kWsHeader + nf4::gated_workspace_bytes(true, false, M, N, K, r);
+    case NF4_OP_GATED_FWD_F32: return nf4::kWsHeader + nf4::gated_workspace_bytes(false, true, M, N, K, r);
+    case NF4_OP_GATED_BWD_F32: return nf4::kWsHeader + nf4::gated_workspace_bytes(true, true, M, N, K, r);
     default: return 0;
   }
 }
@@ -664,6 +670,107 @@ nf4_status int8_linear_fwd(const int8_t* w_codes, const float* w_scale, int64_t 
   float* scales = reinterpret_cast<float*>(codes + round_up(size_t(M) * size_t(K), 256));
   int launches = 0;
   const cudaError_t e = nf4::launch_int8_linear(a, x, x_scale, codes, scales, sm_count(), st, &launches);
+  return finish(e, launches);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks and common arguments of the two gated entry points.  With M == 0 there are no
+// activations: x may be null.
+nf4_status gated_args(const nf4_weight* w_gate, const nf4_weight* w_up, const void* x, int64_t M, const void* A,
+                      const void* B, int r, float alpha, int activation, int compute_dtype, void* workspace,
+                      size_t ws_bytes, bool backward, nf4::GatedArgs* out) {
+  if (M < 0) return NF4_ERR_SHAPE;
+  // the linear checks; with no rows A stands in for x
+  nf4_status s = check_linear(w_gate, M > 0 ? x : A, M > 0 ? M : 1, A, B, r, alpha, compute_dtype);
+  if (s == NF4_OK) s = check_linear(w_up, M > 0 ? x : A, M > 0 ? M : 1, A, B, r, alpha, compute_dtype);
+  if (s != NF4_OK) return s;
+  if (activation != NF4_ACT_SILU && activation != NF4_ACT_GELU_TANH) return NF4_ERR_INVALID_ARG;
+  if (w_gate->rows != w_up->rows || w_gate->cols != w_up->cols || w_gate->block_size != w_up->block_size)
+    return NF4_ERR_SHAPE;
+  if ((w_gate->double_quant != 0) != (w_up->double_quant != 0)) return NF4_ERR_INVALID_ARG;
+  const int64_t N = w_gate->rows, K = w_gate->cols;
+  // the kernels' tile arithmetic is 32-bit
+  if (M > (int64_t(1) << 30) || N > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return NF4_ERR_SHAPE;
+  if (workspace == nullptr || !aligned16(workspace)) return NF4_ERR_WORKSPACE;
+  const bool f32 = compute_dtype == NF4_F32;
+  if (ws_bytes < nf4::kWsHeader + nf4::gated_workspace_bytes(backward, f32, M, N, K, r)) return NF4_ERR_WORKSPACE;
+  *out = nf4::GatedArgs{};
+  out->w[0] = w_gate;
+  out->w[1] = w_up;
+  out->M = M;
+  out->N = N;
+  out->K = K;
+  out->r = r;
+  out->s = alpha / float(r);
+  out->f16 = compute_dtype == NF4_F16 ? 1 : 0;
+  out->f32 = f32 ? 1 : 0;
+  out->act = activation;
+  out->x = x;
+  out->A = A;
+  out->B = B;
+  out->ws = static_cast<uint8_t*>(workspace);
+  if (!status_word(out->ws, &out->status)) return NF4_ERR_CUDA;
+  return NF4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nf4_status qlora_gated_fwd(const nf4_weight* w_gate, const nf4_weight* w_up, const void* x, int64_t M, const void* A,
+                           const void* B, int r, float alpha, int activation, int compute_dtype, const void* bias,
+                           void* h, void* pre_out, void* t_out, void* workspace, size_t ws_bytes, void* stream) {
+  NF4_API_RANGE("qlora_gated_fwd");
+  nf4::GatedArgs a;
+  const nf4_status s = gated_args(w_gate, w_up, x, M, A, B, r, alpha, activation, compute_dtype, workspace, ws_bytes,
+                                  false, &a);
+  if (s != NF4_OK) return s;
+  if (M > 0 && h == nullptr) return NF4_ERR_INVALID_ARG;
+  if ((h && !aligned16(h)) || (bias && !aligned16(bias)) || (pre_out && !aligned16(pre_out)) ||
+      (t_out && !aligned16(t_out)))
+    return NF4_ERR_ALIGNMENT;
+  if (M == 0) return NF4_OK;
+  a.bias = bias;
+  a.h = h;
+  a.pre_out = pre_out;
+  a.t_out = t_out;
+  int launches = 0;
+  const cudaError_t e = nf4::launch_gated_fwd(a, sm_count(), static_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches);
+}
+
+nf4_status qlora_gated_bwd(const nf4_weight* w_gate, const nf4_weight* w_up, const void* x, int64_t M, const void* A,
+                           const void* B, int r, float alpha, int activation, int compute_dtype, const void* dh,
+                           const void* pre, const void* t, float* dA, float* dB, void* dx, void* workspace,
+                           size_t ws_bytes, void* stream) {
+  NF4_API_RANGE("qlora_gated_bwd");
+  nf4::GatedArgs a;
+  const nf4_status s = gated_args(w_gate, w_up, x, M, A, B, r, alpha, activation, compute_dtype, workspace, ws_bytes,
+                                  true, &a);
+  if (s != NF4_OK) return s;
+  if ((M > 0 && (dh == nullptr || pre == nullptr)) || dA == nullptr || dB == nullptr) return NF4_ERR_INVALID_ARG;
+  if ((dh && !aligned16(dh)) || (pre && !aligned16(pre)) || (t && !aligned16(t)) || !aligned16(dA) || !aligned16(dB) ||
+      (dx && !aligned16(dx)))
+    return NF4_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) {   // no rows: every gradient is zero
+    const size_t per = 2 * size_t(r) * sizeof(float);
+    if (cudaMemsetAsync(dA, 0, per * size_t(a.K), st) != cudaSuccess ||
+        cudaMemsetAsync(dB, 0, per * size_t(a.N), st) != cudaSuccess)
+      return NF4_ERR_CUDA;
+    return NF4_OK;
+  }
+  a.dh = dh;
+  a.pre_in = pre;
+  a.t_in = t;
+  a.dA = dA;
+  a.dB = dB;
+  a.dx = dx;
+  int launches = 0;
+  const cudaError_t e = nf4::launch_gated_bwd(a, sm_count(), st, &launches);
   return finish(e, launches);
 }
 

@@ -1,0 +1,704 @@
+// The rank-r products of the gated feed-forward layer on the sm_100a tensor cores, both
+// projections p in one launch each:
+//   T_p  = s x A_p^T                 [2, M, r]
+//   d_0  = dh u act'(g) (dg),  d_1 = dh act(g) (du)
+//   U_p  = s d_p B_p                 [2, M, r]
+//   dB_p = d_p^T T_p                 fp32 [2, N, r]
+//   dA_p = U_p^T x                   fp32 [2, r, K]
+// A tile is 128 rows of the result by 64 adapter columns of both projections (a further
+// grid dimension for r > 64); the reduction runs in steps of 64 and is split over the CTAs
+// of a cluster, which sum their fp32 partials through distributed shared memory in a fixed
+// order.
+//
+// T and dA are fed by TMA.  U and dB make their A operand, d, on the way: sixteen warps
+// read dh, g and u (a step ahead, in registers), compute dg and du in fp32 and write them
+// as 16-bit terms, swizzled, into shared memory; U's warps store the first terms to global
+// memory too, for dx.  dB computes d a second time instead of reading it: the fp32 value
+// is what it needs, and dh, g and u are 3/4 of the bytes of two terms of dg and du.
+//
+// Gradients are fp32, and one rounding of d or U to 16 bits would be their largest error by
+// far (2^-9 against 2^-24).  So d and U enter as three bf16 terms that together hold 24
+// bits, or two f16 terms, the second scaled by 2^11 (22 bits; see expert_grad.cu).  The tensor core
+// truncates when it adds to an accumulator: the first terms of even and odd steps have an
+// accumulator each and the small terms a third, summed in fp32 at the end.
+#include <algorithm>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "expert_grad.h"
+#include "gated_act.cuh"
+#include "gated_rank.h"
+#include "nf4_common.cuh"
+#include "nf4_dequant.cuh"
+#include "ring_wait.cuh"
+#include "tc_common.cuh"
+#include "tensor_maps.h"
+
+namespace nf4 {
+namespace {
+
+using namespace tc;
+using expert::elect_one;
+using expert::pack2;
+using expert::ring_wait;
+using expert::unpack2;
+using expert::warp_wait;
+
+constexpr int kCols = 64;                          // adapter columns of a tile, per projection
+constexpr uint32_t kTileBytes = 128 * 128;         // 128 x 64 or 64 x 128 16-bit values
+constexpr uint32_t kBoxBytes = 64 * 128;           // 64 x 64
+constexpr int kMaxSlices = 8;
+constexpr uint32_t kParkBytes = 128 * 2 * kCols * 4;   // a CTA's partial
+
+// The term that comes after `first` in a split of v: what rounding left.  Nothing is left
+// of an infinity (whose difference to itself would be NaN).
+__device__ __forceinline__ float rest(float v, float first) {
+  const float d = v - first;
+  return fabsf(d) < __uint_as_float(0x7f800000u) ? d : 0.0f;
+}
+
+// Four consecutive columns (`col` .. of 0 .. 2 kCols) of row `row` of the result.
+template <GatedRankKind KIND>
+__device__ __forceinline__ void store4(const GatedRankParams& p, int row, int col, int col0, float4 v) {
+  const int proj = col >= kCols ? 1 : 0;
+  const int j = col0 + col - proj * kCols;
+  if (j >= p.r) return;
+  if (KIND == kGatedT || KIND == kGatedU) {
+    if (row >= p.M) return;
+    const bool f16 = p.f16 != 0;
+    float u[4] = {v.x * p.scale, v.y * p.scale, v.z * p.scale, v.w * p.scale};
+    const int terms = KIND == kGatedU ? p.terms : 1;
+    uint16_t* o = p.out16 + (int64_t(proj) * terms * p.M + row) * p.r + j;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (i >= terms) break;
+      const uint2 w = make_uint2(pack2(f16, u[0], u[1]), pack2(f16, u[2], u[3]));
+      *reinterpret_cast<uint2*>(o + int64_t(i) * p.M * p.r) = w;
+      const float2 a = unpack2(f16, w.x), b = unpack2(f16, w.y);
+      const float rounded[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = rest(u[e], rounded[e]) * (f16 ? kULoMul : 1.0f);
+    }
+  } else if (KIND == kGatedDB) {
+    if (row < p.N) *reinterpret_cast<float4*>(p.out32 + (int64_t(proj) * p.N + row) * p.r + j) = v;
+  } else {
+    if (row >= p.K) return;
+    float* o = p.out32 + (int64_t(proj) * p.r + j) * p.K + row;
+    o[0] = v.x;
+    o[int64_t(p.K)] = v.y;
+    o[2 * int64_t(p.K)] = v.z;
+    o[3 * int64_t(p.K)] = v.w;
+  }
+}
+
+// A CTA's sums of 32 columns at `c`, lane = row: the accumulators joined.  acc: TMEM address
+// of the first; `steps` of this CTA; a third accumulator with the small terms if `small`.
+__device__ __forceinline__ void join_accs(uint32_t at, uint32_t stride, int steps, bool small, float lo_scale,
+                                          float (&f)[32]) {
+  uint32_t v[32];
+  if (steps == 0) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = 0.0f;
+    return;
+  }
+  tmem_ld_32x32b_x32(at, v);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+  if (steps > 1) {
+    tmem_ld_32x32b_x32(at + stride, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] += __uint_as_float(v[i]);
+  }
+  if (small) {
+    tmem_ld_32x32b_x32(at + 2 * stride, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = fmaf(__uint_as_float(v[i]), lo_scale, f[i]);
+  }
+}
+
+// 32 columns at `c` of tile row `prow` to the result or, with several slices, to the parked
+// partial (16-byte chunks swizzled by row).
+template <GatedRankKind KIND>
+__device__ __forceinline__ void finish32(const GatedRankParams& p, float* park, int row0, int prow, int c, int col0,
+                                         const float (&f)[32]) {
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    const float4 q = make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]);
+    const int col = c + 4 * g;
+    if (p.slices == 1) store4<KIND>(p, row0 + prow, col, col0, q);
+    else *reinterpret_cast<float4*>(park + prow * (2 * kCols) + 4 * ((col >> 2) ^ (prow & 7))) = q;
+  }
+}
+
+// The slices' partials of a tile: CTA q of the cluster sums its share of the rows over the
+// slices in their order.  All threads of the CTA; the second barrier keeps the partials alive.
+template <GatedRankKind KIND>
+__device__ __forceinline__ void sum_slices(const GatedRankParams& p, const float* park, int row0, int col0) {
+  cluster_sync();
+  const int q = int(cluster_ctarank()), S = p.slices;
+  const int r0 = q * 128 / S, r1 = (q + 1) * 128 / S;
+  const int rows = r1 - r0;
+  constexpr int kVec = 2 * kCols / 4;
+  const uint32_t base = smem_u32(park);
+  for (int i = threadIdx.x; i < rows * kVec; i += blockDim.x) {
+    // dA: neighbouring threads on neighbouring rows, which its transposed result keeps together
+    const int cv = KIND == kGatedDA ? i / rows : i % kVec;
+    const int trow = r0 + (KIND == kGatedDA ? i % rows : i / kVec);
+    const uint32_t off = uint32_t((trow * (2 * kCols) + 4 * (cv ^ (trow & 7))) * 4);
+    float4 part[kMaxSlices], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int sl = 0; sl < kMaxSlices; ++sl)   // all on their way before the first is needed
+      if (sl < S) part[sl] = ld_shared_cluster_f4(mapa_shared(base + off, uint32_t(sl)));
+#pragma unroll
+    for (int sl = 0; sl < kMaxSlices; ++sl) {
+      if (sl >= S) break;
+      acc.x += part[sl].x;
+      acc.y += part[sl].y;
+      acc.z += part[sl].z;
+      acc.w += part[sl].w;
+    }
+    store4<KIND>(p, row0 + trow, 4 * cv, col0, acc);
+  }
+  cluster_sync();
+}
+
+// This CTA's steps of the reduction.
+struct Share {
+  int step0, steps;
+};
+__device__ __forceinline__ Share share_of(const GatedRankParams& p) {
+  const int q = blockIdx.y;
+  const int s0 = int(int64_t(p.red_steps) * q / p.slices), s1 = int(int64_t(p.red_steps) * (q + 1) / p.slices);
+  return Share{s0, s1 - s0};
+}
+
+// ------------------------------------------------------------------ T and dA: operands by TMA
+
+constexpr int kTmaThreads = 256;    // A loads, B loads, MMA, TMEM; four epilogue warps
+constexpr int tma_boxes(GatedRankKind kind, int terms) { return kind == kGatedT ? 2 : 2 * terms; }
+constexpr uint32_t tma_stage_bytes(GatedRankKind kind, int terms) {
+  return kTileBytes + uint32_t(tma_boxes(kind, terms)) * kBoxBytes;
+}
+constexpr int tma_stages(GatedRankKind kind) { return kind == kGatedT ? 4 : 3; }
+
+struct TmaShared {
+  uint64_t full[4];
+  uint64_t empty[4];
+  uint64_t accum;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+};
+constexpr size_t tma_smem(GatedRankKind kind) {
+  return size_t(tma_stages(kind)) * tma_stage_bytes(kind, 3) + sizeof(TmaShared) + 1024;
+}
+static_assert(tma_smem(kGatedDA) <= 232448 && tma_stages(kGatedT) * tma_stage_bytes(kGatedT, 1) >= kParkBytes, "shared memory");
+
+template <GatedRankKind KIND>
+__global__ void __launch_bounds__(kTmaThreads, 1)
+    gated_tma_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const GatedRankParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = expert::align_1024(smem_raw);
+  constexpr int kStages = tma_stages(KIND);
+  const int terms = KIND == kGatedT ? 1 : p.terms;
+  const int boxes = tma_boxes(KIND, terms);
+  const uint32_t stage_bytes = tma_stage_bytes(KIND, terms);
+  TmaShared* sh = reinterpret_cast<TmaShared*>(smem + kStages * tma_stage_bytes(KIND, 3));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  volatile uint32_t* abort_flag = &sh->abort_flag;
+  const int row0 = blockIdx.x * 128;
+  const int col0 = blockIdx.z * kCols;
+  const Share w = share_of(p);
+  constexpr uint32_t kAccCols = KIND == kGatedT ? 256 : 512;
+  // T: even and odd steps; dA: those and the small terms, each of 2 kCols columns
+  constexpr uint32_t kAccStride = 2 * kCols;
+
+  // A kernel launched as this one's programmatic dependent may start on the SMs this grid
+  // leaves free; it waits for this grid before it reads the result.
+  grid_dep_launch();
+  if (threadIdx.x == 0) {
+    tma_prefetch(&tm_a);
+    tma_prefetch(&tm_b);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sh->full[s], 2);
+      mbar_init(&sh->empty[s], 1);
+    }
+    mbar_init(&sh->accum, 1);
+    sh->abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 3) {
+    tmem_alloc(&sh->tmem_base, kAccCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+
+  if (warp < 2) {
+    const bool issue = elect_one();
+    int issued = 0, s = 0;
+    uint32_t ph = 1;
+    for (int i = 0; i < w.steps; ++i) {
+      if (!ring_wait(&sh->empty[s], ph, abort_flag, p.status)) break;
+      if (issue) {
+        uint8_t* a = smem + s * stage_bytes;
+        uint8_t* b = a + kTileBytes;
+        const int red0 = (w.step0 + i) * 64;
+        if (warp == 0) {
+          mbar_arrive_expect_tx(&sh->full[s], kTileBytes);
+          if (KIND == kGatedT) {
+            tma_load_2d(a, &tm_a, &sh->full[s], red0, row0);
+          } else {
+            tma_load_2d(a, &tm_a, &sh->full[s], row0, red0);
+            tma_load_2d(a + kBoxBytes, &tm_a, &sh->full[s], row0 + 64, red0);
+          }
+        } else {
+          mbar_arrive_expect_tx(&sh->full[s], uint32_t(boxes) * kBoxBytes);
+          for (int z = 0; z < boxes; ++z) {
+            if (KIND == kGatedT) tma_load_3d(b + z * kBoxBytes, &tm_b, &sh->full[s], red0, col0, z);
+            else tma_load_3d(b + z * kBoxBytes, &tm_b, &sh->full[s], col0, red0, z);
+          }
+        }
+      }
+      __syncwarp();
+      ++issued;
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    if (*abort_flag) {   // unwind: wait (bounded) for the copies in flight
+      for (int i = max(0, issued - kStages); i < issued; ++i) {
+        uint32_t none = 0;
+        ring_wait(&sh->full[i % kStages], (i / kStages) & 1, &none, nullptr);
+      }
+    }
+  } else if (warp == 2) {
+    const bool issue = elect_one();
+    bool ok = true;
+    int s = 0, issued = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < w.steps; ++i) {
+      ok = ring_wait(&sh->full[s], ph, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t a_base = smem_u32(smem + s * stage_bytes);
+      if (issue) {
+        const uint32_t d = tmem + uint32_t(i & 1) * kAccStride;
+        if (KIND == kGatedT) {   // both projections' rows of A lie one after another: N = 128
+          const uint32_t idesc = idesc_f32acc(128, 2 * kCols, false, false, p.f16 != 0);
+          const uint64_t adesc = smem_desc_sw128(a_base, 16, 1024), bdesc = smem_desc_sw128(a_base + kTileBytes, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) umma_f16(d, adesc + kk * 2, bdesc + kk * 2, idesc, (i > 1 || kk > 0) ? 1u : 0u);
+        } else {
+          const uint32_t idesc = idesc_f32acc(128, kCols, true, true, p.f16 != 0);
+          const uint64_t adesc = smem_desc_sw128(a_base, 8192, 1024), bdesc = smem_desc_sw128(a_base + kTileBytes, 8192, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint64_t bz = bdesc + uint32_t(z * terms) * (kBoxBytes >> 4) + kk * 128;
+              const uint32_t dz = uint32_t(z * kCols);
+              umma_f16(d + dz, adesc + kk * 128, bz, idesc, (i > 1 || kk > 0) ? 1u : 0u);
+              umma_f16(tmem + 2 * kAccStride + dz, adesc + kk * 128, bz + (kBoxBytes >> 4), idesc, (i > 0 || kk > 0) ? 1u : 0u);
+              if (terms > 2) umma_f16(tmem + 2 * kAccStride + dz, adesc + kk * 128, bz + 2 * (kBoxBytes >> 4), idesc, 1u);
+            }
+          }
+        }
+        // the last step's commit goes to accum (nobody waits on its stage)
+        umma_commit(i + 1 < w.steps ? &sh->empty[s] : &sh->accum);
+      }
+      __syncwarp();
+      ++issued;
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    if (issue && !ok) drain_issued(sh->empty, issued, kStages);
+    else if (issue && w.steps == 0) mbar_arrive(&sh->accum);
+  } else if (warp >= 4) {
+    const bool ok = warp_wait(&sh->accum, 0, abort_flag, p.status);
+    tc_fence_after();
+    const int quad = warp - 4;
+    const float lo_scale = p.f16 ? 1.0f / kULoMul : 1.0f;
+    for (int c = 0; c < 2 * kCols; c += 32) {
+      float f[32];
+      join_accs(tmem + (uint32_t(quad * 32) << 16) + c, kAccStride, ok ? w.steps : 0, KIND == kGatedDA, lo_scale, f);
+      finish32<KIND>(p, reinterpret_cast<float*>(smem), row0, quad * 32 + lane, c, col0, f);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (p.slices > 1) sum_slices<KIND>(p, reinterpret_cast<float*>(smem), row0, col0);
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kAccCols);
+  }
+}
+
+// ------------------------------------------------------------------ U and dB: d made on the way
+
+constexpr int kMkWarps = 16;                                    // they make d, and finish the tile
+constexpr int kMkThreads = 32 * (kMkWarps + 2);                 // and B loads, MMA
+constexpr int kMkBufs = 2;
+constexpr uint32_t kMkOpBytes = 6 * kTileBytes;                 // terms of dg, then of du
+constexpr uint32_t kMkBBytes = 2 * kBoxBytes;
+
+struct MkShared {
+  uint64_t opfull[kMkBufs];   // a step's terms are written
+  uint64_t bfull[kMkBufs];    // its B boxes landed
+  uint64_t empty[kMkBufs];    // the MMAs that read them finished
+  uint64_t accum;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+};
+constexpr size_t kMkSmem = size_t(kMkBufs) * (kMkOpBytes + kMkBBytes) + sizeof(MkShared) + 1024;
+static_assert(kMkSmem <= 232448, "shared memory of one CTA");
+
+template <bool F16>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = unpack2(F16, w[i]);
+    f[2 * i] = a.x;
+    f[2 * i + 1] = a.y;
+  }
+}
+
+template <GatedRankKind KIND, bool F16>
+__global__ void __launch_bounds__(kMkThreads, 1)
+    gated_make_kernel(const __grid_constant__ CUtensorMap tm_b, const GatedRankParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = expert::align_1024(smem_raw);
+  constexpr int kTerms = gated_terms(F16);
+  MkShared* sh = reinterpret_cast<MkShared*>(smem + kMkBufs * (kMkOpBytes + kMkBBytes));
+  auto op_tile = [&](int buf, int proj, int term) { return smem + buf * kMkOpBytes + uint32_t(proj * 3 + term) * kTileBytes; };
+  auto b_box = [&](int buf, int proj) { return smem + kMkBufs * kMkOpBytes + buf * kMkBBytes + proj * kBoxBytes; };
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  volatile uint32_t* abort_flag = &sh->abort_flag;
+  const int row0 = blockIdx.x * 128;
+  const int col0 = blockIdx.z * kCols;
+  const Share w = share_of(p);
+  constexpr uint32_t kAccStride = 2 * kCols;
+
+  grid_dep_launch();
+  if (threadIdx.x == 0) {
+    tma_prefetch(&tm_b);
+    for (int b = 0; b < kMkBufs; ++b) {
+      mbar_init(&sh->opfull[b], kMkWarps);
+      mbar_init(&sh->bfull[b], 1);
+      mbar_init(&sh->empty[b], 1);
+    }
+    mbar_init(&sh->accum, 1);
+    sh->abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == kMkWarps) {
+    tmem_alloc(&sh->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+
+  if (warp < kMkWarps) {
+    // ---------------- d of 128 x 64 (U) or 64 x 128 (dB) elements a step: a thread takes
+    // eight of them twice, at row t / 8 and 16-byte chunk t % 8 of each half of the tile
+    const int tr = threadIdx.x >> 3, tc = threadIdx.x & 7;
+    const int64_t mn = int64_t(p.M) * p.N;
+    uint4 in[2][3];                // dh, g, u
+    int64_t at[2];
+    bool there[2];
+    auto fetch = [&](int i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int red0 = (w.step0 + i) * 64;
+        const int m = KIND == kGatedU ? row0 + 64 * h + tr : red0 + tr;
+        const int n = KIND == kGatedU ? red0 + 8 * tc : row0 + 64 * h + 8 * tc;
+        there[h] = i < w.steps && m < p.M && n < p.N;
+        at[h] = int64_t(m) * p.N + n;
+#pragma unroll
+        for (int j = 0; j < 3; ++j) in[h][j] = make_uint4(0u, 0u, 0u, 0u);
+        if (there[h]) {
+          in[h][0] = __ldg(reinterpret_cast<const uint4*>(p.dh + at[h]));
+          in[h][1] = __ldg(reinterpret_cast<const uint4*>(p.pre + at[h]));
+          in[h][2] = __ldg(reinterpret_cast<const uint4*>(p.pre + mn + at[h]));
+        }
+      }
+    };
+    const uint32_t off = sw128_offset(uint32_t(tr), uint32_t(tc));
+    bool ok = true;
+    fetch(0);
+    for (int i = 0; i < w.steps; ++i) {
+      const int b = i & 1;
+      uint4 d[2][2][3];   // half, projection, term
+      int64_t now[2] = {at[0], at[1]};
+      bool write[2] = {there[0], there[1]};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float dh[8], g[8], u[8];
+        unpack8<F16>(in[h][0], dh);
+        unpack8<F16>(in[h][1], g);
+        unpack8<F16>(in[h][2], u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const gated::ActGrad ag = gated::act_grad<true>(p.act, g[e]);
+          g[e] = dh[e] * u[e] * ag.d;
+          u[e] = dh[e] * ag.a;
+        }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          float* v = z == 0 ? g : u;
+#pragma unroll
+          for (int term = 0; term < kTerms; ++term) {
+            uint32_t q[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              q[e] = pack2(F16, v[2 * e], v[2 * e + 1]);
+              if (term + 1 < kTerms) {
+                const float2 a = unpack2(F16, q[e]);
+                v[2 * e] = rest(v[2 * e], a.x) * (F16 ? kULoMul : 1.0f);
+                v[2 * e + 1] = rest(v[2 * e + 1], a.y) * (F16 ? kULoMul : 1.0f);
+              }
+            }
+            d[h][z][term] = make_uint4(q[0], q[1], q[2], q[3]);
+          }
+        }
+      }
+      fetch(i + 1);
+      if (ok) ok = warp_wait(&sh->empty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.status);
+      if (!ok) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int term = 0; term < kTerms; ++term)
+            *reinterpret_cast<uint4*>(op_tile(b, z, term) + uint32_t(h) * kBoxBytes + off) = d[h][z][term];
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->opfull[b]);
+      if (KIND == kGatedU && blockIdx.z == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (write[h]) {
+            *reinterpret_cast<uint4*>(p.d + now[h]) = d[h][0][0];
+            *reinterpret_cast<uint4*>(p.d + mn + now[h]) = d[h][1][0];
+          }
+      }
+    }
+    // ---------------- the tile's sums: four warps a TMEM quadrant, 32 columns each
+    if (ok) ok = warp_wait(&sh->accum, 0, abort_flag, p.status);
+    tc_fence_after();
+    const int quad = warp & 3, c = (warp >> 2) * 32;
+    float f[32];
+    join_accs(tmem + (uint32_t(quad * 32) << 16) + c, kAccStride, ok ? w.steps : 0, true, F16 ? 1.0f / kULoMul : 1.0f, f);
+    finish32<KIND>(p, reinterpret_cast<float*>(smem), row0, quad * 32 + lane, c, col0, f);
+  } else if (warp == kMkWarps) {
+    // ---------------- MMA
+    const bool issue = elect_one();
+    bool ok = true;
+    int issued = 0;
+    constexpr bool kAMn = KIND == kGatedDB;
+    constexpr uint32_t idesc = idesc_f32acc(128, kCols, kAMn, true, F16);
+    for (int i = 0; i < w.steps; ++i) {
+      const int b = i & 1;
+      const uint32_t ph = (i >> 1) & 1;
+      ok = ring_wait(&sh->opfull[b], ph, abort_flag, p.status) && ring_wait(&sh->bfull[b], ph, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      if (issue) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const uint64_t bdesc = smem_desc_sw128(smem_u32(b_box(b, z)), 8192, 1024);
+          const uint64_t adesc = kAMn ? smem_desc_sw128(smem_u32(op_tile(b, z, 0)), 8192, 1024)
+                                      : smem_desc_sw128(smem_u32(op_tile(b, z, 0)), 16, 1024);
+          constexpr uint32_t kASub = kAMn ? 128 : 2;
+          const uint32_t dz = uint32_t(z * kCols);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            umma_f16(tmem + uint32_t(i & 1) * kAccStride + dz, adesc + kk * kASub, bdesc + kk * 128, idesc, (i > 1 || kk > 0) ? 1u : 0u);
+#pragma unroll
+            for (int term = 1; term < kTerms; ++term)
+              umma_f16(tmem + 2 * kAccStride + dz, adesc + uint32_t(term) * (kTileBytes >> 4) + kk * kASub, bdesc + kk * 128,
+                       idesc, (i > 0 || kk > 0 || term > 1) ? 1u : 0u);
+          }
+        }
+        // the last step's commit goes to accum (nobody waits on its buffer)
+        umma_commit(i + 1 < w.steps ? &sh->empty[b] : &sh->accum);
+      }
+      __syncwarp();
+      ++issued;
+    }
+    if (issue && !ok) drain_issued(sh->empty, issued, kMkBufs);
+    else if (issue && w.steps == 0) mbar_arrive(&sh->accum);
+  } else {
+    // ---------------- B rows (U) or T rows (dB) of a step, both projections
+    const bool issue = elect_one();
+    int issued = 0;
+    for (int i = 0; i < w.steps; ++i) {
+      const int b = i & 1;
+      if (!ring_wait(&sh->empty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.status)) break;
+      if (issue) {
+        mbar_arrive_expect_tx(&sh->bfull[b], kMkBBytes);
+        for (int z = 0; z < 2; ++z) tma_load_3d(b_box(b, z), &tm_b, &sh->bfull[b], col0, (w.step0 + i) * 64, z);
+      }
+      __syncwarp();
+      ++issued;
+    }
+    if (*abort_flag) {   // unwind: wait (bounded) for the copies in flight
+      for (int i = max(0, issued - kMkBufs); i < issued; ++i) {
+        uint32_t none = 0;
+        ring_wait(&sh->bfull[i & 1], (i >> 1) & 1, &none, nullptr);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (p.slices > 1) sum_slices<KIND>(p, reinterpret_cast<float*>(smem), row0, col0);
+  if (warp == kMkWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+PerDeviceOnce g_attr_done;
+
+cudaError_t set_attrs() {
+  const int dev = PerDeviceOnce::current();
+  if (g_attr_done.done(dev)) return cudaSuccess;
+  const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(gated_tma_kernel<kGatedT>, attr, int(tma_smem(kGatedT)));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(gated_tma_kernel<kGatedDA>, attr, int(tma_smem(kGatedDA)));
+  const void* make[] = {(const void*)gated_make_kernel<kGatedU, false>, (const void*)gated_make_kernel<kGatedU, true>,
+                        (const void*)gated_make_kernel<kGatedDB, false>, (const void*)gated_make_kernel<kGatedDB, true>};
+  for (const void* k : make)
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, attr, int(kMkSmem));
+  if (e == cudaSuccess) g_attr_done.mark(dev);
+  return e;
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// CTAs of a cluster: as many as give the fewest steps on the SM with the most, two steps a
+// CTA at least, fewer where that ties.
+int pick_slices(int64_t tiles, int64_t steps, int sms) {
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= kMaxSlices && (s == 1 || steps / s >= 2); ++s) {
+    const int64_t cost = cdiv(tiles * s, sms) * (cdiv(steps, s) + 2);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+// in: kGatedDA the terms of U, kGatedDB T; d: kGatedU dg and du; out: the result.
+bool GatedRank::prepare(const GatedArgs& a, GatedRankKind k, const void* in, void* d, void* out, int sms) {
+  kind = k;
+  const uint64_t M = uint64_t(a.M), N = uint64_t(a.N), K = uint64_t(a.K), r = uint64_t(a.r);
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  p = GatedRankParams{};
+  p.M = int(a.M);
+  p.N = int(a.N);
+  p.K = int(a.K);
+  p.r = a.r;
+  p.f16 = a.f16;
+  p.act = a.act;
+  p.terms = gated_terms(a.f16 != 0);
+  p.scale = a.s;
+  p.dh = static_cast<const uint16_t*>(a.dh);
+  p.pre = static_cast<const uint16_t*>(a.pre_in);
+  p.d = static_cast<uint16_t*>(d);
+  p.status = a.status;
+  bool ok = true;
+  int64_t rows = 0, red = 0;
+  switch (k) {
+    case kGatedT:
+      ok = encode_map_2d(&ma, a.x, MapElem::k16, K, M, 64, 128, sw) && encode_map_stack(&mb, a.A, MapElem::k16, K, r, 2, 64, 64, sw);
+      rows = a.M, red = a.K;
+      break;
+    case kGatedDA:
+      ok = encode_map_2d(&ma, a.x, MapElem::k16, K, M, 64, 64, sw) &&
+           encode_map_stack(&mb, in, MapElem::k16, r, M, uint64_t(2 * p.terms), 64, 64, sw);
+      rows = a.K, red = a.M;
+      break;
+    case kGatedU:
+      ok = encode_map_stack(&mb, a.B, MapElem::k16, r, N, 2, 64, 64, sw);
+      rows = a.M, red = a.N;
+      break;
+    case kGatedDB:
+      ok = encode_map_stack(&mb, in, MapElem::k16, r, M, 2, 64, 64, sw);
+      rows = a.N, red = a.M;
+      break;
+  }
+  if (k == kGatedT || k == kGatedU) p.out16 = static_cast<uint16_t*>(out);
+  else p.out32 = static_cast<float*>(out);
+  p.red_steps = int(cdiv(red, 64));
+  const int64_t tiles = cdiv(rows, 128), groups = cdiv(a.r, kCols);
+  p.slices = pick_slices(tiles * groups, p.red_steps, sms);
+  grid = dim3(unsigned(tiles), unsigned(p.slices), unsigned(groups));
+  return ok && tiles <= int64_t(0x7fffffff);
+}
+
+cudaError_t GatedRank::run(cudaStream_t st, int* launches) const {
+  cudaError_t e = set_attrs();
+  if (e != cudaSuccess) return e;
+  const bool tma = kind == kGatedT || kind == kGatedDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(tma ? kTmaThreads : kMkThreads, 1, 1);
+  cfg.dynamicSmemBytes = tma ? tma_smem(kind) : kMkSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = grid.y;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int ids[] = {kKGatedT, kKGatedDA, kKGatedU, kKGatedDB};
+  NF4_PROF_BEGIN(st, ids[kind]);
+  switch (kind) {
+    case kGatedT: e = cudaLaunchKernelEx(&cfg, gated_tma_kernel<kGatedT>, ma, mb, p); break;
+    case kGatedDA: e = cudaLaunchKernelEx(&cfg, gated_tma_kernel<kGatedDA>, ma, mb, p); break;
+    case kGatedU:
+      e = p.f16 ? cudaLaunchKernelEx(&cfg, gated_make_kernel<kGatedU, true>, mb, p)
+                : cudaLaunchKernelEx(&cfg, gated_make_kernel<kGatedU, false>, mb, p);
+      break;
+    case kGatedDB:
+      e = p.f16 ? cudaLaunchKernelEx(&cfg, gated_make_kernel<kGatedDB, true>, mb, p)
+                : cudaLaunchKernelEx(&cfg, gated_make_kernel<kGatedDB, false>, mb, p);
+      break;
+  }
+  NF4_PROF_END(st, ids[kind]);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+}  // namespace nf4

@@ -201,6 +201,13 @@ enum KernelId {
   kKGroupedDx,       // experts: dx
   kKInt8Quantize,
   kKInt8Linear,
+  kKGatedT,          // gated layer: T = s x A_p^T
+  kKGatedFwd,        // h (and g, u)
+  kKGatedU,          // U = s d_p B_p, and dg, du
+  kKGatedDB,         // dB_p = d_p^T T
+  kKGatedDA,         // dA_p = U_p^T x
+  kKGatedDx,         // dx
+  kKGatedAct,        // the elementwise products of the fp32 mode
   kNumKernelIds
 };
 

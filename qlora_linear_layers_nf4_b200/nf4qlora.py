@@ -24,6 +24,8 @@ STATUS_NAMES = {
 NF4_F32, NF4_BF16, NF4_F16 = 0, 1, 2
 OP_QUANTIZE, OP_DEQUANTIZE, OP_LINEAR_FWD, OP_LINEAR_BWD, OP_MERGE = 0, 1, 2, 3, 4
 OP_GROUPED_FWD, OP_GROUPED_BWD, OP_INT8_LINEAR = 5, 6, 7
+OP_GATED_FWD, OP_GATED_BWD, OP_GATED_FWD_F32, OP_GATED_BWD_F32 = 8, 9, 10, 11
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 
 EXPORTED = (
     "nf4_status_string", "nf4_version", "nf4_codebook", "nf4_launch_count",
@@ -32,6 +34,7 @@ EXPORTED = (
     "nf4_dequantize", "qlora_linear_fwd", "qlora_linear_bwd", "nf4_quantize_noalloc",
     "nf4_merge", "nf4_quantize_typed", "nf4_check_wait_timeout", "nf4_absmax_max",
     "nf4_double_quant", "qlora_grouped_fwd", "qlora_grouped_bwd", "int8_quantize", "int8_linear_fwd",
+    "qlora_gated_fwd", "qlora_gated_bwd",
     "nf4_status_on_device", "nf4_read_device_status",
 )
 
@@ -116,6 +119,12 @@ def lib() -> ctypes.CDLL:
     L.qlora_grouped_bwd.argtypes = [ctypes.POINTER(CWeight), i32, vp, i64, vp, vp, vp, i32, f32, i32, vp,
                                     vp, vp, vp, vp, vp, sz, vp]
     L.qlora_grouped_bwd.restype = i32
+    L.qlora_gated_fwd.argtypes = [ctypes.POINTER(CWeight), ctypes.POINTER(CWeight), vp, i64, vp, vp, i32, f32, i32, i32,
+                                  vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_gated_fwd.restype = i32
+    L.qlora_gated_bwd.argtypes = [ctypes.POINTER(CWeight), ctypes.POINTER(CWeight), vp, i64, vp, vp, i32, f32, i32, i32,
+                                  vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_gated_bwd.restype = i32
     L.int8_quantize.argtypes = [vp, i32, i64, i64, vp, vp, vp]
     L.int8_quantize.restype = i32
     L.int8_linear_fwd.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, sz, vp]
@@ -621,6 +630,101 @@ def grouped_bwd(q: QuantizedWeight, x, offsets, A, B, alpha: float, dy, t=None, 
                                      ws.get(need, dev).data_ptr(), need, here)
     if st:
         raise NF4Error(st, "qlora_grouped_bwd")
+    return dA, dB, dx
+
+
+@dataclass
+class GatedSaved:
+    """What gated_bwd takes of a forward."""
+    pre: object                      # [2, M, N] in the compute type: g, then u
+    t: object | None                 # [2, M, r]: T = (alpha / r) x A^T of both (None: recomputed)
+
+
+def _gated_shapes(gate: QuantizedWeight, up: QuantizedWeight, x, A, activation: str):
+    """(M, N, K, r, activation's number) of a gated call."""
+    if x.dim() != 2 or A.dim() != 3:
+        raise ValueError("x must be 2-D ([M, K]) and A 3-D ([2, r, K])")
+    if (gate.rows, gate.cols, gate.block_size, bool(gate.double_quant)) != (up.rows, up.cols, up.block_size, bool(up.double_quant)):
+        raise ValueError("the gate's and the up projection's weights must agree in shape, block size and double_quant")
+    if up.device != gate.device:
+        raise ValueError(f"the up projection's weight is on {up.device}, the gate's on {gate.device}")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    return int(x.shape[0]), gate.rows, gate.cols, int(A.shape[1]), act
+
+
+@_on_stream
+def gated_fwd(gate: QuantizedWeight, up: QuantizedWeight, x, A, B, alpha: float, activation: str = "silu", bias=None,
+              want_saved: bool = True, out=None, saved: GatedSaved | None = None, workspace: Workspace | None = None):
+    """Gated feed-forward layer h = act(g) * u of two QLoRA linears of x; returns (h, GatedSaved or None).
+
+    g and u are the layers of `gate` and `up` (weights [N, K] of one shape, block size and
+    double_quant); A [2, r, K], B [2, N, r] and bias [2, N] hold the gate's adapter (bias)
+    first.  activation: "silu" or "gelu_tanh".  What a backward needs (g, u and T) is written
+    to `saved`, or to tensors made here unless want_saved is False; a given `saved` without a
+    `t` leaves T out."""
+    import torch
+    dt = _compute_dtype(x)
+    M, N, K, r, act = _gated_shapes(gate, up, x, A, activation)
+    dev = gate.device
+    _fits("x", x, (M, K), x.dtype, dev)
+    _fits("A", A, (2, r, K), x.dtype, dev)
+    _fits("B", B, (2, N, r), x.dtype, dev)
+    _fits("bias", bias, (2, N), x.dtype, dev)
+    _fits("out", out, (M, N), x.dtype, dev)
+    if saved is not None:
+        _fits("saved.pre", saved.pre, (2, M, N), x.dtype, dev)
+        _fits("saved.t", saved.t, (2, M, r), x.dtype, dev)
+    here = _here(dev)
+    need = _workspace_size(OP_GATED_FWD_F32 if dt == NF4_F32 else OP_GATED_FWD, M, N, K, r)
+    ws = _scratch(workspace, dev, here)
+    h = out if out is not None else torch.empty((M, N), dtype=x.dtype, device=dev)
+    if want_saved and saved is None:
+        saved = GatedSaved(torch.empty((2, M, N), dtype=x.dtype, device=dev), torch.empty((2, M, r), dtype=x.dtype, device=dev))
+    with ws.lock:
+        st = lib().qlora_gated_fwd(gate.c_struct(), up.c_struct(), x.data_ptr(), M, A.data_ptr(), B.data_ptr(), r, alpha, act, dt,
+                                   _at(bias), h.data_ptr(), None if saved is None else _at(saved.pre),
+                                   None if saved is None else _at(saved.t), ws.get(need, dev).data_ptr(), need, here)
+    if st:
+        raise NF4Error(st, "qlora_gated_fwd")
+    return h, saved
+
+
+@_on_stream
+def gated_bwd(gate: QuantizedWeight, up: QuantizedWeight, x, A, B, alpha: float, dh, saved: GatedSaved,
+              activation: str = "silu", want_dx: bool = True, dA=None, dB=None, dx=None,
+              workspace: Workspace | None = None):
+    """Adapter backward of gated_fwd from what it saved; returns (dA fp32 [2, r, K],
+    dB fp32 [2, N, r], dx [M, K] in x's dtype or None)."""
+    import torch
+    dt = _compute_dtype(x)
+    M, N, K, r, act = _gated_shapes(gate, up, x, A, activation)
+    dev = gate.device
+    if saved.pre is None:
+        raise ValueError("saved.pre: gated_bwd needs the g and u that gated_fwd saved")
+    _fits("x", x, (M, K), x.dtype, dev)
+    _fits("A", A, (2, r, K), x.dtype, dev)
+    _fits("B", B, (2, N, r), x.dtype, dev)
+    _fits("dh", dh, (M, N), x.dtype, dev)
+    _fits("saved.pre", saved.pre, (2, M, N), x.dtype, dev)
+    _fits("saved.t", saved.t, (2, M, r), x.dtype, dev)
+    _fits("dA", dA, (2, r, K), torch.float32, dev)
+    _fits("dB", dB, (2, N, r), torch.float32, dev)
+    _fits("dx", dx, (M, K), x.dtype, dev)
+    here = _here(dev)
+    need = _workspace_size(OP_GATED_BWD_F32 if dt == NF4_F32 else OP_GATED_BWD, M, N, K, r)
+    ws = _scratch(workspace, dev, here)
+    dA = dA if dA is not None else torch.empty((2, r, K), dtype=torch.float32, device=dev)
+    dB = dB if dB is not None else torch.empty((2, N, r), dtype=torch.float32, device=dev)
+    if want_dx and dx is None:
+        dx = torch.empty((M, K), dtype=x.dtype, device=dev)
+    with ws.lock:
+        st = lib().qlora_gated_bwd(gate.c_struct(), up.c_struct(), x.data_ptr(), M, A.data_ptr(), B.data_ptr(), r, alpha, act, dt,
+                                   dh.data_ptr(), saved.pre.data_ptr(), _at(saved.t), dA.data_ptr(), dB.data_ptr(), _at(dx),
+                                   ws.get(need, dev).data_ptr(), need, here)
+    if st:
+        raise NF4Error(st, "qlora_gated_bwd")
     return dA, dB, dx
 
 
