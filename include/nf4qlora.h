@@ -98,7 +98,8 @@ typedef enum {
   NF4_OP_GATED_FWD = 8,      /* compute types BF16 and F16 */
   NF4_OP_GATED_BWD = 9,
   NF4_OP_GATED_FWD_F32 = 10, /* compute type F32 */
-  NF4_OP_GATED_BWD_F32 = 11
+  NF4_OP_GATED_BWD_F32 = 11,
+  NF4_OP_FP8_LINEAR = 12
 } nf4_op;
 
 /* The gate's activation: x / (1 + exp(-x)), and 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))). */
@@ -177,8 +178,8 @@ NF4_API nf4_status nf4_profile_get(int kernel_id, int64_t* launches, double* tot
  * Bytes of workspace an operation needs (0 = none).  M, N, K, r are the
  * linear-layer sizes (N = W rows, K = W cols); for NF4_OP_QUANTIZE and
  * NF4_OP_DEQUANTIZE pass N = rows, K = cols and M = r = 0; for the grouped
- * operations N is the rows of one expert; for NF4_OP_INT8_LINEAR r,
- * block_size and double_quant are not used.  Needs no GPU.
+ * operations N is the rows of one expert; for NF4_OP_INT8_LINEAR and
+ * NF4_OP_FP8_LINEAR r, block_size and double_quant are not used.  Needs no GPU.
  */
 NF4_API size_t nf4_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int block_size,
                            int double_quant);
@@ -576,6 +577,56 @@ NF4_API nf4_status int8_linear_fwd(const int8_t* w_codes, const float* w_scale, 
                                    const void* x, const float* x_scale, int64_t M, int compute_dtype,
                                    const void* bias, void* y, void* workspace, size_t ws_bytes,
                                    void* stream);
+
+/*
+ * Quantization to 8-bit floating point (e4m3: largest value 448) with one fp32 scale for
+ * each block of 128, for the operands of fp8_linear_fwd.
+ *   x           [rows, cols] of in_dtype (NF4_F32, NF4_BF16, NF4_F16), 16-byte aligned;
+ *               0 <= rows, cols <= 2^30, neither a multiple of anything.
+ *   block_rows  1: a block is 128 columns of one row (activations); 128: of 128 rows (a
+ *               weight, for instance one that nf4_merge made dense).  The last block of a
+ *               row, and the last rows, may be short.
+ *   scales      fp32 [ceil(rows / block_rows), ceil(cols / 128)], 4-byte aligned:
+ *               fp32(max |x| of the block / 448).
+ *   codes       e4m3 [rows, cols], 16-byte aligned: the value nearest to fp32(x / scale),
+ *               ties to even, within -448 .. 448 (both quotients IEEE fp32 divisions).
+ * A block of zeros, or one so small that its scale is 0, has codes 0.  A block that holds
+ * NaN or Inf has scale NaN and codes 0, so what is computed from it is NaN.
+ */
+NF4_API nf4_status fp8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols, int block_rows,
+                                uint8_t* codes, float* scales, void* stream);
+
+/*
+ * The inverse: out = code * scale of its block, one fp32 product, rounded to out_dtype
+ * (NF4_F32, NF4_BF16 or NF4_F16).  Layouts and alignment as in fp8_quantize; out
+ * [rows, cols], 16-byte aligned.
+ */
+NF4_API nf4_status fp8_dequantize(const uint8_t* codes, const float* scales, int64_t rows, int64_t cols,
+                                  int block_rows, int out_dtype, void* out, void* stream);
+
+/*
+ * Linear layer on 8-bit floating point:
+ *   y[m, n] = sum_b x_scale[m, b] w_scale[n / 128, b] (sum over k in block b of x[m, k] w[n, k]) (+ bias[n])
+ * with b the blocks of 128 along K; a block's products are summed in fp32 by the tensor
+ * core, the blocks, scales and bias in fp32, and y is rounded once to compute_dtype.
+ *   w_codes        e4m3 [N, K], w_scale fp32 [ceil(N / 128), ceil(K / 128)] (4-byte
+ *                  aligned): a weight from fp8_quantize with block_rows 128.  N % 8 == 0,
+ *                  K % 16 == 0; M, N, K up to 2^30.
+ *   x, x_scale     x_scale NULL: x is [M, K] of compute_dtype and is quantized in the call
+ *                  exactly as fp8_quantize does with block_rows 1, into the workspace.
+ *                  Otherwise x is e4m3 [M, K] with fp32 scales [M, ceil(K / 128)] (4-byte
+ *                  aligned).  M >= 1.
+ *   compute_dtype  NF4_BF16, NF4_F16 or NF4_F32: type of y, bias and, without x_scale, of x.
+ *   bias           [N] or NULL.
+ *   y              [M, N], written.
+ *   workspace      >= nf4_workspace_bytes(NF4_OP_FP8_LINEAR, M, N, K, 0, 0, 0).
+ * A token that is not finite leaves the others as they are.  It is a serving operator: it
+ * has no backward pass.
+ */
+NF4_API nf4_status fp8_linear_fwd(const uint8_t* w_codes, const float* w_scale, int64_t N, int64_t K,
+                                  const void* x, const float* x_scale, int64_t M, int compute_dtype,
+                                  const void* bias, void* y, void* workspace, size_t ws_bytes,
+                                  void* stream);
 
 #ifdef __cplusplus
 }

@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "nf4_common.cuh"
+#include "fp8.h"
 #include "gated.h"
 #include "kernels.h"
 #include "nvtx_range.h"
@@ -78,6 +79,13 @@ size_t int8_linear_ws(int64_t M, int64_t K) {
   return nf4::kWsHeader + round_up(size_t(M) * size_t(K), 256) + round_up(size_t(M) * sizeof(float), 256);
 }
 
+// 8-bit floating point linear workspace: the header, then the codes and scales of x.
+size_t fp8_linear_ws(int64_t M, int64_t K) {
+  if (M < 0 || K < 0) return nf4::kWsHeader;
+  const size_t blocks = size_t((K + nf4::kFp8Block - 1) / nf4::kFp8Block);
+  return nf4::kWsHeader + round_up(size_t(M) * size_t(K), 256) + round_up(size_t(M) * blocks * sizeof(float), 256);
+}
+
 // Checks shared by the linear entry points.
 nf4_status check_linear(const nf4_weight* w, const void* x, int64_t M, const void* A,
                         const void* B, int r, float alpha, int compute_dtype) {
@@ -125,7 +133,8 @@ const char* const kKernelNames[nf4::kNumKernelIds] = {
     "fused_nf4_gemm_fwd", "fused_nf4_gemm_dx", "nf4_gemv", "nf4_merge", "gemm_f32", "nf4_absmax_max",
     "adapter_gemm_U", "adapter_gemm_dB", "adapter_gemm_dA", "grouped_T", "grouped_fwd", "grouped_U",
     "grouped_dB", "grouped_dA", "grouped_grad", "grouped_dx", "int8_quantize", "int8_linear",
-    "gated_T", "gated_fwd", "gated_U", "gated_dB", "gated_dA", "gated_dx", "gated_act_f32"};
+    "gated_T", "gated_fwd", "gated_U", "gated_dB", "gated_dA", "gated_dx", "gated_act_f32",
+    "fp8_quantize", "fp8_dequantize", "fp8_linear"};
 
 cudaEvent_t prof_event() {
   if (!g_prof_free.empty()) {
@@ -250,6 +259,7 @@ size_t nf4_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int b
     case NF4_OP_GROUPED_FWD: return nf4::kWsHeader + nf4::grouped_workspace_bytes(false, M, N, K, r);
     case NF4_OP_GROUPED_BWD: return nf4::kWsHeader + nf4::grouped_workspace_bytes(true, M, N, K, r);
     case NF4_OP_INT8_LINEAR: return int8_linear_ws(M, K);
+    case NF4_OP_FP8_LINEAR: return fp8_linear_ws(M, K);
     case NF4_OP_GATED_FWD: return nf4::kWsHeader + nf4::gated_workspace_bytes(false, false, M, N, K, r);
     case NF4_OP_GATED_BWD: return nf4::kWsHeader + nf4::gated_workspace_bytes(true, false, M, N, K, r);
     case NF4_OP_GATED_FWD_F32: return nf4::kWsHeader + nf4::gated_workspace_bytes(false, true, M, N, K, r);
@@ -771,6 +781,76 @@ nf4_status qlora_gated_bwd(const nf4_weight* w_gate, const nf4_weight* w_up, con
   a.dx = dx;
   int launches = 0;
   const cudaError_t e = nf4::launch_gated_bwd(a, sm_count(), st, &launches);
+  return finish(e, launches);
+}
+
+}  // extern "C"
+
+extern "C" {
+
+nf4_status fp8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols, int block_rows, uint8_t* codes,
+                        float* scales, void* stream) {
+  NF4_API_RANGE("fp8_quantize");
+  if (in_dtype != NF4_F32 && in_dtype != NF4_BF16 && in_dtype != NF4_F16) return NF4_ERR_INVALID_ARG;
+  if (block_rows != 1 && block_rows != nf4::kFp8Block) return NF4_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 0 || rows > (int64_t(1) << 30) || cols > (int64_t(1) << 30)) return NF4_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return NF4_OK;
+  if (x == nullptr || codes == nullptr || scales == nullptr) return NF4_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned4(scales)) return NF4_ERR_ALIGNMENT;
+  // a block (128 x 128) is a CTA
+  if (block_rows > 1 && (rows + 127) / 128 * ((cols + 127) / 128) > INT32_MAX) return NF4_ERR_SHAPE;
+  int launches = 0;
+  const cudaError_t e = nf4::launch_fp8_quantize(x, in_dtype, rows, cols, block_rows, codes, scales, sm_count(),
+                                                 static_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches);
+}
+
+nf4_status fp8_dequantize(const uint8_t* codes, const float* scales, int64_t rows, int64_t cols, int block_rows,
+                          int out_dtype, void* out, void* stream) {
+  NF4_API_RANGE("fp8_dequantize");
+  if (out_dtype != NF4_F32 && out_dtype != NF4_BF16 && out_dtype != NF4_F16) return NF4_ERR_INVALID_ARG;
+  if (block_rows != 1 && block_rows != nf4::kFp8Block) return NF4_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 0 || rows > (int64_t(1) << 30) || cols > (int64_t(1) << 30)) return NF4_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return NF4_OK;
+  if (codes == nullptr || scales == nullptr || out == nullptr) return NF4_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned4(scales) || !aligned16(out)) return NF4_ERR_ALIGNMENT;
+  int launches = 0;
+  const cudaError_t e = nf4::launch_fp8_dequantize(codes, scales, rows, cols, block_rows, out_dtype, out, sm_count(),
+                                                   static_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches);
+}
+
+nf4_status fp8_linear_fwd(const uint8_t* w_codes, const float* w_scale, int64_t N, int64_t K, const void* x,
+                          const float* x_scale, int64_t M, int compute_dtype, const void* bias, void* y,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  NF4_API_RANGE("fp8_linear_fwd");
+  if (w_codes == nullptr || w_scale == nullptr || x == nullptr || y == nullptr) return NF4_ERR_INVALID_ARG;
+  if (compute_dtype != NF4_BF16 && compute_dtype != NF4_F16 && compute_dtype != NF4_F32)
+    return NF4_ERR_INVALID_ARG;
+  if (M < 1 || N < 1 || K < 16 || N % 8 != 0 || K % 16 != 0 || M > (int64_t(1) << 30) || N > (int64_t(1) << 30) ||
+      K > (int64_t(1) << 30))
+    return NF4_ERR_SHAPE;
+  if (!aligned16(w_codes) || !aligned4(w_scale) || !aligned16(x) || (x_scale && !aligned4(x_scale)) ||
+      !aligned16(y) || (bias && !aligned16(bias)))
+    return NF4_ERR_ALIGNMENT;
+  if (workspace == nullptr || !aligned16(workspace)) return NF4_ERR_WORKSPACE;
+  if (ws_bytes < fp8_linear_ws(M, K)) return NF4_ERR_WORKSPACE;
+  nf4::Fp8LinearArgs a{};
+  a.w = w_codes;
+  a.w_scale = w_scale;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.dtype = compute_dtype;
+  a.bias = bias;
+  a.y = y;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (!status_word(ws, &a.status)) return NF4_ERR_CUDA;
+  uint8_t* codes = ws + nf4::kWsHeader;
+  float* scales = reinterpret_cast<float*>(codes + round_up(size_t(M) * size_t(K), 256));
+  int launches = 0;
+  const cudaError_t e = nf4::launch_fp8_linear(a, x, x_scale, codes, scales, sm_count(),
+                                               static_cast<cudaStream_t>(stream), &launches);
   return finish(e, launches);
 }
 

@@ -1,0 +1,515 @@
+// 8-bit floating point (e4m3) with a scale for each block of 128: the quantizer, its
+// inverse, and the linear layer for few tokens.
+//
+// A block is 128 columns of one row (activations: one scale a token and 128 channels) or of
+// 128 rows (weights).  scale = fp32(max |x| / 448), code = the e4m3 value nearest to
+// v = fp32(x / scale), ties to even; both quotients IEEE fp32 divisions, so the codes do not
+// depend on which kernel made them.
+#include <algorithm>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "fp8.h"
+#include "nf4_common.cuh"
+#include "tc_common.cuh"
+
+namespace nf4 {
+namespace {
+
+using namespace tc;
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+  __device__ static float one(const float* p) { return __ldg(p); }
+  __device__ static void unpack(const uint4& v, float* f) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+  }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  __device__ static void unpack(const uint4& v, float* f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Elem<__half> {
+  __device__ static float one(const __half* p) { return __half2float(*p); }
+  __device__ static void unpack(const uint4& v, float* f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    }
+  }
+};
+template <typename T>
+constexpr int kVec = 16 / int(sizeof(T));   // elements of a 16-byte load
+
+__device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
+
+// A block's scale from the bits of its largest magnitude; NaN if one element is not finite.
+__device__ __forceinline__ float block_scale(uint32_t top) {
+  return top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __fdiv_rn(__uint_as_float(top), 448.0f);
+}
+
+// Two codes (a scale of 0 or NaN gives zeros).
+__device__ __forceinline__ uint32_t codes2(float a, float b, float scale) {
+  if (!(scale > 0.0f)) return 0u;
+  return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t codes4(const float* f, float scale) {
+  return codes2(f[0], f[1], scale) | (codes2(f[2], f[3], scale) << 16);
+}
+
+// ------------------------------------------------------------------ quantize
+
+constexpr int kQThreads = 256;
+
+// Blocks of one row.  VEC: rows start on vector boundaries, and a group of 128 / kVec lanes
+// takes a block; else a warp takes one, element by element.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kQThreads) fp8_rows_kernel(const T* __restrict__ x, int rows, int cols,
+                                                             uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  constexpr int V = VEC ? kVec<T> : 4;
+  constexpr int kLanes = VEC ? kFp8Block / V : 32;
+  constexpr int kGroups = kQThreads / kLanes;
+  grid_dep_wait();
+  const int kb = (cols + kFp8Block - 1) / kFp8Block;
+  const int64_t blocks = int64_t(rows) * kb;
+  const int l = threadIdx.x % kLanes;
+  for (int64_t b = int64_t(blockIdx.x) * kGroups + threadIdx.x / kLanes; b < blocks; b += int64_t(gridDim.x) * kGroups) {
+    const int64_t row = b / kb;
+    const int c0 = int(b - row * kb) * kFp8Block;
+    const int n = min(kFp8Block, cols - c0);
+    const T* src = x + row * cols + c0;
+    uint8_t* dst = codes + row * cols + c0;
+    float f[V];
+    uint32_t top = 0;
+    if (VEC) {
+      const uint4 v = V * l < n ? __ldg(reinterpret_cast<const uint4*>(src) + l) : make_uint4(0u, 0u, 0u, 0u);
+      Elem<T>::unpack(v, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = l + 32 * i < n ? Elem<T>::one(src + l + 32 * i) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = max(top, magnitude(f[i]));
+    const unsigned mask = kLanes == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
+    top = __reduce_max_sync(mask, top);
+    const float s = block_scale(top);
+    if (l == 0) scales[b] = s;
+    if (VEC) {
+      if (V * l < n) {
+        if (V == 4) reinterpret_cast<uint32_t*>(dst)[l] = codes4(f, s);
+        else reinterpret_cast<uint2*>(dst)[l] = make_uint2(codes4(f, s), codes4(f + (V == 8 ? 4 : 0), s));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (l + 32 * i < n) dst[l + 32 * i] = uint8_t(codes2(f[i], 0.0f, s) & 0xffu);
+    }
+  }
+}
+
+// Blocks of 128 x 128, a CTA each, kept in registers between the maximum and the codes.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kQThreads) fp8_tile_kernel(const T* __restrict__ x, int rows, int cols, int kb,
+                                                             uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  constexpr int V = VEC ? kVec<T> : 4;
+  constexpr int kPer = kFp8Block / V;                        // vectors of a row
+  constexpr int kKeep = kFp8Block * kPer / kQThreads;        // and of a thread
+  grid_dep_wait();
+  const int br = blockIdx.x / kb, bc = blockIdx.x - br * kb;
+  const int64_t r0 = int64_t(br) * kFp8Block;
+  const int c0 = bc * kFp8Block;
+  const int t = threadIdx.x;
+  float f[kKeep][V];
+  uint32_t top = 0;
+  if (VEC) {
+    uint4 v[kKeep];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      const int at = t + i * kQThreads, c = c0 + at % kPer * V;
+      const int64_t r = r0 + at / kPer;
+      v[i] = r < rows && c < cols ? __ldg(reinterpret_cast<const uint4*>(x + r * cols + c)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) Elem<T>::unpack(v[i], f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int at = t + (i * V + j) * kQThreads, c = c0 + at % kFp8Block;
+        const int64_t r = r0 + at / kFp8Block;
+        f[i][j] = r < rows && c < cols ? Elem<T>::one(x + r * cols + c) : 0.0f;
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) top = max(top, magnitude(f[i][j]));
+  __shared__ uint32_t part[kQThreads / 32];
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((t & 31) == 0) part[t >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQThreads / 32; ++i) top = max(top, part[i]);
+  const float s = block_scale(top);
+  if (t == 0) scales[blockIdx.x] = s;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    if (VEC) {
+      const int at = t + i * kQThreads, c = c0 + at % kPer * V;
+      const int64_t r = r0 + at / kPer;
+      if (r < rows && c < cols) {
+        uint8_t* dst = codes + r * cols + c;
+        if (V == 4) *reinterpret_cast<uint32_t*>(dst) = codes4(f[i], s);
+        else *reinterpret_cast<uint2*>(dst) = make_uint2(codes4(f[i], s), codes4(f[i] + (V == 8 ? 4 : 0), s));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int at = t + (i * V + j) * kQThreads, c = c0 + at % kFp8Block;
+        const int64_t r = r0 + at / kFp8Block;
+        if (r < rows && c < cols) codes[r * cols + c] = uint8_t(codes2(f[i][j], 0.0f, s) & 0xffu);
+      }
+    }
+  }
+}
+
+void pdl_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned grid, unsigned threads, cudaStream_t st) {
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3(grid, 1, 1);
+  cfg->blockDim = dim3(threads, 1, 1);
+  cfg->stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = prof_on() ? 0 : 1;
+}
+
+template <typename T>
+cudaError_t quantize_t(const void* x, int64_t rows, int64_t cols, int block_rows, uint8_t* codes, float* scales, int sms,
+                       cudaStream_t st) {
+  const T* xt = static_cast<const T*>(x);
+  const bool vec = cols % kVec<T> == 0;
+  const int64_t kb = (cols + kFp8Block - 1) / kFp8Block;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  if (block_rows == 1) {
+    const int64_t per = kQThreads / (vec ? kFp8Block / kVec<T> : 32);
+    pdl_config(&cfg, attr, unsigned(std::min<int64_t>((rows * kb + per - 1) / per, int64_t(sms) * 16)), kQThreads, st);
+    return vec ? cudaLaunchKernelEx(&cfg, fp8_rows_kernel<T, true>, xt, int(rows), int(cols), codes, scales)
+               : cudaLaunchKernelEx(&cfg, fp8_rows_kernel<T, false>, xt, int(rows), int(cols), codes, scales);
+  }
+  const int64_t tiles = (rows + kFp8Block - 1) / kFp8Block * kb;
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  pdl_config(&cfg, attr, unsigned(tiles), kQThreads, st);
+  return vec ? cudaLaunchKernelEx(&cfg, fp8_tile_kernel<T, true>, xt, int(rows), int(cols), int(kb), codes, scales)
+             : cudaLaunchKernelEx(&cfg, fp8_tile_kernel<T, false>, xt, int(rows), int(cols), int(kb), codes, scales);
+}
+
+// ------------------------------------------------------------------ dequantize
+
+__device__ __forceinline__ void put(float* o, float v) { *o = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half* o, float v) { *o = __float2half_rn(v); }
+
+__device__ __forceinline__ float2 values2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(two), __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+
+// VEC: eight codes a thread, in one row (the row length is a multiple of eight).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kQThreads) fp8_dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                                   const float* __restrict__ scales, int64_t rows, int cols,
+                                                                   int row_shift, T* __restrict__ out) {
+  constexpr int V = VEC ? 8 : 1;
+  grid_dep_wait();
+  const int kb = (cols + kFp8Block - 1) / kFp8Block, per = cols / V;
+  const int64_t total = rows * per;
+  for (int64_t i = int64_t(blockIdx.x) * kQThreads + threadIdx.x; i < total; i += int64_t(gridDim.x) * kQThreads) {
+    const int64_t row = i / per;
+    const int c = int(i - row * per) * V;
+    const float s = __ldg(scales + (row >> row_shift) * kb + c / kFp8Block);
+    if (VEC) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes) + i);
+      const uint32_t two[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+      alignas(16) T v[V];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = values2(two[j]);
+        put(&v[(2 * j) % V], __fmul_rn(f.x, s));
+        put(&v[(2 * j + 1) % V], __fmul_rn(f.y, s));
+      }
+      uint4* o = reinterpret_cast<uint4*>(out + i * V);
+#pragma unroll
+      for (int j = 0; j < int(sizeof(v) / 16); ++j) o[j] = reinterpret_cast<const uint4*>(v)[j];
+    } else {
+      put(out + i, __fmul_rn(values2(__ldg(codes + i)).x, s));
+    }
+  }
+}
+
+template <typename T>
+cudaError_t dequantize_t(const uint8_t* codes, const float* scales, int64_t rows, int64_t cols, int block_rows, void* out,
+                         int sms, cudaStream_t st) {
+  const bool vec = cols % 8 == 0;
+  const int64_t work = rows * cols / (vec ? 8 : 1);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  pdl_config(&cfg, attr, unsigned(std::max<int64_t>(1, std::min<int64_t>((work + kQThreads - 1) / kQThreads, int64_t(sms) * 32))),
+             kQThreads, st);
+  const int shift = block_rows == 1 ? 0 : 7;
+  T* o = static_cast<T*>(out);
+  return vec ? cudaLaunchKernelEx(&cfg, fp8_dequantize_kernel<T, true>, codes, scales, rows, int(cols), shift, o)
+             : cudaLaunchKernelEx(&cfg, fp8_dequantize_kernel<T, false>, codes, scales, rows, int(cols), shift, o);
+}
+
+// ------------------------------------------------------------------ linear, few tokens
+
+// y for a few tokens: the weight bytes are the whole cost.  A CTA holds the codes of all
+// tokens in shared memory, quantized here unless they came so, and takes 16 weight rows at
+// a time, its eight warps an eighth of the blocks along K each.  The weight goes from global
+// memory into the A fragments of mma.sync m16n8k32 (e4m3): the k order inside a block is
+// free as long as both operands agree, so a lane's share of a row and block is 32
+// contiguous bytes.  A block's sum is scaled and added in fp32; the warps meet in shared
+// memory.
+constexpr int kSmWarps = 8;
+constexpr int kSmThreads = 32 * kSmWarps;
+constexpr int kSmAhead = 4;                        // blocks whose loads are in flight
+constexpr int64_t kSmMaxCodes = 96 * 1024;         // M * K: two CTAs an SM
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void store_y(const Fp8LinearArgs& a, int64_t m, int64_t n, float v) {
+  const int64_t at = m * a.N + n;
+  if (a.dtype == NF4_F32) {
+    if (a.bias != nullptr) v = __fadd_rn(v, static_cast<const float*>(a.bias)[n]);
+    static_cast<float*>(a.y)[at] = v;
+  } else if (a.dtype == NF4_F16) {
+    if (a.bias != nullptr) v = __fadd_rn(v, __half2float(static_cast<const __half*>(a.bias)[n]));
+    static_cast<__half*>(a.y)[at] = __float2half_rn(v);
+  } else {
+    if (a.bias != nullptr) v = __fadd_rn(v, __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[n]));
+    static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+  }
+}
+
+// Shared memory: codes [8 NT][kb * 128 + 16] (16: a token's rows start in other banks),
+// scales [kb][8 NT], partial sums [warp][16 rows][8 NT].
+__host__ __device__ constexpr size_t small_smem(int nt, int kb) {
+  return size_t(8 * nt) * (size_t(kb) * 128 + 16) + size_t(kb) * 8 * nt * 4 + size_t(kSmWarps) * 16 * 8 * nt * 4;
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(kSmThreads) fp8_small_kernel(const Fp8LinearArgs a, const T* __restrict__ x,
+                                                               const float* __restrict__ given_scale) {
+  extern __shared__ __align__(16) uint8_t codes[];
+  constexpr int NP = 8 * NT;
+  const int K = int(a.K), M = int(a.M);
+  const int kb = (K + kFp8Block - 1) / kFp8Block;
+  const int stride = kb * 128 + 16;
+  float* sx = reinterpret_cast<float*>(codes + size_t(NP) * stride);
+  float* part = sx + kb * NP;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, q = lane & 3;
+  grid_dep_wait();
+  const int groups = int((a.N + 15) / 16);
+  const int b0 = kb * warp / kSmWarps, b1 = kb * (warp + 1) / kSmWarps;   // this warp's blocks
+  uint4 wv[kSmAhead][2][2];                        // block, row (g, g + 8), half of its 32 bytes
+  auto load_w = [&](int grp, int b) {
+#pragma unroll
+    for (int j = 0; j < kSmAhead; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t n = min(int64_t(grp) * 16 + 8 * h + g, a.N - 1);
+        const int k = (b + j) * kFp8Block + 32 * q;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          wv[j][h][i] = b + j < b1 && k + 16 * i < K ? __ldg(reinterpret_cast<const uint4*>(a.w + n * K + k + 16 * i))
+                                                    : make_uint4(0u, 0u, 0u, 0u);
+      }
+  };
+  int grp = blockIdx.x;
+  load_w(grp, b0);
+
+  for (int i = warp; i < NP * kb; i += kSmWarps) {
+    const int m = i / kb, b = i - m * kb;
+    uint32_t c = 0;
+    float s = 0.0f;
+    if (m < M) {
+      const int k = b * kFp8Block + 4 * lane;      // K is a multiple of 16
+      if constexpr (sizeof(T) == 1) {
+        if (k < K) c = __ldg(reinterpret_cast<const uint32_t*>(x + int64_t(m) * K + k));
+        s = __ldg(given_scale + int64_t(m) * kb + b);
+      } else {
+        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (k < K) {
+          if constexpr (sizeof(T) == 4) {
+            Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(x + int64_t(m) * K + k)), f);
+          } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(x + int64_t(m) * K + k));
+            float e[8];
+            Elem<T>::unpack(make_uint4(v.x, v.y, 0u, 0u), e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = e[j];
+          }
+        }
+        const uint32_t top = max(max(magnitude(f[0]), magnitude(f[1])), max(magnitude(f[2]), magnitude(f[3])));
+        s = block_scale(__reduce_max_sync(0xffffffffu, top));
+        c = codes4(f, s);
+      }
+    }
+    *reinterpret_cast<uint32_t*>(codes + m * stride + b * kFp8Block + 4 * lane) = c;
+    if (lane == 0) sx[b * NP + m] = s;
+  }
+  __syncthreads();
+
+  for (; grp < groups; grp += gridDim.x) {
+    float acc[NT][4];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.0f;
+    const float* ws = a.w_scale + int64_t(grp / 8) * kb;   // sixteen rows lie in one block of 128
+    for (int b = b0; b < b1; b += kSmAhead) {
+#pragma unroll
+      for (int j = 0; j < kSmAhead; ++j) {
+        if (b + j >= b1) break;
+        const float sw = __ldg(ws + b + j);
+        const uint32_t r0[8] = {wv[j][0][0].x, wv[j][0][0].y, wv[j][0][0].z, wv[j][0][0].w,
+                                wv[j][0][1].x, wv[j][0][1].y, wv[j][0][1].z, wv[j][0][1].w};
+        const uint32_t r1[8] = {wv[j][1][0].x, wv[j][1][0].y, wv[j][1][0].z, wv[j][1][0].w,
+                                wv[j][1][1].x, wv[j][1][1].y, wv[j][1][1].z, wv[j][1][1].w};
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          const uint4* xc = reinterpret_cast<const uint4*>(codes + (8 * c + g) * stride + (b + j) * kFp8Block + 32 * q);
+          const uint4 x0 = xc[0], x1 = xc[1];
+          const uint32_t xw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma_e4m3(d, r0[2 * i], r1[2 * i], r0[2 * i + 1], r1[2 * i + 1], xw[2 * i], xw[2 * i + 1]);
+          const float2 s = *reinterpret_cast<const float2*>(sx + (b + j) * NP + 8 * c + 2 * q);
+          acc[c][0] = fmaf(d[0], s.x * sw, acc[c][0]);
+          acc[c][1] = fmaf(d[1], s.y * sw, acc[c][1]);
+          acc[c][2] = fmaf(d[2], s.x * sw, acc[c][2]);
+          acc[c][3] = fmaf(d[3], s.y * sw, acc[c][3]);
+        }
+      }
+      if (b + kSmAhead < b1) load_w(grp, b + kSmAhead);
+    }
+    if (grp + int(gridDim.x) < groups) load_w(grp + int(gridDim.x), b0);
+    float* mine = part + warp * (16 * NP);         // [token][row]
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      mine[(8 * c + 2 * q) * 16 + g] = acc[c][0];
+      mine[(8 * c + 2 * q + 1) * 16 + g] = acc[c][1];
+      mine[(8 * c + 2 * q) * 16 + g + 8] = acc[c][2];
+      mine[(8 * c + 2 * q + 1) * 16 + g + 8] = acc[c][3];
+    }
+    __syncthreads();
+    for (int i = t; i < 16 * M; i += kSmThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int wp = 0; wp < kSmWarps; ++wp) v += part[wp * (16 * NP) + i];
+      const int64_t n = int64_t(grp) * 16 + (i & 15);
+      if (n < a.N) store_y(a, i >> 4, n, v);
+    }
+    __syncthreads();   // part may be written again
+  }
+}
+
+template <typename T, int NT>
+cudaError_t small_tn(const Fp8LinearArgs& a, const void* x, const float* scale, int sms, cudaStream_t st) {
+  static PerDeviceOnce attr_done;
+  const int dev = PerDeviceOnce::current();
+  if (!attr_done.done(dev)) {
+    const cudaError_t e = cudaFuncSetAttribute(fp8_small_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    if (e != cudaSuccess) return e;
+    attr_done.mark(dev);
+  }
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  pdl_config(&cfg, attr, unsigned(std::min<int64_t>((a.N + 15) / 16, 2 * int64_t(sms))), kSmThreads, st);
+  cfg.dynamicSmemBytes = small_smem(NT, int((a.K + kFp8Block - 1) / kFp8Block));
+  return cudaLaunchKernelEx(&cfg, fp8_small_kernel<T, NT>, a, static_cast<const T*>(x), scale);
+}
+template <typename T>
+cudaError_t small_t(const Fp8LinearArgs& a, const void* x, const float* scale, int sms, cudaStream_t st) {
+  return a.M <= 8 ? small_tn<T, 1>(a, x, scale, sms, st) : a.M <= 16 ? small_tn<T, 2>(a, x, scale, sms, st)
+                                                                     : small_tn<T, 4>(a, x, scale, sms, st);
+}
+
+bool use_small(const Fp8LinearArgs& a) { return a.M <= 32 && ((a.M + 7) / 8 * 8) * a.K <= kSmMaxCodes; }
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols, int block_rows, uint8_t* codes,
+                                float* scales, int sms, cudaStream_t st, int* launches) {
+  NF4_PROF_BEGIN(st, kKFp8Quantize);
+  cudaError_t e = in_dtype == NF4_F32   ? quantize_t<float>(x, rows, cols, block_rows, codes, scales, sms, st)
+                  : in_dtype == NF4_F16 ? quantize_t<__half>(x, rows, cols, block_rows, codes, scales, sms, st)
+                                        : quantize_t<__nv_bfloat16>(x, rows, cols, block_rows, codes, scales, sms, st);
+  NF4_PROF_END(st, kKFp8Quantize);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+cudaError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int64_t rows, int64_t cols, int block_rows,
+                                  int out_dtype, void* out, int sms, cudaStream_t st, int* launches) {
+  NF4_PROF_BEGIN(st, kKFp8Dequantize);
+  cudaError_t e = out_dtype == NF4_F32   ? dequantize_t<float>(codes, scales, rows, cols, block_rows, out, sms, st)
+                  : out_dtype == NF4_F16 ? dequantize_t<__half>(codes, scales, rows, cols, block_rows, out, sms, st)
+                                         : dequantize_t<__nv_bfloat16>(codes, scales, rows, cols, block_rows, out, sms, st);
+  NF4_PROF_END(st, kKFp8Dequantize);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+cudaError_t launch_fp8_linear(const Fp8LinearArgs& given, const void* x, const float* x_scale, uint8_t* codes,
+                              float* scales, int sms, cudaStream_t st, int* launches) {
+  Fp8LinearArgs a = given;
+  if (use_small(a)) {
+    NF4_PROF_BEGIN(st, kKFp8Linear);
+    cudaError_t e = x_scale != nullptr   ? small_t<uint8_t>(a, x, x_scale, sms, st)
+                    : a.dtype == NF4_F32 ? small_t<float>(a, x, nullptr, sms, st)
+                    : a.dtype == NF4_F16 ? small_t<__half>(a, x, nullptr, sms, st)
+                                         : small_t<__nv_bfloat16>(a, x, nullptr, sms, st);
+    NF4_PROF_END(st, kKFp8Linear);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess) ++*launches;
+    return e;
+  }
+  a.x = x_scale != nullptr ? static_cast<const uint8_t*>(x) : codes;
+  a.x_scale = x_scale != nullptr ? x_scale : scales;
+  Fp8Gemm g;
+  if (!g.prepare(a, sms)) return cudaErrorInvalidValue;
+  if (x_scale == nullptr) {
+    const cudaError_t e = launch_fp8_quantize(x, a.dtype, a.M, a.K, 1, codes, scales, sms, st, launches);
+    if (e != cudaSuccess) return e;
+  }
+  return g.run(st, launches);
+}
+
+}  // namespace nf4

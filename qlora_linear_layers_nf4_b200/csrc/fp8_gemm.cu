@@ -1,0 +1,391 @@
+// The 8-bit floating point linear on the sm_100a tensor cores:
+//   y[m, n] = sum_b sx[m, b] sw[n / 128, b] (sum_{k in block b} wq[n, k] xq[m, k]) (+ bias[n])
+//
+// Tokens on the TMEM lanes (A), weight rows as N (B), both K-major e4m3 by TMA; a ring stage
+// is one block of 128 along K, four kind::f8f6f4 MMAs.  The scales change from block to
+// block, so the MMAs of a block start a fresh accumulator, one of two that alternate, and
+// the epilogue warps add it to fp32 sums in registers, one FMA an element with the product
+// of the two scales: a lane is a token and the columns of a warp lie in one weight block, so
+// that product is one number per thread and block.
+//
+// Wide tiles are 256 x 256 by a pair of CTAs (cta_group::2): the MMAs of a block take 512
+// cycles, reading the accumulator (128 x 256 of it in each CTA) 256 and the FMAs 256, on
+// eight warps of 128 columns each.  Where such tiles would leave SMs idle, a CTA takes
+// 128 x 128, 64 or 32.
+// Roles: warp 0 token TMA, warp 1 weight TMA, warp 2 MMA (the pair's leader issues), from
+// warp 4 on the sums.  Output in pieces of 32 x 32 through swizzled shared memory by TMA.
+#include <algorithm>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fp8.h"
+#include "nf4_common.cuh"
+#include "nf4_dequant.cuh"
+#include "pair_tile.cuh"
+#include "ring_wait.cuh"
+#include "tc_common.cuh"
+#include "tensor_maps.h"
+
+namespace nf4 {
+namespace {
+
+using namespace tc;
+using namespace expert;
+
+constexpr int kEpiWarp = 4;
+constexpr uint32_t kXBytes = 128 * 128;
+constexpr uint32_t kStageOut = 4096;     // of a warp: two 32 x 32 pieces of 16 bits, or one of 32
+
+template <int NT>
+struct Cfg {
+  static constexpr int kPair = NT == 256 ? 2 : 1;                 // CTAs of a tile
+  static constexpr int kRows = 128 * kPair;                       // tokens of a tile
+  static constexpr int kCols = NT > 128 ? 128 : NT;               // columns of a warp
+  static constexpr int kEpiWarps = NT == 256 ? 8 : 4;
+  static constexpr int kThreads = 32 * (kEpiWarp + kEpiWarps);
+  static constexpr uint32_t kWBytes = uint32_t(NT / kPair) * 128;
+  static constexpr uint32_t kStage = kXBytes + kWBytes;
+  static constexpr int kStages = 6;
+  static constexpr uint32_t kTmem = NT == 256 ? 512 : 2 * NT;
+};
+
+struct Fp8Shared {
+  uint64_t full[6];
+  uint64_t empty[6];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+};
+template <int NT>
+constexpr size_t fp8_smem() {
+  return size_t(Cfg<NT>::kStages) * Cfg<NT>::kStage + Cfg<NT>::kEpiWarps * kStageOut + sizeof(Fp8Shared) + 1024;
+}
+static_assert(fp8_smem<256>() <= 232448, "shared memory of one CTA");
+
+// e4m3 x e4m3 -> fp32 (kind::f8f6f4, both K-major).
+template <int PAIR>
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  if (PAIR == 2) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+constexpr uint32_t idesc_e4m3(int M, int N) { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
+
+template <int NT>
+__device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& my, const Fp8Params& p) {
+  using C = Cfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = expert::align_1024(smem_raw);
+  uint8_t* out_base = smem + C::kStages * C::kStage;
+  Fp8Shared* sh = reinterpret_cast<Fp8Shared*>(out_base + C::kEpiWarps * kStageOut);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = C::kPair == 2 ? cluster_ctarank() : 0u;
+  volatile uint32_t* abort_flag = &sh->abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh->acc_full[b], 1);
+      mbar_init(&sh->acc_empty[b], C::kEpiWarps * C::kPair);   // leader: both CTAs' warps
+    }
+    mbar_init(&sh->drain, 1);
+    sh->abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch(&mx);
+    tma_prefetch(&mw);
+    tma_prefetch(&my);
+  }
+  if (warp == 2) {
+    if (C::kPair == 2) {
+      tmem_alloc_pair(&sh->tmem_base, C::kTmem);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&sh->tmem_base, C::kTmem);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  if (C::kPair == 2) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  const int first = int(blockIdx.x) / C::kPair, step = int(gridDim.x) / C::kPair;
+  auto leader_bar = [&](uint64_t* bar) { return C::kPair == 2 ? mapa_shared(smem_u32(bar), 0) : smem_u32(bar); };
+  grid_dep_wait();
+
+  if (warp < 2) {
+    // ---------------- TMA: tokens (warp 0, which expects every byte of a stage) and weight
+    const bool issue = elect_one();
+    bool ok = true;
+    int s = 0, issued = 0;
+    uint32_t ph = 1;
+    for (int id = first; id < p.tiles && ok; id += step) {
+      const int ct = id / p.row_tiles, rt = id - ct * p.row_tiles;
+      const int y = warp == 0 ? rt * C::kRows + 128 * int(rank) : ct * NT + (NT / C::kPair) * int(rank);
+      for (int b = 0; b < p.kb; ++b) {
+        ok = ring_wait(&sh->empty[s], ph, abort_flag, p.status);
+        if (!ok) break;
+        if (issue) {
+          uint8_t* dst = smem + s * C::kStage + (warp == 0 ? 0u : kXBytes);
+          if (warp == 0 && rank == 0) mbar_arrive_expect_tx(&sh->full[s], C::kPair * C::kStage);
+          if (C::kPair == 2) tma_load_2d_pair(dst, warp == 0 ? &mx : &mw, leader_bar(&sh->full[s]), b * 128, y);
+          else tma_load_2d(dst, warp == 0 ? &mx : &mw, &sh->full[s], b * 128, y);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == C::kStages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (*abort_flag)   // unwind: wait (bounded) for the stages in flight
+      for (int j = max(0, issued - C::kStages); j < issued; ++j) {
+        uint32_t none = 0;
+        ring_wait(&sh->empty[j % C::kStages], (j / C::kStages) & 1, &none, nullptr);
+      }
+  } else if (warp == 2) {
+    // ---------------- MMA
+    if (rank == 0) {
+      const bool issue = elect_one();
+      const uint64_t x_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t w_desc = smem_desc_sw128(smem_u32(smem) + kXBytes, 16, 1024);
+      constexpr uint32_t idesc = idesc_e4m3(C::kRows, NT);
+      bool ok = true;
+      int s = 0, n = 0;
+      uint32_t ph = 0;
+      for (int id = first; id < p.tiles && ok; id += step) {
+        for (int b = 0; b < p.kb; ++b, ++n) {
+          ok = mbar_wait_cluster(&sh->acc_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, p.status);
+          if (ok) ok = mbar_wait_cluster(&sh->full[s], ph, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (issue) {
+            const uint32_t d = tmem + uint32_t(n & 1) * uint32_t(NT);
+            const uint32_t at = uint32_t(s) * (C::kStage >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_f8<C::kPair>(d, x_desc + at + kk * 2, w_desc + at + kk * 2, idesc, kk > 0 ? 1u : 0u);
+            // one commit a block: the warps that read the accumulator give the stage back
+            if (C::kPair == 2) umma_commit_pair_mc(&sh->acc_full[n & 1], 0x3);
+            else umma_commit(&sh->acc_full[n & 1]);
+          }
+          __syncwarp();
+          if (++s == C::kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok && issue) {   // unwind: wait (bounded) for the MMAs in flight
+        if (C::kPair == 2) umma_commit_pair_mc(&sh->drain, 0x1);
+        else umma_commit(&sh->drain);
+        uint32_t none = 0;
+        ring_wait(&sh->drain, 0, &none, nullptr);
+      }
+    }
+  } else if (warp >= kEpiWarp) {
+    // ---------------- sums: lane = token, C::kCols columns a warp
+    const int quad = warp & 3, half = (warp - kEpiWarp) >> 2;
+    uint8_t* buf = out_base + (warp - kEpiWarp) * kStageOut;
+    int s = 0, n = 0;
+    uint32_t pieces = 0;   // stored so far: they alternate between the two halves of buf
+    bool ok = true;
+    for (int id = first; id < p.tiles && ok; id += step) {
+      const int ct = id / p.row_tiles, rt = id - ct * p.row_tiles;
+      const int row0 = rt * C::kRows + 128 * int(rank) + quad * 32, col0 = ct * NT + half * C::kCols;
+      const float* sx = p.x_scale + int64_t(min(row0 + lane, p.M - 1)) * p.kb;
+      const float* sw = p.w_scale + int64_t(min(col0, p.N - 1) / 128) * p.kb;
+      float acc[C::kCols];
+#pragma unroll
+      for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
+      float scale = __ldg(sx) * __ldg(sw);
+      for (int b = 0; b < p.kb; ++b, ++n) {
+        const int nb = min(b + 1, p.kb - 1);
+        const float nx = __ldg(sx + nb), nw = __ldg(sw + nb);
+        ok = warp_wait(&sh->acc_full[n & 1], (n >> 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        if (warp == kEpiWarp && lane == 0) mbar_arrive(&sh->empty[s]);
+        if (++s == C::kStages) s = 0;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < C::kCols; c += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + uint32_t(n & 1) * uint32_t(NT) + half * C::kCols + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), scale, acc[c + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (C::kPair == 2) arrive_leader(leader_bar(&sh->acc_empty[n & 1]));
+          else mbar_arrive(&sh->acc_empty[n & 1]);
+        }
+        scale = nx * nw;
+      }
+      if (!ok) break;
+      // ---- bias, rounding, 32 x 32 pieces through shared memory
+#pragma unroll
+      for (int c = 0; c < C::kCols; c += 32) {
+        const int col = col0 + c;
+        if (col >= p.N || row0 >= p.M) break;
+        if (p.bias != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int at = min(col + i, p.N - 1);
+            acc[c + i] += p.dtype == NF4_F32   ? __ldg(static_cast<const float*>(p.bias) + at)
+                          : p.dtype == NF4_F16 ? __half2float(static_cast<const __half*>(p.bias)[at])
+                                               : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[at]);
+          }
+        }
+        const bool wide = p.dtype == NF4_F32;
+        uint8_t* piece = buf + (wide ? 0u : (pieces++ & 1u) * 2048u);
+        if (lane == 0) {   // the store that used the piece has read it
+          if (wide) bulk_wait_group_read<0>();
+          else bulk_wait_group_read<1>();
+        }
+        __syncwarp();
+        if (wide) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(piece + sw128_offset(uint32_t(lane), uint32_t(j))) =
+                make_float4(acc[c + 4 * j], acc[c + 4 * j + 1], acc[c + 4 * j + 2], acc[c + 4 * j + 3]);
+        } else {
+          const bool f16 = p.dtype == NF4_F16;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)   // 64-byte rows, 64-byte swizzle: chunk j at j ^ ((row >> 1) & 3)
+            *reinterpret_cast<uint4*>(piece + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pack2(f16, acc[c + 8 * j], acc[c + 8 * j + 1]), pack2(f16, acc[c + 8 * j + 2], acc[c + 8 * j + 3]),
+                           pack2(f16, acc[c + 8 * j + 4], acc[c + 8 * j + 5]), pack2(f16, acc[c + 8 * j + 6], acc[c + 8 * j + 7]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&my, piece, col, row0);   // rows past M, columns past N: clipped
+          bulk_commit_group();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group_all();
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (C::kPair == 2) cluster_sync();
+  else __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    if (C::kPair == 2) tmem_dealloc_pair(tmem, C::kTmem);
+    else tmem_dealloc(tmem, C::kTmem);
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<256>::kThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+                    const __grid_constant__ CUtensorMap my, const Fp8Params p) {
+  fp8_gemm_body<256>(mx, mw, my, p);
+}
+template <int NT>
+__global__ void __launch_bounds__(Cfg<NT>::kThreads, 1)
+    fp8_tile_gemm_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+                         const __grid_constant__ CUtensorMap my, const Fp8Params p) {
+  fp8_gemm_body<NT>(mx, mw, my, p);
+}
+
+PerDeviceOnce g_attr_done;
+
+cudaError_t set_attrs() {
+  const int dev = PerDeviceOnce::current();
+  if (g_attr_done.done(dev)) return cudaSuccess;
+  const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel, attr, int(fp8_smem<256>()));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_tile_gemm_kernel<128>, attr, int(fp8_smem<128>()));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_tile_gemm_kernel<64>, attr, int(fp8_smem<64>()));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_tile_gemm_kernel<32>, attr, int(fp8_smem<32>()));
+  if (e == cudaSuccess) g_attr_done.mark(dev);
+  return e;
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+bool Fp8Gemm::prepare(const Fp8LinearArgs& a, int sms) {
+  const uint64_t M = uint64_t(a.M), N = uint64_t(a.N), K = uint64_t(a.K);
+  // The widest tile that still gives every SM one.
+  tile_n = 32;
+  const int64_t row_tiles = cdiv(a.M, 128);
+  if (cdiv(a.M, 256) * cdiv(a.N, 256) * 2 >= sms && a.M > 128) tile_n = 256;
+  else if (row_tiles * cdiv(a.N, 128) >= sms) tile_n = 128;
+  else if (row_tiles * cdiv(a.N, 64) >= sms) tile_n = 64;
+  const int pair = tile_n == 256 ? 2 : 1;
+  const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B;
+  bool ok = encode_map_2d(&mx, a.x, MapElem::kU8, K, M, 128, 128, s128) &&
+            encode_map_2d(&mw, a.w, MapElem::kU8, K, N, 128, uint32_t(tile_n / pair), s128);
+  ok = ok && (a.dtype == NF4_F32 ? make_map_2d_f32(&my, a.y, N, M, 32, 32, s128)
+                                 : encode_map_2d(&my, a.y, MapElem::k16, N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B));
+  p = Fp8Params{};
+  p.M = int(a.M);
+  p.N = int(a.N);
+  p.kb = int(cdiv(a.K, kFp8Block));
+  p.row_tiles = int(cdiv(a.M, 128 * pair));
+  const int64_t tiles = int64_t(p.row_tiles) * cdiv(a.N, tile_n);
+  p.tiles = int(tiles);
+  p.dtype = a.dtype;
+  p.w_scale = a.w_scale;
+  p.x_scale = a.x_scale;
+  p.bias = a.bias;
+  p.status = a.status;
+  grid = unsigned(pair * std::min<int64_t>(tiles, std::max(sms / pair, 1)));
+  return ok && tiles <= int64_t(0x7fffffff);
+}
+
+cudaError_t Fp8Gemm::run(cudaStream_t st, int* launches) const {
+  cudaError_t e = set_attrs();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = prof_on() ? 0 : 1;
+  NF4_PROF_BEGIN(st, kKFp8Linear);
+  auto go = [&](auto kernel, int threads, size_t smem) {
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelEx(&cfg, kernel, mx, mw, my, p);
+  };
+  e = tile_n == 256   ? go(fp8_pair_kernel, Cfg<256>::kThreads, fp8_smem<256>())
+      : tile_n == 128 ? go(fp8_tile_gemm_kernel<128>, Cfg<128>::kThreads, fp8_smem<128>())
+      : tile_n == 64  ? go(fp8_tile_gemm_kernel<64>, Cfg<64>::kThreads, fp8_smem<64>())
+                      : go(fp8_tile_gemm_kernel<32>, Cfg<32>::kThreads, fp8_smem<32>());
+  NF4_PROF_END(st, kKFp8Linear);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+}  // namespace nf4

@@ -208,6 +208,9 @@ enum KernelId {
   kKGatedDA,         // dA_p = U_p^T x
   kKGatedDx,         // dx
   kKGatedAct,        // the elementwise products of the fp32 mode
+  kKFp8Quantize,
+  kKFp8Dequantize,
+  kKFp8Linear,
   kNumKernelIds
 };
 

@@ -25,6 +25,7 @@ NF4_F32, NF4_BF16, NF4_F16 = 0, 1, 2
 OP_QUANTIZE, OP_DEQUANTIZE, OP_LINEAR_FWD, OP_LINEAR_BWD, OP_MERGE = 0, 1, 2, 3, 4
 OP_GROUPED_FWD, OP_GROUPED_BWD, OP_INT8_LINEAR = 5, 6, 7
 OP_GATED_FWD, OP_GATED_BWD, OP_GATED_FWD_F32, OP_GATED_BWD_F32 = 8, 9, 10, 11
+OP_FP8_LINEAR = 12
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 
 EXPORTED = (
@@ -34,7 +35,7 @@ EXPORTED = (
     "nf4_dequantize", "qlora_linear_fwd", "qlora_linear_bwd", "nf4_quantize_noalloc",
     "nf4_merge", "nf4_quantize_typed", "nf4_check_wait_timeout", "nf4_absmax_max",
     "nf4_double_quant", "qlora_grouped_fwd", "qlora_grouped_bwd", "int8_quantize", "int8_linear_fwd",
-    "qlora_gated_fwd", "qlora_gated_bwd",
+    "qlora_gated_fwd", "qlora_gated_bwd", "fp8_quantize", "fp8_dequantize", "fp8_linear_fwd",
     "nf4_status_on_device", "nf4_read_device_status",
 )
 
@@ -129,6 +130,12 @@ def lib() -> ctypes.CDLL:
     L.int8_quantize.restype = i32
     L.int8_linear_fwd.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, sz, vp]
     L.int8_linear_fwd.restype = i32
+    L.fp8_quantize.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp]
+    L.fp8_quantize.restype = i32
+    L.fp8_dequantize.argtypes = [vp, vp, i64, i64, i32, i32, vp, vp]
+    L.fp8_dequantize.restype = i32
+    L.fp8_linear_fwd.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, sz, vp]
+    L.fp8_linear_fwd.restype = i32
     L.nf4_status_on_device.argtypes = [i32]
     L.nf4_status_on_device.restype = i32
     L.nf4_read_device_status.argtypes = [vp]
@@ -802,4 +809,118 @@ def int8_linear_fwd(w: Int8Matrix, x, bias=None, out_dtype=None, out=None,
                                    y.data_ptr(), ws.get(need, dev).data_ptr(), need, here)
     if st:
         raise NF4Error(st, "int8_linear_fwd")
+    return y
+
+
+@dataclass
+class Fp8Matrix:
+    """Device tensors of a matrix in 8-bit floating point with one scale for each block of
+    128 columns and `block_rows` rows."""
+    codes: object                    # float8_e4m3fn [rows, cols]
+    scale: object                    # fp32 [ceil(rows / block_rows), ceil(cols / 128)]
+    block_rows: int                  # 1 (activations) or 128 (weights)
+
+
+def _fp8_blocks(rows: int, cols: int, block_rows: int):
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    return -(-rows // block_rows), -(-cols // 128)
+
+
+def _fp8_fits(name: str, q: Fp8Matrix, rows: int, cols: int, device):
+    import torch
+    _fits(name + ".codes", q.codes, (rows, cols), torch.float8_e4m3fn, device)
+    _fits(name + ".scale", q.scale, _fp8_blocks(rows, cols, q.block_rows), torch.float32, device)
+
+
+@_on_stream
+def fp8_quantize(x, block_rows: int = 1, codes=None, scale=None) -> Fp8Matrix:
+    """Quantize a 2-D float32, bfloat16 or float16 CUDA tensor to e4m3, one scale for each
+    128 columns of a row (block_rows 1: activations) or of 128 rows (128: a weight)."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D ([rows, cols])")
+    dt = _compute_dtype(x)
+    rows, cols = int(x.shape[0]), int(x.shape[1])
+    blocks = _fp8_blocks(rows, cols, block_rows)
+    _fits("x", x, (rows, cols), x.dtype, x.device)
+    _fits("codes", codes, (rows, cols), torch.float8_e4m3fn, x.device)
+    _fits("scale", scale, blocks, torch.float32, x.device)
+    here = _here(x.device)
+    codes = codes if codes is not None else torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
+    scale = scale if scale is not None else torch.empty(blocks, dtype=torch.float32, device=x.device)
+    st = lib().fp8_quantize(x.data_ptr(), dt, rows, cols, block_rows, codes.data_ptr(), scale.data_ptr(), here)
+    if st:
+        raise NF4Error(st, "fp8_quantize")
+    return Fp8Matrix(codes, scale, block_rows)
+
+
+@_on_stream
+def fp8_dequantize(q: Fp8Matrix, out_dtype=None, out=None):
+    """The matrix that the codes and scales stand for, in float32 unless out_dtype (bfloat16,
+    float16) or the dtype of `out` says otherwise."""
+    import torch
+    if q.codes.dim() != 2:
+        raise ValueError("codes must be 2-D ([rows, cols])")
+    rows, cols = int(q.codes.shape[0]), int(q.codes.shape[1])
+    dev = q.codes.device
+    _fp8_fits("q", q, rows, cols, dev)
+    if out_dtype is None:
+        out_dtype = torch.float32 if out is None else out.dtype
+    _fits("out", out, (rows, cols), out_dtype, dev)
+    here = _here(dev)
+    out = out if out is not None else torch.empty((rows, cols), dtype=out_dtype, device=dev)
+    st = lib().fp8_dequantize(q.codes.data_ptr(), q.scale.data_ptr(), rows, cols, q.block_rows, _compute_dtype(out),
+                              out.data_ptr(), here)
+    if st:
+        raise NF4Error(st, "fp8_dequantize")
+    return out
+
+
+@_on_stream
+def fp8_linear_fwd(w: Fp8Matrix, x, bias=None, out_dtype=None, out=None, workspace: Workspace | None = None):
+    """y = x w^T (+ bias), [M, N], of a weight in e4m3 with 128 x 128 blocks.
+
+    x is a bfloat16, float16 or float32 tensor [M, K], quantized in the call with a scale per
+    token and 128 channels (y comes back in its dtype), or an Fp8Matrix with block_rows 1 (y in
+    `out_dtype`, bfloat16 unless given)."""
+    import torch
+    if w.codes.dim() != 2:
+        raise ValueError("w.codes must be 2-D ([N, K])")
+    if w.block_rows != 128:
+        raise ValueError("w must have blocks of 128 rows (fp8_quantize with block_rows=128)")
+    N, K = int(w.codes.shape[0]), int(w.codes.shape[1])
+    dev = w.codes.device
+    _fp8_fits("w", w, N, K, dev)
+    if isinstance(x, Fp8Matrix):
+        if x.block_rows != 1:
+            raise ValueError("x must have a scale per row (fp8_quantize with block_rows=1)")
+        xv, xs = x.codes, x.scale
+        y_dtype = out_dtype if out_dtype is not None else torch.bfloat16
+    else:
+        xv, xs = x, None
+        y_dtype = x.dtype
+        if out_dtype is not None and out_dtype != y_dtype:
+            raise TypeError(f"out_dtype: {out_dtype}, but a {y_dtype} x gives a {y_dtype} y")
+    dt = {torch.bfloat16: NF4_BF16, torch.float16: NF4_F16, torch.float32: NF4_F32}.get(y_dtype)
+    if dt is None:
+        raise TypeError(f"compute dtype must be bfloat16, float16 or float32, got {y_dtype}")
+    if xv.dim() != 2:
+        raise ValueError("x must be 2-D ([M, K])")
+    M = int(xv.shape[0])
+    if xs is None:
+        _fits("x", xv, (M, K), y_dtype, dev)
+    else:
+        _fp8_fits("x", x, M, K, dev)
+    _fits("bias", bias, (N,), y_dtype, dev)
+    _fits("out", out, (M, N), y_dtype, dev)
+    here = _here(dev)
+    need = _workspace_size(OP_FP8_LINEAR, M, N, K, 0)
+    ws = _scratch(workspace, dev, here)
+    y = out if out is not None else torch.empty((M, N), dtype=y_dtype, device=dev)
+    with ws.lock:
+        st = lib().fp8_linear_fwd(w.codes.data_ptr(), w.scale.data_ptr(), N, K, xv.data_ptr(), _at(xs), M, dt, _at(bias),
+                                  y.data_ptr(), ws.get(need, dev).data_ptr(), need, here)
+    if st:
+        raise NF4Error(st, "fp8_linear_fwd")
     return y
