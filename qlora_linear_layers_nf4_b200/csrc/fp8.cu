@@ -61,66 +61,93 @@ constexpr int kVec = 16 / int(sizeof(T));   // elements of a 16-byte load
 
 __device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
-// A block's scale from the bits of its largest magnitude; NaN if one element is not finite.
-__device__ __forceinline__ float block_scale(uint32_t top) {
-  return top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __fdiv_rn(__uint_as_float(top), 448.0f);
+// A block's scale, from the bits of its largest magnitude: NaN if one element is not finite.
+// hi and lo: 2^-21 above and below 1 / s.  fp32(x / s) lies between x lo and x hi (each
+// product is within 2^-23 of its exact value), so where both give the same code there is no
+// need to divide: rounding is monotonic.  They differ for about one element in 2^17.
+struct BlockScale {
+  float s, hi, lo;
+  bool divide;      // a subnormal scale, whose reciprocal may overflow
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t top) {
+  BlockScale b;
+  b.s = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __fdiv_rn(__uint_as_float(top), 448.0f);
+  b.divide = b.s < 1.17549435e-38f;
+  const float inv = __fdiv_rn(1.0f, b.s);
+  b.hi = inv * (1.0f + 4.76837158e-7f);
+  b.lo = inv * (1.0f - 4.76837158e-7f);
+  return b;
 }
 
-// Two codes (a scale of 0 or NaN gives zeros).
-__device__ __forceinline__ uint32_t codes2(float a, float b, float scale) {
-  if (!(scale > 0.0f)) return 0u;
-  return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ uint32_t codes4(const float* f, float scale) {
-  return codes2(f[0], f[1], scale) | (codes2(f[2], f[3], scale) << 16);
+// Four codes (a scale of 0 or NaN gives zeros).
+__device__ __forceinline__ uint32_t codes4(const float* f, const BlockScale& b) {
+  if (!(b.s > 0.0f)) return 0u;
+  const uint32_t hi = e4m3x2(f[0] * b.hi, f[1] * b.hi) | (e4m3x2(f[2] * b.hi, f[3] * b.hi) << 16);
+  const uint32_t lo = e4m3x2(f[0] * b.lo, f[1] * b.lo) | (e4m3x2(f[2] * b.lo, f[3] * b.lo) << 16);
+  if (hi == lo && !b.divide) return hi;
+  return e4m3x2(__fdiv_rn(f[0], b.s), __fdiv_rn(f[1], b.s)) | (e4m3x2(__fdiv_rn(f[2], b.s), __fdiv_rn(f[3], b.s)) << 16);
+}
+__device__ __forceinline__ uint8_t code1(float f, const BlockScale& b) {
+  return b.s > 0.0f ? uint8_t(e4m3x2(__fdiv_rn(f, b.s), 0.0f)) : uint8_t(0);
 }
 
 // ------------------------------------------------------------------ quantize
 
 constexpr int kQThreads = 256;
 
-// Blocks of one row.  VEC: rows start on vector boundaries, and a group of 128 / kVec lanes
-// takes a block; else a warp takes one, element by element.
+// Blocks of one row, eight lanes a block and sixteen elements a lane (what a block costs
+// beside its elements, the scale above all, is shared by as many).  VEC: rows start on vector
+// boundaries; else element by element.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kQThreads) fp8_rows_kernel(const T* __restrict__ x, int rows, int cols,
                                                              uint8_t* __restrict__ codes, float* __restrict__ scales) {
-  constexpr int V = VEC ? kVec<T> : 4;
-  constexpr int kLanes = VEC ? kFp8Block / V : 32;
+  constexpr int kLanes = 8, kMine = kFp8Block / kLanes;
+  constexpr int V = VEC ? kVec<T> : 1;
+  constexpr int kLoads = kMine / V;
   constexpr int kGroups = kQThreads / kLanes;
   grid_dep_wait();
   const int kb = (cols + kFp8Block - 1) / kFp8Block;
   const int64_t blocks = int64_t(rows) * kb;
   const int l = threadIdx.x % kLanes;
-  for (int64_t b = int64_t(blockIdx.x) * kGroups + threadIdx.x / kLanes; b < blocks; b += int64_t(gridDim.x) * kGroups) {
-    const int64_t row = b / kb;
+  const int64_t stride = int64_t(gridDim.x) * kGroups;
+  // every lane of a warp takes part in the shuffles: the last round may have no block
+  for (int64_t first = int64_t(blockIdx.x) * kGroups + (threadIdx.x & ~31) / kLanes; first < blocks; first += stride) {
+    const int64_t b = first + (threadIdx.x & 31) / kLanes;
+    const int64_t row = blocks <= 0xffffffffll ? int64_t(uint32_t(b) / uint32_t(kb)) : b / kb;
     const int c0 = int(b - row * kb) * kFp8Block;
-    const int n = min(kFp8Block, cols - c0);
-    const T* src = x + row * cols + c0;
-    uint8_t* dst = codes + row * cols + c0;
-    float f[V];
-    uint32_t top = 0;
+    const int n = b < blocks ? min(kFp8Block, cols - c0) : 0;
+    const int64_t at = row * cols + c0;
+    float f[kMine];
     if (VEC) {
-      const uint4 v = V * l < n ? __ldg(reinterpret_cast<const uint4*>(src) + l) : make_uint4(0u, 0u, 0u, 0u);
-      Elem<T>::unpack(v, f);
-    } else {
+      uint4 v[kLoads];
 #pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = l + 32 * i < n ? Elem<T>::one(src + l + 32 * i) : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) top = max(top, magnitude(f[i]));
-    const unsigned mask = kLanes == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
-    top = __reduce_max_sync(mask, top);
-    const float s = block_scale(top);
-    if (l == 0) scales[b] = s;
-    if (VEC) {
-      if (V * l < n) {
-        if (V == 4) reinterpret_cast<uint32_t*>(dst)[l] = codes4(f, s);
-        else reinterpret_cast<uint2*>(dst)[l] = make_uint2(codes4(f, s), codes4(f + (V == 8 ? 4 : 0), s));
+      for (int i = 0; i < kLoads; ++i) {
+        const int c = (i * kLanes + l) * V;
+        v[i] = c < n ? __ldg(reinterpret_cast<const uint4*>(x + at + c)) : make_uint4(0u, 0u, 0u, 0u);
       }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) Elem<T>::unpack(v[i], f + i * V);
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (l + 32 * i < n) dst[l + 32 * i] = uint8_t(codes2(f[i], 0.0f, s) & 0xffu);
+      for (int i = 0; i < kLoads; ++i) f[i] = i * kLanes + l < n ? Elem<T>::one(x + at + i * kLanes + l) : 0.0f;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) top = max(top, magnitude(f[i]));
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const BlockScale s = block_scale(top);
+    if (l == 0 && n > 0) scales[b] = s.s;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int c = (i * kLanes + l) * V;
+      if (c >= n) continue;
+      if (V == 1) codes[at + c] = code1(f[i], s);
+      else if (V == 4) *reinterpret_cast<uint32_t*>(codes + at + c) = codes4(f + i * V, s);
+      else *reinterpret_cast<uint2*>(codes + at + c) = make_uint2(codes4(f + i * V, s), codes4(f + i * V + (V == 8 ? 4 : 0), s));
     }
   }
 }
@@ -169,8 +196,8 @@ __global__ void __launch_bounds__(kQThreads) fp8_tile_kernel(const T* __restrict
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kQThreads / 32; ++i) top = max(top, part[i]);
-  const float s = block_scale(top);
-  if (t == 0) scales[blockIdx.x] = s;
+  const BlockScale s = block_scale(top);
+  if (t == 0) scales[blockIdx.x] = s.s;
 #pragma unroll
   for (int i = 0; i < kKeep; ++i) {
     if (VEC) {
@@ -186,7 +213,7 @@ __global__ void __launch_bounds__(kQThreads) fp8_tile_kernel(const T* __restrict
       for (int j = 0; j < V; ++j) {
         const int at = t + (i * V + j) * kQThreads, c = c0 + at % kFp8Block;
         const int64_t r = r0 + at / kFp8Block;
-        if (r < rows && c < cols) codes[r * cols + c] = uint8_t(codes2(f[i][j], 0.0f, s) & 0xffu);
+        if (r < rows && c < cols) codes[r * cols + c] = code1(f[i][j], s);
       }
     }
   }
@@ -212,8 +239,8 @@ cudaError_t quantize_t(const void* x, int64_t rows, int64_t cols, int block_rows
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   if (block_rows == 1) {
-    const int64_t per = kQThreads / (vec ? kFp8Block / kVec<T> : 32);
-    pdl_config(&cfg, attr, unsigned(std::min<int64_t>((rows * kb + per - 1) / per, int64_t(sms) * 16)), kQThreads, st);
+    constexpr int64_t per = kQThreads / 8;
+    pdl_config(&cfg, attr, unsigned(std::min<int64_t>((rows * kb + per - 1) / per, int64_t(sms) * 32)), kQThreads, st);
     return vec ? cudaLaunchKernelEx(&cfg, fp8_rows_kernel<T, true>, xt, int(rows), int(cols), codes, scales)
                : cudaLaunchKernelEx(&cfg, fp8_rows_kernel<T, false>, xt, int(rows), int(cols), codes, scales);
   }
@@ -288,13 +315,13 @@ cudaError_t dequantize_t(const uint8_t* codes, const float* scales, int64_t rows
 // tokens in shared memory, quantized here unless they came so, and takes 16 weight rows at
 // a time, its eight warps an eighth of the blocks along K each.  The weight goes from global
 // memory into the A fragments of mma.sync m16n8k32 (e4m3): the k order inside a block is
-// free as long as both operands agree, so a lane's share of a row and block is 32
-// contiguous bytes.  A block's sum is scaled and added in fp32; the warps meet in shared
+// free as long as both operands agree, so a lane's share of a row and block is two pieces
+// of 16 contiguous bytes, and the four lanes of a row load 64.  A block's sum is scaled and added in fp32; the warps meet in shared
 // memory.
 constexpr int kSmWarps = 8;
 constexpr int kSmThreads = 32 * kSmWarps;
 constexpr int kSmAhead = 4;                        // blocks whose loads are in flight
-constexpr int64_t kSmMaxCodes = 96 * 1024;         // M * K: two CTAs an SM
+constexpr int64_t kSmMaxCodes = 96 * 1024;         // M * K
 
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -317,79 +344,87 @@ __device__ __forceinline__ void store_y(const Fp8LinearArgs& a, int64_t m, int64
   }
 }
 
-// Shared memory: codes [8 NT][kb * 128 + 16] (16: a token's rows start in other banks),
-// scales [kb][8 NT], partial sums [warp][16 rows][8 NT].
-__host__ __device__ constexpr size_t small_smem(int nt, int kb) {
-  return size_t(8 * nt) * (size_t(kb) * 128 + 16) + size_t(kb) * 8 * nt * 4 + size_t(kSmWarps) * 16 * 8 * nt * 4;
+// Shared memory: codes [M][kb * 128 + 64] (64: neighbouring tokens lie in other banks),
+// scales [kb][8] (those past M are never used), partial sums [warp][8][16 rows].
+__host__ __device__ constexpr size_t small_smem(int m, int kb) {
+  return size_t(m) * (size_t(kb) * 128 + 64) + size_t(kb) * 8 * 4 + size_t(kSmWarps) * 16 * 8 * 4;
 }
 
-template <typename T, int NT>
+template <typename T>
 __global__ void __launch_bounds__(kSmThreads) fp8_small_kernel(const Fp8LinearArgs a, const T* __restrict__ x,
                                                                const float* __restrict__ given_scale) {
   extern __shared__ __align__(16) uint8_t codes[];
-  constexpr int NP = 8 * NT;
+  constexpr int NP = 8;
   const int K = int(a.K), M = int(a.M);
   const int kb = (K + kFp8Block - 1) / kFp8Block;
-  const int stride = kb * 128 + 16;
-  float* sx = reinterpret_cast<float*>(codes + size_t(NP) * stride);
+  const int stride = kb * 128 + 64;
+  float* sx = reinterpret_cast<float*>(codes + size_t(M) * stride);
   float* part = sx + kb * NP;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, q = lane & 3;
   grid_dep_wait();
   const int groups = int((a.N + 15) / 16);
   const int b0 = kb * warp / kSmWarps, b1 = kb * (warp + 1) / kSmWarps;   // this warp's blocks
-  uint4 wv[kSmAhead][2][2];                        // block, row (g, g + 8), half of its 32 bytes
+  uint4 wv[kSmAhead][2][2];                        // block, row (g, g + 8), 64-byte half
   auto load_w = [&](int grp, int b) {
 #pragma unroll
     for (int j = 0; j < kSmAhead; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t n = min(int64_t(grp) * 16 + 8 * h + g, a.N - 1);
-        const int k = (b + j) * kFp8Block + 32 * q;
+        const int k = (b + j) * kFp8Block + 16 * q;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          wv[j][h][i] = b + j < b1 && k + 16 * i < K ? __ldg(reinterpret_cast<const uint4*>(a.w + n * K + k + 16 * i))
+          wv[j][h][i] = b + j < b1 && k + 64 * i < K ? __ldg(reinterpret_cast<const uint4*>(a.w + n * K + k + 64 * i))
                                                     : make_uint4(0u, 0u, 0u, 0u);
       }
   };
   int grp = blockIdx.x;
   load_w(grp, b0);
 
-  for (int i = warp; i < NP * kb; i += kSmWarps) {
-    const int m = i / kb, b = i - m * kb;
-    uint32_t c = 0;
-    float s = 0.0f;
-    if (m < M) {
-      const int k = b * kFp8Block + 4 * lane;      // K is a multiple of 16
-      if constexpr (sizeof(T) == 1) {
-        if (k < K) c = __ldg(reinterpret_cast<const uint32_t*>(x + int64_t(m) * K + k));
-        s = __ldg(given_scale + int64_t(m) * kb + b);
-      } else {
-        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (k < K) {
+  // The tokens' codes and scales; several loads of a thread in flight.  K is a multiple of 16,
+  // a row's last block is filled up with zeros.
+  if constexpr (sizeof(T) == 1) {
+    for (int i = t; i < M * kb * 8; i += kSmThreads) {
+      const int m = i / (kb * 8), v = i - m * (kb * 8);
+      *reinterpret_cast<uint4*>(codes + m * stride + 16 * v) =
+          16 * v < K ? __ldg(reinterpret_cast<const uint4*>(x + int64_t(m) * K) + v) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    for (int i = t; i < M * kb; i += kSmThreads) sx[i % kb * NP + i / kb] = __ldg(given_scale + i);
+  } else {
+    constexpr int kBatch = 4;
+    for (int i0 = warp; i0 < M * kb; i0 += kSmWarps * kBatch) {
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * kSmWarps, m = i / kb, k = (i - m * kb) * kFp8Block + 4 * lane;
+        raw[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (m < M && k < K) {
           if constexpr (sizeof(T) == 4) {
-            Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(x + int64_t(m) * K + k)), f);
+            raw[j] = __ldg(reinterpret_cast<const uint4*>(x + int64_t(m) * K + k));
           } else {
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(x + int64_t(m) * K + k));
-            float e[8];
-            Elem<T>::unpack(make_uint4(v.x, v.y, 0u, 0u), e);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = e[j];
+            raw[j].x = v.x;
+            raw[j].y = v.y;
           }
         }
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * kSmWarps, m = i / kb, b = i - m * kb;
+        if (m >= M) break;
+        float f[kVec<T>];                          // four elements
+        Elem<T>::unpack(raw[j], f);
         const uint32_t top = max(max(magnitude(f[0]), magnitude(f[1])), max(magnitude(f[2]), magnitude(f[3])));
-        s = block_scale(__reduce_max_sync(0xffffffffu, top));
-        c = codes4(f, s);
+        const BlockScale s = block_scale(__reduce_max_sync(0xffffffffu, top));
+        *reinterpret_cast<uint32_t*>(codes + m * stride + b * kFp8Block + 4 * lane) = codes4(f, s);
+        if (lane == 0) sx[b * NP + m] = s.s;
       }
     }
-    *reinterpret_cast<uint32_t*>(codes + m * stride + b * kFp8Block + 4 * lane) = c;
-    if (lane == 0) sx[b * NP + m] = s;
   }
   __syncthreads();
 
   for (; grp < groups; grp += gridDim.x) {
-    float acc[NT][4];
-#pragma unroll
-    for (int c = 0; c < NT; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.0f;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     const float* ws = a.w_scale + int64_t(grp / 8) * kb;   // sixteen rows lie in one block of 128
     for (int b = b0; b < b1; b += kSmAhead) {
 #pragma unroll
@@ -400,32 +435,29 @@ __global__ void __launch_bounds__(kSmThreads) fp8_small_kernel(const Fp8LinearAr
                                 wv[j][0][1].x, wv[j][0][1].y, wv[j][0][1].z, wv[j][0][1].w};
         const uint32_t r1[8] = {wv[j][1][0].x, wv[j][1][0].y, wv[j][1][0].z, wv[j][1][0].w,
                                 wv[j][1][1].x, wv[j][1][1].y, wv[j][1][1].z, wv[j][1][1].w};
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          const uint4* xc = reinterpret_cast<const uint4*>(codes + (8 * c + g) * stride + (b + j) * kFp8Block + 32 * q);
-          const uint4 x0 = xc[0], x1 = xc[1];
-          const uint32_t xw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mma_e4m3(d, r0[2 * i], r1[2 * i], r0[2 * i + 1], r1[2 * i + 1], xw[2 * i], xw[2 * i + 1]);
-          const float2 s = *reinterpret_cast<const float2*>(sx + (b + j) * NP + 8 * c + 2 * q);
-          acc[c][0] = fmaf(d[0], s.x * sw, acc[c][0]);
-          acc[c][1] = fmaf(d[1], s.y * sw, acc[c][1]);
-          acc[c][2] = fmaf(d[2], s.x * sw, acc[c][2]);
-          acc[c][3] = fmaf(d[3], s.y * sw, acc[c][3]);
+        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+        if (g < M) {
+          const uint4* xc = reinterpret_cast<const uint4*>(codes + g * stride + (b + j) * kFp8Block + 16 * q);
+          x0 = xc[0], x1 = xc[4];
         }
+        const uint32_t xw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma_e4m3(d, r0[2 * i], r1[2 * i], r0[2 * i + 1], r1[2 * i + 1], xw[2 * i], xw[2 * i + 1]);
+        const float2 s = *reinterpret_cast<const float2*>(sx + (b + j) * NP + 2 * q);
+        acc[0] = fmaf(d[0], s.x * sw, acc[0]);
+        acc[1] = fmaf(d[1], s.y * sw, acc[1]);
+        acc[2] = fmaf(d[2], s.x * sw, acc[2]);
+        acc[3] = fmaf(d[3], s.y * sw, acc[3]);
       }
       if (b + kSmAhead < b1) load_w(grp, b + kSmAhead);
     }
     if (grp + int(gridDim.x) < groups) load_w(grp + int(gridDim.x), b0);
     float* mine = part + warp * (16 * NP);         // [token][row]
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      mine[(8 * c + 2 * q) * 16 + g] = acc[c][0];
-      mine[(8 * c + 2 * q + 1) * 16 + g] = acc[c][1];
-      mine[(8 * c + 2 * q) * 16 + g + 8] = acc[c][2];
-      mine[(8 * c + 2 * q + 1) * 16 + g + 8] = acc[c][3];
-    }
+    mine[(2 * q) * 16 + g] = acc[0];
+    mine[(2 * q + 1) * 16 + g] = acc[1];
+    mine[(2 * q) * 16 + g + 8] = acc[2];
+    mine[(2 * q + 1) * 16 + g + 8] = acc[3];
     __syncthreads();
     for (int i = t; i < 16 * M; i += kSmThreads) {
       float v = 0.0f;
@@ -438,28 +470,29 @@ __global__ void __launch_bounds__(kSmThreads) fp8_small_kernel(const Fp8LinearAr
   }
 }
 
-template <typename T, int NT>
-cudaError_t small_tn(const Fp8LinearArgs& a, const void* x, const float* scale, int sms, cudaStream_t st) {
+template <typename T>
+cudaError_t small_t(const Fp8LinearArgs& a, const void* x, const float* scale, int sms, cudaStream_t st) {
   static PerDeviceOnce attr_done;
   const int dev = PerDeviceOnce::current();
   if (!attr_done.done(dev)) {
-    const cudaError_t e = cudaFuncSetAttribute(fp8_small_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    const cudaError_t e = cudaFuncSetAttribute(fp8_small_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
     attr_done.mark(dev);
   }
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   pdl_config(&cfg, attr, unsigned(std::min<int64_t>((a.N + 15) / 16, 2 * int64_t(sms))), kSmThreads, st);
-  cfg.dynamicSmemBytes = small_smem(NT, int((a.K + kFp8Block - 1) / kFp8Block));
-  return cudaLaunchKernelEx(&cfg, fp8_small_kernel<T, NT>, a, static_cast<const T*>(x), scale);
-}
-template <typename T>
-cudaError_t small_t(const Fp8LinearArgs& a, const void* x, const float* scale, int sms, cudaStream_t st) {
-  return a.M <= 8 ? small_tn<T, 1>(a, x, scale, sms, st) : a.M <= 16 ? small_tn<T, 2>(a, x, scale, sms, st)
-                                                                     : small_tn<T, 4>(a, x, scale, sms, st);
+  cfg.dynamicSmemBytes = small_smem(int(a.M), int((a.K + kFp8Block - 1) / kFp8Block));
+  return cudaLaunchKernelEx(&cfg, fp8_small_kernel<T>, a, static_cast<const T*>(x), scale);
 }
 
-bool use_small(const Fp8LinearArgs& a) { return a.M <= 32 && ((a.M + 7) / 8 * 8) * a.K <= kSmMaxCodes; }
+// Up to eight tokens (one MMA column group) the weight is streamed.  Measured, this against
+// the tensor-core kernel with the same codes, us: 4096 x 4096 with 1, 8, 12 and 16 tokens
+// 7.1, 7.8, 11.4 and 13.2 against 12.1; 11008 x 4096 with 8 and 16 12.8 and 20.7 against 21.
+bool use_small(const Fp8LinearArgs& a) { return a.M <= 8 && a.M * a.K <= kSmMaxCodes; }
+// Every CTA quantizes all tokens again: up to two tokens of 4096 that costs less than a
+// launch (1, 2, 4 tokens: 8.6, 10.2, 13.3 us; with a launch of its own before 9.6 to 9.8).
+bool quantize_inside(const Fp8LinearArgs& a) { return a.M * a.K <= 8192; }
 
 }  // namespace
 
@@ -490,26 +523,26 @@ cudaError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int
 cudaError_t launch_fp8_linear(const Fp8LinearArgs& given, const void* x, const float* x_scale, uint8_t* codes,
                               float* scales, int sms, cudaStream_t st, int* launches) {
   Fp8LinearArgs a = given;
-  if (use_small(a)) {
-    NF4_PROF_BEGIN(st, kKFp8Linear);
-    cudaError_t e = x_scale != nullptr   ? small_t<uint8_t>(a, x, x_scale, sms, st)
-                    : a.dtype == NF4_F32 ? small_t<float>(a, x, nullptr, sms, st)
-                    : a.dtype == NF4_F16 ? small_t<__half>(a, x, nullptr, sms, st)
-                                         : small_t<__nv_bfloat16>(a, x, nullptr, sms, st);
-    NF4_PROF_END(st, kKFp8Linear);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e == cudaSuccess) ++*launches;
-    return e;
-  }
+  const bool small = use_small(a);
+  const bool inside = small && x_scale == nullptr && quantize_inside(a);
   a.x = x_scale != nullptr ? static_cast<const uint8_t*>(x) : codes;
   a.x_scale = x_scale != nullptr ? x_scale : scales;
   Fp8Gemm g;
-  if (!g.prepare(a, sms)) return cudaErrorInvalidValue;
-  if (x_scale == nullptr) {
+  if (!small && !g.prepare(a, sms)) return cudaErrorInvalidValue;
+  if (x_scale == nullptr && !inside) {
     const cudaError_t e = launch_fp8_quantize(x, a.dtype, a.M, a.K, 1, codes, scales, sms, st, launches);
     if (e != cudaSuccess) return e;
   }
-  return g.run(st, launches);
+  if (!small) return g.run(st, launches);
+  NF4_PROF_BEGIN(st, kKFp8Linear);
+  cudaError_t e = !inside              ? small_t<uint8_t>(a, a.x, a.x_scale, sms, st)
+                  : a.dtype == NF4_F32 ? small_t<float>(a, x, nullptr, sms, st)
+                  : a.dtype == NF4_F16 ? small_t<__half>(a, x, nullptr, sms, st)
+                                       : small_t<__nv_bfloat16>(a, x, nullptr, sms, st);
+  NF4_PROF_END(st, kKFp8Linear);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 }  // namespace nf4

@@ -34,6 +34,7 @@ struct Fp8Params {
   int M, N;
   int kb;                  // blocks of 128 along K
   int row_tiles, tiles;
+  uint32_t x_bytes;        // of a CTA's tokens in a stage
   int dtype;
   const float* w_scale;
   const float* x_scale;

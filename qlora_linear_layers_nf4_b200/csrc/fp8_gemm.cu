@@ -36,14 +36,14 @@ using namespace expert;
 
 constexpr int kEpiWarp = 4;
 constexpr uint32_t kXBytes = 128 * 128;
-constexpr uint32_t kStageOut = 4096;     // of a warp: two 32 x 32 pieces of 16 bits, or one of 32
+constexpr uint32_t kPiece = 2048;        // of a warp: 32 rows of 64 bytes of the result
 
 template <int NT>
 struct Cfg {
   static constexpr int kPair = NT == 256 ? 2 : 1;                 // CTAs of a tile
   static constexpr int kRows = 128 * kPair;                       // tokens of a tile
   static constexpr int kCols = NT > 128 ? 128 : NT;               // columns of a warp
-  static constexpr int kEpiWarps = NT == 256 ? 8 : 4;
+  static constexpr int kEpiWarps = 4 * NT / kCols;
   static constexpr int kThreads = 32 * (kEpiWarp + kEpiWarps);
   static constexpr uint32_t kWBytes = uint32_t(NT / kPair) * 128;
   static constexpr uint32_t kStage = kXBytes + kWBytes;
@@ -62,9 +62,25 @@ struct Fp8Shared {
 };
 template <int NT>
 constexpr size_t fp8_smem() {
-  return size_t(Cfg<NT>::kStages) * Cfg<NT>::kStage + Cfg<NT>::kEpiWarps * kStageOut + sizeof(Fp8Shared) + 1024;
+  return size_t(Cfg<NT>::kStages) * Cfg<NT>::kStage + Cfg<NT>::kEpiWarps * kPiece + sizeof(Fp8Shared) + 1024;
 }
 static_assert(fp8_smem<256>() <= 232448, "shared memory of one CTA");
+
+// The wait of a whole warp, every lane polling: a poll that succeeds at once costs no shuffle.
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait(bar, parity, abort_flag, status);
+}
+
+// acc + v * scale of two columns in one instruction.
+__device__ __forceinline__ void add2(float2& acc, uint32_t v0, uint32_t v1, float2 scale) {
+  uint64_t a, v, s;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(acc.x), "f"(acc.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(s) : "f"(scale.x), "f"(scale.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(s));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(acc.x), "=f"(acc.y) : "l"(a));
+}
 
 // e4m3 x e4m3 -> fp32 (kind::f8f6f4, both K-major).
 template <int PAIR>
@@ -93,7 +109,7 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = expert::align_1024(smem_raw);
   uint8_t* out_base = smem + C::kStages * C::kStage;
-  Fp8Shared* sh = reinterpret_cast<Fp8Shared*>(out_base + C::kEpiWarps * kStageOut);
+  Fp8Shared* sh = reinterpret_cast<Fp8Shared*>(out_base + C::kEpiWarps * kPiece);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = C::kPair == 2 ? cluster_ctarank() : 0u;
@@ -133,9 +149,15 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
   const int first = int(blockIdx.x) / C::kPair, step = int(gridDim.x) / C::kPair;
   auto leader_bar = [&](uint64_t* bar) { return C::kPair == 2 ? mapa_shared(smem_u32(bar), 0) : smem_u32(bar); };
   grid_dep_wait();
+  // The sums of wide tiles want more registers than an even split gives: 4 warps x 56 + 8 x 224,
+  // the 12 x 168 that the CTA was launched with.
+  auto few_registers = [] {
+    if constexpr (NT == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  };
 
   if (warp < 2) {
     // ---------------- TMA: tokens (warp 0, which expects every byte of a stage) and weight
+    few_registers();
     const bool issue = elect_one();
     bool ok = true;
     int s = 0, issued = 0;
@@ -148,7 +170,7 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
         if (!ok) break;
         if (issue) {
           uint8_t* dst = smem + s * C::kStage + (warp == 0 ? 0u : kXBytes);
-          if (warp == 0 && rank == 0) mbar_arrive_expect_tx(&sh->full[s], C::kPair * C::kStage);
+          if (warp == 0 && rank == 0) mbar_arrive_expect_tx(&sh->full[s], C::kPair * (p.x_bytes + C::kWBytes));
           if (C::kPair == 2) tma_load_2d_pair(dst, warp == 0 ? &mx : &mw, leader_bar(&sh->full[s]), b * 128, y);
           else tma_load_2d(dst, warp == 0 ? &mx : &mw, &sh->full[s], b * 128, y);
         }
@@ -167,6 +189,7 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
       }
   } else if (warp == 2) {
     // ---------------- MMA
+    few_registers();
     if (rank == 0) {
       const bool issue = elect_one();
       const uint64_t x_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
@@ -177,8 +200,8 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
       uint32_t ph = 0;
       for (int id = first; id < p.tiles && ok; id += step) {
         for (int b = 0; b < p.kb; ++b, ++n) {
-          ok = mbar_wait_cluster(&sh->acc_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, p.status);
-          if (ok) ok = mbar_wait_cluster(&sh->full[s], ph, abort_flag, p.status);
+          ok = mbar_wait_cluster(&sh->full[s], ph, abort_flag, p.status);
+          if (ok) ok = mbar_wait_cluster(&sh->acc_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
           if (issue) {
@@ -204,86 +227,107 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
         ring_wait(&sh->drain, 0, &none, nullptr);
       }
     }
-  } else if (warp >= kEpiWarp) {
+  } else if (warp == 3) {
+    few_registers();
+  } else {
     // ---------------- sums: lane = token, C::kCols columns a warp
-    const int quad = warp & 3, half = (warp - kEpiWarp) >> 2;
-    uint8_t* buf = out_base + (warp - kEpiWarp) * kStageOut;
+    if constexpr (NT == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int quad = warp & 3, group = (warp - kEpiWarp) >> 2;   // TMEM lanes; columns
+    uint8_t* buf = out_base + (warp - kEpiWarp) * kPiece;
     int s = 0, n = 0;
-    uint32_t pieces = 0;   // stored so far: they alternate between the two halves of buf
     bool ok = true;
     for (int id = first; id < p.tiles && ok; id += step) {
       const int ct = id / p.row_tiles, rt = id - ct * p.row_tiles;
-      const int row0 = rt * C::kRows + 128 * int(rank) + quad * 32, col0 = ct * NT + half * C::kCols;
+      const int row0 = rt * C::kRows + 128 * int(rank) + quad * 32, col0 = ct * NT + group * C::kCols;
       const float* sx = p.x_scale + int64_t(min(row0 + lane, p.M - 1)) * p.kb;
       const float* sw = p.w_scale + int64_t(min(col0, p.N - 1) / 128) * p.kb;
-      float acc[C::kCols];
+      float nx = __ldg(sx), nw = __ldg(sw);
+      float2 acc[C::kCols / 2];
 #pragma unroll
-      for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
-      float scale = __ldg(sx) * __ldg(sw);
+      for (int i = 0; i < C::kCols / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
       for (int b = 0; b < p.kb; ++b, ++n) {
-        const int nb = min(b + 1, p.kb - 1);
-        const float nx = __ldg(sx + nb), nw = __ldg(sw + nb);
-        ok = warp_wait(&sh->acc_full[n & 1], (n >> 1) & 1, abort_flag, p.status);
+        ok = all_wait(&sh->acc_full[n & 1], (n >> 1) & 1, abort_flag, p.status);
         if (!ok) break;
-        if (warp == kEpiWarp && lane == 0) mbar_arrive(&sh->empty[s]);
+        if (warp == kEpiWarp + C::kEpiWarps - 1 && lane == 0) mbar_arrive(&sh->empty[s]);
         if (++s == C::kStages) s = 0;
         tc_fence_after();
+        const uint32_t at = tmem + (uint32_t(quad * 32) << 16) + uint32_t(n & 1) * uint32_t(NT) + group * C::kCols;
+        const float2 scale = make_float2(nx * nw, nx * nw);   // loaded a block ahead
+        const int nb = min(b + 1, p.kb - 1);
+        nx = __ldg(sx + nb);
+        nw = __ldg(sw + nb);
+        // 32 columns are on their way while the 32 before are added
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(at, v[0]);
 #pragma unroll
-        for (int c = 0; c < C::kCols; c += 32) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + uint32_t(n & 1) * uint32_t(NT) + half * C::kCols + c, v);
+        for (int c = 0; c < C::kCols / 32; ++c) {
           tmem_ld_wait();
+          if (c + 1 < C::kCols / 32) {
+            tmem_ld_32x32b_x32(at + 32 * (c + 1), v[(c + 1) & 1]);
+          } else {   // every column is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (C::kPair == 2) arrive_leader(leader_bar(&sh->acc_empty[n & 1]));
+              else mbar_arrive(&sh->acc_empty[n & 1]);
+            }
+          }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), scale, acc[c + i]);
+          for (int i = 0; i < 16; ++i) add2(acc[16 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], scale);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (C::kPair == 2) arrive_leader(leader_bar(&sh->acc_empty[n & 1]));
-          else mbar_arrive(&sh->acc_empty[n & 1]);
-        }
-        scale = nx * nw;
       }
       if (!ok) break;
-      // ---- bias, rounding, 32 x 32 pieces through shared memory
+      // ---- bias, rounding; pieces of 32 rows x 64 bytes through shared memory (64-byte
+      // swizzle: chunk j at j ^ ((row >> 1) & 3))
+      if (p.bias != nullptr) {
+        auto bias_at = [&](int col) {
+          const int at = min(col, p.N - 1);
+          return p.dtype == NF4_F32   ? __ldg(static_cast<const float*>(p.bias) + at)
+                 : p.dtype == NF4_F16 ? __half2float(static_cast<const __half*>(p.bias)[at])
+                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[at]);
+        };
 #pragma unroll
-      for (int c = 0; c < C::kCols; c += 32) {
-        const int col = col0 + c;
-        if (col >= p.N || row0 >= p.M) break;
-        if (p.bias != nullptr) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int at = min(col + i, p.N - 1);
-            acc[c + i] += p.dtype == NF4_F32   ? __ldg(static_cast<const float*>(p.bias) + at)
-                          : p.dtype == NF4_F16 ? __half2float(static_cast<const __half*>(p.bias)[at])
-                                               : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[at]);
-          }
+        for (int i = 0; i < C::kCols / 2; ++i) {
+          acc[i].x += bias_at(col0 + 2 * i);
+          acc[i].y += bias_at(col0 + 2 * i + 1);
         }
-        const bool wide = p.dtype == NF4_F32;
-        uint8_t* piece = buf + (wide ? 0u : (pieces++ & 1u) * 2048u);
-        if (lane == 0) {   // the store that used the piece has read it
-          if (wide) bulk_wait_group_read<0>();
-          else bulk_wait_group_read<1>();
-        }
+      }
+      auto piece = [&](int col, const uint4 (&chunk)[4]) {
+        if (lane == 0) bulk_wait_group_read<0>();   // the store before has read the piece
         __syncwarp();
-        if (wide) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float4*>(piece + sw128_offset(uint32_t(lane), uint32_t(j))) =
-                make_float4(acc[c + 4 * j], acc[c + 4 * j + 1], acc[c + 4 * j + 2], acc[c + 4 * j + 3]);
-        } else {
-          const bool f16 = p.dtype == NF4_F16;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)   // 64-byte rows, 64-byte swizzle: chunk j at j ^ ((row >> 1) & 3)
-            *reinterpret_cast<uint4*>(piece + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(pack2(f16, acc[c + 8 * j], acc[c + 8 * j + 1]), pack2(f16, acc[c + 8 * j + 2], acc[c + 8 * j + 3]),
-                           pack2(f16, acc[c + 8 * j + 4], acc[c + 8 * j + 5]), pack2(f16, acc[c + 8 * j + 6], acc[c + 8 * j + 7]));
-        }
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = chunk[j];
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&my, piece, col, row0);   // rows past M, columns past N: clipped
+          tma_store_2d(&my, buf, col, row0);   // rows past M, columns past N: clipped
           bulk_commit_group();
+        }
+      };
+      if (p.dtype == NF4_F32) {
+#pragma unroll
+        for (int c = 0; c < C::kCols; c += 16) {
+          if (col0 + c >= p.N || row0 >= p.M) break;
+          uint4 chunk[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            chunk[j] = make_uint4(__float_as_uint(acc[c / 2 + 2 * j].x), __float_as_uint(acc[c / 2 + 2 * j].y),
+                                  __float_as_uint(acc[c / 2 + 2 * j + 1].x), __float_as_uint(acc[c / 2 + 2 * j + 1].y));
+          piece(col0 + c, chunk);
+        }
+      } else {
+        const bool f16 = p.dtype == NF4_F16;
+#pragma unroll
+        for (int c = 0; c < C::kCols; c += 32) {
+          if (col0 + c >= p.N || row0 >= p.M) break;
+          uint4 chunk[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            chunk[j] = make_uint4(pack2(f16, acc[c / 2 + 4 * j].x, acc[c / 2 + 4 * j].y),
+                                  pack2(f16, acc[c / 2 + 4 * j + 1].x, acc[c / 2 + 4 * j + 1].y),
+                                  pack2(f16, acc[c / 2 + 4 * j + 2].x, acc[c / 2 + 4 * j + 2].y),
+                                  pack2(f16, acc[c / 2 + 4 * j + 3].x, acc[c / 2 + 4 * j + 3].y));
+          piece(col0 + c, chunk);
         }
       }
     }
@@ -340,11 +384,15 @@ bool Fp8Gemm::prepare(const Fp8LinearArgs& a, int sms) {
   else if (row_tiles * cdiv(a.N, 128) >= sms) tile_n = 128;
   else if (row_tiles * cdiv(a.N, 64) >= sms) tile_n = 64;
   const int pair = tile_n == 256 ? 2 : 1;
+  // Few tokens: a box of as many rows (the other lanes' results are never stored).  With
+  // fewer than 32 tokens in boxes of 128 rows 4096 x 4096 took 18 us against 11.4 with 33.
+  const int x_rows = a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
   const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B;
-  bool ok = encode_map_2d(&mx, a.x, MapElem::kU8, K, M, 128, 128, s128) &&
+  bool ok = encode_map_2d(&mx, a.x, MapElem::kU8, K, M, 128, uint32_t(x_rows), s128) &&
             encode_map_2d(&mw, a.w, MapElem::kU8, K, N, 128, uint32_t(tile_n / pair), s128);
-  ok = ok && (a.dtype == NF4_F32 ? make_map_2d_f32(&my, a.y, N, M, 32, 32, s128)
-                                 : encode_map_2d(&my, a.y, MapElem::k16, N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B));
+  const uint32_t rows = uint32_t(std::min<uint64_t>(M, 32));
+  ok = ok && (a.dtype == NF4_F32 ? make_map_2d_f32(&my, a.y, N, M, 16, rows, CU_TENSOR_MAP_SWIZZLE_64B)
+                                 : encode_map_2d(&my, a.y, MapElem::k16, N, M, 32, rows, CU_TENSOR_MAP_SWIZZLE_64B));
   p = Fp8Params{};
   p.M = int(a.M);
   p.N = int(a.N);
@@ -352,6 +400,7 @@ bool Fp8Gemm::prepare(const Fp8LinearArgs& a, int sms) {
   p.row_tiles = int(cdiv(a.M, 128 * pair));
   const int64_t tiles = int64_t(p.row_tiles) * cdiv(a.N, tile_n);
   p.tiles = int(tiles);
+  p.x_bytes = uint32_t(x_rows) * 128u;
   p.dtype = a.dtype;
   p.w_scale = a.w_scale;
   p.x_scale = a.x_scale;
