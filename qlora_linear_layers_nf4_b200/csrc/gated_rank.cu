@@ -10,7 +10,7 @@
 // of a cluster, which sum their fp32 partials through distributed shared memory in a fixed
 // order.
 //
-// T and dA are fed by TMA.  U and dB make their A operand, d, on the way: sixteen warps
+// T and dA are fed by TMA.  U and dB make their A operand, d, on the way: eight warps
 // read dh, g and u (a step ahead, in registers), compute dg and du in fp32 and write them
 // as 16-bit terms, swizzled, into shared memory; U's warps store the first terms to global
 // memory too, for dx.  dB computes d a second time instead of reading it: the fp32 value
@@ -22,6 +22,7 @@
 // truncates when it adds to an accumulator: the first terms of even and odd steps have an
 // accumulator each and the small terms a third, summed in fp32 at the end.
 #include <algorithm>
+#include <atomic>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
 
 // ------------------------------------------------------------------ U and dB: d made on the way
 
-constexpr int kMkWarps = 16;                                    // they make d, and finish the tile
+constexpr int kMkWarps = 8;                                     // they make d, and finish the tile
 constexpr int kMkThreads = 32 * (kMkWarps + 2);                 // and B loads, MMA
 constexpr int kMkBufs = 2;
 constexpr uint32_t kMkOpBytes = 6 * kTileBytes;                 // terms of dg, then of du
@@ -367,18 +368,61 @@ struct MkShared {
 constexpr size_t kMkSmem = size_t(kMkBufs) * (kMkOpBytes + kMkBBytes) + sizeof(MkShared) + 1024;
 static_assert(kMkSmem <= 232448, "shared memory of one CTA");
 
+// Two 16-bit values to fp32.
 template <bool F16>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ gated::F2 wide2(uint32_t w) {
+  if (F16) {
+    const float2 f = unpack2(true, w);
+    return gated::f2(f.x, f.y);
+  }
+  return gated::f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// Eight values as 16-bit terms, each what the roundings before it left (f16's second one
+// scaled).  Of a first term that is not finite nothing is left over.
+template <bool F16>
+__device__ __forceinline__ void split8(gated::F2 (&v)[4], uint4 (&term)[3]) {
+  constexpr int kTerms = gated_terms(F16);
+  float top = 0.0f;   // largest magnitude, NaN if there is one
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = unpack2(F16, w[i]);
-    f[2 * i] = a.x;
-    f[2 * i + 1] = a.y;
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = gated::split2(v[e]);
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(top) : "f"(f.x), "f"(f.y), "f"(top));
+  }
+  // from half a step above the type's largest value on, the first term is infinite
+  const bool finite = top < (F16 ? 65520.0f : 3.3961775e38f);
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t) {
+    uint32_t q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = gated::split2(v[e]);
+      q[e] = pack2(F16, f.x, f.y);
+      if (t + 1 < kTerms) {
+        v[e] = gated::fma2(wide2<F16>(q[e]), gated::both(-1.0f), v[e]);
+        if (F16) v[e] = gated::mul2(v[e], gated::both(kULoMul));
+      }
+    }
+    if (t == 0 && !finite) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = gated::split2(v[e]);
+        v[e] = gated::f2(fabsf(f.x) < __uint_as_float(0x7f800000u) ? f.x : 0.0f,
+                         fabsf(f.y) < __uint_as_float(0x7f800000u) ? f.y : 0.0f);
+      }
+    }
+    term[t] = make_uint4(q[0], q[1], q[2], q[3]);
   }
 }
 
-template <GatedRankKind KIND, bool F16>
+// A 16-byte load that stays where it is written: it is made long before its use.
+__device__ __forceinline__ uint4 load_ahead(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+template <GatedRankKind KIND, bool F16, int ACT>
 __global__ void __launch_bounds__(kMkThreads, 1)
     gated_make_kernel(const __grid_constant__ CUtensorMap tm_b, const GatedRankParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -418,98 +462,95 @@ __global__ void __launch_bounds__(kMkThreads, 1)
   const uint32_t tmem = sh->tmem_base;
 
   if (warp < kMkWarps) {
-    // ---------------- d of 128 x 64 (U) or 64 x 128 (dB) elements a step: a thread takes
-    // eight of them twice, at row t / 8 and 16-byte chunk t % 8 of each half of the tile
+    // ---------------- d of 128 x 64 (U) or 64 x 128 (dB) elements a step, as two halves of
+    // 64 x 64: a thread takes eight elements (16-byte chunk t % 8 of row t / 8 and so on) kPer
+    // times.  Their dh, g and u are loaded a step ahead, as soon as those
+    // before are used.
     const int tr = threadIdx.x >> 3, tc = threadIdx.x & 7;
     const int64_t mn = int64_t(p.M) * p.N;
-    uint4 in[2][3];                // dh, g, u
-    int64_t at[2];
-    bool there[2];
-    auto fetch = [&](int i) {
+    const int red0 = w.step0 * 64;
+    // chunk c (half half_of(c), row row_of(c)) in the first step; a step later it is `ahead` further.  `left`: how far the reduction index may still go.
+    const int64_t ahead = KIND == kGatedU ? 64 : int64_t(64) * p.N;
+    constexpr int kPer = 1024 / (32 * kMkWarps), kPerHalf = kPer / 2;
+    auto half_of = [](int c) { return c / kPerHalf; };
+    auto row_of = [&](int c) { return c % kPerHalf * (64 / kPerHalf) + tr; };
+    int64_t at[kPer];
+    int left[kPer];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int red0 = (w.step0 + i) * 64;
-        const int m = KIND == kGatedU ? row0 + 64 * h + tr : red0 + tr;
-        const int n = KIND == kGatedU ? red0 + 8 * tc : row0 + 64 * h + 8 * tc;
-        there[h] = i < w.steps && m < p.M && n < p.N;
-        at[h] = int64_t(m) * p.N + n;
+    for (int c = 0; c < kPer; ++c) {
+      const int r = row_of(c);
+      const int m = KIND == kGatedU ? row0 + 64 * half_of(c) + r : red0 + r;
+      const int n = KIND == kGatedU ? red0 + 8 * tc : row0 + 64 * half_of(c) + 8 * tc;
+      at[c] = int64_t(m) * p.N + n;
+      left[c] = KIND == kGatedU ? (m < p.M ? p.N - n : 0) : (n < p.N ? p.M - m : 0);
+    }
+    uint4 in[kPer][3];             // dh, g, u
+    auto fetch = [&](int c, int i) {
+      const bool there = i < w.steps && 64 * i < left[c];
 #pragma unroll
-        for (int j = 0; j < 3; ++j) in[h][j] = make_uint4(0u, 0u, 0u, 0u);
-        if (there[h]) {
-          in[h][0] = __ldg(reinterpret_cast<const uint4*>(p.dh + at[h]));
-          in[h][1] = __ldg(reinterpret_cast<const uint4*>(p.pre + at[h]));
-          in[h][2] = __ldg(reinterpret_cast<const uint4*>(p.pre + mn + at[h]));
-        }
+      for (int j = 0; j < 3; ++j) in[c][j] = make_uint4(0u, 0u, 0u, 0u);
+      if (there) {
+        const int64_t e = at[c] + ahead * i;
+        in[c][0] = load_ahead(p.dh + e);
+        in[c][1] = load_ahead(p.pre + e);
+        in[c][2] = load_ahead(p.pre + mn + e);
       }
     };
-    const uint32_t off = sw128_offset(uint32_t(tr), uint32_t(tc));
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) fetch(c, 0);
     bool ok = true;
-    fetch(0);
     for (int i = 0; i < w.steps; ++i) {
       const int b = i & 1;
-      uint4 d[2][2][3];   // half, projection, term
-      int64_t now[2] = {at[0], at[1]};
-      bool write[2] = {there[0], there[1]};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float dh[8], g[8], u[8];
-        unpack8<F16>(in[h][0], dh);
-        unpack8<F16>(in[h][1], g);
-        unpack8<F16>(in[h][2], u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const gated::ActGrad ag = gated::act_grad<true>(p.act, g[e]);
-          g[e] = dh[e] * u[e] * ag.d;
-          u[e] = dh[e] * ag.a;
-        }
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          float* v = z == 0 ? g : u;
-#pragma unroll
-          for (int term = 0; term < kTerms; ++term) {
-            uint32_t q[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              q[e] = pack2(F16, v[2 * e], v[2 * e + 1]);
-              if (term + 1 < kTerms) {
-                const float2 a = unpack2(F16, q[e]);
-                v[2 * e] = rest(v[2 * e], a.x) * (F16 ? kULoMul : 1.0f);
-                v[2 * e + 1] = rest(v[2 * e + 1], a.y) * (F16 ? kULoMul : 1.0f);
-              }
-            }
-            d[h][z][term] = make_uint4(q[0], q[1], q[2], q[3]);
-          }
-        }
-      }
-      fetch(i + 1);
       if (ok) ok = warp_wait(&sh->empty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.status);
       if (!ok) break;
+      uint8_t* ops = op_tile(b, 0, 0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int c = 0; c < kPer; ++c) {
+        gated::F2 dg[4], du[4];
+        const uint32_t wd[4] = {in[c][0].x, in[c][0].y, in[c][0].z, in[c][0].w};
+        const uint32_t wg[4] = {in[c][1].x, in[c][1].y, in[c][1].z, in[c][1].w};
+        const uint32_t wu[4] = {in[c][2].x, in[c][2].y, in[c][2].z, in[c][2].w};
 #pragma unroll
-        for (int z = 0; z < 2; ++z)
+        for (int e = 0; e < 4; ++e) {
+          const gated::F2 dh = wide2<F16>(wd[e]);
+          gated::F2 a, d;
+          gated::act_grad2<ACT>(wide2<F16>(wg[e]), &a, &d);
+          dg[e] = gated::mul2(gated::mul2(dh, wide2<F16>(wu[e])), d);
+          du[e] = gated::mul2(dh, a);
+        }
+        fetch(c, i + 1);
+        const uint32_t off = uint32_t(half_of(c)) * kBoxBytes + sw128_offset(uint32_t(row_of(c)), uint32_t(tc));
+        uint4 first[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          uint4 d[3];
+          split8<F16>(z == 0 ? dg : du, d);
+          first[z] = d[0];
 #pragma unroll
           for (int term = 0; term < kTerms; ++term)
-            *reinterpret_cast<uint4*>(op_tile(b, z, term) + uint32_t(h) * kBoxBytes + off) = d[h][z][term];
+            *reinterpret_cast<uint4*>(ops + uint32_t(3 * z + term) * kTileBytes + off) = d[term];
+        }
+        
+        if (KIND == kGatedU && blockIdx.z == 0 && 64 * i < left[c]) {
+          const int64_t e = at[c] + ahead * i;
+          *reinterpret_cast<uint4*>(p.d + e) = first[0];
+          *reinterpret_cast<uint4*>(p.d + mn + e) = first[1];
+        }
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->opfull[b]);
-      if (KIND == kGatedU && blockIdx.z == 0) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (write[h]) {
-            *reinterpret_cast<uint4*>(p.d + now[h]) = d[h][0][0];
-            *reinterpret_cast<uint4*>(p.d + mn + now[h]) = d[h][1][0];
-          }
-      }
     }
-    // ---------------- the tile's sums: four warps a TMEM quadrant, 32 columns each
+    // ---------------- the tile's sums: lanes by warp % 4, columns by warp / 4
     if (ok) ok = warp_wait(&sh->accum, 0, abort_flag, p.status);
     tc_fence_after();
-    const int quad = warp & 3, c = (warp >> 2) * 32;
-    float f[32];
-    join_accs(tmem + (uint32_t(quad * 32) << 16) + c, kAccStride, ok ? w.steps : 0, true, F16 ? 1.0f / kULoMul : 1.0f, f);
-    finish32<KIND>(p, reinterpret_cast<float*>(smem), row0, quad * 32 + lane, c, col0, f);
+    const int quad = warp & 3;
+    constexpr int kWide = 2 * kCols / (kMkWarps / 4);
+    for (int c = (warp >> 2) * kWide; c < (warp >> 2) * kWide + kWide; c += 32) {
+      float f[32];
+      join_accs(tmem + (uint32_t(quad * 32) << 16) + c, kAccStride, ok ? w.steps : 0, true, F16 ? 1.0f / kULoMul : 1.0f, f);
+      finish32<KIND>(p, reinterpret_cast<float*>(smem), row0, quad * 32 + lane, c, col0, f);
+    }
   } else if (warp == kMkWarps) {
     // ---------------- MMA
     const bool issue = elect_one();
@@ -584,15 +625,20 @@ __global__ void __launch_bounds__(kMkThreads, 1)
 
 PerDeviceOnce g_attr_done;
 
+// The kernels that make d: [dB][f16][activation].
+const void* const kMake[] = {
+    (const void*)gated_make_kernel<kGatedU, false, gated::kSilu>,  (const void*)gated_make_kernel<kGatedU, false, gated::kGeluTanh>,
+    (const void*)gated_make_kernel<kGatedU, true, gated::kSilu>,   (const void*)gated_make_kernel<kGatedU, true, gated::kGeluTanh>,
+    (const void*)gated_make_kernel<kGatedDB, false, gated::kSilu>, (const void*)gated_make_kernel<kGatedDB, false, gated::kGeluTanh>,
+    (const void*)gated_make_kernel<kGatedDB, true, gated::kSilu>,  (const void*)gated_make_kernel<kGatedDB, true, gated::kGeluTanh>};
+
 cudaError_t set_attrs() {
   const int dev = PerDeviceOnce::current();
   if (g_attr_done.done(dev)) return cudaSuccess;
   const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e = cudaFuncSetAttribute(gated_tma_kernel<kGatedT>, attr, int(tma_smem(kGatedT)));
   if (e == cudaSuccess) e = cudaFuncSetAttribute(gated_tma_kernel<kGatedDA>, attr, int(tma_smem(kGatedDA)));
-  const void* make[] = {(const void*)gated_make_kernel<kGatedU, false>, (const void*)gated_make_kernel<kGatedU, true>,
-                        (const void*)gated_make_kernel<kGatedDB, false>, (const void*)gated_make_kernel<kGatedDB, true>};
-  for (const void* k : make)
+  for (const void* k : kMake)
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, attr, int(kMkSmem));
   if (e == cudaSuccess) g_attr_done.mark(dev);
   return e;
@@ -600,13 +646,40 @@ cudaError_t set_attrs() {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// CTAs of a cluster: as many as give the fewest steps on the SM with the most, two steps a
-// CTA at least, fewer where that ties.
+// Clusters of s CTAs that the device runs at once (GPCs hold whole clusters, so it is less
+// than its SMs / s), asked once a device; `threads` and `smem` of the larger kernels.
+int clusters_at_once(int s, int sms) {
+  static std::atomic<int> known[64][kMaxSlices + 1];
+  const int dev = PerDeviceOnce::current();
+  if (dev < 0 || dev >= 64) return std::max(1, sms / s);
+  int n = known[dev][s].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, unsigned(s), 1);
+  cfg.blockDim = dim3(kMkThreads, 1, 1);
+  cfg.dynamicSmemBytes = kMkSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = unsigned(s);
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kMake[0], &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = std::max(1, sms / s);
+  }
+  known[dev][s].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// CTAs of a cluster: as many as give the fewest rounds of steps, a CTA's start and end
+// counted as four, two steps a CTA at least, fewer where that ties.
 int pick_slices(int64_t tiles, int64_t steps, int sms) {
   int best = 1;
   int64_t best_cost = INT64_MAX;
   for (int s = 1; s <= kMaxSlices && (s == 1 || steps / s >= 2); ++s) {
-    const int64_t cost = cdiv(tiles * s, sms) * (cdiv(steps, s) + 2);
+    const int64_t cost = cdiv(tiles, clusters_at_once(s, sms)) * (cdiv(steps, s) + 4);
     if (cost < best_cost) {
       best_cost = cost;
       best = s;
@@ -658,6 +731,7 @@ bool GatedRank::prepare(const GatedArgs& a, GatedRankKind k, const void* in, voi
   }
   if (k == kGatedT || k == kGatedU) p.out16 = static_cast<uint16_t*>(out);
   else p.out32 = static_cast<float*>(out);
+  if (set_attrs() != cudaSuccess) return false;
   p.red_steps = int(cdiv(red, 64));
   const int64_t tiles = cdiv(rows, 128), groups = cdiv(a.r, kCols);
   p.slices = pick_slices(tiles * groups, p.red_steps, sms);
@@ -686,14 +760,10 @@ cudaError_t GatedRank::run(cudaStream_t st, int* launches) const {
   switch (kind) {
     case kGatedT: e = cudaLaunchKernelEx(&cfg, gated_tma_kernel<kGatedT>, ma, mb, p); break;
     case kGatedDA: e = cudaLaunchKernelEx(&cfg, gated_tma_kernel<kGatedDA>, ma, mb, p); break;
-    case kGatedU:
-      e = p.f16 ? cudaLaunchKernelEx(&cfg, gated_make_kernel<kGatedU, true>, mb, p)
-                : cudaLaunchKernelEx(&cfg, gated_make_kernel<kGatedU, false>, mb, p);
-      break;
-    case kGatedDB:
-      e = p.f16 ? cudaLaunchKernelEx(&cfg, gated_make_kernel<kGatedDB, true>, mb, p)
-                : cudaLaunchKernelEx(&cfg, gated_make_kernel<kGatedDB, false>, mb, p);
-      break;
+    default: {
+      using Make = void (*)(CUtensorMap, GatedRankParams);
+      e = cudaLaunchKernelEx(&cfg, reinterpret_cast<Make>(const_cast<void*>(kMake[(kind == kGatedDB ? 4 : 0) + (p.f16 ? 2 : 0) + p.act])), mb, p);
+    }
   }
   NF4_PROF_END(st, ids[kind]);
   if (e == cudaSuccess) e = cudaGetLastError();
