@@ -38,6 +38,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "decode_common.cuh"
 #include "expert_decode.h"
 #include "grouped.cuh"
 #include "kernels.h"
@@ -51,6 +52,7 @@ namespace nf4 {
 namespace {
 
 using namespace tc;
+using namespace decode;
 using expert::ring_wait;
 using expert::warp_wait;
 
@@ -87,56 +89,6 @@ constexpr size_t dc_smem() {
   return size_t(dc_stages(NP)) * dc_stage_bytes(NP) + kLutBytes + sizeof(DcShared<NP>) + 1024;
 }
 static_assert(dc_smem<16>() <= 232448 && dc_smem<8>() <= 232448, "shared memory of one CTA");
-
-template <bool F16>
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (F16) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  } else {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-}
-
-template <bool F16>
-__device__ __forceinline__ float2 two_floats(uint32_t w) {
-  return F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
-             : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t two_rounded(float lo, float hi) {
-  if (F16) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <bool F16>
-__device__ __forceinline__ uint16_t one_rounded(float v) {
-  return uint16_t(two_rounded<F16>(v, 0.0f) & 0xffffu);
-}
-template <bool F16>
-__device__ __forceinline__ float one_float(uint16_t v) {
-  return two_floats<F16>(uint32_t(v)).x;
-}
-
-// Two weights: byte J of `word` looked up in the lane's copy of the table, times
-// the scale, rounded to the compute type.
-template <int J, bool F16>
-__device__ __forceinline__ uint32_t two_weights(const uint8_t* lut, uint32_t word, uint32_t lane8, float scale) {
-  uint32_t at;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(at) : "r"(word), "r"(lane8), "n"(0x5504 | (J << 4)));   // {lane8.b0, word.bJ, 0, 0}
-  const float2 l = *reinterpret_cast<const float2*>(lut + at);
-  return two_rounded<F16>(__fmul_rn(l.x, scale), __fmul_rn(l.y, scale));
-}
 
 // A tile of the work list: row group, its expert and first row, 128 W rows.  The
 // roles walk the tiles of a share one after another.
@@ -519,19 +471,6 @@ __global__ void __launch_bounds__(kDcThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->red_full);
   }
-}
-
-// Eight products of two 16-byte chunks of 16-bit values, added to acc in order.
-template <bool F16>
-__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
-  const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 u = two_floats<F16>(aw[i]), v = two_floats<F16>(bw[i]);
-    acc = fmaf(u.x, v.x, acc);
-    acc = fmaf(u.y, v.y, acc);
-  }
-  return acc;
 }
 
 // T = s x A_e^T for a few rows: one CTA per adapter row and token, fp32 sums in

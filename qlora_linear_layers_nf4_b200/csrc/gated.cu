@@ -5,6 +5,7 @@
 
 #include "gated.h"
 #include "gated_act.cuh"
+#include "gated_decode.h"
 #include "gated_rank.h"
 #include "nf4_common.cuh"
 
@@ -14,6 +15,9 @@ namespace {
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 size_t mr_bytes(int64_t M, int r, size_t size) { return align256(size_t(M) * size_t(r) * size); }
 size_t pair_bytes(int64_t M, int64_t N, size_t size) { return align256(2 * size_t(M) * size_t(N) * size); }
+
+// Few tokens: stream the weights (16 tokens a pass) instead of feeding the GEMM.
+bool use_decode(int64_t M) { return M <= 32; }
 
 // ------------------------------------------------------------------ fp32 mode
 //
@@ -114,19 +118,25 @@ cudaError_t bwd_f32(const GatedArgs& a, int sms, cudaStream_t st, int* launches)
 
 }  // namespace
 
-// 16-bit: fwd [T]; bwd [T] [terms of U] [dg, du].
+// 16-bit: fwd [T] [the decode kernel's partials and counters]; bwd [T] [terms of U] [dg, du].
 // fp32: the dense layer's, then fwd [g, u]; bwd [dg, du] [the second projection's dx].
 size_t gated_workspace_bytes(bool backward, bool f32, int64_t M, int64_t N, int64_t K, int r) {
   if (M < 0 || N < 0 || K < 0 || r < 0) return 0;
   if (f32)
     return linear_workspace_bytes(backward, M, N, K, r) + pair_bytes(M, N, 4) + (backward ? align256(size_t(M) * size_t(K) * 4) : 0);
   const size_t t = mr_bytes(2 * M, r, 2);
-  return backward ? t + mr_bytes(6 * M, r, 2) + pair_bytes(M, N, 2) : t;
+  return backward ? t + mr_bytes(6 * M, r, 2) + pair_bytes(M, N, 2) : t + gated_decode_scratch_bytes();
 }
 
 cudaError_t launch_gated_fwd(const GatedArgs& a, int sms, cudaStream_t st, int* launches) {
   if (a.f32) return fwd_f32(a, sms, st, launches);
   void* T = a.t_out != nullptr ? a.t_out : a.ws + kWsHeader;
+  GatedDecode d;
+  if (use_decode(a.M)) {
+    if (!d.prepare(a, T, a.ws + kWsHeader + mr_bytes(2 * a.M, a.r, 2), sms)) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_gated_t_small(a, T, d.p.counters, st, launches);
+    return e == cudaSuccess ? d.run(st, launches) : e;
+  }
   GatedRank t;
   GatedGemm h;
   if (!t.prepare(a, kGatedT, nullptr, nullptr, T, sms) || !h.prepare(a, false, a.x, T, sms)) return cudaErrorInvalidValue;
@@ -142,14 +152,16 @@ cudaError_t launch_gated_bwd(const GatedArgs& a, int sms, cudaStream_t st, int* 
   const void* T = a.t_in != nullptr ? a.t_in : ws;
   GatedRank t, u, db, da;
   GatedGemm dx;
-  bool ok = a.t_in != nullptr || t.prepare(a, kGatedT, nullptr, nullptr, ws, sms);
+  // T again comes from the kernel that made it in the forward: the same bits
+  const bool small_t = use_decode(a.M);
+  bool ok = a.t_in != nullptr || small_t || t.prepare(a, kGatedT, nullptr, nullptr, ws, sms);
   ok = ok && u.prepare(a, kGatedU, nullptr, d, U, sms);
   ok = ok && db.prepare(a, kGatedDB, T, nullptr, a.dB, sms);
   ok = ok && da.prepare(a, kGatedDA, U, nullptr, a.dA, sms);
   ok = ok && (a.dx == nullptr || dx.prepare(a, true, d, U, sms));
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
-  if (a.t_in == nullptr) e = t.run(st, launches);
+  if (a.t_in == nullptr) e = small_t ? launch_gated_t_small(a, ws, nullptr, st, launches) : t.run(st, launches);
   if (e == cudaSuccess) e = u.run(st, launches);
   if (e == cudaSuccess && a.dx != nullptr) e = dx.run(st, launches);
   if (e == cudaSuccess) e = db.run(st, launches);
