@@ -43,6 +43,7 @@ struct GatedMaps {
   CUtensorMap ad_l, ad_s;     // T or U [2][M][r]: the same
   CUtensorMap wad;            // backward: A [2][r][K]
   CUtensorMap codes[2];       // backward: NF4 codes
+  CUtensorMap h, pre;         // forward: the results, in pieces of 32 tokens x 64 outputs
 };
 
 struct GatedParams {

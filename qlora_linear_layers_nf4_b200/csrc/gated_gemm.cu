@@ -17,7 +17,7 @@
 // du against the up projection's, then the two adapters.
 //
 // Roles in each CTA: warp 0 token TMA, warp 1 weight-side TMA (kDx), warp 2 MMA (issued by
-// the pair's leader), warps 4-7 epilogue, the rest dequant.  Rings: six stages of [weight
+// the pair's leader), from warp 4 on one or two epilogue groups, then the dequant groups.  Rings: six stages of [weight
 // tile 16 KB | tokens 16 KB], or four with 32 KB of tokens; six code slots (kDx); two
 // accumulators of 256 TMEM columns.
 #include <algorithm>
@@ -50,15 +50,19 @@ constexpr uint32_t kWBytes = 128 * 128;     // weight tile of a CTA: 128 x 128 b
 constexpr uint32_t kTBytes = 128 * 128;     // its tokens of one part
 constexpr uint32_t kCodeBytes = 128 * 32;   // kDx: NF4 codes of one step
 constexpr int kCodeSlots = 6;
-constexpr int kEpiWarp = 4;                 // warps 4..7
-constexpr int kDeqWarp = 8;
+constexpr int kEpiWarp = 4;
 
 constexpr int tile_w(int mode) { return mode == kFwd ? 128 : 256; }   // outputs of a pair's tile
 constexpr int stages_of(int parts) { return parts == 2 ? 4 : 6; }
 // Dequant groups of four warps each take every deq_groups-th step; the stages and
 // the code slots are multiples of their number, so that each belongs to one group.
 constexpr int deq_groups(int parts) { return parts == 2 ? 2 : 3; }
-constexpr int threads_of(int parts) { return 32 * (kDeqWarp + 4 * deq_groups(parts)); }
+// Epilogue groups of four warps.  The forward's epilogue (an exponential and a reciprocal an
+// output) cannot run under the next tile's MMAs where a tile fills both accumulators: two
+// groups take its pieces in turn.
+constexpr int epi_groups(int mode, int parts) { return mode == 0 && parts == 2 ? 2 : 1; }
+constexpr int deq_warp(int mode, int parts) { return kEpiWarp + 4 * epi_groups(mode, parts); }
+constexpr int threads_of(int mode, int parts) { return 32 * (deq_warp(mode, parts) + 4 * deq_groups(parts)); }
 constexpr uint32_t stage_bytes_of(int parts) { return kWBytes + uint32_t(parts) * kTBytes; }
 
 struct GemmShared {
@@ -73,15 +77,19 @@ struct GemmShared {
   uint32_t abort_flag;
 };
 
+// Behind the ring: kDx the code slots, kFwd two sets of staged pieces (h, g, u).
+constexpr uint32_t kPiece = 32 * 128;
+constexpr uint32_t extra_bytes(int mode) { return mode == kDx ? kCodeSlots * kCodeBytes : 2 * 3 * kPiece; }
 constexpr size_t gemm_smem(int mode, int parts) {
-  return size_t(stages_of(parts)) * stage_bytes_of(parts) + (mode == kDx ? kCodeSlots * kCodeBytes : 0) +
-         sizeof(GemmShared) + 1024;
+  return size_t(stages_of(parts)) * stage_bytes_of(parts) + extra_bytes(mode) + sizeof(GemmShared) + 1024;
 }
-static_assert(gemm_smem(kDx, 1) <= 232448 && gemm_smem(kDx, 2) <= 232448, "shared memory of one CTA");
+static_assert(gemm_smem(kDx, 1) <= 232448 && gemm_smem(kDx, 2) <= 232448 && gemm_smem(kFwd, 1) <= 232448 &&
+                  gemm_smem(kFwd, 2) <= 232448,
+              "shared memory of one CTA");
 
 struct Tile {
   int t0, cnt;  // first token, tokens
-  int nt[2];    // MMA columns of the parts (multiples of 16; 0: no second part)
+  int nt[2];    // MMA columns of the parts (multiples of 16, of a first of two of 32; 0: no second part)
   int n0;       // first output
 };
 
@@ -94,7 +102,7 @@ __device__ __forceinline__ Tile tile_at(const GatedParams& p, int id) {
   t.t0 = rt * p.tile_rows;
   t.cnt = min(p.tile_rows, p.M - t.t0);
   const int nt = (t.cnt + 15) & ~15;
-  t.nt[0] = PARTS == 2 && nt > kPartT ? ((nt >> 1) + 15) & ~15 : nt;
+  t.nt[0] = PARTS == 2 && nt > kPartT ? ((nt >> 1) + 31) & ~31 : nt;
   t.nt[1] = nt - t.nt[0];
   t.n0 = ct * tile_w(MODE);
   return t;
@@ -108,36 +116,44 @@ __device__ __forceinline__ uint32_t code_offset(uint32_t row) {
   return R * 64u + ((c ^ ((R >> 1) & 3u)) << 4);
 }
 
-// Sixteen values a lane, of token 2 j + (lane & 1) and output col, to a row-major matrix:
-// lanes two apart (neighbouring outputs) trade so that each stores two outputs of a token.
-// `left`: tokens from the first on that are stored.
+// Sixteen values a lane, of tokens 2 j + (lane & 1) and output `out` of a CTA's 64, into a
+// staged piece [32 tokens][64 outputs] (128-byte swizzle): lanes two apart (neighbouring
+// outputs) trade so that each writes two outputs of a token.
 template <bool F16>
-__device__ __forceinline__ void store_pairs(const float (&v)[16], uint16_t* out, int64_t cols, int64_t row0, int col,
-                                            int left, bool col_ok) {
+__device__ __forceinline__ void stage_pairs(const float (&v)[16], uint8_t* piece, int out) {
   const int lane = threadIdx.x & 31;
-  const int odd = lane & 1;
   const bool hi = lane & 2;
-  uint16_t* o = out + (row0 + odd + (hi ? 2 : 0)) * cols + (col & ~1);
-  const int first = odd + (hi ? 2 : 0);
+  const uint32_t first = uint32_t(lane & 1) + (hi ? 2u : 0u);
+  const uint32_t chunk = uint32_t(out) >> 3, in = (uint32_t(out) & 6u) * 2u;
 #pragma unroll
   for (int j = 0; j < 16; j += 2) {
     const float got = __shfl_xor_sync(0xffffffffu, hi ? v[j] : v[j + 1], 2);
     const uint32_t two = pack2(F16, hi ? got : v[j], hi ? v[j + 1] : got);
-    if (col_ok && 2 * j + first < left) *reinterpret_cast<uint32_t*>(o + int64_t(2 * j) * cols) = two;
+    *reinterpret_cast<uint32_t*>(piece + sw128_offset(first + 2u * uint32_t(j), chunk) + in) = two;
   }
 }
 
+// Tiled store of a 3-D box.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 template <int MODE, bool F16, int PARTS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PARTS), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PARTS), 1)
     gated_gemm_kernel(const __grid_constant__ GatedMaps maps, const GatedParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = expert::align_1024(smem_raw);
   constexpr int kStages = stages_of(PARTS);
   constexpr int kDeqGroups = deq_groups(PARTS);
+  constexpr int kEpiGroups = epi_groups(MODE, PARTS);
+  constexpr int kDeqWarp = deq_warp(MODE, PARTS);
   static_assert(kStages % kDeqGroups == 0 && kCodeSlots % kDeqGroups == 0, "a stage and a slot belong to one group");
   constexpr uint32_t kStageBytes = stage_bytes_of(PARTS);
   uint8_t* code_base = smem + kStages * kStageBytes;
-  GemmShared* sh = reinterpret_cast<GemmShared*>(code_base + (MODE == kDx ? kCodeSlots * kCodeBytes : 0));
+  GemmShared* sh = reinterpret_cast<GemmShared*>(code_base + extra_bytes(MODE));
   auto stage_w = [&](int s) { return smem + s * kStageBytes; };
   auto stage_t = [&](int s) { return smem + s * kStageBytes + kWBytes; };
 
@@ -159,7 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PARTS), 1
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->acc_full[b], 1);
-      mbar_init(&sh->acc_empty[b], 8);   // leader: the epilogue warps of both CTAs
+      mbar_init(&sh->acc_empty[b], 8 * kEpiGroups);   // leader: the epilogue warps of both CTAs
     }
     mbar_init(&sh->drain, 1);
     sh->abort_flag = 0;
@@ -167,6 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PARTS), 1
     fence_proxy_async_smem();
     tma_prefetch(&maps.tok_l);
     tma_prefetch(&maps.tok_s);
+    if (MODE == kFwd) tma_prefetch(&maps.h);
   }
   if (warp == 2) {
     tmem_alloc_pair(&sh->tmem_base, 512);
@@ -185,9 +202,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PARTS), 1
   auto ad_proj = [&](int k) { return k - p.main_steps >= p.ad_steps ? 1 : 0; };
   auto ad_r0 = [&](int k) { return (k - p.main_steps - (ad_proj(k) ? p.ad_steps : 0)) * 64; };
 
+  // With two epilogue groups the 20 warps of 96 registers share them as 4 x 56 (loads, MMA),
+  // 8 x 88 (epilogue) and 8 x 120 (dequant).
+  constexpr bool kShare = kEpiGroups == 2;
+  auto few_registers = [] {
+    if constexpr (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  };
+
   // The single-issuer roles run as whole warps with one elected lane, so that
   // their counters and addresses stay in uniform registers.
   if (warp == 0) {
+    few_registers();
     // ---------------- tokens: this CTA's half of the tile, in a 128-row box (or
     // a 32-row one)
     const bool issue = elect_one();
@@ -243,6 +268,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PARTS), 1
       }
   } else if (warp == 1) {
     // ---------------- kDx: the codes of every main step
+    few_registers();
     if (MODE == kDx) {
       const bool issue = elect_one();
       int s = 0;
@@ -274,6 +300,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PARTS), 1
     }
   } else if (warp == 2) {
     // ---------------- MMA: the leader's warp walks the steps, one lane issues
+    few_registers();
     if (rank == 0) {
       const bool issue = elect_one();
       // descriptors of stage 0; a stage is kStageBytes further, a K substep 32
@@ -331,12 +358,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PARTS), 1
         ring_wait(&sh->drain, 0, &none, nullptr);
       }
     }
-  } else if (warp >= kEpiWarp && warp < kDeqWarp) {
+  } else if (warp == 3) {
+    few_registers();
+  } else if (warp < kDeqWarp) {
     // ---------------- epilogue: lane = output (kFwd: projection lane & 1 of output
     // lane >> 1), register = token
-    const int quad = warp - kEpiWarp;
+    if constexpr (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    const int quad = warp & 3, group = (warp - kEpiWarp) >> 2;
     const int odd = lane & 1;
     int n = 0, last = 0;   // last: stage of the tile's last step
+    [[maybe_unused]] int pieces = 0;   // kFwd: stored so far
     bool ok = true;
     for (int id = pair; id < tiles && ok; id += pairs) {
       const Tile t = tile_at<MODE, PARTS>(p, id);
@@ -357,15 +388,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PARTS), 1
         const int t0 = h == 0 ? t.t0 : t.t0 + t.nt[0];
         const int cnt = h + 1 == parts ? t.t0 + t.cnt - t0 : t.nt[0];
         ok = warp_wait<300>(&sh->acc_full[n & 1], (n >> 1) & 1, abort_flag, p.status);
+        if (MODE == kFwd) ok = named_barrier_and(1 + group, 128, ok);   // the warps that store together go on together
         if (!ok) break;
-        if (h + 1 == parts && quad == 0 && lane == 0) mbar_arrive(&sh->empty[(last + kStages - 1) % kStages]);
+        if (h + 1 == parts && group == 0 && quad == 0 && lane == 0) mbar_arrive(&sh->empty[(last + kStages - 1) % kStages]);
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c * 32 < cnt; ++c) {
+        for (int c = group; c * 32 < cnt; c += kEpiGroups) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + uint32_t(n & 1) * 256u + c * 32, v);
           tmem_ld_wait();
-          const int left = cnt - c * 32;
+          [[maybe_unused]] const int left = cnt - c * 32;
           const int64_t row0 = int64_t(t0) + c * 32;
           if (MODE == kFwd) {
             float g[16], u[16];
@@ -376,14 +408,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PARTS), 1
               g[i / 2] = odd ? got : a;
               u[i / 2] = odd ? b : got;
             }
-            uint16_t* pre = static_cast<uint16_t*>(p.pre);
-            if (pre != nullptr) {
-              store_pairs<F16>(g, pre, p.out_cols, row0, col, left, col_ok);
-              store_pairs<F16>(u, pre + int64_t(p.M) * p.out_cols, p.out_cols, row0, col, left, col_ok);
+            // Pieces [32 tokens][64 outputs] of the group's four warps leave by TMA as whole lines.  (As 32-byte pieces straight from
+            // registers the forward of 4096 tokens with g and u took 728 us against 600
+            // without.)
+            constexpr int kSets = kEpiGroups == 2 ? 1 : 2;   // of a group
+            uint8_t* piece = code_base + (group + pieces % kSets) * (3 * kPiece);
+            if (pieces >= kSets) {   // the stores of kSets pieces ago have read this set
+              if (quad == 0 && lane == 0) bulk_wait_group_read<kSets - 1>();
+              named_barrier(1 + group, 128);
+            }
+            ++pieces;
+            const int out = quad * 16 + (lane >> 1);
+            const bool pre = p.pre != nullptr;
+            if (pre) {
+              stage_pairs<F16>(g, piece + kPiece, out);
+              stage_pairs<F16>(u, piece + 2 * kPiece, out);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) g[i] = gated::act<true>(p.act, g[i]) * u[i];
-            store_pairs<F16>(g, static_cast<uint16_t*>(p.out), p.out_cols, row0, col, left, col_ok);
+            stage_pairs<F16>(g, piece, out);
+            fence_proxy_async_smem();
+            named_barrier(1 + group, 128);
+            if (quad == 0 && lane == 0) {
+              const int x0 = t.n0 + 64 * int(rank);
+              if (x0 < p.out_cols) {   // outputs past N and tokens past M are clipped
+                tma_store_3d(&maps.h, piece, x0, int(row0), 0);
+                if (pre) {
+                  tma_store_3d(&maps.pre, piece + kPiece, x0, int(row0), 0);
+                  tma_store_3d(&maps.pre, piece + 2 * kPiece, x0, int(row0), 1);
+                }
+              }
+              bulk_commit_group();
+            }
           } else {
             // two lanes trade so that each stores two neighbouring outputs of one token
             uint16_t* o = static_cast<uint16_t*>(p.out) + (row0 + odd) * p.out_cols + (col & ~1);
@@ -401,11 +457,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PARTS), 1
         if (lane == 0) arrive_leader(leader_bar(&sh->acc_empty[n & 1]));
       }
     }
+    if (MODE == kFwd && quad == 0 && lane == 0) bulk_wait_group_all();
   } else if (warp >= kDeqWarp) {
     // ---------------- dequant warps: one thread per weight-tile row and step, so
     // the table of a block's sixteen values is built once.  A group of four warps
     // takes every kDeqGroups-th step: decoding (codes to registers) needs no free
     // stage, so it runs ahead of the MMAs, and only the stores wait for the stage.
+    if constexpr (kShare) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     const int group = (warp - kDeqWarp) >> 2;
     const int row = threadIdx.x & 127;
     const bool dq = p.dq != 0;
@@ -533,7 +591,7 @@ cudaError_t set_attrs() {
   for (const void* k : kernels)
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               int(std::max(gemm_smem(kDx, 1), gemm_smem(kDx, 2))));
+                               int(std::max(std::max(gemm_smem(kDx, 1), gemm_smem(kDx, 2)), std::max(gemm_smem(kFwd, 1), gemm_smem(kFwd, 2)))));
   if (e == cudaSuccess) g_attr_done.mark(dev);
   return e;
 }
@@ -544,7 +602,7 @@ cudaError_t launch(const GatedGemm& L, cudaStream_t st, int* launches) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(L.grid, 1, 1);
-  cfg.blockDim = dim3(threads_of(PARTS), 1, 1);
+  cfg.blockDim = dim3(threads_of(MODE, PARTS), 1, 1);
   cfg.dynamicSmemBytes = gemm_smem(MODE, PARTS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -592,7 +650,11 @@ bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, cons
   bool ok = encode_map_stack(&maps.tok_l, tok, MapElem::k16, cols, M, depth, 64, 128, s128) &&
             encode_map_stack(&maps.tok_s, tok, MapElem::k16, cols, M, depth, 64, 32, s128) &&
             ad_map(&maps.ad_l, ad, r, M, ad_terms, 128) && ad_map(&maps.ad_s, ad, r, M, ad_terms, 32);
-  maps.wad = maps.codes[0] = maps.codes[1] = maps.tok_l;
+  maps.wad = maps.codes[0] = maps.codes[1] = maps.h = maps.pre = maps.tok_l;
+  if (!backward) {
+    ok = ok && encode_map_stack(&maps.h, a.h, MapElem::k16, N, M, 1, 64, 32, s128);
+    if (a.pre_out != nullptr) ok = ok && encode_map_stack(&maps.pre, a.pre_out, MapElem::k16, N, M, 2, 64, 32, s128);
+  }
   if (backward) {
     ok = ok && encode_map_stack(&maps.wad, a.A, MapElem::k16, K, r, 2, 64, 64, s128);
     for (int i = 0; i < 2; ++i)   // a step's codes: 128 columns of 64 W rows
@@ -609,7 +671,7 @@ bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, cons
   p.ad_steps = (a.r + 63) / 64;
   p.col_tiles = int(col_tiles);
   p.row_tiles = int(cdiv(a.M, int64_t(parts) * kPartT));
-  p.tile_rows = int((cdiv(a.M, p.row_tiles) + 15) & ~int64_t(15));
+  p.tile_rows = int((cdiv(a.M, p.row_tiles) + 31) & ~int64_t(31));   // pieces of 32 tokens are stored whole
   p.block_chunks_shift = log2_block(a.w[0]->block_size) - 6;
   p.dq = a.w[0]->double_quant;
   p.act = a.act;
