@@ -501,7 +501,7 @@ NF4_API nf4_status qlora_grouped_bwd(const nf4_weight* w, int num_experts, const
  *                  qlora_gated_bwd takes as `pre`.
  *   t_out          [2, M, r] compute_dtype, or NULL: T, rounded; its `t`.
  *   workspace      >= nf4_workspace_bytes(NF4_OP_GATED_FWD, M, N, K, r, 64, dq), with
- *                  NF4_F32 of NF4_OP_GATED_FWD_F32 (which holds g and u).
+ *                  NF4_F32 of NF4_OP_GATED_FWD_F32.
  * A token's result depends on the tokens beside it only through the order of its sums.  In
  * BF16 and F16 a T beyond the compute type's range makes g and u of its token non-finite in
  * both projections.

@@ -36,6 +36,11 @@ size_t gated_workspace_bytes(bool backward, bool f32, int64_t M, int64_t N, int6
 cudaError_t launch_gated_fwd(const GatedArgs& a, int sms, cudaStream_t stream, int* launches);
 cudaError_t launch_gated_bwd(const GatedArgs& a, int sms, cudaStream_t stream, int* launches);
 
+// The F32 compute dtype, on the CUDA cores (gated_simt.cu).
+size_t gated_f32_workspace_bytes(bool backward, int64_t M, int64_t N, int r);
+cudaError_t launch_gated_fwd_f32(const GatedArgs& a, int sms, cudaStream_t stream, int* launches);
+cudaError_t launch_gated_bwd_f32(const GatedArgs& a, int sms, cudaStream_t stream, int* launches);
+
 // ---- gated_gemm.cu
 
 struct GatedMaps {

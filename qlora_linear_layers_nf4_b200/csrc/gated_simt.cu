@@ -1,0 +1,364 @@
+// Gated feed-forward layer on the CUDA cores: the fp32 mode, where every product and sum is an
+// fp32 operation.
+//
+// One kernel does every product of both projections z (a grid dimension):
+//     C_z(i, j) = alpha sum over up to four segments of a(i, kk) b(j, kk)
+// with each operand a dense matrix in either major order or a projection's NF4 weight decoded
+// on load; a second form keeps the sums of both projections and finishes h = act(g) u.
+// T x T tiles (64, or 32 where those would leave SMs idle), 256 threads, the reduction in
+// slices of 32 through shared memory with the loads of the next two slices in flight; a
+// slice's products are summed by themselves before they are added to the others.
+#include <algorithm>
+
+#include <cuda_runtime.h>
+
+#include "gated.h"
+#include "gated_act.cuh"
+#include "nf4_common.cuh"
+
+namespace nf4 {
+namespace {
+
+constexpr int kSK = 32;
+constexpr int kSThreads = 256;
+
+// Element (i, kk).  Contiguous runs of four stay inside an operand: every row length is a
+// multiple of eight.
+struct SimtOperand {
+  const float* p;        // null: the NF4 weight w
+  int w;
+  int64_t ld;            // elements between consecutive stored rows
+  int kmajor;            // 1: (i, kk) at p[i * ld + kk]; 0: at p[kk * ld + i]
+  int64_t extent;        // of i
+  int64_t z_stride;      // elements to the other projection's matrix
+  int z_w;               // 1: the other projection's weight is the other one
+};
+
+struct SimtSegment {
+  SimtOperand a, b;
+  int64_t kdim;
+};
+
+struct SimtWeight {
+  const uint8_t* codes;
+  const float* absmax;
+  const uint8_t* absmax_q;
+  const float* absmax_scale;
+};
+
+struct SimtParams {
+  SimtSegment seg[4];
+  int nseg;
+  int64_t rows, cols;
+  float* c;              // [z][rows][cols]
+  float alpha;
+  int col_tiles;
+  SimtWeight w[2];
+  int dq, bs_shift;
+  // the gated form: seg[0], seg[1] of projection 0, 2 and 3 of projection 1
+  const float* bias;     // [2][cols] or null
+  float* pre;            // [2][rows][cols] or null
+  int act;
+};
+
+template <int T, bool GATED>
+__global__ void __launch_bounds__(kSThreads) gated_simt_kernel(const SimtParams p) {
+  constexpr int kRow = T + 4;
+  constexpr int kLoads = T * kSK / 4 / kSThreads;      // runs of four a thread, per operand and slice
+  constexpr int kOwn = T / 16;                         // results of a thread per dimension
+  __shared__ float sa[2][kSK * kRow];
+  __shared__ float sb[2][kSK * kRow];
+  __shared__ float lut[16];
+  const int t = threadIdx.x;
+  if (t < 16) lut[t] = level(t);
+  __syncthreads();
+  const int64_t j0 = int64_t(blockIdx.x % p.col_tiles) * T, i0 = int64_t(blockIdx.x / p.col_tiles) * T;
+  const int z = blockIdx.z;
+
+  // Run l of a slice.  kmajor: index = (t + 256 l) / 8, kk = 4 (t % 8) ..; else kk, then index.
+  auto load = [&](const SimtOperand& o, int64_t first, int64_t k0, int64_t kend, float4 (&v)[kLoads]) {
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+      const int q = t + kSThreads * l;
+      const int64_t i = first + (o.kmajor ? q / (kSK / 4) : 4 * (q % (T / 4)));
+      const int64_t kk = k0 + (o.kmajor ? 4 * (q % (kSK / 4)) : q / (T / 4));
+      v[l] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i >= o.extent || kk >= kend) continue;
+      const int64_t at = o.kmajor ? i * o.ld + kk : kk * o.ld + i;
+      if (o.p != nullptr) {
+        v[l] = __ldg(reinterpret_cast<const float4*>(o.p + z * o.z_stride + at));
+      } else {
+        const SimtWeight& w = p.w[o.w ^ (z & o.z_w)];
+        const uint32_t two = __ldg(reinterpret_cast<const uint16_t*>(w.codes + (at >> 1)));
+        const int64_t blk = at >> p.bs_shift;
+        const float s = p.dq ? __fmul_rn(float(__ldg(w.absmax_q + blk)), __ldg(w.absmax_scale)) : __ldg(w.absmax + blk);
+        v[l] = make_float4(__fmul_rn(lut[(two >> 4) & 15u], s), __fmul_rn(lut[two & 15u], s),
+                           __fmul_rn(lut[two >> 12], s), __fmul_rn(lut[(two >> 8) & 15u], s));
+      }
+    }
+  };
+  auto park = [&](const SimtOperand& o, float* s, const float4 (&v)[kLoads]) {
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+      const int q = t + kSThreads * l;
+      if (o.kmajor) {
+        float* d = s + 4 * (q % (kSK / 4)) * kRow + q / (kSK / 4);
+        d[0] = v[l].x;
+        d[kRow] = v[l].y;
+        d[2 * kRow] = v[l].z;
+        d[3 * kRow] = v[l].w;
+      } else {
+        *reinterpret_cast<float4*>(s + q / (T / 4) * kRow + 4 * (q % (T / 4))) = v[l];
+      }
+    }
+  };
+
+  const int ty = t >> 4, tx = t & 15;
+  constexpr int kSets = GATED ? 2 : 1;
+  float acc[kSets][kOwn][kOwn];
+#pragma unroll
+  for (int g = 0; g < kSets; ++g)
+#pragma unroll
+    for (int a = 0; a < kOwn; ++a)
+#pragma unroll
+      for (int b = 0; b < kOwn; ++b) acc[g][a][b] = 0.0f;
+
+  int cur = 0;
+  auto segment = [&](const SimtSegment& sg, float (&into)[kOwn][kOwn]) {
+    const int64_t slices = (sg.kdim + kSK - 1) / kSK;
+    float4 va[2][kLoads], vb[2][kLoads];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      load(sg.a, i0, h * kSK, sg.kdim, va[h]);
+      load(sg.b, j0, h * kSK, sg.kdim, vb[h]);
+    }
+    auto slice = [&](int64_t s, float4 (&xa)[kLoads], float4 (&xb)[kLoads]) {
+      park(sg.a, sa[cur], xa);
+      park(sg.b, sb[cur], xb);
+      __syncthreads();
+      load(sg.a, i0, (s + 2) * kSK, sg.kdim, xa);
+      load(sg.b, j0, (s + 2) * kSK, sg.kdim, xb);
+      float sum[kOwn][kOwn];
+#pragma unroll
+      for (int a = 0; a < kOwn; ++a)
+#pragma unroll
+        for (int b = 0; b < kOwn; ++b) sum[a][b] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < kSK; ++kk) {
+        float ar[kOwn], br[kOwn];
+#pragma unroll
+        for (int a = 0; a < kOwn; ++a) {
+          ar[a] = sa[cur][kk * kRow + kOwn * ty + a];
+          br[a] = sb[cur][kk * kRow + kOwn * tx + a];
+        }
+#pragma unroll
+        for (int a = 0; a < kOwn; ++a)
+#pragma unroll
+          for (int b = 0; b < kOwn; ++b) sum[a][b] = fmaf(ar[a], br[b], sum[a][b]);
+      }
+#pragma unroll
+      for (int a = 0; a < kOwn; ++a)
+#pragma unroll
+        for (int b = 0; b < kOwn; ++b) into[a][b] += sum[a][b];
+      cur ^= 1;   // the barrier of the next slice separates its writes from these reads' buffer
+    };
+    for (int64_t s = 0; s < slices; s += 2) {
+      slice(s, va[0], vb[0]);
+      if (s + 1 < slices) slice(s + 1, va[1], vb[1]);
+    }
+  };
+  if (GATED) {
+    segment(p.seg[0], acc[0]);
+    segment(p.seg[1], acc[0]);
+    segment(p.seg[2], acc[kSets - 1]);
+    segment(p.seg[3], acc[kSets - 1]);
+  } else {
+    for (int g = 0; g < p.nseg; ++g) segment(p.seg[g], acc[0]);
+  }
+
+#pragma unroll
+  for (int a = 0; a < kOwn; ++a) {
+    const int64_t i = i0 + kOwn * ty + a;
+    if (i >= p.rows) continue;
+#pragma unroll
+    for (int b = 0; b < kOwn; ++b) {
+      const int64_t j = j0 + kOwn * tx + b;
+      if (j >= p.cols) continue;
+      const int64_t at = i * p.cols + j;
+      if (GATED) {
+        float g = acc[0][a][b], u = acc[kSets - 1][a][b];
+        if (p.bias != nullptr) {
+          g = __fadd_rn(g, __ldg(p.bias + j));
+          u = __fadd_rn(u, __ldg(p.bias + p.cols + j));
+        }
+        if (p.pre != nullptr) {
+          p.pre[at] = g;
+          p.pre[p.rows * p.cols + at] = u;
+        }
+        p.c[at] = gated::act<false>(p.act, g) * u;
+      } else {
+        p.c[z * p.rows * p.cols + at] = __fmul_rn(p.alpha, acc[0][a][b]);
+      }
+    }
+  }
+}
+
+// dg, du
+__global__ void __launch_bounds__(kSThreads)
+    gated_grad_f32_kernel(const float* __restrict__ dh, const float* __restrict__ pre, float* __restrict__ d, int64_t n, int act) {
+  for (int64_t i = int64_t(blockIdx.x) * kSThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kSThreads) {
+    const gated::ActGrad a = gated::act_grad<false>(act, pre[i]);
+    const float v = dh[i];
+    d[i] = v * pre[n + i] * a.d;
+    d[n + i] = v * a.a;
+  }
+}
+
+SimtOperand dense(const void* p, int64_t ld, bool kmajor, int64_t extent, int64_t z_stride) {
+  return SimtOperand{static_cast<const float*>(p), 0, ld, kmajor ? 1 : 0, extent, z_stride, 0};
+}
+SimtOperand weight(int w, int64_t ld, bool kmajor, int64_t extent) { return SimtOperand{nullptr, w, ld, kmajor ? 1 : 0, extent, 0, 0}; }
+
+SimtParams common(const GatedArgs& a) {
+  SimtParams p{};
+  p.alpha = 1.0f;
+  for (int z = 0; z < 2; ++z) p.w[z] = SimtWeight{a.w[z]->codes, a.w[z]->absmax, a.w[z]->absmax_q, a.w[z]->absmax_scale};
+  p.dq = a.w[0]->double_quant ? 1 : 0;
+  p.bs_shift = log2_block(a.w[0]->block_size);
+  p.act = a.act;
+  return p;
+}
+
+struct Launch {
+  SimtParams p;
+  int zs, id;            // results (projections) of the launch
+  bool gated;
+};
+
+// 64 x 64 tiles where there are enough of them for the SMs: fewer loads a product.
+bool large_tiles(const Launch& l, int sms) { return (l.p.rows + 63) / 64 * ((l.p.cols + 63) / 64) * l.zs >= sms; }
+
+bool fits(const Launch& l) { return (l.p.rows + 31) / 32 * ((l.p.cols + 31) / 32) <= int64_t(0x7fffffff); }
+
+cudaError_t run(Launch l, int sms, cudaStream_t st, int* launches) {
+  const bool large = large_tiles(l, sms);
+  const int64_t t = large ? 64 : 32;
+  const int64_t ct = (l.p.cols + t - 1) / t, rt = (l.p.rows + t - 1) / t;
+  l.p.col_tiles = int(ct);
+  const dim3 grid(unsigned(ct * rt), 1, unsigned(l.zs));
+  NF4_PROF_BEGIN(st, l.id);
+  if (l.gated) {
+    if (large) gated_simt_kernel<64, true><<<grid, kSThreads, 0, st>>>(l.p);
+    else gated_simt_kernel<32, true><<<grid, kSThreads, 0, st>>>(l.p);
+  } else {
+    if (large) gated_simt_kernel<64, false><<<grid, kSThreads, 0, st>>>(l.p);
+    else gated_simt_kernel<32, false><<<grid, kSThreads, 0, st>>>(l.p);
+  }
+  NF4_PROF_END(st, l.id);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+Launch product_T(const GatedArgs& a, void* T) {
+  Launch l{common(a), 2, kKGatedT, false};
+  l.p.nseg = 1;
+  l.p.seg[0] = SimtSegment{dense(a.x, a.K, true, a.M, 0), dense(a.A, a.K, true, a.r, int64_t(a.r) * a.K), a.K};
+  l.p.rows = a.M;
+  l.p.cols = a.r;
+  l.p.c = static_cast<float*>(T);
+  l.p.alpha = a.s;
+  return l;
+}
+
+size_t t_bytes(int64_t M, int r) { return (2 * size_t(M) * size_t(r) * 4 + 255) / 256 * 256; }
+
+}  // namespace
+
+// [T] and, backward, [U] [dg, du]
+size_t gated_f32_workspace_bytes(bool backward, int64_t M, int64_t N, int r) {
+  return backward ? 2 * t_bytes(M, r) + (2 * size_t(M) * size_t(N) * 4 + 255) / 256 * 256 : t_bytes(M, r);
+}
+
+cudaError_t launch_gated_fwd_f32(const GatedArgs& a, int sms, cudaStream_t st, int* launches) {
+  float* T = a.t_out != nullptr ? static_cast<float*>(a.t_out) : reinterpret_cast<float*>(a.ws + kWsHeader);
+  const Launch t = product_T(a, T);
+  Launch h{common(a), 1, kKGatedFwd, true};
+  for (int z = 0; z < 2; ++z) {
+    h.p.seg[2 * z] = SimtSegment{dense(a.x, a.K, true, a.M, 0), weight(z, a.K, true, a.N), a.K};
+    h.p.seg[2 * z + 1] = SimtSegment{dense(T + int64_t(z) * a.M * a.r, a.r, true, a.M, 0),
+                                     dense(static_cast<const float*>(a.B) + int64_t(z) * a.N * a.r, a.r, true, a.N, 0), a.r};
+  }
+  h.p.rows = a.M;
+  h.p.cols = a.N;
+  h.p.c = static_cast<float*>(a.h);
+  h.p.bias = static_cast<const float*>(a.bias);
+  h.p.pre = static_cast<float*>(a.pre_out);
+  if (!fits(t) || !fits(h)) return cudaErrorInvalidValue;
+  const cudaError_t e = run(t, sms, st, launches);
+  return e == cudaSuccess ? run(h, sms, st, launches) : e;
+}
+
+cudaError_t launch_gated_bwd_f32(const GatedArgs& a, int sms, cudaStream_t st, int* launches) {
+  uint8_t* ws = a.ws + kWsHeader;
+  float* U = reinterpret_cast<float*>(ws + t_bytes(a.M, a.r));
+  float* d = reinterpret_cast<float*>(ws + 2 * t_bytes(a.M, a.r));
+  const float* T = a.t_in != nullptr ? static_cast<const float*>(a.t_in) : reinterpret_cast<const float*>(ws);
+  const int64_t mn = a.M * a.N, mr = a.M * a.r;
+  Launch l[5];
+  int n = 0;
+  if (a.t_in == nullptr) l[n++] = product_T(a, ws);
+  {  // U_z = s d_z B_z
+    Launch u{common(a), 2, kKGatedU, false};
+    u.p.nseg = 1;
+    u.p.seg[0] = SimtSegment{dense(d, a.N, true, a.M, mn), dense(a.B, a.r, false, a.r, a.N * a.r), a.N};
+    u.p.rows = a.M;
+    u.p.cols = a.r;
+    u.p.c = U;
+    u.p.alpha = a.s;
+    l[n++] = u;
+  }
+  {  // dB_z = d_z^T T_z
+    Launch b{common(a), 2, kKGatedDB, false};
+    b.p.nseg = 1;
+    b.p.seg[0] = SimtSegment{dense(d, a.N, false, a.N, mn), dense(T, a.r, false, a.r, mr), a.M};
+    b.p.rows = a.N;
+    b.p.cols = a.r;
+    b.p.c = a.dB;
+    l[n++] = b;
+  }
+  {  // dA_z = U_z^T x
+    Launch b{common(a), 2, kKGatedDA, false};
+    b.p.nseg = 1;
+    b.p.seg[0] = SimtSegment{dense(U, a.r, false, a.r, mr), dense(a.x, a.K, false, a.K, 0), a.M};
+    b.p.rows = a.r;
+    b.p.cols = a.K;
+    b.p.c = a.dA;
+    l[n++] = b;
+  }
+  if (a.dx != nullptr) {  // dx = sum_z d_z W'_z + U_z A_z
+    Launch x{common(a), 1, kKGatedDx, false};
+    x.p.nseg = 4;
+    for (int z = 0; z < 2; ++z) {
+      x.p.seg[z] = SimtSegment{dense(d + z * mn, a.N, true, a.M, 0), weight(z, a.K, false, a.K), a.N};
+      x.p.seg[2 + z] = SimtSegment{dense(U + z * mr, a.r, true, a.M, 0),
+                                   dense(static_cast<const float*>(a.A) + int64_t(z) * a.r * a.K, a.K, false, a.K, 0), a.r};
+    }
+    x.p.rows = a.M;
+    x.p.cols = a.K;
+    x.p.c = static_cast<float*>(a.dx);
+    l[n++] = x;
+  }
+  for (int i = 0; i < n; ++i)
+    if (!fits(l[i])) return cudaErrorInvalidValue;
+  NF4_PROF_BEGIN(st, kKGatedAct);
+  gated_grad_f32_kernel<<<unsigned(std::max<int64_t>(1, std::min<int64_t>((mn + kSThreads - 1) / kSThreads, int64_t(sms) * 8))), kSThreads, 0, st>>>(
+      static_cast<const float*>(a.dh), static_cast<const float*>(a.pre_in), d, mn, a.act);
+  NF4_PROF_END(st, kKGatedAct);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  for (int i = 0; i < n && e == cudaSuccess; ++i) e = run(l[i], sms, st, launches);
+  return e;
+}
+
+}  // namespace nf4

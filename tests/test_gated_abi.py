@@ -58,8 +58,8 @@ def test_workspace_sizes():
     w = lambda op, m=100: Q.workspace_bytes(op, m, 264, 192, 16, 64, True)
     assert w(Q.OP_GATED_FWD) >= 256 + 2 * 100 * 16 * 2
     assert w(Q.OP_GATED_BWD) >= 256 + 2 * 100 * 264 * 2 + 4 * 2 * 100 * 16 * 2
-    assert w(Q.OP_GATED_FWD_F32) >= 256 + 2 * 100 * 264 * 4 + 100 * 16 * 4
-    assert w(Q.OP_GATED_BWD_F32) >= 256 + 2 * 100 * 264 * 4 + 100 * 192 * 4 + 2 * 100 * 16 * 4
+    assert w(Q.OP_GATED_FWD_F32) >= 256 + 2 * 100 * 16 * 4
+    assert w(Q.OP_GATED_BWD_F32) >= 256 + 2 * 100 * 264 * 4 + 2 * 2 * 100 * 16 * 4
     for op in (Q.OP_GATED_FWD, Q.OP_GATED_BWD, Q.OP_GATED_FWD_F32, Q.OP_GATED_BWD_F32):
         assert w(op, 0) >= 256
         need = w(op)
