@@ -62,8 +62,9 @@ cudaError_t launch_gated_bwd(const GatedArgs& a, int sms, cudaStream_t st, int* 
   if (a.t_in == nullptr) e = small_t ? launch_gated_t_small(a, ws, nullptr, st, launches) : t.run(st, launches);
   if (e == cudaSuccess) e = u.run(st, launches);
   if (e == cudaSuccess && a.dx != nullptr) e = dx.run(st, launches);
-  if (e == cudaSuccess) e = db.run(st, launches);
-  if (e == cudaSuccess) e = da.run(st, launches);
+  // dx lets dB start when U is complete, dB lets dA
+  if (e == cudaSuccess) e = db.run(st, launches, /*beside=*/a.dx != nullptr);
+  if (e == cudaSuccess) e = da.run(st, launches, /*beside=*/true);
   return e;
 }
 

@@ -218,7 +218,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
     const bool issue = elect_one();
     // kDx: dg and du come from the kernels before, kFwd's T too
     bool waited = MODE == kDx, ok = true;
-    if (MODE == kDx) grid_dep_wait();
+    if (MODE == kDx) {
+      grid_dep_wait();
+      // The gradients, launched behind this kernel, read nothing of it: they may fill the SMs
+      // that it leaves free, now that what they read is complete.
+      grid_dep_launch();
+    }
     int s = 0, issued = 0;
     uint32_t ph = 1;
     for (int id = pair; id < tiles && ok; id += pairs) {

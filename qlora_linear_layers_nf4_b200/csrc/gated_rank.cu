@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (p.slices > 1) sum_slices<KIND>(p, reinterpret_cast<float*>(smem), row0, col0);
+  if (KIND == kGatedDA) grid_dep_wait();   // see GatedRank::run
   if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tmem, kAccCols);
@@ -615,6 +616,7 @@ __global__ void __launch_bounds__(kMkThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (p.slices > 1) sum_slices<KIND>(p, reinterpret_cast<float*>(smem), row0, col0);
+  if (KIND == kGatedDB) grid_dep_wait();   // see GatedRank::run
   if (warp == kMkWarps) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -739,7 +741,11 @@ bool GatedRank::prepare(const GatedArgs& a, GatedRankKind k, const void* in, voi
   return ok && tiles <= int64_t(0x7fffffff);
 }
 
-cudaError_t GatedRank::run(cudaStream_t st, int* launches) const {
+// beside: run beside the kernel before on the stream, which must have let this one start
+// only when what it reads was complete.  dB and dA run so beside dx and each other; they wait
+// for the kernel before at their end, so that what comes after them on the stream finds
+// everything done.
+cudaError_t GatedRank::run(cudaStream_t st, int* launches, bool beside) const {
   cudaError_t e = set_attrs();
   if (e != cudaSuccess) return e;
   const bool tma = kind == kGatedT || kind == kGatedDA;
@@ -748,13 +754,15 @@ cudaError_t GatedRank::run(cudaStream_t st, int* launches) const {
   cfg.blockDim = dim3(tma ? kTmaThreads : kMkThreads, 1, 1);
   cfg.dynamicSmemBytes = tma ? tma_smem(kind) : kMkSmem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
   attr[0].val.clusterDim.y = grid.y;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = beside && !prof_on() ? 2 : 1;
   const int ids[] = {kKGatedT, kKGatedDA, kKGatedU, kKGatedDB};
   NF4_PROF_BEGIN(st, ids[kind]);
   switch (kind) {

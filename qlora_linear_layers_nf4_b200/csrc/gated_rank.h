@@ -36,7 +36,7 @@ struct GatedRank {
   GatedRankParams p;
   dim3 grid;
   bool prepare(const GatedArgs& a, GatedRankKind kind, const void* in, void* d, void* out, int sms);
-  cudaError_t run(cudaStream_t st, int* launches) const;
+  cudaError_t run(cudaStream_t st, int* launches, bool beside = false) const;
 };
 
 constexpr int gated_terms(bool f16) { return f16 ? 2 : 3; }
