@@ -354,20 +354,24 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
 
 constexpr int kMkWarps = 8;                                     // they make d, and finish the tile
 constexpr int kMkThreads = 32 * (kMkWarps + 2);                 // and B loads, MMA
-constexpr int kMkBufs = 2;
+constexpr int kMkPer = 4;                                       // chunks of eight elements a thread has of a step
+constexpr int kMkAhead = 2 * kMkPer;                            // and how many it copies ahead
+constexpr uint32_t kMkInBytes = 32 * kMkWarps * 16;             // a chunk's dh, g or u, of all threads
+constexpr int kMkBufs = 2;                                      // B of a step
 constexpr uint32_t kMkOpBytes = 6 * kTileBytes;                 // terms of dg, then of du
 constexpr uint32_t kMkBBytes = 2 * kBoxBytes;
 
 struct MkShared {
-  uint64_t opfull[kMkBufs];   // a step's terms are written
-  uint64_t bfull[kMkBufs];    // its B boxes landed
-  uint64_t empty[kMkBufs];    // the MMAs that read them finished
+  uint64_t opfull;            // a step's terms are written
+  uint64_t opempty;           // the MMAs that read them finished
+  uint64_t bfull[kMkBufs];    // a step's B boxes landed
+  uint64_t bempty[kMkBufs];   // and were read
   uint64_t accum;
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
-constexpr size_t kMkSmem = size_t(kMkBufs) * (kMkOpBytes + kMkBBytes) + sizeof(MkShared) + 1024;
-static_assert(kMkSmem <= 232448, "shared memory of one CTA");
+constexpr size_t kMkSmem = kMkOpBytes + size_t(kMkAhead) * 3 * kMkInBytes + kMkBufs * kMkBBytes + sizeof(MkShared) + 1024;
+static_assert(kMkSmem <= 232448 && kMkOpBytes >= kParkBytes, "shared memory of one CTA");
 
 // Two 16-bit values to fp32.
 template <bool F16>
@@ -416,11 +420,9 @@ __device__ __forceinline__ void split8(gated::F2 (&v)[4], uint4 (&term)[3]) {
   }
 }
 
-// A 16-byte load that stays where it is written: it is made long before its use.
-__device__ __forceinline__ uint4 load_ahead(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// 16 bytes from global to shared memory, or zeros, asynchronously.
+__device__ __forceinline__ void copy_ahead(uint32_t dst, const uint16_t* src, bool there) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 template <GatedRankKind KIND, bool F16, int ACT>
@@ -429,9 +431,11 @@ __global__ void __launch_bounds__(kMkThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = expert::align_1024(smem_raw);
   constexpr int kTerms = gated_terms(F16);
-  MkShared* sh = reinterpret_cast<MkShared*>(smem + kMkBufs * (kMkOpBytes + kMkBBytes));
-  auto op_tile = [&](int buf, int proj, int term) { return smem + buf * kMkOpBytes + uint32_t(proj * 3 + term) * kTileBytes; };
-  auto b_box = [&](int buf, int proj) { return smem + kMkBufs * kMkOpBytes + buf * kMkBBytes + proj * kBoxBytes; };
+  uint8_t* b_base = smem + kMkOpBytes;
+  uint8_t* inputs = b_base + kMkBufs * kMkBBytes;
+  MkShared* sh = reinterpret_cast<MkShared*>(inputs + kMkAhead * 3 * kMkInBytes);
+  auto op_tile = [&](int proj, int term) { return smem + uint32_t(proj * 3 + term) * kTileBytes; };
+  auto b_box = [&](int buf, int proj) { return b_base + buf * kMkBBytes + proj * kBoxBytes; };
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   volatile uint32_t* abort_flag = &sh->abort_flag;
@@ -443,10 +447,11 @@ __global__ void __launch_bounds__(kMkThreads, 1)
   grid_dep_launch();
   if (threadIdx.x == 0) {
     tma_prefetch(&tm_b);
+    mbar_init(&sh->opfull, kMkWarps);
+    mbar_init(&sh->opempty, 1);
     for (int b = 0; b < kMkBufs; ++b) {
-      mbar_init(&sh->opfull[b], kMkWarps);
       mbar_init(&sh->bfull[b], 1);
-      mbar_init(&sh->empty[b], 1);
+      mbar_init(&sh->bempty[b], 1);
     }
     mbar_init(&sh->accum, 1);
     sh->abort_flag = 0;
@@ -464,53 +469,52 @@ __global__ void __launch_bounds__(kMkThreads, 1)
 
   if (warp < kMkWarps) {
     // ---------------- d of 128 x 64 (U) or 64 x 128 (dB) elements a step, as two halves of
-    // 64 x 64: a thread takes eight elements (16-byte chunk t % 8 of row t / 8 and so on) kPer
-    // times.  Their dh, g and u are loaded a step ahead, as soon as those
-    // before are used.
+    // 64 x 64: a thread takes chunks of eight elements (16-byte chunk t % 8) of four rows.  It
+    // copies their dh, g and u to shared memory two steps ahead (as registers one step ahead
+    // allowed half of the bytes in flight), and keeps a step's terms until the MMAs have read
+    // the step before.
     const int tr = threadIdx.x >> 3, tc = threadIdx.x & 7;
     const int64_t mn = int64_t(p.M) * p.N;
     const int red0 = w.step0 * 64;
-    // chunk c (half half_of(c), row row_of(c)) in the first step; a step later it is `ahead` further.  `left`: how far the reduction index may still go.
+    // chunk c (half c / 2, row 32 (c % 2) + t / 8) in the first step; a step later it is
+    // `ahead` further.  `left`: how far the reduction index may still go.
     const int64_t ahead = KIND == kGatedU ? 64 : int64_t(64) * p.N;
-    constexpr int kPer = 1024 / (32 * kMkWarps), kPerHalf = kPer / 2;
-    auto half_of = [](int c) { return c / kPerHalf; };
-    auto row_of = [&](int c) { return c % kPerHalf * (64 / kPerHalf) + tr; };
-    int64_t at[kPer];
-    int left[kPer];
+    int64_t at[kMkPer];
+    int left[kMkPer];
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) {
-      const int r = row_of(c);
-      const int m = KIND == kGatedU ? row0 + 64 * half_of(c) + r : red0 + r;
-      const int n = KIND == kGatedU ? red0 + 8 * tc : row0 + 64 * half_of(c) + 8 * tc;
+    for (int c = 0; c < kMkPer; ++c) {
+      const int r = 32 * (c & 1) + tr;
+      const int m = KIND == kGatedU ? row0 + 64 * (c >> 1) + r : red0 + r;
+      const int n = KIND == kGatedU ? red0 + 8 * tc : row0 + 64 * (c >> 1) + 8 * tc;
       at[c] = int64_t(m) * p.N + n;
       left[c] = KIND == kGatedU ? (m < p.M ? p.N - n : 0) : (n < p.N ? p.M - m : 0);
     }
-    uint4 in[kPer][3];             // dh, g, u
-    auto fetch = [&](int c, int i) {
-      const bool there = i < w.steps && 64 * i < left[c];
-#pragma unroll
-      for (int j = 0; j < 3; ++j) in[c][j] = make_uint4(0u, 0u, 0u, 0u);
-      if (there) {
-        const int64_t e = at[c] + ahead * i;
-        in[c][0] = load_ahead(p.dh + e);
-        in[c][1] = load_ahead(p.pre + e);
-        in[c][2] = load_ahead(p.pre + mn + e);
+    auto place = [&](int c, int i) { return uint32_t((kMkPer * i + c) % kMkAhead) * (3 * kMkInBytes) + uint32_t(threadIdx.x) * 16u; };
+    auto copy = [&](int c, int i) {
+      if (i < w.steps) {
+        const bool there = 64 * i < left[c];
+        const int64_t e = there ? at[c] + ahead * i : 0;
+        const uint32_t dst = smem_u32(inputs) + place(c, i);
+        copy_ahead(dst, p.dh + e, there);
+        copy_ahead(dst + kMkInBytes, p.pre + e, there);
+        copy_ahead(dst + 2 * kMkInBytes, p.pre + mn + e, there);
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) fetch(c, 0);
+    for (int j = 0; j < kMkAhead; ++j) copy(j % kMkPer, j / kMkPer);
     bool ok = true;
     for (int i = 0; i < w.steps; ++i) {
-      const int b = i & 1;
-      if (ok) ok = warp_wait(&sh->empty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.status);
-      if (!ok) break;
-      uint8_t* ops = op_tile(b, 0, 0);
+      uint4 term[kMkPer][2][3];
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) {
+      for (int c = 0; c < kMkPer; ++c) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kMkAhead - 1) : "memory");
+        const uint8_t* src = inputs + place(c, i);
+        const uint4 vd = *reinterpret_cast<const uint4*>(src);
+        const uint4 vg = *reinterpret_cast<const uint4*>(src + kMkInBytes);
+        const uint4 vu = *reinterpret_cast<const uint4*>(src + 2 * kMkInBytes);
+        const uint32_t wd[4] = {vd.x, vd.y, vd.z, vd.w}, wg[4] = {vg.x, vg.y, vg.z, vg.w}, wu[4] = {vu.x, vu.y, vu.z, vu.w};
         gated::F2 dg[4], du[4];
-        const uint32_t wd[4] = {in[c][0].x, in[c][0].y, in[c][0].z, in[c][0].w};
-        const uint32_t wg[4] = {in[c][1].x, in[c][1].y, in[c][1].z, in[c][1].w};
-        const uint32_t wu[4] = {in[c][2].x, in[c][2].y, in[c][2].z, in[c][2].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const gated::F2 dh = wide2<F16>(wd[e]);
@@ -519,29 +523,30 @@ __global__ void __launch_bounds__(kMkThreads, 1)
           dg[e] = gated::mul2(gated::mul2(dh, wide2<F16>(wu[e])), d);
           du[e] = gated::mul2(dh, a);
         }
-        fetch(c, i + 1);
-        const uint32_t off = uint32_t(half_of(c)) * kBoxBytes + sw128_offset(uint32_t(row_of(c)), uint32_t(tc));
-        uint4 first[2];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          uint4 d[3];
-          split8<F16>(z == 0 ? dg : du, d);
-          first[z] = d[0];
-#pragma unroll
-          for (int term = 0; term < kTerms; ++term)
-            *reinterpret_cast<uint4*>(ops + uint32_t(3 * z + term) * kTileBytes + off) = d[term];
-        }
-        
+        split8<F16>(dg, term[c][0]);
+        split8<F16>(du, term[c][1]);
+        copy(c, i + 2);          // into the place just read
         if (KIND == kGatedU && blockIdx.z == 0 && 64 * i < left[c]) {
           const int64_t e = at[c] + ahead * i;
-          *reinterpret_cast<uint4*>(p.d + e) = first[0];
-          *reinterpret_cast<uint4*>(p.d + mn + e) = first[1];
+          *reinterpret_cast<uint4*>(p.d + e) = term[c][0][0];
+          *reinterpret_cast<uint4*>(p.d + mn + e) = term[c][1][0];
         }
+      }
+      if (ok) ok = warp_wait(&sh->opempty, uint32_t(i & 1) ^ 1u, abort_flag, p.status);
+      if (!ok) break;
+#pragma unroll
+      for (int c = 0; c < kMkPer; ++c) {
+        const uint32_t off = uint32_t(c >> 1) * kBoxBytes + sw128_offset(uint32_t(32 * (c & 1) + tr), uint32_t(tc));
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int e = 0; e < kTerms; ++e) *reinterpret_cast<uint4*>(op_tile(z, e) + off) = term[c][z][e];
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->opfull[b]);
+      if (lane == 0) mbar_arrive(&sh->opfull);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     // ---------------- the tile's sums: lanes by warp % 4, columns by warp / 4
     if (ok) ok = warp_wait(&sh->accum, 0, abort_flag, p.status);
     tc_fence_after();
@@ -562,15 +567,15 @@ __global__ void __launch_bounds__(kMkThreads, 1)
     for (int i = 0; i < w.steps; ++i) {
       const int b = i & 1;
       const uint32_t ph = (i >> 1) & 1;
-      ok = ring_wait(&sh->opfull[b], ph, abort_flag, p.status) && ring_wait(&sh->bfull[b], ph, abort_flag, p.status);
+      ok = ring_wait(&sh->bfull[b], ph, abort_flag, p.status) && ring_wait(&sh->opfull, uint32_t(i & 1), abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
       if (issue) {
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const uint64_t bdesc = smem_desc_sw128(smem_u32(b_box(b, z)), 8192, 1024);
-          const uint64_t adesc = kAMn ? smem_desc_sw128(smem_u32(op_tile(b, z, 0)), 8192, 1024)
-                                      : smem_desc_sw128(smem_u32(op_tile(b, z, 0)), 16, 1024);
+          const uint64_t adesc = kAMn ? smem_desc_sw128(smem_u32(op_tile(z, 0)), 8192, 1024)
+                                      : smem_desc_sw128(smem_u32(op_tile(z, 0)), 16, 1024);
           constexpr uint32_t kASub = kAMn ? 128 : 2;
           const uint32_t dz = uint32_t(z * kCols);
 #pragma unroll
@@ -582,13 +587,14 @@ __global__ void __launch_bounds__(kMkThreads, 1)
                        idesc, (i > 0 || kk > 0 || term > 1) ? 1u : 0u);
           }
         }
-        // the last step's commit goes to accum (nobody waits on its buffer)
-        umma_commit(i + 1 < w.steps ? &sh->empty[b] : &sh->accum);
+        // the last step's commit goes to accum (nobody waits on its tiles)
+        umma_commit(i + 1 < w.steps ? &sh->opempty : &sh->accum);
+        umma_commit(&sh->bempty[b]);
       }
       __syncwarp();
       ++issued;
     }
-    if (issue && !ok) drain_issued(sh->empty, issued, kMkBufs);
+    if (issue && !ok) drain_issued(sh->bempty, issued, kMkBufs);
     else if (issue && w.steps == 0) mbar_arrive(&sh->accum);
   } else {
     // ---------------- B rows (U) or T rows (dB) of a step, both projections
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(kMkThreads, 1)
     int issued = 0;
     for (int i = 0; i < w.steps; ++i) {
       const int b = i & 1;
-      if (!ring_wait(&sh->empty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.status)) break;
+      if (!ring_wait(&sh->bempty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.status)) break;
       if (issue) {
         mbar_arrive_expect_tx(&sh->bfull[b], kMkBBytes);
         for (int z = 0; z < 2; ++z) tma_load_3d(b_box(b, z), &tm_b, &sh->bfull[b], col0, (w.step0 + i) * 64, z);
