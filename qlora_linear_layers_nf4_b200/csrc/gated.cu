@@ -18,12 +18,12 @@ bool use_decode(int64_t M) { return M <= 32; }
 
 }  // namespace
 
-// fwd [T] [the decode kernel's partials and counters]; bwd [T] [terms of U] [dg, du]
+// fwd [T] [the decode kernel's partials and counters]; bwd [T] [terms of U] [dg, du] [dx in splits]
 size_t gated_workspace_bytes(bool backward, bool f32, int64_t M, int64_t N, int64_t K, int r) {
   if (M < 0 || N < 0 || K < 0 || r < 0) return 0;
   if (f32) return gated_f32_workspace_bytes(backward, M, N, r);
   const size_t t = mr_bytes(2 * M, r, 2);
-  return backward ? t + mr_bytes(6 * M, r, 2) + pair_bytes(M, N, 2) : t + gated_decode_scratch_bytes();
+  return backward ? t + mr_bytes(6 * M, r, 2) + pair_bytes(M, N, 2) + gated_split_bytes(M, K) : t + gated_decode_scratch_bytes();
 }
 
 cudaError_t launch_gated_fwd(const GatedArgs& a, int sms, cudaStream_t st, int* launches) {
@@ -37,7 +37,7 @@ cudaError_t launch_gated_fwd(const GatedArgs& a, int sms, cudaStream_t st, int* 
   }
   GatedRank t;
   GatedGemm h;
-  if (!t.prepare(a, kGatedT, nullptr, nullptr, T, sms) || !h.prepare(a, false, a.x, T, sms)) return cudaErrorInvalidValue;
+  if (!t.prepare(a, kGatedT, nullptr, nullptr, T, sms) || !h.prepare(a, false, a.x, T, nullptr, sms)) return cudaErrorInvalidValue;
   const cudaError_t e = t.run(st, launches);
   return e == cudaSuccess ? h.run(st, launches) : e;
 }
@@ -47,6 +47,7 @@ cudaError_t launch_gated_bwd(const GatedArgs& a, int sms, cudaStream_t st, int* 
   uint8_t* ws = a.ws + kWsHeader;
   uint8_t* U = ws + mr_bytes(2 * a.M, a.r, 2);
   uint8_t* d = U + mr_bytes(6 * a.M, a.r, 2);
+  uint8_t* splits = d + pair_bytes(a.M, a.N, 2);
   const void* T = a.t_in != nullptr ? a.t_in : ws;
   GatedRank t, u, db, da;
   GatedGemm dx;
@@ -56,7 +57,7 @@ cudaError_t launch_gated_bwd(const GatedArgs& a, int sms, cudaStream_t st, int* 
   ok = ok && u.prepare(a, kGatedU, nullptr, d, U, sms);
   ok = ok && db.prepare(a, kGatedDB, T, nullptr, a.dB, sms);
   ok = ok && da.prepare(a, kGatedDA, U, nullptr, a.dA, sms);
-  ok = ok && (a.dx == nullptr || dx.prepare(a, true, d, U, sms));
+  ok = ok && (a.dx == nullptr || dx.prepare(a, true, d, U, splits, sms));
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   if (a.t_in == nullptr) e = small_t ? launch_gated_t_small(a, ws, nullptr, st, launches) : t.run(st, launches);
@@ -65,6 +66,7 @@ cudaError_t launch_gated_bwd(const GatedArgs& a, int sms, cudaStream_t st, int* 
   // dx lets dB start when U is complete, dB lets dA
   if (e == cudaSuccess) e = db.run(st, launches, /*beside=*/a.dx != nullptr);
   if (e == cudaSuccess) e = da.run(st, launches, /*beside=*/true);
+  if (e == cudaSuccess && a.dx != nullptr) e = dx.sum(st, launches);
   return e;
 }
 

@@ -88,16 +88,28 @@ static_assert(gemm_smem(kDx, 1) <= 232448 && gemm_smem(kDx, 2) <= 232448 && gemm
               "shared memory of one CTA");
 
 struct Tile {
+  int k0, k1;   // its steps: all of them, or a split's
+  int split;
   int t0, cnt;  // first token, tokens
   int nt[2];    // MMA columns of the parts (multiples of 16, of a first of two of 32; 0: no second part)
   int n0;       // first output
 };
 
-// Tile `id`, ordered by output tile, then token tile: the pairs that run together share
-// weight tiles and tokens.
+// Tile `id`, ordered by output tile, then token tile (then split): the pairs that run together
+// share weight tiles and tokens.
 template <int MODE, int PARTS>
 __device__ __forceinline__ Tile tile_at(const GatedParams& p, int id) {
   Tile t;
+  const int steps = p.main_steps + 2 * p.ad_steps;
+  t.split = 0;
+  t.k0 = 0;
+  t.k1 = steps;
+  if (MODE == kDx && p.splits > 1) {
+    t.split = id % p.splits;
+    id /= p.splits;
+    t.k0 = steps * t.split / p.splits;
+    t.k1 = steps * (t.split + 1) / p.splits;
+  }
   const int ct = id / p.row_tiles, rt = id - ct * p.row_tiles;
   t.t0 = rt * p.tile_rows;
   t.cnt = min(p.tile_rows, p.M - t.t0);
@@ -193,8 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
-  const int tiles = p.row_tiles * p.col_tiles;
-  const int steps = p.main_steps + 2 * p.ad_steps;
+  const int tiles = p.row_tiles * p.col_tiles * (MODE == kDx ? p.splits : 1);
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   auto leader_bar = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
   // projection and first index within it of a main step, and of an adapter step
@@ -236,7 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
       const int y2 = t.t0 + t.nt[0] + int(rank) * (t.nt[1] >> 1);
       const CUtensorMap* tok = large ? &maps.tok_l : &maps.tok_s;
       const CUtensorMap* ad = large ? &maps.ad_l : &maps.ad_s;
-      for (int k = 0; k < steps; ++k) {
+      for (int k = t.k0; k < t.k1; ++k) {
         ok = ring_wait(&sh->empty[s], ph, abort_flag, p.status);
         if (!ok) break;
         const bool main = k < p.main_steps;
@@ -282,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
       for (int id = pair; id < tiles && ok; id += pairs) {
         const Tile t = tile_at<MODE, PARTS>(p, id);
         const int n0 = t.n0 + 128 * int(rank);
-        for (int k = 0; k < steps; ++k) {
+        for (int k = t.k0; k < t.k1; ++k) {
           if (k < p.main_steps) {
             ok = ring_wait(&sh->cempty[s], (ph >> s) & 1u, abort_flag, p.status);
             if (!ok) break;
@@ -320,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
       for (int id = pair; id < tiles && ok; id += pairs) {
         const Tile t = tile_at<MODE, PARTS>(p, id);
         const int parts = PARTS == 2 && t.nt[1] > 0 ? 2 : 1;
-        for (int k = 0; k < steps && ok; ++k) {
+        for (int k = t.k0; k < t.k1 && ok; ++k) {
           ok = mbar_wait_cluster(&sh->full[s], ph, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
@@ -330,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
           for (int h = 0; h < PARTS; ++h) {
             if (h >= parts) break;
             const int b = (n + h) & 1;
-            if (k == 0) {
+            if (k == t.k0) {
               ok = mbar_wait_cluster(&sh->acc_empty[b], (((n + h) >> 1) & 1) ^ 1, abort_flag, p.status);
               if (!ok) break;
               tc_fence_after();
@@ -341,11 +352,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
             if (issue) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                if (kk * 16 < left) umma_f16_pair(d, wd + kk * kWSub, td + kk * kTSub, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+                if (kk * 16 < left) umma_f16_pair(d, wd + kk * kWSub, td + kk * kTSub, idesc, (k > t.k0 || kk > 0) ? 1u : 0u);
               // The last step's commits go to the accumulators' barriers; the
               // epilogue then releases that step's stage.  MMAs finish in order,
               // so a commit covers the whole accumulation.
-              if (k + 1 == steps) umma_commit_pair_mc(&sh->acc_full[b], 0x3);
+              if (k + 1 == t.k1) umma_commit_pair_mc(&sh->acc_full[b], 0x3);
               else if (h + 1 == parts) umma_commit_pair_mc(&sh->empty[s], 0x3);
             }
           }
@@ -385,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
         bias = F16 ? __half2float(static_cast<const __half*>(p.bias)[at])
                    : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[at]);
       }
-      last = (last + steps) % kStages;
+      last = (last + t.k1 - t.k0) % kStages;
       const int parts = PARTS == 2 && t.nt[1] > 0 ? 2 : 1;
 #pragma unroll 1
       for (int h = 0; h < PARTS; ++h, ++n) {
@@ -446,6 +457,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
               bulk_commit_group();
             }
           } else {
+            if (p.splits > 1) {   // fp32 sums of the split, added up by the kernel after
+              float* o = p.partials + (int64_t(t.split) * p.M + row0) * p.out_cols + col;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (col_ok && i < left) __stcg(o + int64_t(i) * p.out_cols, __uint_as_float(v[i]));
+              continue;
+            }
             // two lanes trade so that each stores two neighbouring outputs of one token
             uint16_t* o = static_cast<uint16_t*>(p.out) + (row0 + odd) * p.out_cols + (col & ~1);
 #pragma unroll
@@ -509,11 +527,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
       auto load_codes = [&](int k) -> Codes {
         return load_codes64(p.codes[rp] + uint64_t(chunk_at(k)) * 32u, p.codes32[rp] != 0);
       };
-      const int first = (group + kDeqGroups - base % kDeqGroups) % kDeqGroups;
+      const int first = t.k0 + (group + kDeqGroups - base % kDeqGroups) % kDeqGroups;
       uint32_t raw0 = raw_scale(first), raw1 = raw_scale(first + kDeqGroups);
       Codes next;
       if (MODE == kFwd) next = load_codes(first);
-      for (int k = first; k < steps; k += kDeqGroups) {
+      for (int k = first; k < t.k1; k += kDeqGroups) {
         const uint32_t raw = raw0;
         raw0 = raw1;
         raw1 = raw_scale(k + 2 * kDeqGroups);
@@ -567,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
         own_slot += kDeqGroups;
         if (own_slot >= kCodeSlots) own_slot -= kCodeSlots;
       }
-      base += steps;
+      base += t.k1 - t.k0;
     }
   }
 
@@ -577,6 +595,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// dx from the splits' sums, in their order: four outputs a thread.
+constexpr int kSumThreads = 256;
+template <bool F16>
+__global__ void __launch_bounds__(kSumThreads) gated_sum_kernel(const float* __restrict__ parts, int splits, int64_t n, uint16_t* __restrict__ out) {
+  for (int64_t i = (int64_t(blockIdx.x) * kSumThreads + threadIdx.x) * 4; i < n; i += int64_t(gridDim.x) * kSumThreads * 4) {
+    float4 v = __ldcg(reinterpret_cast<const float4*>(parts + i));
+    for (int s = 1; s < splits; ++s) {
+      const float4 w = __ldcg(reinterpret_cast<const float4*>(parts + int64_t(s) * n + i));
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    *reinterpret_cast<uint2*>(out + i) = make_uint2(pack2(F16, v.x, v.y), pack2(F16, v.z, v.w));
   }
 }
 
@@ -639,9 +674,24 @@ bool ad_map(CUtensorMap* map, const void* ad, uint64_t r, uint64_t M, uint64_t t
   return encode_map(map, ad, MapElem::k16, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+
+// Splits of dx's reduction where its tiles leave at least half of the CTA pairs idle: a step
+// costs the decoding of its weights whatever the tokens, so few tiles with many steps are
+// slow (100 tokens, 4000 x 2048: 8 tiles of 127 steps, 65 us).  Eight steps a split at least.
+int dx_splits(int64_t tiles, int steps, int sms) {
+  const int64_t pairs = std::min(std::max(sms / 2, 1), kGatedMaxPairs);
+  return int(std::max<int64_t>(1, std::min<int64_t>(pairs / tiles, steps / 8)));
+}
+
 }  // namespace
 
-bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, const void* ad, int sms) {
+// Splits' sums: as many tiles of 256 x 256 as there are pairs at most, fp32.
+size_t gated_split_bytes(int64_t M, int64_t K) {
+  const int64_t tiles = cdiv(M, 256) * cdiv(K, 256);
+  return tiles * 2 <= kGatedMaxPairs ? size_t(kGatedMaxPairs / tiles) * size_t(M) * size_t(K) * sizeof(float) : 0;
+}
+
+bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, const void* ad, void* scratch, int sms) {
   dx = backward;
   f16 = a.f16 != 0;
   const uint64_t M = uint64_t(a.M), N = uint64_t(a.N), K = uint64_t(a.K), r = uint64_t(a.r);
@@ -692,10 +742,25 @@ bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, cons
   p.out = backward ? a.dx : a.h;
   p.pre = backward ? nullptr : a.pre_out;
   p.status = a.status;
-  const int64_t tiles = int64_t(p.row_tiles) * p.col_tiles;
+  p.splits = backward ? dx_splits(int64_t(p.row_tiles) * p.col_tiles, p.main_steps + 2 * p.ad_steps, sms) : 1;
+  p.partials = static_cast<float*>(scratch);
+  const int64_t tiles = int64_t(p.row_tiles) * p.col_tiles * p.splits;
   grid = 2u * unsigned(std::min<int64_t>(tiles, std::max(sms / 2, 1)));
   // chunks are counted in 32 bits: weights of up to 2.7e11 elements
   return ok && N * (K / 64) <= 0xffffffffull && tiles <= int64_t(0x7fffffff);
+}
+
+cudaError_t GatedGemm::sum(cudaStream_t st, int* launches) const {
+  if (p.splits == 1) return cudaSuccess;
+  const int64_t n = int64_t(p.M) * p.out_cols;   // a multiple of 64
+  const unsigned ctas = unsigned(std::min<int64_t>((n / 4 + kSumThreads - 1) / kSumThreads, 4096));
+  NF4_PROF_BEGIN(st, kKGatedDx);
+  if (f16) gated_sum_kernel<true><<<ctas, kSumThreads, 0, st>>>(p.partials, p.splits, n, static_cast<uint16_t*>(p.out));
+  else gated_sum_kernel<false><<<ctas, kSumThreads, 0, st>>>(p.partials, p.splits, n, static_cast<uint16_t*>(p.out));
+  NF4_PROF_END(st, kKGatedDx);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 cudaError_t GatedGemm::run(cudaStream_t st, int* launches) const {
