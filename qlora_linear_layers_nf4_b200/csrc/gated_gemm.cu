@@ -685,10 +685,15 @@ int dx_splits(int64_t tiles, int steps, int sms) {
 
 }  // namespace
 
-// Splits' sums: as many tiles of 256 x 256 as there are pairs at most, fp32.
+// Splits' sums, fp32: as many of M x K as there are splits.  More rows make more tiles and so
+// fewer splits: the size is the largest of any number of rows up to M, so that a workspace for
+// M serves fewer.
 size_t gated_split_bytes(int64_t M, int64_t K) {
-  const int64_t tiles = cdiv(M, 256) * cdiv(K, 256);
-  return tiles * 2 <= kGatedMaxPairs ? size_t(kGatedMaxPairs / tiles) * size_t(M) * size_t(K) * sizeof(float) : 0;
+  const int64_t k_tiles = cdiv(K, 256);
+  int64_t rows = 0;
+  for (int64_t m_tiles = 1; (m_tiles - 1) * 256 < M && 2 * m_tiles * k_tiles <= kGatedMaxPairs; ++m_tiles)
+    rows = std::max(rows, kGatedMaxPairs / (m_tiles * k_tiles) * std::min(M, m_tiles * 256));
+  return size_t(rows) * size_t(K) * sizeof(float);
 }
 
 bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, const void* ad, void* scratch, int sms) {

@@ -197,3 +197,60 @@ def test_rows_behind_the_batch_stay(cuda_device):
             Q.fp8_linear_fwd(L.w, L.x, out=big[:m])
             L.check(big[:m])
             assert (big[m:] == 7).all()
+
+
+@pytest.mark.parametrize("m", [1, 6, 40, 300])
+def test_captured_and_on_another_stream(cuda_device, m):
+    import torch
+    Q = _Q()
+    L = Lin(cuda_device, m, 520, 400, bias=True)
+    want = Q.fp8_linear_fwd(L.w, L.x, bias=L.bias)
+    q = Q.fp8_quantize(L.x)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    y = Q.fp8_linear_fwd(L.w, L.x, bias=L.bias, stream=side)
+    side.synchronize()
+    assert y.equal(want)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = Q.fp8_linear_fwd(L.w, L.x, bias=L.bias)
+            codes = Q.fp8_quantize(L.x)
+            back = Q.fp8_dequantize(codes, torch.bfloat16)
+        graphs.append((g, out, codes, back))
+    for _ in range(3):
+        for g, out, codes, back in graphs:
+            g.replay()
+        between = Q.fp8_linear_fwd(L.w, L.x, bias=L.bias)
+        torch.cuda.synchronize()
+        assert between.equal(want)
+        for g, out, codes, back in graphs:
+            assert out.equal(want) and codes.codes.view(torch.uint8).equal(q.codes.view(torch.uint8)) and codes.scale.equal(q.scale)
+            assert back.equal(Q.fp8_dequantize(q, torch.bfloat16))
+    assert Q.read_status() == 0 and Q.read_status(side) == 0
+
+
+def test_a_merged_weight(cuda_device):
+    """What serves a trained adapter: merge, quantize, linear.  Against the merged weight itself a product is off by at
+    most half a step of each operand, 2^-4 of it (or 2^-10 scales where e4m3 is subnormal)."""
+    import torch
+    Q = _Q()
+    gen = torch.Generator().manual_seed(5)
+    n, k, r = 264, 320, 16
+    q = Q.quantize((torch.randn(n, k, generator=gen) * 0.02).to(cuda_device), 64, True)
+    A, B = ((torch.randn(*s, generator=gen) * 0.05).to(torch.bfloat16).to(cuda_device) for s in ((r, k), (n, r)))
+    dense = Q.merge(q, A, B, 32.0, "f32")
+    w = Q.fp8_quantize(dense, 128)
+    back = Q.fp8_dequantize(w).double()
+    step = torch.maximum(dense.double().abs() * 2.0 ** -4, spread(w.scale.double(), 128, n, k) * 2.0 ** -10)
+    assert ((back - dense.double()).abs() <= step * (1 + 2.0 ** -20)).all()
+    for m in (1, 100):
+        x = torch.randn(m, k, generator=gen).to(torch.bfloat16).to(cuda_device)
+        y = Q.fp8_linear_fwd(w, x).double()
+        xa, wa = x.double().abs(), dense.double().abs()
+        sx = spread(Q.fp8_quantize(x).scale.double(), 1, m, k)
+        ex = torch.maximum(xa * 2.0 ** -4, sx * 2.0 ** -10)
+        bound = ex @ (wa + step).T + xa @ step.T
+        want = x.double() @ dense.double().T
+        assert ((y - want).abs() <= bound * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()).all()

@@ -67,3 +67,54 @@ def test_workspace_sizes():
         dt = 0 if op in (Q.OP_GATED_FWD_F32, Q.OP_GATED_BWD_F32) else 2
         cw = dict(gate=_cw(264, 192), up=_cw(264, 192), m=100)
         assert call(dt=dt, wsb=need - 1, **cw) == 5
+
+
+# ---- the binding's own checks, on tensors of the CPU: each is made before the library is called
+
+
+def _layer(n=64, k=128, r=8, m=3, dtype=None):
+    import torch
+    dt = dtype or torch.bfloat16
+    q = lambda: Q.QuantizedWeight(torch.zeros(n * k // 2, dtype=torch.uint8), torch.zeros(n * k // 64), None, None, n, k, 64, False)
+    return dict(gate=q(), up=q(), x=torch.zeros(m, k, dtype=dt), A=torch.zeros(2, r, k, dtype=dt), B=torch.zeros(2, n, r, dtype=dt),
+                alpha=16.0)
+
+
+def test_binding_refusals():
+    import torch
+    from dataclasses import replace
+    L = _layer()
+    bf = torch.bfloat16
+    saved = Q.GatedSaved(torch.zeros(2, 3, 64, dtype=bf), torch.zeros(2, 3, 8, dtype=bf))
+    dh = torch.zeros(3, 64, dtype=bf)
+    bad = [(dict(x=torch.zeros(128, dtype=bf)), ValueError), (dict(A=torch.zeros(8, 128, dtype=bf)), ValueError),
+           (dict(A=torch.zeros(1, 8, 128, dtype=bf)), ValueError), (dict(B=torch.zeros(2, 64, 16, dtype=bf)), ValueError),
+           (dict(B=torch.zeros(2, 64, 8)), TypeError), (dict(x=torch.zeros(3, 128, dtype=torch.int32)), TypeError),
+           (dict(x=torch.zeros(3, 256, dtype=bf)[:, ::2]), ValueError),
+           (dict(activation="relu"), ValueError), (dict(up=replace(L["up"], block_size=128)), ValueError),
+           (dict(up=replace(L["up"], cols=64)), ValueError), (dict(up=replace(L["up"], double_quant=True)), ValueError)]
+    for change, error in bad:
+        with pytest.raises(error):
+            Q.gated_fwd(**{**L, **change})
+        with pytest.raises(error):
+            Q.gated_bwd(**{**L, **change}, dh=dh, saved=saved)
+    for name, t in (("bias", torch.zeros(64, dtype=bf)), ("out", torch.zeros(3, 65, dtype=bf)),
+                    ("saved", Q.GatedSaved(torch.zeros(2, 3, 64), None)), ("saved", Q.GatedSaved(saved.pre, torch.zeros(2, 3, 9, dtype=bf)))):
+        with pytest.raises((ValueError, TypeError)):
+            Q.gated_fwd(**L, **{name: t})
+    for change in (dict(dh=dh[:2]), dict(saved=Q.GatedSaved(None, saved.t)), dict(saved=Q.GatedSaved(saved.pre[:, :2], saved.t)),
+                   dict(dA=torch.zeros(2, 8, 128, dtype=bf)), dict(dB=torch.zeros(2, 8, 64)), dict(dx=torch.zeros(3, 128))):
+        with pytest.raises((ValueError, TypeError)):
+            Q.gated_bwd(**L, **{**dict(dh=dh, saved=saved), **change})
+    with pytest.raises(ValueError, match="not the current CUDA device"):
+        Q.gated_fwd(**L)
+    with pytest.raises(ValueError, match="not the current CUDA device"):
+        Q.gated_bwd(**L, dh=dh, saved=saved)
+
+
+@pytest.mark.parametrize("op", [Q.OP_GATED_FWD, Q.OP_GATED_BWD, Q.OP_GATED_FWD_F32, Q.OP_GATED_BWD_F32])
+@pytest.mark.parametrize("n,k,r", [(8, 64, 8), (2000, 512, 64), (5000, 4096, 128), (64, 20480, 16)])
+def test_a_workspace_serves_smaller_batches(op, n, k, r):
+    rows = [0, 1, 2, 31, 32, 33, 64, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1000, 1024, 1025, 2560, 2561, 5000, 10240, 10241, 20000]
+    sizes = [Q.workspace_bytes(op, m, n, k, r, 64, True) for m in rows]
+    assert sizes == sorted(sizes)

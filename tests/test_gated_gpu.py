@@ -50,10 +50,16 @@ def logistic_parts(g, act):
     return y, torch.sigmoid(y), slope
 
 
-def within(name, got, want, bound):
+def within(name, got, want, bound, top=math.inf):
+    """top: the least size that the type rounds to infinity.  What is that large by more than the bound has to be
+    infinite, with its sign; what is so by less may be."""
     import torch
     got = got.double()
     assert got.shape == want.shape, name
+    if math.isfinite(top):
+        over, inf = want.abs() - top, got.isinf() & (got.sign() == want.sign())
+        assert inf[over > bound].all(), f"{name} should be infinite"
+        got = torch.where(inf & (over >= -bound), want, got)
     assert torch.isfinite(got).all(), f"{name} is not finite"
     off = (got - want).abs() - bound
     worst = off.argmax().item() if off.numel() else 0
@@ -110,7 +116,8 @@ class Layer:
         a = g * q
         eq = (8 + 4 * y.abs().clamp(max=90)) * F
         bound = 1.13 * err[0] * (u.abs() + err[1]) + a.abs() * err[1] + (eq + 3 * F) * a.abs() * u.abs() + 2.0 ** -125 * (g * u).abs()
-        within("h", h[rows], a * u, e * (a * u).abs() + (1 + e) * bound + (2.0 ** -25 if self.dtype == "f16" else 0.0))
+        f16 = self.dtype == "f16"   # which rounds to infinity from 65520 on, half a step above its largest, 65504
+        within("h", h[rows], a * u, e * (a * u).abs() + (1 + e) * bound + (2.0 ** -25 if f16 else 0.0), 65520.0 if f16 else math.inf)
 
     def check_bwd(self, dA, dB, dx, saved, rows=slice(None)):
         e = HALF[self.dtype]
