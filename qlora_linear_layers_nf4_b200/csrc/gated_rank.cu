@@ -18,9 +18,13 @@
 //
 // Gradients are fp32, and one rounding of d or U to 16 bits would be their largest error by
 // far (2^-9 against 2^-24).  So d and U enter as three bf16 terms that together hold 24
-// bits, or two f16 terms, the second scaled by 2^11 (22 bits; see expert_grad.cu).  The tensor core
-// truncates when it adds to an accumulator: the first terms of even and odd steps have an
-// accumulator each and the small terms a third, summed in fp32 at the end.
+// bits, or two f16 terms, the second scaled by 2^11 (22 bits; see expert_grad.cu).  The tensor
+// core truncates when it adds to an accumulator, each time by 2^-26 of it on average and
+// always towards zero, so that the loss grows with the number of instructions.  So the first
+// terms go by turns into two accumulators, and no more than 16 instructions into one before
+// it is added to a total in fp32 (rounded) and begun anew, while the other takes the next
+// ones; the small terms have a third.  At 4096 tokens, 11008 x 4096 that took dA's error from
+// 2.0e-6 to 5.1e-7 and dB's from 8.2e-7 to 3.1e-7 relative to 64 bits.
 #include <algorithm>
 #include <atomic>
 
@@ -51,6 +55,7 @@ constexpr int kCols = 64;                          // adapter columns of a tile,
 constexpr uint32_t kTileBytes = 128 * 128;         // 128 x 64 or 64 x 128 16-bit values
 constexpr uint32_t kBoxBytes = 64 * 128;           // 64 x 64
 constexpr int kMaxSlices = 8;
+constexpr int kWindow = 4;                         // steps (of four instructions) into an accumulator
 constexpr uint32_t kParkBytes = 128 * 2 * kCols * 4;   // a CTA's partial
 
 // The term that comes after `first` in a split of v: what rounding left.  Nothing is left
@@ -94,9 +99,18 @@ __device__ __forceinline__ void store4(const GatedRankParams& p, int row, int co
   }
 }
 
-// A CTA's sums of 32 columns at `c`, lane = row: the accumulators joined.  acc: TMEM address
-// of the first; `steps` of this CTA; a third accumulator with the small terms if `small`.
-__device__ __forceinline__ void join_accs(uint32_t at, uint32_t stride, int steps, bool small, float lo_scale,
+__device__ __forceinline__ void add32(uint32_t at, float (&f)[32]) {
+  uint32_t v[32];
+  tmem_ld_32x32b_x32(at, v);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] += __uint_as_float(v[i]);
+}
+
+// A CTA's sums of 32 columns, lane = row: the accumulators joined.  at: TMEM address of the
+// first, the others `stride` further each: of even steps, odd steps and, with `make`, of the
+// small terms and the total of the windows before.  `steps` of this CTA.
+__device__ __forceinline__ void join_accs(uint32_t at, uint32_t stride, int steps, bool make, float lo_scale,
                                           float (&f)[32]) {
   uint32_t v[32];
   if (steps == 0) {
@@ -108,13 +122,9 @@ __device__ __forceinline__ void join_accs(uint32_t at, uint32_t stride, int step
   tmem_ld_wait();
 #pragma unroll
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-  if (steps > 1) {
-    tmem_ld_32x32b_x32(at + stride, v);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] += __uint_as_float(v[i]);
-  }
-  if (small) {
+  if (steps > 1) add32(at + stride, f);
+  if (make) {
+    if (steps > 2 * kWindow) add32(at + 3 * stride, f);
     tmem_ld_32x32b_x32(at + 2 * stride, v);
     tmem_ld_wait();
 #pragma unroll
@@ -191,6 +201,8 @@ struct TmaShared {
   uint64_t full[4];
   uint64_t empty[4];
   uint64_t accum;
+  uint64_t accfull[2];        // dA: a window's MMAs finished
+  uint64_t accempty[2];       // and its sums were read
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
@@ -217,7 +229,7 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
   const int col0 = blockIdx.z * kCols;
   const Share w = share_of(p);
   constexpr uint32_t kAccCols = KIND == kGatedT ? 256 : 512;
-  // T: even and odd steps; dA: those and the small terms, each of 2 kCols columns
+  // T: even and odd steps; dA: even and odd windows and the small terms, each of 2 kCols columns
   constexpr uint32_t kAccStride = 2 * kCols;
 
   // A kernel launched as this one's programmatic dependent may start on the SMs this grid
@@ -231,6 +243,10 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
       mbar_init(&sh->empty[s], 1);
     }
     mbar_init(&sh->accum, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh->accfull[b], 1);
+      mbar_init(&sh->accempty[b], 4);
+    }
     sh->abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -289,12 +305,15 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
     int s = 0, issued = 0;
     uint32_t ph = 0;
     for (int i = 0; i < w.steps; ++i) {
+      const int window = i / kWindow, begun = i % kWindow;
       ok = ring_wait(&sh->full[s], ph, abort_flag, p.status);
+      if (KIND == kGatedDA && ok && begun == 0)
+        ok = ring_wait(&sh->accempty[window & 1], uint32_t((window >> 1) & 1) ^ 1u, abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
       const uint32_t a_base = smem_u32(smem + s * stage_bytes);
       if (issue) {
-        const uint32_t d = tmem + uint32_t(i & 1) * kAccStride;
+        const uint32_t d = tmem + uint32_t((KIND == kGatedT ? i : window) & 1) * kAccStride;
         if (KIND == kGatedT) {   // both projections' rows of A lie one after another: N = 128
           const uint32_t idesc = idesc_f32acc(128, 2 * kCols, false, false, p.f16 != 0);
           const uint64_t adesc = smem_desc_sw128(a_base, 16, 1024), bdesc = smem_desc_sw128(a_base + kTileBytes, 16, 1024);
@@ -309,14 +328,16 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
             for (int z = 0; z < 2; ++z) {
               const uint64_t bz = bdesc + uint32_t(z * terms) * (kBoxBytes >> 4) + kk * 128;
               const uint32_t dz = uint32_t(z * kCols);
-              umma_f16(d + dz, adesc + kk * 128, bz, idesc, (i > 1 || kk > 0) ? 1u : 0u);
+              umma_f16(d + dz, adesc + kk * 128, bz, idesc, (begun > 0 || kk > 0) ? 1u : 0u);
               umma_f16(tmem + 2 * kAccStride + dz, adesc + kk * 128, bz + (kBoxBytes >> 4), idesc, (i > 0 || kk > 0) ? 1u : 0u);
               if (terms > 2) umma_f16(tmem + 2 * kAccStride + dz, adesc + kk * 128, bz + 2 * (kBoxBytes >> 4), idesc, 1u);
             }
           }
         }
-        // the last step's commit goes to accum (nobody waits on its stage)
-        umma_commit(i + 1 < w.steps ? &sh->empty[s] : &sh->accum);
+        // nobody waits on the last step's stage
+        if (i + 1 < w.steps) umma_commit(&sh->empty[s]);
+        else if (KIND == kGatedT) umma_commit(&sh->accum);
+        if (KIND == kGatedDA && (begun == kWindow - 1 || i + 1 == w.steps)) umma_commit(&sh->accfull[window & 1]);
       }
       __syncwarp();
       ++issued;
@@ -328,14 +349,46 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
     if (issue && !ok) drain_issued(sh->empty, issued, kStages);
     else if (issue && w.steps == 0) mbar_arrive(&sh->accum);
   } else if (warp >= 4) {
-    const bool ok = warp_wait(&sh->accum, 0, abort_flag, p.status);
-    tc_fence_after();
     const int quad = warp - 4;
-    const float lo_scale = p.f16 ? 1.0f / kULoMul : 1.0f;
-    for (int c = 0; c < 2 * kCols; c += 32) {
-      float f[32];
-      join_accs(tmem + (uint32_t(quad * 32) << 16) + c, kAccStride, ok ? w.steps : 0, KIND == kGatedDA, lo_scale, f);
-      finish32<KIND>(p, reinterpret_cast<float*>(smem), row0, quad * 32 + lane, c, col0, f);
+    const uint32_t at = tmem + (uint32_t(quad * 32) << 16);
+    float* park = reinterpret_cast<float*>(smem);
+    if (KIND == kGatedT) {
+      const bool ok = warp_wait(&sh->accum, 0, abort_flag, p.status);
+      tc_fence_after();
+      for (int c = 0; c < 2 * kCols; c += 32) {
+        float f[32];
+        join_accs(at + c, kAccStride, ok ? w.steps : 0, false, 1.0f, f);
+        finish32<KIND>(p, park, row0, quad * 32 + lane, c, col0, f);
+      }
+    } else {
+      float f[2 * kCols / 32][32];
+#pragma unroll
+      for (int c = 0; c < 2 * kCols / 32; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[c][i] = 0.0f;
+      bool ok = true;
+      for (int i = 0; i * kWindow < w.steps; ++i) {
+        ok = warp_wait(&sh->accfull[i & 1], uint32_t(i >> 1) & 1u, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2 * kCols / 32; ++c) add32(at + uint32_t(i & 1) * kAccStride + 32 * c, f[c]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->accempty[i & 1]);
+      }
+      const float lo_scale = p.f16 ? 1.0f / kULoMul : 1.0f;
+#pragma unroll
+      for (int c = 0; c < 2 * kCols / 32; ++c) {
+        if (ok && w.steps > 0) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(at + 2 * kAccStride + 32 * c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[c][i] = fmaf(__uint_as_float(v[i]), lo_scale, f[c][i]);
+        }
+        finish32<KIND>(p, park, row0, quad * 32 + lane, 32 * c, col0, f[c]);
+      }
     }
   }
 
@@ -474,6 +527,7 @@ __global__ void __launch_bounds__(kMkThreads, 1)
     // allowed half of the bytes in flight), and keeps a step's terms until the MMAs have read
     // the step before.
     const int tr = threadIdx.x >> 3, tc = threadIdx.x & 7;
+    constexpr int kWide = 2 * kCols / (kMkWarps / 4);
     const int64_t mn = int64_t(p.M) * p.N;
     const int red0 = w.step0 * 64;
     // chunk c (half c / 2, row 32 (c % 2) + t / 8) in the first step; a step later it is
@@ -504,7 +558,29 @@ __global__ void __launch_bounds__(kMkThreads, 1)
 #pragma unroll
     for (int j = 0; j < kMkAhead; ++j) copy(j % kMkPer, j / kMkPer);
     bool ok = true;
+    const uint32_t acc_at = tmem + (uint32_t((warp & 3) * 32) << 16) + (warp >> 2) * kWide;
     for (int i = 0; i < w.steps; ++i) {
+      // the accumulator that step i begins anew: its MMAs finished before the last step's
+      // terms were written, and the next wait for this step's
+      const bool drained = i >= 2 * kWindow && i % (2 * kWindow) < 2;
+      if (drained) {
+        tc_fence_after();
+        for (int c = 0; c < kWide; c += 32) {
+          uint32_t v[32];
+          float f[32];
+          const uint32_t total = acc_at + 3 * kAccStride + c;
+          tmem_ld_32x32b_x32(acc_at + uint32_t(i & 1) * kAccStride + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
+          if (i > 2 * kWindow) add32(total, f);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(f[e]);
+          tmem_st_32x32b_x32(total, v);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+      }
       uint4 term[kMkPer][2][3];
 #pragma unroll
       for (int c = 0; c < kMkPer; ++c) {
@@ -551,7 +627,6 @@ __global__ void __launch_bounds__(kMkThreads, 1)
     if (ok) ok = warp_wait(&sh->accum, 0, abort_flag, p.status);
     tc_fence_after();
     const int quad = warp & 3;
-    constexpr int kWide = 2 * kCols / (kMkWarps / 4);
     for (int c = (warp >> 2) * kWide; c < (warp >> 2) * kWide + kWide; c += 32) {
       float f[32];
       join_accs(tmem + (uint32_t(quad * 32) << 16) + c, kAccStride, ok ? w.steps : 0, true, F16 ? 1.0f / kULoMul : 1.0f, f);
@@ -580,7 +655,8 @@ __global__ void __launch_bounds__(kMkThreads, 1)
           const uint32_t dz = uint32_t(z * kCols);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            umma_f16(tmem + uint32_t(i & 1) * kAccStride + dz, adesc + kk * kASub, bdesc + kk * 128, idesc, (i > 1 || kk > 0) ? 1u : 0u);
+            umma_f16(tmem + uint32_t(i & 1) * kAccStride + dz, adesc + kk * kASub, bdesc + kk * 128, idesc,
+                     (i % (2 * kWindow) > 1 || kk > 0) ? 1u : 0u);
 #pragma unroll
             for (int term = 1; term < kTerms; ++term)
               umma_f16(tmem + 2 * kAccStride + dz, adesc + uint32_t(term) * (kTileBytes >> 4) + kk * kASub, bdesc + kk * 128,
