@@ -55,8 +55,10 @@ template <int J, bool F16>
 __device__ __forceinline__ uint32_t two_weights(const uint8_t* lut, uint32_t word, uint32_t lane8, float scale) {
   uint32_t at;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(at) : "r"(word), "r"(lane8), "n"(0x5504 | (J << 4)));   // {lane8.b0, word.bJ, 0, 0}
-  const float2 l = *reinterpret_cast<const float2*>(lut + at);
-  return two_rounded<F16>(__fmul_rn(l.x, scale), __fmul_rn(l.y, scale));
+  uint64_t l = *reinterpret_cast<const uint64_t*>(lut + at), s2;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(scale));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(l) : "l"(s2));
+  return two_rounded<F16>(__uint_as_float(uint32_t(l)), __uint_as_float(uint32_t(l >> 32)));
 }
 
 // Eight products of two 16-byte chunks of 16-bit values, added to acc in order.

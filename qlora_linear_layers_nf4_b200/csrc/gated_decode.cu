@@ -419,26 +419,34 @@ __global__ void __launch_bounds__(kDcThreads, 1)
       for (int i = 0; i < 4; ++i) acc[0][c][i] += acc[1][c][i];
 
     // The adapters' products enter the tile's first part, as MMAs with the rows of B as A
-    // (of one projection, the other's zero) and T as B; the groups take 16 columns in turn.
+    // (of one projection, the other's zero) and T as B; the groups take 32 columns in turn,
+    // a lane eight consecutive ones of its rows in a load (two at a time were 45.7 us against
+    // 34.7 with 16 tokens and r = 64).
     if (first_part) {
       if (!waited) grid_dep_wait();   // T of the kernel before
       waited = true;
       const int n = min(t.nt * kDcOutputs + set * 8 + g, p.N - 1);
-      for (int j0 = 16 * group; j0 < p.r; j0 += 16 * kGroups) {
-        const int ja = j0 + 2 * q, jb = ja + 8;   // r is a multiple of 8: the second half may be missing
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      for (int j = 32 * group + 8 * q; j - 8 * q < p.r; j += 32 * kGroups) {   // r is a multiple of 8
+        const bool there = j < p.r;
+        uint4 bv[2], tv[2][NT8];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          const uint16_t* brow = p.B + (int64_t(z) * p.N + n) * p.r;
-          uint32_t a[4] = {0u, 0u, 0u, 0u};
-          a[z] = __ldg(reinterpret_cast<const uint32_t*>(brow + ja));
-          a[2 + z] = jb < p.r ? __ldg(reinterpret_cast<const uint32_t*>(brow + jb)) : 0u;
+          bv[z] = there ? __ldg(reinterpret_cast<const uint4*>(p.B + (int64_t(z) * p.N + n) * p.r + j)) : none;
 #pragma unroll
           for (int c = 0; c < NT8; ++c) {
             const int m = t.rt * NP + 8 * c + g;
-            const uint16_t* trow = p.T + (int64_t(z) * p.M + min(m, p.M - 1)) * p.r;
-            const uint32_t b0 = m < p.M ? __ldcg(reinterpret_cast<const uint32_t*>(trow + ja)) : 0u;
-            const uint32_t b1 = m < p.M && jb < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(trow + jb)) : 0u;
-            mma_16816<F16>(acc[0][c], a, b0, b1);
+            tv[z][c] = there && m < p.M ? __ldcg(reinterpret_cast<const uint4*>(p.T + (int64_t(z) * p.M + m) * p.r + j)) : none;
+          }
+        }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          uint32_t lo[4] = {0u, 0u, 0u, 0u}, hi[4] = {0u, 0u, 0u, 0u};
+          lo[z] = bv[z].x, lo[2 + z] = bv[z].y, hi[z] = bv[z].z, hi[2 + z] = bv[z].w;
+#pragma unroll
+          for (int c = 0; c < NT8; ++c) {
+            mma_16816<F16>(acc[0][c], lo, tv[z][c].x, tv[z][c].y);
+            mma_16816<F16>(acc[0][c], hi, tv[z][c].z, tv[z][c].w);
           }
         }
       }
@@ -459,44 +467,55 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   }
 }
 
-// T_p = s x A_p^T of a few tokens: a CTA takes one adapter row and up to eight tokens, fp32
-// sums in a fixed order.  Also clears the decode kernel's counters.
-constexpr int kTsThreads = 256;
-constexpr int kTsTokens = 8;
+// T_p = s x A_p^T of a few tokens.  A CTA takes eight adapter rows and sixteen tokens; its
+// 32 warps share the columns in pieces of 32, a lane eight of them of its row of A and of two
+// tokens (an MMA's k positions are free as long as both operands agree), and their fp32 sums
+// are joined in a fixed order.  It is latency that counts: all loads of a row of 4096 are on
+// their way at once, and the few CTAs leave the other SMs to the decode kernel, which starts
+// beside them.  (A CTA of eight warps for each adapter row and eight tokens, summing products
+// of fp32, read x once per adapter row: a call of 16 tokens with r = 64 took 52.6 us against
+// 45.7, of 8 with r = 16 34.1 against 30.0.)  Also clears the decode kernel's counters.
+constexpr int kTsWarps = 32;
+constexpr int kTsRows = 8;
+constexpr int kTsTokens = 16;
 template <bool F16>
-__global__ void __launch_bounds__(kTsThreads)
+__global__ void __launch_bounds__(32 * kTsWarps, 1)
     gated_t_small_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ A, int M, int K, int r, float scale,
                          uint16_t* __restrict__ T, int* counters, int n_counters) {
-  __shared__ float part[kTsThreads / 32][kTsTokens];
+  __shared__ float part[kTsWarps][kTsTokens * kTsRows];
   grid_dep_launch();
-  const int j = blockIdx.x, m0 = blockIdx.y * kTsTokens;   // j: of both projections' rows
-  const int tokens = min(kTsTokens, M - m0);
-  if (j == 0 && m0 == 0)
-    for (int i = threadIdx.x; i < n_counters; i += kTsThreads) counters[i] = 0;
-  const uint4* a = reinterpret_cast<const uint4*>(A + int64_t(j) * K);
-  float acc[kTsTokens];
-#pragma unroll
-  for (int m = 0; m < kTsTokens; ++m) acc[m] = 0.0f;
-#pragma unroll 2
-  for (int k = threadIdx.x; k < K / 8; k += kTsThreads) {
-    const uint4 av = __ldg(a + k);
-#pragma unroll
-    for (int m = 0; m < kTsTokens; ++m)
-      if (m < tokens) acc[m] = dot8<F16>(av, __ldg(reinterpret_cast<const uint4*>(x + int64_t(m0 + m) * K) + k), acc[m]);
+  const int j0 = blockIdx.x * kTsRows, m0 = blockIdx.y * kTsTokens;   // j0: of both projections' rows
+  if (blockIdx.x == 0 && m0 == 0)
+    for (int i = threadIdx.x; i < n_counters; i += 32 * kTsWarps) counters[i] = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q = lane & 3;
+  const bool there[2] = {m0 + g < M, m0 + g + 8 < M};
+  const uint16_t* a = A + int64_t(j0 + g) * K + 8 * q;
+  const uint16_t* x0 = x + int64_t(m0 + g) * K + 8 * q;
+  const uint16_t* x1 = x0 + int64_t(8) * K;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  float acc[2][4] = {};
+#pragma unroll 4
+  for (int k = 32 * warp; k < K; k += 32 * kTsWarps) {
+    const uint4 av = __ldg(reinterpret_cast<const uint4*>(a + k));
+    const uint4 u = there[0] ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : none;
+    const uint4 v = there[1] ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : none;
+    const uint32_t lo[4] = {u.x, v.x, u.y, v.y}, hi[4] = {u.z, v.z, u.w, v.w};
+    mma_16816<F16>(acc[0], lo, av.x, av.y);
+    mma_16816<F16>(acc[1], hi, av.z, av.w);
   }
 #pragma unroll
-  for (int m = 0; m < kTsTokens; ++m) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][m] = acc[m];
-  }
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<float2*>(&part[warp][(g + 8 * i) * kTsRows + 2 * q]) =
+        make_float2(acc[0][2 * i] + acc[1][2 * i], acc[0][2 * i + 1] + acc[1][2 * i + 1]);
   __syncthreads();
-  if (threadIdx.x < tokens) {
+  const int m = m0 + int(threadIdx.x) / kTsRows, j = j0 + int(threadIdx.x) % kTsRows;
+  if (threadIdx.x < kTsTokens * kTsRows && m < M) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kTsThreads / 32; ++w) v += part[w][threadIdx.x];
+    for (int w = 0; w < kTsWarps; ++w) v += part[w][threadIdx.x];
     const int z = j >= r ? 1 : 0;
-    T[(int64_t(z) * M + m0 + int(threadIdx.x)) * r + j - z * r] = one_rounded<F16>(scale * v);
+    T[(int64_t(z) * M + m) * r + j - z * r] = one_rounded<F16>(scale * v);
   }
 }
 
@@ -589,16 +608,16 @@ cudaError_t GatedDecode::run(cudaStream_t st, int* launches) const {
 }
 
 cudaError_t launch_gated_t_small(const GatedArgs& a, void* T, int* counters, cudaStream_t st, int* launches) {
-  const dim3 grid(unsigned(2 * a.r), unsigned((a.M + kTsTokens - 1) / kTsTokens), 1);
+  const dim3 grid(unsigned(2 * a.r / kTsRows), unsigned((a.M + kTsTokens - 1) / kTsTokens), 1);
   const auto* x = static_cast<const uint16_t*>(a.x);
   const auto* A = static_cast<const uint16_t*>(a.A);
   auto* t = static_cast<uint16_t*>(T);
   const int n = counters != nullptr ? kGatedDecodeMaxCtas : 0;
   NF4_PROF_BEGIN(st, kKGatedT);
   if (a.f16)
-    gated_t_small_kernel<true><<<grid, kTsThreads, 0, st>>>(x, A, int(a.M), int(a.K), a.r, a.s, t, counters, n);
+    gated_t_small_kernel<true><<<grid, 32 * kTsWarps, 0, st>>>(x, A, int(a.M), int(a.K), a.r, a.s, t, counters, n);
   else
-    gated_t_small_kernel<false><<<grid, kTsThreads, 0, st>>>(x, A, int(a.M), int(a.K), a.r, a.s, t, counters, n);
+    gated_t_small_kernel<false><<<grid, 32 * kTsWarps, 0, st>>>(x, A, int(a.M), int(a.K), a.r, a.s, t, counters, n);
   NF4_PROF_END(st, kKGatedT);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) ++*launches;
