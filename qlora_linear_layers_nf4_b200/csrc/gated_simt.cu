@@ -7,7 +7,10 @@
 // on load; a second form keeps the sums of both projections and finishes h = act(g) u.
 // T x T tiles (64, or 32 where those would leave SMs idle), 256 threads, the reduction in
 // slices of 32 through shared memory with the loads of the next two slices in flight; a
-// slice's products are summed by themselves before they are added to the others.
+// slice's products are summed by themselves before they are added to the others.  What a
+// slice takes is the latency of few warps, so where there are few tiles a cluster of CTAs
+// shares a tile's slices and sums its parts through distributed shared memory in their order:
+// the backward of 301 rows, 512 x 512 and r = 8, six launches, went from 96 to 55 us.
 #include <algorithm>
 
 #include <cuda_runtime.h>
@@ -15,12 +18,14 @@
 #include "gated.h"
 #include "gated_act.cuh"
 #include "nf4_common.cuh"
+#include "tc_common.cuh"
 
 namespace nf4 {
 namespace {
 
 constexpr int kSK = 32;
 constexpr int kSThreads = 256;
+constexpr int kSMaxCluster = 8;
 
 // Element (i, kk).  Contiguous runs of four stay inside an operand: every row length is a
 // multiple of eight.
@@ -61,13 +66,23 @@ struct SimtParams {
   int act;
 };
 
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 template <int T, bool GATED>
-__global__ void __launch_bounds__(kSThreads) gated_simt_kernel(const SimtParams p) {
+__global__ void __launch_bounds__(kSThreads, 2) gated_simt_kernel(const SimtParams p) {
   constexpr int kRow = T + 4;
   constexpr int kLoads = T * kSK / 4 / kSThreads;      // runs of four a thread, per operand and slice
-  constexpr int kOwn = T / 16;                         // results of a thread per dimension
-  __shared__ float sa[2][kSK * kRow];
-  __shared__ float sb[2][kSK * kRow];
+  // A thread has 4 x 4 results, so that eight values read from shared memory feed 16 FMAs (2 x 2
+  // were bound by those reads); the 32 x 32 tile's 64 threads are there four times, each with
+  // a quarter of a slice, joined at the end.
+  constexpr int kOwn = 4;
+  constexpr int kSide = T / kOwn, kTeams = kSThreads / (kSide * kSide);
+  __shared__ __align__(16) float sa[2][kSK * kRow];
+  __shared__ __align__(16) float sb[2][kSK * kRow];
   __shared__ float lut[16];
   const int t = threadIdx.x;
   if (t < 16) lut[t] = level(t);
@@ -76,31 +91,52 @@ __global__ void __launch_bounds__(kSThreads) gated_simt_kernel(const SimtParams 
   const int z = blockIdx.z;
 
   // Run l of a slice.  kmajor: index = (t + 256 l) / 8, kk = 4 (t % 8) ..; else kk, then index.
-  auto load = [&](const SimtOperand& o, int64_t first, int64_t k0, int64_t kend, float4 (&v)[kLoads]) {
+  struct Runs {
+    int64_t at[kLoads];    // element of the run in slice 0
+    int64_t step;          // elements to the next slice
+    int left[kLoads];      // slices that have the run
+  };
+  auto runs = [&](const SimtOperand& o, int64_t first, int64_t kend) {
+    Runs r;
+    r.step = o.kmajor ? kSK : kSK * o.ld;
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) {
       const int q = t + kSThreads * l;
       const int64_t i = first + (o.kmajor ? q / (kSK / 4) : 4 * (q % (T / 4)));
-      const int64_t kk = k0 + (o.kmajor ? 4 * (q % (kSK / 4)) : q / (T / 4));
+      const int64_t kk = o.kmajor ? 4 * (q % (kSK / 4)) : q / (T / 4);
+      r.at[l] = o.kmajor ? i * o.ld + kk : kk * o.ld + i;
+      r.left[l] = i < o.extent ? int((kend - kk + kSK - 1) / kSK) : 0;
+    }
+    return r;
+  };
+  auto load = [&](const SimtOperand& o, const Runs& r, int slice, float4 (&v)[kLoads]) {
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
       v[l] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i >= o.extent || kk >= kend) continue;
-      const int64_t at = o.kmajor ? i * o.ld + kk : kk * o.ld + i;
+      if (slice >= r.left[l]) continue;
+      const int64_t at = r.at[l] + slice * r.step;
       if (o.p != nullptr) {
         v[l] = __ldg(reinterpret_cast<const float4*>(o.p + z * o.z_stride + at));
-      } else {
+      } else {   // as it lies, decoded when it is parked: nothing waits for the load here
         const SimtWeight& w = p.w[o.w ^ (z & o.z_w)];
-        const uint32_t two = __ldg(reinterpret_cast<const uint16_t*>(w.codes + (at >> 1)));
         const int64_t blk = at >> p.bs_shift;
-        const float s = p.dq ? __fmul_rn(float(__ldg(w.absmax_q + blk)), __ldg(w.absmax_scale)) : __ldg(w.absmax + blk);
-        v[l] = make_float4(__fmul_rn(lut[(two >> 4) & 15u], s), __fmul_rn(lut[two & 15u], s),
-                           __fmul_rn(lut[two >> 12], s), __fmul_rn(lut[(two >> 8) & 15u], s));
+        v[l].x = __uint_as_float(uint32_t(__ldg(reinterpret_cast<const uint16_t*>(w.codes + (at >> 1)))));
+        v[l].y = p.dq ? __uint_as_float(uint32_t(__ldg(w.absmax_q + blk))) : __ldg(w.absmax + blk);
+        v[l].w = 1.0f;   // there
       }
     }
   };
-  auto park = [&](const SimtOperand& o, float* s, const float4 (&v)[kLoads]) {
+  const float s_g[2] = {p.dq ? __ldg(p.w[0].absmax_scale) : 0.0f, p.dq ? __ldg(p.w[1].absmax_scale) : 0.0f};
+  auto park = [&](const SimtOperand& o, float* s, float4 (&v)[kLoads]) {
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) {
       const int q = t + kSThreads * l;
+      if (o.p == nullptr && v[l].w != 0.0f) {
+        const uint32_t two = __float_as_uint(v[l].x);
+        const float c = p.dq ? __fmul_rn(float(__float_as_uint(v[l].y)), s_g[o.w ^ (z & o.z_w)]) : v[l].y;
+        v[l] = make_float4(__fmul_rn(lut[(two >> 4) & 15u], c), __fmul_rn(lut[two & 15u], c),
+                           __fmul_rn(lut[two >> 12], c), __fmul_rn(lut[(two >> 8) & 15u], c));
+      }
       if (o.kmajor) {
         float* d = s + 4 * (q % (kSK / 4)) * kRow + q / (kSK / 4);
         d[0] = v[l].x;
@@ -113,7 +149,7 @@ __global__ void __launch_bounds__(kSThreads) gated_simt_kernel(const SimtParams 
     }
   };
 
-  const int ty = t >> 4, tx = t & 15;
+  const int team = t / (kSide * kSide), ty = t % (kSide * kSide) / kSide, tx = t % kSide;
   constexpr int kSets = GATED ? 2 : 1;
   float acc[kSets][kOwn][kOwn];
 #pragma unroll
@@ -123,34 +159,36 @@ __global__ void __launch_bounds__(kSThreads) gated_simt_kernel(const SimtParams 
 #pragma unroll
       for (int b = 0; b < kOwn; ++b) acc[g][a][b] = 0.0f;
 
+  const int part = blockIdx.y, parts = gridDim.y;   // CTAs of a cluster share the slices
   int cur = 0;
   auto segment = [&](const SimtSegment& sg, float (&into)[kOwn][kOwn]) {
-    const int64_t slices = (sg.kdim + kSK - 1) / kSK;
+    const int64_t all = (sg.kdim + kSK - 1) / kSK;
+    const int begin = int(all * part / parts), slices = int(all * (part + 1) / parts);
+    if (begin == slices) return;
+    const Runs ra = runs(sg.a, i0, sg.kdim), rb = runs(sg.b, j0, sg.kdim);
     float4 va[2][kLoads], vb[2][kLoads];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      load(sg.a, i0, h * kSK, sg.kdim, va[h]);
-      load(sg.b, j0, h * kSK, sg.kdim, vb[h]);
+      load(sg.a, ra, begin + h, va[h]);
+      load(sg.b, rb, begin + h, vb[h]);
     }
-    auto slice = [&](int64_t s, float4 (&xa)[kLoads], float4 (&xb)[kLoads]) {
+    auto slice = [&](int s, float4 (&xa)[kLoads], float4 (&xb)[kLoads]) {
       park(sg.a, sa[cur], xa);
       park(sg.b, sb[cur], xb);
       __syncthreads();
-      load(sg.a, i0, (s + 2) * kSK, sg.kdim, xa);
-      load(sg.b, j0, (s + 2) * kSK, sg.kdim, xb);
+      load(sg.a, ra, s + 2, xa);
+      load(sg.b, rb, s + 2, xb);
       float sum[kOwn][kOwn];
 #pragma unroll
       for (int a = 0; a < kOwn; ++a)
 #pragma unroll
         for (int b = 0; b < kOwn; ++b) sum[a][b] = 0.0f;
 #pragma unroll
-      for (int kk = 0; kk < kSK; ++kk) {
-        float ar[kOwn], br[kOwn];
-#pragma unroll
-        for (int a = 0; a < kOwn; ++a) {
-          ar[a] = sa[cur][kk * kRow + kOwn * ty + a];
-          br[a] = sb[cur][kk * kRow + kOwn * tx + a];
-        }
+      for (int kk = 0; kk < kSK / kTeams; ++kk) {
+        const int row = (team * (kSK / kTeams) + kk) * kRow;
+        const float4 a4 = *reinterpret_cast<const float4*>(&sa[cur][row + kOwn * ty]);
+        const float4 b4 = *reinterpret_cast<const float4*>(&sb[cur][row + kOwn * tx]);
+        const float ar[kOwn] = {a4.x, a4.y, a4.z, a4.w}, br[kOwn] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
         for (int a = 0; a < kOwn; ++a)
 #pragma unroll
@@ -162,7 +200,7 @@ __global__ void __launch_bounds__(kSThreads) gated_simt_kernel(const SimtParams 
         for (int b = 0; b < kOwn; ++b) into[a][b] += sum[a][b];
       cur ^= 1;   // the barrier of the next slice separates its writes from these reads' buffer
     };
-    for (int64_t s = 0; s < slices; s += 2) {
+    for (int s = begin; s < slices; s += 2) {
       slice(s, va[0], vb[0]);
       if (s + 1 < slices) slice(s + 1, va[1], vb[1]);
     }
@@ -176,31 +214,80 @@ __global__ void __launch_bounds__(kSThreads) gated_simt_kernel(const SimtParams 
     for (int g = 0; g < p.nseg; ++g) segment(p.seg[g], acc[0]);
   }
 
-#pragma unroll
-  for (int a = 0; a < kOwn; ++a) {
-    const int64_t i = i0 + kOwn * ty + a;
-    if (i >= p.rows) continue;
-#pragma unroll
-    for (int b = 0; b < kOwn; ++b) {
-      const int64_t j = j0 + kOwn * tx + b;
-      if (j >= p.cols) continue;
-      const int64_t at = i * p.cols + j;
-      if (GATED) {
-        float g = acc[0][a][b], u = acc[kSets - 1][a][b];
-        if (p.bias != nullptr) {
-          g = __fadd_rn(g, __ldg(p.bias + j));
-          u = __fadd_rn(u, __ldg(p.bias + p.cols + j));
-        }
-        if (p.pre != nullptr) {
-          p.pre[at] = g;
-          p.pre[p.rows * p.cols + at] = u;
-        }
-        p.c[at] = gated::act<false>(p.act, g) * u;
-      } else {
-        p.c[z * p.rows * p.cols + at] = __fmul_rn(p.alpha, acc[0][a][b]);
+  auto finish = [&](int row, int col, const float (&v)[kSets]) {   // of the tile
+    const int64_t i = i0 + row, j = j0 + col;
+    if (i >= p.rows || j >= p.cols) return;
+    const int64_t at = i * p.cols + j;
+    if (GATED) {
+      float g = v[0], u = v[kSets - 1];
+      if (p.bias != nullptr) {
+        g = __fadd_rn(g, __ldg(p.bias + j));
+        u = __fadd_rn(u, __ldg(p.bias + p.cols + j));
       }
+      if (p.pre != nullptr) {
+        p.pre[at] = g;
+        p.pre[p.rows * p.cols + at] = u;
+      }
+      p.c[at] = gated::act<false>(p.act, g) * u;
+    } else {
+      p.c[z * p.rows * p.cols + at] = __fmul_rn(p.alpha, v[0]);
     }
+  };
+  float* mine[2] = {&sa[0][0], &sb[0][0]};   // sums, from here on
+  auto store_sums = [&]() {
+#pragma unroll
+    for (int g = 0; g < kSets; ++g)
+#pragma unroll
+      for (int a = 0; a < kOwn; ++a)
+        *reinterpret_cast<float4*>(&mine[g][(kOwn * ty + a) * T + kOwn * tx]) =
+            make_float4(acc[g][a][0], acc[g][a][1], acc[g][a][2], acc[g][a][3]);
+  };
+  __syncthreads();
+#pragma unroll
+  for (int m = 1; m < kTeams; ++m) {
+    if (team == m) store_sums();
+    __syncthreads();
+    if (team == 0) {
+#pragma unroll
+      for (int g = 0; g < kSets; ++g)
+#pragma unroll
+        for (int a = 0; a < kOwn; ++a)
+#pragma unroll
+          for (int b = 0; b < kOwn; ++b) acc[g][a][b] += mine[g][(kOwn * ty + a) * T + kOwn * tx + b];
+    }
+    __syncthreads();
   }
+  if (parts == 1) {
+    if (team != 0) return;
+#pragma unroll
+    for (int a = 0; a < kOwn; ++a)
+#pragma unroll
+      for (int b = 0; b < kOwn; ++b) {
+        float v[kSets];
+#pragma unroll
+        for (int g = 0; g < kSets; ++g) v[g] = acc[g][a][b];
+        finish(kOwn * ty + a, kOwn * tx + b, v);
+      }
+    return;
+  }
+  if (team == 0) store_sums();
+  tc::cluster_sync();
+  for (int e = T * T * part / parts + t; e < T * T * (part + 1) / parts; e += kSThreads) {
+    float v[kSets];
+#pragma unroll
+    for (int g = 0; g < kSets; ++g) {
+      float one[kSMaxCluster];
+#pragma unroll
+      for (int c = 0; c < kSMaxCluster; ++c)   // all on their way before the first is needed
+        one[c] = c < parts ? ld_shared_cluster(tc::mapa_shared(tc::smem_u32(mine[g] + e), uint32_t(c))) : 0.0f;
+      v[g] = one[0];
+#pragma unroll
+      for (int c = 1; c < kSMaxCluster; ++c)
+        if (c < parts) v[g] += one[c];
+    }
+    finish(e / T, e % T, v);
+  }
+  tc::cluster_sync();   // the sums stay until all have read them
 }
 
 // dg, du
@@ -235,8 +322,28 @@ struct Launch {
   bool gated;
 };
 
-// 64 x 64 tiles where there are enough of them for the SMs: fewer loads a product.
-bool large_tiles(const Launch& l, int sms) { return (l.p.rows + 63) / 64 * ((l.p.cols + 63) / 64) * l.zs >= sms; }
+int64_t slices_of(const Launch& l) {
+  int64_t most = 0;
+  for (int g = 0; g < (l.gated ? 4 : l.p.nseg); ++g) most = std::max(most, (l.p.seg[g].kdim + kSK - 1) / kSK);
+  return most;
+}
+int64_t tiles_of(const Launch& l, int64_t t) { return (l.p.rows + t - 1) / t * ((l.p.cols + t - 1) / t) * l.zs; }
+
+// Parts of a tile's slices: a power of two (clusters of seven waited for each other: 68 us
+// against 55 for the backward of 301 rows, 512 x 512), such that all run at once at two CTAs
+// an SM, an eighth of them left to the GPCs' remainders, and two slices a part at least.
+int64_t parts_of(const Launch& l, int64_t tiles, int sms) {
+  int64_t parts = 1;
+  while (parts < kSMaxCluster && 2 * parts * tiles <= 2 * int64_t(sms) * 7 / 8 && slices_of(l) >= 4 * parts) parts *= 2;
+  return parts;
+}
+
+// 64 x 64 tiles, which take half of the instructions a product, where their parts are enough
+// for the SMs.
+bool large_tiles(const Launch& l, int sms) {
+  const int64_t tiles = tiles_of(l, 64);
+  return l.p.rows > 32 && l.p.cols > 32 && tiles * parts_of(l, tiles, sms) >= sms;
+}
 
 bool fits(const Launch& l) { return (l.p.rows + 31) / 32 * ((l.p.cols + 31) / 32) <= int64_t(0x7fffffff); }
 
@@ -245,17 +352,24 @@ cudaError_t run(Launch l, int sms, cudaStream_t st, int* launches) {
   const int64_t t = large ? 64 : 32;
   const int64_t ct = (l.p.cols + t - 1) / t, rt = (l.p.rows + t - 1) / t;
   l.p.col_tiles = int(ct);
-  const dim3 grid(unsigned(ct * rt), 1, unsigned(l.zs));
+  const int64_t parts = parts_of(l, ct * rt * l.zs, sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ct * rt), unsigned(parts), unsigned(l.zs));
+  cfg.blockDim = dim3(kSThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = unsigned(parts);
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   NF4_PROF_BEGIN(st, l.id);
-  if (l.gated) {
-    if (large) gated_simt_kernel<64, true><<<grid, kSThreads, 0, st>>>(l.p);
-    else gated_simt_kernel<32, true><<<grid, kSThreads, 0, st>>>(l.p);
-  } else {
-    if (large) gated_simt_kernel<64, false><<<grid, kSThreads, 0, st>>>(l.p);
-    else gated_simt_kernel<32, false><<<grid, kSThreads, 0, st>>>(l.p);
-  }
+  cudaError_t e;
+  if (l.gated) e = large ? cudaLaunchKernelEx(&cfg, gated_simt_kernel<64, true>, l.p) : cudaLaunchKernelEx(&cfg, gated_simt_kernel<32, true>, l.p);
+  else e = large ? cudaLaunchKernelEx(&cfg, gated_simt_kernel<64, false>, l.p) : cudaLaunchKernelEx(&cfg, gated_simt_kernel<32, false>, l.p);
   NF4_PROF_END(st, l.id);
-  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess) ++*launches;
   return e;
 }
