@@ -10,9 +10,11 @@
 // of a cluster, which sum their fp32 partials through distributed shared memory in a fixed
 // order.
 //
-// T and dA are fed by TMA.  U and dB make their A operand, d, on the way: eight warps
-// read dh, g and u (a step ahead, in registers), compute dg and du in fp32 and write them
-// as 16-bit terms, swizzled, into shared memory; U's warps store the first terms to global
+// T and dA are fed by TMA.  U and dB make their A operand, d, on the way: sixteen warps
+// read dh, g and u (copied two steps ahead), compute dg and du in fp32 and write them as
+// 16-bit terms, swizzled, into shared memory (eight warps of twice the work took 118 and 117 us
+// for U and dB at 4096 tokens, 11008 x 4096, against 98 and 107: a step is its arithmetic's
+// latency more than its rate); U's warps store the first terms to global
 // memory too, for dx.  dB computes d a second time instead of reading it: the fp32 value
 // is what it needs, and dh, g and u are 3/4 of the bytes of two terms of dg and du.
 //
@@ -405,9 +407,10 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
 
 // ------------------------------------------------------------------ U and dB: d made on the way
 
-constexpr int kMkWarps = 8;                                     // they make d, and finish the tile
+constexpr int kMkWarps = 16;                                    // they make d, and finish the tile
 constexpr int kMkThreads = 32 * (kMkWarps + 2);                 // and B loads, MMA
-constexpr int kMkPer = 4;                                       // chunks of eight elements a thread has of a step
+constexpr int kMkPass = 4 * kMkWarps;                           // rows that a chunk of every thread covers
+constexpr int kMkPer = 128 / kMkPass;                           // chunks of eight elements a thread has of a step
 constexpr int kMkAhead = 2 * kMkPer;                            // and how many it copies ahead
 constexpr uint32_t kMkInBytes = 32 * kMkWarps * 16;             // a chunk's dh, g or u, of all threads
 constexpr int kMkBufs = 2;                                      // B of a step
@@ -522,7 +525,7 @@ __global__ void __launch_bounds__(kMkThreads, 1)
 
   if (warp < kMkWarps) {
     // ---------------- d of 128 x 64 (U) or 64 x 128 (dB) elements a step, as two halves of
-    // 64 x 64: a thread takes chunks of eight elements (16-byte chunk t % 8) of four rows.  It
+    // 64 x 64: a thread takes chunks of eight elements (16-byte chunk t % 8) of two rows.  It
     // copies their dh, g and u to shared memory two steps ahead (as registers one step ahead
     // allowed half of the bytes in flight), and keeps a step's terms until the MMAs have read
     // the step before.
@@ -530,16 +533,16 @@ __global__ void __launch_bounds__(kMkThreads, 1)
     constexpr int kWide = 2 * kCols / (kMkWarps / 4);
     const int64_t mn = int64_t(p.M) * p.N;
     const int red0 = w.step0 * 64;
-    // chunk c (half c / 2, row 32 (c % 2) + t / 8) in the first step; a step later it is
+    // chunk c (row kMkPass c + t / 8 of both halves) in the first step; a step later it is
     // `ahead` further.  `left`: how far the reduction index may still go.
     const int64_t ahead = KIND == kGatedU ? 64 : int64_t(64) * p.N;
     int64_t at[kMkPer];
     int left[kMkPer];
 #pragma unroll
     for (int c = 0; c < kMkPer; ++c) {
-      const int r = 32 * (c & 1) + tr;
-      const int m = KIND == kGatedU ? row0 + 64 * (c >> 1) + r : red0 + r;
-      const int n = KIND == kGatedU ? red0 + 8 * tc : row0 + 64 * (c >> 1) + 8 * tc;
+      const int half = c * kMkPass / 64, r = c * kMkPass % 64 + tr;
+      const int m = KIND == kGatedU ? row0 + 64 * half + r : red0 + r;
+      const int n = KIND == kGatedU ? red0 + 8 * tc : row0 + 64 * half + 8 * tc;
       at[c] = int64_t(m) * p.N + n;
       left[c] = KIND == kGatedU ? (m < p.M ? p.N - n : 0) : (n < p.N ? p.M - m : 0);
     }
@@ -612,7 +615,7 @@ __global__ void __launch_bounds__(kMkThreads, 1)
       if (!ok) break;
 #pragma unroll
       for (int c = 0; c < kMkPer; ++c) {
-        const uint32_t off = uint32_t(c >> 1) * kBoxBytes + sw128_offset(uint32_t(32 * (c & 1) + tr), uint32_t(tc));
+        const uint32_t off = uint32_t(c * kMkPass / 64) * kBoxBytes + sw128_offset(uint32_t(c * kMkPass % 64 + tr), uint32_t(tc));
 #pragma unroll
         for (int z = 0; z < 2; ++z)
 #pragma unroll
