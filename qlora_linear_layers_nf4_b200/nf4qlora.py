@@ -686,9 +686,9 @@ def gated_fwd(gate: QuantizedWeight, up: QuantizedWeight, x, A, B, alpha: float,
     here = _here(dev)
     need = _workspace_size(OP_GATED_FWD_F32 if dt == NF4_F32 else OP_GATED_FWD, M, N, K, r)
     ws = _scratch(workspace, dev, here)
-    h = out if out is not None else torch.empty((M, N), dtype=x.dtype, device=dev)
+    h = out if out is not None else torch.empty(M, N, dtype=x.dtype, device=dev)
     if want_saved and saved is None:
-        saved = GatedSaved(torch.empty((2, M, N), dtype=x.dtype, device=dev), torch.empty((2, M, r), dtype=x.dtype, device=dev))
+        saved = GatedSaved(torch.empty(2, M, N, dtype=x.dtype, device=dev), torch.empty(2, M, r, dtype=x.dtype, device=dev))
     with ws.lock:
         st = lib().qlora_gated_fwd(gate.c_struct(), up.c_struct(), x.data_ptr(), M, A.data_ptr(), B.data_ptr(), r, alpha, act, dt,
                                    _at(bias), h.data_ptr(), None if saved is None else _at(saved.pre),
@@ -722,10 +722,10 @@ def gated_bwd(gate: QuantizedWeight, up: QuantizedWeight, x, A, B, alpha: float,
     here = _here(dev)
     need = _workspace_size(OP_GATED_BWD_F32 if dt == NF4_F32 else OP_GATED_BWD, M, N, K, r)
     ws = _scratch(workspace, dev, here)
-    dA = dA if dA is not None else torch.empty((2, r, K), dtype=torch.float32, device=dev)
-    dB = dB if dB is not None else torch.empty((2, N, r), dtype=torch.float32, device=dev)
+    dA = dA if dA is not None else torch.empty(2, r, K, dtype=torch.float32, device=dev)
+    dB = dB if dB is not None else torch.empty(2, N, r, dtype=torch.float32, device=dev)
     if want_dx and dx is None:
-        dx = torch.empty((M, K), dtype=x.dtype, device=dev)
+        dx = torch.empty(M, K, dtype=x.dtype, device=dev)
     with ws.lock:
         st = lib().qlora_gated_bwd(gate.c_struct(), up.c_struct(), x.data_ptr(), M, A.data_ptr(), B.data_ptr(), r, alpha, act, dt,
                                    dh.data_ptr(), saved.pre.data_ptr(), _at(saved.t), dA.data_ptr(), dB.data_ptr(), _at(dx),
@@ -847,8 +847,8 @@ def fp8_quantize(x, block_rows: int = 1, codes=None, scale=None) -> Fp8Matrix:
     _fits("codes", codes, (rows, cols), torch.float8_e4m3fn, x.device)
     _fits("scale", scale, blocks, torch.float32, x.device)
     here = _here(x.device)
-    codes = codes if codes is not None else torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
-    scale = scale if scale is not None else torch.empty(blocks, dtype=torch.float32, device=x.device)
+    codes = codes if codes is not None else torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    scale = scale if scale is not None else torch.empty(*blocks, dtype=torch.float32, device=x.device)
     st = lib().fp8_quantize(x.data_ptr(), dt, rows, cols, block_rows, codes.data_ptr(), scale.data_ptr(), here)
     if st:
         raise NF4Error(st, "fp8_quantize")
@@ -869,7 +869,7 @@ def fp8_dequantize(q: Fp8Matrix, out_dtype=None, out=None):
         out_dtype = torch.float32 if out is None else out.dtype
     _fits("out", out, (rows, cols), out_dtype, dev)
     here = _here(dev)
-    out = out if out is not None else torch.empty((rows, cols), dtype=out_dtype, device=dev)
+    out = out if out is not None else torch.empty(rows, cols, dtype=out_dtype, device=dev)
     st = lib().fp8_dequantize(q.codes.data_ptr(), q.scale.data_ptr(), rows, cols, q.block_rows, _compute_dtype(out),
                               out.data_ptr(), here)
     if st:
@@ -917,7 +917,7 @@ def fp8_linear_fwd(w: Fp8Matrix, x, bias=None, out_dtype=None, out=None, workspa
     here = _here(dev)
     need = _workspace_size(OP_FP8_LINEAR, M, N, K, 0)
     ws = _scratch(workspace, dev, here)
-    y = out if out is not None else torch.empty((M, N), dtype=y_dtype, device=dev)
+    y = out if out is not None else torch.empty(M, N, dtype=y_dtype, device=dev)
     with ws.lock:
         st = lib().fp8_linear_fwd(w.codes.data_ptr(), w.scale.data_ptr(), N, K, xv.data_ptr(), _at(xs), M, dt, _at(bias),
                                   y.data_ptr(), ws.get(need, dev).data_ptr(), need, here)
