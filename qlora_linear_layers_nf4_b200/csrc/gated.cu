@@ -13,7 +13,10 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 size_t mr_bytes(int64_t M, int r, size_t size) { return align256(size_t(M) * size_t(r) * size); }
 size_t pair_bytes(int64_t M, int64_t N, size_t size) { return align256(2 * size_t(M) * size_t(N) * size); }
 
-// Few tokens: stream the weights (16 tokens a pass) instead of feeding the GEMM.
+// Few tokens: stream the weights (16 tokens a pass) instead of feeding the GEMM.  Measured, this
+// against the GEMM, us: 11008 x 4096 with 1, 16, 32, 40 and 64 tokens 29, 35, 55, 74 and 94 against
+// 65 to 68; 512 x 512 with 8 and 32 9.7 and 11.4 against 11.5; 1000 x 4096 with 32 23 against 35;
+// 4096 x 1024 with 32 16.6 against 15.1.
 bool use_decode(int64_t M) { return M <= 32; }
 
 }  // namespace

@@ -18,6 +18,11 @@
 // memory too, for dx.  dB computes d a second time instead of reading it: the fp32 value
 // is what it needs, and dh, g and u are 3/4 of the bytes of two terms of dg and du.
 //
+// Measured at 4096 tokens, 11008 x 4096, r = 64: U 98 us (reads 270 MB, writes 180: 4.6 TB/s), dB
+// 107 (270 MB, 2.5 TB/s), dA 25, T 16.  U and dB are bound by the latency of making d, a step's
+// arithmetic and its way into shared memory (issue 32 to 38 %, DRAM 27 to 34 %), and by clusters
+// that leave 20 to 52 of 148 SMs idle.
+//
 // Gradients are fp32, and one rounding of d or U to 16 bits would be their largest error by
 // far (2^-9 against 2^-24).  So d and U enter as three bf16 terms that together hold 24
 // bits, or two f16 terms, the second scaled by 2^11 (22 bits; see expert_grad.cu).  The tensor
