@@ -1,6 +1,8 @@
 // Gated feed-forward layer: the launches of a call.  Every launch is prepared (its tensor maps
 // encoded) before the first is enqueued, so a call that fails on the host enqueues nothing.
 
+#include <algorithm>
+
 #include "gated.h"
 #include "gated_decode.h"
 #include "gated_rank.h"
@@ -26,23 +28,26 @@ size_t gated_workspace_bytes(bool backward, bool f32, int64_t M, int64_t N, int6
   if (M < 0 || N < 0 || K < 0 || r < 0) return 0;
   if (f32) return gated_f32_workspace_bytes(backward, M, N, r);
   const size_t t = mr_bytes(2 * M, r, 2);
-  return backward ? t + mr_bytes(6 * M, r, 2) + pair_bytes(M, N, 2) + gated_split_bytes(M, K) : t + gated_decode_scratch_bytes();
+  const size_t splits = gated_split_bytes(backward, M, N, K);
+  return backward ? t + mr_bytes(6 * M, r, 2) + pair_bytes(M, N, 2) + splits : t + std::max(splits, gated_decode_scratch_bytes());
 }
 
 cudaError_t launch_gated_fwd(const GatedArgs& a, int sms, cudaStream_t st, int* launches) {
   if (a.f32) return launch_gated_fwd_f32(a, sms, st, launches);
   void* T = a.t_out != nullptr ? a.t_out : a.ws + kWsHeader;
   GatedDecode d;
+  uint8_t* scratch = a.ws + kWsHeader + mr_bytes(2 * a.M, a.r, 2);
   if (use_decode(a.M)) {
-    if (!d.prepare(a, T, a.ws + kWsHeader + mr_bytes(2 * a.M, a.r, 2), sms)) return cudaErrorInvalidValue;
+    if (!d.prepare(a, T, scratch, sms)) return cudaErrorInvalidValue;
     const cudaError_t e = launch_gated_t_small(a, T, d.p.counters, st, launches);
     return e == cudaSuccess ? d.run(st, launches) : e;
   }
   GatedRank t;
   GatedGemm h;
-  if (!t.prepare(a, kGatedT, nullptr, nullptr, T, sms) || !h.prepare(a, false, a.x, T, nullptr, sms)) return cudaErrorInvalidValue;
-  const cudaError_t e = t.run(st, launches);
-  return e == cudaSuccess ? h.run(st, launches) : e;
+  if (!t.prepare(a, kGatedT, nullptr, nullptr, T, sms) || !h.prepare(a, false, a.x, T, scratch, sms)) return cudaErrorInvalidValue;
+  cudaError_t e = t.run(st, launches);
+  if (e == cudaSuccess) e = h.run(st, launches);
+  return e == cudaSuccess ? h.sum(st, launches) : e;
 }
 
 cudaError_t launch_gated_bwd(const GatedArgs& a, int sms, cudaStream_t st, int* launches) {

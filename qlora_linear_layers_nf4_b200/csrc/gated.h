@@ -71,16 +71,17 @@ struct GatedParams {
   const void* bias;
   void* out;                  // h or dx
   void* pre;                  // forward: [2][M][N] or null
-  int splits;                 // dx: of the reduction
-  float* partials;            // dx in several splits: [split][M][K]
+  int splits;                 // of the reduction
+  float* partials;            // of several splits: [split][M][2][N] or [split][M][K]
   uint32_t* status;
 };
 
 constexpr int kGatedMaxPairs = 80;   // most CTA pairs that splits are made for
-size_t gated_split_bytes(int64_t M, int64_t K);
+size_t gated_split_bytes(bool backward, int64_t M, int64_t N, int64_t K);
 
 // h (and g, u) or dx, prepared on the host before the first launch of a call.  `ad`: T
-// [2][M][r], or the terms of U [2][terms][M][r], of which the first are read; `tok`: x, or dg and du [2][M][N]; the kernels launched before write them.
+// [2][M][r], or the terms of U [2][terms][M][r], of which the first are read; `tok`: x, or dg
+// and du [2][M][N]; the kernels launched before write them.  `scratch`: gated_split_bytes.
 struct GatedGemm {
   GatedMaps maps;
   GatedParams p;
@@ -89,7 +90,7 @@ struct GatedGemm {
   bool dx = false, f16 = false;
   bool prepare(const GatedArgs& a, bool backward, const void* tok, const void* ad, void* scratch, int sms);
   cudaError_t run(cudaStream_t st, int* launches) const;
-  cudaError_t sum(cudaStream_t st, int* launches) const;   // dx: adds up the splits, if there are several
+  cudaError_t sum(cudaStream_t st, int* launches) const;   // adds up the splits, if there are several
 };
 
 }  // namespace nf4

@@ -108,7 +108,7 @@ __device__ __forceinline__ Tile tile_at(const GatedParams& p, int id) {
   t.split = 0;
   t.k0 = 0;
   t.k1 = steps;
-  if (MODE == kDx && p.splits > 1) {
+  if (p.splits > 1) {
     t.split = id % p.splits;
     id /= p.splits;
     t.k0 = steps * t.split / p.splits;
@@ -209,7 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
-  const int tiles = p.row_tiles * p.col_tiles * (MODE == kDx ? p.splits : 1);
+  const int tiles = p.row_tiles * p.col_tiles * p.splits;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   auto leader_bar = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
   // projection and first index within it of a main step, and of an adapter step
@@ -417,9 +417,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
           uint32_t v[32];
           tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + uint32_t(n & 1) * 256u + c * 32, v);
           tmem_ld_wait();
-          [[maybe_unused]] const int left = cnt - c * 32;
+          const int left = cnt - c * 32;
           const int64_t row0 = int64_t(t0) + c * 32;
           if (MODE == kFwd) {
+            if (PARTS == 1 && p.splits > 1) {   // fp32 sums of the split, added up by the kernel after
+              float* o = p.partials + ((int64_t(t.split) * p.M + row0) * 2 + odd) * p.out_cols + col;
+#pragma unroll
+              for (int i = 0; i < 32; ++i, o += 2 * int64_t(p.out_cols))
+                if (col_ok && i < left) __stcg(o, __uint_as_float(v[i]));
+              continue;
+            }
             float g[16], u[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
@@ -462,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
               bulk_commit_group();
             }
           } else {
-            if (p.splits > 1) {   // fp32 sums of the split, added up by the kernel after
+            if (PARTS == 1 && p.splits > 1) {   // likewise
               float* o = p.partials + (int64_t(t.split) * p.M + row0) * p.out_cols + col;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
@@ -603,20 +610,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE, PAR
   }
 }
 
-// dx from the splits' sums, in their order: four outputs a thread.
 constexpr int kSumThreads = 256;
+
+// Four values of every split, added up in their order.
+__device__ __forceinline__ float4 sum4(const float* __restrict__ parts, int splits, int64_t stride) {
+  float4 v = __ldcg(reinterpret_cast<const float4*>(parts));
+  for (int s = 1; s < splits; ++s) {
+    const float4 w = __ldcg(reinterpret_cast<const float4*>(parts + int64_t(s) * stride));
+    v.x += w.x;
+    v.y += w.y;
+    v.z += w.z;
+    v.w += w.w;
+  }
+  return v;
+}
+template <bool F16>
+__device__ __forceinline__ uint2 round4(float4 v) {
+  return make_uint2(pack2(F16, v.x, v.y), pack2(F16, v.z, v.w));
+}
+
+// h, and g and u, from the splits' sums [split][M][2][N]: four outputs a thread.
+template <bool F16>
+__global__ void __launch_bounds__(kSumThreads) gated_finish_kernel(const GatedParams p) {
+  const int64_t n = int64_t(p.M) * p.out_cols;
+  uint16_t* h = static_cast<uint16_t*>(p.out);
+  uint16_t* pre = static_cast<uint16_t*>(p.pre);
+  for (int64_t i = (int64_t(blockIdx.x) * kSumThreads + threadIdx.x) * 4; i < n; i += int64_t(gridDim.x) * kSumThreads * 4) {
+    const int64_t row = i / p.out_cols;
+    const int col = int(i - row * p.out_cols);
+    float4 v[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      v[z] = sum4(p.partials + (2 * row + z) * p.out_cols + col, p.splits, 2 * n);
+      if (p.bias != nullptr) {
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.bias) + int64_t(z) * p.out_cols + col));
+        const float2 lo = unpack2(F16, b.x), hi = unpack2(F16, b.y);
+        v[z] = make_float4(v[z].x + lo.x, v[z].y + lo.y, v[z].z + hi.x, v[z].w + hi.y);
+      }
+      if (pre != nullptr) *reinterpret_cast<uint2*>(pre + z * n + i) = round4<F16>(v[z]);
+    }
+    *reinterpret_cast<uint2*>(h + i) =
+        round4<F16>(make_float4(gated::act<true>(p.act, v[0].x) * v[1].x, gated::act<true>(p.act, v[0].y) * v[1].y,
+                                gated::act<true>(p.act, v[0].z) * v[1].z, gated::act<true>(p.act, v[0].w) * v[1].w));
+  }
+}
+
+// dx from the splits' sums: four outputs a thread.
 template <bool F16>
 __global__ void __launch_bounds__(kSumThreads) gated_sum_kernel(const float* __restrict__ parts, int splits, int64_t n, uint16_t* __restrict__ out) {
   for (int64_t i = (int64_t(blockIdx.x) * kSumThreads + threadIdx.x) * 4; i < n; i += int64_t(gridDim.x) * kSumThreads * 4) {
-    float4 v = __ldcg(reinterpret_cast<const float4*>(parts + i));
-    for (int s = 1; s < splits; ++s) {
-      const float4 w = __ldcg(reinterpret_cast<const float4*>(parts + int64_t(s) * n + i));
-      v.x += w.x;
-      v.y += w.y;
-      v.z += w.z;
-      v.w += w.w;
-    }
-    *reinterpret_cast<uint2*>(out + i) = make_uint2(pack2(F16, v.x, v.y), pack2(F16, v.z, v.w));
+    *reinterpret_cast<uint2*>(out + i) = round4<F16>(sum4(parts + i, splits, n));
   }
 }
 
@@ -680,25 +723,28 @@ bool ad_map(CUtensorMap* map, const void* ad, uint64_t r, uint64_t M, uint64_t t
 }
 
 
-// Splits of dx's reduction where its tiles leave at least half of the CTA pairs idle: a step
+// Splits of the reduction where the tiles leave at least half of the CTA pairs idle: a step
 // costs the decoding of its weights whatever the tokens, so few tiles with many steps are
-// slow (100 tokens, 4000 x 2048: 8 tiles of 127 steps, 65 us).  Eight steps a split at least.
-int dx_splits(int64_t tiles, int steps, int sms) {
+// slow (dx of 100 tokens, 4000 x 2048: 8 tiles of 127 steps, 65 us; with splits the forward of
+// 64 tokens, 1000 x 4096, takes 19 us against 35, of 300, 512 x 8192, 33 against 68).  Eight
+// steps a split at least, and none of fewer than 24 (333 tokens, 1032 x 1088: 22.4 against 21.9).
+int splits_of(int64_t tiles, int steps, int sms) {
+  if (steps < 24) return 1;
   const int64_t pairs = std::min(std::max(sms / 2, 1), kGatedMaxPairs);
   return int(std::max<int64_t>(1, std::min<int64_t>(pairs / tiles, steps / 8)));
 }
 
 }  // namespace
 
-// Splits' sums, fp32: as many of M x K as there are splits.  More rows make more tiles and so
-// fewer splits: the size is the largest of any number of rows up to M, so that a workspace for
-// M serves fewer.
-size_t gated_split_bytes(int64_t M, int64_t K) {
-  const int64_t k_tiles = cdiv(K, 256);
+// Splits' sums, fp32: [split][M][K] or, forward, [split][M][2][N].  More rows make more tiles
+// and so fewer splits: the size is the largest of any number of rows up to M, so that a
+// workspace for M serves fewer.
+size_t gated_split_bytes(bool backward, int64_t M, int64_t N, int64_t K) {
+  const int64_t col_tiles = backward ? cdiv(K, tile_w(kDx)) : cdiv(N, tile_w(kFwd));
   int64_t rows = 0;
-  for (int64_t m_tiles = 1; (m_tiles - 1) * 256 < M && 2 * m_tiles * k_tiles <= kGatedMaxPairs; ++m_tiles)
-    rows = std::max(rows, kGatedMaxPairs / (m_tiles * k_tiles) * std::min(M, m_tiles * 256));
-  return size_t(rows) * size_t(K) * sizeof(float);
+  for (int64_t m_tiles = 1; (m_tiles - 1) * kPartT < M && 2 * m_tiles * col_tiles <= kGatedMaxPairs; ++m_tiles)
+    rows = std::max(rows, kGatedMaxPairs / (m_tiles * col_tiles) * std::min(M, m_tiles * kPartT));
+  return size_t(rows) * size_t(backward ? K : 2 * N) * sizeof(float);
 }
 
 bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, const void* ad, void* scratch, int sms) {
@@ -752,7 +798,7 @@ bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, cons
   p.out = backward ? a.dx : a.h;
   p.pre = backward ? nullptr : a.pre_out;
   p.status = a.status;
-  p.splits = backward ? dx_splits(int64_t(p.row_tiles) * p.col_tiles, p.main_steps + 2 * p.ad_steps, sms) : 1;
+  p.splits = parts == 2 ? 1 : splits_of(int64_t(p.row_tiles) * p.col_tiles, p.main_steps + 2 * p.ad_steps, sms);
   p.partials = static_cast<float*>(scratch);
   const int64_t tiles = int64_t(p.row_tiles) * p.col_tiles * p.splits;
   grid = 2u * unsigned(std::min<int64_t>(tiles, std::max(sms / 2, 1)));
@@ -762,12 +808,15 @@ bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, cons
 
 cudaError_t GatedGemm::sum(cudaStream_t st, int* launches) const {
   if (p.splits == 1) return cudaSuccess;
-  const int64_t n = int64_t(p.M) * p.out_cols;   // a multiple of 64
+  const int64_t n = int64_t(p.M) * p.out_cols;   // a multiple of 8
   const unsigned ctas = unsigned(std::min<int64_t>((n / 4 + kSumThreads - 1) / kSumThreads, 4096));
-  NF4_PROF_BEGIN(st, kKGatedDx);
-  if (f16) gated_sum_kernel<true><<<ctas, kSumThreads, 0, st>>>(p.partials, p.splits, n, static_cast<uint16_t*>(p.out));
+  const int id = dx ? kKGatedDx : kKGatedFwd;
+  NF4_PROF_BEGIN(st, id);
+  if (!dx && f16) gated_finish_kernel<true><<<ctas, kSumThreads, 0, st>>>(p);
+  else if (!dx) gated_finish_kernel<false><<<ctas, kSumThreads, 0, st>>>(p);
+  else if (f16) gated_sum_kernel<true><<<ctas, kSumThreads, 0, st>>>(p.partials, p.splits, n, static_cast<uint16_t*>(p.out));
   else gated_sum_kernel<false><<<ctas, kSumThreads, 0, st>>>(p.partials, p.splits, n, static_cast<uint16_t*>(p.out));
-  NF4_PROF_END(st, kKGatedDx);
+  NF4_PROF_END(st, id);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) ++*launches;
   return e;

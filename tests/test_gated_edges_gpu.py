@@ -223,3 +223,22 @@ def test_feed_forward_block(cuda_device):
         off = (got.double() - want).norm() / want.norm()
         assert off <= 8 * 2.0 ** -8, f"{name}: {off:.2e}"
     ok_status()
+
+
+@pytest.mark.parametrize("m,n,k,r,dtype,act", [(33, 72, 4096, 8, "bf16", "silu"), (64, 1000, 2048, 24, "f16", "gelu_tanh"),
+                                               (129, 136, 8192, 72, "bf16", "silu"), (257, 520, 1600, 256, "f16", "silu"),
+                                               (300, 264, 4160, 16, "bf16", "gelu_tanh")])
+def test_long_reductions_of_few_tiles(cuda_device, m, n, k, r, dtype, act):
+    """Few output tiles share a long reduction over K among several CTA pairs, forward and (N long) backward."""
+    import torch
+    Q = _Q()
+    L = Layer(cuda_device, m, n, k, r, dtype, bias=True, act=act)
+    big = torch.full((m + 3, n), 7.0, dtype=_dt(dtype), device=cuda_device)
+    h, saved = L.fwd(out=big[:m])
+    L.check_fwd(h, saved)
+    assert (big[m:] == 7).all()
+    assert L.fwd(want_saved=False)[0].equal(h)
+    L = Layer(cuda_device, m, k, 64, r, dtype, act=act)
+    saved = L.fwd()[1]
+    L.check_bwd(*L.bwd(saved), saved)
+    ok_status()
