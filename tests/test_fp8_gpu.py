@@ -254,3 +254,40 @@ def test_a_merged_weight(cuda_device):
         bound = ex @ (wa + step).T + xa @ step.T
         want = x.double() @ dense.double().T
         assert ((y - want).abs() <= bound * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()).all()
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_more_than_two_to_the_31_elements(cuda_device, block_rows):
+    """Offsets past 32 bits: the last rows of a matrix are those of the same rows by themselves."""
+    import torch
+    Q = _Q()
+    rows, cols = 128 * 513 + 41, 32_776
+    if torch.cuda.mem_get_info()[0] < 40e9:
+        pytest.skip("needs 40 GB")
+    gen = torch.Generator(device=cuda_device).manual_seed(2)
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=cuda_device)
+    x[-169:] = torch.randn(169, cols, generator=gen, device=cuda_device).to(torch.bfloat16)
+    q, last = Q.fp8_quantize(x, block_rows), Q.fp8_quantize(x[-169:].clone(), block_rows)
+    del x
+    assert q.codes[-169:].view(torch.uint8).equal(last.codes.view(torch.uint8))
+    assert q.scale[-last.scale.shape[0]:].equal(last.scale)
+    back = Q.fp8_dequantize(q, torch.bfloat16)
+    assert back[-169:].equal(Q.fp8_dequantize(last, torch.bfloat16))
+    del back, q
+    torch.cuda.empty_cache()
+
+
+def test_linear_with_more_than_two_to_the_31_results(cuda_device):
+    import torch
+    Q = _Q()
+    m, n, k = 70_041, 32_776, 144
+    if torch.cuda.mem_get_info()[0] < 20e9:
+        pytest.skip("needs 20 GB")
+    gen = torch.Generator(device=cuda_device).manual_seed(3)
+    w = Q.fp8_quantize(torch.randn(n, k, generator=gen, device=cuda_device), 128)
+    x = torch.randn(m, k, generator=gen, device=cuda_device).to(torch.bfloat16)
+    y = Q.fp8_linear_fwd(w, x)
+    for rows in (slice(0, 130), slice(m // 2, m // 2 + 130), slice(m - 130, m)):
+        assert y[rows].equal(Q.fp8_linear_fwd(w, x[rows].clone()))
+    del y
+    torch.cuda.empty_cache()

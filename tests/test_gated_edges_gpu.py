@@ -242,3 +242,27 @@ def test_long_reductions_of_few_tiles(cuda_device, m, n, k, r, dtype, act):
     saved = L.fwd()[1]
     L.check_bwd(*L.bwd(saved), saved)
     ok_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_more_than_two_to_the_31_elements(cuda_device, dtype):
+    """Offsets past 32 bits in h, g, u, dh, dg and du: the last rows, which alone have gradients, are checked."""
+    import torch
+    m, n, k = 70_041, 32_776, 64
+    if torch.cuda.mem_get_info()[0] < 60e9:
+        pytest.skip("needs 60 GB")
+    L = Layer(cuda_device, 8, n, k, 8, dtype)
+    gen = torch.Generator(device=cuda_device).manual_seed(1)
+    L.x = torch.randn(m, k, generator=gen, device=cuda_device).to(_dt(dtype))
+    L.dh = torch.zeros(m, n, dtype=_dt(dtype), device=cuda_device)
+    L.dh[-45:] = torch.randn(45, n, generator=gen, device=cuda_device).to(_dt(dtype))
+    h, saved = L.fwd()
+    for rows in (slice(0, 40), slice(m // 2, m // 2 + 40), slice(m - 45, m)):
+        L.check_fwd(h, saved, rows)
+    del h
+    dA, dB, dx = L.bwd(saved)
+    L.check_bwd(dA, dB, dx, saved, slice(m - 45, m))
+    assert not dx[:-45].any()
+    ok_status()
+    del L, saved, dx
+    torch.cuda.empty_cache()

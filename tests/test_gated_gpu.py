@@ -95,7 +95,7 @@ class Layer:
 
     def check_fwd(self, h, saved, rows=slice(None)):
         e = HALF[self.dtype]
-        x, A, B = self.x.double()[rows], self.A.double(), self.B.double()
+        x, A, B = self.x[rows].double(), self.A.double(), self.B.double()
         pre, err = [], []
         for p in range(2):
             tw = self.s * (x @ A[p].T)
@@ -122,8 +122,8 @@ class Layer:
     def check_bwd(self, dA, dB, dx, saved, rows=slice(None)):
         e = HALF[self.dtype]
         S, S0 = SPLIT[self.dtype]
-        x, dh, A, B = self.x.double()[rows], self.dh.double()[rows], self.A.double(), self.B.double()
-        g, u, t = saved.pre[0].double()[rows], saved.pre[1].double()[rows], saved.t.double()[:, rows]
+        x, dh, A, B = self.x[rows].double(), self.dh[rows].double(), self.A.double(), self.B.double()
+        g, u, t = saved.pre[0][rows].double(), saved.pre[1][rows].double(), saved.t[:, rows].double()
         m = x.shape[0]
         y, q, slope = logistic_parts(g, self.act)
         p = q * (1 - q)
