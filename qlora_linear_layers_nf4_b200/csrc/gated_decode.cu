@@ -8,14 +8,15 @@
 // hold 64 outputs of both projections: 128 weight rows, a unit of work 256 columns of them
 // (16 KB of codes), an equal share of the units for every SM.  A warp takes 8 gate rows as the
 // MMA rows 0 .. 7 and the same 8 up rows as 8 .. 15, so a thread that finishes a gate row has
-// the up row of its output in the next lane.  Half of the weights, the gate's, are decoded
-// with byte permutes, the up projection's with shared-memory lookups; the adapters' products
+// the up row of its output in the next lane.  A quarter of the weights, half of the gate's,
+// are decoded with byte permutes, the others with shared-memory lookups (44032 x 4096 and one
+// token: half and half 77 us, a quarter 72, an eighth 73, none 76.5); the adapters' products
 // are two MMAs, T_0 with the up rows zero and T_1 with the gate rows zero.
 //
-// Bound by decoding: at 44032 x 4096 the byte-permute pipe is 62 % busy, issue 55 %, shared
-// memory 54 %, DRAM 29 %.  Two weights of 11008 x 4096 (47 MB) take 29 us with one token (1.6
-// TB/s), 35 with 16, of which 12 are start, T and the join of split tiles; the rest grows by
-// 17 us (one token) to 20 (16 tokens) for each such pair of weights.
+// Bound by decoding: about four instructions a weight on issue, the byte-permute pipe and
+// shared memory, each half to two thirds busy.  Two weights of 11008 x 4096 (47 MB) take 27 us
+// with one token (1.7 TB/s), 34 with 16, of which 12 are start, T and the join of split tiles;
+// the rest grows by 15 us (one token) to 19 (16 tokens) for each such pair of weights.
 #include <algorithm>
 
 #include <cuda.h>
@@ -350,8 +351,8 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   // A warp takes 8 outputs of a unit, their gate rows as the MMA rows g and their up rows as
   // g + 8.  The four lanes of an output take a 64-wide block each, whole: the k index of an
   // MMA is free as long as W' and x agree, so lane q's four k positions are columns of block
-  // q.  The gate's row is decoded with byte permutes from a table of its block's sixteen
-  // products (as in the GEMM), the up row with the shared-memory lookups.
+  // q.  Half of the gate's row is decoded with byte permutes from a table of its block's
+  // sixteen products (as in the GEMM), the rest with the shared-memory lookups.
   const int group = warp / kDcGroupWarps;
   const int set = warp % kDcGroupWarps;     // outputs 8 set ..
   const int g = lane >> 2, q = lane & 3;
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kDcThreads, 1)
 #pragma unroll
       for (int c = 0; c < NT8; ++c) acc[i][c][0] = acc[i][c][1] = acc[i][c][2] = acc[i][c][3] = 0.0f;
     for (; kc < kend; kc += kGroups) {
-      if (ok) ok = warp_wait(&sh->full[s], ph, abort_flag, p.status);
+      if (ok && !__all_sync(0xffffffffu, mbar_try_wait(&sh->full[s], ph))) ok = warp_wait(&sh->full[s], ph, abort_flag, p.status);
       if (ok) {
         const uint8_t* st = smem + s * dc_stage_bytes(NP);
         float2 scale = *reinterpret_cast<const float2*>(&sh->scales[s][q][set * 16 + 2 * g]);
@@ -397,7 +398,8 @@ __global__ void __launch_bounds__(kDcThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t c0 = h ? w0.y : w0.x, c1 = h ? w1.y : w1.x;
-            const uint4 v = expert::decode8(c0, table);
+            const uint2 lo = expert::decode4(c0 & 0x7777u, ((c0 >> 1) & 0x4444u) | 0x3210u, table);
+            const uint4 v = make_uint4(lo.x, lo.y, two_weights<2, F16>(lut, c0, lane8, scale.x), two_weights<3, F16>(lut, c0, lane8, scale.x));
             const uint32_t a0[4] = {v.x, two_weights<0, F16>(lut, c1, lane8, scale.y), v.y, two_weights<1, F16>(lut, c1, lane8, scale.y)};
             const uint32_t a1[4] = {v.z, two_weights<2, F16>(lut, c1, lane8, scale.y), v.w, two_weights<3, F16>(lut, c1, lane8, scale.y)};
 #pragma unroll
