@@ -30,7 +30,20 @@ struct Elem<float> {
     f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
     f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
   }
+  // The bits of the largest magnitude: of the vector's and `top` in the type's own form
+  // (16-bit types two at a time), and that as a float's.
+  __device__ static uint32_t larger(const uint4& v, uint32_t top) {
+    top = __vimax3_u32(v.x & 0x7fffffffu, v.y & 0x7fffffffu, top);
+    return __vimax3_u32(v.z & 0x7fffffffu, v.w & 0x7fffffffu, top);
+  }
+  __device__ static uint32_t as_float(uint32_t top) { return top; }
 };
+// Of 16-bit types.
+__device__ __forceinline__ uint32_t larger2(const uint4& v, uint32_t top) {
+  top = __vimax3_u16x2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, top);
+  return __vimax3_u16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu, top);
+}
+__device__ __forceinline__ uint32_t halves_max(uint32_t top) { return max(top & 0xffffu, top >> 16); }
 template <>
 struct Elem<__nv_bfloat16> {
   __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -42,6 +55,8 @@ struct Elem<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  __device__ static uint32_t larger(const uint4& v, uint32_t top) { return larger2(v, top); }
+  __device__ static uint32_t as_float(uint32_t top) { return halves_max(top) << 16; }
 };
 template <>
 struct Elem<__half> {
@@ -55,6 +70,10 @@ struct Elem<__half> {
       f[2 * i + 1] = h.y;
     }
   }
+  __device__ static uint32_t larger(const uint4& v, uint32_t top) { return larger2(v, top); }
+  __device__ static uint32_t as_float(uint32_t top) {
+    return __float_as_uint(__half2float(__ushort_as_half(uint16_t(halves_max(top)))));
+  }
 };
 template <typename T>
 constexpr int kVec = 16 / int(sizeof(T));   // elements of a 16-byte load
@@ -62,9 +81,10 @@ constexpr int kVec = 16 / int(sizeof(T));   // elements of a 16-byte load
 __device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
 // A block's scale, from the bits of its largest magnitude: NaN if one element is not finite.
-// hi and lo: 2^-21 above and below 1 / s.  fp32(x / s) lies between x lo and x hi (each
-// product is within 2^-23 of its exact value), so where both give the same code there is no
-// need to divide: rounding is monotonic.  They differ for about one element in 2^17.
+// hi and lo: 2^-21 above and below 1 / s.  fp32(x / s) lies between x lo and x hi (the
+// reciprocal is within 2^-23 of its exact value, each product within 2^-24 of its own), so
+// where both give the same code there is no need to divide: rounding is monotonic.  They
+// differ for about one element in 2^17.
 struct BlockScale {
   float s, hi, lo;
   bool divide;      // a subnormal scale, whose reciprocal may overflow
@@ -73,7 +93,8 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t top) {
   BlockScale b;
   b.s = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __fdiv_rn(__uint_as_float(top), 448.0f);
   b.divide = b.s < 1.17549435e-38f;
-  const float inv = __fdiv_rn(1.0f, b.s);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(b.s));
   b.hi = inv * (1.0f + 4.76837158e-7f);
   b.lo = inv * (1.0f - 4.76837158e-7f);
   return b;
@@ -82,11 +103,26 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t top) {
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
+// Two products in one instruction.
+__device__ __forceinline__ float2 mul2(float a, float b, float by) {
+  float2 r;
+  asm("{\n\t.reg .b64 v, s;\n\t"
+      "mov.b64 v, {%2, %3};\n\t"
+      "mov.b64 s, {%4, %4};\n\t"
+      "mul.rn.f32x2 v, v, s;\n\t"
+      "mov.b64 {%0, %1}, v;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a), "f"(b), "f"(by));
+  return r;
+}
 // Four codes (a scale of 0 or NaN gives zeros).
 __device__ __forceinline__ uint32_t codes4(const float* f, const BlockScale& b) {
   if (!(b.s > 0.0f)) return 0u;
-  const uint32_t hi = e4m3x2(f[0] * b.hi, f[1] * b.hi) | (e4m3x2(f[2] * b.hi, f[3] * b.hi) << 16);
-  const uint32_t lo = e4m3x2(f[0] * b.lo, f[1] * b.lo) | (e4m3x2(f[2] * b.lo, f[3] * b.lo) << 16);
+  auto codes = [&](float by) {
+    const float2 a = mul2(f[0], f[1], by), c = mul2(f[2], f[3], by);
+    return e4m3x2(a.x, a.y) | (e4m3x2(c.x, c.y) << 16);
+  };
+  const uint32_t hi = codes(b.hi), lo = codes(b.lo);
   if (hi == lo && !b.divide) return hi;
   return e4m3x2(__fdiv_rn(f[0], b.s), __fdiv_rn(f[1], b.s)) | (e4m3x2(__fdiv_rn(f[2], b.s), __fdiv_rn(f[3], b.s)) << 16);
 }
@@ -94,13 +130,24 @@ __device__ __forceinline__ uint8_t code1(float f, const BlockScale& b) {
   return b.s > 0.0f ? uint8_t(e4m3x2(__fdiv_rn(f, b.s), 0.0f)) : uint8_t(0);
 }
 
+// The codes of a vector.
+template <typename T>
+__device__ __forceinline__ void put_codes(uint8_t* dst, const uint4& v, const BlockScale& b) {
+  float f[kVec<T>];
+  Elem<T>::unpack(v, f);
+  if constexpr (kVec<T> == 4) *reinterpret_cast<uint32_t*>(dst) = codes4(f, b);
+  else *reinterpret_cast<uint2*>(dst) = make_uint2(codes4(f, b), codes4(f + 4, b));
+}
+
 // ------------------------------------------------------------------ quantize
 
 constexpr int kQThreads = 256;
 
 // Blocks of one row, eight lanes a block and sixteen elements a lane (what a block costs
-// beside its elements, the scale above all, is shared by as many).  VEC: rows start on vector
-// boundaries; else element by element.
+// beside its elements, the scale above all, is shared by as many; four lanes were no faster).
+// The vectors stay as they were loaded until their codes are made.  4096 x 4096 takes 13.9 us
+// from 16-bit types (3.6 TB/s; issue is what bounds it), 14.6 from fp32 (5.8 TB/s).  VEC: rows
+// start on vector boundaries; else element by element.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kQThreads) fp8_rows_kernel(const T* __restrict__ x, int rows, int cols,
                                                              uint8_t* __restrict__ codes, float* __restrict__ scales) {
@@ -120,23 +167,24 @@ __global__ void __launch_bounds__(kQThreads) fp8_rows_kernel(const T* __restrict
     const int c0 = int(b - row * kb) * kFp8Block;
     const int n = b < blocks ? min(kFp8Block, cols - c0) : 0;
     const int64_t at = row * cols + c0;
-    float f[kMine];
+    uint4 v[VEC ? kLoads : 1];
+    float f[VEC ? V : kMine];
+    uint32_t top = 0;
     if (VEC) {
-      uint4 v[kLoads];
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int c = (i * kLanes + l) * V;
         v[i] = c < n ? __ldg(reinterpret_cast<const uint4*>(x + at + c)) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) Elem<T>::unpack(v[i], f + i * V);
+      for (int i = 0; i < kLoads; ++i) top = Elem<T>::larger(v[i], top);
+      top = Elem<T>::as_float(top);
     } else {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) f[i] = i * kLanes + l < n ? Elem<T>::one(x + at + i * kLanes + l) : 0.0f;
-    }
-    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) top = max(top, magnitude(f[i]));
+      for (int i = 0; i < kMine; ++i) top = max(top, magnitude(f[i]));
+    }
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const BlockScale s = block_scale(top);
@@ -145,16 +193,17 @@ __global__ void __launch_bounds__(kQThreads) fp8_rows_kernel(const T* __restrict
     for (int i = 0; i < kLoads; ++i) {
       const int c = (i * kLanes + l) * V;
       if (c >= n) continue;
-      if (V == 1) codes[at + c] = code1(f[i], s);
-      else if (V == 4) *reinterpret_cast<uint32_t*>(codes + at + c) = codes4(f + i * V, s);
-      else *reinterpret_cast<uint2*>(codes + at + c) = make_uint2(codes4(f + i * V, s), codes4(f + i * V + (V == 8 ? 4 : 0), s));
+      if constexpr (VEC) put_codes<T>(codes + at + c, v[i], s);
+      else codes[at + c] = code1(f[i], s);
     }
   }
 }
 
-// Blocks of 128 x 128, a CTA each, kept in registers between the maximum and the codes.
+// Blocks of 128 x 128, a CTA each, kept in registers between the maximum and the codes: three
+// CTAs an SM of fp32 (a third one took 11008 x 4096 from 46.5 to 38.4 us, 5.9 TB/s), four of
+// 16-bit types (30 us, 4.5 TB/s).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kQThreads) fp8_tile_kernel(const T* __restrict__ x, int rows, int cols, int kb,
+__global__ void __launch_bounds__(kQThreads, VEC ? (sizeof(T) == 4 ? 3 : 4) : 2) fp8_tile_kernel(const T* __restrict__ x, int rows, int cols, int kb,
                                                              uint8_t* __restrict__ codes, float* __restrict__ scales) {
   constexpr int V = VEC ? kVec<T> : 4;
   constexpr int kPer = kFp8Block / V;                        // vectors of a row
@@ -164,10 +213,10 @@ __global__ void __launch_bounds__(kQThreads) fp8_tile_kernel(const T* __restrict
   const int64_t r0 = int64_t(br) * kFp8Block;
   const int c0 = bc * kFp8Block;
   const int t = threadIdx.x;
-  float f[kKeep][V];
+  uint4 v[VEC ? kKeep : 1];
+  float f[VEC ? 1 : kKeep][V];
   uint32_t top = 0;
   if (VEC) {
-    uint4 v[kKeep];
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) {
       const int at = t + i * kQThreads, c = c0 + at % kPer * V;
@@ -175,7 +224,8 @@ __global__ void __launch_bounds__(kQThreads) fp8_tile_kernel(const T* __restrict
       v[i] = r < rows && c < cols ? __ldg(reinterpret_cast<const uint4*>(x + r * cols + c)) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i) Elem<T>::unpack(v[i], f[i]);
+    for (int i = 0; i < kKeep; ++i) top = Elem<T>::larger(v[i], top);
+    top = Elem<T>::as_float(top);
   } else {
 #pragma unroll
     for (int i = 0; i < kKeep; ++i)
@@ -184,12 +234,9 @@ __global__ void __launch_bounds__(kQThreads) fp8_tile_kernel(const T* __restrict
         const int at = t + (i * V + j) * kQThreads, c = c0 + at % kFp8Block;
         const int64_t r = r0 + at / kFp8Block;
         f[i][j] = r < rows && c < cols ? Elem<T>::one(x + r * cols + c) : 0.0f;
+        top = max(top, magnitude(f[i][j]));
       }
   }
-#pragma unroll
-  for (int i = 0; i < kKeep; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) top = max(top, magnitude(f[i][j]));
   __shared__ uint32_t part[kQThreads / 32];
   top = __reduce_max_sync(0xffffffffu, top);
   if ((t & 31) == 0) part[t >> 5] = top;
@@ -200,14 +247,10 @@ __global__ void __launch_bounds__(kQThreads) fp8_tile_kernel(const T* __restrict
   if (t == 0) scales[blockIdx.x] = s.s;
 #pragma unroll
   for (int i = 0; i < kKeep; ++i) {
-    if (VEC) {
+    if constexpr (VEC) {
       const int at = t + i * kQThreads, c = c0 + at % kPer * V;
       const int64_t r = r0 + at / kPer;
-      if (r < rows && c < cols) {
-        uint8_t* dst = codes + r * cols + c;
-        if (V == 4) *reinterpret_cast<uint32_t*>(dst) = codes4(f[i], s);
-        else *reinterpret_cast<uint2*>(dst) = make_uint2(codes4(f[i], s), codes4(f[i] + (V == 8 ? 4 : 0), s));
-      }
+      if (r < rows && c < cols) put_codes<T>(codes + r * cols + c, v[i], s);
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -262,12 +305,13 @@ __device__ __forceinline__ float2 values2(uint32_t two) {
   return __half22float2(__half2(h));
 }
 
-// VEC: eight codes a thread, in one row (the row length is a multiple of eight).
-template <typename T, bool VEC>
+// V codes a thread, in one row (the row length is a multiple of V): 16 bytes of results, so
+// that a warp writes whole lines (16 codes a thread: 51 us against 46 for 11008 x 4096 in
+// fp32, 4.9 TB/s, most of it writes).
+template <typename T, int V>
 __global__ void __launch_bounds__(kQThreads) fp8_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                    const float* __restrict__ scales, int64_t rows, int cols,
                                                                    int row_shift, T* __restrict__ out) {
-  constexpr int V = VEC ? 8 : 1;
   grid_dep_wait();
   const int kb = (cols + kFp8Block - 1) / kFp8Block, per = cols / V;
   const int64_t total = rows * per;
@@ -275,15 +319,16 @@ __global__ void __launch_bounds__(kQThreads) fp8_dequantize_kernel(const uint8_t
     const int64_t row = i / per;
     const int c = int(i - row * per) * V;
     const float s = __ldg(scales + (row >> row_shift) * kb + c / kFp8Block);
-    if (VEC) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes) + i);
-      const uint32_t two[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+    if constexpr (V > 1) {
+      uint32_t w[V / 4];
+      if constexpr (V == 4) w[0] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
+      else *reinterpret_cast<uint2*>(w) = __ldg(reinterpret_cast<const uint2*>(codes) + i);
       alignas(16) T v[V];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = values2(two[j]);
-        put(&v[(2 * j) % V], __fmul_rn(f.x, s));
-        put(&v[(2 * j + 1) % V], __fmul_rn(f.y, s));
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 f = values2((w[j / 2] >> (16 * (j & 1))) & 0xffffu);
+        put(&v[2 * j], __fmul_rn(f.x, s));
+        put(&v[2 * j + 1], __fmul_rn(f.y, s));
       }
       uint4* o = reinterpret_cast<uint4*>(out + i * V);
 #pragma unroll
@@ -297,16 +342,17 @@ __global__ void __launch_bounds__(kQThreads) fp8_dequantize_kernel(const uint8_t
 template <typename T>
 cudaError_t dequantize_t(const uint8_t* codes, const float* scales, int64_t rows, int64_t cols, int block_rows, void* out,
                          int sms, cudaStream_t st) {
-  const bool vec = cols % 8 == 0;
-  const int64_t work = rows * cols / (vec ? 8 : 1);
+  constexpr int V = kVec<T>;
+  const bool vec = cols % V == 0;
+  const int64_t work = rows * cols / (vec ? V : 1);
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   pdl_config(&cfg, attr, unsigned(std::max<int64_t>(1, std::min<int64_t>((work + kQThreads - 1) / kQThreads, int64_t(sms) * 32))),
              kQThreads, st);
   const int shift = block_rows == 1 ? 0 : 7;
   T* o = static_cast<T*>(out);
-  return vec ? cudaLaunchKernelEx(&cfg, fp8_dequantize_kernel<T, true>, codes, scales, rows, int(cols), shift, o)
-             : cudaLaunchKernelEx(&cfg, fp8_dequantize_kernel<T, false>, codes, scales, rows, int(cols), shift, o);
+  return vec ? cudaLaunchKernelEx(&cfg, fp8_dequantize_kernel<T, V>, codes, scales, rows, int(cols), shift, o)
+             : cudaLaunchKernelEx(&cfg, fp8_dequantize_kernel<T, 1>, codes, scales, rows, int(cols), shift, o);
 }
 
 // ------------------------------------------------------------------ linear, few tokens
