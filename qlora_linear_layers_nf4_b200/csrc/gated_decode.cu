@@ -13,8 +13,8 @@
 // token: half and half 77 us, a quarter 72, an eighth 73, none 76.5); the adapters' products
 // are two MMAs, T_0 with the up rows zero and T_1 with the gate rows zero.
 //
-// Bound by decoding: about four instructions a weight on issue, the byte-permute pipe and
-// shared memory, each half to two thirds busy.  Two weights of 11008 x 4096 (47 MB) take 27 us
+// Bound by decoding: four instructions a weight; at 44032 x 4096 shared memory is 73 % busy, the
+// byte-permute pipe 58 %, issue 57 %, DRAM 31 %.  Two weights of 11008 x 4096 (47 MB) take 27 us
 // with one token (1.7 TB/s), 34 with 16, of which 12 are start, T and the join of split tiles;
 // the rest grows by 15 us (one token) to 19 (16 tokens) for each such pair of weights.
 #include <algorithm>
