@@ -1,7 +1,7 @@
 // Gated feed-forward layer on the CUDA cores: the fp32 mode, where every product and sum is an
 // fp32 operation.
 //
-// One kernel does every product of both projections z (a grid dimension):
+// One kernel does every product of both projections z:
 //     C_z(i, j) = alpha sum over up to four segments of a(i, kk) b(j, kk)
 // with each operand a dense matrix in either major order or a projection's NF4 weight decoded
 // on load; a second form keeps the sums of both projections and finishes h = act(g) u.
@@ -10,7 +10,8 @@
 // slice's products are summed by themselves before they are added to the others.  What a
 // slice takes is the latency of few warps, so where there are few tiles a cluster of CTAs
 // shares a tile's slices and sums its parts through distributed shared memory in their order:
-// the backward of 301 rows, 512 x 512 and r = 8, six launches, went from 96 to 55 us.
+// the backward of 301 rows, 512 x 512 and r = 8 went from 96 to 55 us, and to 45 with U and dB,
+// and dA and dx, in one launch each.
 #include <algorithm>
 
 #include <cuda_runtime.h>
@@ -72,8 +73,16 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
   return v;
 }
 
+// Two products in one launch, where neither reads the other's result: the first one's tiles,
+// then the second one's.
+struct SimtPair {
+  SimtParams p[2];
+  int tiles[2];          // of one z
+  int blocks0;           // of the first, all z
+};
+
 template <int T, bool GATED>
-__global__ void __launch_bounds__(kSThreads, 2) gated_simt_kernel(const SimtParams p) {
+__global__ void __launch_bounds__(kSThreads, 2) gated_simt_kernel(const __grid_constant__ SimtPair pair) {
   constexpr int kRow = T + 4;
   constexpr int kLoads = T * kSK / 4 / kSThreads;      // runs of four a thread, per operand and slice
   // A thread has 4 x 4 results, so that eight values read from shared memory feed 16 FMAs (2 x 2
@@ -87,8 +96,11 @@ __global__ void __launch_bounds__(kSThreads, 2) gated_simt_kernel(const SimtPara
   const int t = threadIdx.x;
   if (t < 16) lut[t] = level(t);
   __syncthreads();
-  const int64_t j0 = int64_t(blockIdx.x % p.col_tiles) * T, i0 = int64_t(blockIdx.x / p.col_tiles) * T;
-  const int z = blockIdx.z;
+  const int which = !GATED && int(blockIdx.x) >= pair.blocks0 ? 1 : 0;
+  const SimtParams& p = pair.p[which];
+  const int block = int(blockIdx.x) - (which ? pair.blocks0 : 0);
+  const int z = block / pair.tiles[which], tile = block - z * pair.tiles[which];
+  const int64_t j0 = int64_t(tile % p.col_tiles) * T, i0 = int64_t(tile / p.col_tiles) * T;
 
   // Run l of a slice.  kmajor: index = (t + 256 l) / 8, kk = 4 (t % 8) ..; else kk, then index.
   struct Runs {
@@ -327,34 +339,50 @@ int64_t slices_of(const Launch& l) {
   for (int g = 0; g < (l.gated ? 4 : l.p.nseg); ++g) most = std::max(most, (l.p.seg[g].kdim + kSK - 1) / kSK);
   return most;
 }
-int64_t tiles_of(const Launch& l, int64_t t) { return (l.p.rows + t - 1) / t * ((l.p.cols + t - 1) / t) * l.zs; }
+int64_t col_tiles(const Launch& l, int64_t t) { return (l.p.cols + t - 1) / t; }
+int64_t tiles_of(const Launch& l, int64_t t) { return (l.p.rows + t - 1) / t * col_tiles(l, t); }
 
 // Parts of a tile's slices: a power of two (clusters of seven waited for each other: 68 us
 // against 55 for the backward of 301 rows, 512 x 512), such that all run at once at two CTAs
 // an SM, an eighth of them left to the GPCs' remainders, and two slices a part at least.
-int64_t parts_of(const Launch& l, int64_t tiles, int sms) {
+int64_t parts_of(int64_t slices, int64_t tiles, int sms) {
   int64_t parts = 1;
-  while (parts < kSMaxCluster && 2 * parts * tiles <= 2 * int64_t(sms) * 7 / 8 && slices_of(l) >= 4 * parts) parts *= 2;
+  while (parts < kSMaxCluster && 2 * parts * tiles <= 2 * int64_t(sms) * 7 / 8 && slices >= 4 * parts) parts *= 2;
   return parts;
 }
 
-// 64 x 64 tiles, which take half of the instructions a product, where their parts are enough
-// for the SMs.
-bool large_tiles(const Launch& l, int sms) {
-  const int64_t tiles = tiles_of(l, 64);
-  return l.p.rows > 32 && l.p.cols > 32 && tiles * parts_of(l, tiles, sms) >= sms;
-}
+// The tiles are counted in 32 bits (those of both products of a launch together).
+bool fits(const Launch& l) { return tiles_of(l, 32) * l.zs <= int64_t(0x3fffffff); }
 
-bool fits(const Launch& l) { return (l.p.rows + 31) / 32 * ((l.p.cols + 31) / 32) <= int64_t(0x7fffffff); }
-
-cudaError_t run(Launch l, int sms, cudaStream_t st, int* launches) {
-  const bool large = large_tiles(l, sms);
-  const int64_t t = large ? 64 : 32;
-  const int64_t ct = (l.p.cols + t - 1) / t, rt = (l.p.rows + t - 1) / t;
-  l.p.col_tiles = int(ct);
-  const int64_t parts = parts_of(l, ct * rt * l.zs, sms);
+// One product, or two that do not read each other's results.
+cudaError_t run(const Launch& a, const Launch* b, int sms, cudaStream_t st, int* launches) {
+  const Launch* l[2] = {&a, b};
+  const int n = b != nullptr ? 2 : 1;
+  int64_t blocks[2], slices = 0;
+  auto count = [&](int64_t t) {   // CTAs of one part
+    int64_t all = 0;
+    for (int i = 0; i < n; ++i) all += blocks[i] = tiles_of(*l[i], t) * l[i]->zs;
+    return all;
+  };
+  bool narrow = true;
+  for (int i = 0; i < n; ++i) {
+    slices = std::max(slices, slices_of(*l[i]));
+    narrow = narrow && (l[i]->p.rows <= 32 || l[i]->p.cols <= 32);
+  }
+  // 64 x 64 tiles, which take half of the instructions a product, where their parts are enough
+  // for the SMs.
+  const int64_t wide = count(64);
+  const bool large = !narrow && wide * parts_of(slices, wide, sms) >= sms;
+  const int64_t t = large ? 64 : 32, all = count(t), parts = parts_of(slices, all, sms);
+  SimtPair pair{};
+  for (int i = 0; i < n; ++i) {
+    pair.p[i] = l[i]->p;
+    pair.p[i].col_tiles = int(col_tiles(*l[i], t));
+    pair.tiles[i] = int(tiles_of(*l[i], t));
+  }
+  pair.blocks0 = int(blocks[0]);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(ct * rt), unsigned(parts), unsigned(l.zs));
+  cfg.gridDim = dim3(unsigned(all), unsigned(parts), 1);
   cfg.blockDim = dim3(kSThreads, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -364,11 +392,11 @@ cudaError_t run(Launch l, int sms, cudaStream_t st, int* launches) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  NF4_PROF_BEGIN(st, l.id);
+  NF4_PROF_BEGIN(st, a.id);
   cudaError_t e;
-  if (l.gated) e = large ? cudaLaunchKernelEx(&cfg, gated_simt_kernel<64, true>, l.p) : cudaLaunchKernelEx(&cfg, gated_simt_kernel<32, true>, l.p);
-  else e = large ? cudaLaunchKernelEx(&cfg, gated_simt_kernel<64, false>, l.p) : cudaLaunchKernelEx(&cfg, gated_simt_kernel<32, false>, l.p);
-  NF4_PROF_END(st, l.id);
+  if (a.gated) e = large ? cudaLaunchKernelEx(&cfg, gated_simt_kernel<64, true>, pair) : cudaLaunchKernelEx(&cfg, gated_simt_kernel<32, true>, pair);
+  else e = large ? cudaLaunchKernelEx(&cfg, gated_simt_kernel<64, false>, pair) : cudaLaunchKernelEx(&cfg, gated_simt_kernel<32, false>, pair);
+  NF4_PROF_END(st, a.id);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess) ++*launches;
   return e;
@@ -409,8 +437,8 @@ cudaError_t launch_gated_fwd_f32(const GatedArgs& a, int sms, cudaStream_t st, i
   h.p.bias = static_cast<const float*>(a.bias);
   h.p.pre = static_cast<float*>(a.pre_out);
   if (!fits(t) || !fits(h)) return cudaErrorInvalidValue;
-  const cudaError_t e = run(t, sms, st, launches);
-  return e == cudaSuccess ? run(h, sms, st, launches) : e;
+  const cudaError_t e = run(t, nullptr, sms, st, launches);
+  return e == cudaSuccess ? run(h, nullptr, sms, st, launches) : e;
 }
 
 cudaError_t launch_gated_bwd_f32(const GatedArgs& a, int sms, cudaStream_t st, int* launches) {
@@ -419,59 +447,56 @@ cudaError_t launch_gated_bwd_f32(const GatedArgs& a, int sms, cudaStream_t st, i
   float* d = reinterpret_cast<float*>(ws + 2 * t_bytes(a.M, a.r));
   const float* T = a.t_in != nullptr ? static_cast<const float*>(a.t_in) : reinterpret_cast<const float*>(ws);
   const int64_t mn = a.M * a.N, mr = a.M * a.r;
-  Launch l[5];
-  int n = 0;
-  if (a.t_in == nullptr) l[n++] = product_T(a, ws);
+  const bool with_t = a.t_in == nullptr, with_dx = a.dx != nullptr;
+  const Launch t = product_T(a, ws);
+  Launch u{}, db{}, da{}, dx{};
   {  // U_z = s d_z B_z
-    Launch u{common(a), 2, kKGatedU, false};
+    u = Launch{common(a), 2, kKGatedU, false};
     u.p.nseg = 1;
     u.p.seg[0] = SimtSegment{dense(d, a.N, true, a.M, mn), dense(a.B, a.r, false, a.r, a.N * a.r), a.N};
     u.p.rows = a.M;
     u.p.cols = a.r;
     u.p.c = U;
     u.p.alpha = a.s;
-    l[n++] = u;
   }
   {  // dB_z = d_z^T T_z
-    Launch b{common(a), 2, kKGatedDB, false};
-    b.p.nseg = 1;
-    b.p.seg[0] = SimtSegment{dense(d, a.N, false, a.N, mn), dense(T, a.r, false, a.r, mr), a.M};
-    b.p.rows = a.N;
-    b.p.cols = a.r;
-    b.p.c = a.dB;
-    l[n++] = b;
+    db = Launch{common(a), 2, kKGatedDB, false};
+    db.p.nseg = 1;
+    db.p.seg[0] = SimtSegment{dense(d, a.N, false, a.N, mn), dense(T, a.r, false, a.r, mr), a.M};
+    db.p.rows = a.N;
+    db.p.cols = a.r;
+    db.p.c = a.dB;
   }
   {  // dA_z = U_z^T x
-    Launch b{common(a), 2, kKGatedDA, false};
-    b.p.nseg = 1;
-    b.p.seg[0] = SimtSegment{dense(U, a.r, false, a.r, mr), dense(a.x, a.K, false, a.K, 0), a.M};
-    b.p.rows = a.r;
-    b.p.cols = a.K;
-    b.p.c = a.dA;
-    l[n++] = b;
+    da = Launch{common(a), 2, kKGatedDA, false};
+    da.p.nseg = 1;
+    da.p.seg[0] = SimtSegment{dense(U, a.r, false, a.r, mr), dense(a.x, a.K, false, a.K, 0), a.M};
+    da.p.rows = a.r;
+    da.p.cols = a.K;
+    da.p.c = a.dA;
   }
-  if (a.dx != nullptr) {  // dx = sum_z d_z W'_z + U_z A_z
-    Launch x{common(a), 1, kKGatedDx, false};
-    x.p.nseg = 4;
+  if (with_dx) {  // dx = sum_z d_z W'_z + U_z A_z
+    dx = Launch{common(a), 1, kKGatedDx, false};
+    dx.p.nseg = 4;
     for (int z = 0; z < 2; ++z) {
-      x.p.seg[z] = SimtSegment{dense(d + z * mn, a.N, true, a.M, 0), weight(z, a.K, false, a.K), a.N};
-      x.p.seg[2 + z] = SimtSegment{dense(U + z * mr, a.r, true, a.M, 0),
-                                   dense(static_cast<const float*>(a.A) + int64_t(z) * a.r * a.K, a.K, false, a.K, 0), a.r};
+      dx.p.seg[z] = SimtSegment{dense(d + z * mn, a.N, true, a.M, 0), weight(z, a.K, false, a.K), a.N};
+      dx.p.seg[2 + z] = SimtSegment{dense(U + z * mr, a.r, true, a.M, 0),
+                                    dense(static_cast<const float*>(a.A) + int64_t(z) * a.r * a.K, a.K, false, a.K, 0), a.r};
     }
-    x.p.rows = a.M;
-    x.p.cols = a.K;
-    x.p.c = static_cast<float*>(a.dx);
-    l[n++] = x;
+    dx.p.rows = a.M;
+    dx.p.cols = a.K;
+    dx.p.c = static_cast<float*>(a.dx);
   }
-  for (int i = 0; i < n; ++i)
-    if (!fits(l[i])) return cudaErrorInvalidValue;
+  if (!fits(t) || !fits(u) || !fits(db) || !fits(da) || (with_dx && !fits(dx))) return cudaErrorInvalidValue;
   NF4_PROF_BEGIN(st, kKGatedAct);
   gated_grad_f32_kernel<<<unsigned(std::max<int64_t>(1, std::min<int64_t>((mn + kSThreads - 1) / kSThreads, int64_t(sms) * 8))), kSThreads, 0, st>>>(
       static_cast<const float*>(a.dh), static_cast<const float*>(a.pre_in), d, mn, a.act);
   NF4_PROF_END(st, kKGatedAct);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) ++*launches;
-  for (int i = 0; i < n && e == cudaSuccess; ++i) e = run(l[i], sms, st, launches);
+  if (e == cudaSuccess && with_t) e = run(t, nullptr, sms, st, launches);
+  if (e == cudaSuccess) e = run(u, &db, sms, st, launches);
+  if (e == cudaSuccess) e = with_dx ? run(dx, &da, sms, st, launches) : run(da, nullptr, sms, st, launches);
   return e;
 }
 
