@@ -728,10 +728,14 @@ bool ad_map(CUtensorMap* map, const void* ad, uint64_t r, uint64_t M, uint64_t t
 // slow (dx of 100 tokens, 4000 x 2048: 8 tiles of 127 steps, 65 us; with splits the forward of
 // 64 tokens, 1000 x 4096, takes 19 us against 35, of 300, 512 x 8192, 33 against 68).  Eight
 // steps a split at least, and none of fewer than 24 (333 tokens, 1032 x 1088: 22.4 against 21.9).
-int splits_of(int64_t tiles, int steps, int sms) {
+// dx keeps to two thirds of the SMs, and leaves the others to dB and dA beside it, unless it is
+// long itself, 20 steps for every pair (100 tokens, 4000 x 2048, 8 tiles of 126 steps: 6 splits
+// 39 us, 9 splits 45; 16 tokens, 4096 x 4096, 16 tiles of 130: 3 splits 46 us, 4 splits 42).
+int splits_of(bool backward, int64_t tiles, int steps, int sms) {
   if (steps < 24) return 1;
   const int64_t pairs = std::min(std::max(sms / 2, 1), kGatedMaxPairs);
-  return int(std::max<int64_t>(1, std::min<int64_t>(pairs / tiles, steps / 8)));
+  const int64_t most = backward && steps * tiles < 20 * pairs ? ((sms + 2) / 3 + tiles / 2) / tiles : pairs;
+  return int(std::max<int64_t>(1, std::min<int64_t>({most, pairs / tiles, steps / 8})));
 }
 
 }  // namespace
@@ -782,7 +786,7 @@ bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, cons
   p.ad_steps = (a.r + 63) / 64;
   p.col_tiles = int(col_tiles);
   p.row_tiles = int(cdiv(a.M, int64_t(parts) * kPartT));
-  p.splits = parts == 2 ? 1 : splits_of(int64_t(p.row_tiles) * p.col_tiles, p.main_steps + 2 * p.ad_steps, sms);
+  p.splits = parts == 2 ? 1 : splits_of(backward, int64_t(p.row_tiles) * p.col_tiles, p.main_steps + 2 * p.ad_steps, sms);
   // Forward: CTA pairs left over take tiles of fewer tokens, whose MMAs and epilogue are shorter
   // (333 tokens, 1032 x 1088: 21.4 -> 17.0 us; 256, 512 x 512: 18.3 -> 12.4).  Beside dx, dB and
   // dA run on them (with smaller tiles the backward of 512 tokens, 1024 x 1024, took 39 us, not 32).
