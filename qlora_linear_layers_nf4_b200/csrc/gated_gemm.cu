@@ -723,32 +723,57 @@ bool ad_map(CUtensorMap* map, const void* ad, uint64_t r, uint64_t M, uint64_t t
 }
 
 
-// Splits of the reduction where the tiles leave at least half of the CTA pairs idle: a step
-// costs the decoding of its weights whatever the tokens, so few tiles with many steps are
-// slow (dx of 100 tokens, 4000 x 2048: 8 tiles of 127 steps, 65 us; with splits the forward of
-// 64 tokens, 1000 x 4096, takes 19 us against 35, of 300, 512 x 8192, 33 against 68).  Eight
-// steps a split at least, and none of fewer than 24 (333 tokens, 1032 x 1088: 22.4 against 21.9).
-// dx keeps to two thirds of the SMs, and leaves the others to dB and dA beside it, unless it is
-// long itself, 20 steps for every pair (100 tokens, 4000 x 2048, 8 tiles of 126 steps: 6 splits
-// 39 us, 9 splits 45; 16 tokens, 4096 x 4096, 16 tiles of 130: 3 splits 46 us, 4 splits 42).
-int splits_of(bool backward, int64_t tiles, int steps, int sms) {
+// Splits of a reduction: a step costs the decoding of its weights whatever the tokens, so few
+// tiles with many steps are slow (dx of 100 tokens, 4000 x 2048: 8 tiles of 127 steps, 65 us).
+// Eight steps a split at least, and none of fewer than 24 (333 tokens, 1032 x 1088: 22.4 against
+// 21.9).
+
+// dx fills the pairs that its tiles leave idle, if those are half or more.  It keeps to two
+// thirds of the SMs, and leaves the others to dB and dA beside it, unless it is long itself, 20
+// steps for every pair (100 tokens, 4000 x 2048, 8 tiles of 126 steps: 6 splits 39 us, 9 splits
+// 45; 16 tokens, 4096 x 4096, 16 tiles of 130: 3 splits 46 us, 4 splits 42).
+int dx_splits(int64_t tiles, int steps, int sms) {
   if (steps < 24) return 1;
   const int64_t pairs = std::min(std::max(sms / 2, 1), kGatedMaxPairs);
-  const int64_t most = backward && steps * tiles < 20 * pairs ? ((sms + 2) / 3 + tiles / 2) / tiles : pairs;
+  const int64_t most = steps * tiles < 20 * pairs ? ((sms + 2) / 3 + tiles / 2) / tiles : pairs;
   return int(std::max<int64_t>(1, std::min<int64_t>({most, pairs / tiles, steps / 8})));
+}
+
+// The forward takes what costs least by these measured parts, in ns: 460 a step, 1,000 a tile,
+// 3,500 for the launch that adds the splits up, and their sums written and read at 5 TB/s
+// (64 tokens, 1000 x 4096, 8 tiles: 35 us, with 8 splits 17; 11008 x 4096, 86 tiles on 74 pairs:
+// 67 us, with 3 splits 55; 14336 x 4096, 112 tiles: 68 us, with 2 to 5 splits 67 to 72).
+constexpr int kMaxFwdSplits = 16;
+constexpr size_t kMaxFwdSums = size_t(40) << 20;
+size_t fwd_sums(int64_t splits, int64_t M, int64_t N) { return size_t(splits) * size_t(M) * size_t(2 * N) * sizeof(float); }
+int fwd_splits(int64_t M, int64_t N, int64_t tiles, int steps, int sms) {
+  if (steps < 24) return 1;
+  const int64_t pairs = std::max(sms / 2, 1);
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= kMaxFwdSplits && (s == 1 || (steps / s >= 8 && fwd_sums(s, M, N) <= kMaxFwdSums)); ++s) {
+    const int64_t sums = s > 1 ? 3500 + int64_t(2 * fwd_sums(s, M, N) / 5000) : 0;
+    const int64_t cost = cdiv(tiles * s, pairs) * (cdiv(steps, s) * 460 + 1000) + sums;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
-// Splits' sums, fp32: [split][M][K] or, forward, [split][M][2][N].  More rows make more tiles
-// and so fewer splits: the size is the largest of any number of rows up to M, so that a
+// Splits' sums, fp32: [split][M][K] or, forward, [split][M][2][N].  In dx more rows make more
+// tiles and so fewer splits: the size is the largest of any number of rows up to M, so that a
 // workspace for M serves fewer.
 size_t gated_split_bytes(bool backward, int64_t M, int64_t N, int64_t K) {
-  const int64_t col_tiles = backward ? cdiv(K, tile_w(kDx)) : cdiv(N, tile_w(kFwd));
+  if (!backward) return std::min(kMaxFwdSums, fwd_sums(kMaxFwdSplits, M, N));
+  const int64_t col_tiles = cdiv(K, tile_w(kDx));
   int64_t rows = 0;
   for (int64_t m_tiles = 1; (m_tiles - 1) * kPartT < M && 2 * m_tiles * col_tiles <= kGatedMaxPairs; ++m_tiles)
     rows = std::max(rows, kGatedMaxPairs / (m_tiles * col_tiles) * std::min(M, m_tiles * kPartT));
-  return size_t(rows) * size_t(backward ? K : 2 * N) * sizeof(float);
+  return size_t(rows) * size_t(K) * sizeof(float);
 }
 
 bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, const void* ad, void* scratch, int sms) {
@@ -786,7 +811,9 @@ bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, cons
   p.ad_steps = (a.r + 63) / 64;
   p.col_tiles = int(col_tiles);
   p.row_tiles = int(cdiv(a.M, int64_t(parts) * kPartT));
-  p.splits = parts == 2 ? 1 : splits_of(backward, int64_t(p.row_tiles) * p.col_tiles, p.main_steps + 2 * p.ad_steps, sms);
+  const int64_t tiles256 = int64_t(p.row_tiles) * p.col_tiles;
+  const int steps = p.main_steps + 2 * p.ad_steps;
+  p.splits = parts == 2 ? 1 : backward ? dx_splits(tiles256, steps, sms) : fwd_splits(a.M, a.N, tiles256, steps, sms);
   // Forward: CTA pairs left over take tiles of fewer tokens, whose MMAs and epilogue are shorter
   // (333 tokens, 1032 x 1088: 21.4 -> 17.0 us; 256, 512 x 512: 18.3 -> 12.4).  Beside dx, dB and
   // dA run on them (with smaller tiles the backward of 512 tokens, 1024 x 1024, took 39 us, not 32).
