@@ -16,9 +16,9 @@ size_t mr_bytes(int64_t M, int r, size_t size) { return align256(size_t(M) * siz
 size_t pair_bytes(int64_t M, int64_t N, size_t size) { return align256(2 * size_t(M) * size_t(N) * size); }
 
 // Few tokens: stream the weights (16 tokens a pass) instead of feeding the GEMM.  Measured, this
-// against the GEMM, us: 11008 x 4096 with 1, 16, 32, 40 and 64 tokens 29, 35, 55, 74 and 94 against
-// 65 to 68; 512 x 512 with 8 and 32 9.7 and 11.4 against 11.5; 1000 x 4096 with 32 23 against 35;
-// 4096 x 1024 with 32 16.6 against 15.1.
+// against the GEMM, us: 11008 x 4096 with 1, 16, 17 and 32 tokens 27, 33, 51 and 52 against 53 to
+// 58; 4096 x 4096 with 16 and 32 18 and 28 against 24 and 25; 1000 x 4096 with 1 and 32 10.6 and
+// 15.1 against 16.5; 4096 x 1024 with 16 12.3 against 15.1.
 bool use_decode(int64_t M) { return M <= 32; }
 
 }  // namespace
