@@ -6,7 +6,8 @@
 //
 // The kernel is the expert layer's weight-streaming one (expert_decode.cu) with tiles that
 // hold 64 outputs of both projections: 128 weight rows, a unit of work 256 columns of them
-// (16 KB of codes), an equal share of the units for every SM (or, of few tiles, every tile).  A warp takes 8 gate rows as the
+// (16 KB of codes); every SM has the same number of whole tiles, and before them a share of
+// the tiles that are left over.  A warp takes 8 gate rows as the
 // MMA rows 0 .. 7 and the same 8 up rows as 8 .. 15, so a thread that finishes a gate row has
 // the up row of its output in the next lane.  A quarter of the weights, half of the gate's,
 // are decoded with byte permutes, the others with shared-memory lookups (44032 x 4096 and one
@@ -14,8 +15,9 @@
 // are two MMAs, T_0 with the up rows zero and T_1 with the gate rows zero.
 //
 // Bound by decoding: four instructions a weight; at 44032 x 4096 shared memory is 73 % busy, the
-// byte-permute pipe 58 %, issue 57 %, DRAM 31 %.  Two weights of 11008 x 4096 (47 MB) take 27 us
-// with one token (1.7 TB/s), 34 with 16, of which 12 are start, T and the join of split tiles;
+// byte-permute pipe 58 %, issue 57 %, DRAM 31 %.  Two weights of 11008 x 4096 (47 MB) take 24 us
+// with one token (1.9 TB/s), 31 with 16, of which 9 are start and T (equal shares of all units,
+// with the join of split tiles at their end: 27 and 33);
 // the rest grows by 15 us (one token) to 19 (16 tokens) for each such pair of weights.
 #include <algorithm>
 
@@ -137,25 +139,43 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   }
   __syncthreads();
 
-  // Shares: CTA c of G takes units [units c / G, units (c + 1) / G).  G counts the
-  // CTAs with work, at least one unit each.
+  // Work of a CTA: a share of the first `rest` tiles, then `whole` tiles of its own.  Of those
+  // first tiles CTA c of G takes units [units c / G, units (c + 1) / G); tiles that so fall to
+  // several CTAs are joined while their last contributor's own tiles still run.
   const uint32_t kch = uint32_t(p.k_chunks);
-  const uint32_t units = uint32_t(p.row_tiles) * uint32_t(p.n_tiles) * kch;   // < 2^31
-  const uint32_t G = min(gridDim.x, units);
-  const bool works = blockIdx.x < G;
-  const uint32_t u0 = works ? uint32_t(uint64_t(units) * blockIdx.x / G) : 0u;
-  const uint32_t u1 = works ? uint32_t(uint64_t(units) * (blockIdx.x + 1) / G) : 0u;
-  const uint32_t tile0 = u0 / kch;
-  const int kc0 = int(u0 - tile0 * kch);             // the share's first chunk of its first tile
+  const uint32_t units = uint32_t(p.rest) * kch;     // < 2^31, as all tiles' units are
+  const uint32_t G = uint32_t(p.rest_ctas);
+  const bool shares = blockIdx.x < G;
+  const uint32_t share0 = shares ? uint32_t(uint64_t(units) * blockIdx.x / G) : 0u;
+  const uint32_t share1 = shares ? uint32_t(uint64_t(units) * (blockIdx.x + 1) / G) : 0u;
+  const uint32_t own0 = (uint32_t(p.rest) + blockIdx.x * uint32_t(p.whole)) * kch, own1 = own0 + uint32_t(p.whole) * kch;
+  struct Range {
+    uint32_t u0, u1, tile0;
+    int kc0;      // the range's first chunk of its first tile
+    int group0;   // the group that takes its first unit: groups take a CTA's units in turn
+  };
+  auto range_at = [&](int i) {
+    Range r;
+    r.u0 = i ? own0 : share0;
+    r.u1 = i ? own1 : share1;
+    r.tile0 = r.u0 / kch;
+    r.kc0 = int(r.u0 - r.tile0 * kch);
+    r.group0 = i ? int((share1 - share0) % kGroups) : 0;
+    return r;
+  };
 
   if (warp == kProducer) {
     // ---------------- producer
-    if (u0 < u1) {
-      DcTile t = dc_tile(p.n_tiles, tile0);
-      int kc = kc0, s = 0, issued = 0;
-      uint32_t ph = 1;
-      for (uint32_t u = u0; u < u1; ++u) {
-        if (!warp_wait(&sh->empty[s], ph, abort_flag, p.status)) break;
+    int s = 0, issued = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int i = 0; i < 2 && ok; ++i) {
+      const Range r = range_at(i);
+      DcTile t = dc_tile(p.n_tiles, r.tile0);
+      int kc = r.kc0;
+      for (uint32_t u = r.u0; u < r.u1; ++u) {
+        ok = warp_wait(&sh->empty[s], ph, abort_flag, p.status);
+        if (!ok) break;
         if (lane == 0) {
           uint8_t* dst = smem + s * dc_stage_bytes(NP);
           mbar_arrive_expect_tx(&sh->full[s], dc_stage_bytes(NP));
@@ -174,12 +194,12 @@ __global__ void __launch_bounds__(kDcThreads, 1)
           ph ^= 1;
         }
       }
-      if (*abort_flag)   // unwind: wait (bounded) for the boxes in flight
-        for (int j = max(0, issued - kStages); j < issued; ++j) {
-          uint32_t none = 0;
-          ring_wait(&sh->full[j % kStages], (j / kStages) & 1, &none, nullptr);
-        }
     }
+    if (*abort_flag)   // unwind: wait (bounded) for the boxes in flight
+      for (int j = max(0, issued - kStages); j < issued; ++j) {
+        uint32_t none = 0;
+        ring_wait(&sh->full[j % kStages], (j / kStages) & 1, &none, nullptr);
+      }
     return;
   }
 
@@ -214,48 +234,52 @@ __global__ void __launch_bounds__(kDcThreads, 1)
         }
       }
     };
-    DcTile t{};
-    int kc = kc0 + group;
-    auto settle = [&]() {   // (t, kc) to the tile that holds the chunk
-      while (kc >= p.k_chunks) {
-        kc -= p.k_chunks;
-        dc_next(p.n_tiles, t);
-      }
-    };
-    if (u0 + uint32_t(group) < u1) {
-      t = dc_tile(p.n_tiles, tile0);
-      settle();
-      load_scales(t, kc);
-    }
     int s = group;
     uint32_t ph = 1;
-    for (uint32_t u = u0 + group; u < u1; u += kGroups) {
-      uint4 now[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) now[i] = raw[i];
-      if (u + kGroups < u1) {
-        kc += kGroups;
-        settle();
-        load_scales(t, kc);
-      }
-      if (!warp_wait(&sh->empty[s], ph, abort_flag, p.status)) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
-        if (vec && dq) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = (now[i].x >> (8 * j)) & 0xffu;
+    bool ok = true;
+    for (int i = 0; i < 2 && ok; ++i) {
+      const Range r = range_at(i);
+      const uint32_t first = uint32_t((group + kGroups - r.group0) % kGroups);
+      if (r.u0 + first >= r.u1) continue;
+      DcTile t = dc_tile(p.n_tiles, r.tile0);
+      int kc = r.kc0 + int(first);
+      auto settle = [&]() {   // (t, kc) to the tile that holds the chunk
+        while (kc >= p.k_chunks) {
+          kc -= p.k_chunks;
+          dc_next(p.n_tiles, t);
         }
+      };
+      settle();
+      load_scales(t, kc);
+      for (uint32_t u = r.u0 + first; u < r.u1; u += kGroups) {
+        uint4 now[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sh->scales[s][j][2 * (32 * (i & 1) + lane) + (i >> 1)] = dq ? __fmul_rn(float(w[j]), s_g[i >> 1]) : __uint_as_float(w[j]);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->full[s]);
-      s += kGroups;
-      if (s >= kStages) {
-        s -= kStages;
-        ph ^= 1;
+        for (int i = 0; i < 4; ++i) now[i] = raw[i];
+        if (u + kGroups < r.u1) {
+          kc += kGroups;
+          settle();
+          load_scales(t, kc);
+        }
+        ok = warp_wait(&sh->empty[s], ph, abort_flag, p.status);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+          if (vec && dq) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = (now[i].x >> (8 * j)) & 0xffu;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sh->scales[s][j][2 * (32 * (i & 1) + lane) + (i >> 1)] = dq ? __fmul_rn(float(w[j]), s_g[i >> 1]) : __uint_as_float(w[j]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->full[s]);
+        s += kGroups;
+        if (s >= kStages) {
+          s -= kStages;
+          ph ^= 1;
+        }
       }
     }
     return;
@@ -267,82 +291,84 @@ __global__ void __launch_bounds__(kDcThreads, 1)
     const int row = threadIdx.x - 32 * kConsumers;
     bool ok = true, waited = false;
     uint32_t ph = 0;
-    DcTile t{};
-    if (u0 < u1) t = dc_tile(p.n_tiles, tile0);
-    uint32_t tile_u = tile0 * kch;            // first unit of the tile, in whatever CTA
-    for (uint32_t u = u0; u < u1; tile_u += kch, dc_next(p.n_tiles, t)) {
-      const bool starts = u == tile_u;        // this CTA has the tile's first chunk
-      const uint32_t end = min(u1, tile_u + kch);
-      const bool split = end - u < kch;
-      u = end;
-      const int rows = min(NP, p.M - t.rt * NP);
-      const int n = t.nt * kDcOutputs + (row >> 1);
-      if (starts) {
-        const uint16_t* b = p.B + (int64_t(row & 1) * p.N + min(n, p.N - 1)) * p.r;
-        for (int j = 0; j < p.r; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + j));
-      }
-      if (!waited) grid_dep_wait();   // the counters' zeros, of the kernel before
-      waited = true;
-      if (ok) ok = warp_wait<100>(&sh->red_full, ph, abort_flag, p.status);
-      ph ^= 1;
-      float v[NP];
+    for (int i = 0; i < 2; ++i) {
+      const Range r = range_at(i);
+      DcTile t = dc_tile(p.n_tiles, r.tile0);
+      uint32_t tile_u = r.tile0 * kch;          // first unit of the tile, in whatever CTA
+      for (uint32_t u = r.u0; u < r.u1; tile_u += kch, dc_next(p.n_tiles, t)) {
+        const bool starts = u == tile_u;        // this CTA has the tile's first chunk
+        const uint32_t end = min(r.u1, tile_u + kch);
+        const bool split = end - u < kch;
+        u = end;
+        const int rows = min(NP, p.M - t.rt * NP);
+        const int n = t.nt * kDcOutputs + (row >> 1);
+        if (starts) {
+          const uint16_t* b = p.B + (int64_t(row & 1) * p.N + min(n, p.N - 1)) * p.r;
+          for (int j = 0; j < p.r; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + j));
+        }
+        if (!waited) grid_dep_wait();   // the counters' zeros, of the kernel before
+        waited = true;
+        if (ok) ok = warp_wait<100>(&sh->red_full, ph, abort_flag, p.status);
+        ph ^= 1;
+        float v[NP];
 #pragma unroll
-      for (int m = 0; m < NP; ++m) {
-        v[m] = 0.0f;
+        for (int m = 0; m < NP; ++m) {
+          v[m] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) v[m] += sh->red[i][m * kDcRows + row];
-      }
-      bool finish = true;
-      if (split) {
-        // contributors are consecutive CTAs, the first from chunk 0
-        const uint32_t c0 = uint32_t((uint64_t(tile_u + 1) * G - 1) / units);
-        const uint32_t c1 = uint32_t((uint64_t(tile_u + kch) * G - 1) / units);
-        float* mine = p.partials + (size_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * (kDcRows * NP) + row;
+          for (int i = 0; i < kGroups; ++i) v[m] += sh->red[i][m * kDcRows + row];
+        }
+        bool finish = true;
+        if (split) {
+          // contributors are consecutive CTAs, the first from chunk 0
+          const uint32_t c0 = uint32_t((uint64_t(tile_u + 1) * G - 1) / units);
+          const uint32_t c1 = uint32_t((uint64_t(tile_u + kch) * G - 1) / units);
+          float* mine = p.partials + (size_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * (kDcRows * NP) + row;
 #pragma unroll
-        for (int m = 0; m < NP; ++m)
-          if (m < rows) __stcg(mine + m * kDcRows, v[m]);
-        __threadfence();
-        named_barrier(1, kEpi);
-        if (row == 0) sh->last = atomicAdd(p.counters + c0, 1) == int(c1 - c0);
-        named_barrier(1, kEpi);
-        finish = sh->last != 0;
-        if (finish) {
-          // a contributor's rows are loaded together: one after another they were a
-          // tail of 13 us behind the last tile (a tenth of a 16-token step)
+          for (int m = 0; m < NP; ++m)
+            if (m < rows) __stcg(mine + m * kDcRows, v[m]);
           __threadfence();
+          named_barrier(1, kEpi);
+          if (row == 0) sh->last = atomicAdd(p.counters + c0, 1) == int(c1 - c0);
+          named_barrier(1, kEpi);
+          finish = sh->last != 0;
+          if (finish) {
+            // a contributor's rows are loaded together: one after another they were a
+            // tail of 13 us behind the last tile (a tenth of a 16-token step)
+            __threadfence();
 #pragma unroll
-          for (int m = 0; m < NP; ++m) v[m] = 0.0f;
+            for (int m = 0; m < NP; ++m) v[m] = 0.0f;
 #pragma unroll 2
-          for (uint32_t c = c0; c <= c1; ++c) {
-            const float* part = p.partials + (size_t(c) * 2 + (c == c0 ? 1 : 0)) * (kDcRows * NP) + row;
+            for (uint32_t c = c0; c <= c1; ++c) {
+              const float* part = p.partials + (size_t(c) * 2 + (c == c0 ? 1 : 0)) * (kDcRows * NP) + row;
 #pragma unroll
-            for (int m = 0; m < NP; ++m)
-              if (m < rows) v[m] += __ldcg(part + m * kDcRows);
+              for (int m = 0; m < NP; ++m)
+                if (m < rows) v[m] += __ldcg(part + m * kDcRows);
+            }
           }
         }
-      }
-      // Lanes 2 i and 2 i + 1 hold g and u of one output: the even lane takes the even
-      // tokens, the odd one the odd tokens.
-      if (finish && ok) {
-        const int odd = row & 1;
-        const bool there = n < p.N;
-        const float bias = there && p.bias != nullptr ? one_float<F16>(__ldg(p.bias + int64_t(odd) * p.N + n)) : 0.0f;
+        // Lanes 2 i and 2 i + 1 hold g and u of one output: the even lane takes the even
+        // tokens, the odd one the odd tokens.
+        if (finish && ok) {
+          const int odd = row & 1;
+          const bool there = n < p.N;
+          const float bias = there && p.bias != nullptr ? one_float<F16>(__ldg(p.bias + int64_t(odd) * p.N + n)) : 0.0f;
 #pragma unroll
-        for (int m = 0; m < NP; m += 2) {
-          const float a = v[m] + bias, b = v[m + 1] + bias;
-          const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-          const float g = odd ? got : a, u = odd ? b : got;
-          if (!there || m + odd >= rows) continue;
-          const int64_t at = int64_t(t.rt * NP + m + odd) * p.N + n;
-          p.h[at] = one_rounded<F16>(gated::act<true>(p.act, g) * u);
-          if (p.pre != nullptr) {
-            p.pre[at] = one_rounded<F16>(g);
-            p.pre[int64_t(p.M) * p.N + at] = one_rounded<F16>(u);
+          for (int m = 0; m < NP; m += 2) {
+            const float a = v[m] + bias, b = v[m + 1] + bias;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+            const float g = odd ? got : a, u = odd ? b : got;
+            if (!there || m + odd >= rows) continue;
+            const int64_t at = int64_t(t.rt * NP + m + odd) * p.N + n;
+            p.h[at] = one_rounded<F16>(gated::act<true>(p.act, g) * u);
+            if (p.pre != nullptr) {
+              p.pre[at] = one_rounded<F16>(g);
+              p.pre[int64_t(p.M) * p.N + at] = one_rounded<F16>(u);
+            }
           }
         }
+        named_barrier(1, kEpi);   // red and last may be written again
+        if (lane == 0) mbar_arrive(&sh->red_free);
       }
-      named_barrier(1, kEpi);   // red and last may be written again
-      if (lane == 0) mbar_arrive(&sh->red_free);
     }
     if (!waited) grid_dep_wait();
     return;
@@ -372,106 +398,108 @@ __global__ void __launch_bounds__(kDcThreads, 1)
     code_at[i] = row * 128u + ((uint32_t(2 * q + (q >> 1)) ^ (row & 7u)) << 4) + (uint32_t(q & 1) << 3);
   }
   const uint32_t x_at = kDcCodeBytes + uint32_t(q) * (NP * 128) + uint32_t(g) * 128u + (uint32_t((2 * q) ^ g) << 4);
-  DcTile t{};
-  if (u0 < u1) t = dc_tile(p.n_tiles, tile0);
-  int kc = kc0 + group;                     // chunk of this warp's next unit, counted from tile t
-  uint32_t tile_u = tile0 * kch;
-  for (uint32_t seg = u0; seg < u1; tile_u += kch, dc_next(p.n_tiles, t)) {
-    const bool first_part = seg == tile_u;
-    seg = min(u1, tile_u + kch);
-    const int kend = int(seg - tile_u);     // this CTA's chunks of the tile end here
-    float acc[2][NT8][4];                   // of even and odd MMAs
+  for (int part = 0; part < 2; ++part) {
+    const Range r = range_at(part);
+    DcTile t = dc_tile(p.n_tiles, r.tile0);
+    int kc = r.kc0 + (group + kGroups - r.group0) % kGroups;   // chunk of this warp's next unit, counted from tile t
+    uint32_t tile_u = r.tile0 * kch;
+    for (uint32_t seg = r.u0; seg < r.u1; tile_u += kch, dc_next(p.n_tiles, t)) {
+      const bool first_part = seg == tile_u;
+      seg = min(r.u1, tile_u + kch);
+      const int kend = int(seg - tile_u);     // this CTA's chunks of the tile end here
+      float acc[2][NT8][4];                   // of even and odd MMAs
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int c = 0; c < NT8; ++c) acc[i][c][0] = acc[i][c][1] = acc[i][c][2] = acc[i][c][3] = 0.0f;
-    for (; kc < kend; kc += kGroups) {
-      if (ok && !__all_sync(0xffffffffu, mbar_try_wait(&sh->full[s], ph))) ok = warp_wait(&sh->full[s], ph, abort_flag, p.status);
-      if (ok) {
-        const uint8_t* st = smem + s * dc_stage_bytes(NP);
-        float2 scale = *reinterpret_cast<const float2*>(&sh->scales[s][q][set * 16 + 2 * g]);
-        if (kc * kDcBlocks + q >= kb_per_row) scale = make_float2(0.0f, 0.0f);   // past the row's end: x is zero there
-        const expert::BlockTable table = expert::make_table(scale.x, F16);
+        for (int c = 0; c < NT8; ++c) acc[i][c][0] = acc[i][c][1] = acc[i][c][2] = acc[i][c][3] = 0.0f;
+      for (; kc < kend; kc += kGroups) {
+        if (ok && !__all_sync(0xffffffffu, mbar_try_wait(&sh->full[s], ph))) ok = warp_wait(&sh->full[s], ph, abort_flag, p.status);
+        if (ok) {
+          const uint8_t* st = smem + s * dc_stage_bytes(NP);
+          float2 scale = *reinterpret_cast<const float2*>(&sh->scales[s][q][set * 16 + 2 * g]);
+          if (kc * kDcBlocks + q >= kb_per_row) scale = make_float2(0.0f, 0.0f);   // past the row's end: x is zero there
+          const expert::BlockTable table = expert::make_table(scale.x, F16);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint2 w0 = *reinterpret_cast<const uint2*>(st + (code_at[0] ^ (m * 8u)));
-          const uint2 w1 = *reinterpret_cast<const uint2*>(st + (code_at[1] ^ (m * 8u)));
+          for (int m = 0; m < 4; ++m) {
+            const uint2 w0 = *reinterpret_cast<const uint2*>(st + (code_at[0] ^ (m * 8u)));
+            const uint2 w1 = *reinterpret_cast<const uint2*>(st + (code_at[1] ^ (m * 8u)));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t c0 = h ? w0.y : w0.x, c1 = h ? w1.y : w1.x;
-            const uint2 lo = expert::decode4(c0 & 0x7777u, ((c0 >> 1) & 0x4444u) | 0x3210u, table);
-            const uint4 v = make_uint4(lo.x, lo.y, two_weights<2, F16>(lut, c0, lane8, scale.x), two_weights<3, F16>(lut, c0, lane8, scale.x));
-            const uint32_t a0[4] = {v.x, two_weights<0, F16>(lut, c1, lane8, scale.y), v.y, two_weights<1, F16>(lut, c1, lane8, scale.y)};
-            const uint32_t a1[4] = {v.z, two_weights<2, F16>(lut, c1, lane8, scale.y), v.w, two_weights<3, F16>(lut, c1, lane8, scale.y)};
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t c0 = h ? w0.y : w0.x, c1 = h ? w1.y : w1.x;
+              const uint2 lo = expert::decode4(c0 & 0x7777u, ((c0 >> 1) & 0x4444u) | 0x3210u, table);
+              const uint4 v = make_uint4(lo.x, lo.y, two_weights<2, F16>(lut, c0, lane8, scale.x), two_weights<3, F16>(lut, c0, lane8, scale.x));
+              const uint32_t a0[4] = {v.x, two_weights<0, F16>(lut, c1, lane8, scale.y), v.y, two_weights<1, F16>(lut, c1, lane8, scale.y)};
+              const uint32_t a1[4] = {v.z, two_weights<2, F16>(lut, c1, lane8, scale.y), v.w, two_weights<3, F16>(lut, c1, lane8, scale.y)};
+#pragma unroll
+              for (int c = 0; c < NT8; ++c) {
+                const uint4 xv = *reinterpret_cast<const uint4*>(st + (x_at ^ ((2 * m + h) * 16u)) + c * 1024);
+                mma_16816<F16>(acc[0][c], a0, xv.x, xv.y);
+                mma_16816<F16>(acc[1][c], a1, xv.z, xv.w);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&sh->empty[s]);
+        s += kGroups;
+        if (s >= kStages) {
+          s -= kStages;
+          ph ^= 1;
+        }
+      }
+      kc -= p.k_chunks;
+#pragma unroll
+      for (int c = 0; c < NT8; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[0][c][i] += acc[1][c][i];
+
+      // The adapters' products enter the tile's first part, as MMAs with the rows of B as A
+      // (of one projection, the other's zero) and T as B; the groups take 32 columns in turn,
+      // a lane eight consecutive ones of its rows in a load (two at a time were 45.7 us against
+      // 34.7 with 16 tokens and r = 64).
+      if (first_part) {
+        if (!waited) grid_dep_wait();   // T of the kernel before
+        waited = true;
+        const int n = min(t.nt * kDcOutputs + set * 8 + g, p.N - 1);
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 32 * group + 8 * q; j - 8 * q < p.r; j += 32 * kGroups) {   // r is a multiple of 8
+          const bool there = j < p.r;
+          uint4 bv[2], tv[2][NT8];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            bv[z] = there ? __ldg(reinterpret_cast<const uint4*>(p.B + (int64_t(z) * p.N + n) * p.r + j)) : none;
 #pragma unroll
             for (int c = 0; c < NT8; ++c) {
-              const uint4 xv = *reinterpret_cast<const uint4*>(st + (x_at ^ ((2 * m + h) * 16u)) + c * 1024);
-              mma_16816<F16>(acc[0][c], a0, xv.x, xv.y);
-              mma_16816<F16>(acc[1][c], a1, xv.z, xv.w);
+              const int m = t.rt * NP + 8 * c + g;
+              tv[z][c] = there && m < p.M ? __ldcg(reinterpret_cast<const uint4*>(p.T + (int64_t(z) * p.M + m) * p.r + j)) : none;
+            }
+          }
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            uint32_t lo[4] = {0u, 0u, 0u, 0u}, hi[4] = {0u, 0u, 0u, 0u};
+            lo[z] = bv[z].x, lo[2 + z] = bv[z].y, hi[z] = bv[z].z, hi[2 + z] = bv[z].w;
+#pragma unroll
+            for (int c = 0; c < NT8; ++c) {
+              mma_16816<F16>(acc[0][c], lo, tv[z][c].x, tv[z][c].y);
+              mma_16816<F16>(acc[0][c], hi, tv[z][c].z, tv[z][c].w);
             }
           }
         }
       }
+
+      // the tile's sums, for the finishing warps
+      if (ok) ok = warp_wait(&sh->red_free, red_ph, abort_flag, p.status);
+      red_ph ^= 1;
+      const int row = set * 16 + 2 * g;
+#pragma unroll
+      for (int c = 0; c < NT8; ++c) {
+        float* o = sh->red[group] + (8 * c + 2 * q) * kDcRows + row;
+        *reinterpret_cast<float2*>(o) = make_float2(acc[0][c][0], acc[0][c][2]);
+        *reinterpret_cast<float2*>(o + kDcRows) = make_float2(acc[0][c][1], acc[0][c][3]);
+      }
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&sh->empty[s]);
-      s += kGroups;
-      if (s >= kStages) {
-        s -= kStages;
-        ph ^= 1;
-      }
+      if (lane == 0) mbar_arrive(&sh->red_full);
     }
-    kc -= p.k_chunks;
-#pragma unroll
-    for (int c = 0; c < NT8; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[0][c][i] += acc[1][c][i];
-
-    // The adapters' products enter the tile's first part, as MMAs with the rows of B as A
-    // (of one projection, the other's zero) and T as B; the groups take 32 columns in turn,
-    // a lane eight consecutive ones of its rows in a load (two at a time were 45.7 us against
-    // 34.7 with 16 tokens and r = 64).
-    if (first_part) {
-      if (!waited) grid_dep_wait();   // T of the kernel before
-      waited = true;
-      const int n = min(t.nt * kDcOutputs + set * 8 + g, p.N - 1);
-      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-      for (int j = 32 * group + 8 * q; j - 8 * q < p.r; j += 32 * kGroups) {   // r is a multiple of 8
-        const bool there = j < p.r;
-        uint4 bv[2], tv[2][NT8];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          bv[z] = there ? __ldg(reinterpret_cast<const uint4*>(p.B + (int64_t(z) * p.N + n) * p.r + j)) : none;
-#pragma unroll
-          for (int c = 0; c < NT8; ++c) {
-            const int m = t.rt * NP + 8 * c + g;
-            tv[z][c] = there && m < p.M ? __ldcg(reinterpret_cast<const uint4*>(p.T + (int64_t(z) * p.M + m) * p.r + j)) : none;
-          }
-        }
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          uint32_t lo[4] = {0u, 0u, 0u, 0u}, hi[4] = {0u, 0u, 0u, 0u};
-          lo[z] = bv[z].x, lo[2 + z] = bv[z].y, hi[z] = bv[z].z, hi[2 + z] = bv[z].w;
-#pragma unroll
-          for (int c = 0; c < NT8; ++c) {
-            mma_16816<F16>(acc[0][c], lo, tv[z][c].x, tv[z][c].y);
-            mma_16816<F16>(acc[0][c], hi, tv[z][c].z, tv[z][c].w);
-          }
-        }
-      }
-    }
-
-    // the tile's sums, for the finishing warps
-    if (ok) ok = warp_wait(&sh->red_free, red_ph, abort_flag, p.status);
-    red_ph ^= 1;
-    const int row = set * 16 + 2 * g;
-#pragma unroll
-    for (int c = 0; c < NT8; ++c) {
-      float* o = sh->red[group] + (8 * c + 2 * q) * kDcRows + row;
-      *reinterpret_cast<float2*>(o) = make_float2(acc[0][c][0], acc[0][c][2]);
-      *reinterpret_cast<float2*>(o + kDcRows) = make_float2(acc[0][c][1], acc[0][c][3]);
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh->red_full);
   }
 }
 
@@ -599,12 +627,16 @@ bool GatedDecode::prepare(const GatedArgs& a, const void* T, uint8_t* scratch, i
   p.vec_scales = a.w[0]->block_size == 64 && a.K % 256 == 0;   // scale pointers are 16-byte aligned
   const int64_t most = int64_t(p.row_tiles) * p.n_tiles * p.k_chunks;
   if (most > int64_t(0x7fffffff)) return false;
-  // With two SMs or more for a tile each tile has CTAs of its own, up to eight: a share that
-  // straddles two tiles stores and joins parts of both (1000 x 4096: one token 15.6 -> 10.6 us,
-  // 16 tokens 28.5 -> 14.2; 4096 x 4096, 16 tokens: 20.6 -> 18.4).
+  // Whole tiles for every SM, and the rest shared: where it leaves two SMs or more for a tile
+  // each has CTAs of its own, up to eight, as a share that straddles two tiles stores and joins
+  // parts of both (1000 x 4096: one token 15.6 -> 10.6 us, 16 tokens 28.5 -> 14.2; 4096 x 4096,
+  // 16 tokens: 20.6 -> 18.4).
   const int64_t tiles = int64_t(p.row_tiles) * p.n_tiles, ctas = std::min(sms, kGatedDecodeMaxCtas);
-  const int64_t each = std::min<int64_t>({8, ctas / tiles, p.k_chunks});
-  grid = unsigned(each >= 2 ? each * tiles : std::min(ctas, most));
+  p.whole = int(tiles / ctas);
+  p.rest = int(tiles % ctas);
+  const int64_t each = p.rest > 0 ? std::min<int64_t>({8, ctas / p.rest, p.k_chunks}) : 0;
+  p.rest_ctas = int(each >= 2 ? each * p.rest : std::min<int64_t>(ctas, int64_t(p.rest) * p.k_chunks));
+  grid = unsigned(p.whole > 0 ? ctas : p.rest_ctas);
   return ok;
 }
 

@@ -13,6 +13,8 @@ struct GatedDecodeParams {
   int M, N, K, r;
   int n_tiles, k_chunks;    // tiles of 64 outputs, 256-wide chunks of a row
   int row_tiles;            // groups of tokens
+  int whole;                // tiles that a CTA has of its own, behind
+  int rest, rest_ctas;      // the first tiles, which rest_ctas CTAs share
   int bs_shift, dq, act;
   int vec_scales;           // a row's four scales of a chunk are one aligned vector
   const uint8_t* absmax_q[2];
