@@ -39,6 +39,7 @@ struct Fp8Params {
   const float* w_scale;
   const float* x_scale;
   const void* bias;
+  void* y;
   uint32_t* status;
 };
 
@@ -49,6 +50,7 @@ struct Fp8Gemm {
   Fp8Params p;
   unsigned grid = 0;
   int tile_n = 0;          // 256: pairs of CTAs, 256 x 256; else 128 x tile_n
+  int parts = 1;           // CTAs (a cluster) that share a tile's blocks along K; of 128 x tile_n
   bool prepare(const Fp8LinearArgs& a, int sms);
   cudaError_t run(cudaStream_t st, int* launches) const;
 };

@@ -11,7 +11,8 @@
 // Wide tiles are 256 x 256 by a pair of CTAs (cta_group::2): the MMAs of a block take 512
 // cycles, reading the accumulator (128 x 256 of it in each CTA) 256 and the FMAs 256, on
 // eight warps of 128 columns each.  Where such tiles would leave SMs idle, a CTA takes
-// 128 x 128, 64 or 32.
+// 128 x 128, 64 or 32, and the blocks along K may be shared by a cluster of CTAs, which add
+// their fp32 sums through distributed shared memory in their order.
 // Roles: warp 0 token TMA, warp 1 weight TMA, warp 2 MMA (the pair's leader issues), from
 // warp 4 on the sums.  Output in pieces of 32 rows of 64 bytes through shared memory by TMA.
 //
@@ -42,6 +43,7 @@ using namespace expert;
 
 constexpr int kEpiWarp = 4;
 constexpr uint32_t kXBytes = 128 * 128;
+constexpr int kMaxParts = 8;
 constexpr uint32_t kPiece = 2048;        // of a warp: 32 rows of 64 bytes of the result
 
 template <int NT>
@@ -109,6 +111,57 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64
 }
 constexpr uint32_t idesc_e4m3(int M, int N) { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
 
+// Element of a parked tile [128][NT]: 16-byte chunks swizzled by row.
+template <int NT>
+__device__ __forceinline__ int park_at(int row, int col) {
+  return row * NT + 4 * ((col >> 2) ^ (row & 7)) + (col & 3);
+}
+
+__device__ __forceinline__ float bias_of(const Fp8Params& p, int col) {
+  const int at = min(col, p.N - 1);
+  return p.dtype == NF4_F32   ? __ldg(static_cast<const float*>(p.bias) + at)
+         : p.dtype == NF4_F16 ? __half2float(static_cast<const __half*>(p.bias)[at])
+                              : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[at]);
+}
+
+// The parts of a tile added up in their order, each CTA of the cluster a share of the rows.
+// All threads; the second barrier keeps the parts alive.
+template <int NT>
+__device__ __forceinline__ void join_parts(const Fp8Params& p, const float* park, int parts, int id) {
+  cluster_sync();
+  const int q = int(cluster_ctarank());
+  const int ct = id / p.row_tiles, rt = id - ct * p.row_tiles;
+  const int rows = min(128, p.M - rt * 128), r0 = rows * q / parts, r1 = rows * (q + 1) / parts;
+  constexpr int kVec = NT / 4;
+  const uint32_t base = smem_u32(park);
+  for (int i = threadIdx.x; i < (r1 - r0) * kVec; i += blockDim.x) {
+    const int row = r0 + i / kVec, c = 4 * (i % kVec), col = ct * NT + c;
+    float4 part[kMaxParts], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < kMaxParts; ++s)   // all on their way before the first is needed
+      if (s < parts) part[s] = ld_shared_cluster_f4(mapa_shared(base + uint32_t(park_at<NT>(row, c)) * 4u, uint32_t(s)));
+#pragma unroll
+    for (int s = 0; s < kMaxParts; ++s) {
+      if (s >= parts) break;
+      v.x += part[s].x;
+      v.y += part[s].y;
+      v.z += part[s].z;
+      v.w += part[s].w;
+    }
+    if (col >= p.N) continue;
+    if (p.bias != nullptr)
+      v = make_float4(v.x + bias_of(p, col), v.y + bias_of(p, col + 1), v.z + bias_of(p, col + 2), v.w + bias_of(p, col + 3));
+    const int64_t at = int64_t(rt * 128 + row) * p.N + col;
+    if (p.dtype == NF4_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = v;
+    } else {
+      const bool f16 = p.dtype == NF4_F16;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) = make_uint2(pack2(f16, v.x, v.y), pack2(f16, v.z, v.w));
+    }
+  }
+  cluster_sync();
+}
+
 template <int NT>
 __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& my, const Fp8Params& p) {
   using C = Cfg<NT>;
@@ -153,6 +206,9 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   const int first = int(blockIdx.x) / C::kPair, step = int(gridDim.x) / C::kPair;
+  // Blocks of this CTA: all, or (one tile a CTA) its part of them; the parts' sums are joined.
+  const int parts = C::kPair == 2 ? 1 : int(gridDim.y);
+  const int b0 = parts == 1 ? 0 : p.kb * int(blockIdx.y) / parts, b1 = parts == 1 ? p.kb : p.kb * (int(blockIdx.y) + 1) / parts;
   auto leader_bar = [&](uint64_t* bar) { return C::kPair == 2 ? mapa_shared(smem_u32(bar), 0) : smem_u32(bar); };
   grid_dep_wait();
   // The sums of wide tiles want more registers than an even split gives: 4 warps x 56 + 8 x 224,
@@ -171,7 +227,7 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
     for (int id = first; id < p.tiles && ok; id += step) {
       const int ct = id / p.row_tiles, rt = id - ct * p.row_tiles;
       const int y = warp == 0 ? rt * C::kRows + 128 * int(rank) : ct * NT + (NT / C::kPair) * int(rank);
-      for (int b = 0; b < p.kb; ++b) {
+      for (int b = b0; b < b1; ++b) {
         ok = ring_wait(&sh->empty[s], ph, abort_flag, p.status);
         if (!ok) break;
         if (issue) {
@@ -205,7 +261,7 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
       int s = 0, n = 0;
       uint32_t ph = 0;
       for (int id = first; id < p.tiles && ok; id += step) {
-        for (int b = 0; b < p.kb; ++b, ++n) {
+        for (int b = b0; b < b1; ++b, ++n) {
           ok = mbar_wait_cluster(&sh->full[s], ph, abort_flag, p.status);
           if (ok) ok = mbar_wait_cluster(&sh->acc_empty[n & 1], ((n >> 1) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
@@ -247,11 +303,11 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
       const int row0 = rt * C::kRows + 128 * int(rank) + quad * 32, col0 = ct * NT + group * C::kCols;
       const float* sx = p.x_scale + int64_t(min(row0 + lane, p.M - 1)) * p.kb;
       const float* sw = p.w_scale + int64_t(min(col0, p.N - 1) / 128) * p.kb;
-      float nx = __ldg(sx), nw = __ldg(sw);
+      float nx = __ldg(sx + b0), nw = __ldg(sw + b0);
       float2 acc[C::kCols / 2];
 #pragma unroll
       for (int i = 0; i < C::kCols / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      for (int b = 0; b < p.kb; ++b, ++n) {
+      for (int b = b0; b < b1; ++b, ++n) {
         ok = all_wait(&sh->acc_full[n & 1], (n >> 1) & 1, abort_flag, p.status);
         if (!ok) break;
         if (warp == kEpiWarp + C::kEpiWarps - 1 && lane == 0) mbar_arrive(&sh->empty[s]);
@@ -259,7 +315,7 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
         tc_fence_after();
         const uint32_t at = tmem + (uint32_t(quad * 32) << 16) + uint32_t(n & 1) * uint32_t(NT) + group * C::kCols;
         const float2 scale = make_float2(nx * nw, nx * nw);   // loaded a block ahead
-        const int nb = min(b + 1, p.kb - 1);
+        const int nb = min(b + 1, b1 - 1);
         nx = __ldg(sx + nb);
         nw = __ldg(sw + nb);
         // 32 columns are on their way while the 32 before are added
@@ -283,19 +339,22 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
         }
       }
       if (!ok) break;
+      if (C::kPair == 1 && parts > 1) {   // for the other CTAs: the ring is done with
+        float* park = reinterpret_cast<float*>(smem);
+        const int row = quad * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < C::kCols; c += 4)
+          *reinterpret_cast<float4*>(park + park_at<NT>(row, group * C::kCols + c)) =
+              make_float4(acc[c / 2].x, acc[c / 2].y, acc[c / 2 + 1].x, acc[c / 2 + 1].y);
+        break;
+      }
       // ---- bias, rounding; pieces of 32 rows x 64 bytes through shared memory (64-byte
       // swizzle: chunk j at j ^ ((row >> 1) & 3))
       if (p.bias != nullptr) {
-        auto bias_at = [&](int col) {
-          const int at = min(col, p.N - 1);
-          return p.dtype == NF4_F32   ? __ldg(static_cast<const float*>(p.bias) + at)
-                 : p.dtype == NF4_F16 ? __half2float(static_cast<const __half*>(p.bias)[at])
-                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[at]);
-        };
 #pragma unroll
         for (int i = 0; i < C::kCols / 2; ++i) {
-          acc[i].x += bias_at(col0 + 2 * i);
-          acc[i].y += bias_at(col0 + 2 * i + 1);
+          acc[i].x += bias_of(p, col0 + 2 * i);
+          acc[i].y += bias_of(p, col0 + 2 * i + 1);
         }
       }
       auto piece = [&](int col, const uint4 (&chunk)[4]) {
@@ -344,6 +403,7 @@ __device__ __forceinline__ void fp8_gemm_body(const CUtensorMap& mx, const CUten
   tc_fence_before();
   if (C::kPair == 2) cluster_sync();
   else __syncthreads();
+  if (C::kPair == 1 && parts > 1) join_parts<NT>(p, reinterpret_cast<const float*>(smem), parts, first);
   if (warp == 2) {
     tc_fence_after();
     if (C::kPair == 2) tmem_dealloc_pair(tmem, C::kTmem);
@@ -383,12 +443,31 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool Fp8Gemm::prepare(const Fp8LinearArgs& a, int sms) {
   const uint64_t M = uint64_t(a.M), N = uint64_t(a.N), K = uint64_t(a.K);
-  // The widest tile that still gives every SM one.
-  tile_n = 32;
-  const int64_t row_tiles = cdiv(a.M, 128);
-  if (cdiv(a.M, 256) * cdiv(a.N, 256) * 2 >= sms && a.M > 128) tile_n = 256;
-  else if (row_tiles * cdiv(a.N, 128) >= sms) tile_n = 128;
-  else if (row_tiles * cdiv(a.N, 64) >= sms) tile_n = 64;
+  const int64_t row_tiles = cdiv(a.M, 128), kb = cdiv(a.K, kFp8Block);
+  tile_n = 256;
+  parts = 1;
+  if (a.M <= 128 || cdiv(a.M, 256) * cdiv(a.N, 256) * 2 < sms) {
+    // Pairs would leave SMs idle: of narrower tiles, and parts of their blocks, what takes least
+    // by these measured times, in ns: 230, 275 or 350 a block of 32, 64 or 128 columns, 1,000 a
+    // tile and 2,500 to join parts.  16 tokens through 4096 x 4096 take 8.9 us (128 columns, four
+    // parts) against 10.7 with 32 columns, through 1024 x 8192 7.1 against 16.0; 64 through 11008 x
+    // 4096 14.6 with 128 columns, 21.3 with 64; 333 through 1000 x 2064 7.8 with 32, 8.8 with 128.
+    int64_t best = INT64_MAX;
+    const int64_t block_ns[3] = {350, 275, 230};
+    for (int w = 0; w < 3; ++w)
+      for (int s = 1; s <= kMaxParts && (s == 1 || kb / s >= 2); s *= 2) {
+        const int64_t tiles = row_tiles * cdiv(a.N, 128 >> w);
+        // a tile a CTA, all at once: GPCs hold whole clusters (16 of eight did not fit: 11.4 us
+        // against 7.1 of 8)
+        if (s > 1 && tiles * s > (s == 8 ? sms * 2 / 3 : sms * 7 / 8)) break;
+        const int64_t cost = cdiv(tiles, sms) * (cdiv(kb, s) * block_ns[w] + 1000) + (s > 1 ? 2500 : 0);
+        if (cost < best) {
+          best = cost;
+          tile_n = 128 >> w;
+          parts = s;
+        }
+      }
+  }
   const int pair = tile_n == 256 ? 2 : 1;
   // Few tokens: a box of as many rows (the other lanes' results are never stored).  With
   // fewer than 32 tokens in boxes of 128 rows 4096 x 4096 took 18 us against 11.4 with 33.
@@ -402,7 +481,7 @@ bool Fp8Gemm::prepare(const Fp8LinearArgs& a, int sms) {
   p = Fp8Params{};
   p.M = int(a.M);
   p.N = int(a.N);
-  p.kb = int(cdiv(a.K, kFp8Block));
+  p.kb = int(kb);
   p.row_tiles = int(cdiv(a.M, 128 * pair));
   const int64_t tiles = int64_t(p.row_tiles) * cdiv(a.N, tile_n);
   p.tiles = int(tiles);
@@ -411,8 +490,9 @@ bool Fp8Gemm::prepare(const Fp8LinearArgs& a, int sms) {
   p.w_scale = a.w_scale;
   p.x_scale = a.x_scale;
   p.bias = a.bias;
+  p.y = a.y;
   p.status = a.status;
-  grid = unsigned(pair * std::min<int64_t>(tiles, std::max(sms / pair, 1)));
+  grid = unsigned(parts > 1 ? tiles : pair * std::min<int64_t>(tiles, std::max(sms / pair, 1)));   // parts: a tile a CTA
   return ok && tiles <= int64_t(0x7fffffff);
 }
 
@@ -420,13 +500,20 @@ cudaError_t Fp8Gemm::run(cudaStream_t st, int* launches) const {
   cudaError_t e = set_attrs();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.gridDim = dim3(grid, unsigned(parts), 1);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int attrs = 0;
+  if (parts > 1) {
+    attr[attrs].id = cudaLaunchAttributeClusterDimension;
+    attr[attrs].val.clusterDim.x = 1;
+    attr[attrs].val.clusterDim.y = unsigned(parts);
+    attr[attrs++].val.clusterDim.z = 1;
+  }
+  attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[attrs].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = prof_on() ? 0 : 1;
+  cfg.numAttrs = unsigned(prof_on() ? attrs : attrs + 1);
   NF4_PROF_BEGIN(st, kKFp8Linear);
   auto go = [&](auto kernel, int threads, size_t smem) {
     cfg.blockDim = dim3(unsigned(threads), 1, 1);

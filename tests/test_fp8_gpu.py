@@ -291,3 +291,24 @@ def test_linear_with_more_than_two_to_the_31_results(cuda_device):
         assert y[rows].equal(Q.fp8_linear_fwd(w, x[rows].clone()))
     del y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(9, 1024, 8192), (16, 264, 4096), (40, 520, 11008), (127, 136, 6000), (129, 1000, 4112), (200, 72, 16384),
+                                   (64, 11008, 512), (33, 4104, 4096)])
+def test_few_tiles_share_a_long_sum(cuda_device, m, n, k, dtype):
+    import torch
+    Q = _Q()
+    L = Lin(cuda_device, m, n, k, dtype, bias=True)
+    big = torch.full((m + 5, n), 7.0, dtype=L.x.dtype, device=cuda_device)
+    y = Q.fp8_linear_fwd(L.w, L.x, bias=L.bias, out=big[:m])
+    L.check(y)
+    assert (big[m:] == 7).all()
+    for _ in range(3):
+        assert Q.fp8_linear_fwd(L.w, L.x, bias=L.bias).equal(y)
+    x = L.x.clone()
+    x[1, 5] = float("nan")
+    z = Q.fp8_linear_fwd(L.w, x, bias=L.bias)
+    rows = torch.arange(m, device=cuda_device) != 1
+    assert z[rows].equal(y[rows]) and not torch.isfinite(z[1]).any()
+    assert Q.read_status() == 0
