@@ -534,8 +534,9 @@ cudaError_t small_t(const Fp8LinearArgs& a, const void* x, const float* scale, i
 }
 
 // Up to eight tokens (one MMA column group) the weight is streamed.  Measured, this against
-// the tensor-core kernel with the same codes, us: 4096 x 4096 with 1, 8, 12 and 16 tokens
-// 7.1, 7.8, 11.4 and 13.2 against 12.1; 11008 x 4096 with 8 and 16 12.8 and 20.7 against 21.
+// the tensor-core kernel with the same codes, us: 4096 x 4096 with 1 and 8 tokens 6.5 and 7.6
+// against 8.5 and 9.0; 1024 x 8192 5.2 and 6.5 against 7.0; 11008 x 4096 12.1 and 13.0 against
+// 13.5 and 14.0; 4096 x 11008 12.4 and 15.2 against 13.8.
 bool use_small(const Fp8LinearArgs& a) { return a.M <= 8 && a.M * a.K <= kSmMaxCodes; }
 // Every CTA quantizes all tokens again: up to two tokens of 4096 that costs less than a
 // launch (1, 2, 4 tokens: 8.6, 10.2, 13.3 us; with a launch of its own before 9.6 to 9.8).
