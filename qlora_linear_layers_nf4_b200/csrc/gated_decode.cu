@@ -16,7 +16,7 @@
 //
 // Bound by decoding: four instructions a weight; at 44032 x 4096 shared memory is 73 % busy, the
 // byte-permute pipe 58 %, issue 57 %, DRAM 31 %.  Two weights of 11008 x 4096 (47 MB) take 24 us
-// with one token (1.9 TB/s), 31 with 16, of which 9 are start and T (equal shares of all units,
+// with one token (2.0 TB/s), 29 with 16, of which 8 are start and T (equal shares of all units,
 // with the join of split tiles at their end: 27 and 33);
 // the rest grows by 15 us (one token) to 19 (16 tokens) for each such pair of weights.
 #include <algorithm>
@@ -124,18 +124,6 @@ __global__ void __launch_bounds__(kDcThreads, 1)
     tma_prefetch(&tm_gate);
     tma_prefetch(&tm_up);
     tma_prefetch(&tm_x);
-  }
-  if (warp < kConsumers) {
-    // Lookup table: byte (even element in the high nibble) -> two levels, one copy per lane.
-    uint32_t my = 0;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) my = (lane & 15) == c ? level_bits(c) : my;
-    const float lv = __uint_as_float(my);
-    for (int e = warp; e < 256; e += kConsumers) {
-      const float hi = __shfl_sync(0xffffffffu, lv, e >> 4);
-      const float lo = __shfl_sync(0xffffffffu, lv, e & 15);
-      reinterpret_cast<float2*>(lut)[e * 32 + lane] = make_float2(hi, lo);
-    }
   }
   __syncthreads();
 
@@ -380,6 +368,20 @@ __global__ void __launch_bounds__(kDcThreads, 1)
   // MMA is free as long as W' and x agree, so lane q's four k positions are columns of block
   // q.  Half of the gate's row is decoded with byte permutes from a table of its block's
   // sixteen products (as in the GEMM), the rest with the shared-memory lookups.
+  //
+  // Lookup table: byte (even element in the high nibble) -> two levels, one copy per lane.  It
+  // is made while the first loads are on their way (before the roles part it cost 0.6 us more).
+  uint32_t my = 0;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) my = (lane & 15) == c ? level_bits(c) : my;
+  const float lv = __uint_as_float(my);
+  for (int e = warp; e < 256; e += kConsumers) {
+    const float hi = __shfl_sync(0xffffffffu, lv, e >> 4);
+    const float lo = __shfl_sync(0xffffffffu, lv, e & 15);
+    reinterpret_cast<float2*>(lut)[e * 32 + lane] = make_float2(hi, lo);
+  }
+  named_barrier(2, 32 * kConsumers);
+
   const int group = warp / kDcGroupWarps;
   const int set = warp % kDcGroupWarps;     // outputs 8 set ..
   const int g = lane >> 2, q = lane & 3;
