@@ -368,7 +368,6 @@ cudaError_t dequantize_t(const uint8_t* codes, const float* scales, int64_t rows
 constexpr int kSmWarps = 8;
 constexpr int kSmThreads = 32 * kSmWarps;
 constexpr int kSmAhead = 4;                        // blocks whose loads are in flight
-constexpr int64_t kSmMaxCodes = 96 * 1024;         // M * K
 
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -409,7 +408,7 @@ __global__ void __launch_bounds__(kSmThreads) fp8_small_kernel(const Fp8LinearAr
   float* part = sx + kb * NP;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, q = lane & 3;
   grid_dep_wait();
-  const int groups = int((a.N + 15) / 16);
+  const int groups = int((a.N + kFp8SmallRows - 1) / kFp8SmallRows);
   const int b0 = kb * warp / kSmWarps, b1 = kb * (warp + 1) / kSmWarps;   // this warp's blocks
   uint4 wv[kSmAhead][2][2];                        // block, row (g, g + 8), 64-byte half
   auto load_w = [&](int grp, int b) {
@@ -528,19 +527,10 @@ cudaError_t small_t(const Fp8LinearArgs& a, const void* x, const float* scale, i
   }
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  pdl_config(&cfg, attr, unsigned(std::min<int64_t>((a.N + 15) / 16, 2 * int64_t(sms))), kSmThreads, st);
+  pdl_config(&cfg, attr, unsigned(fp8_small_ctas(a.N, sms)), kSmThreads, st);
   cfg.dynamicSmemBytes = small_smem(int(a.M), int((a.K + kFp8Block - 1) / kFp8Block));
   return cudaLaunchKernelEx(&cfg, fp8_small_kernel<T>, a, static_cast<const T*>(x), scale);
 }
-
-// Up to eight tokens (one MMA column group) the weight is streamed.  Measured, this against
-// the tensor-core kernel with the same codes, us: 4096 x 4096 with 1 and 8 tokens 6.5 and 7.6
-// against 8.5 and 9.0; 1024 x 8192 5.2 and 6.5 against 7.0; 11008 x 4096 12.1 and 13.0 against
-// 13.5 and 14.0; 4096 x 11008 12.4 and 15.2 against 13.8.
-bool use_small(const Fp8LinearArgs& a) { return a.M <= 8 && a.M * a.K <= kSmMaxCodes; }
-// Every CTA quantizes all tokens again: up to two tokens of 4096 that costs less than a
-// launch (1, 2, 4 tokens: 8.6, 10.2, 13.3 us; with a launch of its own before 9.6 to 9.8).
-bool quantize_inside(const Fp8LinearArgs& a) { return a.M * a.K <= 8192; }
 
 }  // namespace
 
@@ -571,8 +561,8 @@ cudaError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int
 cudaError_t launch_fp8_linear(const Fp8LinearArgs& given, const void* x, const float* x_scale, uint8_t* codes,
                               float* scales, int sms, cudaStream_t st, int* launches) {
   Fp8LinearArgs a = given;
-  const bool small = use_small(a);
-  const bool inside = small && x_scale == nullptr && quantize_inside(a);
+  const bool small = fp8_streams(a.M, a.K);
+  const bool inside = small && x_scale == nullptr && fp8_quantizes_inside(a.M, a.K);
   a.x = x_scale != nullptr ? static_cast<const uint8_t*>(x) : codes;
   a.x_scale = x_scale != nullptr ? x_scale : scales;
   Fp8Gemm g;

@@ -3,11 +3,10 @@
 
 #include <cuda.h>
 
+#include "fp8_plan.h"
 #include "kernels.h"
 
 namespace nf4 {
-
-constexpr int kFp8Block = 128;   // columns (and rows of a weight) that share a scale
 
 struct Fp8LinearArgs {
   const uint8_t* w;        // [N, K] e4m3
@@ -49,8 +48,8 @@ struct Fp8Gemm {
   CUtensorMap mx, mw, my;
   Fp8Params p;
   unsigned grid = 0;
-  int tile_n = 0;          // 256: pairs of CTAs, 256 x 256; else 128 x tile_n
-  int parts = 1;           // CTAs (a cluster) that share a tile's blocks along K; of 128 x tile_n
+  int tile_n = 0;          // as in Fp8GemmPlan
+  int parts = 1;
   bool prepare(const Fp8LinearArgs& a, int sms);
   cudaError_t run(cudaStream_t st, int* launches) const;
 };

@@ -43,7 +43,7 @@ using namespace expert;
 
 constexpr int kEpiWarp = 4;
 constexpr uint32_t kXBytes = 128 * 128;
-constexpr int kMaxParts = 8;
+constexpr int kMaxParts = kFp8MaxParts;
 constexpr uint32_t kPiece = 2048;        // of a warp: 32 rows of 64 bytes of the result
 
 template <int NT>
@@ -443,31 +443,9 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool Fp8Gemm::prepare(const Fp8LinearArgs& a, int sms) {
   const uint64_t M = uint64_t(a.M), N = uint64_t(a.N), K = uint64_t(a.K);
-  const int64_t row_tiles = cdiv(a.M, 128), kb = cdiv(a.K, kFp8Block);
-  tile_n = 256;
-  parts = 1;
-  if (a.M <= 128 || cdiv(a.M, 256) * cdiv(a.N, 256) * 2 < sms) {
-    // Pairs would leave SMs idle: of narrower tiles, and parts of their blocks, what takes least
-    // by these measured times, in ns: 230, 275 or 350 a block of 32, 64 or 128 columns, 1,000 a
-    // tile and 2,500 to join parts.  16 tokens through 4096 x 4096 take 8.9 us (128 columns, four
-    // parts) against 10.7 with 32 columns, through 1024 x 8192 7.1 against 16.0; 64 through 11008 x
-    // 4096 14.6 with 128 columns, 21.3 with 64; 333 through 1000 x 2064 7.8 with 32, 8.8 with 128.
-    int64_t best = INT64_MAX;
-    const int64_t block_ns[3] = {350, 275, 230};
-    for (int w = 0; w < 3; ++w)
-      for (int s = 1; s <= kMaxParts && (s == 1 || kb / s >= 2); s *= 2) {
-        const int64_t tiles = row_tiles * cdiv(a.N, 128 >> w);
-        // a tile a CTA, all at once: GPCs hold whole clusters (16 of eight did not fit: 11.4 us
-        // against 7.1 of 8)
-        if (s > 1 && tiles * s > (s == 8 ? sms * 2 / 3 : sms * 7 / 8)) break;
-        const int64_t cost = cdiv(tiles, sms) * (cdiv(kb, s) * block_ns[w] + 1000) + (s > 1 ? 2500 : 0);
-        if (cost < best) {
-          best = cost;
-          tile_n = 128 >> w;
-          parts = s;
-        }
-      }
-  }
+  const Fp8GemmPlan plan = fp8_gemm_plan(a.M, a.N, a.K, sms);
+  tile_n = plan.tile_n;
+  parts = plan.parts;
   const int pair = tile_n == 256 ? 2 : 1;
   // Few tokens: a box of as many rows (the other lanes' results are never stored).  With
   // fewer than 32 tokens in boxes of 128 rows 4096 x 4096 took 18 us against 11.4 with 33.
@@ -481,7 +459,7 @@ bool Fp8Gemm::prepare(const Fp8LinearArgs& a, int sms) {
   p = Fp8Params{};
   p.M = int(a.M);
   p.N = int(a.N);
-  p.kb = int(kb);
+  p.kb = int(cdiv(a.K, kFp8Block));
   p.row_tiles = int(cdiv(a.M, 128 * pair));
   const int64_t tiles = int64_t(p.row_tiles) * cdiv(a.N, tile_n);
   p.tiles = int(tiles);

@@ -15,12 +15,6 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 size_t mr_bytes(int64_t M, int r, size_t size) { return align256(size_t(M) * size_t(r) * size); }
 size_t pair_bytes(int64_t M, int64_t N, size_t size) { return align256(2 * size_t(M) * size_t(N) * size); }
 
-// Few tokens: stream the weights (16 tokens a pass) instead of feeding the GEMM.  Measured, this
-// against the GEMM, us: 11008 x 4096 with 1, 16, 17 and 32 tokens 27, 33, 51 and 52 against 53 to
-// 58; 4096 x 4096 with 16 and 32 18 and 28 against 24 and 25; 1000 x 4096 with 1 and 32 10.6 and
-// 15.1 against 16.5; 4096 x 1024 with 16 12.3 against 15.1.
-bool use_decode(int64_t M) { return M <= 32; }
-
 }  // namespace
 
 // fwd [T] [the decode kernel's partials and counters]; bwd [T] [terms of U] [dg, du] [dx in splits]
@@ -37,7 +31,7 @@ cudaError_t launch_gated_fwd(const GatedArgs& a, int sms, cudaStream_t st, int* 
   void* T = a.t_out != nullptr ? a.t_out : a.ws + kWsHeader;
   GatedDecode d;
   uint8_t* scratch = a.ws + kWsHeader + mr_bytes(2 * a.M, a.r, 2);
-  if (use_decode(a.M)) {
+  if (gated_streams(a.M)) {
     if (!d.prepare(a, T, scratch, sms)) return cudaErrorInvalidValue;
     const cudaError_t e = launch_gated_t_small(a, T, d.p.counters, st, launches);
     return e == cudaSuccess ? d.run(st, launches) : e;
@@ -60,7 +54,7 @@ cudaError_t launch_gated_bwd(const GatedArgs& a, int sms, cudaStream_t st, int* 
   GatedRank t, u, db, da;
   GatedGemm dx;
   // T again comes from the kernel that made it in the forward: the same bits
-  const bool small_t = use_decode(a.M);
+  const bool small_t = gated_streams(a.M);
   bool ok = a.t_in != nullptr || small_t || t.prepare(a, kGatedT, nullptr, nullptr, ws, sms);
   ok = ok && u.prepare(a, kGatedU, nullptr, d, U, sms);
   ok = ok && db.prepare(a, kGatedDB, T, nullptr, a.dB, sms);

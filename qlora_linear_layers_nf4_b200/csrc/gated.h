@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 
+#include "gated_plan.h"
 #include "kernels.h"
 
 namespace nf4 {
@@ -75,9 +76,6 @@ struct GatedParams {
   float* partials;            // of several splits: [split][M][2][N] or [split][M][K]
   uint32_t* status;
 };
-
-constexpr int kGatedMaxPairs = 80;   // most CTA pairs that splits are made for
-size_t gated_split_bytes(bool backward, int64_t M, int64_t N, int64_t K);
 
 // h (and g, u) or dx, prepared on the host before the first launch of a call.  `ad`: T
 // [2][M][r], or the terms of U [2][terms][M][r], of which the first are read; `tok`: x, or dg

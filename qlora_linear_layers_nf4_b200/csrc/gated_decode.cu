@@ -46,8 +46,9 @@ using expert::warp_wait;
 constexpr int kDcGroupWarps = 8;                     // 16 rows each
 constexpr int kDcEpiWarps = 4;                       // finish tiles, a thread per row
 constexpr int kDcRows = 32 * kDcEpiWarps;
-constexpr int kDcOutputs = kDcRows / 2;               // of a tile, a gate and an up row each
-constexpr int kDcBlocks = 4;                         // 64-wide K blocks per unit
+constexpr int kDcOutputs = kGatedDecodeOutputs;       // of a tile, a gate and an up row each
+static_assert(2 * kDcOutputs == kDcRows, "a row a thread");
+constexpr int kDcBlocks = kGatedDecodeChunk / 64;    // 64-wide K blocks per unit
 constexpr uint32_t kDcCodeBytes = kDcRows * 128;
 constexpr uint32_t kLutBytes = 256 * 256;            // entry e, lane l at 256 e + 8 l
 
@@ -591,7 +592,8 @@ cudaError_t launch(const GatedDecode& L, cudaStream_t st) {
 size_t gated_decode_scratch_bytes() { return size_t(kGatedDecodeMaxCtas) * (2 * kDcRows * 16 * sizeof(float) + 16); }
 
 bool GatedDecode::prepare(const GatedArgs& a, const void* T, uint8_t* scratch, int sms) {
-  np = a.M <= 8 ? 8 : 16;
+  const GatedDecodePlan plan = gated_decode_plan(a.M, a.N, a.K, sms);
+  np = plan.np;
   f16 = a.f16 != 0;
   const uint64_t K = uint64_t(a.K), N = uint64_t(a.N), M = uint64_t(a.M), kb = K / 64;
   bool ok = true;
@@ -607,9 +609,12 @@ bool GatedDecode::prepare(const GatedArgs& a, const void* T, uint8_t* scratch, i
   p.N = int(a.N);
   p.K = int(a.K);
   p.r = a.r;
-  p.n_tiles = int((a.N + kDcOutputs - 1) / kDcOutputs);
-  p.k_chunks = int((a.K + 255) / 256);
-  p.row_tiles = int((a.M + np - 1) / np);
+  p.n_tiles = plan.n_tiles;
+  p.k_chunks = plan.k_chunks;
+  p.row_tiles = plan.row_tiles;
+  p.whole = plan.whole;
+  p.rest = plan.rest;
+  p.rest_ctas = plan.rest_ctas;
   p.bs_shift = log2_block(a.w[0]->block_size);
   p.dq = a.w[0]->double_quant;
   p.act = a.act;
@@ -627,19 +632,8 @@ bool GatedDecode::prepare(const GatedArgs& a, const void* T, uint8_t* scratch, i
   p.counters = reinterpret_cast<int*>(scratch + size_t(kGatedDecodeMaxCtas) * 2 * kDcRows * 16 * sizeof(float));
   p.status = a.status;
   p.vec_scales = a.w[0]->block_size == 64 && a.K % 256 == 0;   // scale pointers are 16-byte aligned
-  const int64_t most = int64_t(p.row_tiles) * p.n_tiles * p.k_chunks;
-  if (most > int64_t(0x7fffffff)) return false;
-  // Whole tiles for every SM, and the rest shared: where it leaves two SMs or more for a tile
-  // each has CTAs of its own, up to eight, as a share that straddles two tiles stores and joins
-  // parts of both (1000 x 4096: one token 15.6 -> 10.6 us, 16 tokens 28.5 -> 14.2; 4096 x 4096,
-  // 16 tokens: 20.6 -> 18.4).
-  const int64_t tiles = int64_t(p.row_tiles) * p.n_tiles, ctas = std::min(sms, kGatedDecodeMaxCtas);
-  p.whole = int(tiles / ctas);
-  p.rest = int(tiles % ctas);
-  const int64_t each = p.rest > 0 ? std::min<int64_t>({8, ctas / p.rest, p.k_chunks}) : 0;
-  p.rest_ctas = int(each >= 2 ? each * p.rest : std::min<int64_t>(ctas, int64_t(p.rest) * p.k_chunks));
-  grid = unsigned(p.whole > 0 ? ctas : p.rest_ctas);
-  return ok;
+  grid = unsigned(plan.ctas);
+  return ok && plan.fits;
 }
 
 cudaError_t GatedDecode::run(cudaStream_t st, int* launches) const {

@@ -7,8 +7,6 @@
 
 namespace nf4 {
 
-constexpr int kGatedDecodeMaxCtas = 160;   // most CTAs of a launch; sizes the scratch
-
 struct GatedDecodeParams {
   int M, N, K, r;
   int n_tiles, k_chunks;    // tiles of 64 outputs, 256-wide chunks of a row

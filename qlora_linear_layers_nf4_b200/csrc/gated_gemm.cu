@@ -49,14 +49,14 @@ using namespace expert;
 constexpr int kFwd = 0;
 constexpr int kDx = 1;
 
-constexpr int kPartT = 256;                 // tokens of one MMA at most, half in each CTA
+constexpr int kPartT = kGatedPartT;         // tokens of one MMA at most, half in each CTA
 constexpr uint32_t kWBytes = 128 * 128;     // weight tile of a CTA: 128 x 128 bytes
 constexpr uint32_t kTBytes = 128 * 128;     // its tokens of one part
 constexpr uint32_t kCodeBytes = 128 * 32;   // kDx: NF4 codes of one step
 constexpr int kCodeSlots = 6;
 constexpr int kEpiWarp = 4;
 
-constexpr int tile_w(int mode) { return mode == kFwd ? 128 : 256; }   // outputs of a pair's tile
+constexpr int tile_w(int mode) { return gated_tile_w(mode == kDx); }   // outputs of a pair's tile
 constexpr int stages_of(int parts) { return parts == 2 ? 4 : 6; }
 // Dequant groups of four warps each take every deq_groups-th step; the stages and
 // the code slots are multiples of their number, so that each belongs to one group.
@@ -713,8 +713,6 @@ cudaError_t launch_mode(const GatedGemm& L, cudaStream_t st, int* launches) {
   return L.f16 ? launch<MODE, true, 1>(L, st, launches) : launch<MODE, false, 1>(L, st, launches);
 }
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // T [2][M][r], or the first of each projection's terms of U [2][terms][M][r].
 bool ad_map(CUtensorMap* map, const void* ad, uint64_t r, uint64_t M, uint64_t terms, uint32_t box_rows) {
   const uint64_t dims[3] = {r, M, 2}, strides[2] = {r * 2, terms * M * r * 2};
@@ -722,68 +720,14 @@ bool ad_map(CUtensorMap* map, const void* ad, uint64_t r, uint64_t M, uint64_t t
   return encode_map(map, ad, MapElem::k16, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-
-// Splits of a reduction: a step costs the decoding of its weights whatever the tokens, so few
-// tiles with many steps are slow (dx of 100 tokens, 4000 x 2048: 8 tiles of 127 steps, 65 us).
-// Eight steps a split at least, and none of fewer than 24 (333 tokens, 1032 x 1088: 22.4 against
-// 21.9).
-
-// dx fills the pairs that its tiles leave idle, if those are half or more.  It keeps to two
-// thirds of the SMs, and leaves the others to dB and dA beside it, unless it is long itself, 20
-// steps for every pair (100 tokens, 4000 x 2048, 8 tiles of 126 steps: 6 splits 39 us, 9 splits
-// 45; 16 tokens, 4096 x 4096, 16 tiles of 130: 3 splits 46 us, 4 splits 42).
-int dx_splits(int64_t tiles, int steps, int sms) {
-  if (steps < 24) return 1;
-  const int64_t pairs = std::min(std::max(sms / 2, 1), kGatedMaxPairs);
-  const int64_t most = steps * tiles < 20 * pairs ? ((sms + 2) / 3 + tiles / 2) / tiles : pairs;
-  return int(std::max<int64_t>(1, std::min<int64_t>({most, pairs / tiles, steps / 8})));
-}
-
-// The forward takes what costs least by these measured parts, in ns: 460 a step, 1,000 a tile,
-// 3,500 for the launch that adds the splits up, and their sums written and read at 5 TB/s
-// (64 tokens, 1000 x 4096, 8 tiles: 35 us, with 8 splits 17; 11008 x 4096, 86 tiles on 74 pairs:
-// 67 us, with 3 splits 55; 14336 x 4096, 112 tiles: 68 us, with 2 to 5 splits 67 to 72).
-constexpr int kMaxFwdSplits = 16;
-constexpr size_t kMaxFwdSums = size_t(40) << 20;
-size_t fwd_sums(int64_t splits, int64_t M, int64_t N) { return size_t(splits) * size_t(M) * size_t(2 * N) * sizeof(float); }
-int fwd_splits(int64_t M, int64_t N, int64_t tiles, int steps, int sms) {
-  if (steps < 24) return 1;
-  const int64_t pairs = std::max(sms / 2, 1);
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
-  for (int s = 1; s <= kMaxFwdSplits && (s == 1 || (steps / s >= 8 && fwd_sums(s, M, N) <= kMaxFwdSums)); ++s) {
-    const int64_t sums = s > 1 ? 3500 + int64_t(2 * fwd_sums(s, M, N) / 5000) : 0;
-    const int64_t cost = cdiv(tiles * s, pairs) * (cdiv(steps, s) * 460 + 1000) + sums;
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = s;
-    }
-  }
-  return best;
-}
-
 }  // namespace
-
-// Splits' sums, fp32: [split][M][K] or, forward, [split][M][2][N].  In dx more rows make more
-// tiles and so fewer splits: the size is the largest of any number of rows up to M, so that a
-// workspace for M serves fewer.
-size_t gated_split_bytes(bool backward, int64_t M, int64_t N, int64_t K) {
-  if (!backward) return std::min(kMaxFwdSums, fwd_sums(kMaxFwdSplits, M, N));
-  const int64_t col_tiles = cdiv(K, tile_w(kDx));
-  int64_t rows = 0;
-  for (int64_t m_tiles = 1; (m_tiles - 1) * kPartT < M && 2 * m_tiles * col_tiles <= kGatedMaxPairs; ++m_tiles)
-    rows = std::max(rows, kGatedMaxPairs / (m_tiles * col_tiles) * std::min(M, m_tiles * kPartT));
-  return size_t(rows) * size_t(K) * sizeof(float);
-}
 
 bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, const void* ad, void* scratch, int sms) {
   dx = backward;
   f16 = a.f16 != 0;
   const uint64_t M = uint64_t(a.M), N = uint64_t(a.N), K = uint64_t(a.K), r = uint64_t(a.r);
-  const int64_t col_tiles = cdiv(backward ? a.K : a.N, tile_w(backward ? kDx : kFwd));
-  // Two MMAs a decoded weight tile where there are more tokens than one MMA takes and
-  // one-MMA tiles would need a second wave of CTA pairs (the expert GEMM's rule).
-  parts = a.M > kPartT && a.M / kPartT * col_tiles > sms / 2 ? 2 : 1;
+  const GatedGemmPlan plan = gated_gemm_plan(backward, a.M, a.N, a.K, a.r, sms);
+  parts = plan.parts;
   const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t depth = backward ? 2 : 1, cols = backward ? N : K;
   const uint64_t ad_terms = backward ? uint64_t(gated_terms(f16)) : 1;
@@ -806,21 +750,13 @@ bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, cons
   p.w_rows = int(a.N);
   p.w_cols = int(a.K);
   p.r = a.r;
-  p.half_steps = int(backward ? cdiv(a.N, 64) : a.K / 64);
-  p.main_steps = backward ? 2 * p.half_steps : p.half_steps;
-  p.ad_steps = (a.r + 63) / 64;
-  p.col_tiles = int(col_tiles);
-  p.row_tiles = int(cdiv(a.M, int64_t(parts) * kPartT));
-  const int64_t tiles256 = int64_t(p.row_tiles) * p.col_tiles;
-  const int steps = p.main_steps + 2 * p.ad_steps;
-  p.splits = parts == 2 ? 1 : backward ? dx_splits(tiles256, steps, sms) : fwd_splits(a.M, a.N, tiles256, steps, sms);
-  // Forward: CTA pairs left over take tiles of fewer tokens, whose MMAs and epilogue are shorter
-  // (333 tokens, 1032 x 1088: 21.4 -> 17.0 us; 256, 512 x 512: 18.3 -> 12.4).  Beside dx, dB and
-  // dA run on them (with smaller tiles the backward of 512 tokens, 1024 x 1024, took 39 us, not 32).
-  const int64_t spare = backward ? 1 : sms / 2 / (int64_t(p.row_tiles) * p.col_tiles * p.splits);
-  if (spare > 1) p.row_tiles = int(std::max<int64_t>(p.row_tiles, std::min(p.row_tiles * spare, cdiv(a.M, 64))));
-  p.tile_rows = int((cdiv(a.M, p.row_tiles) + 31) & ~int64_t(31));   // pieces of 32 tokens are stored whole
-  p.row_tiles = int(cdiv(a.M, p.tile_rows));
+  p.half_steps = plan.half_steps;
+  p.main_steps = plan.main_steps;
+  p.ad_steps = plan.ad_steps;
+  p.col_tiles = plan.col_tiles;
+  p.row_tiles = plan.row_tiles;
+  p.tile_rows = plan.tile_rows;
+  p.splits = plan.splits;
   p.block_chunks_shift = log2_block(a.w[0]->block_size) - 6;
   p.dq = a.w[0]->double_quant;
   p.act = a.act;
@@ -837,10 +773,9 @@ bool GatedGemm::prepare(const GatedArgs& a, bool backward, const void* tok, cons
   p.pre = backward ? nullptr : a.pre_out;
   p.status = a.status;
   p.partials = static_cast<float*>(scratch);
-  const int64_t tiles = int64_t(p.row_tiles) * p.col_tiles * p.splits;
-  grid = 2u * unsigned(std::min<int64_t>(tiles, std::max(sms / 2, 1)));
+  grid = 2u * unsigned(plan.pairs);
   // chunks are counted in 32 bits: weights of up to 2.7e11 elements
-  return ok && N * (K / 64) <= 0xffffffffull && tiles <= int64_t(0x7fffffff);
+  return ok && N * (K / 64) <= 0xffffffffull && plan.tiles <= int64_t(0x7fffffff);
 }
 
 cudaError_t GatedGemm::sum(cudaStream_t st, int* launches) const {
