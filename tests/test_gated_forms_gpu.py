@@ -1,5 +1,5 @@
 """The gated layer in the forms that full-size layers take and small ones do not: the work splits of the streaming
-forward.  That each size takes its form is
+forward, tiles of two MMAs.  That each size takes its form is
 checked without a GPU, in test_plans.py.  Bounds as in test_gated_gpu.py."""
 import pytest
 
@@ -35,4 +35,43 @@ def test_work_splits_of_few_tokens(cuda_device, m, n, k, r, dtype, act, whole, r
         again, s = L.fwd()
         assert again.equal(h) and s.pre.equal(saved.pre) and s.t.equal(saved.t)
     assert L.fwd(want_saved=False)[0].equal(h)
+    ok_status()
+
+
+# m, n, k, r, dtype, block, dq, act: forwards of two MMAs a weight tile
+TWO_MMAS_FWD = [
+    (300, 9600, 128, 64, "bf16", 64, True, "silu"),
+    (300, 9480, 192, 24, "f16", 128, False, "gelu_tanh"),      # a short last tile of outputs
+    (520, 6008, 320, 72, "f16", 64, True, "silu"),             # the last token tile has one part
+]
+
+
+@pytest.mark.parametrize("m,n,k,r,dtype,block,dq,act", TWO_MMAS_FWD)
+def test_forward_of_two_mmas_a_tile(cuda_device, m, n, k, r, dtype, block, dq, act):
+    L = Layer(cuda_device, m, n, k, r, dtype, block, dq, True, act)
+    h, saved = L.fwd()
+    L.check_fwd(h, saved)
+    assert L.fwd(want_saved=False)[0].equal(h)
+    ok_status()
+
+
+# the same of dx: training batches
+TWO_MMAS_DX = [
+    (1500, 200, 4096, 24, "bf16", 64, True, "silu"),
+    (1500, 200, 4032, 24, "f16", 64, False, "gelu_tanh"),      # a short last tile of columns
+    (520, 72, 9728, 16, "bf16", 128, False, "gelu_tanh"),      # the last token tile has one part
+    (520, 136, 9728, 8, "f16", 64, True, "silu"),
+    (800, 1096, 6400, 72, "bf16", 64, True, "gelu_tanh"),      # more steps than stages and code slots, several rounds
+    (1300, 520, 4160, 200, "f16", 256, True, "silu"),
+]
+
+
+@pytest.mark.parametrize("m,n,k,r,dtype,block,dq,act", TWO_MMAS_DX)
+def test_backward_of_two_mmas_a_tile(cuda_device, m, n, k, r, dtype, block, dq, act):
+    L = Layer(cuda_device, m, n, k, r, dtype, block, dq, False, act)
+    _, saved = L.fwd()
+    dA, dB, dx = L.bwd(saved)
+    L.check_bwd(dA, dB, dx, saved)
+    for _ in range(3):
+        assert all(a.equal(b) for a, b in zip((dA, dB, dx), L.bwd(saved)))
     ok_status()

@@ -9,3 +9,12 @@ def test_decode_cases_take_their_splits():
     for case, p, s in zip(forms.DECODE, plans, streams):
         kind = "none" if p["rest"] == 0 else "own" if p["rest_ctas"] % p["rest"] == 0 and p["rest_ctas"] > p["rest"] else "straddle"
         assert s["streams"] and (p["whole"], kind) == case[-2:], (case, p)
+
+
+def test_two_mma_cases_take_two():
+    for backward, cases in ((0, forms.TWO_MMAS_FWD), (1, forms.TWO_MMAS_DX)):
+        plans = ask(*[("gemm", backward, m, n, k, r, SMS) for m, n, k, r, *_ in cases])
+        assert all(p["parts"] == 2 for p in plans), plans
+        # one of them ends with a token tile of a single part, one has more tiles than CTA pairs
+        assert any(0 < m - (p["row_tiles"] - 1) * p["tile_rows"] <= 256 < p["tile_rows"] for (m, *_), p in zip(cases, plans))
+        assert any(p["tiles"] > p["pairs"] for p in plans)
