@@ -1,5 +1,5 @@
 """The gated layer in the forms that full-size layers take and small ones do not: the work splits of the streaming
-forward, tiles of two MMAs.  That each size takes its form is
+forward, tiles of two MMAs, several rounds of split tiles.  That each size takes its form is
 checked without a GPU, in test_plans.py.  Bounds as in test_gated_gpu.py."""
 import pytest
 
@@ -74,4 +74,19 @@ def test_backward_of_two_mmas_a_tile(cuda_device, m, n, k, r, dtype, block, dq, 
     L.check_bwd(dA, dB, dx, saved)
     for _ in range(3):
         assert all(a.equal(b) for a, b in zip((dA, dB, dx), L.bwd(saved)))
+    ok_status()
+
+
+# m, n, k, r, dtype: forwards whose splits are more tiles than the CTA pairs take at once
+ROUNDS_OF_SPLITS = [(33, 9608, 2560, 16, "bf16"), (64, 9608, 2560, 24, "f16"), (40, 10400, 3008, 72, "bf16")]
+
+
+@pytest.mark.parametrize("m,n,k,r,dtype", ROUNDS_OF_SPLITS)
+def test_rounds_of_split_tiles(cuda_device, m, n, k, r, dtype):
+    L = Layer(cuda_device, m, n, k, r, dtype, bias=True)
+    h, saved = L.fwd()
+    L.check_fwd(h, saved)
+    for _ in range(3):
+        again, s = L.fwd()
+        assert again.equal(h) and s.pre.equal(saved.pre)
     ok_status()

@@ -18,3 +18,8 @@ def test_two_mma_cases_take_two():
         # one of them ends with a token tile of a single part, one has more tiles than CTA pairs
         assert any(0 < m - (p["row_tiles"] - 1) * p["tile_rows"] <= 256 < p["tile_rows"] for (m, *_), p in zip(cases, plans))
         assert any(p["tiles"] > p["pairs"] for p in plans)
+
+
+def test_split_cases_take_several_rounds():
+    for (m, n, k, r, _), p in zip(forms.ROUNDS_OF_SPLITS, ask(*[("gemm", 0, m, n, k, r, SMS) for m, n, k, r, _ in forms.ROUNDS_OF_SPLITS])):
+        assert p["splits"] > 1 and p["tiles"] > 2 * p["pairs"], ((m, n, k, r), p)
