@@ -1,5 +1,5 @@
 """The gated layer in the forms that full-size layers take and small ones do not: the work splits of the streaming
-forward, tiles of two MMAs, several rounds of split tiles.  That each size takes its form is
+forward, tiles of two MMAs, several rounds of split tiles, long sums over tokens.  That each size takes its form is
 checked without a GPU, in test_plans.py.  Bounds as in test_gated_gpu.py."""
 import pytest
 
@@ -89,4 +89,34 @@ def test_rounds_of_split_tiles(cuda_device, m, n, k, r, dtype):
     for _ in range(3):
         again, s = L.fwd()
         assert again.equal(h) and s.pre.equal(saved.pre)
+    ok_status()
+
+
+# m, n, k, r: long sums over tokens with enough tiles that a CTA has about seventy of their steps of 64: of U (over n)
+# and dB, and of dA
+LONG_SUMS = [(9000, 8200, 128, 16), (9000, 136, 8256, 16)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n,k,r", LONG_SUMS)
+def test_sums_brought_to_fp32_in_time(cuda_device, m, n, k, r, dtype):
+    """dA and dB of many tokens, every row nonzero, relative to 64 bits in norm.  The tensor core loses up to 2^-25 of an
+    accumulator at an instruction (towards zero, so the losses add up), and no more than 16 go into one before it is added
+    to an fp32 total: 16 * 2^-25 of a sum; dA has that of U and of its own.  The activation's fp32 values and the terms'
+    24 (22) bits are within 2^-22.  Seventy steps are 140 instructions into each accumulator: left there they would lose
+    about 140 * 2^-26 * 2 / 3 = 1.4e-6 in each sum."""
+    L = Layer(cuda_device, m, n, k, r, dtype)
+    _, saved = L.fwd()
+    dA, dB, dx = L.bwd(saved)
+    d = [v.double() for v in (L.dh, saved.pre[0], saved.pre[1])]
+    sig = d[1].sigmoid()
+    d = (d[0] * d[2] * (sig + d[1] * sig * (1 - sig)), d[0] * d[1] * sig)
+    window = 16 * 2.0 ** -25
+    for i in range(2):
+        want = d[i].T @ saved.t[i].double()
+        off = (dB[i].double() - want).norm() / want.norm()
+        assert off <= window + 2.0 ** -22, f"dB: {off:.2e}"
+        want = (L.s * (d[i] @ L.B[i].double())).T @ L.x.double()
+        off = (dA[i].double() - want).norm() / want.norm()
+        assert off <= 2 * window + 2.0 ** -22, f"dA: {off:.2e}"
     ok_status()
