@@ -1,4 +1,5 @@
 """CPU checks of the rules that cut calls into work: the sizes that GPU tests run take the forms that they are there for."""
+from tests import test_fp8_forms_gpu as fp8
 from tests import test_gated_forms_gpu as forms
 from tests.plans import SMS, ask
 
@@ -23,3 +24,8 @@ def test_two_mma_cases_take_two():
 def test_split_cases_take_several_rounds():
     for (m, n, k, r, _), p in zip(forms.ROUNDS_OF_SPLITS, ask(*[("gemm", 0, m, n, k, r, SMS) for m, n, k, r, _ in forms.ROUNDS_OF_SPLITS])):
         assert p["splits"] > 1 and p["tiles"] > 2 * p["pairs"], ((m, n, k, r), p)
+
+
+def test_streamed_8_bit_cases_take_several_rounds():
+    for (m, n, k, *_, rounds), p in zip(fp8.STREAMED, ask(*[("fp8", m, n, k, SMS) for m, n, k, *_ in fp8.STREAMED])):
+        assert p["streams"] and -(-p["groups"] // p["ctas"]) == rounds, ((m, n, k), p)
