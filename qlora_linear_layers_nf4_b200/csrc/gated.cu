@@ -31,7 +31,7 @@ cudaError_t launch_gated_fwd(const GatedArgs& a, int sms, cudaStream_t st, int* 
   void* T = a.t_out != nullptr ? a.t_out : a.ws + kWsHeader;
   GatedDecode d;
   uint8_t* scratch = a.ws + kWsHeader + mr_bytes(2 * a.M, a.r, 2);
-  if (gated_streams(a.M)) {
+  if (gated_streams(a.M, a.N, a.K, a.r, sms)) {
     if (!d.prepare(a, T, scratch, sms)) return cudaErrorInvalidValue;
     const cudaError_t e = launch_gated_t_small(a, T, d.p.counters, st, launches);
     return e == cudaSuccess ? d.run(st, launches) : e;
@@ -54,7 +54,7 @@ cudaError_t launch_gated_bwd(const GatedArgs& a, int sms, cudaStream_t st, int* 
   GatedRank t, u, db, da;
   GatedGemm dx;
   // T again comes from the kernel that made it in the forward: the same bits
-  const bool small_t = gated_streams(a.M);
+  const bool small_t = gated_streams(a.M, a.N, a.K, a.r, sms);
   bool ok = a.t_in != nullptr || small_t || t.prepare(a, kGatedT, nullptr, nullptr, ws, sms);
   ok = ok && u.prepare(a, kGatedU, nullptr, d, U, sms);
   ok = ok && db.prepare(a, kGatedDB, T, nullptr, a.dB, sms);

@@ -78,18 +78,18 @@ constexpr size_t kGatedMaxFwdSums = size_t(40) << 20;
 inline size_t gated_fwd_sums(int64_t splits, int64_t M, int64_t N) {
   return size_t(splits) * size_t(M) * size_t(2 * N) * sizeof(float);
 }
-inline int gated_fwd_splits(int64_t M, int64_t N, int64_t tiles, int steps, int sms) {
-  if (steps < 24) return 1;
+struct GatedFwdSplits {
+  int splits;
+  int64_t ns;
+};
+inline GatedFwdSplits gated_fwd_splits(int64_t M, int64_t N, int64_t tiles, int steps, int sms) {
   const int64_t pairs = std::max(sms / 2, 1);
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
-  for (int s = 1; s <= kGatedMaxFwdSplits && (s == 1 || (steps / s >= 8 && gated_fwd_sums(s, M, N) <= kGatedMaxFwdSums)); ++s) {
+  GatedFwdSplits best{1, INT64_MAX};
+  for (int s = 1; s <= kGatedMaxFwdSplits; ++s) {
+    if (s > 1 && (steps < 24 || steps / s < 8 || gated_fwd_sums(s, M, N) > kGatedMaxFwdSums)) break;
     const int64_t sums = s > 1 ? 3500 + int64_t(2 * gated_fwd_sums(s, M, N) / 5000) : 0;
-    const int64_t cost = plan_cdiv(tiles * s, pairs) * (plan_cdiv(steps, s) * 460 + 1000) + sums;
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = s;
-    }
+    const int64_t ns = plan_cdiv(tiles * s, pairs) * (plan_cdiv(steps, s) * 460 + 1000) + sums;
+    if (ns < best.ns) best = GatedFwdSplits{s, ns};
   }
   return best;
 }
@@ -130,7 +130,7 @@ inline GatedGemmPlan gated_gemm_plan(bool backward, int64_t M, int64_t N, int64_
   p.row_tiles = int(plan_cdiv(M, int64_t(p.parts) * kGatedPartT));
   const int64_t tiles256 = int64_t(p.row_tiles) * p.col_tiles;
   const int steps = p.main_steps + 2 * p.ad_steps;
-  p.splits = p.parts == 2 ? 1 : backward ? gated_dx_splits(tiles256, steps, sms) : gated_fwd_splits(M, N, tiles256, steps, sms);
+  p.splits = p.parts == 2 ? 1 : backward ? gated_dx_splits(tiles256, steps, sms) : gated_fwd_splits(M, N, tiles256, steps, sms).splits;
   // Forward: CTA pairs left over take tiles of fewer tokens, whose MMAs and epilogue are shorter
   // (333 tokens, 1032 x 1088: 21.4 -> 17.0 us; 256, 512 x 512: 18.3 -> 12.4).  Beside dx, dB and
   // dA run on them (with smaller tiles the backward of 512 tokens, 1024 x 1024, took 39 us, not 32).
@@ -145,10 +145,33 @@ inline GatedGemmPlan gated_gemm_plan(bool backward, int64_t M, int64_t N, int64_
 
 // ---- between the two
 
-// Few tokens: stream the weights (16 tokens a pass) instead of feeding the GEMM.  Measured, this
-// against the GEMM, us: 11008 x 4096 with 1, 16, 17 and 32 tokens 27, 33, 51 and 52 against 53 to
-// 58; 4096 x 4096 with 16 and 32 18 and 28 against 24 and 25; 1000 x 4096 with 1 and 32 10.6 and
-// 15.1 against 16.5; 4096 x 1024 with 16 12.3 against 15.1.
-inline bool gated_streams(int64_t M) { return M <= 32; }
+// Few tokens: stream the weights (16 tokens a pass) instead of feeding the GEMM.  Up to 16 tokens
+// always (graphs of calls over weights larger than L2, r = 16, us, this against the GEMM with 16
+// tokens: 4096 x 4096 18.6 and 25.7, 2560 x 2560 16.3 and 18.3, 4096 x 512 10.9 and 11.6, 8192 x
+// 1024 16.5 and 16.6, 28672 x 8192 109 and 221).  From 17 to 32, two passes, where tiles are whole
+// or have CTAs of their own (24 tokens: 11008 x 4096 47 and 53, 1000 x 4096 15 and 17, 1024 x 1024
+// 11 and 15, 5504 x 4096 28 and 32, 14336 x 4096 58 and 63); where shares straddle tiles, what
+// takes less by measured parts, in ns: here 8,700 (start and T), 990 a unit, 2,700 for joins
+// behind tiles of a CTA's own or 5,500 without; there the splits' cost and 6,000.  4096 x 4096 28.6
+// and 25.9, 2752 x 4096 23.9 and 21.9, 2560 x 2560 21.9 and 18.4, 8192 x 2048 25.2 and 23.5, 17920 x
+// 4096 72 and 66 go to the GEMM, 7168 x 4096 35 and 38, 13824 x 5120 69 and 74, 12032 x 4096 52 and
+// 53 do not.  It is off by up to 6 % where the GEMM has about as many tiles as there are pairs
+// (9216 outputs, K 2048, 4096, 5120: 27, 42, 49 and 29, 44, 51, to the GEMM).  Rows from 6144 on
+// always stream: their codes come slower to the GEMM (3000 x 6144 29 and 34, 4096 x 6144 and x 8192
+// 35 and 35, 41 and 42, 2752 x 8192 34 and 33).
+//
+// A rule without M in each range: a workspace for M serves fewer rows, and the backward makes T by
+// the kernel that made it in the forward.
+constexpr int kGatedAlwaysStream = 16, kGatedMayStream = 32;
+inline bool gated_streams(int64_t M, int64_t N, int64_t K, int r, int sms) {
+  if (M <= kGatedAlwaysStream) return true;
+  if (M > kGatedMayStream) return false;
+  const GatedDecodePlan d = gated_decode_plan(kGatedMayStream, N, K, sms);
+  const bool straddle = d.rest > 0 && d.rest_ctas < 2 * d.rest;
+  if (!straddle || K >= 6144) return true;
+  const int64_t units = int64_t(d.whole) * d.k_chunks * 990 + int64_t(d.rest) * d.k_chunks * 990 / d.rest_ctas;
+  const GatedFwdSplits g = gated_fwd_splits(kGatedMayStream, N, plan_cdiv(N, gated_tile_w(false)), int(K / 64) + 2 * ((r + 63) / 64), sms);
+  return 8700 + units + (d.whole > 0 ? 2700 : 5500) <= 6000 + g.ns;
+}
 
 }  // namespace nf4

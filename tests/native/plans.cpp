@@ -19,8 +19,8 @@ int main() {
       const nf4::GatedGemmPlan p = nf4::gated_gemm_plan(v[0] != 0, v[1], v[2], v[3], int(v[4]), int(v[5]));
       std::printf("parts %d main_steps %d ad_steps %d col_tiles %d row_tiles %d tile_rows %d splits %d tiles %lld pairs %d\n",
                   p.parts, p.main_steps, p.ad_steps, p.col_tiles, p.row_tiles, p.tile_rows, p.splits, (long long)p.tiles, p.pairs);
-    } else if (w == 's' && n == 4) {   // streams M N K sms
-      std::printf("streams %d\n", nf4::gated_streams(v[0]) ? 1 : 0);
+    } else if (w == 's' && n == 5) {   // streams M N K r sms
+      std::printf("streams %d\n", nf4::gated_streams(v[0], v[1], v[2], int(v[3]), int(v[4])) ? 1 : 0);
     } else if (w == 'b' && n == 4) {   // bytes backward M N K: of the splits' sums
       std::printf("bytes %zu\n", nf4::gated_split_bytes(v[0] != 0, v[1], v[2], v[3]));
     } else if (w == 'f' && n == 4) {   // fp8 M N K sms

@@ -1,6 +1,6 @@
 """The gated layer in the forms that full-size layers take and small ones do not: the work splits of the streaming
-forward, tiles of two MMAs, several rounds of split tiles, long sums over tokens.  That each size takes its form is
-checked without a GPU, in test_plans.py.  Bounds as in test_gated_gpu.py."""
+forward, few tokens by the GEMM, tiles of two MMAs, several rounds of split tiles, long sums over tokens.  That each
+size takes its form is checked without a GPU, in test_plans.py.  Bounds as in test_gated_gpu.py."""
 import pytest
 
 from tests.test_gated_gpu import Layer, ok_status
@@ -35,6 +35,25 @@ def test_work_splits_of_few_tokens(cuda_device, m, n, k, r, dtype, act, whole, r
         again, s = L.fwd()
         assert again.equal(h) and s.pre.equal(saved.pre) and s.t.equal(saved.t)
     assert L.fwd(want_saved=False)[0].equal(h)
+    ok_status()
+
+
+# m, n, k, r, dtype: few tokens that the GEMM takes, as shares of the streaming kernel would straddle tiles
+FEW_BY_GEMM = [(17, 4096, 512, 16, "bf16"), (32, 4096, 512, 72, "f16"), (24, 2560, 2560, 24, "bf16"), (31, 8200, 1024, 8, "f16")]
+
+
+@pytest.mark.parametrize("m,n,k,r,dtype", FEW_BY_GEMM)
+def test_few_tokens_by_the_gemm(cuda_device, m, n, k, r, dtype):
+    from qlora_linear_layers_nf4_b200 import nf4qlora as Q
+    import torch
+    L = Layer(cuda_device, m, n, k, r, dtype, bias=True)
+    big = torch.full((m + 3, n), 7.0, dtype=L.x.dtype, device=cuda_device)
+    h, saved = L.fwd(out=big[:m])
+    L.check_fwd(h, saved)
+    assert (big[m:] == 7).all() and L.fwd(want_saved=False)[0].equal(h)
+    grads = L.bwd(saved)
+    L.check_bwd(*grads, saved)
+    assert all(a.equal(b) for a, b in zip(grads, L.bwd(Q.GatedSaved(saved.pre, None))))   # T again: the same bits
     ok_status()
 
 
