@@ -561,8 +561,8 @@ cudaError_t launch_fp8_dequantize(const uint8_t* codes, const float* scales, int
 cudaError_t launch_fp8_linear(const Fp8LinearArgs& given, const void* x, const float* x_scale, uint8_t* codes,
                               float* scales, int sms, cudaStream_t st, int* launches) {
   Fp8LinearArgs a = given;
-  const bool small = fp8_streams(a.M, a.K);
-  const bool inside = small && x_scale == nullptr && fp8_quantizes_inside(a.M, a.K);
+  const bool small = fp8_streams(a.M, a.N, a.K, sms);
+  const bool inside = small && x_scale == nullptr && fp8_quantizes_inside(a.M, a.N, a.K);
   a.x = x_scale != nullptr ? static_cast<const uint8_t*>(x) : codes;
   a.x_scale = x_scale != nullptr ? x_scale : scales;
   Fp8Gemm g;

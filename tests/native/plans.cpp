@@ -25,8 +25,8 @@ int main() {
       std::printf("bytes %zu\n", nf4::gated_split_bytes(v[0] != 0, v[1], v[2], v[3]));
     } else if (w == 'f' && n == 4) {   // fp8 M N K sms
       const nf4::Fp8GemmPlan p = nf4::fp8_gemm_plan(v[0], v[1], v[2], int(v[3]));
-      std::printf("streams %d inside %d groups %lld ctas %lld tile_n %d parts %d\n", nf4::fp8_streams(v[0], v[2]) ? 1 : 0,
-                  nf4::fp8_quantizes_inside(v[0], v[2]) ? 1 : 0, (long long)nf4::fp8_small_groups(v[1]),
+      std::printf("streams %d inside %d groups %lld ctas %lld tile_n %d parts %d\n", nf4::fp8_streams(v[0], v[1], v[2], int(v[3])) ? 1 : 0,
+                  nf4::fp8_quantizes_inside(v[0], v[1], v[2]) ? 1 : 0, (long long)nf4::fp8_small_groups(v[1]),
                   (long long)nf4::fp8_small_ctas(v[1], int(v[3])), p.tile_n, p.parts);
     } else {
       std::fprintf(stderr, "unknown: %s", line);
