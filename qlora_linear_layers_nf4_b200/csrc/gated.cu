@@ -22,7 +22,7 @@ size_t gated_workspace_bytes(bool backward, bool f32, int64_t M, int64_t N, int6
   if (M < 0 || N < 0 || K < 0 || r < 0) return 0;
   if (f32) return gated_f32_workspace_bytes(backward, M, N, r);
   const size_t t = mr_bytes(2 * M, r, 2);
-  const size_t splits = gated_split_bytes(backward, M, N, K);
+  const size_t splits = gated_split_bytes(backward, M, N, K, r);
   return backward ? t + mr_bytes(6 * M, r, 2) + pair_bytes(M, N, 2) + splits : t + std::max(splits, gated_decode_scratch_bytes());
 }
 

@@ -94,15 +94,24 @@ inline GatedFwdSplits gated_fwd_splits(int64_t M, int64_t N, int64_t tiles, int 
   return best;
 }
 
+// Steps of 64 of the reduction: one projection's and the adapters' (forward), or both's (dx).
+inline int64_t gated_steps(bool backward, int64_t N, int64_t K, int r) {
+  return (backward ? 2 * plan_cdiv(N, 64) : K / 64) + 2 * ((r + 63) / 64);
+}
+
 // Splits' sums, fp32: [split][M][K] or, forward, [split][M][2][N].  In dx more rows make more
 // tiles and so fewer splits: the size is the largest of any number of rows up to M, so that a
 // workspace for M serves fewer.
-inline size_t gated_split_bytes(bool backward, int64_t M, int64_t N, int64_t K) {
-  if (!backward) return std::min(kGatedMaxFwdSums, gated_fwd_sums(kGatedMaxFwdSplits, M, N));
+constexpr int kGatedAlwaysStream = 16, kGatedMayStream = 32;   // tokens, see gated_streams
+inline size_t gated_split_bytes(bool backward, int64_t M, int64_t N, int64_t K, int r) {
+  const int64_t steps = gated_steps(backward, N, K, r);
+  if (steps < 24) return 0;
+  if (!backward)
+    return M <= kGatedAlwaysStream ? 0 : std::min(kGatedMaxFwdSums, gated_fwd_sums(std::min<int64_t>(kGatedMaxFwdSplits, steps / 8), M, N));
   const int64_t col_tiles = plan_cdiv(K, gated_tile_w(true));
   int64_t rows = 0;
   for (int64_t m_tiles = 1; (m_tiles - 1) * kGatedPartT < M && 2 * m_tiles * col_tiles <= kGatedMaxPairs; ++m_tiles)
-    rows = std::max(rows, kGatedMaxPairs / (m_tiles * col_tiles) * std::min(M, m_tiles * kGatedPartT));
+    rows = std::max(rows, std::min(kGatedMaxPairs / (m_tiles * col_tiles), steps / 8) * std::min(M, m_tiles * kGatedPartT));
   return size_t(rows) * size_t(K) * sizeof(float);
 }
 
@@ -129,7 +138,7 @@ inline GatedGemmPlan gated_gemm_plan(bool backward, int64_t M, int64_t N, int64_
   p.col_tiles = int(col_tiles);
   p.row_tiles = int(plan_cdiv(M, int64_t(p.parts) * kGatedPartT));
   const int64_t tiles256 = int64_t(p.row_tiles) * p.col_tiles;
-  const int steps = p.main_steps + 2 * p.ad_steps;
+  const int steps = int(gated_steps(backward, N, K, r));
   p.splits = p.parts == 2 ? 1 : backward ? gated_dx_splits(tiles256, steps, sms) : gated_fwd_splits(M, N, tiles256, steps, sms).splits;
   // Forward: CTA pairs left over take tiles of fewer tokens, whose MMAs and epilogue are shorter
   // (333 tokens, 1032 x 1088: 21.4 -> 17.0 us; 256, 512 x 512: 18.3 -> 12.4).  Beside dx, dB and
@@ -162,7 +171,6 @@ inline GatedGemmPlan gated_gemm_plan(bool backward, int64_t M, int64_t N, int64_
 //
 // A rule without M in each range: a workspace for M serves fewer rows, and the backward makes T by
 // the kernel that made it in the forward.
-constexpr int kGatedAlwaysStream = 16, kGatedMayStream = 32;
 inline bool gated_streams(int64_t M, int64_t N, int64_t K, int r, int sms) {
   if (M <= kGatedAlwaysStream) return true;
   if (M > kGatedMayStream) return false;
@@ -170,7 +178,7 @@ inline bool gated_streams(int64_t M, int64_t N, int64_t K, int r, int sms) {
   const bool straddle = d.rest > 0 && d.rest_ctas < 2 * d.rest;
   if (!straddle || K >= 6144) return true;
   const int64_t units = int64_t(d.whole) * d.k_chunks * 990 + int64_t(d.rest) * d.k_chunks * 990 / d.rest_ctas;
-  const GatedFwdSplits g = gated_fwd_splits(kGatedMayStream, N, plan_cdiv(N, gated_tile_w(false)), int(K / 64) + 2 * ((r + 63) / 64), sms);
+  const GatedFwdSplits g = gated_fwd_splits(kGatedMayStream, N, plan_cdiv(N, gated_tile_w(false)), int(gated_steps(false, N, K, r)), sms);
   return 8700 + units + (d.whole > 0 ? 2700 : 5500) <= 6000 + g.ns;
 }
 

@@ -21,8 +21,8 @@ int main() {
                   p.parts, p.main_steps, p.ad_steps, p.col_tiles, p.row_tiles, p.tile_rows, p.splits, (long long)p.tiles, p.pairs);
     } else if (w == 's' && n == 5) {   // streams M N K r sms
       std::printf("streams %d\n", nf4::gated_streams(v[0], v[1], v[2], int(v[3]), int(v[4])) ? 1 : 0);
-    } else if (w == 'b' && n == 4) {   // bytes backward M N K: of the splits' sums
-      std::printf("bytes %zu\n", nf4::gated_split_bytes(v[0] != 0, v[1], v[2], v[3]));
+    } else if (w == 'b' && n == 5) {   // bytes backward M N K r: of the splits' sums
+      std::printf("bytes %zu\n", nf4::gated_split_bytes(v[0] != 0, v[1], v[2], v[3], int(v[4])));
     } else if (w == 'f' && n == 4) {   // fp8 M N K sms
       const nf4::Fp8GemmPlan p = nf4::fp8_gemm_plan(v[0], v[1], v[2], int(v[3]));
       std::printf("streams %d inside %d groups %lld ctas %lld tile_n %d parts %d\n", nf4::fp8_streams(v[0], v[1], v[2], int(v[3])) ? 1 : 0,

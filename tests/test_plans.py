@@ -1,4 +1,8 @@
 """CPU checks of the rules that cut calls into work: the sizes that GPU tests run take the forms that they are there for."""
+import math
+import random
+
+from qlora_linear_layers_nf4_b200 import nf4qlora as Q
 from tests import test_fp8_forms_gpu as fp8
 from tests import test_gated_forms_gpu as forms
 from tests.plans import SMS, ask
@@ -149,3 +153,22 @@ def test_the_faster_8_bit_kernel_takes_few_tokens():
     for (m, n, k, inside, before), p in zip(cases, ask(*[("fp8", m, n, k, SMS) for m, n, k, *_ in cases])):
         if p["streams"]:
             assert (inside if p["inside"] else before) <= 1.11 * min(inside, before), (m, n, k, p)
+
+
+def test_splits_fit_their_workspace():
+    """On devices of any number of SMs; and batches that always stream their weights have no room for splits."""
+    rng = random.Random(7)
+    cases = [(rng.randint(0, 1), round(math.exp(rng.uniform(0, 9))), 8 * round(math.exp(rng.uniform(0, 7.6))),
+              64 * round(math.exp(rng.uniform(0, 5.2))), 8 * rng.randint(1, 32), rng.choice((16, 78, 132, 148, 160, 200))) for _ in range(20000)]
+    plans = ask(*[("gemm", *c) for c in cases])
+    room = ask(*[("bytes", *c[:5]) for c in cases])
+    streams = ask(*[("streams", *c[1:]) for c in cases])
+    split = 0
+    for (back, m, n, k, r, _), p, b, s in zip(cases, plans, room, streams):
+        if p["splits"] > 1 and (back or not s["streams"]):
+            split += 1
+            assert p["splits"] * m * (k if back else 2 * n) * 4 <= b["bytes"], (back, m, n, k, r, p)
+    assert split > 1000
+    for m in (1, 16):
+        assert Q.workspace_bytes(Q.OP_GATED_FWD, m, 11008, 4096, 64, 64, True) < 4 << 20
+    assert Q.workspace_bytes(Q.OP_GATED_FWD, 100, 11008, 1024, 64, 64, True) < 4 << 20   # too few steps to split
