@@ -502,9 +502,10 @@ NF4_API nf4_status qlora_grouped_bwd(const nf4_weight* w, int num_experts, const
  *   t_out          [2, M, r] compute_dtype, or NULL: T, rounded; its `t`.
  *   workspace      >= nf4_workspace_bytes(NF4_OP_GATED_FWD, M, N, K, r, 64, dq), with
  *                  NF4_F32 of NF4_OP_GATED_FWD_F32.
- * A token's result depends on the tokens beside it only through the order of its sums.  In
- * BF16 and F16 a T beyond the compute type's range makes g and u of its token non-finite in
- * both projections.
+ * What is written (the workspace too) may overlap neither an input nor another output
+ * (NF4_ERR_INVALID_ARG).  A token's result depends on the tokens beside it only through the order
+ * of its sums.  In BF16 and F16 a T beyond the compute type's range makes g and u of its
+ * token non-finite in both projections.
  */
 NF4_API nf4_status qlora_gated_fwd(const nf4_weight* w_gate, const nf4_weight* w_up, const void* x,
                                    int64_t M, const void* A, const void* B, int r, float alpha,
@@ -530,6 +531,8 @@ NF4_API nf4_status qlora_gated_fwd(const nf4_weight* w_gate, const nf4_weight* w
  * arguments as in qlora_gated_fwd.
  *   workspace      >= nf4_workspace_bytes(NF4_OP_GATED_BWD, M, N, K, r, 64, dq), with
  *                  NF4_F32 of NF4_OP_GATED_BWD_F32 (they hold dg and du).
+ * Overlaps as in qlora_gated_fwd: the gradients are made beside each other, so dx may not be
+ * written over x or dh.
  */
 NF4_API nf4_status qlora_gated_bwd(const nf4_weight* w_gate, const nf4_weight* w_up, const void* x,
                                    int64_t M, const void* A, const void* B, int r, float alpha,
@@ -591,7 +594,9 @@ NF4_API nf4_status int8_linear_fwd(const int8_t* w_codes, const float* w_scale, 
  *   codes       e4m3 [rows, cols], 16-byte aligned: the value nearest to fp32(x / scale),
  *               ties to even, within -448 .. 448 (both quotients IEEE fp32 divisions).
  * A block of zeros, or one so small that its scale is 0, has codes 0.  A block that holds
- * NaN or Inf has scale NaN and codes 0, so what is computed from it is NaN.
+ * NaN or Inf has scale NaN and codes 0, so what is computed from it is NaN.  Here and in the two
+ * calls below, what is written (a workspace too) may overlap neither an input nor another output
+ * (NF4_ERR_INVALID_ARG).
  */
 NF4_API nf4_status fp8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols, int block_rows,
                                 uint8_t* codes, float* scales, void* stream);

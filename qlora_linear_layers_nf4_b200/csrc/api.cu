@@ -3,6 +3,7 @@
 // the stream was left untouched (the "refuse before writing anything" rule).
 #include <atomic>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -27,6 +28,27 @@ int sm_count() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Memory that a call reads or writes.  Kernels of one call run beside each other and read their
+// inputs more than once, so what they write may lie on nothing else.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y ? y - x < a.bytes : x - y < b.bytes;
+}
+bool outputs_overlap(std::initializer_list<Span> ins, std::initializer_list<Span> outs) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (overlap(*o, i)) return true;
+    for (auto q = outs.begin(); q != o; ++q)
+      if (overlap(*o, *q)) return true;
+  }
+  return false;
+}
 
 nf4_status finish(cudaError_t e, int launches) {
   g_launches += launches;
@@ -687,6 +709,21 @@ nf4_status int8_linear_fwd(const int8_t* w_codes, const float* w_scale, int64_t 
 
 namespace {
 
+Span codes_of(const nf4_weight* w) { return Span{w->codes, size_t(w->rows) * size_t(w->cols) / 2}; }
+Span scales_of(const nf4_weight* w) {
+  const size_t blocks = (size_t(w->rows) * size_t(w->cols) + size_t(w->block_size) - 1) / size_t(w->block_size);
+  return w->double_quant ? Span{w->absmax_q, blocks} : Span{w->absmax, blocks * sizeof(float)};
+}
+
+// Scales of a quantized matrix [rows, cols] in 8-bit floating point, in bytes.
+size_t fp8_scale_bytes(int64_t rows, int64_t cols, int block_rows) {
+  return size_t((rows + block_rows - 1) / block_rows) * size_t((cols + nf4::kFp8Block - 1) / nf4::kFp8Block) * sizeof(float);
+}
+
+size_t gated_ws(bool backward, const nf4::GatedArgs& a) {
+  return nf4::kWsHeader + nf4::gated_workspace_bytes(backward, a.f32 != 0, a.M, a.N, a.K, a.r);
+}
+
 // Checks and common arguments of the two gated entry points.  With M == 0 there are no
 // activations: x may be null.
 nf4_status gated_args(const nf4_weight* w_gate, const nf4_weight* w_up, const void* x, int64_t M, const void* A,
@@ -706,7 +743,6 @@ nf4_status gated_args(const nf4_weight* w_gate, const nf4_weight* w_up, const vo
   if (M > (int64_t(1) << 30) || N > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return NF4_ERR_SHAPE;
   if (workspace == nullptr || !aligned16(workspace)) return NF4_ERR_WORKSPACE;
   const bool f32 = compute_dtype == NF4_F32;
-  if (ws_bytes < nf4::kWsHeader + nf4::gated_workspace_bytes(backward, f32, M, N, K, r)) return NF4_ERR_WORKSPACE;
   *out = nf4::GatedArgs{};
   out->w[0] = w_gate;
   out->w[1] = w_up;
@@ -722,6 +758,7 @@ nf4_status gated_args(const nf4_weight* w_gate, const nf4_weight* w_up, const vo
   out->A = A;
   out->B = B;
   out->ws = static_cast<uint8_t*>(workspace);
+  if (ws_bytes < gated_ws(backward, *out)) return NF4_ERR_WORKSPACE;
   if (!status_word(out->ws, &out->status)) return NF4_ERR_CUDA;
   return NF4_OK;
 }
@@ -743,13 +780,18 @@ nf4_status qlora_gated_fwd(const nf4_weight* w_gate, const nf4_weight* w_up, con
       (t_out && !aligned16(t_out)))
     return NF4_ERR_ALIGNMENT;
   if (M == 0) return NF4_OK;
+  const size_t e = a.f32 ? 4 : 2, m = size_t(M), n = size_t(a.N), k = size_t(a.K), nr = size_t(r);
+  if (outputs_overlap({codes_of(w_gate), scales_of(w_gate), codes_of(w_up), scales_of(w_up), {x, m * k * e}, {A, 2 * nr * k * e}, {B, 2 * n * nr * e},
+                       {bias, 2 * n * e}},
+                      {{h, m * n * e}, {pre_out, 2 * m * n * e}, {t_out, 2 * m * nr * e}, {workspace, gated_ws(false, a)}}))
+    return NF4_ERR_INVALID_ARG;
   a.bias = bias;
   a.h = h;
   a.pre_out = pre_out;
   a.t_out = t_out;
   int launches = 0;
-  const cudaError_t e = nf4::launch_gated_fwd(a, sm_count(), static_cast<cudaStream_t>(stream), &launches);
-  return finish(e, launches);
+  const cudaError_t err = nf4::launch_gated_fwd(a, sm_count(), static_cast<cudaStream_t>(stream), &launches);
+  return finish(err, launches);
 }
 
 nf4_status qlora_gated_bwd(const nf4_weight* w_gate, const nf4_weight* w_up, const void* x, int64_t M, const void* A,
@@ -773,6 +815,11 @@ nf4_status qlora_gated_bwd(const nf4_weight* w_gate, const nf4_weight* w_up, con
       return NF4_ERR_CUDA;
     return NF4_OK;
   }
+  const size_t e = a.f32 ? 4 : 2, m = size_t(M), n = size_t(a.N), k = size_t(a.K), nr = size_t(r);
+  if (outputs_overlap({codes_of(w_gate), scales_of(w_gate), codes_of(w_up), scales_of(w_up), {x, m * k * e}, {A, 2 * nr * k * e}, {B, 2 * n * nr * e},
+                       {dh, m * n * e}, {pre, 2 * m * n * e}, {t, 2 * m * nr * e}},
+                      {{dA, 2 * nr * k * 4}, {dB, 2 * n * nr * 4}, {dx, m * k * e}, {workspace, gated_ws(true, a)}}))
+    return NF4_ERR_INVALID_ARG;
   a.dh = dh;
   a.pre_in = pre;
   a.t_in = t;
@@ -780,8 +827,8 @@ nf4_status qlora_gated_bwd(const nf4_weight* w_gate, const nf4_weight* w_up, con
   a.dB = dB;
   a.dx = dx;
   int launches = 0;
-  const cudaError_t e = nf4::launch_gated_bwd(a, sm_count(), st, &launches);
-  return finish(e, launches);
+  const cudaError_t err = nf4::launch_gated_bwd(a, sm_count(), st, &launches);
+  return finish(err, launches);
 }
 
 }  // extern "C"
@@ -799,6 +846,9 @@ nf4_status fp8_quantize(const void* x, int in_dtype, int64_t rows, int64_t cols,
   if (!aligned16(x) || !aligned16(codes) || !aligned4(scales)) return NF4_ERR_ALIGNMENT;
   // a block (128 x 128) is a CTA
   if (block_rows > 1 && (rows + 127) / 128 * ((cols + 127) / 128) > INT32_MAX) return NF4_ERR_SHAPE;
+  const size_t n = size_t(rows) * size_t(cols);
+  if (outputs_overlap({{x, n * (in_dtype == NF4_F32 ? 4 : 2)}}, {{codes, n}, {scales, fp8_scale_bytes(rows, cols, block_rows)}}))
+    return NF4_ERR_INVALID_ARG;
   int launches = 0;
   const cudaError_t e = nf4::launch_fp8_quantize(x, in_dtype, rows, cols, block_rows, codes, scales, sm_count(),
                                                  static_cast<cudaStream_t>(stream), &launches);
@@ -814,6 +864,9 @@ nf4_status fp8_dequantize(const uint8_t* codes, const float* scales, int64_t row
   if (rows == 0 || cols == 0) return NF4_OK;
   if (codes == nullptr || scales == nullptr || out == nullptr) return NF4_ERR_INVALID_ARG;
   if (!aligned16(codes) || !aligned4(scales) || !aligned16(out)) return NF4_ERR_ALIGNMENT;
+  const size_t n = size_t(rows) * size_t(cols);
+  if (outputs_overlap({{codes, n}, {scales, fp8_scale_bytes(rows, cols, block_rows)}}, {{out, n * (out_dtype == NF4_F32 ? 4 : 2)}}))
+    return NF4_ERR_INVALID_ARG;
   int launches = 0;
   const cudaError_t e = nf4::launch_fp8_dequantize(codes, scales, rows, cols, block_rows, out_dtype, out, sm_count(),
                                                    static_cast<cudaStream_t>(stream), &launches);
@@ -835,6 +888,11 @@ nf4_status fp8_linear_fwd(const uint8_t* w_codes, const float* w_scale, int64_t 
     return NF4_ERR_ALIGNMENT;
   if (workspace == nullptr || !aligned16(workspace)) return NF4_ERR_WORKSPACE;
   if (ws_bytes < fp8_linear_ws(M, K)) return NF4_ERR_WORKSPACE;
+  const size_t m = size_t(M), n = size_t(N), k = size_t(K), size = compute_dtype == NF4_F32 ? 4 : 2;
+  if (outputs_overlap({{w_codes, n * k}, {w_scale, fp8_scale_bytes(N, K, nf4::kFp8Block)}, {x, m * k * (x_scale != nullptr ? 1 : size)},
+                       {x_scale, fp8_scale_bytes(M, K, 1)}, {bias, n * size}},
+                      {{y, m * n * size}, {workspace, fp8_linear_ws(M, K)}}))
+    return NF4_ERR_INVALID_ARG;
   nf4::Fp8LinearArgs a{};
   a.w = w_codes;
   a.w_scale = w_scale;

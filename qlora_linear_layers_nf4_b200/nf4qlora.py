@@ -703,7 +703,8 @@ def gated_bwd(gate: QuantizedWeight, up: QuantizedWeight, x, A, B, alpha: float,
               activation: str = "silu", want_dx: bool = True, dA=None, dB=None, dx=None,
               workspace: Workspace | None = None):
     """Adapter backward of gated_fwd from what it saved; returns (dA fp32 [2, r, K],
-    dB fp32 [2, N, r], dx [M, K] in x's dtype or None)."""
+    dB fp32 [2, N, r], dx [M, K] in x's dtype or None).  Given outputs may not overlap an input:
+    dx is made beside dA, which reads x."""
     import torch
     dt = _compute_dtype(x)
     M, N, K, r, act = _gated_shapes(gate, up, x, A, activation)
