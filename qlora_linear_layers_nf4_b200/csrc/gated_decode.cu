@@ -14,11 +14,11 @@
 // token: half and half 77 us, a quarter 72, an eighth 73, none 76.5); the adapters' products
 // are two MMAs, T_0 with the up rows zero and T_1 with the gate rows zero.
 //
-// Bound by decoding: four instructions a weight; at 44032 x 4096 shared memory is 73 % busy, the
-// byte-permute pipe 58 %, issue 57 %, DRAM 31 %.  Two weights of 11008 x 4096 (47 MB) take 24 us
-// with one token (2.0 TB/s), 29 with 16, of which 8 are start and T (equal shares of all units,
-// with the join of split tiles at their end: 27 and 33);
-// the rest grows by 15 us (one token) to 19 (16 tokens) for each such pair of weights.
+// Bound by decoding: four instructions a weight; at 44032 x 4096 (one token, 16 tokens) shared
+// memory is 74 and 77 % busy, the byte-permute pipe 57 and 51 %, issue 57 and 54 %, DRAM 31 and 27 %.
+// Two weights of 11008 x 4096 (47 MB) take 23 to 24 us with one token (2.0 TB/s), 29 with 16, of
+// which 8 to 9 are start and T, whose CTAs hold SMs whole (equal shares of all units, with the join
+// of split tiles at their end: 27 and 33).  A unit, 256 columns of a tile, takes a CTA 1 us.
 #include <algorithm>
 
 #include <cuda.h>

@@ -72,7 +72,9 @@ __device__ __forceinline__ float rest(float v, float first) {
   return fabsf(d) < __uint_as_float(0x7f800000u) ? d : 0.0f;
 }
 
-// Four consecutive columns (`col` .. of 0 .. 2 kCols) of row `row` of the result.
+// Four consecutive columns (`col` .. of 0 .. 2 kCols) of row `row` of the result.  T is rounded to
+// the compute type, which is what the forward's MMAs and a saved t take; U's first term, of as
+// many as keep its bits for dA, is what dx's MMAs take.
 template <GatedRankKind KIND>
 __device__ __forceinline__ void store4(const GatedRankParams& p, int row, int col, int col0, float4 v) {
   const int proj = col >= kCols ? 1 : 0;
@@ -610,6 +612,7 @@ __global__ void __launch_bounds__(kMkThreads, 1)
         split8<F16>(dg, term[c][0]);
         split8<F16>(du, term[c][1]);
         copy(c, i + 2);          // into the place just read
+        // dx's MMAs take dg and du of the compute type: the first terms
         if (KIND == kGatedU && blockIdx.z == 0 && 64 * i < left[c]) {
           const int64_t e = at[c] + ahead * i;
           *reinterpret_cast<uint4*>(p.d + e) = term[c][0][0];

@@ -533,7 +533,7 @@ class _CapturedScratch:
 
 
 def read_status(stream=None) -> int:
-    """What the GPU found in the expert and 8-bit calls made without a workspace,
+    """What the GPU found in the expert, gated and 8-bit calls made without a workspace,
     since the last reading: the eager calls of `stream` (a torch stream; the
     current one unless given) and the replays of all captured calls on its
     device, as far as they have run.  NF4_OK, or the first code recorded
