@@ -1,8 +1,11 @@
 """The forms that calls take, asked of the rules that the library is built with (plain C++, so no GPU is needed)."""
 import functools
 import os
+import shutil
 import subprocess
 import tempfile
+
+import pytest
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(os.path.dirname(HERE), "qlora_linear_layers_nf4_b200", "csrc")
@@ -11,6 +14,8 @@ SMS = 148   # of the device that the sizes in the tests are chosen for
 
 @functools.lru_cache(maxsize=None)
 def _program():
+    if shutil.which("g++") is None:
+        pytest.skip("needs g++")
     exe = os.path.join(tempfile.mkdtemp(), "plans")
     subprocess.run(["g++", "-O1", "-std=c++17", "-I", CSRC, "-o", exe, os.path.join(HERE, "native", "plans.cpp")], check=True)
     return exe
